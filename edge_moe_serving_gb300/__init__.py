@@ -10,13 +10,14 @@ package fails loudly when the library is missing.
 import ctypes
 import os
 
-from ctypes import c_double, c_int, c_int32, c_uint32, c_uint64, c_ulonglong, c_size_t, c_void_p, c_char_p, POINTER
+from ctypes import c_double, c_float, c_int, c_int32, c_uint32, c_uint64, c_ulonglong, c_size_t, c_void_p, c_char_p, POINTER
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libmoe.so")
 
 MOE_OK, MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_WORKSPACE, MOE_ERR_CUDA = range(5)
 MOE_DEV_ERR_BAD_ID, MOE_DEV_ERR_UNBOUND, MOE_DEV_ERR_BAD_SLOT, MOE_DEV_ERR_TIMEOUT = 1, 2, 4, 8
+MOE_DEV_ERR_BAD_SEQ, MOE_DEV_ERR_BAD_PAGE, MOE_DEV_ERR_CAPACITY = 16, 32, 64
 MOE_FILL_LOWEST_ID, MOE_FILL_RANDOM = 0, 1
 MOE_FFN_AUTO, MOE_FFN_GEMV, MOE_FFN_GEMM = 0, 1, 2
 MOE_STAGING_TAG = 1 << 30
@@ -67,6 +68,12 @@ class moe_cache_fp4(ctypes.Structure):
     _fields_ = [("cache", moe_pool_nvfp4), ("staging", moe_pool_nvfp4), ("slot_table", c_void_p),
                 ("owner", c_void_p), ("stamp", c_void_p), ("clock", c_void_p), ("n_layers", c_int32),
                 ("E", c_int32), ("H", c_int32), ("I", c_int32), ("format", c_int32), ("reserved", c_int32)]
+
+
+class moe_kv_cache(ctypes.Structure):
+    _fields_ = [("pages", c_void_p), ("table", c_void_p), ("lens", c_void_p), ("refs", c_void_p),
+                ("n_layers", c_int32), ("n_pages", c_int32), ("page_tokens", c_int32), ("rank", c_int32),
+                ("rope", c_int32), ("max_seqs", c_int32), ("max_blocks", c_int32), ("reserved", c_int32)]
 
 
 class moe_bw_profile(ctypes.Structure):
@@ -128,6 +135,19 @@ def _load():
         "moe_layer_forward": (c_int, [POINTER(moe_layer), POINTER(moe_cache), P, c_int, P, c_uint32, c_int,
                                       c_int, c_uint64, c_int, POINTER(moe_layer_buffers), P, c_size_t, P, P,
                                       P]),
+        "moe_kv_workspace_size": (c_size_t, [POINTER(moe_kv_cache), c_int]),
+        "moe_kv_reserve": (c_int, [POINTER(moe_kv_cache), P, P, c_int, P, c_size_t, P, P]),
+        "moe_kv_append": (c_int, [POINTER(moe_kv_cache), c_int, P, P, P, c_int, P, P]),
+        "moe_kv_fork": (c_int, [POINTER(moe_kv_cache), P, P, c_int, P, c_size_t, P, P]),
+        "moe_kv_free": (c_int, [POINTER(moe_kv_cache), P, c_int, P, P]),
+        "moe_kv_compact": (c_int, [POINTER(moe_kv_cache), P, P, c_size_t, P, P]),
+        "moe_latent_decode_workspace_size": (c_size_t, [POINTER(moe_kv_cache), c_int, c_int, c_int, c_int]),
+        "moe_latent_decode": (c_int, [POINTER(moe_kv_cache), c_int, P, P, c_int, c_int, c_int, c_float, c_int, P, P,
+                                      P, c_size_t, P, P]),
+        "moe_latent_prefill_workspace_size": (c_size_t, [POINTER(moe_kv_cache), c_int, c_int, c_int, c_int, c_int,
+                                                         c_int]),
+        "moe_latent_prefill": (c_int, [POINTER(moe_kv_cache), c_int, P, P, P, c_int, c_int, c_int, c_int, c_int, P,
+                                       c_float, c_int, P, P, c_size_t, P, P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -145,7 +165,10 @@ EXPORTED = ["moe_version", "moe_status_string", "moe_check_bounded_wait", "moe_k
             "moe_expert_ffn_grouped_noalloc", "moe_expert_ffn_mxfp4_workspace_size", "moe_expert_ffn_mxfp4",
             "moe_expert_ffn_nvfp4_workspace_size", "moe_expert_ffn_nvfp4", "moe_layer_fp4_workspace_size",
             "moe_layer_forward_fp4", "moe_combine",
-            "moe_layer_workspace_size", "moe_layer_forward", "moe_prefill_double_buffered"]
+            "moe_layer_workspace_size", "moe_layer_forward", "moe_prefill_double_buffered",
+            "moe_kv_workspace_size", "moe_kv_reserve", "moe_kv_append", "moe_kv_fork", "moe_kv_free",
+            "moe_kv_compact", "moe_latent_decode_workspace_size", "moe_latent_decode",
+            "moe_latent_prefill_workspace_size", "moe_latent_prefill"]
 
 
 def lib():
@@ -334,3 +357,53 @@ def moe_prefill_double_buffered(layers, source, layer_buf, state, x, T, out, ffn
     return _check("moe_prefill_double_buffered", _lib.moe_prefill_double_buffered(
         larr, n, ctypes.byref(source), barr, ctypes.byref(state), xs, T, outs, ffn_mode, overlap, _p(ws), ws_bytes,
         _p(dev_status), _s(stream), _s(copy_stream)))
+
+
+def moe_kv_workspace_size(cache, n):
+    return _lib.moe_kv_workspace_size(ctypes.byref(cache), n)
+
+
+def moe_kv_reserve(cache, seqs, n_new, n, ws, ws_bytes, dev_status, stream=None):
+    return _check("moe_kv_reserve", _lib.moe_kv_reserve(
+        ctypes.byref(cache), _p(seqs), _p(n_new), n, _p(ws), ws_bytes, _p(dev_status), _s(stream)))
+
+
+def moe_kv_append(cache, layer, rows, tok_seq, tok_pos, N, dev_status, stream=None):
+    return _check("moe_kv_append", _lib.moe_kv_append(
+        ctypes.byref(cache), layer, _p(rows), _p(tok_seq), _p(tok_pos), N, _p(dev_status), _s(stream)))
+
+
+def moe_kv_fork(cache, src, dst, n, ws, ws_bytes, dev_status, stream=None):
+    return _check("moe_kv_fork", _lib.moe_kv_fork(
+        ctypes.byref(cache), _p(src), _p(dst), n, _p(ws), ws_bytes, _p(dev_status), _s(stream)))
+
+
+def moe_kv_free(cache, seqs, n, dev_status, stream=None):
+    return _check("moe_kv_free", _lib.moe_kv_free(ctypes.byref(cache), _p(seqs), n, _p(dev_status), _s(stream)))
+
+
+def moe_kv_compact(cache, n_live_opt, ws, ws_bytes, dev_status, stream=None):
+    return _check("moe_kv_compact", _lib.moe_kv_compact(
+        ctypes.byref(cache), _p(n_live_opt), _p(ws), ws_bytes, _p(dev_status), _s(stream)))
+
+
+def moe_latent_decode_workspace_size(cache, B, Q, heads, shared_tokens):
+    return _lib.moe_latent_decode_workspace_size(ctypes.byref(cache), B, Q, heads, shared_tokens)
+
+
+def moe_latent_decode(cache, layer, q, seqs, B, Q, heads, scale, shared_tokens, out, lse_opt, ws, ws_bytes,
+                      dev_status, stream=None):
+    return _check("moe_latent_decode", _lib.moe_latent_decode(
+        ctypes.byref(cache), layer, _p(q), _p(seqs), B, Q, heads, scale, shared_tokens, _p(out), _p(lse_opt),
+        _p(ws), ws_bytes, _p(dev_status), _s(stream)))
+
+
+def moe_latent_prefill_workspace_size(cache, B, T, heads, dn, dv, kv_tokens):
+    return _lib.moe_latent_prefill_workspace_size(ctypes.byref(cache), B, T, heads, dn, dv, kv_tokens)
+
+
+def moe_latent_prefill(cache, layer, q, seqs, q_offsets, B, T, heads, dn, dv, w_kv, scale, kv_tokens, out, ws,
+                       ws_bytes, dev_status, stream=None):
+    return _check("moe_latent_prefill", _lib.moe_latent_prefill(
+        ctypes.byref(cache), layer, _p(q), _p(seqs), _p(q_offsets), B, T, heads, dn, dv, _p(w_kv), scale, kv_tokens,
+        _p(out), _p(ws), ws_bytes, _p(dev_status), _s(stream)))

@@ -62,6 +62,9 @@ typedef struct CUstream_st* moe_stream_t; /* same type as cudaStream_t; NULL = l
 #define MOE_DEV_ERR_UNBOUND 2u    /* an expert's slot-table entry was -1; its rows were not written */
 #define MOE_DEV_ERR_BAD_SLOT 4u   /* a slot-table entry pointed outside its pool; treated as unbound */
 #define MOE_DEV_ERR_TIMEOUT 8u    /* a bounded wait in a pipelined kernel ran out; its tile was abandoned */
+#define MOE_DEV_ERR_BAD_SEQ 16u   /* a sequence id, token position or query range outside the cache; skipped */
+#define MOE_DEV_ERR_BAD_PAGE 32u  /* a block-table entry names no page, or an append meets a page others share */
+#define MOE_DEV_ERR_CAPACITY 64u  /* too few free pages, blocks or workspace rows; the call changed nothing */
 
 /* fill policy of moe_cache_bind_slots: which q misses form the fill set F */
 #define MOE_FILL_LOWEST_ID 0  /* the q misses with the lowest expert ids */
@@ -549,6 +552,142 @@ int moe_prefill_double_buffered(const moe_layer* layers, int n_layers, const moe
                                 const moe_pool* layer_buf, const moe_cache* state, const void* const* x, int T,
                                 void* const* out, int ffn_mode, int overlap, void* ws, size_t ws_bytes,
                                 uint32_t* dev_status, moe_stream_t stream, moe_stream_t copy_stream);
+
+/* ---------------------------------------------------------------- paged latent cache
+ * Keys and values of latent attention, the layer that stands before each MoE
+ * layer in the models of [P] section 5.1, kept as one row per token and layer:
+ * the latent vector all heads share (`rank` values) followed by the rotary key
+ * (`rope` values).  Rows live in pages of page_tokens tokens; token t of
+ * sequence s is row t % page_tokens of page table[s, t / page_tokens], in
+ * every layer alike.  [P] section 4.1 pages its cache and shares prefixes the
+ * same way; compaction leaves the pool's tail free, memory the elastic expert
+ * cache of [P] section 3.3 can take.
+ *   pages [n_layers, n_pages, page_tokens, rank + rope] bf16
+ *   table [max_seqs, max_blocks] int32  page of each block, -1 = none
+ *   lens  [max_seqs] int32              tokens held; blocks held = ceil(lens / page_tokens)
+ *   refs  [n_pages] int32               block-table entries that name the page; 0 = free
+ * An empty cache has table = -1, lens = 0, refs = 0.  Pages hold any bits
+ * where no token was stored, NaN among them: nothing reads those.
+ * Every call below checks the struct: MOE_ERR_INVALID_ARG for a NULL struct or
+ * array, a size below 1 (rope: below 0); MOE_ERR_UNSUPPORTED for page_tokens
+ * not in {16, 32, 64, 128}, rank or rope not a multiple of 8, max_seqs above
+ * 8192, n_layers * n_pages * page_tokens or max_seqs * max_blocks above
+ * INT_MAX, pages not 16-byte aligned, an int32 array not 4-byte aligned. */
+typedef struct moe_kv_cache {
+  void* pages;
+  int32_t* table;
+  int32_t* lens;
+  int32_t* refs;
+  int32_t n_layers;
+  int32_t n_pages;
+  int32_t page_tokens;
+  int32_t rank;
+  int32_t rope;
+  int32_t max_seqs;
+  int32_t max_blocks;
+  int32_t reserved;   /* 0 */
+} moe_kv_cache;
+
+/* Bytes of ws that the page calls below need for lists of up to n sequences
+ * (0 for a bad struct or n < 0). */
+size_t moe_kv_workspace_size(const moe_kv_cache* cache, int n);
+
+/* Grows n sequences: seqs[i] gets room for n_new[i] >= 0 more tokens (its
+ * missing blocks are the lowest free pages, in list order) and lens[seqs[i]]
+ * grows by n_new[i].  Too few free pages or a sequence past max_blocks:
+ * MOE_DEV_ERR_CAPACITY, and no sequence changes.  An id outside [0, max_seqs),
+ * a negative n_new and every repeat of an id: MOE_DEV_ERR_BAD_SEQ, that entry
+ * is skipped.  n <= max_seqs, else MOE_ERR_INVALID_ARG. */
+int moe_kv_reserve(const moe_kv_cache* cache, const int32_t* seqs, const int32_t* n_new, int n, void* ws,
+                   size_t ws_bytes, uint32_t* dev_status, moe_stream_t stream);
+
+/* Stores N rows (bf16 [N, rank + rope], 16-byte aligned) in one layer: row i is
+ * token tok_pos[i] of sequence tok_seq[i], inside the length that
+ * moe_kv_reserve gave it.  Entries out of range set MOE_DEV_ERR_BAD_SEQ, entries
+ * whose page is missing or shared (refs > 1) MOE_DEV_ERR_BAD_PAGE; both are skipped. */
+int moe_kv_append(const moe_kv_cache* cache, int layer, const void* rows, const int32_t* tok_seq,
+                  const int32_t* tok_pos, int N, uint32_t* dev_status, moe_stream_t stream);
+
+/* Makes dst[i] a copy of src[i] for n pairs at once, every source as it was
+ * before the call (a permutation or a fan-out among the same sequences is
+ * fine): full pages are shared, a partly filled last page is copied (its
+ * valid rows, every layer) to the lowest page that was free before the call,
+ * in list order, and the pages dst[i] held are released.  src[i] == dst[i] does
+ * nothing.  Too few free pages: MOE_DEV_ERR_CAPACITY, nothing changes.  Ids
+ * outside [0, max_seqs) and repeats of a dst: MOE_DEV_ERR_BAD_SEQ, skipped. */
+int moe_kv_fork(const moe_kv_cache* cache, const int32_t* src, const int32_t* dst, int n, void* ws,
+                size_t ws_bytes, uint32_t* dev_status, moe_stream_t stream);
+
+/* Empties n sequences: their pages' refs drop by one and their blocks become
+ * -1.  Repeats and empty sequences do nothing; ids out of range set
+ * MOE_DEV_ERR_BAD_SEQ. */
+int moe_kv_free(const moe_kv_cache* cache, const int32_t* seqs, int n, uint32_t* dev_status, moe_stream_t stream);
+
+/* Moves the pages in use to the front of the pool: with n_live pages in use,
+ * the ones at index >= n_live move, in ascending order, into the free pages
+ * below n_live, in ascending order (all layers), and the block tables
+ * follow.  n_live_opt: device int32, or NULL.  Pages from n_live on are free
+ * afterwards. */
+int moe_kv_compact(const moe_kv_cache* cache, int32_t* n_live_opt, void* ws, size_t ws_bytes,
+                   uint32_t* dev_status, moe_stream_t stream);
+
+/* ---------------------------------------------------------------- latent attention, absorbed form
+ * Attention of the newest Q tokens of each of B sequences over the cache,
+ * with the key projection folded into the queries (the form for single
+ * tokens): for query i of sequence seqs[b], of length len, and head h,
+ *   s[t] = scale * q[b*Q + i, h, :] . row_t            t < len - Q + i + 1
+ *   out[b*Q + i, h, :] = sum_t softmax(s)[t] * row_t[0:rank]
+ *   lse[b*Q + i, h] = log sum_t exp(s[t])
+ * q bf16 [B*Q, heads, rank + rope], out bf16 [B*Q, heads, rank], lse_opt fp32
+ * [B*Q, heads] or NULL.  The Q tokens are in the cache already.  Products are
+ * accumulated in fp32; the probabilities are rounded to bf16 for the second
+ * product, their sum is not.  A query that sees no token (a sequence shorter
+ * than Q, or a bad id) gets zeros and lse = -inf.
+ * shared_tokens > 0 (a multiple of page_tokens): the first shared_tokens
+ * tokens of all B sequences are the ones in the pages of seqs[0] (as
+ * moe_kv_fork leaves them); they are then read and multiplied once for the
+ * whole batch, and the partial results are merged.
+ * A block-table entry that names no page sets MOE_DEV_ERR_BAD_PAGE; the rows
+ * of that sequence are then unspecified.
+ * Errors: the struct's; MOE_ERR_INVALID_ARG for layer outside [0, n_layers),
+ * B < 0, Q or heads < 1, shared_tokens negative, not a multiple of page_tokens or beyond
+ * max_blocks, a scale that is not finite, NULL q, seqs or out (B > 0);
+ * MOE_ERR_UNSUPPORTED for rank not in {128, 256, 384, 512}, rope not a
+ * multiple of 16 up to 64, B > 4096, Q * heads > 1024, q or out not 16-byte aligned;
+ * MOE_ERR_WORKSPACE / MOE_ERR_UNSUPPORTED for ws.  B = 0 is a no-op. */
+size_t moe_latent_decode_workspace_size(const moe_kv_cache* cache, int B, int Q, int heads, int shared_tokens);
+int moe_latent_decode(const moe_kv_cache* cache, int layer, const void* q, const int32_t* seqs, int B, int Q,
+                      int heads, float scale, int shared_tokens, void* out, float* lse_opt, void* ws,
+                      size_t ws_bytes, uint32_t* dev_status, moe_stream_t stream);
+
+/* ---------------------------------------------------------------- latent attention, expanded form
+ * Causal attention of prompt tokens, keys and values expanded per head from
+ * the cached latents (the form for prompts and chunks of prompts):
+ *   k_t[h] = (w_kv[h, 0:dn] l_t, r_t),  v_t[h] = w_kv[h, dn:dn+dv] l_t   (row_t = (l_t, r_t))
+ *   out[i, h] = sum_t softmax_t(scale * q[i, h] . k_t[h]) v_t[h]
+ * Query rows q_offsets[b] .. q_offsets[b+1]-1 are the newest tokens of
+ * sequence seqs[b], which is in the cache already: with n of them and length
+ * len, row j sees t < len - n + j + 1.  q bf16 [T, heads, dn + rope], w_kv bf16
+ * [heads, dn + dv, rank], out bf16 [T, heads, dv]; q_offsets int32 [B + 1],
+ * ascending from 0 to T.  k and v are rounded to bf16 for the products,
+ * which accumulate in fp32, as do the softmax statistics.
+ * kv_tokens: host bound on the sum of the B lengths (sizes the workspace); a
+ * sum the workspace has no rows for sets MOE_DEV_ERR_CAPACITY and nothing is
+ * written.  A bad id or
+ * query range sets MOE_DEV_ERR_BAD_SEQ, its rows are not written.  A missing page sets
+ * MOE_DEV_ERR_BAD_PAGE, its sequence's rows are unspecified.
+ * Errors: the struct's; MOE_ERR_INVALID_ARG for layer outside [0, n_layers), B or T < 0,
+ * heads < 1, kv_tokens < 0 (< 1 with queries), a scale that is not finite, NULL q, seqs, q_offsets, w_kv or
+ * out (B and T > 0); MOE_ERR_UNSUPPORTED for rank not in {128, 256, 384, 512}, rope not a
+ * multiple of 16 up to 64, dn or dv not 64 or 128, heads > 1024, B > 4096, T * heads or
+ * (kv_tokens + 128 B) * heads above INT_MAX, q, w_kv or out not 16-byte aligned; MOE_ERR_WORKSPACE /
+ * MOE_ERR_UNSUPPORTED for ws.  B = 0 or T = 0 is a no-op. */
+size_t moe_latent_prefill_workspace_size(const moe_kv_cache* cache, int B, int T, int heads, int dn, int dv,
+                                         int kv_tokens);
+int moe_latent_prefill(const moe_kv_cache* cache, int layer, const void* q, const int32_t* seqs,
+                       const int32_t* q_offsets, int B, int T, int heads, int dn, int dv, const void* w_kv,
+                       float scale, int kv_tokens, void* out, void* ws, size_t ws_bytes, uint32_t* dev_status,
+                       moe_stream_t stream);
 
 #ifdef __cplusplus
 }
