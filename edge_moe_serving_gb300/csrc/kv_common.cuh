@@ -70,6 +70,7 @@ inline int check_latent(const moe_kv_cache* c, int layer) {
   if (st != MOE_OK) return st;
   if (layer < 0 || layer >= c->n_layers) return MOE_ERR_INVALID_ARG;
   if ((c->rank % 128) || c->rank > 512 || (c->rope % 16) || c->rope > 64) return MOE_ERR_UNSUPPORTED;
+  if ((long long)c->max_blocks * c->page_tokens > (1 << 27)) return MOE_ERR_UNSUPPORTED;   // tile sums of a batch are ints
   return MOE_OK;
 }
 

@@ -1,97 +1,794 @@
 // Absorbed latent attention over the paged cache: every head's keys are the
-// cached rows themselves and its values their first `rank` entries.
+// cached rows themselves and its values their first `rank` entries, so all
+// heads of a sequence share one pass over its rows.
 //
-// Simple form: one CTA per (query token, head).  Its warps take the tokens in
-// turn; a warp holds the query and its running output in registers, 32 lanes
-// over the row, and keeps the running maximum m and sum l of the softmax
-// (log2 domain), so each row is read once: o and l are scaled by 2^(m - m')
-// when the maximum grows.  The warps' (m, l, o) are joined at the end.
+// Per 64-token tile and up to 64 query rows (a row = one query token of one head):
+//   S   = Q K^T    M = query rows (64), N = tokens, K = rank + rope
+//   O^T += V^T P^T  M = latent entries (128 a slice), N = query rows, K = tokens
+// S is taken with the query rows as M so that a row's softmax is one thread's;
+// O is taken transposed because 64 rows x 512 entries then fill 4 slices x N
+// columns of tensor memory (256 of 512), leaving room for two S tiles, and
+// because few heads cost few columns.  V^T reads the very tile K was read
+// from: the same shared-memory bytes as an operand with M contiguous.
+// P (bf16) overwrites the tile's rotary chunk, which S no longer needs.
+//
+// Softmax: running maximum m and sum l per row in the log2 domain, fp32.  O is
+// rescaled only when a row's maximum rises by more than 2^8: until then the
+// old maximum keeps all terms below 2^8 and the sums exact to fp32 as before.
+//
+// Work: the sequences' tiles form one line that is cut evenly over the CTAs
+// (teams of G CTAs where a sequence has G > 1 row tiles, so that its rows are
+// read from HBM once and from L2 by the others).  A cut sequence leaves fp32
+// partial (O, m, l) per piece; combine_kernel joins the pieces in order.  A
+// shared prefix is a second line: row tiles over the whole batch's query rows
+// against the prefix's tiles.
+//
+// Roles (192 threads): warp 0 = TMA producer, warp 1 = MMA issuer (and TMEM
+// owner), warps 2..5 = softmax, rescaling and epilogue.  Every mbarrier wait is
+// bounded; on expiry the CTA reports MOE_DEV_ERR_TIMEOUT, drains and returns.
 #include <cmath>
 
 #include "kv_common.cuh"
+#include "tc_common.cuh"
 
 namespace moe {
 namespace {
 
-constexpr int kWarps = 8;
-constexpr int kMaxRow = 576;
+using namespace tc;
+
+constexpr int kTok = 64;                 // tokens of a tile
+constexpr int kRows = 64;                // query rows of a tile at most
+constexpr int kChunk = kTok * kBK * 2;   // 8 KB: 64 tokens x 64 entries (also 64 query rows x 64 entries)
+constexpr int kMaxPairs = 4;             // 128-entry slices of the latent
+constexpr int kMaxSlots = 4;             // tiles in flight
+constexpr int kBatch = 512;              // sequences of one launch (lengths and tile sums in shared memory)
+constexpr int kThreads = 192;
+constexpr int kSoftThreads = 128;
+constexpr int kTmemCols = 512;
+constexpr int kSCol = 256;               // S tiles at columns 256 and 320; O slices at 0, 64, 128, 192
+constexpr float kGrow = 8.0f;            // log2 of the growth of a row's maximum that forces a rescaling
 
 struct DecodeParams {
   KvView kv;
-  int layer, B, Q, heads, shared;
-  float scale_log2;   // scale * log2(e): the exponentials are powers of two
-  const __nv_bfloat16* q;
+  int layer, B, Q, heads, rope, shared;
+  int pairs, slots;          // rank / 128; tiles in flight
+  int G, NR, teams;          // row tiles of a sequence, their rows, and CTA teams
+  int Gp, NRp, np, ctas;     // row tiles of the prefix, their rows, prefix tiles; CTAs of the grid
+  float scale_log2;          // scale * log2(e): the exponentials are powers of two
   const int32_t* seqs;
+  const int32_t* prefix_seq;
   __nv_bfloat16* out;
   float* lse;
+  int32_t* plan;             // [B + 1] tile sums, for the combine
+  float* part_s;             // suffix pieces: [2 teams G (+ B G with a prefix)][NR][rank]
+  float4* ml_s;              // their (m, l, l of the rounded probabilities)
+  float* part_p;             // prefix pieces: [2 ctas + Gp][NRp][rank]
+  float4* ml_p;
   uint32_t* status;
 };
 
-__global__ void __launch_bounds__(32 * kWarps)
-decode_simple_kernel(const DecodeParams p) {
-  __shared__ float s_o[kWarps][512];
-  __shared__ float s_m[kWarps], s_l[kWarps];
+struct Seg {
+  int row0, rows, N;   // query rows
+  int b, seq;          // sequence of the batch (suffix) whose tokens these are; its id in the cache
+  int tok0, tok1;
+  float* part;         // where a piece goes; nullptr: the whole sequence, straight to out
+  float4* ml;
+  bool prefix;
+};
+
+__device__ __host__ inline int up16(int v) { return (v + 15) & ~15; }
+__device__ inline int per_cta(long long tiles, int parts) { return (int)((tiles + parts - 1) / parts); }
+
+// A CTA's pieces: first of the prefix line, then of the sequences' line.
+struct SegIter {
+  const DecodeParams& p;
+  const int* pref;
+  const int* len;
+  long long pos, end;
+  int b, team, g, per;
+  bool first;
+  int phase;
+
+  __device__ SegIter(const DecodeParams& p_, const int* pref_, const int* len_) : p(p_), pref(pref_), len(len_) {
+    phase = 0;
+    const long long total = (long long)p.Gp * p.np;
+    const int pp = per_cta(total, p.ctas);
+    pos = min(total, (long long)blockIdx.x * pp);
+    end = min(total, pos + pp);
+    first = true;
+  }
+  __device__ void start_suffix() {
+    phase = 1;
+    first = true;
+    team = blockIdx.x / p.G;
+    g = blockIdx.x - team * p.G;
+    const int total = pref[p.B];
+    per = per_cta(total, p.teams);
+    pos = team < p.teams ? min((long long)total, (long long)team * per) : total;
+    end = min((long long)total, pos + per);
+    int lo = 0, hi = p.B;   // the last b with pref[b] <= pos
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (pref[mid] <= pos) lo = mid;
+      else hi = mid;
+    }
+    b = lo;
+  }
+  __device__ bool next(Seg& s) {
+    const int rank = p.kv.rank;
+    if (phase == 0) {
+      if (pos < end) {
+        const int i = (int)(pos / p.np), x0 = (int)(pos - (long long)i * p.np);
+        const int x1 = (int)min((long long)p.np, x0 + end - pos);
+        s.prefix = true;
+        s.b = 0;
+        s.seq = *p.prefix_seq;
+        s.row0 = i * p.NRp;
+        s.rows = min(p.NRp, p.B * p.Q * p.heads - s.row0);
+        s.tok0 = x0 * kTok;
+        s.tok1 = min(x1 * kTok, p.shared);
+        const int slot = (x0 == 0 && x1 == p.np) ? 2 * p.ctas + i : 2 * blockIdx.x + (first ? 0 : 1);
+        s.part = p.part_p + (size_t)slot * p.NRp * rank;
+        s.ml = p.ml_p + (size_t)slot * p.NRp;
+        s.N = up16(s.rows);
+        pos += x1 - x0;
+        first = false;
+        return true;
+      }
+      start_suffix();
+    }
+    if (pos >= end) return false;
+    while (pref[b + 1] <= pos) ++b;
+    const int n = pref[b + 1] - pref[b], x0 = (int)(pos - pref[b]), x1 = (int)min((long long)n, x0 + end - pos);
+    s.prefix = false;
+    s.b = b;
+    s.seq = p.seqs[b];
+    s.row0 = b * p.Q * p.heads + g * p.NR;
+    s.rows = min(p.NR, p.Q * p.heads - g * p.NR);
+    s.tok0 = p.shared + x0 * kTok;
+    s.tok1 = min(p.shared + x1 * kTok, len[b]);
+    const bool whole = x0 == 0 && x1 == n;
+    s.part = nullptr;
+    s.ml = nullptr;
+    if (!whole || p.np) {
+      const int slot = whole ? 2 * p.teams * p.G + b * p.G + g : 2 * blockIdx.x + (first ? 0 : 1);
+      s.part = p.part_s + (size_t)slot * p.NR * rank;
+      s.ml = p.ml_s + (size_t)slot * p.NR;
+    }
+    s.N = up16(s.rows);
+    pos += x1 - x0;
+    first = false;
+    return true;
+  }
+};
+
+// 32 lanes x 16 consecutive fp32 columns.
+__device__ inline void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+__device__ inline void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};"
+      ::"r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(taddr));
+}
+__device__ inline void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// Descriptor of an operand whose M (or N) index is contiguous: 64-entry
+// chunks `lbo` bytes apart, 8 consecutive k rows (128 bytes each) every 1024.
+__device__ inline uint64_t smem_desc_mn(uint32_t addr, uint32_t lbo) {
+  return (uint64_t)((addr & 0x3FFFFu) >> 4) | (uint64_t)(lbo >> 4) << 16 | (uint64_t)(1024 >> 4) << 32 |
+         (uint64_t)1 << 46 | (uint64_t)2 << 61;
+}
+constexpr uint32_t kTransA = 1u << 15;
+
+__device__ inline float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// A softmax warp's wait: one answer for its lanes, which leave it together (the
+// barrier and tensor-memory instructions that follow are warp-wide).
+__device__ inline bool soft_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+  const bool ok = mbar_wait(bar, parity, abort_flag);
+  return __all_sync(0xffffffffu, ok);
+}
+
+// OR of a predicate over the softmax warps (named barrier 1): the same answer in every thread.
+__device__ inline bool soft_any(bool v) {
+  uint32_t r;
+  __syncwarp();
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n bar.red.or.pred q, 1, %2, p;\n selp.u32 %0, 1, 0, q;\n}\n"
+      : "=r"(r)
+      : "r"((uint32_t)v), "n"(kSoftThreads)
+      : "memory");
+  return r != 0;
+}
+
+struct Shared {
+  uint64_t full[kMaxSlots][kMaxPairs + 1], empty[kMaxSlots][kMaxPairs + 1];   // per 128-entry pair, then the rotary chunk
+  uint64_t q_full, q_empty, s_full[2], s_empty[2], p_full, pv_done, drain;
+  uint32_t tmem;
+  int abort;
+  float factor[kRows];   // rescaling of each row; in the epilogue 1 / l
+  int warp_sum[kThreads / 32];
+  int pref[kBatch + 1];
+  int len[kBatch];
+};
+
+// The MMA issuer's wait: while `bar` is not there yet, `other` is issued as soon as it can be.
+template <typename F>
+__device__ inline bool wait_or(uint64_t* bar, uint32_t parity, volatile int* abort_flag, F&& other) {
+  unsigned long long start = 0;
+  for (uint32_t it = 0;; ++it) {
+    if (mbar_try_wait_parity(bar, parity)) return true;
+    other();
+    if ((it & 63) == 63) {
+      if (*abort_flag) return false;
+      const unsigned long long now = globaltimer_ns();
+      if (start == 0) start = now;
+      else if (now - start > kWaitLimitNs) {
+        *abort_flag = 1;
+        return false;
+      }
+    }
+  }
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+decode_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_constant__ CUtensorMap map_q16,
+              const __grid_constant__ CUtensorMap map_q64, const DecodeParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ Shared sh;
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int chunks = 2 * p.pairs + 1;               // the last one holds the rotary part, then P
+  uint8_t* sq = smem;
+  uint8_t* skv = smem + chunks * kChunk;
+  const int slot_bytes = chunks * kChunk;
+
+  if (tid == 0) {
+    for (int s = 0; s < p.slots; ++s)
+      for (int j = 0; j <= p.pairs; ++j) {
+        mbar_init(&sh.full[s][j], 1);
+        mbar_init(&sh.empty[s][j], 1);
+      }
+    mbar_init(&sh.q_full, 1);
+    mbar_init(&sh.q_empty, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sh.s_full[i], 1);
+      mbar_init(&sh.s_empty[i], kSoftThreads);
+    }
+    mbar_init(&sh.p_full, kSoftThreads);
+    mbar_init(&sh.pv_done, 1);
+    mbar_init(&sh.drain, 1);
+    sh.abort = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&sh.tmem)),
+                 "r"(kTmemCols));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  pdl_wait();
+  // lengths and tile sums of the batch (every CTA for itself)
+  {
+    int carry = 0;
+    for (int b0 = 0; b0 < p.B; b0 += kThreads) {
+      const int b = b0 + tid;
+      int n = 0;
+      if (b < p.B) {
+        const int s = p.seqs[b];
+        const bool good = s >= 0 && s < p.kv.max_seqs;
+        const int len = good ? p.kv.len_of(s) : 0;
+        if (!good && blockIdx.x == 0) set_status(p.status, MOE_DEV_ERR_BAD_SEQ);
+        sh.len[b] = len;
+        n = len > p.shared ? (len - p.shared + kTok - 1) / kTok : 0;
+      }
+      int inc = n;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += u;
+      }
+      if (lane == 31) sh.warp_sum[warp] = inc;
+      __syncthreads();
+      int base = carry;
+      for (int w = 0; w < warp; ++w) base += sh.warp_sum[w];
+      for (int w = 0; w < kThreads / 32; ++w) carry += sh.warp_sum[w];
+      if (b < p.B) sh.pref[b + 1] = base + inc;
+      __syncthreads();
+    }
+    if (tid == 0) sh.pref[0] = 0;
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (blockIdx.x == 0)
+    for (int b = tid; b <= p.B; b += kThreads) p.plan[b] = sh.pref[b];
+  const uint32_t tmem = sh.tmem;
+  volatile int* abort_flag = &sh.abort;
+  SegIter it(p, sh.pref, sh.len);
+  Seg sg;
+
+  if (warp == 0) {
+    // ------------------------------------------------ TMA producer
+    int tile = 0, nseg = 0;
+    bool q_armed = false, ok = true;
+    const int page = p.kv.page_tokens, box = min(page, kTok), boxes = kTok / box;
+    const bool pseq_ok = p.np == 0 || (*p.prefix_seq >= 0 && *p.prefix_seq < p.kv.max_seqs);
+    while (ok && it.next(sg)) {
+      if (lane == 0) {
+        ok = mbar_wait(&sh.q_empty, (nseg & 1) ^ 1u, abort_flag);
+        if (ok) {
+          const int cq = 2 * p.pairs + (p.rope ? 1 : 0);
+          mbar_expect_tx(&sh.q_full, (uint32_t)(cq * sg.N * 128));
+          q_armed = true;
+          for (int c = 0; c < cq; ++c) {
+            if (sg.N == kRows) tma_load_2d(sq + c * kChunk, &map_q64, &sh.q_full, c * kBK, sg.row0);
+            else
+              for (int r = 0; r < sg.N; r += 16)
+                tma_load_2d(sq + c * kChunk + r * 128, &map_q16, &sh.q_full, c * kBK, sg.row0 + r);
+          }
+        }
+      }
+      ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
+      ++nseg;
+      const bool seq_ok = sg.prefix ? pseq_ok : true;   // a bad id in the batch has no tokens
+      for (int t0 = sg.tok0; ok && t0 < sg.tok1; t0 += kTok, ++tile) {
+        const int n_tok = min(kTok, sg.tok1 - t0);
+        const int nb = (n_tok + box - 1) / box;         // boxes that hold tokens
+        int row = 0;
+        if (lane < boxes && lane < nb) {
+          const int t = t0 + lane * box;
+          int pg = seq_ok ? p.kv.table[(size_t)sg.seq * p.kv.max_blocks + (t >> p.kv.page_shift)] : -1;
+          if (pg < 0 || pg >= p.kv.n_pages) {
+            set_status(p.status, seq_ok ? MOE_DEV_ERR_BAD_PAGE : MOE_DEV_ERR_BAD_SEQ);
+            pg = 0;
+          }
+          row = (p.layer * p.kv.n_pages + pg) * page + (t & (page - 1));
+        }
+        const int slot = tile % p.slots;
+        const uint32_t par = ((tile / p.slots) & 1) ^ 1u;
+        uint8_t* base = skv + slot * slot_bytes;
+        for (int j = 0; j <= p.pairs && ok; ++j) {
+          if (j == p.pairs && p.rope == 0) break;
+          if (lane == 0) {
+            ok = mbar_wait(&sh.empty[slot][j], par, abort_flag);
+            if (ok) mbar_expect_tx(&sh.full[slot][j], (uint32_t)(nb * box * 128 * (j < p.pairs ? 2 : 1)));
+          }
+          ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
+          if (!ok) break;
+          for (int i = 0; i < nb; ++i) {
+            const int r = __shfl_sync(0xffffffffu, row, i);
+            if (lane == 0) {
+              uint8_t* dst = base + 2 * j * kChunk + i * box * 128;
+              tma_load_2d(dst, &map_kv, &sh.full[slot][j], 2 * j * kBK, r);
+              if (j < p.pairs) tma_load_2d(dst + kChunk, &map_kv, &sh.full[slot][j], 2 * j * kBK + kBK, r);
+            }
+          }
+        }
+      }
+    }
+    // drain: whatever was asked for lands before the CTA can exit (a barrier's
+    // latest load is its latest phase; after an abort the last tile's barriers
+    // may not all be armed, and the bounded wait outlasts any copy)
+    if (lane == 0) {
+      volatile int no_abort = 0;
+      if (q_armed) mbar_wait(&sh.q_full, (nseg - 1) & 1, &no_abort);
+      for (int s = 0; s < p.slots; ++s) {
+        const int loads = tile / p.slots + (tile % p.slots > s ? 1 : 0);
+        for (int j = 0; j <= p.pairs; ++j) {
+          if (j == p.pairs && p.rope == 0) break;
+          if (loads > 0) mbar_wait(&sh.full[s][j], (loads - 1) & 1, &no_abort);
+        }
+      }
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------ MMA issuer
+    if (lane == 0) {
+      int tile = 0, nseg = 0;
+      bool issued = false, ok = true;
+      bool pending = false, pv_first = false;
+      int pv_tile = 0, pv_n = 0;
+      const uint32_t idesc_s = make_idesc(64, kTok);
+      const uint32_t q0 = smem_u32(sq);
+      auto issue_pv = [&]() {
+        tc_fence_after();
+        const int slot = pv_tile % p.slots;
+        const uint32_t base = smem_u32(skv + slot * slot_bytes);
+        const uint32_t pb = base + 2 * p.pairs * kChunk;
+        const uint32_t idesc = make_idesc(128, pv_n) | kTransA;
+        for (int j = 0; j < p.pairs; ++j) {
+#pragma unroll
+          for (int k = 0; k < kTok / kUK; ++k)
+            tc_mma(tmem + j * kRows, smem_desc_mn(base + 2 * j * kChunk + k * kUK * 128, kChunk),
+                   smem_desc(pb + k * kUK * 2), idesc, (pv_first && k == 0) ? 0u : 1u);
+          tc_commit(&sh.empty[slot][j]);
+        }
+        if (p.rope) tc_commit(&sh.empty[slot][p.pairs]);
+        tc_commit(&sh.pv_done);
+        pending = false;
+      };
+      auto maybe_pv = [&]() {
+        if (pending && mbar_try_wait_parity(&sh.p_full, pv_tile & 1)) issue_pv();
+      };
+      while (ok && it.next(sg)) {
+        ok = wait_or(&sh.q_full, nseg & 1, abort_flag, maybe_pv);
+        for (int t0 = sg.tok0; ok && t0 < sg.tok1; t0 += kTok, ++tile) {
+          const int slot = tile % p.slots, buf = tile & 1;
+          const uint32_t par = (tile / p.slots) & 1;
+          ok = wait_or(&sh.s_empty[buf], ((tile >> 1) & 1) ^ 1u, abort_flag, maybe_pv);
+          if (!ok) break;
+          const uint32_t base = smem_u32(skv + slot * slot_bytes);
+          const uint32_t d = tmem + kSCol + buf * kTok;
+          for (int j = 0; j <= p.pairs; ++j) {
+            const int steps = j < p.pairs ? 8 : p.rope / kUK;
+            if (steps == 0) break;
+            ok = wait_or(&sh.full[slot][j], par, abort_flag, maybe_pv);
+            if (!ok) break;
+            tc_fence_after();
+            for (int k = 0; k < steps; ++k) {
+              const uint32_t off = (2 * j + (k >> 2)) * kChunk + (k & 3) * kUK * 2;
+              tc_mma(d, smem_desc(q0 + off), smem_desc(base + off), idesc_s, (j | k) ? 1u : 0u);
+            }
+            issued = true;
+          }
+          if (!ok) break;
+          tc_commit(&sh.s_full[buf]);
+          if (t0 + kTok >= sg.tok1) tc_commit(&sh.q_empty);
+          if (pending) {
+            ok = mbar_wait(&sh.p_full, pv_tile & 1, abort_flag);
+            if (!ok) break;
+            issue_pv();
+          }
+          pending = true;
+          pv_first = t0 == sg.tok0;
+          pv_tile = tile;
+          pv_n = sg.N;
+        }
+        ++nseg;
+      }
+      if (ok && pending) {
+        if (mbar_wait(&sh.p_full, pv_tile & 1, abort_flag)) issue_pv();
+      }
+      if (issued) {   // every issued MMA completes before tensor memory is released
+        volatile int no_abort = 0;
+        tc_commit(&sh.drain);
+        mbar_wait(&sh.drain, 0, &no_abort);
+      }
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------ softmax, rescaling, epilogue
+    const int quarter = warp & 3, st = tid - 64;
+    const uint32_t lane_base = tmem + ((uint32_t)(quarter * 32) << 16);
+    const int r = quarter * 16 + lane;          // this thread's query row (lanes 0..15): M = 64 fills 16 lanes a quarter
+    const int rank = p.kv.rank;
+    int tile = 0;
+    bool fail = false;
+    while (!fail && it.next(sg)) {
+      const bool active = lane < 16 && r < sg.rows;
+      int limit = 0;
+      if (active) {
+        const int gr = sg.row0 + r, bq = gr / p.heads, b = bq / p.Q;
+        limit = sh.len[b] - p.Q + (bq - b * p.Q) + 1;
+      }
+      float m = -INFINITY;
+      float2 l = make_float2(0.0f, 0.0f);   // sum of the probabilities, and of what they are rounded to
+      for (int t0 = sg.tok0; t0 < sg.tok1; t0 += kTok, ++tile) {
+        const int buf = tile & 1, slot = tile % p.slots;
+        const int n_tok = min(kTok, sg.tok1 - t0);
+        const int see = active ? max(0, min(n_tok, limit - t0)) : 0;
+        const bool ok = soft_wait(&sh.s_full[buf], (tile >> 1) & 1, abort_flag);
+        float s[kTok];
+        if (ok) {
+          tc_fence_after();
+          uint32_t(&u)[kTok] = reinterpret_cast<uint32_t(&)[kTok]>(s);
+          tmem_ld32(lane_base + kSCol + buf * kTok, *reinterpret_cast<uint32_t(*)[32]>(&u[0]));
+          tmem_ld32(lane_base + kSCol + buf * kTok + 32, *reinterpret_cast<uint32_t(*)[32]>(&u[32]));
+          tmem_ld_wait();
+          tc_fence_before();
+          mbar_arrive(&sh.s_empty[buf]);
+        }
+        float top = -INFINITY;
+        if (__all_sync(0xffffffffu, see == kTok || !active)) {
+#pragma unroll
+          for (int j = 0; j < kTok; ++j) {
+            s[j] *= p.scale_log2;
+            top = fmaxf(top, s[j]);
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < kTok; ++j) {
+            s[j] = j < see ? s[j] * p.scale_log2 : -INFINITY;
+            top = fmaxf(top, s[j]);
+          }
+        }
+        float f = 1.0f;
+        bool grow = false;
+        if (active && top > m) {
+          if (m == -INFINITY) {
+            m = top;             // nothing summed for this row yet
+          } else if (top > m + kGrow) {
+            f = ex2(m - top);
+            l.x *= f;
+            l.y *= f;
+            m = top;
+            grow = true;
+          }
+        }
+        if (lane < 16) sh.factor[r] = f;
+        fail = soft_any(!ok);
+        if (fail) break;
+        if (soft_any(grow)) {
+          // O was last added to by the previous tile's product (the one before it preceded this S in issue order,
+          // so the parity is this product's), and this tile's waits for us
+          const bool done = soft_wait(&sh.pv_done, (tile - 1) & 1, abort_flag);
+          fail = soft_any(!done);
+          if (fail) break;
+          tc_fence_after();
+          for (int j = 0; j < p.pairs; ++j)
+            for (int c = 0; c < sg.N; c += 16) {
+              uint32_t v[16];
+              tmem_ld16(lane_base + j * kRows + c, v);
+              tmem_ld_wait();
+#pragma unroll
+              for (int x = 0; x < 16; ++x) v[x] = __float_as_uint(__uint_as_float(v[x]) * sh.factor[c + x]);
+              tmem_st16(lane_base + j * kRows + c, v);
+            }
+          tmem_st_wait();
+          soft_any(false);       // everyone has read the factors
+        }
+        // Probabilities, rounded to bf16 (the cache's type, the only one the product takes beside it).  Two sums:
+        // of the rounded ones, which the output is divided by (its weights then add up to one, and where few tokens
+        // carry the row most of their rounding cancels), and of the unrounded ones for the log-sum-exp.
+        uint8_t* sp = skv + slot * slot_bytes + 2 * p.pairs * kChunk;
+        if (lane < 16 && r < sg.N) {
+          const float ref = m == -INFINITY ? 0.0f : m;
+          uint8_t* prow = sp + r * 128;
+#pragma unroll
+          for (int v = 0; v < kTok / 8; ++v) {
+            uint32_t w[4];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              const float a = active ? ex2(s[8 * v + 2 * x] - ref) : 0.0f;
+              const float b = active ? ex2(s[8 * v + 2 * x + 1] - ref) : 0.0f;
+              const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+              w[x] = *reinterpret_cast<const uint32_t*>(&h);
+              l.x += a + b;
+              l.y += bf16_lo(w[x]) + bf16_hi(w[x]);
+            }
+            *reinterpret_cast<uint4*>(prow + ((v ^ (r & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        }
+        if (n_tok < kTok) {
+          // places past the last token: any bits may stand there, and 0 * NaN is NaN
+          uint8_t* base = skv + slot * slot_bytes;
+          const int rows = kTok - n_tok;
+          for (int x = st; x < rows * 8 * 2 * p.pairs; x += kSoftThreads) {
+            const int c = x / (rows * 8), y = x - c * rows * 8;
+            *reinterpret_cast<uint4*>(base + c * kChunk + n_tok * 128 + y * 16) = make_uint4(0, 0, 0, 0);
+          }
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        tc_fence_before();
+        mbar_arrive(&sh.p_full);
+      }
+      if (fail) break;
+      // The last S was issued before the product of the tile ahead of it, so that
+      // product may be under way too: its phase first, or the parity would name an older one.
+      const bool done = (tile < 2 || soft_wait(&sh.pv_done, (tile - 2) & 1, abort_flag)) &&
+                        soft_wait(&sh.pv_done, (tile - 1) & 1, abort_flag);
+      if (lane < 16) sh.factor[r] = l.y == 0.0f ? 0.0f : 1.0f / l.y;
+      if (active) {
+        if (sg.part) sg.ml[r] = make_float4(m, l.x, l.y, 0.0f);
+        else if (p.lse) p.lse[sg.row0 + r] = l.x == 0.0f ? -INFINITY : (m + log2f(l.x)) * 0.6931471805599453f;
+      }
+      fail = soft_any(!done);
+      if (fail) break;
+      tc_fence_after();
+      for (int j = 0; j < p.pairs; ++j) {
+        const int dim = j * 128 + quarter * 32 + lane;
+        for (int c = 0; c < sg.N; c += 16) {
+          uint32_t v[16];
+          tmem_ld16(lane_base + j * kRows + c, v);
+          tmem_ld_wait();
+#pragma unroll
+          for (int x = 0; x < 16; ++x) {
+            if (c + x < sg.rows) {
+              if (sg.part) sg.part[(size_t)(c + x) * rank + dim] = __uint_as_float(v[x]);
+              else
+                p.out[(size_t)(sg.row0 + c + x) * rank + dim] =
+                    __float2bfloat16_rn(__uint_as_float(v[x]) * sh.factor[c + x]);
+            }
+          }
+        }
+      }
+      tc_fence_before();
+      soft_any(false);   // the factors are free again
+    }
+  }
+  pdl_trigger();
+  __syncthreads();
+  if (*abort_flag && tid == 0) set_status(p.status, MOE_DEV_ERR_TIMEOUT);
+  tc_fence_after();
+  if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols));
+}
+
+// ---------------------------------------------------------------- combine
+// One CTA per query row: its pieces' (m, l, O) in a fixed order (the prefix's
+// pieces, then the sequence's).  rank / 4 threads cover the row with float4; the
+// rest of the CTA's 256 threads take other pieces, joined through shared memory.
+constexpr int kCombineThreads = 256;
+
+__global__ void __launch_bounds__(kCombineThreads)
+combine_parts_kernel(const DecodeParams p) {
+  __shared__ float4 s_acc[kCombineThreads];
   pdl_wait();
   pdl_trigger();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int row = p.kv.row, rank = p.kv.rank;
-  const size_t qrow = blockIdx.x;   // (b*Q + i)*heads + h
-  const int bq = (int)(qrow / p.heads), b = bq / p.Q, i = bq - b * p.Q;
-  const int seq = p.seqs[b], prefix_seq = p.seqs[0];
-  const bool good = seq >= 0 && seq < p.kv.max_seqs && prefix_seq >= 0 && prefix_seq < p.kv.max_seqs;
-  if (!good && threadIdx.x == 0) set_status(p.status, MOE_DEV_ERR_BAD_SEQ);
-  const int limit = good ? p.kv.len_of(seq) - p.Q + i + 1 : 0;
-  float q[kMaxRow / 32], o[512 / 32];
-#pragma unroll
-  for (int j = 0; j < kMaxRow / 32; ++j) {
-    const int d = lane + 32 * j;
-    q[j] = d < row ? __bfloat162float(p.q[qrow * row + d]) : 0.0f;
+  const int row = blockIdx.x, rank = p.kv.rank;
+  const int per_seq = p.Q * p.heads, b = row / per_seq, in_seq = row - b * per_seq;
+  const int total = p.plan[p.B], x0 = p.plan[b], x1 = p.plan[b + 1];
+  const int per = per_cta(total, p.teams);
+  const int t0 = x1 > x0 ? x0 / per : 0, t1 = x1 > x0 ? (x1 - 1) / per : -1;
+  const int n_s = t1 - t0 + 1;
+  int n_p = 0, c0 = 0, pp = 1, i = 0;
+  if (p.np) {
+    pp = per_cta((long long)p.Gp * p.np, p.ctas);
+    i = row / p.NRp;
+    c0 = (int)((long long)i * p.np / pp);
+    n_p = (int)(((long long)(i + 1) * p.np - 1) / pp) - c0 + 1;
+  } else if (n_s == 1) {
+    return;   // written by decode_kernel
   }
-#pragma unroll
-  for (int j = 0; j < 512 / 32; ++j) o[j] = 0.0f;
-  float m = -INFINITY, l = 0.0f;
-  for (int t = warp; t < limit; t += kWarps) {
-    const int s = t < p.shared ? prefix_seq : seq;
-    int page = p.kv.table[(size_t)s * p.kv.max_blocks + (t >> p.kv.page_shift)];
-    if (page < 0 || page >= p.kv.n_pages) {
-      if (lane == 0) set_status(p.status, MOE_DEV_ERR_BAD_PAGE);
-      page = 0;
+  const int g = in_seq / p.NR;
+  // piece k: its rows and statistics
+  auto piece = [&](int k, const float*& o, float4& ml) {
+    if (k < n_p) {
+      const int c = c0 + k;
+      const long long a = (long long)i * p.np, z = a + p.np, from = (long long)c * pp;
+      const int slot = (a >= from && z <= from + pp) ? 2 * p.ctas + i : 2 * c + (a > from ? 1 : 0);
+      const size_t at = (size_t)slot * p.NRp + (row - i * p.NRp);
+      o = p.part_p + at * rank;
+      ml = p.ml_p[at];
+    } else {
+      const int t = t0 + k - n_p;
+      const long long from = (long long)t * per;
+      const int cta = t * p.G + g;
+      const int slot = (x0 >= from && x1 <= from + per) ? 2 * p.teams * p.G + b * p.G + g : 2 * cta + (x0 > from ? 1 : 0);
+      const size_t at = (size_t)slot * p.NR + (in_seq - g * p.NR);
+      o = p.part_s + at * rank;
+      ml = p.ml_s[at];
     }
-    const __nv_bfloat16* k = p.kv.pages + p.kv.row_offset(p.layer, page, t & (p.kv.page_tokens - 1));
-    float x[kMaxRow / 32], dot = 0.0f;
-#pragma unroll
-    for (int j = 0; j < kMaxRow / 32; ++j) {
-      const int d = lane + 32 * j;
-      x[j] = d < row ? __bfloat162float(k[d]) : 0.0f;
-      dot = fmaf(q[j], x[j], dot);
-    }
-    const float s2 = warp_sum(dot) * p.scale_log2;
-    const float mn = fmaxf(m, s2);
-    const float ref = mn == -INFINITY ? 0.0f : mn;
-    const float f = exp2f(m - ref), w = exp2f(s2 - ref);
-    l = fmaf(l, f, w);
-#pragma unroll
-    for (int j = 0; j < 512 / 32; ++j) o[j] = fmaf(w, x[j], o[j] * f);
-    m = mn;
-  }
-#pragma unroll
-  for (int j = 0; j < 512 / 32; ++j) s_o[warp][lane + 32 * j] = o[j];
-  if (lane == 0) {
-    s_m[warp] = m;
-    s_l[warp] = l;
-  }
-  __syncthreads();
+  };
+  const int n = n_p + n_s, quads = rank / 4, groups = kCombineThreads / quads;
+  const int v = threadIdx.x % quads, grp = threadIdx.x / quads;
+  const float* o;
+  float4 ml;
   float top = -INFINITY;
-  for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s_m[w]);
-  const float ref = top == -INFINITY ? 0.0f : top;
-  float sum = 0.0f;
-  for (int w = 0; w < kWarps; ++w) sum = fmaf(s_l[w], exp2f(s_m[w] - ref), sum);
-  for (int d = threadIdx.x; d < rank; d += blockDim.x) {
-    float v = 0.0f;
-    for (int w = 0; w < kWarps; ++w) v = fmaf(s_o[w][d], exp2f(s_m[w] - ref), v);
-    p.out[qrow * rank + d] = __float2bfloat16_rn(limit > 0 ? v / sum : 0.0f);
+  for (int k = 0; k < n; ++k) {
+    piece(k, o, ml);
+    top = fmaxf(top, ml.x);
   }
-  if (p.lse && threadIdx.x == 0) p.lse[qrow] = limit > 0 ? (ref + log2f(sum)) * 0.6931471805599453f : -INFINITY;
+  const float ref = top == -INFINITY ? 0.0f : top;
+  float l = 0.0f, lr = 0.0f;
+  for (int k = 0; k < n; ++k) {
+    piece(k, o, ml);
+    const float w = ex2(ml.x - ref);
+    l = fmaf(ml.y, w, l);
+    lr = fmaf(ml.z, w, lr);
+  }
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (grp < groups)
+    for (int k = grp; k < n; k += groups) {
+      piece(k, o, ml);
+      const float w = ex2(ml.x - ref);
+      const float4 x = reinterpret_cast<const float4*>(o)[v];
+      acc.x = fmaf(w, x.x, acc.x);
+      acc.y = fmaf(w, x.y, acc.y);
+      acc.z = fmaf(w, x.z, acc.z);
+      acc.w = fmaf(w, x.w, acc.w);
+    }
+  s_acc[threadIdx.x] = acc;
+  __syncthreads();
+  if (threadIdx.x < quads) {
+    for (int q = 1; q < groups; ++q) {
+      const float4 x = s_acc[threadIdx.x + q * quads];
+      acc.x += x.x;
+      acc.y += x.y;
+      acc.z += x.z;
+      acc.w += x.w;
+    }
+    const float inv = lr == 0.0f ? 0.0f : 1.0f / lr;
+    const __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x * inv, acc.y * inv);
+    const __nv_bfloat162 hi = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
+    uint2 packed;
+    packed.x = *reinterpret_cast<const uint32_t*>(&lo);
+    packed.y = *reinterpret_cast<const uint32_t*>(&hi);
+    reinterpret_cast<uint2*>(p.out + (size_t)row * rank)[v] = packed;
+  }
+  if (p.lse && threadIdx.x == 0) p.lse[row] = l == 0.0f ? -INFINITY : (ref + log2f(l)) * 0.6931471805599453f;
+}
+
+// ---------------------------------------------------------------- host side
+struct Tiles {
+  int n, rows;   // row tiles and their rows
+};
+// rows split into tiles of at most 64, evenly, in multiples of 16
+Tiles row_tiles(long long rows) {
+  Tiles t;
+  t.n = (int)((rows + kRows - 1) / kRows);
+  t.rows = up16((int)((rows + t.n - 1) / t.n));
+  t.n = (int)((rows + t.rows - 1) / t.rows);
+  return t;
+}
+
+struct DecodeWs {
+  size_t plan, part_s, ml_s, part_p, ml_p, bytes;
+};
+
+void fill_shape(DecodeParams& p, const moe_kv_cache& c, int B, int Q, int heads, int shared) {
+  p.B = B;
+  p.Q = Q;
+  p.heads = heads;
+  p.shared = shared;
+  p.rope = c.rope;
+  p.pairs = c.rank / 128;
+  p.ctas = num_sms();
+  const Tiles s = row_tiles((long long)Q * heads), f = row_tiles((long long)B * Q * heads);
+  p.G = s.n;
+  p.NR = s.rows;
+  p.teams = p.ctas / s.n;
+  p.np = (shared + kTok - 1) / kTok;
+  p.Gp = p.np ? f.n : 0;
+  p.NRp = f.rows;
+}
+
+DecodeWs decode_ws(const DecodeParams& p, int rank) {
+  DecodeWs w;
+  const size_t ns = (size_t)2 * p.teams * p.G + (p.np ? (size_t)p.B * p.G : 0), np = p.np ? (size_t)2 * p.ctas + p.Gp : 0;
+  w.plan = 0;
+  size_t at = align_up((size_t)(p.B + 1) * sizeof(int32_t), 256);
+  w.part_s = at;
+  at += align_up(ns * p.NR * rank * sizeof(float), 256);
+  w.ml_s = at;
+  at += align_up(ns * p.NR * sizeof(float4), 256);
+  w.part_p = at;
+  at += align_up(np * p.NRp * rank * sizeof(float), 256);
+  w.ml_p = at;
+  at += align_up(np * p.NRp * sizeof(float4), 256);
+  w.bytes = at;
+  return w;
+}
+
+bool decode_shape_ok(int B, int Q, int heads) { return B <= 4096 && (long long)Q * heads <= 1024; }
+
+int launch_decode(const moe_kv_cache& c, DecodeParams p, const void* q, cudaStream_t s) {
+  static_assert(sizeof(Shared) + 1024 + (2 * kMaxPairs + 1) * kChunk * 3 <= 227 * 1024, "shared memory");
+  const int row = c.rank + c.rope, slot = (2 * p.pairs + 1) * kChunk;
+  p.slots = (int)((227 * 1024 - sizeof(Shared) - 1024 - slot) / slot);   // what the query tile leaves
+  if (p.slots > kMaxSlots) p.slots = kMaxSlots;
+  const int smem = (1 + p.slots) * slot + 1024;
+  CUtensorMap kv, q16, q64;
+  const uint64_t rows = (uint64_t)c.n_layers * c.n_pages * c.page_tokens, qrows = (uint64_t)p.B * p.Q * p.heads;
+  if (!make_map(&kv, c.pages, row, rows, c.page_tokens < kTok ? c.page_tokens : kTok) ||
+      !make_map(&q16, q, row, qrows, 16) || !make_map(&q64, q, row, qrows, 64))
+    return MOE_ERR_CUDA;
+  static std::atomic<unsigned char> attr[kMaxDevices];
+  cudaError_t e = once_per_device(attr, [] {
+    return cudaFuncSetAttribute(decode_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                227 * 1024 - (int)sizeof(Shared));
+  });
+  if (e == cudaSuccess) e = launch_k(decode_kernel, p.ctas, kThreads, smem, s, kv, q16, q64, p);
+  if (e == cudaSuccess) e = launch_k(combine_parts_kernel, (unsigned)qrows, kCombineThreads, 0, s, p);
+  return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
 }  // namespace
@@ -102,40 +799,51 @@ using namespace moe;
 extern "C" {
 
 size_t moe_latent_decode_workspace_size(const moe_kv_cache* cache, int B, int Q, int heads, int shared_tokens) {
-  (void)cache, (void)B, (void)Q, (void)heads, (void)shared_tokens;
-  return 0;
+  if (check_latent(cache, 0) != MOE_OK || B < 1 || Q < 1 || heads < 1 || shared_tokens < 0) return 0;
+  if (!decode_shape_ok(B, Q, heads)) return 0;
+  DecodeParams p = {};
+  fill_shape(p, *cache, B < kBatch ? B : kBatch, Q, heads, shared_tokens);
+  return decode_ws(p, cache->rank).bytes;
 }
 
 int moe_latent_decode(const moe_kv_cache* cache, int layer, const void* q, const int32_t* seqs, int B, int Q,
                       int heads, float scale, int shared_tokens, void* out, float* lse_opt, void* ws, size_t ws_bytes,
                       uint32_t* dev_status, moe_stream_t stream) {
-  const int st = check_latent(cache, layer);
+  int st = check_latent(cache, layer);
   if (st == MOE_ERR_INVALID_ARG || check_kv(cache) != MOE_OK) return st;
   if (B < 0 || Q < 1 || heads < 1 || shared_tokens < 0 || !std::isfinite(scale)) return MOE_ERR_INVALID_ARG;
   if (shared_tokens % cache->page_tokens || shared_tokens / cache->page_tokens > cache->max_blocks)
     return MOE_ERR_INVALID_ARG;
   if (B > 0 && (!q || !seqs || !out)) return MOE_ERR_INVALID_ARG;
   if (st != MOE_OK) return st;
-  if (B > 4096 || (long long)Q * heads > 1024) return MOE_ERR_UNSUPPORTED;
+  if (!decode_shape_ok(B, Q, heads)) return MOE_ERR_UNSUPPORTED;
   if (B == 0) return MOE_OK;
   if (!kv_aligned(q, 16) || !kv_aligned(out, 16)) return MOE_ERR_UNSUPPORTED;
-  (void)ws, (void)ws_bytes;
-  DecodeParams p;
-  p.kv = kv_view(*cache);
-  p.layer = layer;
-  p.B = B;
-  p.Q = Q;
-  p.heads = heads;
-  p.shared = shared_tokens;
-  p.scale_log2 = scale * 1.4426950408889634f;
-  p.q = reinterpret_cast<const __nv_bfloat16*>(q);
-  p.seqs = seqs;
-  p.out = reinterpret_cast<__nv_bfloat16*>(out);
-  p.lse = lse_opt;
-  p.status = dev_status;
-  const cudaError_t e = launch_k(decode_simple_kernel, B * Q * heads, 32 * kWarps, 0,
-                                 reinterpret_cast<cudaStream_t>(stream), p);
-  return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+  st = check_ws(ws, ws_bytes, moe_latent_decode_workspace_size(cache, B, Q, heads, shared_tokens));
+  if (st != MOE_OK) return st;
+  for (int b0 = 0; b0 < B && st == MOE_OK; b0 += kBatch) {   // batches of more than 512 sequences: several launches
+    DecodeParams p = {};
+    fill_shape(p, *cache, B - b0 < kBatch ? B - b0 : kBatch, Q, heads, shared_tokens);
+    const DecodeWs w = decode_ws(p, cache->rank);
+    char* base = reinterpret_cast<char*>(ws);
+    const size_t row0 = (size_t)b0 * Q * heads;
+    p.kv = kv_view(*cache);
+    p.layer = layer;
+    p.scale_log2 = scale * 1.4426950408889634f;
+    p.seqs = seqs + b0;
+    p.prefix_seq = seqs;
+    p.out = reinterpret_cast<__nv_bfloat16*>(out) + row0 * cache->rank;
+    p.lse = lse_opt ? lse_opt + row0 : nullptr;
+    p.plan = reinterpret_cast<int32_t*>(base + w.plan);
+    p.part_s = reinterpret_cast<float*>(base + w.part_s);
+    p.ml_s = reinterpret_cast<float4*>(base + w.ml_s);
+    p.part_p = reinterpret_cast<float*>(base + w.part_p);
+    p.ml_p = reinterpret_cast<float4*>(base + w.ml_p);
+    p.status = dev_status;
+    st = launch_decode(*cache, p, reinterpret_cast<const __nv_bfloat16*>(q) + row0 * (cache->rank + cache->rope),
+                       reinterpret_cast<cudaStream_t>(stream));
+  }
+  return st;
 }
 
 }  // extern "C"

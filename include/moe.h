@@ -641,7 +641,9 @@ int moe_kv_compact(const moe_kv_cache* cache, int32_t* n_live_opt, void* ws, siz
  * q bf16 [B*Q, heads, rank + rope], out bf16 [B*Q, heads, rank], lse_opt fp32
  * [B*Q, heads] or NULL.  The Q tokens are in the cache already.  Products are
  * accumulated in fp32; the probabilities are rounded to bf16 for the second
- * product, their sum is not.  A query that sees no token (a sequence shorter
+ * product and divided by the sum of the rounded ones; lse comes from the
+ * unrounded ones.  A cached value that is NaN or infinite reaches
+ * every query of its sequence.  A query that sees no token (a sequence shorter
  * than Q, or a bad id) gets zeros and lse = -inf.
  * shared_tokens > 0 (a multiple of page_tokens): the first shared_tokens
  * tokens of all B sequences are the ones in the pages of seqs[0] (as
@@ -653,7 +655,7 @@ int moe_kv_compact(const moe_kv_cache* cache, int32_t* n_live_opt, void* ws, siz
  * B < 0, Q or heads < 1, shared_tokens negative, not a multiple of page_tokens or beyond
  * max_blocks, a scale that is not finite, NULL q, seqs or out (B > 0);
  * MOE_ERR_UNSUPPORTED for rank not in {128, 256, 384, 512}, rope not a
- * multiple of 16 up to 64, B > 4096, Q * heads > 1024, q or out not 16-byte aligned;
+ * multiple of 16 up to 64, max_blocks * page_tokens above 2^27, B > 4096, Q * heads > 1024, q or out not 16-byte aligned;
  * MOE_ERR_WORKSPACE / MOE_ERR_UNSUPPORTED for ws.  B = 0 is a no-op. */
 size_t moe_latent_decode_workspace_size(const moe_kv_cache* cache, int B, int Q, int heads, int shared_tokens);
 int moe_latent_decode(const moe_kv_cache* cache, int layer, const void* q, const int32_t* seqs, int B, int Q,
@@ -679,7 +681,7 @@ int moe_latent_decode(const moe_kv_cache* cache, int layer, const void* q, const
  * Errors: the struct's; MOE_ERR_INVALID_ARG for layer outside [0, n_layers), B or T < 0,
  * heads < 1, kv_tokens < 0 (< 1 with queries), a scale that is not finite, NULL q, seqs, q_offsets, w_kv or
  * out (B and T > 0); MOE_ERR_UNSUPPORTED for rank not in {128, 256, 384, 512}, rope not a
- * multiple of 16 up to 64, dn or dv not 64 or 128, heads > 1024, B > 4096, T * heads or
+ * multiple of 16 up to 64, max_blocks * page_tokens above 2^27, dn or dv not 64 or 128, heads > 1024, B > 4096, T * heads or
  * (kv_tokens + 128 B) * heads above INT_MAX, q, w_kv or out not 16-byte aligned; MOE_ERR_WORKSPACE /
  * MOE_ERR_UNSUPPORTED for ws.  B = 0 or T = 0 is a no-op. */
 size_t moe_latent_prefill_workspace_size(const moe_kv_cache* cache, int B, int T, int heads, int dn, int dv,

@@ -1,7 +1,8 @@
 """Latent attention over the paged cache (absorbed, shared prefix, expanded)
 against the definition in 64 bits, on caches whose unused places hold NaN.
 
-Bounds, from the roundings the header states (u = 2^-9 is half a bf16 step):
+Bounds, from the roundings the header states (u = 2^-8, the unit roundoff of
+bf16's 8 significand bits: 1 + 2^-8 rounds to 1):
 * absorbed: the probabilities are rounded to bf16 (each off by at most u of
   itself), the output once more, everything else is fp32: scores of a few
   hundred products carry about 2^-24 * sqrt(576) * sum|q||k| scale < 2^-14, which
@@ -24,7 +25,7 @@ from kv_helpers import DEV, Paged, attend64
 
 pytestmark = pytest.mark.gpu
 
-U = 2.0 ** -9
+U = 2.0 ** -8
 LSE_TOL = 2.0 ** -11
 
 
