@@ -23,9 +23,12 @@
 // shared prefix is a second line: row tiles over the whole batch's query rows
 // against the prefix's tiles.
 //
-// Roles (192 threads): warp 0 = TMA producer, warp 1 = MMA issuer (and TMEM
-// owner), warps 2..5 = softmax, rescaling and epilogue.  Every mbarrier wait is
-// bounded; on expiry the CTA reports MOE_DEV_ERR_TIMEOUT, drains and returns.
+// Roles (224 threads): warp 0 = TMA producer, warp 1 = issuer of S (and TMEM
+// owner), warps 2..5 = softmax, rescaling and epilogue, warp 6 = issuer of the
+// value products (an issuer of its own: a tile's value product frees the tile's
+// memory, and must not wait behind the next tile's S, which waits for its loads).
+// Every mbarrier wait is bounded; on expiry the CTA reports
+// MOE_DEV_ERR_TIMEOUT, drains and returns.
 #include <cmath>
 
 #include "kv_common.cuh"
@@ -42,7 +45,7 @@ constexpr int kChunk = kTok * kBK * 2;   // 8 KB: 64 tokens x 64 entries (also 6
 constexpr int kMaxPairs = 4;             // 128-entry slices of the latent
 constexpr int kMaxSlots = 4;             // tiles in flight
 constexpr int kBatch = 512;              // sequences of one launch (lengths and tile sums in shared memory)
-constexpr int kThreads = 192;
+constexpr int kThreads = 224;
 constexpr int kSoftThreads = 128;
 constexpr int kTmemCols = 512;
 constexpr int kSCol = 256;               // S tiles at columns 256 and 320; O slices at 0, 64, 128, 192
@@ -178,6 +181,39 @@ __device__ inline void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
 }
 __device__ inline void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+// 16 lanes x 64 fp32 columns over a warp: thread t gets, for each group i of 8
+// columns, {row t/4, columns 8i + 2(t%4) + 0, 1} and the same of row t/4 + 8.
+__device__ inline void tmem_ld_rows16(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+}
+
+// One thread's latent entry of `rows` accumulator columns (query rows) to dst[row * stride]: 32 lanes write 32
+// neighbouring entries of a row at once.
+template <typename T>
+__device__ inline void store_columns(uint32_t taddr, int rows, int stride, T* dst, const float* factor = nullptr) {
+  for (int c = 0; c < rows; c += 16) {
+    uint32_t v[16];
+    tmem_ld16(taddr + c, v);
+    tmem_ld_wait();
+    const int n = rows - c;
+#pragma unroll
+    for (int x = 0; x < 16; ++x) {
+      if (x < n) {
+        if constexpr (sizeof(T) == 4) dst[x * stride] = __uint_as_float(v[x]);
+        else dst[x * stride] = __float2bfloat16_rn(__uint_as_float(v[x]) * factor[c + x]);
+      }
+    }
+    dst += 16 * stride;
+  }
+}
+
 // Descriptor of an operand whose M (or N) index is contiguous: 64-entry
 // chunks `lbo` bytes apart, 8 consecutive k rows (128 bytes each) every 1024.
 __device__ inline uint64_t smem_desc_mn(uint32_t addr, uint32_t lbo) {
@@ -192,11 +228,20 @@ __device__ inline float ex2(float x) {
   return y;
 }
 
-// A softmax warp's wait: one answer for its lanes, which leave it together (the
-// barrier and tensor-memory instructions that follow are warp-wide).
-__device__ inline bool soft_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+// A value that all lanes of a warp hold, as one the compiler knows to be warp-uniform.
+__device__ inline uint32_t uni(uint32_t v) { return __reduce_max_sync(0xffffffffu, v); }
+
+// A warp's wait: one answer for its lanes, which leave it together (the
+// barrier, tensor-memory and product instructions that follow are warp-wide).
+__device__ inline bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
   const bool ok = mbar_wait(bar, parity, abort_flag);
   return __all_sync(0xffffffffu, ok);
+}
+
+__device__ inline float warp_max(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+  return v;
 }
 
 // OR of a predicate over the softmax warps (named barrier 1): the same answer in every thread.
@@ -213,7 +258,7 @@ __device__ inline bool soft_any(bool v) {
 
 struct Shared {
   uint64_t full[kMaxSlots][kMaxPairs + 1], empty[kMaxSlots][kMaxPairs + 1];   // per 128-entry pair, then the rotary chunk
-  uint64_t q_full, q_empty, s_full[2], s_empty[2], p_full, pv_done, drain;
+  uint64_t q_full, q_empty, s_full[2], s_empty[2], p_full, pv_done[2], drain[2];
   uint32_t tmem;
   int abort;
   float factor[kRows];   // rescaling of each row; in the epilogue 1 / l
@@ -222,27 +267,9 @@ struct Shared {
   int len[kBatch];
 };
 
-// The MMA issuer's wait: while `bar` is not there yet, `other` is issued as soon as it can be.
-template <typename F>
-__device__ inline bool wait_or(uint64_t* bar, uint32_t parity, volatile int* abort_flag, F&& other) {
-  unsigned long long start = 0;
-  for (uint32_t it = 0;; ++it) {
-    if (mbar_try_wait_parity(bar, parity)) return true;
-    other();
-    if ((it & 63) == 63) {
-      if (*abort_flag) return false;
-      const unsigned long long now = globaltimer_ns();
-      if (start == 0) start = now;
-      else if (now - start > kWaitLimitNs) {
-        *abort_flag = 1;
-        return false;
-      }
-    }
-  }
-}
-
 __global__ void __launch_bounds__(kThreads, 1)
-decode_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_constant__ CUtensorMap map_q16,
+decode_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_constant__ CUtensorMap map_pair,
+              const __grid_constant__ CUtensorMap map_q16,
               const __grid_constant__ CUtensorMap map_q64, const DecodeParams p) {
   extern __shared__ uint8_t smem_raw[];
   __shared__ Shared sh;
@@ -264,10 +291,10 @@ decode_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_constant_
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.s_full[i], 1);
       mbar_init(&sh.s_empty[i], kSoftThreads);
+      mbar_init(&sh.pv_done[i], 1);
+      mbar_init(&sh.drain[i], 1);
     }
     mbar_init(&sh.p_full, kSoftThreads);
-    mbar_init(&sh.pv_done, 1);
-    mbar_init(&sh.drain, 1);
     sh.abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -319,69 +346,73 @@ decode_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_constant_
 
   if (warp == 0) {
     // ------------------------------------------------ TMA producer
-    int tile = 0, nseg = 0;
-    bool q_armed = false, ok = true;
-    const int page = p.kv.page_tokens, box = min(page, kTok), boxes = kTok / box;
-    const bool pseq_ok = p.np == 0 || (*p.prefix_seq >= 0 && *p.prefix_seq < p.kv.max_seqs);
-    while (ok && it.next(sg)) {
-      if (lane == 0) {
-        ok = mbar_wait(&sh.q_empty, (nseg & 1) ^ 1u, abort_flag);
-        if (ok) {
-          const int cq = 2 * p.pairs + (p.rope ? 1 : 0);
-          mbar_expect_tx(&sh.q_full, (uint32_t)(cq * sg.N * 128));
-          q_armed = true;
-          for (int c = 0; c < cq; ++c) {
-            if (sg.N == kRows) tma_load_2d(sq + c * kChunk, &map_q64, &sh.q_full, c * kBK, sg.row0);
-            else
-              for (int r = 0; r < sg.N; r += 16)
-                tma_load_2d(sq + c * kChunk + r * 128, &map_q16, &sh.q_full, c * kBK, sg.row0 + r);
-          }
-        }
-      }
-      ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
-      ++nseg;
-      const bool seq_ok = sg.prefix ? pseq_ok : true;   // a bad id in the batch has no tokens
-      for (int t0 = sg.tok0; ok && t0 < sg.tok1; t0 += kTok, ++tile) {
-        const int n_tok = min(kTok, sg.tok1 - t0);
-        const int nb = (n_tok + box - 1) / box;         // boxes that hold tokens
-        int row = 0;
-        if (lane < boxes && lane < nb) {
-          const int t = t0 + lane * box;
-          int pg = seq_ok ? p.kv.table[(size_t)sg.seq * p.kv.max_blocks + (t >> p.kv.page_shift)] : -1;
-          if (pg < 0 || pg >= p.kv.n_pages) {
-            set_status(p.status, seq_ok ? MOE_DEV_ERR_BAD_PAGE : MOE_DEV_ERR_BAD_SEQ);
-            pg = 0;
-          }
-          row = (p.layer * p.kv.n_pages + pg) * page + (t & (page - 1));
-        }
-        const int slot = tile % p.slots;
-        const uint32_t par = ((tile / p.slots) & 1) ^ 1u;
-        uint8_t* base = skv + slot * slot_bytes;
-        for (int j = 0; j <= p.pairs && ok; ++j) {
-          if (j == p.pairs && p.rope == 0) break;
-          if (lane == 0) {
-            ok = mbar_wait(&sh.empty[slot][j], par, abort_flag);
-            if (ok) mbar_expect_tx(&sh.full[slot][j], (uint32_t)(nb * box * 128 * (j < p.pairs ? 2 : 1)));
-          }
-          ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
-          if (!ok) break;
-          for (int i = 0; i < nb; ++i) {
-            const int r = __shfl_sync(0xffffffffu, row, i);
-            if (lane == 0) {
-              uint8_t* dst = base + 2 * j * kChunk + i * box * 128;
-              tma_load_2d(dst, &map_kv, &sh.full[slot][j], 2 * j * kBK, r);
-              if (j < p.pairs) tma_load_2d(dst + kChunk, &map_kv, &sh.full[slot][j], 2 * j * kBK + kBK, r);
-            }
-          }
-        }
-      }
-    }
-    // drain: whatever was asked for lands before the CTA can exit (a barrier's
-    // latest load is its latest phase; after an abort the last tile's barriers
-    // may not all be armed, and the bounded wait outlasts any copy)
     if (lane == 0) {
+      int tile = 0, nseg = 0, slot = 0;
+      uint32_t par = 1;
+      bool ok = true;
+      const int page = p.kv.page_tokens, box = min(page, kTok);
+      const int layer_page = p.layer * p.kv.n_pages, cq = 2 * p.pairs + (p.rope ? 1 : 0);
+      const bool pseq_ok = p.np == 0 || (*p.prefix_seq >= 0 && *p.prefix_seq < p.kv.max_seqs);
+      while (ok && it.next(sg)) {
+        ok = mbar_wait(&sh.q_empty, (nseg & 1) ^ 1u, abort_flag);
+        if (!ok) break;
+        mbar_expect_tx(&sh.q_full, (uint32_t)(cq * sg.N * 128));
+        ++nseg;
+        for (int c = 0; c < cq; ++c) {
+          if (sg.N == kRows) tma_load_2d(sq + c * kChunk, &map_q64, &sh.q_full, c * kBK, sg.row0);
+          else
+            for (int r = 0; r < sg.N; r += 16)
+              tma_load_2d(sq + c * kChunk + r * 128, &map_q16, &sh.q_full, c * kBK, sg.row0 + r);
+        }
+        const bool seq_ok = !sg.prefix || pseq_ok;      // a bad id in the batch has no tokens
+        const int32_t* blocks = p.kv.table + (seq_ok ? (size_t)sg.seq * p.kv.max_blocks : 0);
+        for (int t0 = sg.tok0; ok && t0 < sg.tok1; t0 += kTok) {
+          const int n_tok = min(kTok, sg.tok1 - t0);
+          const int nb = (n_tok + box - 1) / box;       // boxes that hold tokens
+          int row[kTok / 16];
+#pragma unroll
+          for (int i = 0; i < kTok / 16; ++i)
+            if (i < nb) row[i] = seq_ok ? blocks[(t0 + i * box) >> p.kv.page_shift] : -1;
+#pragma unroll
+          for (int i = 0; i < kTok / 16; ++i)
+            if (i < nb) {
+              if (row[i] < 0 || row[i] >= p.kv.n_pages) {
+                set_status(p.status, seq_ok ? MOE_DEV_ERR_BAD_PAGE : MOE_DEV_ERR_BAD_SEQ);
+                row[i] = 0;
+              }
+              row[i] = (layer_page + row[i]) * page + ((t0 + i * box) & (page - 1));
+            }
+          uint8_t* base = skv + slot * slot_bytes;
+          for (int j = 0; j <= p.pairs; ++j) {
+            if (j == p.pairs && p.rope == 0) break;
+            ok = mbar_wait(&sh.empty[slot][j], par, abort_flag);
+            if (!ok) break;
+            uint64_t* bar = &sh.full[slot][j];
+            mbar_expect_tx(bar, (uint32_t)(nb * box * 128 * (j < p.pairs ? 2 : 1)));
+            uint8_t* dst = base + 2 * j * kChunk;
+#pragma unroll
+            for (int i = 0; i < kTok / 16; ++i)
+              if (i < nb) {
+                if (box == kTok && j < p.pairs) {   // both chunks of the pair in one copy
+                  tma_load_3d(dst, &map_pair, bar, 0, row[i], 2 * j);
+                } else {
+                  tma_load_2d(dst + i * box * 128, &map_kv, bar, 2 * j * kBK, row[i]);
+                  if (j < p.pairs) tma_load_2d(dst + kChunk + i * box * 128, &map_kv, bar, 2 * j * kBK + kBK, row[i]);
+                }
+              }
+          }
+          ++tile;
+          if (++slot == p.slots) {
+            slot = 0;
+            par ^= 1u;
+          }
+        }
+      }
+      // drain: whatever was asked for lands before the CTA can exit (a barrier's
+      // latest load is its latest phase; after an abort the last tile's barriers
+      // may not all be armed, and the bounded wait outlasts any copy)
       volatile int no_abort = 0;
-      if (q_armed) mbar_wait(&sh.q_full, (nseg - 1) & 1, &no_abort);
+      if (nseg) mbar_wait(&sh.q_full, (nseg - 1) & 1, &no_abort);
       for (int s = 0; s < p.slots; ++s) {
         const int loads = tile / p.slots + (tile % p.slots > s ? 1 : 0);
         for (int j = 0; j <= p.pairs; ++j) {
@@ -390,147 +421,185 @@ decode_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_constant_
         }
       }
     }
+    __syncwarp();
   } else if (warp == 1) {
-    // ------------------------------------------------ MMA issuer
-    if (lane == 0) {
-      int tile = 0, nseg = 0;
-      bool issued = false, ok = true;
-      bool pending = false, pv_first = false;
-      int pv_tile = 0, pv_n = 0;
-      const uint32_t idesc_s = make_idesc(64, kTok);
-      const uint32_t q0 = smem_u32(sq);
-      auto issue_pv = [&]() {
+    // ------------------------------------------------ issuer of S
+    // The whole warp runs the loop on warp-uniform values; one elected lane issues.
+    int tile = 0, nseg = 0, slot = 0;
+    uint32_t par = 0;
+    bool issued = false, ok = true;
+    constexpr uint32_t idesc_s = make_idesc(64, kTok);
+    const uint32_t tm = uni(tmem), smem0 = uni(smem_u32(smem));
+    const uint64_t dq0 = smem_desc(smem0), dk0 = smem_desc(smem0 + chunks * kChunk);
+    while (__any_sync(0xffffffffu, ok && it.next(sg))) {
+      ok = warp_wait(&sh.q_full, nseg & 1, abort_flag);
+      const int n_tiles = (int)uni((sg.tok1 - sg.tok0 + kTok - 1) / kTok);
+      for (int i = 0; ok && i < n_tiles; ++i, ++tile) {
+        const int buf = tile & 1;
+        ok = warp_wait(&sh.s_empty[buf], ((tile >> 1) & 1) ^ 1u, abort_flag);
+        if (!ok) break;
+        uint64_t dq = dq0, dk = dk0 + ((uint64_t)(slot * slot_bytes) >> 4);
+        const uint32_t d = tm + kSCol + buf * kTok;
+        for (int j = 0; j < p.pairs; ++j) {
+          ok = warp_wait(&sh.full[slot][j], par, abort_flag);
+          if (!ok) break;
+          tc_fence_after();
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const uint64_t off = ((k >> 2) * kChunk + (k & 3) * kUK * 2) >> 4;
+            tc_mma_warp(d, dq + off, dk + off, idesc_s, k ? 1u : (j ? 1u : 0u));
+          }
+          issued = true;
+          dq += (2 * kChunk) >> 4;
+          dk += (2 * kChunk) >> 4;
+        }
+        if (ok && p.rope) {
+          ok = warp_wait(&sh.full[slot][p.pairs], par, abort_flag);
+          if (ok) {
+            tc_fence_after();
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              if (k * kUK < p.rope) tc_mma_warp(d, dq + ((k * kUK * 2) >> 4), dk + ((k * kUK * 2) >> 4), idesc_s, 1u);
+          }
+        }
+        if (!ok) break;
+        tc_commit_warp(&sh.s_full[buf]);
+        if (i == n_tiles - 1) tc_commit_warp(&sh.q_empty);
+        if (++slot == p.slots) {
+          slot = 0;
+          par ^= 1u;
+        }
+      }
+      ++nseg;
+    }
+    if (issued) {   // every issued product completes before tensor memory is released
+      volatile int no_abort = 0;
+      tc_commit_warp(&sh.drain[0]);
+      mbar_wait(&sh.drain[0], 0, &no_abort);
+    }
+    __syncwarp();
+  } else if (warp == 6) {
+    // ------------------------------------------------ issuer of the value products
+    int tile = 0, slot = 0;
+    bool issued = false, ok = true;
+    const uint32_t tm = uni(tmem), smem0 = uni(smem_u32(smem));
+    const uint64_t dv0 = smem_desc_mn(smem0 + chunks * kChunk, kChunk);
+    const uint64_t dp0 = smem_desc(smem0 + chunks * kChunk) + (uint64_t)((2 * p.pairs * kChunk) >> 4);
+    while (__any_sync(0xffffffffu, ok && it.next(sg))) {
+      const int n_tiles = (int)uni((sg.tok1 - sg.tok0 + kTok - 1) / kTok);
+      const uint32_t idesc = make_idesc(128, (int)uni(sg.N)) | kTransA;
+      for (int i = 0; i < n_tiles; ++i, ++tile) {
+        ok = warp_wait(&sh.p_full, tile & 1, abort_flag);   // P is written, so S has read the whole tile
+        if (!ok) break;
         tc_fence_after();
-        const int slot = pv_tile % p.slots;
-        const uint32_t base = smem_u32(skv + slot * slot_bytes);
-        const uint32_t pb = base + 2 * p.pairs * kChunk;
-        const uint32_t idesc = make_idesc(128, pv_n) | kTransA;
+        const uint64_t step = (uint64_t)(slot * slot_bytes) >> 4;
+        uint64_t dv = dv0 + step;
+        const uint64_t dp = dp0 + step;
         for (int j = 0; j < p.pairs; ++j) {
 #pragma unroll
           for (int k = 0; k < kTok / kUK; ++k)
-            tc_mma(tmem + j * kRows, smem_desc_mn(base + 2 * j * kChunk + k * kUK * 128, kChunk),
-                   smem_desc(pb + k * kUK * 2), idesc, (pv_first && k == 0) ? 0u : 1u);
-          tc_commit(&sh.empty[slot][j]);
+            tc_mma_warp(tm + j * kRows, dv + ((k * kUK * 128) >> 4), dp + ((k * kUK * 2) >> 4), idesc,
+                        k ? 1u : (i ? 1u : 0u));
+          tc_commit_warp(&sh.empty[slot][j]);
+          dv += (2 * kChunk) >> 4;
         }
-        if (p.rope) tc_commit(&sh.empty[slot][p.pairs]);
-        tc_commit(&sh.pv_done);
-        pending = false;
-      };
-      auto maybe_pv = [&]() {
-        if (pending && mbar_try_wait_parity(&sh.p_full, pv_tile & 1)) issue_pv();
-      };
-      while (ok && it.next(sg)) {
-        ok = wait_or(&sh.q_full, nseg & 1, abort_flag, maybe_pv);
-        for (int t0 = sg.tok0; ok && t0 < sg.tok1; t0 += kTok, ++tile) {
-          const int slot = tile % p.slots, buf = tile & 1;
-          const uint32_t par = (tile / p.slots) & 1;
-          ok = wait_or(&sh.s_empty[buf], ((tile >> 1) & 1) ^ 1u, abort_flag, maybe_pv);
-          if (!ok) break;
-          const uint32_t base = smem_u32(skv + slot * slot_bytes);
-          const uint32_t d = tmem + kSCol + buf * kTok;
-          for (int j = 0; j <= p.pairs; ++j) {
-            const int steps = j < p.pairs ? 8 : p.rope / kUK;
-            if (steps == 0) break;
-            ok = wait_or(&sh.full[slot][j], par, abort_flag, maybe_pv);
-            if (!ok) break;
-            tc_fence_after();
-            for (int k = 0; k < steps; ++k) {
-              const uint32_t off = (2 * j + (k >> 2)) * kChunk + (k & 3) * kUK * 2;
-              tc_mma(d, smem_desc(q0 + off), smem_desc(base + off), idesc_s, (j | k) ? 1u : 0u);
-            }
-            issued = true;
-          }
-          if (!ok) break;
-          tc_commit(&sh.s_full[buf]);
-          if (t0 + kTok >= sg.tok1) tc_commit(&sh.q_empty);
-          if (pending) {
-            ok = mbar_wait(&sh.p_full, pv_tile & 1, abort_flag);
-            if (!ok) break;
-            issue_pv();
-          }
-          pending = true;
-          pv_first = t0 == sg.tok0;
-          pv_tile = tile;
-          pv_n = sg.N;
-        }
-        ++nseg;
+        if (p.rope) tc_commit_warp(&sh.empty[slot][p.pairs]);
+        tc_commit_warp(&sh.pv_done[tile & 1]);
+        issued = true;
+        if (++slot == p.slots) slot = 0;
       }
-      if (ok && pending) {
-        if (mbar_wait(&sh.p_full, pv_tile & 1, abort_flag)) issue_pv();
-      }
-      if (issued) {   // every issued MMA completes before tensor memory is released
-        volatile int no_abort = 0;
-        tc_commit(&sh.drain);
-        mbar_wait(&sh.drain, 0, &no_abort);
-      }
+    }
+    if (issued) {
+      volatile int no_abort = 0;
+      tc_commit_warp(&sh.drain[1]);
+      mbar_wait(&sh.drain[1], 0, &no_abort);
     }
     __syncwarp();
   } else {
     // ------------------------------------------------ softmax, rescaling, epilogue
-    const int quarter = warp & 3, st = tid - 64;
+    // S has 64 rows, 16 lanes of tensor memory in each warp's quarter.  A thread
+    // holds rows r and r + 8 of its warp's 16 and columns 8 i + 2 (lane % 4) + {0, 1}
+    // of both: four threads share a row, and all 32 lanes have work.
+    const int quarter = warp & 3, st = tid - 64, c2 = 2 * (lane & 3);
     const uint32_t lane_base = tmem + ((uint32_t)(quarter * 32) << 16);
-    const int r = quarter * 16 + lane;          // this thread's query row (lanes 0..15): M = 64 fills 16 lanes a quarter
+    const int r0 = quarter * 16 + (lane >> 2);
     const int rank = p.kv.rank;
     int tile = 0;
     bool fail = false;
     while (!fail && it.next(sg)) {
-      const bool active = lane < 16 && r < sg.rows;
-      int limit = 0;
-      if (active) {
-        const int gr = sg.row0 + r, bq = gr / p.heads, b = bq / p.Q;
-        limit = sh.len[b] - p.Q + (bq - b * p.Q) + 1;
+      int limit[2];
+      bool active[2];
+      float m[2];
+      float2 l[2];   // sums of the probabilities, and of what they are rounded to (this thread's columns)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int r = r0 + 8 * e;
+        active[e] = r < sg.rows;
+        limit[e] = 0;
+        if (active[e]) {
+          const int bq = (sg.row0 + r) / p.heads, b = bq / p.Q;
+          limit[e] = sh.len[b] - p.Q + (bq - b * p.Q) + 1;
+        }
+        m[e] = -INFINITY;
+        l[e] = make_float2(0.0f, 0.0f);
       }
-      float m = -INFINITY;
-      float2 l = make_float2(0.0f, 0.0f);   // sum of the probabilities, and of what they are rounded to
       for (int t0 = sg.tok0; t0 < sg.tok1; t0 += kTok, ++tile) {
         const int buf = tile & 1, slot = tile % p.slots;
         const int n_tok = min(kTok, sg.tok1 - t0);
-        const int see = active ? max(0, min(n_tok, limit - t0)) : 0;
-        const bool ok = soft_wait(&sh.s_full[buf], (tile >> 1) & 1, abort_flag);
-        float s[kTok];
+        // The product of two tiles ago is long over; waiting for each in turn keeps its barrier's phase unambiguous.
+        const bool ok = (tile < 2 || warp_wait(&sh.pv_done[buf], ((tile - 2) >> 1) & 1, abort_flag)) &&
+                        warp_wait(&sh.s_full[buf], (tile >> 1) & 1, abort_flag);
+        float s[32];   // [i][e][2]
         if (ok) {
           tc_fence_after();
-          uint32_t(&u)[kTok] = reinterpret_cast<uint32_t(&)[kTok]>(s);
-          tmem_ld32(lane_base + kSCol + buf * kTok, *reinterpret_cast<uint32_t(*)[32]>(&u[0]));
-          tmem_ld32(lane_base + kSCol + buf * kTok + 32, *reinterpret_cast<uint32_t(*)[32]>(&u[32]));
+          tmem_ld_rows16(lane_base + kSCol + buf * kTok, reinterpret_cast<uint32_t(&)[32]>(s));
           tmem_ld_wait();
           tc_fence_before();
           mbar_arrive(&sh.s_empty[buf]);
         }
-        float top = -INFINITY;
-        if (__all_sync(0xffffffffu, see == kTok || !active)) {
-#pragma unroll
-          for (int j = 0; j < kTok; ++j) {
-            s[j] *= p.scale_log2;
-            top = fmaxf(top, s[j]);
-          }
-        } else {
-#pragma unroll
-          for (int j = 0; j < kTok; ++j) {
-            s[j] = j < see ? s[j] * p.scale_log2 : -INFINITY;
-            top = fmaxf(top, s[j]);
-          }
-        }
-        float f = 1.0f;
         bool grow = false;
-        if (active && top > m) {
-          if (m == -INFINITY) {
-            m = top;             // nothing summed for this row yet
-          } else if (top > m + kGrow) {
-            f = ex2(m - top);
-            l.x *= f;
-            l.y *= f;
-            m = top;
-            grow = true;
+        float ref[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int see = min(n_tok, limit[e] - t0);
+          float top = -INFINITY;
+          if (__all_sync(0xffffffffu, see >= kTok || !active[e])) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              s[4 * i + 2 * e] *= p.scale_log2;
+              s[4 * i + 2 * e + 1] *= p.scale_log2;
+              top = fmaxf(top, fmaxf(s[4 * i + 2 * e], s[4 * i + 2 * e + 1]));
+            }
+          } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              s[4 * i + 2 * e] = 8 * i + c2 < see ? s[4 * i + 2 * e] * p.scale_log2 : -INFINITY;
+              s[4 * i + 2 * e + 1] = 8 * i + c2 + 1 < see ? s[4 * i + 2 * e + 1] * p.scale_log2 : -INFINITY;
+              top = fmaxf(top, fmaxf(s[4 * i + 2 * e], s[4 * i + 2 * e + 1]));
+            }
           }
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+          float f = 1.0f;
+          if (active[e] && top > m[e]) {
+            if (m[e] == -INFINITY) {
+              m[e] = top;             // nothing summed for this row yet
+            } else if (top > m[e] + kGrow) {
+              f = ex2(m[e] - top);
+              l[e].x *= f;
+              l[e].y *= f;
+              m[e] = top;
+              grow = true;
+            }
+          }
+          ref[e] = m[e] == -INFINITY ? 0.0f : m[e];
+          if ((lane & 3) == 0) sh.factor[r0 + 8 * e] = f;
         }
-        if (lane < 16) sh.factor[r] = f;
         fail = soft_any(!ok);
         if (fail) break;
         if (soft_any(grow)) {
-          // O was last added to by the previous tile's product (the one before it preceded this S in issue order,
-          // so the parity is this product's), and this tile's waits for us
-          const bool done = soft_wait(&sh.pv_done, (tile - 1) & 1, abort_flag);
+          // O was last added to by the previous tile's product, and this tile's waits for us
+          const bool done = warp_wait(&sh.pv_done[buf ^ 1], ((tile - 1) >> 1) & 1, abort_flag);
           fail = soft_any(!done);
           if (fail) break;
           tc_fence_after();
@@ -549,23 +618,22 @@ decode_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_constant_
         // Probabilities, rounded to bf16 (the cache's type, the only one the product takes beside it).  Two sums:
         // of the rounded ones, which the output is divided by (its weights then add up to one, and where few tokens
         // carry the row most of their rounding cancels), and of the unrounded ones for the log-sum-exp.
-        uint8_t* sp = skv + slot * slot_bytes + 2 * p.pairs * kChunk;
-        if (lane < 16 && r < sg.N) {
-          const float ref = m == -INFINITY ? 0.0f : m;
-          uint8_t* prow = sp + r * 128;
+        uint8_t* sp = skv + slot * slot_bytes + 2 * p.pairs * kChunk + (lane & 3) * 4;
 #pragma unroll
-          for (int v = 0; v < kTok / 8; ++v) {
-            uint32_t w[4];
+        for (int e = 0; e < 2; ++e) {
+          const int r = r0 + 8 * e;
+          if (r < sg.N) {
+            uint8_t* prow = sp + r * 128;
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              const float a = active ? ex2(s[8 * v + 2 * x] - ref) : 0.0f;
-              const float b = active ? ex2(s[8 * v + 2 * x + 1] - ref) : 0.0f;
+            for (int i = 0; i < 8; ++i) {
+              const float a = active[e] ? ex2(s[4 * i + 2 * e] - ref[e]) : 0.0f;
+              const float b = active[e] ? ex2(s[4 * i + 2 * e + 1] - ref[e]) : 0.0f;
               const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-              w[x] = *reinterpret_cast<const uint32_t*>(&h);
-              l.x += a + b;
-              l.y += bf16_lo(w[x]) + bf16_hi(w[x]);
+              const uint32_t w = *reinterpret_cast<const uint32_t*>(&h);
+              l[e].x += a + b;
+              l[e].y += bf16_lo(w) + bf16_hi(w);
+              *reinterpret_cast<uint32_t*>(prow + ((i ^ (r & 7)) << 4)) = w;
             }
-            *reinterpret_cast<uint4*>(prow + ((v ^ (r & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
           }
         }
         if (n_tok < kTok) {
@@ -582,34 +650,36 @@ decode_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_constant_
         mbar_arrive(&sh.p_full);
       }
       if (fail) break;
-      // The last S was issued before the product of the tile ahead of it, so that
-      // product may be under way too: its phase first, or the parity would name an older one.
-      const bool done = (tile < 2 || soft_wait(&sh.pv_done, (tile - 2) & 1, abort_flag)) &&
-                        soft_wait(&sh.pv_done, (tile - 1) & 1, abort_flag);
-      if (lane < 16) sh.factor[r] = l.y == 0.0f ? 0.0f : 1.0f / l.y;
-      if (active) {
-        if (sg.part) sg.ml[r] = make_float4(m, l.x, l.y, 0.0f);
-        else if (p.lse) p.lse[sg.row0 + r] = l.x == 0.0f ? -INFINITY : (m + log2f(l.x)) * 0.6931471805599453f;
+      const bool done = (tile < 2 || warp_wait(&sh.pv_done[tile & 1], ((tile - 2) >> 1) & 1, abort_flag)) &&
+                        warp_wait(&sh.pv_done[(tile - 1) & 1], ((tile - 1) >> 1) & 1, abort_flag);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+#pragma unroll
+        for (int o = 1; o <= 2; o <<= 1) {
+          l[e].x += __shfl_xor_sync(0xffffffffu, l[e].x, o);
+          l[e].y += __shfl_xor_sync(0xffffffffu, l[e].y, o);
+        }
+        const int r = r0 + 8 * e;
+        if ((lane & 3) == 0) {
+          sh.factor[r] = l[e].y == 0.0f ? 0.0f : 1.0f / l[e].y;
+          if (active[e]) {
+            if (sg.part) sg.ml[r] = make_float4(m[e], l[e].x, l[e].y, 0.0f);
+            else if (p.lse)
+              p.lse[sg.row0 + r] = l[e].x == 0.0f ? -INFINITY : (m[e] + log2f(l[e].x)) * 0.6931471805599453f;
+          }
+        }
       }
       fail = soft_any(!done);
       if (fail) break;
       tc_fence_after();
-      for (int j = 0; j < p.pairs; ++j) {
-        const int dim = j * 128 + quarter * 32 + lane;
-        for (int c = 0; c < sg.N; c += 16) {
-          uint32_t v[16];
-          tmem_ld16(lane_base + j * kRows + c, v);
-          tmem_ld_wait();
-#pragma unroll
-          for (int x = 0; x < 16; ++x) {
-            if (c + x < sg.rows) {
-              if (sg.part) sg.part[(size_t)(c + x) * rank + dim] = __uint_as_float(v[x]);
-              else
-                p.out[(size_t)(sg.row0 + c + x) * rank + dim] =
-                    __float2bfloat16_rn(__uint_as_float(v[x]) * sh.factor[c + x]);
-            }
-          }
-        }
+      const int dim = quarter * 32 + lane;
+      if (sg.part) {
+        float* dst = sg.part + dim;
+        for (int j = 0; j < p.pairs; ++j, dst += 128) store_columns(lane_base + j * kRows, sg.rows, rank, dst);
+      } else {
+        __nv_bfloat16* dst = p.out + (size_t)sg.row0 * rank + dim;
+        for (int j = 0; j < p.pairs; ++j, dst += 128)
+          store_columns(lane_base + j * kRows, sg.rows, rank, dst, sh.factor);
       }
       tc_fence_before();
       soft_any(false);   // the factors are free again
@@ -624,13 +694,21 @@ decode_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_constant_
 
 // ---------------------------------------------------------------- combine
 // One CTA per query row: its pieces' (m, l, O) in a fixed order (the prefix's
-// pieces, then the sequence's).  rank / 4 threads cover the row with float4; the
-// rest of the CTA's 256 threads take other pieces, joined through shared memory.
+// pieces, then the sequence's).  The first warp turns the pieces' statistics
+// into weights; then rank / 4 threads cover the row with float4 loads and the
+// rest of the CTA's 256 threads take other pieces, joined through shared
+// memory.  Bound by the latency of three dependent reads (tile sums,
+// statistics, partial rows) at small sizes, by L2 at large ones.
 constexpr int kCombineThreads = 256;
+constexpr int kMaxPieces = 1024;   // of a row: at most one per CTA of each line
 
 __global__ void __launch_bounds__(kCombineThreads)
 combine_parts_kernel(const DecodeParams p) {
   __shared__ float4 s_acc[kCombineThreads];
+  __shared__ const float* s_o[kMaxPieces];
+  __shared__ float s_w[kMaxPieces];
+  __shared__ float2 s_l;
+  __shared__ float s_ref;
   pdl_wait();
   pdl_trigger();
   const int row = blockIdx.x, rank = p.kv.rank;
@@ -639,65 +717,72 @@ combine_parts_kernel(const DecodeParams p) {
   const int per = per_cta(total, p.teams);
   const int t0 = x1 > x0 ? x0 / per : 0, t1 = x1 > x0 ? (x1 - 1) / per : -1;
   const int n_s = t1 - t0 + 1;
-  int n_p = 0, c0 = 0, pp = 1, i = 0;
+  int n_p = 0;
   if (p.np) {
-    pp = per_cta((long long)p.Gp * p.np, p.ctas);
-    i = row / p.NRp;
-    c0 = (int)((long long)i * p.np / pp);
-    n_p = (int)(((long long)(i + 1) * p.np - 1) / pp) - c0 + 1;
+    const int pp = per_cta((long long)p.Gp * p.np, p.ctas), i = row / p.NRp;
+    const long long a = (long long)i * p.np, z = a + p.np;
+    const int c0 = (int)(a / pp);
+    n_p = (int)((z - 1) / pp) - c0 + 1;
+    for (int k = threadIdx.x; k < n_p; k += kCombineThreads) {
+      const long long from = (long long)(c0 + k) * pp;
+      const int slot = (a >= from && z <= from + pp) ? 2 * p.ctas + i : 2 * (c0 + k) + (a > from ? 1 : 0);
+      const size_t at = (size_t)slot * p.NRp + (row - i * p.NRp);
+      s_o[k] = p.part_p + at * rank;
+    }
   } else if (n_s == 1) {
     return;   // written by decode_kernel
   }
-  const int g = in_seq / p.NR;
-  // piece k: its rows and statistics
-  auto piece = [&](int k, const float*& o, float4& ml) {
-    if (k < n_p) {
-      const int c = c0 + k;
-      const long long a = (long long)i * p.np, z = a + p.np, from = (long long)c * pp;
-      const int slot = (a >= from && z <= from + pp) ? 2 * p.ctas + i : 2 * c + (a > from ? 1 : 0);
-      const size_t at = (size_t)slot * p.NRp + (row - i * p.NRp);
-      o = p.part_p + at * rank;
-      ml = p.ml_p[at];
-    } else {
-      const int t = t0 + k - n_p;
-      const long long from = (long long)t * per;
-      const int cta = t * p.G + g;
-      const int slot = (x0 >= from && x1 <= from + per) ? 2 * p.teams * p.G + b * p.G + g : 2 * cta + (x0 > from ? 1 : 0);
-      const size_t at = (size_t)slot * p.NR + (in_seq - g * p.NR);
-      o = p.part_s + at * rank;
-      ml = p.ml_s[at];
+  const int g = in_seq / p.NR, n = n_p + n_s;
+  for (int k = threadIdx.x; k < n_s; k += kCombineThreads) {
+    const long long from = (long long)(t0 + k) * per;
+    const int slot = (x0 >= from && x1 <= from + per) ? 2 * p.teams * p.G + b * p.G + g
+                                                      : 2 * ((t0 + k) * p.G + g) + (x0 > from ? 1 : 0);
+    const size_t at = (size_t)slot * p.NR + (in_seq - g * p.NR);
+    s_o[n_p + k] = p.part_s + at * rank;
+  }
+  __syncthreads();
+  if (threadIdx.x < 32) {
+    // a piece's statistics sit at its row's index
+    auto stats = [&](int k) {
+      return k < n_p ? p.ml_p[(s_o[k] - p.part_p) / rank] : p.ml_s[(s_o[k] - p.part_s) / rank];
+    };
+    float top = -INFINITY, l = 0.0f, lr = 0.0f;
+    for (int k = threadIdx.x; k < n; k += 32) {
+      const float4 ml = stats(k);
+      const float now = fmaxf(top, ml.x), ref = now == -INFINITY ? 0.0f : now;
+      const float f = ex2(top - ref), w = ex2(ml.x - ref);
+      l = fmaf(l, f, ml.y * w);
+      lr = fmaf(lr, f, ml.z * w);
+      s_w[k] = ml.x;
+      top = now;
     }
-  };
-  const int n = n_p + n_s, quads = rank / 4, groups = kCombineThreads / quads;
+    const float all = warp_max(top), ref = all == -INFINITY ? 0.0f : all;
+    const float f = ex2(top - ref);
+    l = warp_sum(l * f);
+    lr = warp_sum(lr * f);
+    if (threadIdx.x == 0) {
+      s_l = make_float2(l, lr);
+      s_ref = ref;
+    }
+  }
+  __syncthreads();
+  const int quads = rank / 4, groups = kCombineThreads / quads;
   const int v = threadIdx.x % quads, grp = threadIdx.x / quads;
-  const float* o;
-  float4 ml;
-  float top = -INFINITY;
-  for (int k = 0; k < n; ++k) {
-    piece(k, o, ml);
-    top = fmaxf(top, ml.x);
-  }
-  const float ref = top == -INFINITY ? 0.0f : top;
-  float l = 0.0f, lr = 0.0f;
-  for (int k = 0; k < n; ++k) {
-    piece(k, o, ml);
-    const float w = ex2(ml.x - ref);
-    l = fmaf(ml.y, w, l);
-    lr = fmaf(ml.z, w, lr);
-  }
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (grp < groups)
+  if (grp < groups) {
+#pragma unroll 4
     for (int k = grp; k < n; k += groups) {
-      piece(k, o, ml);
-      const float w = ex2(ml.x - ref);
-      const float4 x = reinterpret_cast<const float4*>(o)[v];
+      const float w = ex2(s_w[k] - s_ref);
+      const float4 x = __ldcs(reinterpret_cast<const float4*>(s_o[k]) + v);
       acc.x = fmaf(w, x.x, acc.x);
       acc.y = fmaf(w, x.y, acc.y);
       acc.z = fmaf(w, x.z, acc.z);
       acc.w = fmaf(w, x.w, acc.w);
     }
+  }
   s_acc[threadIdx.x] = acc;
   __syncthreads();
+  const float2 l = s_l;
   if (threadIdx.x < quads) {
     for (int q = 1; q < groups; ++q) {
       const float4 x = s_acc[threadIdx.x + q * quads];
@@ -706,7 +791,7 @@ combine_parts_kernel(const DecodeParams p) {
       acc.z += x.z;
       acc.w += x.w;
     }
-    const float inv = lr == 0.0f ? 0.0f : 1.0f / lr;
+    const float inv = l.y == 0.0f ? 0.0f : 1.0f / l.y;
     const __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x * inv, acc.y * inv);
     const __nv_bfloat162 hi = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
     uint2 packed;
@@ -714,7 +799,7 @@ combine_parts_kernel(const DecodeParams p) {
     packed.y = *reinterpret_cast<const uint32_t*>(&hi);
     reinterpret_cast<uint2*>(p.out + (size_t)row * rank)[v] = packed;
   }
-  if (p.lse && threadIdx.x == 0) p.lse[row] = l == 0.0f ? -INFINITY : (ref + log2f(l)) * 0.6931471805599453f;
+  if (p.lse && threadIdx.x == 0) p.lse[row] = l.x == 0.0f ? -INFINITY : (s_ref + log2f(l.x)) * 0.6931471805599453f;
 }
 
 // ---------------------------------------------------------------- host side
@@ -741,7 +826,7 @@ void fill_shape(DecodeParams& p, const moe_kv_cache& c, int B, int Q, int heads,
   p.shared = shared;
   p.rope = c.rope;
   p.pairs = c.rank / 128;
-  p.ctas = num_sms();
+  p.ctas = num_sms() < kMaxPieces / 2 ? num_sms() : kMaxPieces / 2;
   const Tiles s = row_tiles((long long)Q * heads), f = row_tiles((long long)B * Q * heads);
   p.G = s.n;
   p.NR = s.rows;
@@ -776,17 +861,17 @@ int launch_decode(const moe_kv_cache& c, DecodeParams p, const void* q, cudaStre
   p.slots = (int)((227 * 1024 - sizeof(Shared) - 1024 - slot) / slot);   // what the query tile leaves
   if (p.slots > kMaxSlots) p.slots = kMaxSlots;
   const int smem = (1 + p.slots) * slot + 1024;
-  CUtensorMap kv, q16, q64;
+  CUtensorMap kv, pair, q16, q64;
   const uint64_t rows = (uint64_t)c.n_layers * c.n_pages * c.page_tokens, qrows = (uint64_t)p.B * p.Q * p.heads;
   if (!make_map(&kv, c.pages, row, rows, c.page_tokens < kTok ? c.page_tokens : kTok) ||
-      !make_map(&q16, q, row, qrows, 16) || !make_map(&q64, q, row, qrows, 64))
+      !make_map_chunks(&pair, c.pages, row, rows, kTok, 2) || !make_map(&q16, q, row, qrows, 16) || !make_map(&q64, q, row, qrows, 64))
     return MOE_ERR_CUDA;
   static std::atomic<unsigned char> attr[kMaxDevices];
   cudaError_t e = once_per_device(attr, [] {
     return cudaFuncSetAttribute(decode_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 227 * 1024 - (int)sizeof(Shared));
   });
-  if (e == cudaSuccess) e = launch_k(decode_kernel, p.ctas, kThreads, smem, s, kv, q16, q64, p);
+  if (e == cudaSuccess) e = launch_k(decode_kernel, p.ctas, kThreads, smem, s, kv, pair, q16, q64, p);
   if (e == cudaSuccess) e = launch_k(combine_parts_kernel, (unsigned)qrows, kCombineThreads, 0, s, p);
   return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
