@@ -228,9 +228,6 @@ __device__ inline float ex2(float x) {
   return y;
 }
 
-// A value that all lanes of a warp hold, as one the compiler knows to be warp-uniform.
-__device__ inline uint32_t uni(uint32_t v) { return __reduce_max_sync(0xffffffffu, v); }
-
 // A warp's wait: one answer for its lanes, which leave it together (the
 // barrier, tensor-memory and product instructions that follow are warp-wide).
 __device__ inline bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
@@ -276,7 +273,6 @@ decode_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_constant_
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int chunks = 2 * p.pairs + 1;               // the last one holds the rotary part, then P
-  uint8_t* sq = smem;
   uint8_t* skv = smem + chunks * kChunk;
   const int slot_bytes = chunks * kChunk;
 
@@ -346,79 +342,93 @@ decode_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_constant_
 
   if (warp == 0) {
     // ------------------------------------------------ TMA producer
-    if (lane == 0) {
-      int tile = 0, nseg = 0, slot = 0;
-      uint32_t par = 1;
-      bool ok = true;
-      const int page = p.kv.page_tokens, box = min(page, kTok);
-      const int layer_page = p.layer * p.kv.n_pages, cq = 2 * p.pairs + (p.rope ? 1 : 0);
-      const bool pseq_ok = p.np == 0 || (*p.prefix_seq >= 0 && *p.prefix_seq < p.kv.max_seqs);
-      while (ok && it.next(sg)) {
-        ok = mbar_wait(&sh.q_empty, (nseg & 1) ^ 1u, abort_flag);
-        if (!ok) break;
-        mbar_expect_tx(&sh.q_full, (uint32_t)(cq * sg.N * 128));
-        ++nseg;
-        for (int c = 0; c < cq; ++c) {
-          if (sg.N == kRows) tma_load_2d(sq + c * kChunk, &map_q64, &sh.q_full, c * kBK, sg.row0);
-          else
-            for (int r = 0; r < sg.N; r += 16)
-              tma_load_2d(sq + c * kChunk + r * 128, &map_q16, &sh.q_full, c * kBK, sg.row0 + r);
+    // The whole warp runs the loop on warp-uniform values; one elected lane issues.
+    int tile = 0, nseg = 0, slot = 0;
+    uint32_t par = 1;
+    bool ok = true;
+    const int page = p.kv.page_tokens, box = min(page, kTok);
+    const int layer_page = p.layer * p.kv.n_pages, cq = 2 * p.pairs + (p.rope ? 1 : 0);
+    const bool pseq_ok = p.np == 0 || (*p.prefix_seq >= 0 && *p.prefix_seq < p.kv.max_seqs);
+    const uint32_t smem0 = uni(smem_u32(smem)), kv0 = smem0 + chunks * kChunk;
+    const uint32_t full0 = uni(smem_u32(&sh.full[0][0])), qbar = uni(smem_u32(&sh.q_full));
+    while (__any_sync(0xffffffffu, ok && it.next(sg))) {
+      const bool seq_ok = !sg.prefix || pseq_ok;      // a bad id in the batch has no tokens
+      const int32_t* blocks = p.kv.table + (seq_ok ? (size_t)sg.seq * p.kv.max_blocks : 0);
+      const int tok0 = (int)uni(sg.tok0), tok1 = (int)uni(sg.tok1);
+      // lane i: the pool row where box i of a tile begins; read one tile ahead
+      auto block = [&](int t) { return seq_ok && lane < kTok / box && t < tok1 ? blocks[t >> p.kv.page_shift] : -1; };
+      int ahead = block(tok0 + lane * box);
+      ok = warp_wait(&sh.q_empty, (nseg & 1) ^ 1u, abort_flag);
+      if (!ok) break;
+      const int N = (int)uni(sg.N), row0 = (int)uni(sg.row0);
+      mbar_expect_tx_warp(qbar, (uint32_t)(cq * N * 128));
+      ++nseg;
+      for (int c = 0; c < cq; ++c) {
+        if (N == kRows) tma_load_2d_warp(smem0 + c * kChunk, &map_q64, qbar, c * kBK, row0);
+        else
+          for (int r = 0; r < N; r += 16) tma_load_2d_warp(smem0 + c * kChunk + r * 128, &map_q16, qbar, c * kBK, row0 + r);
+      }
+      for (int t0 = tok0; ok && t0 < tok1; t0 += kTok) {
+        const int nb = (min(kTok, tok1 - t0) + box - 1) / box;       // boxes that hold tokens
+        const int t = t0 + lane * box;
+        int row = ahead;
+        if (lane < nb) {
+          if (row < 0 || row >= p.kv.n_pages) {
+            set_status(p.status, seq_ok ? MOE_DEV_ERR_BAD_PAGE : MOE_DEV_ERR_BAD_SEQ);
+            row = 0;
+          }
+          row = (layer_page + row) * page + (t & (page - 1));
+        } else {
+          row = 0;
         }
-        const bool seq_ok = !sg.prefix || pseq_ok;      // a bad id in the batch has no tokens
-        const int32_t* blocks = p.kv.table + (seq_ok ? (size_t)sg.seq * p.kv.max_blocks : 0);
-        for (int t0 = sg.tok0; ok && t0 < sg.tok1; t0 += kTok) {
-          const int n_tok = min(kTok, sg.tok1 - t0);
-          const int nb = (n_tok + box - 1) / box;       // boxes that hold tokens
-          int row[kTok / 16];
+        ahead = block(t + kTok);
+        int rows[kTok / 16];
 #pragma unroll
-          for (int i = 0; i < kTok / 16; ++i)
-            if (i < nb) row[i] = seq_ok ? blocks[(t0 + i * box) >> p.kv.page_shift] : -1;
-#pragma unroll
-          for (int i = 0; i < kTok / 16; ++i)
-            if (i < nb) {
-              if (row[i] < 0 || row[i] >= p.kv.n_pages) {
-                set_status(p.status, seq_ok ? MOE_DEV_ERR_BAD_PAGE : MOE_DEV_ERR_BAD_SEQ);
-                row[i] = 0;
-              }
-              row[i] = (layer_page + row[i]) * page + ((t0 + i * box) & (page - 1));
-            }
-          uint8_t* base = skv + slot * slot_bytes;
-          for (int j = 0; j <= p.pairs; ++j) {
-            if (j == p.pairs && p.rope == 0) break;
-            ok = mbar_wait(&sh.empty[slot][j], par, abort_flag);
-            if (!ok) break;
-            uint64_t* bar = &sh.full[slot][j];
-            mbar_expect_tx(bar, (uint32_t)(nb * box * 128 * (j < p.pairs ? 2 : 1)));
-            uint8_t* dst = base + 2 * j * kChunk;
+        for (int i = 0; i < kTok / 16; ++i) rows[i] = (int)uni(lane == i ? row : 0);
+        const uint32_t dst = kv0 + slot * slot_bytes, bar = full0 + slot * (uint32_t)sizeof(sh.full[0]);
+        for (int j = 0; j < p.pairs; ++j) {
+          ok = warp_wait(&sh.empty[slot][j], par, abort_flag);
+          if (!ok) break;
+          mbar_expect_tx_warp(bar + 8 * j, (uint32_t)(nb * box * 256));
+          if (box == kTok) {   // both chunks of the pair in one copy
+            tma_load_3d_warp(dst + 2 * j * kChunk, &map_pair, bar + 8 * j, 0, rows[0], 2 * j);
+          } else {
 #pragma unroll
             for (int i = 0; i < kTok / 16; ++i)
               if (i < nb) {
-                if (box == kTok && j < p.pairs) {   // both chunks of the pair in one copy
-                  tma_load_3d(dst, &map_pair, bar, 0, row[i], 2 * j);
-                } else {
-                  tma_load_2d(dst + i * box * 128, &map_kv, bar, 2 * j * kBK, row[i]);
-                  if (j < p.pairs) tma_load_2d(dst + kChunk + i * box * 128, &map_kv, bar, 2 * j * kBK + kBK, row[i]);
-                }
+                tma_load_2d_warp(dst + 2 * j * kChunk + i * box * 128, &map_kv, bar + 8 * j, 2 * j * kBK, rows[i]);
+                tma_load_2d_warp(dst + (2 * j + 1) * kChunk + i * box * 128, &map_kv, bar + 8 * j, 2 * j * kBK + kBK,
+                                 rows[i]);
               }
           }
-          ++tile;
-          if (++slot == p.slots) {
-            slot = 0;
-            par ^= 1u;
+        }
+        if (ok && p.rope) {
+          const int j = p.pairs;
+          ok = warp_wait(&sh.empty[slot][j], par, abort_flag);
+          if (ok) {
+            mbar_expect_tx_warp(bar + 8 * j, (uint32_t)(nb * box * 128));
+#pragma unroll
+            for (int i = 0; i < kTok / 16; ++i)
+              if (i < nb) tma_load_2d_warp(dst + 2 * j * kChunk + i * box * 128, &map_kv, bar + 8 * j, 2 * j * kBK, rows[i]);
           }
         }
-      }
-      // drain: whatever was asked for lands before the CTA can exit (a barrier's
-      // latest load is its latest phase; after an abort the last tile's barriers
-      // may not all be armed, and the bounded wait outlasts any copy)
-      volatile int no_abort = 0;
-      if (nseg) mbar_wait(&sh.q_full, (nseg - 1) & 1, &no_abort);
-      for (int s = 0; s < p.slots; ++s) {
-        const int loads = tile / p.slots + (tile % p.slots > s ? 1 : 0);
-        for (int j = 0; j <= p.pairs; ++j) {
-          if (j == p.pairs && p.rope == 0) break;
-          if (loads > 0) mbar_wait(&sh.full[s][j], (loads - 1) & 1, &no_abort);
+        ++tile;
+        if (++slot == p.slots) {
+          slot = 0;
+          par ^= 1u;
         }
+      }
+    }
+    // drain: whatever was asked for lands before the CTA can exit (a barrier's
+    // latest load is its latest phase; after an abort the last tile's barriers
+    // may not all be armed, and the bounded wait outlasts any copy)
+    volatile int no_abort = 0;
+    if (nseg) mbar_wait(&sh.q_full, (nseg - 1) & 1, &no_abort);
+    for (int s = 0; s < p.slots; ++s) {
+      const int loads = tile / p.slots + (tile % p.slots > s ? 1 : 0);
+      for (int j = 0; j <= p.pairs; ++j) {
+        if (j == p.pairs && p.rope == 0) break;
+        if (loads > 0) mbar_wait(&sh.full[s][j], (loads - 1) & 1, &no_abort);
       }
     }
     __syncwarp();

@@ -50,13 +50,6 @@ __device__ inline void tma_load_2d(void* dst, const CUtensorMap* map, uint64_t* 
       : "memory");
 }
 
-__device__ inline void tma_load_3d(void* dst, const CUtensorMap* map, uint64_t* bar, int c0, int c1, int c2) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];"
-      ::"r"(smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2)
-      : "memory");
-}
-
 // tma_load_2d with an L2 cache policy.
 __device__ inline void tma_load_2d_hint(void* dst, const CUtensorMap* map, uint64_t* bar, int c0, int c1,
                                         uint64_t policy) {
@@ -94,6 +87,34 @@ __device__ inline void tc_mma_warp(uint32_t d_tmem, uint64_t a_desc, uint64_t b_
       ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accum)
       : "memory");
 }
+
+// Copies and byte counts issued by one elected lane of a converged warp, all
+// operands warp-uniform (a copy issued from a diverged lane with operands the
+// compiler cannot prove uniform took about 650 cycles of issue).
+__device__ inline void tma_load_2d_warp(uint32_t dst, const CUtensorMap* map, uint32_t bar, int c0, int c1) {
+  asm volatile(
+      "{\n .reg .pred q;\n elect.sync _|q, 0xffffffff;\n"
+      " @q cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];\n}\n"
+      ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1)
+      : "memory");
+}
+__device__ inline void tma_load_3d_warp(uint32_t dst, const CUtensorMap* map, uint32_t bar, int c0, int c1, int c2) {
+  asm volatile(
+      "{\n .reg .pred q;\n elect.sync _|q, 0xffffffff;\n"
+      " @q cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5}], [%2];\n}\n"
+      ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2)
+      : "memory");
+}
+__device__ inline void mbar_expect_tx_warp(uint32_t bar, uint32_t bytes) {
+  asm volatile(
+      "{\n .reg .pred q;\n elect.sync _|q, 0xffffffff;\n"
+      " @q mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n}\n" ::"r"(bar), "r"(bytes)
+      : "memory");
+}
+
+// A value that all lanes of a warp hold, as one the compiler knows to be warp-uniform.
+__device__ inline uint32_t uni(uint32_t v) { return __reduce_max_sync(0xffffffffu, v); }
 
 __device__ inline void tc_commit_warp(uint64_t* bar) {
   asm volatile(
