@@ -29,6 +29,7 @@
 // memory, and must not wait behind the next tile's S, which waits for its loads).
 // Every mbarrier wait is bounded; on expiry the CTA reports
 // MOE_DEV_ERR_TIMEOUT, drains and returns.
+#include <cfloat>
 #include <cmath>
 
 #include "kv_common.cuh"
@@ -47,6 +48,7 @@ constexpr int kMaxSlots = 4;             // tiles in flight
 constexpr int kBatch = 512;              // sequences of one launch (lengths and tile sums in shared memory)
 constexpr int kThreads = 224;
 constexpr int kSoftThreads = 128;
+constexpr int kHead = 2;                 // tiles' worth of time that a piece costs beside its tiles
 constexpr int kTmemCols = 512;
 constexpr int kSCol = 256;               // S tiles at columns 256 and 320; O slices at 0, 64, 128, 192
 constexpr float kGrow = 8.0f;            // log2 of the growth of a row's maximum that forces a rescaling
@@ -57,6 +59,7 @@ struct DecodeParams {
   int pairs, slots;          // rank / 128; tiles in flight
   int G, NR, teams;          // row tiles of a sequence, their rows, and CTA teams
   int Gp, NRp, np, ctas;     // row tiles of the prefix, their rows, prefix tiles; CTAs of the grid
+  int per_p;                 // tiles of the prefix line that a CTA takes
   float scale_log2;          // scale * log2(e): the exponentials are powers of two
   const int32_t* seqs;
   const int32_t* prefix_seq;
@@ -80,31 +83,36 @@ struct Seg {
 };
 
 __device__ __host__ inline int up16(int v) { return (v + 15) & ~15; }
-__device__ inline int per_cta(long long tiles, int parts) { return (int)((tiles + parts - 1) / parts); }
+__device__ __host__ inline int per_cta(unsigned tiles, unsigned parts) { return (int)((tiles + parts - 1) / parts); }
 
-// A CTA's pieces: first of the prefix line, then of the sequences' line.
+// A CTA's pieces: first of the prefix line, then of the sequences' line, which
+// the CTAs take from the other end (calls too small for both lines to fill the
+// grid keep them on different SMs).  A sequence stands in its line with kHead
+// units ahead of its tiles, for what starting and ending a piece costs.
 struct SegIter {
   const DecodeParams& p;
   const int* pref;
   const int* len;
+  const int* ids;
   long long pos, end;
-  int b, team, g, per;
+  int b, cta, team, g, per;
   bool first;
   int phase;
 
-  __device__ SegIter(const DecodeParams& p_, const int* pref_, const int* len_) : p(p_), pref(pref_), len(len_) {
+  __device__ SegIter(const DecodeParams& p_, const int* pref_, const int* len_, const int* ids_)
+      : p(p_), pref(pref_), len(len_), ids(ids_) {
     phase = 0;
     const long long total = (long long)p.Gp * p.np;
-    const int pp = per_cta(total, p.ctas);
-    pos = min(total, (long long)blockIdx.x * pp);
-    end = min(total, pos + pp);
+    pos = min(total, (long long)blockIdx.x * p.per_p);
+    end = min(total, pos + p.per_p);
     first = true;
   }
   __device__ void start_suffix() {
     phase = 1;
     first = true;
-    team = blockIdx.x / p.G;
-    g = blockIdx.x - team * p.G;
+    cta = p.ctas - 1 - blockIdx.x;
+    team = cta / p.G;
+    g = cta - team * p.G;
     const int total = pref[p.B];
     per = per_cta(total, p.teams);
     pos = team < p.teams ? min((long long)total, (long long)team * per) : total;
@@ -142,10 +150,15 @@ struct SegIter {
     }
     if (pos >= end) return false;
     while (pref[b + 1] <= pos) ++b;
-    const int n = pref[b + 1] - pref[b], x0 = (int)(pos - pref[b]), x1 = (int)min((long long)n, x0 + end - pos);
+    const int n = pref[b + 1] - pref[b] - kHead;
+    int x0 = (int)(pos - pref[b]);
+    const int x1 = (int)min((long long)n, x0 + end - pos - kHead);
+    if (x1 <= 0) return false;             // the range ends within the head of this sequence
+    pos = pref[b] + x1 + kHead;
+    x0 = max(0, x0 - kHead);
     s.prefix = false;
     s.b = b;
-    s.seq = p.seqs[b];
+    s.seq = ids[b];
     s.row0 = b * p.Q * p.heads + g * p.NR;
     s.rows = min(p.NR, p.Q * p.heads - g * p.NR);
     s.tok0 = p.shared + x0 * kTok;
@@ -154,12 +167,11 @@ struct SegIter {
     s.part = nullptr;
     s.ml = nullptr;
     if (!whole || p.np) {
-      const int slot = whole ? 2 * p.teams * p.G + b * p.G + g : 2 * blockIdx.x + (first ? 0 : 1);
+      const int slot = whole ? 2 * p.teams * p.G + b * p.G + g : 2 * cta + (first ? 0 : 1);
       s.part = p.part_s + (size_t)slot * p.NR * rank;
       s.ml = p.ml_s + (size_t)slot * p.NR;
     }
     s.N = up16(s.rows);
-    pos += x1 - x0;
     first = false;
     return true;
   }
@@ -198,16 +210,20 @@ __device__ inline void tmem_ld_rows16(uint32_t taddr, uint32_t (&r)[32]) {
 // neighbouring entries of a row at once.
 template <typename T>
 __device__ inline void store_columns(uint32_t taddr, int rows, int stride, T* dst, const float* factor = nullptr) {
-  for (int c = 0; c < rows; c += 16) {
-    uint32_t v[16];
-    tmem_ld16(taddr + c, v);
+  uint32_t v[2][16];
+  tmem_ld16(taddr, v[0]);
+#pragma unroll
+  for (int c = 0; c < kRows; c += 16) {
+    if (c >= rows) break;
     tmem_ld_wait();
+    if (c + 16 < rows) tmem_ld16(taddr + c + 16, v[(c >> 4) + 1 & 1]);   // the next block arrives behind these stores
     const int n = rows - c;
 #pragma unroll
     for (int x = 0; x < 16; ++x) {
       if (x < n) {
-        if constexpr (sizeof(T) == 4) dst[x * stride] = __uint_as_float(v[x]);
-        else dst[x * stride] = __float2bfloat16_rn(__uint_as_float(v[x]) * factor[c + x]);
+        const float a = __uint_as_float(v[(c >> 4) & 1][x]);
+        if constexpr (sizeof(T) == 4) dst[x * stride] = a;
+        else dst[x * stride] = __float2bfloat16_rn(a * factor[c + x]);
       }
     }
     dst += 16 * stride;
@@ -241,6 +257,24 @@ __device__ inline float warp_max(float v) {
   return v;
 }
 
+// Two fp32 operations in one instruction.
+__device__ inline float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n .reg .b64 x, y, z, w;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n mov.b64 z, {%6, %7};\n"
+      " fma.rn.f32x2 w, x, y, z;\n mov.b64 {%0, %1}, w;\n}\n"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ inline float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n .reg .b64 x, y, w;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n"
+      " add.rn.f32x2 w, x, y;\n mov.b64 {%0, %1}, w;\n}\n"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+
 // OR of a predicate over the softmax warps (named barrier 1): the same answer in every thread.
 __device__ inline bool soft_any(bool v) {
   uint32_t r;
@@ -262,6 +296,7 @@ struct Shared {
   int warp_sum[kThreads / 32];
   int pref[kBatch + 1];
   int len[kBatch];
+  int ids[kBatch];
 };
 
 __global__ void __launch_bounds__(kThreads, 1)
@@ -286,13 +321,19 @@ decode_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_constant_
     mbar_init(&sh.q_empty, 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.s_full[i], 1);
-      mbar_init(&sh.s_empty[i], kSoftThreads);
+      mbar_init(&sh.s_empty[i], kSoftThreads / 32);
       mbar_init(&sh.pv_done[i], 1);
       mbar_init(&sh.drain[i], 1);
     }
-    mbar_init(&sh.p_full, kSoftThreads);
+    mbar_init(&sh.p_full, 1);
     sh.abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (tid == 32 * 2) {
+    prefetch_map(&map_kv);
+    prefetch_map(&map_pair);
+    prefetch_map(&map_q16);
+    prefetch_map(&map_q64);
   }
   if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&sh.tmem)),
@@ -300,6 +341,7 @@ decode_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_constant_
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
   pdl_wait();
+  pdl_trigger();   // the combine's CTAs need no shared memory to speak of: they wait beside these
   // lengths and tile sums of the batch (every CTA for itself)
   {
     int carry = 0;
@@ -312,7 +354,8 @@ decode_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_constant_
         const int len = good ? p.kv.len_of(s) : 0;
         if (!good && blockIdx.x == 0) set_status(p.status, MOE_DEV_ERR_BAD_SEQ);
         sh.len[b] = len;
-        n = len > p.shared ? (len - p.shared + kTok - 1) / kTok : 0;
+        sh.ids[b] = s;
+        n = len > p.shared ? (len - p.shared + kTok - 1) / kTok + kHead : 0;
       }
       int inc = n;
 #pragma unroll
@@ -337,7 +380,7 @@ decode_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_constant_
     for (int b = tid; b <= p.B; b += kThreads) p.plan[b] = sh.pref[b];
   const uint32_t tmem = sh.tmem;
   volatile int* abort_flag = &sh.abort;
-  SegIter it(p, sh.pref, sh.len);
+  SegIter it(p, sh.pref, sh.len, sh.ids);
   Seg sg;
 
   if (warp == 0) {
@@ -351,23 +394,32 @@ decode_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_constant_
     const bool pseq_ok = p.np == 0 || (*p.prefix_seq >= 0 && *p.prefix_seq < p.kv.max_seqs);
     const uint32_t smem0 = uni(smem_u32(smem)), kv0 = smem0 + chunks * kChunk;
     const uint32_t full0 = uni(smem_u32(&sh.full[0][0])), qbar = uni(smem_u32(&sh.q_full));
+    // rows that only this CTA reads leave L2 to the pieces; rows that others read too stay
+    const uint64_t once = l2_evict_first(), shared = l2_normal();
     while (__any_sync(0xffffffffu, ok && it.next(sg))) {
       const bool seq_ok = !sg.prefix || pseq_ok;      // a bad id in the batch has no tokens
+      const uint64_t pol = sg.prefix || p.G > 1 ? shared : once;
       const int32_t* blocks = p.kv.table + (seq_ok ? (size_t)sg.seq * p.kv.max_blocks : 0);
       const int tok0 = (int)uni(sg.tok0), tok1 = (int)uni(sg.tok1);
       // lane i: the pool row where box i of a tile begins; read one tile ahead
       auto block = [&](int t) { return seq_ok && lane < kTok / box && t < tok1 ? blocks[t >> p.kv.page_shift] : -1; };
       int ahead = block(tok0 + lane * box);
-      ok = warp_wait(&sh.q_empty, (nseg & 1) ^ 1u, abort_flag);
-      if (!ok) break;
       const int N = (int)uni(sg.N), row0 = (int)uni(sg.row0);
-      mbar_expect_tx_warp(qbar, (uint32_t)(cq * N * 128));
-      ++nseg;
-      for (int c = 0; c < cq; ++c) {
-        if (N == kRows) tma_load_2d_warp(smem0 + c * kChunk, &map_q64, qbar, c * kBK, row0);
-        else
-          for (int r = 0; r < N; r += 16) tma_load_2d_warp(smem0 + c * kChunk + r * 128, &map_q16, qbar, c * kBK, row0 + r);
-      }
+      // the queries follow the first tile: the tile's memory is free before the last piece's S lets go of its queries
+      auto load_q = [&]() {
+        if (!warp_wait(&sh.q_empty, (nseg & 1) ^ 1u, abort_flag)) return false;
+        mbar_expect_tx_warp(qbar, (uint32_t)(cq * N * 128));
+        ++nseg;
+        for (int c = 0; c < cq; ++c) {
+          if (N == kRows) tma_load_2d_warp(smem0 + c * kChunk, &map_q64, qbar, c * kBK, row0);
+          else
+            for (int r = 0; r < N; r += 16)
+              tma_load_2d_warp(smem0 + c * kChunk + r * 128, &map_q16, qbar, c * kBK, row0 + r);
+        }
+        return true;
+      };
+      const bool q_first = nseg == 0;
+      if (q_first) ok = load_q();
       for (int t0 = tok0; ok && t0 < tok1; t0 += kTok) {
         const int nb = (min(kTok, tok1 - t0) + box - 1) / box;       // boxes that hold tokens
         const int t = t0 + lane * box;
@@ -391,14 +443,14 @@ decode_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_constant_
           if (!ok) break;
           mbar_expect_tx_warp(bar + 8 * j, (uint32_t)(nb * box * 256));
           if (box == kTok) {   // both chunks of the pair in one copy
-            tma_load_3d_warp(dst + 2 * j * kChunk, &map_pair, bar + 8 * j, 0, rows[0], 2 * j);
+            tma_load_3d_hint_warp(dst + 2 * j * kChunk, &map_pair, bar + 8 * j, 0, rows[0], 2 * j, pol);
           } else {
 #pragma unroll
             for (int i = 0; i < kTok / 16; ++i)
               if (i < nb) {
-                tma_load_2d_warp(dst + 2 * j * kChunk + i * box * 128, &map_kv, bar + 8 * j, 2 * j * kBK, rows[i]);
-                tma_load_2d_warp(dst + (2 * j + 1) * kChunk + i * box * 128, &map_kv, bar + 8 * j, 2 * j * kBK + kBK,
-                                 rows[i]);
+                tma_load_2d_hint_warp(dst + 2 * j * kChunk + i * box * 128, &map_kv, bar + 8 * j, 2 * j * kBK, rows[i], pol);
+                tma_load_2d_hint_warp(dst + (2 * j + 1) * kChunk + i * box * 128, &map_kv, bar + 8 * j,
+                                      2 * j * kBK + kBK, rows[i], pol);
               }
           }
         }
@@ -409,9 +461,11 @@ decode_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_constant_
             mbar_expect_tx_warp(bar + 8 * j, (uint32_t)(nb * box * 128));
 #pragma unroll
             for (int i = 0; i < kTok / 16; ++i)
-              if (i < nb) tma_load_2d_warp(dst + 2 * j * kChunk + i * box * 128, &map_kv, bar + 8 * j, 2 * j * kBK, rows[i]);
+              if (i < nb)
+                tma_load_2d_hint_warp(dst + 2 * j * kChunk + i * box * 128, &map_kv, bar + 8 * j, 2 * j * kBK, rows[i], pol);
           }
         }
+        if (ok && t0 == tok0 && !q_first) ok = load_q();
         ++tile;
         if (++slot == p.slots) {
           slot = 0;
@@ -536,6 +590,10 @@ decode_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_constant_
     const int rank = p.kv.rank;
     int tile = 0;
     bool fail = false;
+    const float scale = p.scale_log2;
+    const float unseen = scale >= 0.0f ? -INFINITY : INFINITY;   // what a token out of sight scores
+    if (st < kRows) sh.factor[st] = 1.0f;
+    soft_any(false);
     while (!fail && it.next(sg)) {
       int limit[2];
       bool active[2];
@@ -565,51 +623,87 @@ decode_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_constant_
           tmem_ld_rows16(lane_base + kSCol + buf * kTok, reinterpret_cast<uint32_t(&)[32]>(s));
           tmem_ld_wait();
           tc_fence_before();
-          mbar_arrive(&sh.s_empty[buf]);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh.s_empty[buf]);
         }
-        bool grow = false;
+        bool grow = !ok;
         float ref[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const int see = min(n_tok, limit[e] - t0);
-          float top = -INFINITY;
-          if (__all_sync(0xffffffffu, see >= kTok || !active[e])) {
+          if (!__all_sync(0xffffffffu, see >= kTok || !active[e])) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-              s[4 * i + 2 * e] *= p.scale_log2;
-              s[4 * i + 2 * e + 1] *= p.scale_log2;
-              top = fmaxf(top, fmaxf(s[4 * i + 2 * e], s[4 * i + 2 * e + 1]));
-            }
-          } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              s[4 * i + 2 * e] = 8 * i + c2 < see ? s[4 * i + 2 * e] * p.scale_log2 : -INFINITY;
-              s[4 * i + 2 * e + 1] = 8 * i + c2 + 1 < see ? s[4 * i + 2 * e + 1] * p.scale_log2 : -INFINITY;
-              top = fmaxf(top, fmaxf(s[4 * i + 2 * e], s[4 * i + 2 * e + 1]));
+              if (8 * i + c2 >= see) s[4 * i + 2 * e] = unseen;
+              if (8 * i + c2 + 1 >= see) s[4 * i + 2 * e + 1] = unseen;
             }
           }
-          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-          float f = 1.0f;
+          float top = s[2 * e];
+          if (p.scale_log2 >= 0.0f) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) top = fmaxf(top, fmaxf(s[4 * i + 2 * e], s[4 * i + 2 * e + 1]));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+          } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) top = fminf(top, fminf(s[4 * i + 2 * e], s[4 * i + 2 * e + 1]));
+            top = fminf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = fminf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+          }
+          top = see > 0 ? top * scale : -INFINITY;
           if (active[e] && top > m[e]) {
             if (m[e] == -INFINITY) {
               m[e] = top;             // nothing summed for this row yet
             } else if (top > m[e] + kGrow) {
-              f = ex2(m[e] - top);
+              const float f = ex2(m[e] - top);
               l[e].x *= f;
               l[e].y *= f;
               m[e] = top;
               grow = true;
+              if ((lane & 3) == 0) sh.factor[r0 + 8 * e] = f;
             }
           }
           ref[e] = m[e] == -INFINITY ? 0.0f : m[e];
-          if ((lane & 3) == 0) sh.factor[r0 + 8 * e] = f;
         }
-        fail = soft_any(!ok);
-        if (fail) break;
-        if (soft_any(grow)) {
+        // Probabilities, rounded to bf16 (the cache's type, the only one the product takes beside it).  Two sums:
+        // of the rounded ones, which the output is divided by (its weights then add up to one, and where few tokens
+        // carry the row most of their rounding cancels), and of the unrounded ones for the log-sum-exp.
+        uint8_t* sp = skv + slot * slot_bytes + 2 * p.pairs * kChunk + (lane & 3) * 4;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int r = r0 + 8 * e;
+          if (r < sg.N) {
+            uint8_t* prow = sp + r * 128;
+            float2 sum = make_float2(0.0f, 0.0f), rsum = sum;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              float2 x = fma2(make_float2(s[4 * i + 2 * e], s[4 * i + 2 * e + 1]), make_float2(scale, scale),
+                              make_float2(-ref[e], -ref[e]));
+              x.x = ex2(x.x);
+              x.y = ex2(x.y);
+              const __nv_bfloat162 h = __floats2bfloat162_rn(x.x, x.y);
+              const uint32_t w = *reinterpret_cast<const uint32_t*>(&h);
+              sum = add2(sum, x);
+              rsum = add2(rsum, make_float2(bf16_lo(w), bf16_hi(w)));
+              *reinterpret_cast<uint32_t*>(prow + ((i ^ (r & 7)) << 4)) = w;
+            }
+            l[e].x += sum.x + sum.y;
+            l[e].y += rsum.x + rsum.y;
+          }
+        }
+        if (n_tok < kTok) {
+          // places past the last token: any bits may stand there, and 0 * NaN is NaN
+          uint8_t* base = skv + slot * slot_bytes;
+          const int rows = kTok - n_tok;
+          for (int x = st; x < rows * 8 * 2 * p.pairs; x += kSoftThreads) {
+            const int c = x / (rows * 8), y = x - c * rows * 8;
+            *reinterpret_cast<uint4*>(base + c * kChunk + n_tok * 128 + y * 16) = make_uint4(0, 0, 0, 0);
+          }
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        if (soft_any(grow)) {      // rare: some row's maximum rose by more than 2^8 (or a wait ran out)
           // O was last added to by the previous tile's product, and this tile's waits for us
-          const bool done = warp_wait(&sh.pv_done[buf ^ 1], ((tile - 1) >> 1) & 1, abort_flag);
+          const bool done = ok && warp_wait(&sh.pv_done[buf ^ 1], ((tile - 1) >> 1) & 1, abort_flag);
           fail = soft_any(!done);
           if (fail) break;
           tc_fence_after();
@@ -623,41 +717,15 @@ decode_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_constant_
               tmem_st16(lane_base + j * kRows + c, v);
             }
           tmem_st_wait();
+          tc_fence_before();
           soft_any(false);       // everyone has read the factors
+          if (st < kRows) sh.factor[st] = 1.0f;
+          soft_any(false);
         }
-        // Probabilities, rounded to bf16 (the cache's type, the only one the product takes beside it).  Two sums:
-        // of the rounded ones, which the output is divided by (its weights then add up to one, and where few tokens
-        // carry the row most of their rounding cancels), and of the unrounded ones for the log-sum-exp.
-        uint8_t* sp = skv + slot * slot_bytes + 2 * p.pairs * kChunk + (lane & 3) * 4;
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int r = r0 + 8 * e;
-          if (r < sg.N) {
-            uint8_t* prow = sp + r * 128;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const float a = active[e] ? ex2(s[4 * i + 2 * e] - ref[e]) : 0.0f;
-              const float b = active[e] ? ex2(s[4 * i + 2 * e + 1] - ref[e]) : 0.0f;
-              const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-              const uint32_t w = *reinterpret_cast<const uint32_t*>(&h);
-              l[e].x += a + b;
-              l[e].y += bf16_lo(w) + bf16_hi(w);
-              *reinterpret_cast<uint32_t*>(prow + ((i ^ (r & 7)) << 4)) = w;
-            }
-          }
+        if (st == 0) {
+          tc_fence_before();
+          mbar_arrive(&sh.p_full);
         }
-        if (n_tok < kTok) {
-          // places past the last token: any bits may stand there, and 0 * NaN is NaN
-          uint8_t* base = skv + slot * slot_bytes;
-          const int rows = kTok - n_tok;
-          for (int x = st; x < rows * 8 * 2 * p.pairs; x += kSoftThreads) {
-            const int c = x / (rows * 8), y = x - c * rows * 8;
-            *reinterpret_cast<uint4*>(base + c * kChunk + n_tok * 128 + y * 16) = make_uint4(0, 0, 0, 0);
-          }
-        }
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        tc_fence_before();
-        mbar_arrive(&sh.p_full);
       }
       if (fail) break;
       const bool done = (tile < 2 || warp_wait(&sh.pv_done[tile & 1], ((tile - 2) >> 1) & 1, abort_flag)) &&
@@ -692,10 +760,11 @@ decode_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_constant_
           store_columns(lane_base + j * kRows, sg.rows, rank, dst, sh.factor);
       }
       tc_fence_before();
-      soft_any(false);   // the factors are free again
+      soft_any(false);
+      if (st < kRows) sh.factor[st] = 1.0f;
+      soft_any(false);
     }
   }
-  pdl_trigger();
   __syncthreads();
   if (*abort_flag && tid == 0) set_status(p.status, MOE_DEV_ERR_TIMEOUT);
   tc_fence_after();
@@ -703,105 +772,107 @@ decode_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_constant_
 }
 
 // ---------------------------------------------------------------- combine
-// One CTA per query row: its pieces' (m, l, O) in a fixed order (the prefix's
-// pieces, then the sequence's).  The first warp turns the pieces' statistics
-// into weights; then rank / 4 threads cover the row with float4 loads and the
-// rest of the CTA's 256 threads take other pieces, joined through shared
-// memory.  Bound by the latency of three dependent reads (tile sums,
-// statistics, partial rows) at small sizes, by L2 at large ones.
-constexpr int kCombineThreads = 256;
-constexpr int kMaxPieces = 1024;   // of a row: at most one per CTA of each line
-
-__global__ void __launch_bounds__(kCombineThreads)
+// Per query row: its pieces' (m, l, O) in a fixed order (the prefix's pieces,
+// then the sequence's).  rank / 128 warps cover a row, 128 entries each, and
+// find the pieces and their weights on their own (lane k looks after piece k);
+// with GROUPS > 1 as many sets of warps share the pieces out (few query rows,
+// so many pieces each) and meet in shared memory.  Three dependent reads deep
+// (tile sums, statistics, rows); bound by those at small sizes and by L2 at
+// large ones.
+template <int GROUPS>
+__global__ void __launch_bounds__(128 * GROUPS)
 combine_parts_kernel(const DecodeParams p) {
-  __shared__ float4 s_acc[kCombineThreads];
-  __shared__ const float* s_o[kMaxPieces];
-  __shared__ float s_w[kMaxPieces];
-  __shared__ float2 s_l;
-  __shared__ float s_ref;
+  __shared__ float4 s_acc[GROUPS > 1 ? 128 * GROUPS : 1];
   pdl_wait();
   pdl_trigger();
-  const int row = blockIdx.x, rank = p.kv.rank;
-  const int per_seq = p.Q * p.heads, b = row / per_seq, in_seq = row - b * per_seq;
+  const int row = blockIdx.x, rank = p.kv.rank, lane = threadIdx.x & 31;
+  const int per_seq = p.Q * p.heads, b = row / per_seq, in_seq = row - b * per_seq, g = in_seq / p.NR;
   const int total = p.plan[p.B], x0 = p.plan[b], x1 = p.plan[b + 1];
   const int per = per_cta(total, p.teams);
-  const int t0 = x1 > x0 ? x0 / per : 0, t1 = x1 > x0 ? (x1 - 1) / per : -1;
+  const int t0 = x1 > x0 ? (x0 + kHead) / per : 0, t1 = x1 > x0 ? (x1 - 1) / per : -1;   // from its first tile on
   const int n_s = t1 - t0 + 1;
-  int n_p = 0;
+  int n_p = 0, c0 = 0, pr = 0;
+  long long pa = 0, pp = 1;
   if (p.np) {
-    const int pp = per_cta((long long)p.Gp * p.np, p.ctas), i = row / p.NRp;
-    const long long a = (long long)i * p.np, z = a + p.np;
-    const int c0 = (int)(a / pp);
-    n_p = (int)((z - 1) / pp) - c0 + 1;
-    for (int k = threadIdx.x; k < n_p; k += kCombineThreads) {
-      const long long from = (long long)(c0 + k) * pp;
-      const int slot = (a >= from && z <= from + pp) ? 2 * p.ctas + i : 2 * (c0 + k) + (a > from ? 1 : 0);
-      const size_t at = (size_t)slot * p.NRp + (row - i * p.NRp);
-      s_o[k] = p.part_p + at * rank;
-    }
+    pp = p.per_p;
+    pr = row / p.NRp;
+    pa = (long long)pr * p.np;
+    c0 = (int)(pa / pp);
+    const long long c1 = (pa + p.np - 1) / pp;
+    n_p = (int)c1 - c0 + 1;
   } else if (n_s == 1) {
     return;   // written by decode_kernel
   }
-  const int g = in_seq / p.NR, n = n_p + n_s;
-  for (int k = threadIdx.x; k < n_s; k += kCombineThreads) {
-    const long long from = (long long)(t0 + k) * per;
-    const int slot = (x0 >= from && x1 <= from + per) ? 2 * p.teams * p.G + b * p.G + g
-                                                      : 2 * ((t0 + k) * p.G + g) + (x0 > from ? 1 : 0);
-    const size_t at = (size_t)slot * p.NR + (in_seq - g * p.NR);
-    s_o[n_p + k] = p.part_s + at * rank;
-  }
-  __syncthreads();
-  if (threadIdx.x < 32) {
-    // a piece's statistics sit at its row's index
-    auto stats = [&](int k) {
-      return k < n_p ? p.ml_p[(s_o[k] - p.part_p) / rank] : p.ml_s[(s_o[k] - p.part_s) / rank];
-    };
-    float top = -INFINITY, l = 0.0f, lr = 0.0f;
-    for (int k = threadIdx.x; k < n; k += 32) {
-      const float4 ml = stats(k);
-      const float now = fmaxf(top, ml.x), ref = now == -INFINITY ? 0.0f : now;
-      const float f = ex2(top - ref), w = ex2(ml.x - ref);
-      l = fmaf(l, f, ml.y * w);
-      lr = fmaf(lr, f, ml.z * w);
-      s_w[k] = ml.x;
-      top = now;
+  const int n = n_p + n_s;
+  // where piece k of this row lies: its index among all rows of its line's pieces
+  auto place = [&](int k) {
+    if (k < n_p) {
+      const long long from = (long long)(c0 + k) * pp;
+      const int slot = (pa >= from && pa + p.np <= from + pp) ? 2 * p.ctas + pr : 2 * (c0 + k) + (pa > from ? 1 : 0);
+      return (size_t)slot * p.NRp + (row - pr * p.NRp);
     }
-    const float all = warp_max(top), ref = all == -INFINITY ? 0.0f : all;
-    const float f = ex2(top - ref);
-    l = warp_sum(l * f);
-    lr = warp_sum(lr * f);
-    if (threadIdx.x == 0) {
-      s_l = make_float2(l, lr);
-      s_ref = ref;
-    }
+    const int t = t0 + k - n_p;
+    const long long from = (long long)t * per;
+    const int slot = (x0 + kHead >= from && x1 <= from + per) ? 2 * p.teams * p.G + b * p.G + g
+                                                              : 2 * (t * p.G + g) + (x0 > from ? 1 : 0);
+    return (size_t)slot * p.NR + (in_seq - g * p.NR);
+  };
+  float top = -INFINITY, l = 0.0f, lr = 0.0f;
+  for (int k = lane; k < n; k += 32) {
+    const float4 ml = (k < n_p ? p.ml_p : p.ml_s)[place(k)];
+    const float now = fmaxf(top, ml.x), ref = now == -INFINITY ? 0.0f : now;
+    const float f = ex2(top - ref), w = ex2(ml.x - ref);
+    l = fmaf(l, f, ml.y * w);
+    lr = fmaf(lr, f, ml.z * w);
+    top = now;
   }
-  __syncthreads();
-  const int quads = rank / 4, groups = kCombineThreads / quads;
-  const int v = threadIdx.x % quads, grp = threadIdx.x / quads;
+  const float all = warp_max(top), ref = all == -INFINITY ? 0.0f : all;
+  const float f = ex2(top - ref);
+  l = warp_sum(l * f);
+  lr = warp_sum(lr * f);
+  const int v = threadIdx.x % 128, grp = threadIdx.x / 128;   // float4 of the row; set of warps
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (grp < groups) {
-#pragma unroll 4
-    for (int k = grp; k < n; k += groups) {
-      const float w = ex2(s_w[k] - s_ref);
-      const float4 x = __ldcs(reinterpret_cast<const float4*>(s_o[k]) + v);
-      acc.x = fmaf(w, x.x, acc.x);
-      acc.y = fmaf(w, x.y, acc.y);
-      acc.z = fmaf(w, x.z, acc.z);
-      acc.w = fmaf(w, x.w, acc.w);
+  for (int k0 = 0; k0 < n; k0 += 32) {
+    const int mine = k0 + lane;
+    const size_t at = mine < n ? place(mine) : 0;
+    const float w_mine = mine < n ? ex2((mine < n_p ? p.ml_p : p.ml_s)[at].x - ref) : 0.0f;
+    const int m = min(32, n - k0);
+    for (int kb = grp; kb < m; kb += 8 * GROUPS) {   // eight reads in flight
+      float4 x[8];
+      float w[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int k = kb + j * GROUPS;
+        const size_t a = __shfl_sync(0xffffffffu, at, k & 31);
+        w[j] = __shfl_sync(0xffffffffu, w_mine, k & 31);
+        x[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (k < m && 4 * v < rank)
+          x[j] = __ldcs(reinterpret_cast<const float4*>((k0 + k < n_p ? p.part_p : p.part_s) + a * rank) + v);
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        if (kb + j * GROUPS >= m) break;
+        acc.x = fmaf(w[j], x[j].x, acc.x);
+        acc.y = fmaf(w[j], x[j].y, acc.y);
+        acc.z = fmaf(w[j], x[j].z, acc.z);
+        acc.w = fmaf(w[j], x[j].w, acc.w);
+      }
     }
   }
-  s_acc[threadIdx.x] = acc;
-  __syncthreads();
-  const float2 l = s_l;
-  if (threadIdx.x < quads) {
-    for (int q = 1; q < groups; ++q) {
-      const float4 x = s_acc[threadIdx.x + q * quads];
+  if (GROUPS > 1) {
+    s_acc[threadIdx.x] = acc;
+    __syncthreads();
+    if (grp > 0) return;
+    for (int q = 1; q < GROUPS; ++q) {
+      const float4 x = s_acc[q * 128 + v];
       acc.x += x.x;
       acc.y += x.y;
       acc.z += x.z;
       acc.w += x.w;
     }
-    const float inv = l.y == 0.0f ? 0.0f : 1.0f / l.y;
+  }
+  if (4 * v < rank) {
+    const float inv = lr == 0.0f ? 0.0f : 1.0f / lr;
     const __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x * inv, acc.y * inv);
     const __nv_bfloat162 hi = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
     uint2 packed;
@@ -809,7 +880,7 @@ combine_parts_kernel(const DecodeParams p) {
     packed.y = *reinterpret_cast<const uint32_t*>(&hi);
     reinterpret_cast<uint2*>(p.out + (size_t)row * rank)[v] = packed;
   }
-  if (p.lse && threadIdx.x == 0) p.lse[row] = l.x == 0.0f ? -INFINITY : (s_ref + log2f(l.x)) * 0.6931471805599453f;
+  if (p.lse && threadIdx.x == 0) p.lse[row] = l == 0.0f ? -INFINITY : (ref + log2f(l)) * 0.6931471805599453f;
 }
 
 // ---------------------------------------------------------------- host side
@@ -836,7 +907,7 @@ void fill_shape(DecodeParams& p, const moe_kv_cache& c, int B, int Q, int heads,
   p.shared = shared;
   p.rope = c.rope;
   p.pairs = c.rank / 128;
-  p.ctas = num_sms() < kMaxPieces / 2 ? num_sms() : kMaxPieces / 2;
+  p.ctas = num_sms();
   const Tiles s = row_tiles((long long)Q * heads), f = row_tiles((long long)B * Q * heads);
   p.G = s.n;
   p.NR = s.rows;
@@ -844,6 +915,7 @@ void fill_shape(DecodeParams& p, const moe_kv_cache& c, int B, int Q, int heads,
   p.np = (shared + kTok - 1) / kTok;
   p.Gp = p.np ? f.n : 0;
   p.NRp = f.rows;
+  p.per_p = (int)(((long long)p.Gp * p.np + p.ctas - 1) / p.ctas);
 }
 
 DecodeWs decode_ws(const DecodeParams& p, int rank) {
@@ -882,7 +954,10 @@ int launch_decode(const moe_kv_cache& c, DecodeParams p, const void* q, cudaStre
                                 227 * 1024 - (int)sizeof(Shared));
   });
   if (e == cudaSuccess) e = launch_k(decode_kernel, p.ctas, kThreads, smem, s, kv, pair, q16, q64, p);
-  if (e == cudaSuccess) e = launch_k(combine_parts_kernel, (unsigned)qrows, kCombineThreads, 0, s, p);
+  // 4 sets of warps a row while the rows alone do not fill the SMs (then a row has many pieces)
+  if (e == cudaSuccess)
+    e = qrows <= 4ull * p.ctas ? launch_k(combine_parts_kernel<4>, (unsigned)qrows, 512, 0, s, p)
+                               : launch_k(combine_parts_kernel<1>, (unsigned)qrows, 128, 0, s, p);
   return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
@@ -924,7 +999,8 @@ int moe_latent_decode(const moe_kv_cache* cache, int layer, const void* q, const
     const size_t row0 = (size_t)b0 * Q * heads;
     p.kv = kv_view(*cache);
     p.layer = layer;
-    p.scale_log2 = scale * 1.4426950408889634f;
+    // zero as the smallest normal number: a token out of sight scores -infinity, and 0 * -infinity is NaN
+    p.scale_log2 = scale == 0.0f ? FLT_MIN : scale * 1.4426950408889634f;
     p.seqs = seqs + b0;
     p.prefix_seq = seqs;
     p.out = reinterpret_cast<__nv_bfloat16*>(out) + row0 * cache->rank;
