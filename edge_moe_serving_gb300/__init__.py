@@ -17,7 +17,7 @@ LIB_PATH = os.path.join(_HERE, "libmoe.so")
 
 MOE_OK, MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_WORKSPACE, MOE_ERR_CUDA = range(5)
 MOE_DEV_ERR_BAD_ID, MOE_DEV_ERR_UNBOUND, MOE_DEV_ERR_BAD_SLOT, MOE_DEV_ERR_TIMEOUT = 1, 2, 4, 8
-MOE_DEV_ERR_BAD_SEQ, MOE_DEV_ERR_BAD_PAGE, MOE_DEV_ERR_CAPACITY = 16, 32, 64
+MOE_DEV_ERR_BAD_SEQ, MOE_DEV_ERR_BAD_PAGE, MOE_DEV_ERR_CAPACITY, MOE_DEV_ERR_RANGE = 16, 32, 64, 128
 MOE_FILL_LOWEST_ID, MOE_FILL_RANDOM = 0, 1
 MOE_FFN_AUTO, MOE_FFN_GEMV, MOE_FFN_GEMM = 0, 1, 2
 MOE_STAGING_TAG = 1 << 30

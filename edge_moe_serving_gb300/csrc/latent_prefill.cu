@@ -1,34 +1,58 @@
 // Expanded latent attention of prompt tokens: keys and values are made per
 // head from the cached latents, then a causal softmax attention reads them.
 //
-// Simple form.  expand_kernel: k and v of every cached token and head into the
-// workspace, 32 x 32 output tiles over 32-wide slices of the latents in shared
-// memory (fp32 sums, rounded to bf16 once).  attend_kernel: one warp per
-// (query row, head) with the query and the running output in registers and
-// the softmax's running maximum and sum, each key and value read once per
-// row.
+// plan_kernel    where each sequence's expanded rows begin, and the query blocks
+// expand_kernel  [128 tokens] x [one head's keys and values]: latents W^T, fp32
+//                sums in tensor memory, f16 results into the workspace
+// attend_kernel  256 query rows of one head against that head's keys and
+//                values, 128 tokens at a time
+//
+// Keys, values, queries and probabilities are f16, not bf16: 11 significand
+// bits keep each rounding at 2^-12 where bf16's would put 2^-9 on every key,
+// value and probability, at the same tensor-core rate.  The price is range: an
+// expanded key or value beyond 65504 is clamped and reported
+// (MOE_DEV_ERR_RANGE); a query row is brought into range by its own power of
+// two, which goes into the row's score scale, so queries lose nothing.
 #include <cmath>
 
+#include <cuda_fp16.h>
+
 #include "kv_common.cuh"
+#include "tc_common.cuh"
 
 namespace moe {
 namespace {
 
-constexpr int kTile = 32;
-constexpr int kRowAlign = 128;   // sequences start at multiples of this in the expanded buffers
+using namespace tc;
+
+constexpr int kRowAlign = 128;           // sequences start at multiples of this in the expanded buffers
+constexpr int kBlock = 256;              // query rows of a work item: two tiles of 128
+constexpr int kTile = 128;               // tokens of a tile (and query rows of a tile)
+constexpr int kChunkBytes = kTile * kBK * 2;   // 16 KB: 128 rows x 64 entries
+constexpr int kRing = 8;                 // chunks of keys and values in flight
+constexpr int kThreads = 320;            // producer, MMA issuer, 2 x 4 softmax warps
+constexpr int kTmemCols = 512;
+constexpr float kGrow = 8.0f;            // log2 of the growth of a row's maximum that forces a rescaling
+
+struct QBlock {
+  int b, j0;   // sequence of the batch, first of its query rows
+};
 
 struct PrefillParams {
   KvView kv;
-  int layer, B, T, heads, dn, dv, kv_rows;
+  int layer, B, T, heads, dn, dv, rope, kv_rows, max_blocks_q;
   float scale_log2;
   const __nv_bfloat16* q;
   const int32_t* seqs;
   const int32_t* q_off;
   const __nv_bfloat16* w;
   __nv_bfloat16* out;
-  int32_t* base;            // [B + 1] first expanded row of each sequence; base[B] < 0: over capacity
-  __nv_bfloat16* k;         // [heads, kv_rows, dn]
-  __nv_bfloat16* v;         // [heads, kv_rows, dv]
+  int32_t* base;            // [B + 1] first expanded row of each sequence; base[B]: their end, < 0: over capacity
+  int32_t* counts;          // [0] query blocks, [1] next work item
+  QBlock* blocks;
+  __half* k;                // [heads, kv_rows, dn]
+  __half* v;                // [heads, kv_rows, dv]
+  __half* r;                // [kv_rows, rope]
   uint32_t* status;
 };
 
@@ -37,41 +61,108 @@ __device__ inline int seq_len(const PrefillParams& p, int b) {
   return s >= 0 && s < p.kv.max_seqs ? p.kv.len_of(s) : 0;
 }
 
-// One CTA: where each sequence's expanded rows begin.
-__global__ void layout_kernel(const PrefillParams p) {
-  pdl_wait();
-  pdl_trigger();
-  if (threadIdx.x != 0) return;
-  long long at = 0;
-  for (int b = 0; b < p.B; ++b) {
-    p.base[b] = (int)at;
-    at += (seq_len(p, b) + kRowAlign - 1) / kRowAlign * kRowAlign;
-    if (at > p.kv_rows) {
-      p.base[p.B] = -1;
-      set_status(p.status, MOE_DEV_ERR_CAPACITY);
-      return;
-    }
+// f16 of a value, clamped to its range; NaN and infinities stay what they are.
+__device__ inline __half to_half(float x, bool& clamped) {
+  const float a = fabsf(x);
+  if (a > 65504.0f && a < INFINITY) {
+    clamped = true;
+    x = copysignf(65504.0f, x);
   }
-  p.base[p.B] = (int)at;
+  return __float2half_rn(x);
 }
 
-__global__ void __launch_bounds__(kTile * kTile / 4) expand_kernel(const PrefillParams p) {
-  __shared__ float sx[kTile][kTile + 1], sw[kTile][kTile + 1];
+// ---------------------------------------------------------------- plan
+// One CTA.  Expanded rows: sums of the lengths rounded up to 128.  Query
+// blocks: 256 rows each, a sequence's last block first (it sees most tokens, and
+// long work items started first leave the shortest tail).
+constexpr int kPlanThreads = 512;
+
+__device__ inline void scan2(int (&v)[2], int (&total)[2], int (*sh)[kPlanThreads / 32]) {
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    int inc = v[e];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += u;
+    }
+    if (lane == 31) sh[e][w] = inc;
+    v[e] = inc - v[e];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    int base = 0, all = 0;
+    for (int i = 0; i < kPlanThreads / 32; ++i) {
+      if (i < w) base += sh[e][i];
+      all += sh[e][i];
+    }
+    v[e] += base;
+    total[e] = all;
+  }
+  __syncthreads();
+}
+
+__global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PrefillParams p) {
+  __shared__ int sh[2][kPlanThreads / 32];
+  pdl_wait();
+  pdl_trigger();
+  long long rows = 0;
+  int blocks = 0;
+  for (int b0 = 0; b0 < p.B; b0 += kPlanThreads) {
+    const int b = b0 + threadIdx.x;
+    int v[2] = {0, 0}, total[2], n = 0;
+    if (b < p.B) {
+      const int s = p.seqs[b], len = seq_len(p, b), q0 = p.q_off[b], q1 = p.q_off[b + 1];
+      const bool good = s >= 0 && s < p.kv.max_seqs && q0 >= 0 && q1 >= q0 && q1 <= p.T && q1 - q0 <= len;
+      if (!good) set_status(p.status, MOE_DEV_ERR_BAD_SEQ);
+      n = good ? q1 - q0 : 0;
+      // in units of 128 rows, a length past the buffer as one unit too many: the sums stay small
+      v[0] = min((len + kRowAlign - 1) / kRowAlign, p.kv_rows / kRowAlign + 1);
+      v[1] = (n + kBlock - 1) / kBlock;
+    }
+    const int mine = v[1];
+    scan2(v, total, sh);
+    if (b < p.B) {
+      const long long at = rows + (long long)v[0] * kRowAlign;
+      p.base[b] = at < p.kv_rows ? (int)at : p.kv_rows;
+      for (int i = 0; i < mine; ++i) {
+        const int x = blocks + v[1] + mine - 1 - i;
+        if (x < p.max_blocks_q) p.blocks[x] = QBlock{b, i * kBlock};
+      }
+    }
+    rows += (long long)total[0] * kRowAlign;
+    blocks += total[1];
+  }
+  if (threadIdx.x == 0) {
+    const bool fits = rows <= p.kv_rows;
+    if (!fits) set_status(p.status, MOE_DEV_ERR_CAPACITY);
+    p.base[p.B] = fits ? (int)rows : -1;
+    p.counts[0] = fits ? min(blocks, p.max_blocks_q) : 0;
+    p.counts[1] = 0;
+  }
+}
+
+// ---------------------------------------------------------------- expand (simple form)
+constexpr int kEx = 32;
+
+__global__ void __launch_bounds__(256) expand_kernel(const PrefillParams p) {
+  __shared__ float sx[kEx][kEx + 1], sw[kEx][kEx + 1];
   pdl_wait();
   pdl_trigger();
   const int total = p.base[p.B];
-  const int r0 = blockIdx.x * kTile;
+  const int r0 = blockIdx.x * kEx;
   if (r0 >= total) return;
   int b = 0;
   while (b + 1 < p.B && p.base[b + 1] <= r0) ++b;
   const int t0 = r0 - p.base[b], len = seq_len(p, b);
-  if (t0 >= len) return;
   const int feats = p.dn + p.dv;
-  const int f0 = blockIdx.y * kTile;   // feature of all heads: a tile lies in one head's keys or values
+  const int f0 = blockIdx.y * kEx;
   const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
   float acc[4] = {};
-  for (int c0 = 0; c0 < p.kv.rank; c0 += kTile) {
-    for (int j = ty; j < kTile; j += 8) {
+  for (int c0 = 0; c0 < p.kv.rank; c0 += kEx) {
+    for (int j = ty; j < kEx; j += 8) {
       const int t = t0 + j;
       float x = 0.0f;
       if (t < len) {
@@ -80,83 +171,480 @@ __global__ void __launch_bounds__(kTile * kTile / 4) expand_kernel(const Prefill
           if (tx == 0) set_status(p.status, MOE_DEV_ERR_BAD_PAGE);
           page = 0;
         }
-        x = __bfloat162float(p.kv.pages[p.kv.row_offset(p.layer, page, t & (p.kv.page_tokens - 1)) + c0 + tx]);
+        const size_t at = p.kv.row_offset(p.layer, page, t & (p.kv.page_tokens - 1));
+        x = __bfloat162float(p.kv.pages[at + c0 + tx]);
+        if (f0 == 0 && c0 == 0)
+          for (int d = tx; d < p.rope; d += 32)
+            p.r[(size_t)(r0 + j) * p.rope + d] = __float2half_rn(__bfloat162float(p.kv.pages[at + p.kv.rank + d]));
+      } else if (f0 == 0 && c0 == 0) {
+        for (int d = tx; d < p.rope; d += 32) p.r[(size_t)(r0 + j) * p.rope + d] = __float2half_rn(0.0f);
       }
       sx[j][tx] = x;
       sw[j][tx] = __bfloat162float(p.w[(size_t)(f0 + j) * p.kv.rank + c0 + tx]);
     }
     __syncthreads();
-    for (int c = 0; c < kTile; ++c)
+    for (int c = 0; c < kEx; ++c)
 #pragma unroll
       for (int j = 0; j < 4; ++j) acc[j] = fmaf(sx[ty + 8 * j][c], sw[tx][c], acc[j]);
     __syncthreads();
   }
   const int h = f0 / feats, f = f0 - h * feats + tx;
+  bool clamped = false;
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    if (t0 + ty + 8 * j >= len) continue;
     const size_t r = (size_t)h * p.kv_rows + r0 + ty + 8 * j;
-    if (f < p.dn) p.k[r * p.dn + f] = __float2bfloat16_rn(acc[j]);
-    else p.v[r * p.dv + f - p.dn] = __float2bfloat16_rn(acc[j]);
+    const __half x = to_half(acc[j], clamped);
+    if (f < p.dn) p.k[r * p.dn + f] = x;
+    else p.v[r * p.dv + f - p.dn] = x;
   }
+  if (clamped) set_status(p.status, MOE_DEV_ERR_RANGE);
 }
 
-__global__ void __launch_bounds__(256) attend_kernel(const PrefillParams p) {
+// ---------------------------------------------------------------- attention
+__device__ inline void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};"
+      ::"r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
+        "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]),
+        "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(taddr));
+}
+// Product with the A operand in tensor memory (16-bit entries, two to a column), one elected lane of a warp issuing.
+__device__ inline void tc_mma_ta_warp(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc, uint32_t accum) {
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n elect.sync _|q, 0xffffffff;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n"
+      ::"r"(d_tmem), "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accum)
+      : "memory");
+}
+
+// fp32 accumulation, f16 operands, A and B K-major
+__host__ __device__ constexpr uint32_t idesc_f16(int M, int N) { return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24); }
+struct Shared {
+  uint64_t full[kRing], empty[kRing];            // chunks of keys and values
+  uint64_t q_full[2], q_ready[2], q_empty[2];    // a query tile: loaded, turned to f16, no longer read
+  uint64_t s_full[2], p_ready[2], o_full[2];
+  uint64_t w_full[2], w_empty[2];                // work items
+  uint64_t drain;
+  int item[2];
+  uint32_t tmem;
+  int abort;
+};
+
+// A work item: 256 query rows of one head.
+struct Item {
+  int head, row0, rows, limit0, base, tiles[2];   // row r sees tokens below limit0 + r
+};
+
+__device__ inline bool get_item(const PrefillParams& p, int k, int n_blocks, int group, Item& it) {
+  if (k >= n_blocks * p.heads) return false;
+  // heads in groups that fill the grid once, so that a group's keys and values are read while they are in L2
+  const int per = n_blocks * group, gi = k / per, in = k - gi * per;
+  const int gh = min(group, p.heads - gi * group), x = in / gh;
+  it.head = gi * group + (in - x * gh);
+  const QBlock qb = p.blocks[x];
+  const int q0 = p.q_off[qb.b], n = p.q_off[qb.b + 1] - q0, len = seq_len(p, qb.b);
+  it.row0 = q0 + qb.j0;
+  it.rows = min(kBlock, n - qb.j0);
+  it.limit0 = len - n + qb.j0 + 1;
+  it.base = p.base[qb.b];
+#pragma unroll
+  for (int g = 0; g < 2; ++g) {
+    const int last = min(it.rows, (g + 1) * kTile) - 1;   // the tile's last row sees the most
+    it.tiles[g] = last >= g * kTile ? (it.limit0 + last + kTile - 1) / kTile : 0;
+  }
+  return true;
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+attend_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
+              const __grid_constant__ CUtensorMap map_r, const __grid_constant__ CUtensorMap map_v,
+              const PrefillParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ Shared sh;
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int kc = p.dn / kBK + (p.rope ? 1 : 0), vc = p.dv / kBK;   // chunks of a key and a value tile
+  const int q_bytes = kc * kChunkBytes;                            // a query tile
+
+  if (tid == 0) {
+    for (int i = 0; i < kRing; ++i) {
+      mbar_init(&sh.full[i], 1);
+      mbar_init(&sh.empty[i], 1);
+    }
+    for (int g = 0; g < 2; ++g) {
+      mbar_init(&sh.q_full[g], 1);
+      mbar_init(&sh.q_ready[g], 4);
+      mbar_init(&sh.q_empty[g], 1);
+      mbar_init(&sh.s_full[g], 1);
+      mbar_init(&sh.p_ready[g], 4);
+      mbar_init(&sh.o_full[g], 1);
+      mbar_init(&sh.w_full[g], 1);
+      mbar_init(&sh.w_empty[g], 9);
+    }
+    mbar_init(&sh.drain, 1);
+    sh.abort = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (tid == 64) {
+    prefetch_map(&map_q);
+    prefetch_map(&map_k);
+    prefetch_map(&map_r);
+    prefetch_map(&map_v);
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&sh.tmem)),
+                 "r"(kTmemCols));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
   pdl_wait();
   pdl_trigger();
-  const int lane = threadIdx.x & 31;
-  const long long unit = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
-  if (unit >= (long long)p.T * p.heads || p.base[p.B] < 0) return;
-  const int i = (int)(unit / p.heads), h = (int)(unit - (long long)i * p.heads);
-  int b = 0;
-  while (b + 1 < p.B && p.q_off[b + 1] <= i) ++b;
-  const int q0 = p.q_off[b], q1 = p.q_off[b + 1], seq = p.seqs[b];
-  const int len = seq_len(p, b);
-  if (i < q0 || i >= q1 || q1 - q0 > len || seq < 0 || seq >= p.kv.max_seqs) {
-    if (lane == 0) set_status(p.status, MOE_DEV_ERR_BAD_SEQ);
-    return;
-  }
-  const int limit = len - (q1 - q0) + (i - q0) + 1;
-  const int rope = p.kv.row - p.kv.rank, dim = p.dn + rope;
-  float q[6], o[4];
-#pragma unroll
-  for (int j = 0; j < 6; ++j) q[j] = lane + 32 * j < dim ? __bfloat162float(p.q[(size_t)unit * dim + lane + 32 * j]) : 0.0f;
-#pragma unroll
-  for (int j = 0; j < 4; ++j) o[j] = 0.0f;
-  float m = -INFINITY, l = 0.0f;
-  for (int t = 0; t < limit; ++t) {
-    const size_t r = (size_t)h * p.kv_rows + p.base[b] + t;
-    int page = p.kv.table[(size_t)seq * p.kv.max_blocks + (t >> p.kv.page_shift)];
-    if (page < 0 || page >= p.kv.n_pages) page = 0;
-    const __nv_bfloat16* kr = p.kv.pages + p.kv.row_offset(p.layer, page, t & (p.kv.page_tokens - 1)) + p.kv.rank;
-    float dot = 0.0f;
-#pragma unroll
-    for (int j = 0; j < 6; ++j) {
-      const int d = lane + 32 * j;
-      if (d < dim) dot = fmaf(q[j], __bfloat162float(d < p.dn ? p.k[r * p.dn + d] : kr[d - p.dn]), dot);
+  const uint32_t tmem = sh.tmem;
+  volatile int* abort_flag = &sh.abort;
+  const int n_blocks = p.counts[0];
+  const int group = n_blocks ? max(1, min(p.heads, (int)gridDim.x / n_blocks)) : 1;
+  Item it;
+
+  if (warp == 0) {
+    // ------------------------------------------------ work items and TMA
+    const uint32_t smem0 = uni(smem_u32(smem)), ring0 = smem0 + 2 * q_bytes;
+    const uint32_t full0 = uni(smem_u32(&sh.full[0])), qf0 = uni(smem_u32(&sh.q_full[0]));
+    int n = 0, chunk = 0, q_loads[2] = {0, 0};
+    uint32_t par = 1;
+    bool ok = true;
+    // one chunk into the ring
+    auto load = [&](const CUtensorMap* map, int c0, int c1) {
+      if (!ok) return;
+      const int slot = chunk % kRing;
+      ok = warp_wait(&sh.empty[slot], par, abort_flag);
+      if (!ok) return;
+      mbar_expect_tx_warp(full0 + 8 * slot, kChunkBytes);
+      tma_load_2d_warp(ring0 + slot * kChunkBytes, map, full0 + 8 * slot, c0, c1);
+      if (++chunk % kRing == 0) par ^= 1u;
+    };
+    for (;;) {
+      ok = warp_wait(&sh.w_empty[n & 1], ((n >> 1) & 1) ^ 1u, abort_flag);
+      if (!ok) break;
+      int k = 0;
+      if (lane == 0) {
+        k = atomicAdd(&p.counts[1], 1);
+        sh.item[n & 1] = k;
+        mbar_arrive(&sh.w_full[n & 1]);
+      }
+      k = (int)uni(k);
+      ++n;
+      if (!__any_sync(0xffffffffu, get_item(p, k, n_blocks, group, it))) break;
+      const int row0 = (int)uni(it.row0), head = (int)uni(it.head), base = (int)uni(it.base);
+      const int t[2] = {(int)uni(it.tiles[0]), (int)uni(it.tiles[1])}, tiles = max(t[0], t[1]);
+      for (int g = 0; g < 2 && ok; ++g) {
+        if (!t[g]) continue;
+        ok = warp_wait(&sh.q_empty[g], (q_loads[g] & 1) ^ 1u, abort_flag);
+        if (!ok) break;
+        ++q_loads[g];
+        mbar_expect_tx_warp(qf0 + 8 * g, (uint32_t)q_bytes);
+        for (int c = 0; c < kc; ++c)
+          tma_load_2d_warp(smem0 + g * q_bytes + c * kChunkBytes, &map_q, qf0 + 8 * g, head * (p.dn + p.rope) + c * kBK,
+                           row0 + g * kTile);
+        if (g == 0) {   // the first keys beside the queries
+          for (int c = 0; c < p.dn / kBK; ++c) load(&map_k, c * kBK, head * p.kv_rows + base);
+          if (p.rope) load(&map_r, 0, base);
+        }
+      }
+      for (int i = 0; i < tiles && ok; ++i) {
+        const int at = base + i * kTile;
+        for (int c = 0; c < vc; ++c) load(&map_v, c * kBK, head * p.kv_rows + at);
+        if (i + 1 < tiles) {
+          for (int c = 0; c < p.dn / kBK; ++c) load(&map_k, c * kBK, head * p.kv_rows + at + kTile);
+          if (p.rope) load(&map_r, 0, at + kTile);
+        }
+      }
+      if (!ok) break;
     }
-    const float s2 = warp_sum(dot) * p.scale_log2;
-    const float mn = fmaxf(m, s2);
-    const float ref = mn == -INFINITY ? 0.0f : mn;
-    const float f = exp2f(m - ref), w = exp2f(s2 - ref);
-    l = fmaf(l, f, w);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int d = lane + 32 * j;
-      if (d < p.dv) o[j] = fmaf(w, __bfloat162float(p.v[r * p.dv + d]), o[j] * f);
+    // drain: whatever was asked for lands before the CTA can exit
+    volatile int no_abort = 0;
+    for (int g = 0; g < 2; ++g)
+      if (q_loads[g]) mbar_wait(&sh.q_full[g], (q_loads[g] - 1) & 1, &no_abort);
+    for (int s = 0; s < kRing; ++s) {
+      const int loads = chunk / kRing + (chunk % kRing > s ? 1 : 0);
+      if (loads > 0) mbar_wait(&sh.full[s], (loads - 1) & 1, &no_abort);
     }
-    m = mn;
-  }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ------------------------------------------------ MMA issuer
+    // Order for tiles a, b: S_a(0) S_b(0) | PV_a(i) S_a(i+1) PV_b(i) S_b(i+1): while one tile's softmax runs, the
+    // other tile's products do.  P lies in its S's columns, so S_a(i+1) follows PV_a(i).
+    const uint32_t tm = uni(tmem), smem0 = uni(smem_u32(smem)), ring0 = smem0 + 2 * q_bytes;
+    const uint64_t dq0 = smem_desc(smem0), dk0 = smem_desc(ring0), dv0 = smem_desc_mn(ring0, kChunkBytes);
+    constexpr uint32_t idesc_s = idesc_f16(128, kTile);
+    int n = 0, q_uses[2] = {0, 0}, s_done[2] = {0, 0};
+    int front = 0;                    // ring position of the oldest chunk still needed
+    bool issued = false, ok = true;
+    auto wait_chunks = [&](int at, int count) {
+      for (int c = 0; c < count && ok; ++c) ok = warp_wait(&sh.full[(at + c) % kRing], ((at + c) / kRing) & 1, abort_flag);
+      tc_fence_after();
+    };
+    auto free_chunks = [&](int at, int count) {
+      for (int c = 0; c < count; ++c) tc_commit_warp(&sh.empty[(at + c) % kRing]);
+    };
+    auto issue_s = [&](int g, int at) {
+      const uint64_t dq = dq0 + ((uint64_t)(g * q_bytes) >> 4);
+      for (int c = 0; c < kc; ++c) {
+        const uint64_t a = dq + ((uint64_t)(c * kChunkBytes) >> 4);
+        const uint64_t b = dk0 + ((uint64_t)(((at + c) % kRing) * kChunkBytes) >> 4);
+        const int steps = c < p.dn / kBK ? 4 : p.rope / kUK;
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const int d = lane + 32 * j;
-    if (d < p.dv) p.out[(size_t)unit * p.dv + d] = __float2bfloat16_rn(o[j] / l);
+        for (int s = 0; s < 4; ++s)
+          if (s < steps) tc_mma_warp(tm + g * kTile, a + ((s * kUK * 2) >> 4), b + ((s * kUK * 2) >> 4), idesc_s, (c | s) ? 1u : 0u);
+      }
+      tc_commit_warp(&sh.s_full[g]);
+      issued = true;
+    };
+    auto issue_pv = [&](int g, int at, bool first) {
+      // a value tile's chunks follow one another in the ring, but may wrap around its end: 64 columns at a time
+      for (int c = 0; c < vc; ++c) {
+        const uint64_t b = dv0 + ((uint64_t)(((at + c) % kRing) * kChunkBytes) >> 4);
+#pragma unroll
+        for (int s = 0; s < kTile / kUK; ++s)
+          tc_mma_ta_warp(tm + 256 + g * kTile + c * kBK, tm + g * kTile + s * 8, b + ((s * kUK * 128) >> 4),
+                         idesc_f16(128, kBK) | kTransB, first && s == 0 ? 0u : 1u);
+      }
+    };
+    for (;;) {
+      ok = warp_wait(&sh.w_full[n & 1], (n >> 1) & 1, abort_flag);
+      if (!ok) break;
+      const int k = (int)uni(sh.item[n & 1]);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.w_empty[n & 1]);
+      ++n;
+      if (!__any_sync(0xffffffffu, get_item(p, k, n_blocks, group, it))) break;
+      const int t[2] = {(int)uni(it.tiles[0]), (int)uni(it.tiles[1])}, tiles = max(t[0], t[1]);
+      wait_chunks(front, kc);
+      for (int g = 0; g < 2 && ok; ++g) {
+        if (!t[g]) continue;
+        ok = warp_wait(&sh.q_ready[g], q_uses[g]++ & 1, abort_flag);
+        if (!ok) break;
+        tc_fence_after();
+        issue_s(g, front);
+        if (t[g] == 1) tc_commit_warp(&sh.q_empty[g]);
+      }
+      if (!ok) break;
+      free_chunks(front, kc);
+      front += kc;
+      for (int i = 0; i < tiles && ok; ++i) {
+        const int v_at = front, k_at = front + vc;
+        wait_chunks(v_at, vc);
+        bool have_k = false;
+        for (int g = 0; g < 2 && ok; ++g) {
+          if (i >= t[g]) continue;
+          ok = warp_wait(&sh.p_ready[g], s_done[g]++ & 1, abort_flag);
+          if (!ok) break;
+          tc_fence_after();
+          issue_pv(g, v_at, i == 0);
+          if (i + 1 == t[g]) tc_commit_warp(&sh.o_full[g]);
+          if (i + 1 < t[g]) {
+            if (!have_k) wait_chunks(k_at, kc);
+            if (!ok) break;
+            have_k = true;
+            issue_s(g, k_at);
+            if (i + 2 == t[g]) tc_commit_warp(&sh.q_empty[g]);
+          }
+        }
+        if (!ok) break;
+        free_chunks(v_at, vc);
+        front += vc;
+        if (i + 1 < tiles) {
+          free_chunks(k_at, kc);
+          front += kc;
+        }
+      }
+      if (!ok) break;
+    }
+    if (issued) {   // every issued product completes before tensor memory is released
+      volatile int no_abort = 0;
+      tc_commit_warp(&sh.drain);
+      mbar_wait(&sh.drain, 0, &no_abort);
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------ softmax: tile g = 0 in warps 2..5, 1 in warps 6..9; a thread owns a row
+    const int g = (warp - 2) >> 2, quarter = warp & 3, r = quarter * 32 + lane;
+    const uint32_t lane_base = tmem + ((uint32_t)(quarter * 32) << 16);
+    const uint32_t s_col = lane_base + g * kTile, o_col = lane_base + 256 + g * kTile;
+    uint8_t* qrow = smem + g * q_bytes + r * 128;
+    const int dim = p.dn + p.rope;
+    int n = 0, uses = 0, steps = 0;
+    bool ok = true;
+    for (;;) {
+      ok = warp_wait(&sh.w_full[n & 1], (n >> 1) & 1, abort_flag);
+      if (!ok) break;
+      const int k = sh.item[n & 1];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.w_empty[n & 1]);
+      ++n;
+      if (!__any_sync(0xffffffffu, get_item(p, k, n_blocks, group, it))) break;
+      const int tiles = it.tiles[g];
+      if (!tiles) continue;
+      // the query row in f16, scaled by a power of two so that its largest entry lies in [1, 2)
+      ok = warp_wait(&sh.q_full[g], uses & 1, abort_flag);
+      if (!ok) break;
+      float big = 0.0f;
+      for (int c = 0; c < kc; ++c)
+#pragma unroll
+        for (int x = 0; x < 8; ++x) {
+          if (c * kBK + 8 * x >= dim) break;
+          const uint4 u = *reinterpret_cast<const uint4*>(qrow + c * kChunkBytes + ((x ^ (r & 7)) << 4));
+          const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+          for (int y = 0; y < 4; ++y) big = fmaxf(big, fmaxf(fabsf(bf16_lo(w[y])), fabsf(bf16_hi(w[y]))));
+        }
+      // 2^e from the exponent bits; zero rows and rows with an infinity stay as they are
+      const uint32_t ebits = __float_as_uint(big) & 0x7F800000u;
+      const bool plain = ebits == 0 || ebits == 0x7F800000u || ebits == 0x7F000000u;
+      const float pow2 = plain ? 1.0f : __uint_as_float(ebits), inv = plain ? 1.0f : __uint_as_float(0x7F000000u - ebits);
+      for (int c = 0; c < kc; ++c)
+#pragma unroll
+        for (int x = 0; x < 8; ++x) {
+          uint4* at = reinterpret_cast<uint4*>(qrow + c * kChunkBytes + ((x ^ (r & 7)) << 4));
+          uint4 u = *at;
+          uint32_t* w = &u.x;
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            const __half2 h = __floats2half2_rn(bf16_lo(w[y]) * inv, bf16_hi(w[y]) * inv);
+            w[y] = *reinterpret_cast<const uint32_t*>(&h);
+          }
+          *at = u;
+        }
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.q_ready[g]);
+      ++uses;
+      const float scale = p.scale_log2 * pow2;
+      const bool neg = scale < 0.0f;
+      const int in_block = g * kTile + r, limit = it.limit0 + in_block;
+      float m = -INFINITY, l = 0.0f;
+      for (int i = 0; i < tiles; ++i, ++steps) {
+        ok = warp_wait(&sh.s_full[g], steps & 1, abort_flag);
+        if (!ok) break;
+        tc_fence_after();
+        // Two passes over the row of S, 32 columns at a time, the next ones read behind the work on these: the whole
+        // row would take 128 registers.  P's columns overwrite S's, always behind the reads.
+        const int see = limit - i * kTile;
+        const bool all = __all_sync(0xffffffffu, see >= kTile);
+        float top = neg ? INFINITY : -INFINITY;
+        uint32_t u[2][32];
+        tmem_ld32(s_col, u[0]);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          tmem_ld_wait();
+          tmem_ld32(s_col + 32 * ((c + 1) & 3), u[(c + 1) & 1]);
+          if (neg) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if (all || 32 * c + j < see) top = fminf(top, __uint_as_float(u[c & 1][j]));
+          } else if (all) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) top = fmaxf(top, __uint_as_float(u[c & 1][j]));
+          } else {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) top = fmaxf(top, 32 * c + j < see ? __uint_as_float(u[c & 1][j]) : -INFINITY);
+          }
+        }
+        top = see > 0 ? top * scale : -INFINITY;
+        bool grow = false;
+        float f = 1.0f;
+        if (top > m) {
+          if (m == -INFINITY) {
+            m = top;
+          } else if (top > m + kGrow) {
+            f = ex2(m - top);
+            l *= f;
+            m = top;
+            grow = true;
+          }
+        }
+        const float ref = m == -INFINITY ? 0.0f : m;
+        float2 sum0 = make_float2(0.0f, 0.0f), sum1 = sum0;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          tmem_ld_wait();
+          if (c < 3) tmem_ld32(s_col + 32 * (c + 1), u[(c + 1) & 1]);
+          uint32_t pk[16];
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            float2 x = fma2(make_float2(__uint_as_float(u[c & 1][2 * j]), __uint_as_float(u[c & 1][2 * j + 1])),
+                            make_float2(scale, scale), make_float2(-ref, -ref));
+            x.x = ex2(x.x);
+            x.y = ex2(x.y);
+            if (!all) {
+              x.x = 32 * c + 2 * j < see ? x.x : 0.0f;
+              x.y = 32 * c + 2 * j + 1 < see ? x.y : 0.0f;
+            }
+            if (j & 1) sum1 = add2(sum1, x);
+            else sum0 = add2(sum0, x);
+            const __half2 h = __floats2half2_rn(x.x, x.y);
+            pk[j] = *reinterpret_cast<const uint32_t*>(&h);
+          }
+          tmem_st16(s_col + 16 * c, pk);
+        }
+        l += (sum0.x + sum0.y) + (sum1.x + sum1.y);
+        if (__any_sync(0xffffffffu, grow)) {
+          // this S was issued behind the previous value product, so O is complete; the lanes are this warp's alone
+          for (int c = 0; c < p.dv; c += 32) {
+            uint32_t v[32];
+            tmem_ld32(o_col + c, v);
+            tmem_ld_wait();
+#pragma unroll
+            for (int x = 0; x < 32; ++x) v[x] = __float_as_uint(__uint_as_float(v[x]) * f);
+            tmem_st32(o_col + c, v);
+          }
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.p_ready[g]);
+      }
+      if (!ok) break;
+      ok = warp_wait(&sh.o_full[g], (uses - 1) & 1, abort_flag);
+      if (!ok) break;
+      tc_fence_after();
+      const float inv_l = 1.0f / l;
+      __nv_bfloat16* dst = p.out + ((size_t)(it.row0 + in_block) * p.heads + it.head) * p.dv;
+      for (int c = 0; c < p.dv; c += 32) {
+        uint32_t v[32];
+        tmem_ld32(o_col + c, v);
+        tmem_ld_wait();
+        if (in_block < it.rows) {
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            uint32_t w[4];
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+              const __nv_bfloat162 h = __floats2bfloat162_rn(__uint_as_float(v[8 * x + 2 * y]) * inv_l,
+                                                             __uint_as_float(v[8 * x + 2 * y + 1]) * inv_l);
+              w[y] = *reinterpret_cast<const uint32_t*>(&h);
+            }
+            *reinterpret_cast<uint4*>(dst + c + 8 * x) = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        }
+        __syncwarp();
+      }
+      tc_fence_before();
+    }
   }
+  __syncthreads();
+  if (*abort_flag && tid == 0) set_status(p.status, MOE_DEV_ERR_TIMEOUT);
+  tc_fence_after();
+  if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols));
 }
 
+// ---------------------------------------------------------------- host side
 struct PrefillWs {
-  size_t base, k, v, bytes;
-  int rows;
+  size_t base, counts, blocks, k, v, r, bytes;
+  int rows, n_blocks;
 };
 
 bool prefill_shape_ok(int B, int T, int heads, int dn, int dv, int kv_tokens) {
@@ -164,14 +652,47 @@ bool prefill_shape_ok(int B, int T, int heads, int dn, int dv, int kv_tokens) {
   return (long long)T * heads <= INT_MAX && ((long long)kv_tokens + 128LL * B) * heads <= INT_MAX;
 }
 
-PrefillWs prefill_ws(int B, int heads, int dn, int dv, int kv_tokens) {
+PrefillWs prefill_ws(int B, int T, int heads, int dn, int dv, int rope, int kv_tokens) {
   PrefillWs w;
   w.rows = (kv_tokens + kRowAlign - 1) / kRowAlign * kRowAlign + kRowAlign * (B - 1);
-  w.base = 0;
-  w.k = align_up((size_t)(B + 1) * sizeof(int32_t), 256);
-  w.v = w.k + align_up((size_t)heads * w.rows * dn * 2, 256);
-  w.bytes = w.v + align_up((size_t)heads * w.rows * dv * 2, 256);
+  w.n_blocks = T / kBlock + B;
+  size_t at = 0;
+  w.base = at;
+  at += align_up((size_t)(B + 1) * sizeof(int32_t), 256);
+  w.counts = at;
+  at += 256;
+  w.blocks = at;
+  at += align_up((size_t)w.n_blocks * sizeof(QBlock), 256);
+  w.k = at;
+  at += align_up((size_t)heads * w.rows * dn * 2, 256);
+  w.v = at;
+  at += align_up((size_t)heads * w.rows * dv * 2, 256);
+  w.r = at;
+  at += align_up((size_t)w.rows * (rope ? rope : 8) * 2, 256);
+  w.bytes = at;
   return w;
+}
+
+// f16 bits move like bf16 bits: the maps' element type only has to be 16 bits wide
+int launch_prefill(const PrefillParams& p, cudaStream_t s) {
+  CUtensorMap mq, mk, mr, mv;
+  const uint64_t rows = (uint64_t)p.heads * p.kv_rows;
+  if (!make_map(&mq, p.q, (uint64_t)p.heads * (p.dn + p.rope), p.T, kTile) || !make_map(&mk, p.k, p.dn, rows, kTile) ||
+      !make_map(&mr, p.rope ? (void*)p.r : (void*)p.k, p.rope ? p.rope : p.dn, p.rope ? p.kv_rows : rows, kTile) ||
+      !make_map(&mv, p.v, p.dv, rows, kTile))
+    return MOE_ERR_CUDA;
+  const int smem = 2 * (p.dn / kBK + (p.rope ? 1 : 0)) * kChunkBytes + kRing * kChunkBytes + 1024;
+  static_assert(2 * 3 * kChunkBytes + kRing * kChunkBytes + 1024 + sizeof(Shared) <= 227 * 1024, "shared memory");
+  static std::atomic<unsigned char> attr[kMaxDevices];
+  cudaError_t e = once_per_device(attr, [] {
+    return cudaFuncSetAttribute(attend_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                2 * 3 * kChunkBytes + kRing * kChunkBytes + 1024);
+  });
+  if (e == cudaSuccess) e = launch_k(plan_kernel, 1, kPlanThreads, 0, s, p);
+  if (e == cudaSuccess)
+    e = launch_k(expand_kernel, dim3(p.kv_rows / kEx, p.heads * (p.dn + p.dv) / kEx), 256, 0, s, p);
+  if (e == cudaSuccess) e = launch_k(attend_kernel, num_sms(), kThreads, smem, s, mq, mk, mr, mv, p);
+  return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
 }  // namespace
@@ -183,8 +704,8 @@ extern "C" {
 
 size_t moe_latent_prefill_workspace_size(const moe_kv_cache* cache, int B, int T, int heads, int dn, int dv,
                                          int kv_tokens) {
-  if (check_latent(cache, 0) != MOE_OK || B < 1 || T < 1 || heads < 1 || kv_tokens < 0) return 0;
-  return prefill_shape_ok(B, T, heads, dn, dv, kv_tokens) ? prefill_ws(B, heads, dn, dv, kv_tokens).bytes : 0;
+  if (check_latent(cache, 0) != MOE_OK || B < 1 || T < 1 || heads < 1 || kv_tokens < 1) return 0;
+  return prefill_shape_ok(B, T, heads, dn, dv, kv_tokens) ? prefill_ws(B, T, heads, dn, dv, cache->rope, kv_tokens).bytes : 0;
 }
 
 int moe_latent_prefill(const moe_kv_cache* cache, int layer, const void* q, const int32_t* seqs,
@@ -201,7 +722,7 @@ int moe_latent_prefill(const moe_kv_cache* cache, int layer, const void* q, cons
   if (!prefill_shape_ok(B, T, heads, dn, dv, kv_tokens)) return MOE_ERR_UNSUPPORTED;
   if (!some) return MOE_OK;
   if (!kv_aligned(q, 16) || !kv_aligned(w_kv, 16) || !kv_aligned(out, 16)) return MOE_ERR_UNSUPPORTED;
-  const PrefillWs w = prefill_ws(B, heads, dn, dv, kv_tokens);
+  const PrefillWs w = prefill_ws(B, T, heads, dn, dv, cache->rope, kv_tokens);
   st = check_ws(ws, ws_bytes, w.bytes);
   if (st != MOE_OK) return st;
   char* b = reinterpret_cast<char*>(ws);
@@ -213,7 +734,9 @@ int moe_latent_prefill(const moe_kv_cache* cache, int layer, const void* q, cons
   p.heads = heads;
   p.dn = dn;
   p.dv = dv;
+  p.rope = cache->rope;
   p.kv_rows = w.rows;
+  p.max_blocks_q = w.n_blocks;
   p.scale_log2 = scale * 1.4426950408889634f;
   p.q = reinterpret_cast<const __nv_bfloat16*>(q);
   p.seqs = seqs;
@@ -221,16 +744,13 @@ int moe_latent_prefill(const moe_kv_cache* cache, int layer, const void* q, cons
   p.w = reinterpret_cast<const __nv_bfloat16*>(w_kv);
   p.out = reinterpret_cast<__nv_bfloat16*>(out);
   p.base = reinterpret_cast<int32_t*>(b + w.base);
-  p.k = reinterpret_cast<__nv_bfloat16*>(b + w.k);
-  p.v = reinterpret_cast<__nv_bfloat16*>(b + w.v);
+  p.counts = reinterpret_cast<int32_t*>(b + w.counts);
+  p.blocks = reinterpret_cast<QBlock*>(b + w.blocks);
+  p.k = reinterpret_cast<__half*>(b + w.k);
+  p.v = reinterpret_cast<__half*>(b + w.v);
+  p.r = reinterpret_cast<__half*>(b + w.r);
   p.status = dev_status;
-  const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (launch_k(layout_kernel, 1, 32, 0, s, p) != cudaSuccess) return MOE_ERR_CUDA;
-  if (launch_k(expand_kernel, dim3(w.rows / kTile, heads * (dn + dv) / kTile), 256, 0, s, p) != cudaSuccess)
-    return MOE_ERR_CUDA;
-  const long long units = (long long)T * heads;
-  if (launch_k(attend_kernel, (unsigned)((units + 7) / 8), 256, 0, s, p) != cudaSuccess) return MOE_ERR_CUDA;
-  return MOE_OK;
+  return launch_prefill(p, reinterpret_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"
