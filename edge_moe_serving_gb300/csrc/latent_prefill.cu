@@ -61,14 +61,21 @@ __device__ inline int seq_len(const PrefillParams& p, int b) {
   return s >= 0 && s < p.kv.max_seqs ? p.kv.len_of(s) : 0;
 }
 
-// f16 of a value, clamped to its range; NaN and infinities stay what they are.
-__device__ inline __half to_half(float x, bool& clamped) {
-  const float a = fabsf(x);
-  if (a > 65504.0f && a < INFINITY) {
-    clamped = true;
-    x = copysignf(65504.0f, x);
+// f16 of two values, clamped to its range; NaN and infinities stay what they are.
+__device__ inline uint32_t half2_of(float x, float y, bool& clamped) {
+  const float ax = fabsf(x), ay = fabsf(y);
+  if (fmaxf(ax, ay) > 65504.0f) {
+    if (ax > 65504.0f && ax < INFINITY) {
+      clamped = true;
+      x = copysignf(65504.0f, x);
+    }
+    if (ay > 65504.0f && ay < INFINITY) {
+      clamped = true;
+      y = copysignf(65504.0f, y);
+    }
   }
-  return __float2half_rn(x);
+  const __half2 h = __floats2half2_rn(x, y);
+  return *reinterpret_cast<const uint32_t*>(&h);
 }
 
 // ---------------------------------------------------------------- plan
@@ -144,60 +151,244 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PrefillParams 
   }
 }
 
-// ---------------------------------------------------------------- expand (simple form)
-constexpr int kEx = 32;
+// ---------------------------------------------------------------- expand
+// D[128 tokens, one head's dn + dv features] = latents W_head^T, rank deep: the
+// latents of a token tile stay in shared memory (rank x 128 x 2 bytes) while the
+// CTA's heads' weights pass by in 64-deep stages, so a unit reads only its
+// weights.  Two accumulators in tensor memory (columns 0 and 256): the epilogue
+// of one unit runs under the products of the next.  Rows past a sequence's end
+// are written as zeros (the attention multiplies them by probability 0).
+// Bound by the weights' way from L2 to the SMs: 512 cycles of products per
+// 32 KB stage.
+// Warp 0 = TMA, warp 1 = MMA (and TMEM owner), warps 2..5 = epilogue.
+constexpr int kExThreads = 192;
+constexpr int kExStages = 3;
+constexpr int kExStage = 256 * kBK * 2;    // 32 KB of weights
+constexpr int kMaxChunks = 512 / kBK;
 
-__global__ void __launch_bounds__(256) expand_kernel(const PrefillParams p) {
-  __shared__ float sx[kEx][kEx + 1], sw[kEx][kEx + 1];
+struct ExShared {
+  uint64_t a_full[kMaxChunks], a_empty, b_full[kExStages], b_empty[kExStages], d_full[2], d_empty[2], drain;
+  uint32_t tmem;
+  int abort;
+};
+
+// 32 bytes at once: a whole sector of one row per thread.
+__device__ inline void st_sector(void* dst, const uint32_t* v) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(dst), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+               "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
+
+// The sequence that owns expanded row `row`.
+__device__ inline int seq_of_row(const PrefillParams& p, int row) {
+  int lo = 0, hi = p.B;   // the last b with base[b] <= row; sequences without tokens own no row
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (p.base[mid] <= row) lo = mid;
+    else hi = mid;
+  }
+  return lo;
+}
+
+__global__ void __launch_bounds__(kExThreads, 1)
+expand_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w,
+              const PrefillParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ ExShared sh;
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int chunks = p.kv.rank / kBK, N = p.dn + p.dv;
+  if (tid == 0) {
+    for (int c = 0; c < chunks; ++c) mbar_init(&sh.a_full[c], 1);
+    mbar_init(&sh.a_empty, 1);
+    for (int i = 0; i < kExStages; ++i) {
+      mbar_init(&sh.b_full[i], 1);
+      mbar_init(&sh.b_empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sh.d_full[i], 1);
+      mbar_init(&sh.d_empty[i], 4);
+    }
+    mbar_init(&sh.drain, 1);
+    sh.abort = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (tid == 64) {
+    prefetch_map(&map_x);
+    prefetch_map(&map_w);
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&sh.tmem)),
+                 "r"(kTmemCols));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
   pdl_wait();
   pdl_trigger();
-  const int total = p.base[p.B];
-  const int r0 = blockIdx.x * kEx;
-  if (r0 >= total) return;
-  int b = 0;
-  while (b + 1 < p.B && p.base[b + 1] <= r0) ++b;
-  const int t0 = r0 - p.base[b], len = seq_len(p, b);
-  const int feats = p.dn + p.dv;
-  const int f0 = blockIdx.y * kEx;
-  const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
-  float acc[4] = {};
-  for (int c0 = 0; c0 < p.kv.rank; c0 += kEx) {
-    for (int j = ty; j < kEx; j += 8) {
-      const int t = t0 + j;
-      float x = 0.0f;
-      if (t < len) {
-        int page = p.kv.table[(size_t)p.seqs[b] * p.kv.max_blocks + (t >> p.kv.page_shift)];
-        if (page < 0 || page >= p.kv.n_pages) {
-          if (tx == 0) set_status(p.status, MOE_DEV_ERR_BAD_PAGE);
-          page = 0;
+  const uint32_t tmem = sh.tmem;
+  volatile int* abort_flag = &sh.abort;
+  const int tiles = max(p.base[p.B], 0) / kTile;
+  const int total = tiles * p.heads;                       // units: token tile major, head minor
+  const int per = (total + gridDim.x - 1) / gridDim.x;
+  const int u0 = min(total, (int)blockIdx.x * per), u1 = min(total, u0 + per);
+
+  if (warp == 0) {
+    // ------------------------------------------------ TMA producer
+    const uint32_t smem0 = uni(smem_u32(smem)), b0 = smem0 + chunks * kChunkBytes;
+    const uint32_t af = uni(smem_u32(&sh.a_full[0])), bf = uni(smem_u32(&sh.b_full[0]));
+    const int page = p.kv.page_tokens, box = page;
+    int loaded = 0, stage = 0, fills = 0;
+    uint32_t par = 1;
+    bool ok = true;
+    for (int u = u0; ok && u < u1; ++u) {
+      const int tile = u / p.heads, head = u - tile * p.heads;
+      if (u == u0 || head == 0) {                          // another token tile
+        const int b = seq_of_row(p, tile * kTile), t0 = tile * kTile - p.base[b], len = seq_len(p, b);
+        const int nb = (int)uni((min(kTile, len - t0) + box - 1) / box);
+        int row = 0;
+        if (lane < nb) {
+          int pg = p.kv.table[(size_t)p.seqs[b] * p.kv.max_blocks + ((t0 + lane * box) >> p.kv.page_shift)];
+          if (pg < 0 || pg >= p.kv.n_pages) {
+            set_status(p.status, MOE_DEV_ERR_BAD_PAGE);
+            pg = 0;
+          }
+          row = (p.layer * p.kv.n_pages + pg) * page;
         }
-        const size_t at = p.kv.row_offset(p.layer, page, t & (p.kv.page_tokens - 1));
-        x = __bfloat162float(p.kv.pages[at + c0 + tx]);
-        if (f0 == 0 && c0 == 0)
-          for (int d = tx; d < p.rope; d += 32)
-            p.r[(size_t)(r0 + j) * p.rope + d] = __float2half_rn(__bfloat162float(p.kv.pages[at + p.kv.rank + d]));
-      } else if (f0 == 0 && c0 == 0) {
-        for (int d = tx; d < p.rope; d += 32) p.r[(size_t)(r0 + j) * p.rope + d] = __float2half_rn(0.0f);
+        int rows[kTile / 16];
+#pragma unroll
+        for (int i = 0; i < kTile / 16; ++i) rows[i] = (int)uni(lane == i ? row : 0);
+        ok = warp_wait(&sh.a_empty, (loaded & 1) ^ 1u, abort_flag);
+        if (!ok) break;
+        ++loaded;
+        for (int c = 0; c < chunks; ++c) {
+          mbar_expect_tx_warp(af + 8 * c, (uint32_t)(nb * box * 128));
+#pragma unroll
+          for (int i = 0; i < kTile / 16; ++i)
+            if (i < nb) tma_load_2d_warp(smem0 + c * kChunkBytes + i * box * 128, &map_x, af + 8 * c, c * kBK, rows[i]);
+        }
       }
-      sx[j][tx] = x;
-      sw[j][tx] = __bfloat162float(p.w[(size_t)(f0 + j) * p.kv.rank + c0 + tx]);
+      for (int c = 0; c < chunks; ++c) {
+        ok = warp_wait(&sh.b_empty[stage], par, abort_flag);
+        if (!ok) break;
+        mbar_expect_tx_warp(bf + 8 * stage, (uint32_t)(N * 128));
+        tma_load_2d_warp(b0 + stage * kExStage, &map_w, bf + 8 * stage, c * kBK, head * N);
+        ++fills;
+        if (++stage == kExStages) {
+          stage = 0;
+          par ^= 1u;
+        }
+      }
     }
-    __syncthreads();
-    for (int c = 0; c < kEx; ++c)
+    volatile int no_abort = 0;
+    if (loaded)
+      for (int c = 0; c < chunks; ++c) mbar_wait(&sh.a_full[c], (loaded - 1) & 1, &no_abort);
+    for (int i = 0; i < kExStages; ++i) {
+      const int n = fills / kExStages + (fills % kExStages > i ? 1 : 0);
+      if (n > 0) mbar_wait(&sh.b_full[i], (n - 1) & 1, &no_abort);
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ------------------------------------------------ MMA issuer
+    const uint32_t tm = uni(tmem), smem0 = uni(smem_u32(smem));
+    const uint64_t da0 = smem_desc(smem0), db0 = smem_desc(smem0 + chunks * kChunkBytes);
+    const uint32_t idesc = make_idesc(128, N);
+    int loaded = 0, stage = 0, n = 0;
+    uint32_t par = 0;
+    bool ok = true, issued = false;
+    for (int u = u0; ok && u < u1; ++u, ++n) {
+      const int head = u % p.heads, buf = n & 1;
+      if (u == u0 || head == 0) ++loaded;
+      ok = warp_wait(&sh.d_empty[buf], ((n >> 1) & 1) ^ 1u, abort_flag);
+      for (int c = 0; ok && c < chunks; ++c) {
+        ok = warp_wait(&sh.a_full[c], (loaded - 1) & 1, abort_flag) && warp_wait(&sh.b_full[stage], par, abort_flag);
+        if (!ok) break;
+        tc_fence_after();
+        const uint64_t da = da0 + ((uint64_t)(c * kChunkBytes) >> 4), db = db0 + ((uint64_t)(stage * kExStage) >> 4);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) acc[j] = fmaf(sx[ty + 8 * j][c], sw[tx][c], acc[j]);
-    __syncthreads();
-  }
-  const int h = f0 / feats, f = f0 - h * feats + tx;
-  bool clamped = false;
+        for (int k = 0; k < kBK / kUK; ++k)
+          tc_mma_warp(tm + buf * 256, da + ((k * kUK * 2) >> 4), db + ((k * kUK * 2) >> 4), idesc, k ? 1u : (c ? 1u : 0u));
+        issued = true;
+        tc_commit_warp(&sh.b_empty[stage]);
+        if (++stage == kExStages) {
+          stage = 0;
+          par ^= 1u;
+        }
+      }
+      if (!ok) break;
+      tc_commit_warp(&sh.d_full[buf]);
+      if (head == p.heads - 1) tc_commit_warp(&sh.a_empty);
+    }
+    if (issued) {
+      volatile int no_abort = 0;
+      tc_commit_warp(&sh.drain);
+      mbar_wait(&sh.drain, 0, &no_abort);
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------ epilogue: a thread owns a token row
+    const int quarter = warp & 3, r = quarter * 32 + lane;
+    const uint32_t lane_base = tmem + ((uint32_t)(quarter * 32) << 16);
+    int n = 0, b = 0, t = 0, len = 0;
+    bool clamped = false;
+    for (int u = u0; u < u1; ++u, ++n) {
+      const int tile = u / p.heads, head = u - tile * p.heads, buf = n & 1;
+      const int row = tile * kTile + r;
+      if (u == u0 || head == 0) {
+        b = seq_of_row(p, tile * kTile);
+        t = row - p.base[b];
+        len = seq_len(p, b);
+      }
+      const bool there = t < len;
+      if (head == 0 && p.rope) {                           // the rotary keys, once per token
+        const uint4* src = nullptr;
+        if (there) {
+          int pg = p.kv.table[(size_t)p.seqs[b] * p.kv.max_blocks + (t >> p.kv.page_shift)];
+          if (pg < 0 || pg >= p.kv.n_pages) pg = 0;
+          src = reinterpret_cast<const uint4*>(p.kv.pages + p.kv.row_offset(p.layer, pg, t & (p.kv.page_tokens - 1)) +
+                                               p.kv.rank);
+        }
+        for (int x = 0; x < p.rope / 8; ++x) {
+          const uint4 v = there ? src[x] : make_uint4(0, 0, 0, 0);
+          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+          uint32_t o[4];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const size_t r = (size_t)h * p.kv_rows + r0 + ty + 8 * j;
-    const __half x = to_half(acc[j], clamped);
-    if (f < p.dn) p.k[r * p.dn + f] = x;
-    else p.v[r * p.dv + f - p.dn] = x;
+          for (int y = 0; y < 4; ++y) o[y] = half2_of(bf16_lo(w[y]), bf16_hi(w[y]), clamped);
+          *reinterpret_cast<uint4*>(p.r + (size_t)row * p.rope + 8 * x) = make_uint4(o[0], o[1], o[2], o[3]);
+        }
+      }
+      if (!warp_wait(&sh.d_full[buf], (n >> 1) & 1, abort_flag)) break;
+      tc_fence_after();
+      const size_t at = (size_t)head * p.kv_rows + row;
+      uint32_t v[2][32];
+      const uint32_t col = lane_base + buf * 256;
+      tmem_ld32(col, v[0]);
+#pragma unroll
+      for (int c = 0; c < 8; ++c) {
+        if (32 * c >= N) break;
+        tmem_ld_wait();
+        if (32 * (c + 1) < N) tmem_ld32(col + 32 * (c + 1), v[(c + 1) & 1]);
+        uint32_t o[16];
+#pragma unroll
+        for (int y = 0; y < 16; ++y) {
+          const float e0 = __uint_as_float(v[c & 1][2 * y]), e1 = __uint_as_float(v[c & 1][2 * y + 1]);
+          o[y] = there ? half2_of(e0, e1, clamped) : 0u;
+        }
+        __half* dst = 32 * c < p.dn ? p.k + at * p.dn + 32 * c : p.v + at * p.dv + 32 * c - p.dn;
+        st_sector(dst, o);
+        st_sector(dst + 16, o + 8);
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.d_empty[buf]);
+    }
+    if (clamped) set_status(p.status, MOE_DEV_ERR_RANGE);
   }
-  if (clamped) set_status(p.status, MOE_DEV_ERR_RANGE);
+  __syncthreads();
+  if (*abort_flag && tid == 0) set_status(p.status, MOE_DEV_ERR_TIMEOUT);
+  tc_fence_after();
+  if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols));
 }
 
 // ---------------------------------------------------------------- attention
@@ -675,22 +866,28 @@ PrefillWs prefill_ws(int B, int T, int heads, int dn, int dv, int rope, int kv_t
 
 // f16 bits move like bf16 bits: the maps' element type only has to be 16 bits wide
 int launch_prefill(const PrefillParams& p, cudaStream_t s) {
-  CUtensorMap mq, mk, mr, mv;
+  CUtensorMap mq, mk, mr, mv, mx, mw;
   const uint64_t rows = (uint64_t)p.heads * p.kv_rows;
+  const uint64_t cache_rows = (uint64_t)p.kv.n_layers * p.kv.n_pages * p.kv.page_tokens;
   if (!make_map(&mq, p.q, (uint64_t)p.heads * (p.dn + p.rope), p.T, kTile) || !make_map(&mk, p.k, p.dn, rows, kTile) ||
       !make_map(&mr, p.rope ? (void*)p.r : (void*)p.k, p.rope ? p.rope : p.dn, p.rope ? p.kv_rows : rows, kTile) ||
-      !make_map(&mv, p.v, p.dv, rows, kTile))
+      !make_map(&mv, p.v, p.dv, rows, kTile) || !make_map(&mx, p.kv.pages, p.kv.row, cache_rows, p.kv.page_tokens) ||
+      !make_map(&mw, p.w, p.kv.rank, (uint64_t)p.heads * (p.dn + p.dv), p.dn + p.dv))
     return MOE_ERR_CUDA;
   const int smem = 2 * (p.dn / kBK + (p.rope ? 1 : 0)) * kChunkBytes + kRing * kChunkBytes + 1024;
   static_assert(2 * 3 * kChunkBytes + kRing * kChunkBytes + 1024 + sizeof(Shared) <= 227 * 1024, "shared memory");
+  const int ex_smem = p.kv.rank / kBK * kChunkBytes + kExStages * kExStage + 1024;
+  constexpr int kExSmem = kMaxChunks * kChunkBytes + kExStages * kExStage + 1024;
+  static_assert(kExSmem + sizeof(ExShared) <= 227 * 1024, "shared memory");
   static std::atomic<unsigned char> attr[kMaxDevices];
   cudaError_t e = once_per_device(attr, [] {
+    const cudaError_t x = cudaFuncSetAttribute(expand_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kExSmem);
+    if (x != cudaSuccess) return x;
     return cudaFuncSetAttribute(attend_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 2 * 3 * kChunkBytes + kRing * kChunkBytes + 1024);
   });
   if (e == cudaSuccess) e = launch_k(plan_kernel, 1, kPlanThreads, 0, s, p);
-  if (e == cudaSuccess)
-    e = launch_k(expand_kernel, dim3(p.kv_rows / kEx, p.heads * (p.dn + p.dv) / kEx), 256, 0, s, p);
+  if (e == cudaSuccess) e = launch_k(expand_kernel, num_sms(), kExThreads, ex_smem, s, mx, mw, p);
   if (e == cudaSuccess) e = launch_k(attend_kernel, num_sms(), kThreads, smem, s, mq, mk, mr, mv, p);
   return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
