@@ -29,8 +29,7 @@ constexpr int kRowAlign = 128;           // sequences start at multiples of this
 constexpr int kBlock = 256;              // query rows of a work item: two tiles of 128
 constexpr int kTile = 128;               // tokens of a tile (and query rows of a tile)
 constexpr int kChunkBytes = kTile * kBK * 2;   // 16 KB: 128 rows x 64 entries
-constexpr int kRing = 8;                 // chunks of keys and values in flight
-constexpr int kThreads = 320;            // producer, MMA issuer, 2 x 4 softmax warps
+constexpr int kThreads = 384;            // warps 0..3: producer, MMA issuer, two idle; 4..7 and 8..11: softmax
 constexpr int kTmemCols = 512;
 constexpr float kGrow = 8.0f;            // log2 of the growth of a row's maximum that forces a rescaling
 
@@ -413,7 +412,7 @@ __device__ inline void tc_mma_ta_warp(uint32_t d_tmem, uint32_t a_tmem, uint64_t
 // fp32 accumulation, f16 operands, A and B K-major
 __host__ __device__ constexpr uint32_t idesc_f16(int M, int N) { return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24); }
 struct Shared {
-  uint64_t full[kRing], empty[kRing];            // chunks of keys and values
+  uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
   uint64_t q_full[2], q_ready[2], q_empty[2];    // a query tile: loaded, turned to f16, no longer read
   uint64_t s_full[2], p_ready[2], o_full[2];
   uint64_t w_full[2], w_empty[2];                // work items
@@ -421,6 +420,15 @@ struct Shared {
   int item[2];
   uint32_t tmem;
   int abort;
+};
+
+// Shared memory by the head's chunks of 64 entries (KC: key with its rotary part, VC: value): two query tiles, two
+// key tiles, and two value tiles where they fit (one for heads of 128 + rotary).
+template <int KC, int VC>
+struct Attend {
+  static constexpr int kQ = KC * kChunkBytes, kV = VC * kChunkBytes;
+  static constexpr int kStagesV = 4 * kQ + 2 * kV <= 224 * 1024 ? 2 : 1;
+  static constexpr int kSmem = 4 * kQ + kStagesV * kV + 1024;
 };
 
 // A work item: 256 query rows of one head.
@@ -448,23 +456,23 @@ __device__ inline bool get_item(const PrefillParams& p, int k, int n_blocks, int
   return true;
 }
 
+template <int KC, int VC>
 __global__ void __launch_bounds__(kThreads, 1)
 attend_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
               const __grid_constant__ CUtensorMap map_r, const __grid_constant__ CUtensorMap map_v,
               const PrefillParams p) {
+  using A = Attend<KC, VC>;
   extern __shared__ uint8_t smem_raw[];
   __shared__ Shared sh;
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int kc = p.dn / kBK + (p.rope ? 1 : 0), vc = p.dv / kBK;   // chunks of a key and a value tile
-  const int q_bytes = kc * kChunkBytes;                            // a query tile
 
   if (tid == 0) {
-    for (int i = 0; i < kRing; ++i) {
-      mbar_init(&sh.full[i], 1);
-      mbar_init(&sh.empty[i], 1);
-    }
     for (int g = 0; g < 2; ++g) {
+      mbar_init(&sh.k_full[g], 1);
+      mbar_init(&sh.k_empty[g], 1);
+      mbar_init(&sh.v_full[g], 1);
+      mbar_init(&sh.v_empty[g], 1);
       mbar_init(&sh.q_full[g], 1);
       mbar_init(&sh.q_ready[g], 4);
       mbar_init(&sh.q_empty[g], 1);
@@ -498,174 +506,194 @@ attend_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
   volatile int* abort_flag = &sh.abort;
   const int n_blocks = p.counts[0];
   const int group = n_blocks ? max(1, min(p.heads, (int)gridDim.x / n_blocks)) : 1;
+  const int rope_chunk = p.rope ? 1 : 0, key_chunks = KC - rope_chunk;
   Item it;
-
-  if (warp == 0) {
-    // ------------------------------------------------ work items and TMA
-    const uint32_t smem0 = uni(smem_u32(smem)), ring0 = smem0 + 2 * q_bytes;
-    const uint32_t full0 = uni(smem_u32(&sh.full[0])), qf0 = uni(smem_u32(&sh.q_full[0]));
-    int n = 0, chunk = 0, q_loads[2] = {0, 0};
-    uint32_t par = 1;
-    bool ok = true;
-    // one chunk into the ring
-    auto load = [&](const CUtensorMap* map, int c0, int c1) {
-      if (!ok) return;
-      const int slot = chunk % kRing;
-      ok = warp_wait(&sh.empty[slot], par, abort_flag);
-      if (!ok) return;
-      mbar_expect_tx_warp(full0 + 8 * slot, kChunkBytes);
-      tma_load_2d_warp(ring0 + slot * kChunkBytes, map, full0 + 8 * slot, c0, c1);
-      if (++chunk % kRing == 0) par ^= 1u;
-    };
-    for (;;) {
-      ok = warp_wait(&sh.w_empty[n & 1], ((n >> 1) & 1) ^ 1u, abort_flag);
-      if (!ok) break;
-      int k = 0;
-      if (lane == 0) {
-        k = atomicAdd(&p.counts[1], 1);
-        sh.item[n & 1] = k;
-        mbar_arrive(&sh.w_full[n & 1]);
-      }
-      k = (int)uni(k);
-      ++n;
-      if (!__any_sync(0xffffffffu, get_item(p, k, n_blocks, group, it))) break;
-      const int row0 = (int)uni(it.row0), head = (int)uni(it.head), base = (int)uni(it.base);
-      const int t[2] = {(int)uni(it.tiles[0]), (int)uni(it.tiles[1])}, tiles = max(t[0], t[1]);
-      for (int g = 0; g < 2 && ok; ++g) {
-        if (!t[g]) continue;
-        ok = warp_wait(&sh.q_empty[g], (q_loads[g] & 1) ^ 1u, abort_flag);
-        if (!ok) break;
-        ++q_loads[g];
-        mbar_expect_tx_warp(qf0 + 8 * g, (uint32_t)q_bytes);
-        for (int c = 0; c < kc; ++c)
-          tma_load_2d_warp(smem0 + g * q_bytes + c * kChunkBytes, &map_q, qf0 + 8 * g, head * (p.dn + p.rope) + c * kBK,
+  // A softmax thread holds a row of 128 scores: the first four warps give registers to the other eight
+  // (128 threads x (120 + 192 + 192) = 384 x 168, what the launch has).
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 120;");
+    if (warp == 0) {
+      // ---------------------------------------------- work items and TMA
+      const uint32_t smem0 = uni(smem_u32(smem)), k0 = smem0 + 2 * A::kQ, v0 = k0 + 2 * A::kQ;
+      const uint32_t kf = uni(smem_u32(&sh.k_full[0])), vf = uni(smem_u32(&sh.v_full[0]));
+      const uint32_t qf = uni(smem_u32(&sh.q_full[0]));
+      int n = 0, k_loads = 0, v_loads = 0, q_loads0 = 0, q_loads1 = 0;
+      bool ok = true;
+      auto load_k = [&](int head, int row) {
+        const int st = k_loads & 1;
+        ok = warp_wait(&sh.k_empty[st], ((k_loads >> 1) & 1) ^ 1u, abort_flag);
+        if (!ok) return;
+        ++k_loads;
+        mbar_expect_tx_warp(kf + 8 * st, A::kQ);
+#pragma unroll
+        for (int c = 0; c < KC; ++c) {
+          if (c < key_chunks)
+            tma_load_2d_warp(k0 + st * A::kQ + c * kChunkBytes, &map_k, kf + 8 * st, c * kBK, head * p.kv_rows + row);
+          else
+            tma_load_2d_warp(k0 + st * A::kQ + c * kChunkBytes, &map_r, kf + 8 * st, 0, row);
+        }
+      };
+      auto load_q = [&](int g, int& loads, int head, int row0) {
+        ok = warp_wait(&sh.q_empty[g], (loads & 1) ^ 1u, abort_flag);
+        if (!ok) return;
+        ++loads;
+        mbar_expect_tx_warp(qf + 8 * g, A::kQ);
+#pragma unroll
+        for (int c = 0; c < KC; ++c)
+          tma_load_2d_warp(smem0 + g * A::kQ + c * kChunkBytes, &map_q, qf + 8 * g, head * (p.dn + p.rope) + c * kBK,
                            row0 + g * kTile);
-        if (g == 0) {   // the first keys beside the queries
-          for (int c = 0; c < p.dn / kBK; ++c) load(&map_k, c * kBK, head * p.kv_rows + base);
-          if (p.rope) load(&map_r, 0, base);
-        }
-      }
-      for (int i = 0; i < tiles && ok; ++i) {
-        const int at = base + i * kTile;
-        for (int c = 0; c < vc; ++c) load(&map_v, c * kBK, head * p.kv_rows + at);
-        if (i + 1 < tiles) {
-          for (int c = 0; c < p.dn / kBK; ++c) load(&map_k, c * kBK, head * p.kv_rows + at + kTile);
-          if (p.rope) load(&map_r, 0, at + kTile);
-        }
-      }
-      if (!ok) break;
-    }
-    // drain: whatever was asked for lands before the CTA can exit
-    volatile int no_abort = 0;
-    for (int g = 0; g < 2; ++g)
-      if (q_loads[g]) mbar_wait(&sh.q_full[g], (q_loads[g] - 1) & 1, &no_abort);
-    for (int s = 0; s < kRing; ++s) {
-      const int loads = chunk / kRing + (chunk % kRing > s ? 1 : 0);
-      if (loads > 0) mbar_wait(&sh.full[s], (loads - 1) & 1, &no_abort);
-    }
-    __syncwarp();
-  } else if (warp == 1) {
-    // ------------------------------------------------ MMA issuer
-    // Order for tiles a, b: S_a(0) S_b(0) | PV_a(i) S_a(i+1) PV_b(i) S_b(i+1): while one tile's softmax runs, the
-    // other tile's products do.  P lies in its S's columns, so S_a(i+1) follows PV_a(i).
-    const uint32_t tm = uni(tmem), smem0 = uni(smem_u32(smem)), ring0 = smem0 + 2 * q_bytes;
-    const uint64_t dq0 = smem_desc(smem0), dk0 = smem_desc(ring0), dv0 = smem_desc_mn(ring0, kChunkBytes);
-    constexpr uint32_t idesc_s = idesc_f16(128, kTile);
-    int n = 0, q_uses[2] = {0, 0}, s_done[2] = {0, 0};
-    int front = 0;                    // ring position of the oldest chunk still needed
-    bool issued = false, ok = true;
-    auto wait_chunks = [&](int at, int count) {
-      for (int c = 0; c < count && ok; ++c) ok = warp_wait(&sh.full[(at + c) % kRing], ((at + c) / kRing) & 1, abort_flag);
-      tc_fence_after();
-    };
-    auto free_chunks = [&](int at, int count) {
-      for (int c = 0; c < count; ++c) tc_commit_warp(&sh.empty[(at + c) % kRing]);
-    };
-    auto issue_s = [&](int g, int at) {
-      const uint64_t dq = dq0 + ((uint64_t)(g * q_bytes) >> 4);
-      for (int c = 0; c < kc; ++c) {
-        const uint64_t a = dq + ((uint64_t)(c * kChunkBytes) >> 4);
-        const uint64_t b = dk0 + ((uint64_t)(((at + c) % kRing) * kChunkBytes) >> 4);
-        const int steps = c < p.dn / kBK ? 4 : p.rope / kUK;
-#pragma unroll
-        for (int s = 0; s < 4; ++s)
-          if (s < steps) tc_mma_warp(tm + g * kTile, a + ((s * kUK * 2) >> 4), b + ((s * kUK * 2) >> 4), idesc_s, (c | s) ? 1u : 0u);
-      }
-      tc_commit_warp(&sh.s_full[g]);
-      issued = true;
-    };
-    auto issue_pv = [&](int g, int at, bool first) {
-      // a value tile's chunks follow one another in the ring, but may wrap around its end: 64 columns at a time
-      for (int c = 0; c < vc; ++c) {
-        const uint64_t b = dv0 + ((uint64_t)(((at + c) % kRing) * kChunkBytes) >> 4);
-#pragma unroll
-        for (int s = 0; s < kTile / kUK; ++s)
-          tc_mma_ta_warp(tm + 256 + g * kTile + c * kBK, tm + g * kTile + s * 8, b + ((s * kUK * 128) >> 4),
-                         idesc_f16(128, kBK) | kTransB, first && s == 0 ? 0u : 1u);
-      }
-    };
-    for (;;) {
-      ok = warp_wait(&sh.w_full[n & 1], (n >> 1) & 1, abort_flag);
-      if (!ok) break;
-      const int k = (int)uni(sh.item[n & 1]);
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sh.w_empty[n & 1]);
-      ++n;
-      if (!__any_sync(0xffffffffu, get_item(p, k, n_blocks, group, it))) break;
-      const int t[2] = {(int)uni(it.tiles[0]), (int)uni(it.tiles[1])}, tiles = max(t[0], t[1]);
-      wait_chunks(front, kc);
-      for (int g = 0; g < 2 && ok; ++g) {
-        if (!t[g]) continue;
-        ok = warp_wait(&sh.q_ready[g], q_uses[g]++ & 1, abort_flag);
+      };
+      for (;;) {
+        ok = warp_wait(&sh.w_empty[n & 1], ((n >> 1) & 1) ^ 1u, abort_flag);
         if (!ok) break;
-        tc_fence_after();
-        issue_s(g, front);
-        if (t[g] == 1) tc_commit_warp(&sh.q_empty[g]);
-      }
-      if (!ok) break;
-      free_chunks(front, kc);
-      front += kc;
-      for (int i = 0; i < tiles && ok; ++i) {
-        const int v_at = front, k_at = front + vc;
-        wait_chunks(v_at, vc);
-        bool have_k = false;
-        for (int g = 0; g < 2 && ok; ++g) {
-          if (i >= t[g]) continue;
-          ok = warp_wait(&sh.p_ready[g], s_done[g]++ & 1, abort_flag);
+        int k = 0;
+        if (lane == 0) {
+          k = atomicAdd(&p.counts[1], 1);
+          sh.item[n & 1] = k;
+          mbar_arrive(&sh.w_full[n & 1]);
+        }
+        k = (int)uni(k);
+        ++n;
+        if (!__any_sync(0xffffffffu, get_item(p, k, n_blocks, group, it))) break;
+        const int row0 = (int)uni(it.row0), head = (int)uni(it.head), base = (int)uni(it.base);
+        const int ta = (int)uni(it.tiles[0]), tb = (int)uni(it.tiles[1]), tiles = max(ta, tb);
+        load_q(0, q_loads0, head, row0);
+        if (ok) load_k(head, base);
+        if (ok && tb) load_q(1, q_loads1, head, row0);
+        for (int i = 0; i < tiles && ok; ++i) {
+          if (i + 1 < tiles) load_k(head, base + (i + 1) * kTile);
           if (!ok) break;
+          const int st = v_loads % A::kStagesV;
+          ok = warp_wait(&sh.v_empty[st], ((v_loads / A::kStagesV) & 1) ^ 1u, abort_flag);
+          if (!ok) break;
+          ++v_loads;
+          mbar_expect_tx_warp(vf + 8 * st, A::kV);
+#pragma unroll
+          for (int c = 0; c < VC; ++c)
+            tma_load_2d_warp(v0 + st * A::kV + c * kChunkBytes, &map_v, vf + 8 * st, c * kBK,
+                             head * p.kv_rows + base + i * kTile);
+        }
+        if (!ok) break;
+      }
+      // drain: whatever was asked for lands before the CTA can exit
+      volatile int no_abort = 0;
+      if (q_loads0) mbar_wait(&sh.q_full[0], (q_loads0 - 1) & 1, &no_abort);
+      if (q_loads1) mbar_wait(&sh.q_full[1], (q_loads1 - 1) & 1, &no_abort);
+      for (int st = 0; st < 2; ++st) {
+        const int nk = (k_loads + 1 - st) / 2;
+        if (nk > 0) mbar_wait(&sh.k_full[st], (nk - 1) & 1, &no_abort);
+        const int nv = A::kStagesV == 2 ? (v_loads + 1 - st) / 2 : (st == 0 ? v_loads : 0);
+        if (nv > 0) mbar_wait(&sh.v_full[st], (nv - 1) & 1, &no_abort);
+      }
+      __syncwarp();
+    } else if (warp == 1) {
+      // ---------------------------------------------- MMA issuer
+      // Order for tiles a, b: S_a(0) S_b(0) | PV_a(i) S_a(i+1) PV_b(i) S_b(i+1): while one tile's softmax runs, the
+      // other tile's products do.  P lies in its S's columns, so S_a(i+1) follows PV_a(i).
+      const uint32_t tm = uni(tmem), smem0 = uni(smem_u32(smem));
+      const uint64_t dq0 = smem_desc(smem0), dk0 = smem_desc(smem0 + 2 * A::kQ);
+      const uint64_t dv0 = smem_desc_mn(smem0 + 4 * A::kQ, kChunkBytes);
+      constexpr uint32_t idesc_s = idesc_f16(128, kTile), idesc_v = idesc_f16(128, VC * kBK) | kTransB;
+      const int rope_steps = (int)uni(p.rope / kUK);
+      int n = 0, k_uses = 0, v_uses = 0, q_uses0 = 0, q_uses1 = 0, p_uses0 = 0, p_uses1 = 0;
+      bool issued = false, ok = true;
+      auto issue_s = [&](int g, int st) {
+        const uint64_t dq = dq0 + (uint64_t)((g * A::kQ) >> 4), dk = dk0 + (uint64_t)((st * A::kQ) >> 4);
+#pragma unroll
+        for (int c = 0; c < KC; ++c) {
+          const int steps = c < key_chunks ? 4 : rope_steps;
+#pragma unroll
+          for (int x = 0; x < 4; ++x)
+            if (x < steps)
+              tc_mma_warp(tm + g * kTile, dq + ((c * kChunkBytes + x * kUK * 2) >> 4),
+                          dk + ((c * kChunkBytes + x * kUK * 2) >> 4), idesc_s, (c | x) ? 1u : 0u);
+        }
+        tc_commit_warp(&sh.s_full[g]);
+        issued = true;
+      };
+      auto issue_pv = [&](int g, int st, uint32_t acc) {
+        const uint64_t dv = dv0 + (uint64_t)((st * A::kV) >> 4);
+#pragma unroll
+        for (int x = 0; x < kTile / kUK; ++x)
+          tc_mma_ta_warp(tm + 256 + g * kTile, tm + g * kTile + x * 8, dv + ((x * kUK * 128) >> 4), idesc_v, x ? 1u : acc);
+      };
+      for (;;) {
+        ok = warp_wait(&sh.w_full[n & 1], (n >> 1) & 1, abort_flag);
+        if (!ok) break;
+        const int k = (int)uni(sh.item[n & 1]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.w_empty[n & 1]);
+        ++n;
+        if (!__any_sync(0xffffffffu, get_item(p, k, n_blocks, group, it))) break;
+        const int ta = (int)uni(it.tiles[0]), tb = (int)uni(it.tiles[1]), tiles = max(ta, tb);
+        ok = warp_wait(&sh.k_full[k_uses & 1], (k_uses >> 1) & 1, abort_flag) &&
+             warp_wait(&sh.q_ready[0], q_uses0 & 1, abort_flag);
+        if (!ok) break;
+        ++q_uses0;
+        tc_fence_after();
+        issue_s(0, k_uses & 1);
+        if (ta == 1) tc_commit_warp(&sh.q_empty[0]);
+        if (tb) {
+          ok = warp_wait(&sh.q_ready[1], q_uses1 & 1, abort_flag);
+          if (!ok) break;
+          ++q_uses1;
           tc_fence_after();
-          issue_pv(g, v_at, i == 0);
-          if (i + 1 == t[g]) tc_commit_warp(&sh.o_full[g]);
-          if (i + 1 < t[g]) {
-            if (!have_k) wait_chunks(k_at, kc);
-            if (!ok) break;
+          issue_s(1, k_uses & 1);
+          if (tb == 1) tc_commit_warp(&sh.q_empty[1]);
+        }
+        tc_commit_warp(&sh.k_empty[k_uses & 1]);
+        ++k_uses;
+        for (int i = 0; i < tiles; ++i) {
+          const int vs = v_uses % A::kStagesV, ks = k_uses & 1;
+          const uint32_t acc = i ? 1u : 0u;
+          bool have_v = false, have_k = false;
+          // both tiles of the step; a tile that sees fewer tokens ends earlier
+          auto tile_step = [&](int g, int t, int& p_uses) {
+            if (i >= t || !ok) return;
+            ok = warp_wait(&sh.p_ready[g], p_uses & 1, abort_flag);
+            ++p_uses;
+            if (ok && !have_v) ok = warp_wait(&sh.v_full[vs], (v_uses / A::kStagesV) & 1, abort_flag);
+            if (!ok) return;
+            have_v = true;
+            tc_fence_after();
+            issue_pv(g, vs, acc);
+            if (i + 1 == t) {
+              tc_commit_warp(&sh.o_full[g]);
+              return;
+            }
+            if (!have_k) ok = warp_wait(&sh.k_full[ks], (k_uses >> 1) & 1, abort_flag);
+            if (!ok) return;
             have_k = true;
-            issue_s(g, k_at);
-            if (i + 2 == t[g]) tc_commit_warp(&sh.q_empty[g]);
+            tc_fence_after();
+            issue_s(g, ks);
+            if (i + 2 == t) tc_commit_warp(&sh.q_empty[g]);
+          };
+          tile_step(0, ta, p_uses0);
+          tile_step(1, tb, p_uses1);
+          if (!ok) break;
+          tc_commit_warp(&sh.v_empty[vs]);
+          ++v_uses;
+          if (i + 1 < tiles) {
+            tc_commit_warp(&sh.k_empty[ks]);
+            ++k_uses;
           }
         }
         if (!ok) break;
-        free_chunks(v_at, vc);
-        front += vc;
-        if (i + 1 < tiles) {
-          free_chunks(k_at, kc);
-          front += kc;
-        }
       }
-      if (!ok) break;
+      if (issued) {   // every issued product completes before tensor memory is released
+        volatile int no_abort = 0;
+        tc_commit_warp(&sh.drain);
+        mbar_wait(&sh.drain, 0, &no_abort);
+      }
+      __syncwarp();
     }
-    if (issued) {   // every issued product completes before tensor memory is released
-      volatile int no_abort = 0;
-      tc_commit_warp(&sh.drain);
-      mbar_wait(&sh.drain, 0, &no_abort);
-    }
-    __syncwarp();
   } else {
-    // ------------------------------------------------ softmax: tile g = 0 in warps 2..5, 1 in warps 6..9; a thread owns a row
-    const int g = (warp - 2) >> 2, quarter = warp & 3, r = quarter * 32 + lane;
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
+    // ------------------------------------------------ softmax: tile g = 0 in warps 4..7, 1 in warps 8..11; a thread owns a row
+    const int g = (warp - 4) >> 2, quarter = warp & 3, r = quarter * 32 + lane;
     const uint32_t lane_base = tmem + ((uint32_t)(quarter * 32) << 16);
     const uint32_t s_col = lane_base + g * kTile, o_col = lane_base + 256 + g * kTile;
-    uint8_t* qrow = smem + g * q_bytes + r * 128;
+    uint8_t* qrow = smem + g * A::kQ + r * 128;
     const int dim = p.dn + p.rope;
     int n = 0, uses = 0, steps = 0;
     bool ok = true;
@@ -677,13 +705,14 @@ attend_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
       if (lane == 0) mbar_arrive(&sh.w_empty[n & 1]);
       ++n;
       if (!__any_sync(0xffffffffu, get_item(p, k, n_blocks, group, it))) break;
-      const int tiles = it.tiles[g];
+      const int tiles = g ? it.tiles[1] : it.tiles[0];
       if (!tiles) continue;
       // the query row in f16, scaled by a power of two so that its largest entry lies in [1, 2)
       ok = warp_wait(&sh.q_full[g], uses & 1, abort_flag);
       if (!ok) break;
       float big = 0.0f;
-      for (int c = 0; c < kc; ++c)
+#pragma unroll
+      for (int c = 0; c < KC; ++c)
 #pragma unroll
         for (int x = 0; x < 8; ++x) {
           if (c * kBK + 8 * x >= dim) break;
@@ -696,7 +725,8 @@ attend_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
       const uint32_t ebits = __float_as_uint(big) & 0x7F800000u;
       const bool plain = ebits == 0 || ebits == 0x7F800000u || ebits == 0x7F000000u;
       const float pow2 = plain ? 1.0f : __uint_as_float(ebits), inv = plain ? 1.0f : __uint_as_float(0x7F000000u - ebits);
-      for (int c = 0; c < kc; ++c)
+#pragma unroll
+      for (int c = 0; c < KC; ++c)
 #pragma unroll
         for (int x = 0; x < 8; ++x) {
           uint4* at = reinterpret_cast<uint4*>(qrow + c * kChunkBytes + ((x ^ (r & 7)) << 4));
@@ -715,35 +745,36 @@ attend_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
       ++uses;
       const float scale = p.scale_log2 * pow2;
       const bool neg = scale < 0.0f;
+      const float unseen = neg ? INFINITY : -INFINITY;   // what a token out of sight scores
       const int in_block = g * kTile + r, limit = it.limit0 + in_block;
       float m = -INFINITY, l = 0.0f;
       for (int i = 0; i < tiles; ++i, ++steps) {
         ok = warp_wait(&sh.s_full[g], steps & 1, abort_flag);
         if (!ok) break;
         tc_fence_after();
-        // Two passes over the row of S, 32 columns at a time, the next ones read behind the work on these: the whole
-        // row would take 128 registers.  P's columns overwrite S's, always behind the reads.
+        float s[kTile];
+        uint32_t(&u)[kTile] = reinterpret_cast<uint32_t(&)[kTile]>(s);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld32(s_col + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(&u[32 * c]));
+        tmem_ld_wait();
         const int see = limit - i * kTile;
-        const bool all = __all_sync(0xffffffffu, see >= kTile);
-        float top = neg ? INFINITY : -INFINITY;
-        uint32_t u[2][32];
-        tmem_ld32(s_col, u[0]);
+        if (!__all_sync(0xffffffffu, see >= kTile)) {   // on the diagonal and past the end: out of sight
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          tmem_ld_wait();
-          tmem_ld32(s_col + 32 * ((c + 1) & 3), u[(c + 1) & 1]);
-          if (neg) {
-#pragma unroll
-            for (int j = 0; j < 32; ++j)
-              if (all || 32 * c + j < see) top = fminf(top, __uint_as_float(u[c & 1][j]));
-          } else if (all) {
-#pragma unroll
-            for (int j = 0; j < 32; ++j) top = fmaxf(top, __uint_as_float(u[c & 1][j]));
-          } else {
-#pragma unroll
-            for (int j = 0; j < 32; ++j) top = fmaxf(top, 32 * c + j < see ? __uint_as_float(u[c & 1][j]) : -INFINITY);
-          }
+          for (int j = 0; j < kTile; ++j)
+            if (j >= see) s[j] = unseen;
         }
+        float t4[4] = {s[0], s[1], s[2], s[3]};
+        if (!neg) {
+#pragma unroll
+          for (int j = 4; j < kTile; j += 8)
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+              t4[x] = j + 4 + x < kTile ? fmaxf(t4[x], fmaxf(s[j + x], s[j + 4 + x])) : fmaxf(t4[x], s[j + x]);
+        } else {
+#pragma unroll
+          for (int j = 4; j < kTile; ++j) t4[j & 3] = fminf(t4[j & 3], s[j]);
+        }
+        float top = neg ? fminf(fminf(t4[0], t4[1]), fminf(t4[2], t4[3])) : fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
         top = see > 0 ? top * scale : -INFINITY;
         bool grow = false;
         float f = 1.0f;
@@ -761,19 +792,13 @@ attend_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
         float2 sum0 = make_float2(0.0f, 0.0f), sum1 = sum0;
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          tmem_ld_wait();
-          if (c < 3) tmem_ld32(s_col + 32 * (c + 1), u[(c + 1) & 1]);
           uint32_t pk[16];
 #pragma unroll
           for (int j = 0; j < 16; ++j) {
-            float2 x = fma2(make_float2(__uint_as_float(u[c & 1][2 * j]), __uint_as_float(u[c & 1][2 * j + 1])),
-                            make_float2(scale, scale), make_float2(-ref, -ref));
+            float2 x = fma2(make_float2(s[32 * c + 2 * j], s[32 * c + 2 * j + 1]), make_float2(scale, scale),
+                            make_float2(-ref, -ref));
             x.x = ex2(x.x);
             x.y = ex2(x.y);
-            if (!all) {
-              x.x = 32 * c + 2 * j < see ? x.x : 0.0f;
-              x.y = 32 * c + 2 * j + 1 < see ? x.y : 0.0f;
-            }
             if (j & 1) sum1 = add2(sum1, x);
             else sum0 = add2(sum0, x);
             const __half2 h = __floats2half2_rn(x.x, x.y);
@@ -864,6 +889,18 @@ PrefillWs prefill_ws(int B, int T, int heads, int dn, int dv, int rope, int kv_t
   return w;
 }
 
+template <int KC, int VC>
+cudaError_t launch_attend(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mr, const CUtensorMap& mv,
+                          const PrefillParams& p, cudaStream_t s) {
+  using A = Attend<KC, VC>;
+  static_assert(A::kSmem + sizeof(Shared) <= 227 * 1024, "shared memory");
+  static std::atomic<unsigned char> attr[kMaxDevices];
+  const cudaError_t e = once_per_device(attr, [] {
+    return cudaFuncSetAttribute(attend_kernel<KC, VC>, cudaFuncAttributeMaxDynamicSharedMemorySize, A::kSmem);
+  });
+  return e == cudaSuccess ? launch_k(attend_kernel<KC, VC>, num_sms(), kThreads, A::kSmem, s, mq, mk, mr, mv, p) : e;
+}
+
 // f16 bits move like bf16 bits: the maps' element type only has to be 16 bits wide
 int launch_prefill(const PrefillParams& p, cudaStream_t s) {
   CUtensorMap mq, mk, mr, mv, mx, mw;
@@ -874,21 +911,24 @@ int launch_prefill(const PrefillParams& p, cudaStream_t s) {
       !make_map(&mv, p.v, p.dv, rows, kTile) || !make_map(&mx, p.kv.pages, p.kv.row, cache_rows, p.kv.page_tokens) ||
       !make_map(&mw, p.w, p.kv.rank, (uint64_t)p.heads * (p.dn + p.dv), p.dn + p.dv))
     return MOE_ERR_CUDA;
-  const int smem = 2 * (p.dn / kBK + (p.rope ? 1 : 0)) * kChunkBytes + kRing * kChunkBytes + 1024;
-  static_assert(2 * 3 * kChunkBytes + kRing * kChunkBytes + 1024 + sizeof(Shared) <= 227 * 1024, "shared memory");
   const int ex_smem = p.kv.rank / kBK * kChunkBytes + kExStages * kExStage + 1024;
   constexpr int kExSmem = kMaxChunks * kChunkBytes + kExStages * kExStage + 1024;
   static_assert(kExSmem + sizeof(ExShared) <= 227 * 1024, "shared memory");
   static std::atomic<unsigned char> attr[kMaxDevices];
   cudaError_t e = once_per_device(attr, [] {
-    const cudaError_t x = cudaFuncSetAttribute(expand_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kExSmem);
-    if (x != cudaSuccess) return x;
-    return cudaFuncSetAttribute(attend_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                2 * 3 * kChunkBytes + kRing * kChunkBytes + 1024);
+    return cudaFuncSetAttribute(expand_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kExSmem);
   });
   if (e == cudaSuccess) e = launch_k(plan_kernel, 1, kPlanThreads, 0, s, p);
   if (e == cudaSuccess) e = launch_k(expand_kernel, num_sms(), kExThreads, ex_smem, s, mx, mw, p);
-  if (e == cudaSuccess) e = launch_k(attend_kernel, num_sms(), kThreads, smem, s, mq, mk, mr, mv, p);
+  if (e == cudaSuccess) {
+    const int kc = p.dn / kBK + (p.rope ? 1 : 0), vc = p.dv / kBK;
+    e = vc == 2 ? (kc == 3   ? launch_attend<3, 2>(mq, mk, mr, mv, p, s)
+                   : kc == 2 ? launch_attend<2, 2>(mq, mk, mr, mv, p, s)
+                             : launch_attend<1, 2>(mq, mk, mr, mv, p, s))
+                : (kc == 3   ? launch_attend<3, 1>(mq, mk, mr, mv, p, s)
+                   : kc == 2 ? launch_attend<2, 1>(mq, mk, mr, mv, p, s)
+                             : launch_attend<1, 1>(mq, mk, mr, mv, p, s));
+  }
   return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
@@ -934,7 +974,8 @@ int moe_latent_prefill(const moe_kv_cache* cache, int layer, const void* q, cons
   p.rope = cache->rope;
   p.kv_rows = w.rows;
   p.max_blocks_q = w.n_blocks;
-  p.scale_log2 = scale * 1.4426950408889634f;
+  // zero as a tiny number: a token out of sight scores -infinity, and 0 * -infinity is NaN
+  p.scale_log2 = scale == 0.0f ? 1e-20f : scale * 1.4426950408889634f;
   p.q = reinterpret_cast<const __nv_bfloat16*>(q);
   p.seqs = seqs;
   p.q_off = q_offsets;
