@@ -30,16 +30,20 @@ constexpr int kBlock = 256;              // query rows of a work item: two tiles
 constexpr int kTile = 128;               // tokens of a tile (and query rows of a tile)
 constexpr int kChunkBytes = kTile * kBK * 2;   // 16 KB: 128 rows x 64 entries
 constexpr int kThreads = 384;            // warps 0..3: producer, MMA issuer, two idle; 4..7 and 8..11: softmax
+constexpr int kMaxSplits = 8;
 constexpr int kTmemCols = 512;
 constexpr float kGrow = 8.0f;            // log2 of the growth of a row's maximum that forces a rescaling
 
 struct QBlock {
-  int b, j0;   // sequence of the batch, first of its query rows
+  int row0, rows;   // first of its query rows in q, and how many
+  int limit0;       // row r sees the tokens below limit0 + r
+  int base;         // first expanded row of its sequence
 };
 
 struct PrefillParams {
   KvView kv;
   int layer, B, T, heads, dn, dv, rope, kv_rows, max_blocks_q;
+  int splits;               // shares of a query block's tokens
   float scale_log2;
   const __nv_bfloat16* q;
   const int32_t* seqs;
@@ -52,6 +56,8 @@ struct PrefillParams {
   __half* k;                // [heads, kv_rows, dn]
   __half* v;                // [heads, kv_rows, dv]
   __half* r;                // [kv_rows, rope]
+  float* part;              // with splits: [splits, heads, T, dv] unnormalised outputs
+  float2* ml;               // [splits, heads, T] their (m, l)
   uint32_t* status;
 };
 
@@ -118,9 +124,11 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PrefillParams 
   int blocks = 0;
   for (int b0 = 0; b0 < p.B; b0 += kPlanThreads) {
     const int b = b0 + threadIdx.x;
-    int v[2] = {0, 0}, total[2], n = 0;
+    int v[2] = {0, 0}, total[2], n = 0, len = 0, q0 = 0;
     if (b < p.B) {
-      const int s = p.seqs[b], len = seq_len(p, b), q0 = p.q_off[b], q1 = p.q_off[b + 1];
+      const int s = p.seqs[b], q1 = p.q_off[b + 1];
+      len = seq_len(p, b);
+      q0 = p.q_off[b];
       const bool good = s >= 0 && s < p.kv.max_seqs && q0 >= 0 && q1 >= q0 && q1 <= p.T && q1 - q0 <= len;
       if (!good) set_status(p.status, MOE_DEV_ERR_BAD_SEQ);
       n = good ? q1 - q0 : 0;
@@ -132,10 +140,11 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PrefillParams 
     scan2(v, total, sh);
     if (b < p.B) {
       const long long at = rows + (long long)v[0] * kRowAlign;
-      p.base[b] = at < p.kv_rows ? (int)at : p.kv_rows;
+      const int base = at < p.kv_rows ? (int)at : p.kv_rows;
+      p.base[b] = base;
       for (int i = 0; i < mine; ++i) {
-        const int x = blocks + v[1] + mine - 1 - i;
-        if (x < p.max_blocks_q) p.blocks[x] = QBlock{b, i * kBlock};
+        const int x = blocks + v[1] + mine - 1 - i, j0 = i * kBlock;
+        if (x < p.max_blocks_q) p.blocks[x] = QBlock{q0 + j0, min(kBlock, n - j0), len - n + j0 + 1, base};
       }
     }
     rows += (long long)total[0] * kRowAlign;
@@ -391,15 +400,6 @@ expand_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
 }
 
 // ---------------------------------------------------------------- attention
-__device__ inline void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};"
-      ::"r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
-        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
-        "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]),
-        "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(taddr));
-}
 // Product with the A operand in tensor memory (16-bit entries, two to a column), one elected lane of a warp issuing.
 __device__ inline void tc_mma_ta_warp(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc, uint32_t accum) {
   asm volatile(
@@ -414,7 +414,7 @@ __host__ __device__ constexpr uint32_t idesc_f16(int M, int N) { return (1u << 4
 struct Shared {
   uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
   uint64_t q_full[2], q_ready[2], q_empty[2];    // a query tile: loaded, turned to f16, no longer read
-  uint64_t s_full[2], p_ready[2], o_full[2];
+  uint64_t s_full[2], p_half[2], p_ready[2], o_full[2];   // p_half: the probabilities of the first 64 tokens
   uint64_t w_full[2], w_empty[2];                // work items
   uint64_t drain;
   int item[2];
@@ -431,27 +431,33 @@ struct Attend {
   static constexpr int kSmem = 4 * kQ + kStagesV * kV + 1024;
 };
 
-// A work item: 256 query rows of one head.
+// A work item: 256 query rows of one head against one of p.splits shares of their tokens.
 struct Item {
-  int head, row0, rows, limit0, base, tiles[2];   // row r sees tokens below limit0 + r
+  int head, row0, rows, limit0, base, block, split;
+  int first, tiles[2];   // its first tile of tokens, and how many each query tile takes
 };
 
 __device__ inline bool get_item(const PrefillParams& p, int k, int n_blocks, int group, Item& it) {
-  if (k >= n_blocks * p.heads) return false;
+  if (k >= n_blocks * p.heads * p.splits) return false;
   // heads in groups that fill the grid once, so that a group's keys and values are read while they are in L2
-  const int per = n_blocks * group, gi = k / per, in = k - gi * per;
+  const int units = n_blocks * p.splits, per = units * group, gi = k / per, in = k - gi * per;
   const int gh = min(group, p.heads - gi * group), x = in / gh;
   it.head = gi * group + (in - x * gh);
-  const QBlock qb = p.blocks[x];
-  const int q0 = p.q_off[qb.b], n = p.q_off[qb.b + 1] - q0, len = seq_len(p, qb.b);
-  it.row0 = q0 + qb.j0;
-  it.rows = min(kBlock, n - qb.j0);
-  it.limit0 = len - n + qb.j0 + 1;
-  it.base = p.base[qb.b];
+  it.block = x / p.splits;
+  it.split = x - it.block * p.splits;
+  const int4 qb = __ldg(reinterpret_cast<const int4*>(p.blocks + it.block));
+  it.row0 = qb.x;
+  it.rows = qb.y;
+  it.limit0 = qb.z;
+  it.base = qb.w;
+  const int all = (it.limit0 + it.rows - 1 + kTile - 1) / kTile;   // the last row sees the most
+  const int from = (int)((long long)all * it.split / p.splits), to = (int)((long long)all * (it.split + 1) / p.splits);
+  it.first = from;
 #pragma unroll
   for (int g = 0; g < 2; ++g) {
-    const int last = min(it.rows, (g + 1) * kTile) - 1;   // the tile's last row sees the most
-    it.tiles[g] = last >= g * kTile ? (it.limit0 + last + kTile - 1) / kTile : 0;
+    const int last = min(it.rows, (g + 1) * kTile) - 1;
+    const int mine = last >= g * kTile ? (it.limit0 + last + kTile - 1) / kTile : 0;
+    it.tiles[g] = max(0, min(mine, to) - from);
   }
   return true;
 }
@@ -477,6 +483,7 @@ attend_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
       mbar_init(&sh.q_ready[g], 4);
       mbar_init(&sh.q_empty[g], 1);
       mbar_init(&sh.s_full[g], 1);
+      mbar_init(&sh.p_half[g], 4);
       mbar_init(&sh.p_ready[g], 4);
       mbar_init(&sh.o_full[g], 1);
       mbar_init(&sh.w_full[g], 1);
@@ -505,13 +512,13 @@ attend_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
   const uint32_t tmem = sh.tmem;
   volatile int* abort_flag = &sh.abort;
   const int n_blocks = p.counts[0];
-  const int group = n_blocks ? max(1, min(p.heads, (int)gridDim.x / n_blocks)) : 1;
+  const int group = n_blocks ? max(1, min(p.heads, (int)gridDim.x / (n_blocks * p.splits))) : 1;
   const int rope_chunk = p.rope ? 1 : 0, key_chunks = KC - rope_chunk;
   Item it;
   // A softmax thread holds a row of 128 scores: the first four warps give registers to the other eight
-  // (128 threads x (120 + 192 + 192) = 384 x 168, what the launch has).
+  // (128 threads x (104 + 200 + 200) = 384 x 168, what the launch has).
   if (warp < 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 120;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
     if (warp == 0) {
       // ---------------------------------------------- work items and TMA
       const uint32_t smem0 = uni(smem_u32(smem)), k0 = smem0 + 2 * A::kQ, v0 = k0 + 2 * A::kQ;
@@ -555,10 +562,10 @@ attend_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
         k = (int)uni(k);
         ++n;
         if (!__any_sync(0xffffffffu, get_item(p, k, n_blocks, group, it))) break;
-        const int row0 = (int)uni(it.row0), head = (int)uni(it.head), base = (int)uni(it.base);
+        const int row0 = (int)uni(it.row0), head = (int)uni(it.head), base = (int)uni(it.base + it.first * kTile);
         const int ta = (int)uni(it.tiles[0]), tb = (int)uni(it.tiles[1]), tiles = max(ta, tb);
-        load_q(0, q_loads0, head, row0);
-        if (ok) load_k(head, base);
+        if (ta) load_q(0, q_loads0, head, row0);
+        if (ok && tiles) load_k(head, base);
         if (ok && tb) load_q(1, q_loads1, head, row0);
         for (int i = 0; i < tiles && ok; ++i) {
           if (i + 1 < tiles) load_k(head, base + (i + 1) * kTile);
@@ -611,11 +618,14 @@ attend_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
         tc_commit_warp(&sh.s_full[g]);
         issued = true;
       };
-      auto issue_pv = [&](int g, int st, uint32_t acc) {
+      // half of a value product: 64 tokens
+      auto issue_pv = [&](int g, int st, int half, uint32_t acc) {
         const uint64_t dv = dv0 + (uint64_t)((st * A::kV) >> 4);
 #pragma unroll
-        for (int x = 0; x < kTile / kUK; ++x)
+        for (int y = 0; y < 4; ++y) {
+          const int x = 4 * half + y;
           tc_mma_ta_warp(tm + 256 + g * kTile, tm + g * kTile + x * 8, dv + ((x * kUK * 128) >> 4), idesc_v, x ? 1u : acc);
+        }
       };
       for (;;) {
         ok = warp_wait(&sh.w_full[n & 1], (n >> 1) & 1, abort_flag);
@@ -626,13 +636,17 @@ attend_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
         ++n;
         if (!__any_sync(0xffffffffu, get_item(p, k, n_blocks, group, it))) break;
         const int ta = (int)uni(it.tiles[0]), tb = (int)uni(it.tiles[1]), tiles = max(ta, tb);
-        ok = warp_wait(&sh.k_full[k_uses & 1], (k_uses >> 1) & 1, abort_flag) &&
-             warp_wait(&sh.q_ready[0], q_uses0 & 1, abort_flag);
+        if (!tiles) continue;
+        ok = warp_wait(&sh.k_full[k_uses & 1], (k_uses >> 1) & 1, abort_flag);
         if (!ok) break;
-        ++q_uses0;
-        tc_fence_after();
-        issue_s(0, k_uses & 1);
-        if (ta == 1) tc_commit_warp(&sh.q_empty[0]);
+        if (ta) {
+          ok = warp_wait(&sh.q_ready[0], q_uses0 & 1, abort_flag);
+          if (!ok) break;
+          ++q_uses0;
+          tc_fence_after();
+          issue_s(0, k_uses & 1);
+          if (ta == 1) tc_commit_warp(&sh.q_empty[0]);
+        }
         if (tb) {
           ok = warp_wait(&sh.q_ready[1], q_uses1 & 1, abort_flag);
           if (!ok) break;
@@ -650,13 +664,17 @@ attend_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
           // both tiles of the step; a tile that sees fewer tokens ends earlier
           auto tile_step = [&](int g, int t, int& p_uses) {
             if (i >= t || !ok) return;
-            ok = warp_wait(&sh.p_ready[g], p_uses & 1, abort_flag);
-            ++p_uses;
+            ok = warp_wait(&sh.p_half[g], p_uses & 1, abort_flag);
             if (ok && !have_v) ok = warp_wait(&sh.v_full[vs], (v_uses / A::kStagesV) & 1, abort_flag);
             if (!ok) return;
             have_v = true;
             tc_fence_after();
-            issue_pv(g, vs, acc);
+            issue_pv(g, vs, 0, acc);
+            ok = warp_wait(&sh.p_ready[g], p_uses & 1, abort_flag);
+            if (!ok) return;
+            ++p_uses;
+            tc_fence_after();
+            issue_pv(g, vs, 1, 1u);
             if (i + 1 == t) {
               tc_commit_warp(&sh.o_full[g]);
               return;
@@ -688,7 +706,7 @@ attend_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
       __syncwarp();
     }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
     // ------------------------------------------------ softmax: tile g = 0 in warps 4..7, 1 in warps 8..11; a thread owns a row
     const int g = (warp - 4) >> 2, quarter = warp & 3, r = quarter * 32 + lane;
     const uint32_t lane_base = tmem + ((uint32_t)(quarter * 32) << 16);
@@ -697,56 +715,64 @@ attend_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
     const int dim = p.dn + p.rope;
     int n = 0, uses = 0, steps = 0;
     bool ok = true;
-    for (;;) {
-      ok = warp_wait(&sh.w_full[n & 1], (n >> 1) & 1, abort_flag);
-      if (!ok) break;
-      const int k = sh.item[n & 1];
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sh.w_empty[n & 1]);
-      ++n;
-      if (!__any_sync(0xffffffffu, get_item(p, k, n_blocks, group, it))) break;
-      const int tiles = g ? it.tiles[1] : it.tiles[0];
-      if (!tiles) continue;
-      // the query row in f16, scaled by a power of two so that its largest entry lies in [1, 2)
+    float scale = 0.0f;
+    // The next work item with tokens for this tile, its query row turned to f16 in place, scaled by a power of two so
+    // that its largest entry lies in [1, 2): the power goes into the row's score scale.
+    auto next_item = [&]() {
+      for (;;) {
+        ok = warp_wait(&sh.w_full[n & 1], (n >> 1) & 1, abort_flag);
+        if (!ok) return false;
+        const int k = sh.item[n & 1];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.w_empty[n & 1]);
+        ++n;
+        if (!__any_sync(0xffffffffu, get_item(p, k, n_blocks, group, it))) return false;
+        if (g ? it.tiles[1] : it.tiles[0]) break;
+      }
       ok = warp_wait(&sh.q_full[g], uses & 1, abort_flag);
-      if (!ok) break;
+      if (!ok) return false;
+      ++uses;
       float big = 0.0f;
 #pragma unroll
       for (int c = 0; c < KC; ++c)
 #pragma unroll
         for (int x = 0; x < 8; ++x) {
-          if (c * kBK + 8 * x >= dim) break;
           const uint4 u = *reinterpret_cast<const uint4*>(qrow + c * kChunkBytes + ((x ^ (r & 7)) << 4));
-          const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-          for (int y = 0; y < 4; ++y) big = fmaxf(big, fmaxf(fabsf(bf16_lo(w[y])), fabsf(bf16_hi(w[y]))));
+          if (c * kBK + 8 * x < dim) {
+            const float b0 = fmaxf(fmaxf(fabsf(bf16_lo(u.x)), fabsf(bf16_hi(u.x))), fmaxf(fabsf(bf16_lo(u.y)), fabsf(bf16_hi(u.y))));
+            const float b1 = fmaxf(fmaxf(fabsf(bf16_lo(u.z)), fabsf(bf16_hi(u.z))), fmaxf(fabsf(bf16_lo(u.w)), fabsf(bf16_hi(u.w))));
+            big = fmaxf(big, fmaxf(b0, b1));
+          }
         }
       // 2^e from the exponent bits; zero rows and rows with an infinity stay as they are
       const uint32_t ebits = __float_as_uint(big) & 0x7F800000u;
-      const bool plain = ebits == 0 || ebits == 0x7F800000u || ebits == 0x7F000000u;
+      const bool plain = ebits == 0 || ebits >= 0x7F000000u;
       const float pow2 = plain ? 1.0f : __uint_as_float(ebits), inv = plain ? 1.0f : __uint_as_float(0x7F000000u - ebits);
 #pragma unroll
       for (int c = 0; c < KC; ++c)
 #pragma unroll
         for (int x = 0; x < 8; ++x) {
-          uint4* at = reinterpret_cast<uint4*>(qrow + c * kChunkBytes + ((x ^ (r & 7)) << 4));
-          uint4 u = *at;
-          uint32_t* w = &u.x;
-#pragma unroll
-          for (int y = 0; y < 4; ++y) {
-            const __half2 h = __floats2half2_rn(bf16_lo(w[y]) * inv, bf16_hi(w[y]) * inv);
-            w[y] = *reinterpret_cast<const uint32_t*>(&h);
-          }
-          *at = u;
+          const uint4 u = *reinterpret_cast<const uint4*>(qrow + c * kChunkBytes + ((x ^ (r & 7)) << 4));
+          const __half2 h0 = __floats2half2_rn(bf16_lo(u.x) * inv, bf16_hi(u.x) * inv);
+          const __half2 h1 = __floats2half2_rn(bf16_lo(u.y) * inv, bf16_hi(u.y) * inv);
+          const __half2 h2 = __floats2half2_rn(bf16_lo(u.z) * inv, bf16_hi(u.z) * inv);
+          const __half2 h3 = __floats2half2_rn(bf16_lo(u.w) * inv, bf16_hi(u.w) * inv);
+          *reinterpret_cast<uint4*>(qrow + c * kChunkBytes + ((x ^ (r & 7)) << 4)) =
+              make_uint4(*reinterpret_cast<const uint32_t*>(&h0), *reinterpret_cast<const uint32_t*>(&h1),
+                         *reinterpret_cast<const uint32_t*>(&h2), *reinterpret_cast<const uint32_t*>(&h3));
         }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.q_ready[g]);
-      ++uses;
-      const float scale = p.scale_log2 * pow2;
-      const bool neg = scale < 0.0f;
+      scale = p.scale_log2 * pow2;
+      return true;
+    };
+    bool have = next_item();
+    while (have) {
+      const int tiles = g ? it.tiles[1] : it.tiles[0], first = it.first, in_block = g * kTile + r;
+      const int limit = it.limit0 + in_block - first * kTile;
+      const bool neg = scale < 0.0f, mine = in_block < it.rows;
       const float unseen = neg ? INFINITY : -INFINITY;   // what a token out of sight scores
-      const int in_block = g * kTile + r, limit = it.limit0 + in_block;
       float m = -INFINITY, l = 0.0f;
       for (int i = 0; i < tiles; ++i, ++steps) {
         ok = warp_wait(&sh.s_full[g], steps & 1, abort_flag);
@@ -788,6 +814,17 @@ attend_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
             grow = true;
           }
         }
+        if (__any_sync(0xffffffffu, grow)) {
+          // this S was issued behind the previous value product, so O is complete; the lanes are this warp's alone
+          for (int c = 0; c < VC * kBK; c += 16) {
+            uint32_t v[16];
+            tmem_ld16(o_col + c, v);
+            tmem_ld_wait();
+#pragma unroll
+            for (int x = 0; x < 16; ++x) v[x] = __float_as_uint(__uint_as_float(v[x]) * f);
+            tmem_st16(o_col + c, v);
+          }
+        }
         const float ref = m == -INFINITY ? 0.0f : m;
         float2 sum0 = make_float2(0.0f, 0.0f), sum1 = sum0;
 #pragma unroll
@@ -805,48 +842,55 @@ attend_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
             pk[j] = *reinterpret_cast<const uint32_t*>(&h);
           }
           tmem_st16(s_col + 16 * c, pk);
+          if (c & 1) {   // the value product of 64 tokens starts while the other 64 are still in the making
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(c == 1 ? &sh.p_half[g] : &sh.p_ready[g]);
+          }
         }
         l += (sum0.x + sum0.y) + (sum1.x + sum1.y);
-        if (__any_sync(0xffffffffu, grow)) {
-          // this S was issued behind the previous value product, so O is complete; the lanes are this warp's alone
-          for (int c = 0; c < p.dv; c += 32) {
-            uint32_t v[32];
-            tmem_ld32(o_col + c, v);
-            tmem_ld_wait();
-#pragma unroll
-            for (int x = 0; x < 32; ++x) v[x] = __float_as_uint(__uint_as_float(v[x]) * f);
-            tmem_st32(o_col + c, v);
-          }
-        }
-        tmem_st_wait();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.p_ready[g]);
       }
       if (!ok) break;
-      ok = warp_wait(&sh.o_full[g], (uses - 1) & 1, abort_flag);
-      if (!ok) break;
+      // where this item's results go, and the next item's queries, before the wait for the last product
+      const int used = uses;
+      const size_t row = (size_t)it.row0 + in_block;
+      const int head = it.head, split = it.split;
+      have = next_item();
+      if (!have && !ok) break;
+      if (!warp_wait(&sh.o_full[g], (used - 1) & 1, abort_flag)) break;
       tc_fence_after();
-      const float inv_l = 1.0f / l;
-      __nv_bfloat16* dst = p.out + ((size_t)(it.row0 + in_block) * p.heads + it.head) * p.dv;
-      for (int c = 0; c < p.dv; c += 32) {
-        uint32_t v[32];
-        tmem_ld32(o_col + c, v);
-        tmem_ld_wait();
-        if (in_block < it.rows) {
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            uint32_t w[4];
-#pragma unroll
-            for (int y = 0; y < 4; ++y) {
-              const __nv_bfloat162 h = __floats2bfloat162_rn(__uint_as_float(v[8 * x + 2 * y]) * inv_l,
-                                                             __uint_as_float(v[8 * x + 2 * y + 1]) * inv_l);
-              w[y] = *reinterpret_cast<const uint32_t*>(&h);
-            }
-            *reinterpret_cast<uint4*>(dst + c + 8 * x) = make_uint4(w[0], w[1], w[2], w[3]);
+      if (p.splits > 1) {
+        const size_t at = ((size_t)split * p.heads + head) * p.T + row;
+        if (mine) p.ml[at] = make_float2(m, l);
+        for (int c = 0; c < VC * kBK; c += 16) {
+          uint32_t v[16];
+          tmem_ld16(o_col + c, v);
+          tmem_ld_wait();
+          if (mine) {
+            st_sector(p.part + at * (VC * kBK) + c, v);
+            st_sector(p.part + at * (VC * kBK) + c + 8, v + 8);
           }
+          __syncwarp();
         }
-        __syncwarp();
+      } else {
+        const float inv_l = 1.0f / l;
+        __nv_bfloat16* dst = p.out + (row * p.heads + head) * (VC * kBK);
+        for (int c = 0; c < VC * kBK; c += 16) {
+          uint32_t v[16], w[8];
+          tmem_ld16(o_col + c, v);
+          tmem_ld_wait();
+#pragma unroll
+          for (int y = 0; y < 8; ++y) {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(__uint_as_float(v[2 * y]) * inv_l, __uint_as_float(v[2 * y + 1]) * inv_l);
+            w[y] = *reinterpret_cast<const uint32_t*>(&h);
+          }
+          if (mine) {
+            *reinterpret_cast<uint4*>(dst + c) = make_uint4(w[0], w[1], w[2], w[3]);
+            *reinterpret_cast<uint4*>(dst + c + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+          }
+          __syncwarp();
+        }
       }
       tc_fence_before();
     }
@@ -857,15 +901,74 @@ attend_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
   if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols));
 }
 
+// ---------------------------------------------------------------- combine of the token shares
+// One warp per (query row, head): the shares' outputs weighted by their (m, l), in share order.  A share in which the
+// row's tile had no tokens wrote nothing: which ones did follows from the block, as in get_item.
+__global__ void __launch_bounds__(256) combine_splits_kernel(const PrefillParams p) {
+  pdl_wait();
+  pdl_trigger();
+  const int lane = threadIdx.x & 31, block = blockIdx.x;
+  if (block >= p.counts[0]) return;
+  const int4 qb = __ldg(reinterpret_cast<const int4*>(p.blocks + block));
+  const int all = (qb.z + qb.y - 1 + kTile - 1) / kTile;
+  for (int x = blockIdx.y * 8 + (threadIdx.x >> 5); x < qb.y * p.heads; x += gridDim.y * 8) {
+    const int j = x / p.heads, head = x - j * p.heads;
+    const int last = min(qb.y, (j / kTile + 1) * kTile) - 1, mine = (qb.z + last + kTile - 1) / kTile;
+    const size_t row = (size_t)qb.x + j;
+    float top = -INFINITY;
+    float2 ml[kMaxSplits];
+#pragma unroll
+    for (int s = 0; s < kMaxSplits; ++s) {
+      ml[s] = make_float2(-INFINITY, 0.0f);
+      if (s < p.splits && (int)((long long)all * s / p.splits) < min(mine, (int)((long long)all * (s + 1) / p.splits)))
+        ml[s] = p.ml[((size_t)s * p.heads + head) * p.T + row];
+      top = fmaxf(top, ml[s].x);
+    }
+    const float ref = top == -INFINITY ? 0.0f : top;
+    float l = 0.0f;
+    float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int s = 0; s < kMaxSplits; ++s) {
+      if (s >= p.splits || (ml[s].x == -INFINITY && ml[s].y == 0.0f)) continue;
+      const float w = ex2(ml[s].x - ref);
+      l = fmaf(w, ml[s].y, l);
+      const float* o = p.part + (((size_t)s * p.heads + head) * p.T + row) * p.dv;
+#pragma unroll
+      for (int y = 0; y < 4; ++y)
+        if (lane + 32 * y < p.dv) acc[y] = fmaf(w, o[lane + 32 * y], acc[y]);
+    }
+#pragma unroll
+    for (int y = 0; y < 4; ++y)
+      if (lane + 32 * y < p.dv) p.out[(row * p.heads + head) * p.dv + lane + 32 * y] = __float2bfloat16_rn(acc[y] / l);
+  }
+}
+
 // ---------------------------------------------------------------- host side
 struct PrefillWs {
-  size_t base, counts, blocks, k, v, r, bytes;
-  int rows, n_blocks;
+  size_t base, counts, blocks, k, v, r, part, ml, bytes;
+  int rows, n_blocks, splits;
 };
 
 bool prefill_shape_ok(int B, int T, int heads, int dn, int dv, int kv_tokens) {
   if ((dn != 64 && dn != 128) || (dv != 64 && dv != 128) || heads > 1024 || B > 4096) return false;
   return (long long)T * heads <= INT_MAX && ((long long)kv_tokens + 128LL * B) * heads <= INT_MAX;
+}
+
+// Shares of the tokens where the query blocks and heads alone leave SMs idle: the count whose whole rounds over the
+// SMs come nearest to even work, with 2% charged per share for its partial results (1000 queries of 16 heads over
+// 16000 tokens: 64 items, 2 shares).
+int token_shares(long long items) {
+  const int sms = num_sms();
+  int best = 1;
+  float least = 1e30f;
+  for (int s = 1; s <= kMaxSplits && items < sms; ++s) {
+    const float cost = (float)((items * s + sms - 1) / sms) / s + 0.02f * s;
+    if (cost < least) {
+      least = cost;
+      best = s;
+    }
+  }
+  return best;
 }
 
 PrefillWs prefill_ws(int B, int T, int heads, int dn, int dv, int rope, int kv_tokens) {
@@ -885,6 +988,11 @@ PrefillWs prefill_ws(int B, int T, int heads, int dn, int dv, int rope, int kv_t
   at += align_up((size_t)heads * w.rows * dv * 2, 256);
   w.r = at;
   at += align_up((size_t)w.rows * (rope ? rope : 8) * 2, 256);
+  w.splits = token_shares((long long)w.n_blocks * heads);
+  w.part = at;
+  if (w.splits > 1) at += align_up((size_t)w.splits * heads * T * dv * sizeof(float), 256);
+  w.ml = at;
+  if (w.splits > 1) at += align_up((size_t)w.splits * heads * T * sizeof(float2), 256);
   w.bytes = at;
   return w;
 }
@@ -929,6 +1037,8 @@ int launch_prefill(const PrefillParams& p, cudaStream_t s) {
                    : kc == 2 ? launch_attend<2, 1>(mq, mk, mr, mv, p, s)
                              : launch_attend<1, 1>(mq, mk, mr, mv, p, s));
   }
+  if (e == cudaSuccess && p.splits > 1)
+    e = launch_k(combine_splits_kernel, dim3(p.max_blocks_q, 4 * num_sms() / p.max_blocks_q + 1), 256, 0, s, p);
   return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
@@ -987,6 +1097,9 @@ int moe_latent_prefill(const moe_kv_cache* cache, int layer, const void* q, cons
   p.k = reinterpret_cast<__half*>(b + w.k);
   p.v = reinterpret_cast<__half*>(b + w.v);
   p.r = reinterpret_cast<__half*>(b + w.r);
+  p.splits = w.splits;
+  p.part = reinterpret_cast<float*>(b + w.part);
+  p.ml = reinterpret_cast<float2*>(b + w.ml);
   p.status = dev_status;
   return launch_prefill(p, reinterpret_cast<cudaStream_t>(stream));
 }
