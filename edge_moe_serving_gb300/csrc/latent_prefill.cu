@@ -7,12 +7,14 @@
 // attend_kernel  256 query rows of one head against that head's keys and
 //                values, 128 tokens at a time
 //
-// Keys, values, queries and probabilities are f16, not bf16: 11 significand
-// bits keep each rounding at 2^-12 where bf16's would put 2^-9 on every key,
-// value and probability, at the same tensor-core rate.  The price is range: an
-// expanded key or value beyond 65504 is clamped and reported
-// (MOE_DEV_ERR_RANGE); a query row is brought into range by its own power of
-// two, which goes into the row's score scale, so queries lose nothing.
+// Values and probabilities are f16, not bf16: 11 significand bits keep their
+// roundings at 2^-12 where bf16's 2^-9 on each value and probability would reach
+// the output in full, at the same tensor-core rate.  The price is range: an
+// expanded value beyond 65504 is clamped and reported (MOE_DEV_ERR_RANGE).
+// Queries come in bf16 and keys stay bf16 beside them (one product takes one
+// type): a key's rounding moves a score by about 2^-9 / sqrt(keys' width) of its
+// terms' size, which the softmax averages.
+#include <cfloat>
 #include <cmath>
 
 #include <cuda_fp16.h>
@@ -53,9 +55,9 @@ struct PrefillParams {
   int32_t* base;            // [B + 1] first expanded row of each sequence; base[B]: their end, < 0: over capacity
   int32_t* counts;          // [0] query blocks, [1] next work item
   QBlock* blocks;
-  __half* k;                // [heads, kv_rows, dn]
+  __nv_bfloat16* k;         // [heads, kv_rows, dn]
   __half* v;                // [heads, kv_rows, dv]
-  __half* r;                // [kv_rows, rope]
+  __nv_bfloat16* r;         // [kv_rows, rope]
   float* part;              // with splits: [splits, heads, T, dv] unnormalised outputs
   float2* ml;               // [splits, heads, T] their (m, l)
   uint32_t* status;
@@ -80,6 +82,11 @@ __device__ inline uint32_t half2_of(float x, float y, bool& clamped) {
     }
   }
   const __half2 h = __floats2half2_rn(x, y);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+__device__ inline uint32_t bf16x2_of(float x, float y) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
@@ -358,12 +365,7 @@ expand_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
                                                p.kv.rank);
         }
         for (int x = 0; x < p.rope / 8; ++x) {
-          const uint4 v = there ? src[x] : make_uint4(0, 0, 0, 0);
-          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-          uint32_t o[4];
-#pragma unroll
-          for (int y = 0; y < 4; ++y) o[y] = half2_of(bf16_lo(w[y]), bf16_hi(w[y]), clamped);
-          *reinterpret_cast<uint4*>(p.r + (size_t)row * p.rope + 8 * x) = make_uint4(o[0], o[1], o[2], o[3]);
+          *reinterpret_cast<uint4*>(p.r + (size_t)row * p.rope + 8 * x) = there ? src[x] : make_uint4(0, 0, 0, 0);
         }
       }
       if (!warp_wait(&sh.d_full[buf], (n >> 1) & 1, abort_flag)) break;
@@ -378,14 +380,15 @@ expand_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
         tmem_ld_wait();
         if (32 * (c + 1) < N) tmem_ld32(col + 32 * (c + 1), v[(c + 1) & 1]);
         uint32_t o[16];
+        const bool key = 32 * c < p.dn;
 #pragma unroll
         for (int y = 0; y < 16; ++y) {
           const float e0 = __uint_as_float(v[c & 1][2 * y]), e1 = __uint_as_float(v[c & 1][2 * y + 1]);
-          o[y] = there ? half2_of(e0, e1, clamped) : 0u;
+          o[y] = !there ? 0u : key ? bf16x2_of(e0, e1) : half2_of(e0, e1, clamped);
         }
-        __half* dst = 32 * c < p.dn ? p.k + at * p.dn + 32 * c : p.v + at * p.dv + 32 * c - p.dn;
+        void* dst = key ? (void*)(p.k + at * p.dn + 32 * c) : (void*)(p.v + at * p.dv + 32 * c - p.dn);
         st_sector(dst, o);
-        st_sector(dst + 16, o + 8);
+        st_sector((char*)dst + 32, o + 8);
       }
       tc_fence_before();
       __syncwarp();
@@ -412,8 +415,8 @@ __device__ inline void tc_mma_ta_warp(uint32_t d_tmem, uint32_t a_tmem, uint64_t
 // fp32 accumulation, f16 operands, A and B K-major
 __host__ __device__ constexpr uint32_t idesc_f16(int M, int N) { return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24); }
 struct Shared {
-  uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
-  uint64_t q_full[2], q_ready[2], q_empty[2];    // a query tile: loaded, turned to f16, no longer read
+  uint64_t full[4], empty[4], r_full[2], r_empty[2];   // key and value tiles, rotary key tiles
+  uint64_t q_full[2], q_empty[2];
   uint64_t s_full[2], p_half[2], p_ready[2], o_full[2];   // p_half: the probabilities of the first 64 tokens
   uint64_t w_full[2], w_empty[2];                // work items
   uint64_t drain;
@@ -422,13 +425,15 @@ struct Shared {
   int abort;
 };
 
-// Shared memory by the head's chunks of 64 entries (KC: key with its rotary part, VC: value): two query tiles, two
-// key tiles, and two value tiles where they fit (one for heads of 128 + rotary).
-template <int KC, int VC>
+// Shared memory by the chunks of 64 entries of a query (KC: with the rotary part): two query tiles, two rotary key
+// tiles, and a ring of key and value tiles in the order of their use, K(0) V(0) K(1) V(1) ...: while V(i) and K(i+1)
+// are read, V(i+1) is on its way.
+template <int KC>
 struct Attend {
-  static constexpr int kQ = KC * kChunkBytes, kV = VC * kChunkBytes;
-  static constexpr int kStagesV = 4 * kQ + 2 * kV <= 224 * 1024 ? 2 : 1;
-  static constexpr int kSmem = 4 * kQ + kStagesV * kV + 1024;
+  static constexpr int kQ = KC * kChunkBytes, kUnit = 2 * kChunkBytes;
+  static constexpr int kUnits = KC == 3 ? 3 : 4;
+  static constexpr int kRope = 2 * kQ, kRing = kRope + 2 * kChunkBytes;   // where the parts begin
+  static constexpr int kSmem = kRing + kUnits * kUnit + 1024;
 };
 
 // A work item: 256 query rows of one head against one of p.splits shares of their tokens.
@@ -467,20 +472,21 @@ __global__ void __launch_bounds__(kThreads, 1)
 attend_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
               const __grid_constant__ CUtensorMap map_r, const __grid_constant__ CUtensorMap map_v,
               const PrefillParams p) {
-  using A = Attend<KC, VC>;
+  using A = Attend<KC>;
   extern __shared__ uint8_t smem_raw[];
   __shared__ Shared sh;
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
   if (tid == 0) {
+    for (int i = 0; i < A::kUnits; ++i) {
+      mbar_init(&sh.full[i], 1);
+      mbar_init(&sh.empty[i], 1);
+    }
     for (int g = 0; g < 2; ++g) {
-      mbar_init(&sh.k_full[g], 1);
-      mbar_init(&sh.k_empty[g], 1);
-      mbar_init(&sh.v_full[g], 1);
-      mbar_init(&sh.v_empty[g], 1);
+      mbar_init(&sh.r_full[g], 1);
+      mbar_init(&sh.r_empty[g], 1);
       mbar_init(&sh.q_full[g], 1);
-      mbar_init(&sh.q_ready[g], 4);
       mbar_init(&sh.q_empty[g], 1);
       mbar_init(&sh.s_full[g], 1);
       mbar_init(&sh.p_half[g], 4);
@@ -521,24 +527,37 @@ attend_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
     asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
     if (warp == 0) {
       // ---------------------------------------------- work items and TMA
-      const uint32_t smem0 = uni(smem_u32(smem)), k0 = smem0 + 2 * A::kQ, v0 = k0 + 2 * A::kQ;
-      const uint32_t kf = uni(smem_u32(&sh.k_full[0])), vf = uni(smem_u32(&sh.v_full[0]));
+      const uint32_t smem0 = uni(smem_u32(smem));
+      const uint32_t full0 = uni(smem_u32(&sh.full[0])), rf = uni(smem_u32(&sh.r_full[0]));
       const uint32_t qf = uni(smem_u32(&sh.q_full[0]));
-      int n = 0, k_loads = 0, v_loads = 0, q_loads0 = 0, q_loads1 = 0;
+      int n = 0, units = 0, slot = 0, ropes = 0, q_loads0 = 0, q_loads1 = 0;
+      uint32_t par = 1;
       bool ok = true;
-      auto load_k = [&](int head, int row) {
-        const int st = k_loads & 1;
-        ok = warp_wait(&sh.k_empty[st], ((k_loads >> 1) & 1) ^ 1u, abort_flag);
+      // `chunks` of 64 columns of 128 rows into the next place of the ring
+      auto load_unit = [&](const CUtensorMap* map, int chunks, int row) {
         if (!ok) return;
-        ++k_loads;
-        mbar_expect_tx_warp(kf + 8 * st, A::kQ);
+        ok = warp_wait(&sh.empty[slot], par, abort_flag);
+        if (!ok) return;
+        ++units;
+        mbar_expect_tx_warp(full0 + 8 * slot, (uint32_t)(chunks * kChunkBytes));
 #pragma unroll
-        for (int c = 0; c < KC; ++c) {
-          if (c < key_chunks)
-            tma_load_2d_warp(k0 + st * A::kQ + c * kChunkBytes, &map_k, kf + 8 * st, c * kBK, head * p.kv_rows + row);
-          else
-            tma_load_2d_warp(k0 + st * A::kQ + c * kChunkBytes, &map_r, kf + 8 * st, 0, row);
+        for (int c = 0; c < 2; ++c)
+          if (c < chunks)
+            tma_load_2d_warp(smem0 + A::kRing + slot * A::kUnit + c * kChunkBytes, map, full0 + 8 * slot, c * kBK, row);
+        if (++slot == A::kUnits) {
+          slot = 0;
+          par ^= 1u;
         }
+      };
+      auto load_k = [&](int head, int row) {
+        load_unit(&map_k, key_chunks, head * p.kv_rows + row);
+        if (!rope_chunk || !ok) return;
+        const int st = ropes & 1;
+        ok = warp_wait(&sh.r_empty[st], ((ropes >> 1) & 1) ^ 1u, abort_flag);
+        if (!ok) return;
+        ++ropes;
+        mbar_expect_tx_warp(rf + 8 * st, kChunkBytes);
+        tma_load_2d_warp(smem0 + A::kRope + st * kChunkBytes, &map_r, rf + 8 * st, 0, row);
       };
       auto load_q = [&](int g, int& loads, int head, int row0) {
         ok = warp_wait(&sh.q_empty[g], (loads & 1) ^ 1u, abort_flag);
@@ -550,35 +569,33 @@ attend_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
           tma_load_2d_warp(smem0 + g * A::kQ + c * kChunkBytes, &map_q, qf + 8 * g, head * (p.dn + p.rope) + c * kBK,
                            row0 + g * kTile);
       };
-      for (;;) {
-        ok = warp_wait(&sh.w_empty[n & 1], ((n >> 1) & 1) ^ 1u, abort_flag);
-        if (!ok) break;
+      // the next work item's number, for everyone; fetched one item ahead of its use
+      auto fetch = [&]() {
         int k = 0;
+        ok = warp_wait(&sh.w_empty[n & 1], ((n >> 1) & 1) ^ 1u, abort_flag);
+        if (!ok) return 0;
         if (lane == 0) {
           k = atomicAdd(&p.counts[1], 1);
           sh.item[n & 1] = k;
           mbar_arrive(&sh.w_full[n & 1]);
         }
-        k = (int)uni(k);
         ++n;
+        return (int)uni(k);
+      };
+      int ahead = fetch();
+      while (ok) {
+        const int k = ahead;
         if (!__any_sync(0xffffffffu, get_item(p, k, n_blocks, group, it))) break;
+        ahead = fetch();
+        if (!ok) break;
         const int row0 = (int)uni(it.row0), head = (int)uni(it.head), base = (int)uni(it.base + it.first * kTile);
         const int ta = (int)uni(it.tiles[0]), tb = (int)uni(it.tiles[1]), tiles = max(ta, tb);
         if (ta) load_q(0, q_loads0, head, row0);
         if (ok && tiles) load_k(head, base);
         if (ok && tb) load_q(1, q_loads1, head, row0);
         for (int i = 0; i < tiles && ok; ++i) {
-          if (i + 1 < tiles) load_k(head, base + (i + 1) * kTile);
-          if (!ok) break;
-          const int st = v_loads % A::kStagesV;
-          ok = warp_wait(&sh.v_empty[st], ((v_loads / A::kStagesV) & 1) ^ 1u, abort_flag);
-          if (!ok) break;
-          ++v_loads;
-          mbar_expect_tx_warp(vf + 8 * st, A::kV);
-#pragma unroll
-          for (int c = 0; c < VC; ++c)
-            tma_load_2d_warp(v0 + st * A::kV + c * kChunkBytes, &map_v, vf + 8 * st, c * kBK,
-                             head * p.kv_rows + base + i * kTile);
+          load_unit(&map_v, VC, head * p.kv_rows + base + i * kTile);
+          if (ok && i + 1 < tiles) load_k(head, base + (i + 1) * kTile);
         }
         if (!ok) break;
       }
@@ -586,11 +603,13 @@ attend_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
       volatile int no_abort = 0;
       if (q_loads0) mbar_wait(&sh.q_full[0], (q_loads0 - 1) & 1, &no_abort);
       if (q_loads1) mbar_wait(&sh.q_full[1], (q_loads1 - 1) & 1, &no_abort);
-      for (int st = 0; st < 2; ++st) {
-        const int nk = (k_loads + 1 - st) / 2;
-        if (nk > 0) mbar_wait(&sh.k_full[st], (nk - 1) & 1, &no_abort);
-        const int nv = A::kStagesV == 2 ? (v_loads + 1 - st) / 2 : (st == 0 ? v_loads : 0);
-        if (nv > 0) mbar_wait(&sh.v_full[st], (nv - 1) & 1, &no_abort);
+      for (int i = 0; i < A::kUnits; ++i) {
+        const int loads = units / A::kUnits + (units % A::kUnits > i ? 1 : 0);
+        if (loads > 0) mbar_wait(&sh.full[i], (loads - 1) & 1, &no_abort);
+      }
+      for (int i = 0; i < 2; ++i) {
+        const int loads = (ropes + 1 - i) / 2;
+        if (loads > 0) mbar_wait(&sh.r_full[i], (loads - 1) & 1, &no_abort);
       }
       __syncwarp();
     } else if (warp == 1) {
@@ -598,29 +617,52 @@ attend_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
       // Order for tiles a, b: S_a(0) S_b(0) | PV_a(i) S_a(i+1) PV_b(i) S_b(i+1): while one tile's softmax runs, the
       // other tile's products do.  P lies in its S's columns, so S_a(i+1) follows PV_a(i).
       const uint32_t tm = uni(tmem), smem0 = uni(smem_u32(smem));
-      const uint64_t dq0 = smem_desc(smem0), dk0 = smem_desc(smem0 + 2 * A::kQ);
-      const uint64_t dv0 = smem_desc_mn(smem0 + 4 * A::kQ, kChunkBytes);
-      constexpr uint32_t idesc_s = idesc_f16(128, kTile), idesc_v = idesc_f16(128, VC * kBK) | kTransB;
+      const uint64_t dq0 = smem_desc(smem0), dk0 = smem_desc(smem0 + A::kRing), dr0 = smem_desc(smem0 + A::kRope);
+      const uint64_t dv0 = smem_desc_mn(smem0 + A::kRing, kChunkBytes);
+      constexpr uint32_t idesc_s = make_idesc(128, kTile), idesc_v = idesc_f16(128, VC * kBK) | kTransB;
+      constexpr int KN = KC < 2 ? KC : 2;      // key chunks at most
       const int rope_steps = (int)uni(p.rope / kUK);
-      int n = 0, k_uses = 0, v_uses = 0, q_uses0 = 0, q_uses1 = 0, p_uses0 = 0, p_uses1 = 0;
+      int n = 0, ropes = 0, q_uses0 = 0, q_uses1 = 0, p_uses0 = 0, p_uses1 = 0;
+      int slot = 0, slot2 = 1;                 // the ring's next tile and the one behind it
+      uint32_t par = 0, par2 = 0;
       bool issued = false, ok = true;
-      auto issue_s = [&](int g, int st) {
-        const uint64_t dq = dq0 + (uint64_t)((g * A::kQ) >> 4), dk = dk0 + (uint64_t)((st * A::kQ) >> 4);
+      auto advance = [&]() {                   // the next tile is done with: its place is free once the products are over
+        tc_commit_warp(&sh.empty[slot]);
+        slot = slot2;
+        par = par2;
+        if (++slot2 == A::kUnits) {
+          slot2 = 0;
+          par2 ^= 1u;
+        }
+      };
+      auto wait_k = [&](int at, uint32_t parity) {
+        ok = warp_wait(&sh.full[at], parity, abort_flag);
+        if (ok && rope_chunk) ok = warp_wait(&sh.r_full[ropes & 1], (ropes >> 1) & 1, abort_flag);
+      };
+      auto free_rope = [&]() {
+        if (rope_chunk) tc_commit_warp(&sh.r_empty[ropes++ & 1]);
+      };
+      auto issue_s = [&](int g, int at) {
+        const uint64_t dq = dq0 + (uint64_t)((g * A::kQ) >> 4), dk = dk0 + (uint64_t)((at * A::kUnit) >> 4);
+        const uint64_t dr = dr0 + (uint64_t)(((ropes & 1) * kChunkBytes) >> 4);
 #pragma unroll
-        for (int c = 0; c < KC; ++c) {
-          const int steps = c < key_chunks ? 4 : rope_steps;
+        for (int c = 0; c < KN; ++c)
+          if (c < key_chunks)
 #pragma unroll
-          for (int x = 0; x < 4; ++x)
-            if (x < steps)
+            for (int x = 0; x < 4; ++x)
               tc_mma_warp(tm + g * kTile, dq + ((c * kChunkBytes + x * kUK * 2) >> 4),
                           dk + ((c * kChunkBytes + x * kUK * 2) >> 4), idesc_s, (c | x) ? 1u : 0u);
-        }
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+          if (x < rope_steps)
+            tc_mma_warp(tm + g * kTile, dq + (((KC - 1) * kChunkBytes + x * kUK * 2) >> 4), dr + ((x * kUK * 2) >> 4),
+                        idesc_s, 1u);
         tc_commit_warp(&sh.s_full[g]);
         issued = true;
       };
       // half of a value product: 64 tokens
-      auto issue_pv = [&](int g, int st, int half, uint32_t acc) {
-        const uint64_t dv = dv0 + (uint64_t)((st * A::kV) >> 4);
+      auto issue_pv = [&](int g, int half, uint32_t acc) {
+        const uint64_t dv = dv0 + (uint64_t)((slot * A::kUnit) >> 4);
 #pragma unroll
         for (int y = 0; y < 4; ++y) {
           const int x = 4 * half + y;
@@ -637,63 +679,61 @@ attend_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
         if (!__any_sync(0xffffffffu, get_item(p, k, n_blocks, group, it))) break;
         const int ta = (int)uni(it.tiles[0]), tb = (int)uni(it.tiles[1]), tiles = max(ta, tb);
         if (!tiles) continue;
-        ok = warp_wait(&sh.k_full[k_uses & 1], (k_uses >> 1) & 1, abort_flag);
+        wait_k(slot, par);
         if (!ok) break;
         if (ta) {
-          ok = warp_wait(&sh.q_ready[0], q_uses0 & 1, abort_flag);
+          ok = warp_wait(&sh.q_full[0], q_uses0 & 1, abort_flag);
           if (!ok) break;
           ++q_uses0;
           tc_fence_after();
-          issue_s(0, k_uses & 1);
+          issue_s(0, slot);
           if (ta == 1) tc_commit_warp(&sh.q_empty[0]);
         }
         if (tb) {
-          ok = warp_wait(&sh.q_ready[1], q_uses1 & 1, abort_flag);
+          ok = warp_wait(&sh.q_full[1], q_uses1 & 1, abort_flag);
           if (!ok) break;
           ++q_uses1;
           tc_fence_after();
-          issue_s(1, k_uses & 1);
+          issue_s(1, slot);
           if (tb == 1) tc_commit_warp(&sh.q_empty[1]);
         }
-        tc_commit_warp(&sh.k_empty[k_uses & 1]);
-        ++k_uses;
+        advance();
+        free_rope();
         for (int i = 0; i < tiles; ++i) {
-          const int vs = v_uses % A::kStagesV, ks = k_uses & 1;
           const uint32_t acc = i ? 1u : 0u;
           bool have_v = false, have_k = false;
           // both tiles of the step; a tile that sees fewer tokens ends earlier
           auto tile_step = [&](int g, int t, int& p_uses) {
             if (i >= t || !ok) return;
             ok = warp_wait(&sh.p_half[g], p_uses & 1, abort_flag);
-            if (ok && !have_v) ok = warp_wait(&sh.v_full[vs], (v_uses / A::kStagesV) & 1, abort_flag);
+            if (ok && !have_v) ok = warp_wait(&sh.full[slot], par, abort_flag);
             if (!ok) return;
             have_v = true;
             tc_fence_after();
-            issue_pv(g, vs, 0, acc);
+            issue_pv(g, 0, acc);
             ok = warp_wait(&sh.p_ready[g], p_uses & 1, abort_flag);
             if (!ok) return;
             ++p_uses;
             tc_fence_after();
-            issue_pv(g, vs, 1, 1u);
+            issue_pv(g, 1, 1u);
             if (i + 1 == t) {
               tc_commit_warp(&sh.o_full[g]);
               return;
             }
-            if (!have_k) ok = warp_wait(&sh.k_full[ks], (k_uses >> 1) & 1, abort_flag);
+            if (!have_k) wait_k(slot2, par2);
             if (!ok) return;
             have_k = true;
             tc_fence_after();
-            issue_s(g, ks);
+            issue_s(g, slot2);
             if (i + 2 == t) tc_commit_warp(&sh.q_empty[g]);
           };
           tile_step(0, ta, p_uses0);
           tile_step(1, tb, p_uses1);
           if (!ok) break;
-          tc_commit_warp(&sh.v_empty[vs]);
-          ++v_uses;
+          advance();
           if (i + 1 < tiles) {
-            tc_commit_warp(&sh.k_empty[ks]);
-            ++k_uses;
+            advance();
+            free_rope();
           }
         }
         if (!ok) break;
@@ -711,13 +751,12 @@ attend_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
     const int g = (warp - 4) >> 2, quarter = warp & 3, r = quarter * 32 + lane;
     const uint32_t lane_base = tmem + ((uint32_t)(quarter * 32) << 16);
     const uint32_t s_col = lane_base + g * kTile, o_col = lane_base + 256 + g * kTile;
-    uint8_t* qrow = smem + g * A::kQ + r * 128;
-    const int dim = p.dn + p.rope;
     int n = 0, uses = 0, steps = 0;
     bool ok = true;
-    float scale = 0.0f;
-    // The next work item with tokens for this tile, its query row turned to f16 in place, scaled by a power of two so
-    // that its largest entry lies in [1, 2): the power goes into the row's score scale.
+    const float scale = p.scale_log2;
+    const bool neg = scale < 0.0f;
+    const float unseen = neg ? INFINITY : -INFINITY;   // what a token out of sight scores
+    // the next work item with tokens for this tile
     auto next_item = [&]() {
       for (;;) {
         ok = warp_wait(&sh.w_full[n & 1], (n >> 1) & 1, abort_flag);
@@ -727,52 +766,14 @@ attend_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
         if (lane == 0) mbar_arrive(&sh.w_empty[n & 1]);
         ++n;
         if (!__any_sync(0xffffffffu, get_item(p, k, n_blocks, group, it))) return false;
-        if (g ? it.tiles[1] : it.tiles[0]) break;
+        if (g ? it.tiles[1] : it.tiles[0]) return true;
       }
-      ok = warp_wait(&sh.q_full[g], uses & 1, abort_flag);
-      if (!ok) return false;
-      ++uses;
-      float big = 0.0f;
-#pragma unroll
-      for (int c = 0; c < KC; ++c)
-#pragma unroll
-        for (int x = 0; x < 8; ++x) {
-          const uint4 u = *reinterpret_cast<const uint4*>(qrow + c * kChunkBytes + ((x ^ (r & 7)) << 4));
-          if (c * kBK + 8 * x < dim) {
-            const float b0 = fmaxf(fmaxf(fabsf(bf16_lo(u.x)), fabsf(bf16_hi(u.x))), fmaxf(fabsf(bf16_lo(u.y)), fabsf(bf16_hi(u.y))));
-            const float b1 = fmaxf(fmaxf(fabsf(bf16_lo(u.z)), fabsf(bf16_hi(u.z))), fmaxf(fabsf(bf16_lo(u.w)), fabsf(bf16_hi(u.w))));
-            big = fmaxf(big, fmaxf(b0, b1));
-          }
-        }
-      // 2^e from the exponent bits; zero rows and rows with an infinity stay as they are
-      const uint32_t ebits = __float_as_uint(big) & 0x7F800000u;
-      const bool plain = ebits == 0 || ebits >= 0x7F000000u;
-      const float pow2 = plain ? 1.0f : __uint_as_float(ebits), inv = plain ? 1.0f : __uint_as_float(0x7F000000u - ebits);
-#pragma unroll
-      for (int c = 0; c < KC; ++c)
-#pragma unroll
-        for (int x = 0; x < 8; ++x) {
-          const uint4 u = *reinterpret_cast<const uint4*>(qrow + c * kChunkBytes + ((x ^ (r & 7)) << 4));
-          const __half2 h0 = __floats2half2_rn(bf16_lo(u.x) * inv, bf16_hi(u.x) * inv);
-          const __half2 h1 = __floats2half2_rn(bf16_lo(u.y) * inv, bf16_hi(u.y) * inv);
-          const __half2 h2 = __floats2half2_rn(bf16_lo(u.z) * inv, bf16_hi(u.z) * inv);
-          const __half2 h3 = __floats2half2_rn(bf16_lo(u.w) * inv, bf16_hi(u.w) * inv);
-          *reinterpret_cast<uint4*>(qrow + c * kChunkBytes + ((x ^ (r & 7)) << 4)) =
-              make_uint4(*reinterpret_cast<const uint32_t*>(&h0), *reinterpret_cast<const uint32_t*>(&h1),
-                         *reinterpret_cast<const uint32_t*>(&h2), *reinterpret_cast<const uint32_t*>(&h3));
-        }
-      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sh.q_ready[g]);
-      scale = p.scale_log2 * pow2;
-      return true;
     };
     bool have = next_item();
     while (have) {
       const int tiles = g ? it.tiles[1] : it.tiles[0], first = it.first, in_block = g * kTile + r;
       const int limit = it.limit0 + in_block - first * kTile;
-      const bool neg = scale < 0.0f, mine = in_block < it.rows;
-      const float unseen = neg ? INFINITY : -INFINITY;   // what a token out of sight scores
+      const bool mine = in_block < it.rows;
       float m = -INFINITY, l = 0.0f;
       for (int i = 0; i < tiles; ++i, ++steps) {
         ok = warp_wait(&sh.s_full[g], steps & 1, abort_flag);
@@ -852,45 +853,39 @@ attend_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
         l += (sum0.x + sum0.y) + (sum1.x + sum1.y);
       }
       if (!ok) break;
-      // where this item's results go, and the next item's queries, before the wait for the last product
-      const int used = uses;
+      // where this item's results go; the next item's numbers come before the wait for the last product
       const size_t row = (size_t)it.row0 + in_block;
       const int head = it.head, split = it.split;
       have = next_item();
       if (!have && !ok) break;
-      if (!warp_wait(&sh.o_full[g], (used - 1) & 1, abort_flag)) break;
+      if (!warp_wait(&sh.o_full[g], uses++ & 1, abort_flag)) break;
       tc_fence_after();
-      if (p.splits > 1) {
-        const size_t at = ((size_t)split * p.heads + head) * p.T + row;
-        if (mine) p.ml[at] = make_float2(m, l);
-        for (int c = 0; c < VC * kBK; c += 16) {
-          uint32_t v[16];
-          tmem_ld16(o_col + c, v);
-          tmem_ld_wait();
-          if (mine) {
-            st_sector(p.part + at * (VC * kBK) + c, v);
-            st_sector(p.part + at * (VC * kBK) + c + 8, v + 8);
-          }
-          __syncwarp();
-        }
-      } else {
-        const float inv_l = 1.0f / l;
-        __nv_bfloat16* dst = p.out + (row * p.heads + head) * (VC * kBK);
-        for (int c = 0; c < VC * kBK; c += 16) {
-          uint32_t v[16], w[8];
-          tmem_ld16(o_col + c, v);
-          tmem_ld_wait();
+      const bool parts = p.splits > 1;
+      const size_t at = parts ? ((size_t)split * p.heads + head) * p.T + row : row * p.heads + head;
+      if (parts && mine) p.ml[at] = make_float2(m, l);
+      const float inv_l = 1.0f / l;
+      uint32_t v[2][32];
+      tmem_ld32(o_col, v[0]);
 #pragma unroll
-          for (int y = 0; y < 8; ++y) {
-            const __nv_bfloat162 h = __floats2bfloat162_rn(__uint_as_float(v[2 * y]) * inv_l, __uint_as_float(v[2 * y + 1]) * inv_l);
-            w[y] = *reinterpret_cast<const uint32_t*>(&h);
-          }
+      for (int c = 0; c < VC * kBK; c += 32) {
+        uint32_t(&x)[32] = v[(c >> 5) & 1];
+        tmem_ld_wait();
+        if (c + 32 < VC * kBK) tmem_ld32(o_col + c + 32, v[((c >> 5) + 1) & 1]);
+        if (parts) {
           if (mine) {
-            *reinterpret_cast<uint4*>(dst + c) = make_uint4(w[0], w[1], w[2], w[3]);
-            *reinterpret_cast<uint4*>(dst + c + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+#pragma unroll
+            for (int y = 0; y < 4; ++y) st_sector(p.part + at * (VC * kBK) + c + 8 * y, x + 8 * y);
           }
-          __syncwarp();
+        } else {
+          uint32_t w[16];
+#pragma unroll
+          for (int y = 0; y < 16; ++y) w[y] = bf16x2_of(__uint_as_float(x[2 * y]) * inv_l, __uint_as_float(x[2 * y + 1]) * inv_l);
+          if (mine) {
+            st_sector(p.out + at * (VC * kBK) + c, w);
+            st_sector(p.out + at * (VC * kBK) + c + 16, w + 8);
+          }
         }
+        __syncwarp();
       }
       tc_fence_before();
     }
@@ -1000,7 +995,7 @@ PrefillWs prefill_ws(int B, int T, int heads, int dn, int dv, int rope, int kv_t
 template <int KC, int VC>
 cudaError_t launch_attend(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mr, const CUtensorMap& mv,
                           const PrefillParams& p, cudaStream_t s) {
-  using A = Attend<KC, VC>;
+  using A = Attend<KC>;
   static_assert(A::kSmem + sizeof(Shared) <= 227 * 1024, "shared memory");
   static std::atomic<unsigned char> attr[kMaxDevices];
   const cudaError_t e = once_per_device(attr, [] {
@@ -1068,7 +1063,7 @@ int moe_latent_prefill(const moe_kv_cache* cache, int layer, const void* q, cons
   if (st != MOE_OK) return st;
   if (!prefill_shape_ok(B, T, heads, dn, dv, kv_tokens)) return MOE_ERR_UNSUPPORTED;
   if (!some) return MOE_OK;
-  if (!kv_aligned(q, 16) || !kv_aligned(w_kv, 16) || !kv_aligned(out, 16)) return MOE_ERR_UNSUPPORTED;
+  if (!kv_aligned(q, 16) || !kv_aligned(w_kv, 16) || !kv_aligned(out, 32)) return MOE_ERR_UNSUPPORTED;
   const PrefillWs w = prefill_ws(B, T, heads, dn, dv, cache->rope, kv_tokens);
   st = check_ws(ws, ws_bytes, w.bytes);
   if (st != MOE_OK) return st;
@@ -1084,8 +1079,8 @@ int moe_latent_prefill(const moe_kv_cache* cache, int layer, const void* q, cons
   p.rope = cache->rope;
   p.kv_rows = w.rows;
   p.max_blocks_q = w.n_blocks;
-  // zero as a tiny number: a token out of sight scores -infinity, and 0 * -infinity is NaN
-  p.scale_log2 = scale == 0.0f ? 1e-20f : scale * 1.4426950408889634f;
+  // zero as the smallest normal number: a token out of sight scores -infinity, and 0 * -infinity is NaN
+  p.scale_log2 = scale == 0.0f ? FLT_MIN : scale * 1.4426950408889634f;
   p.q = reinterpret_cast<const __nv_bfloat16*>(q);
   p.seqs = seqs;
   p.q_off = q_offsets;
@@ -1094,9 +1089,9 @@ int moe_latent_prefill(const moe_kv_cache* cache, int layer, const void* q, cons
   p.base = reinterpret_cast<int32_t*>(b + w.base);
   p.counts = reinterpret_cast<int32_t*>(b + w.counts);
   p.blocks = reinterpret_cast<QBlock*>(b + w.blocks);
-  p.k = reinterpret_cast<__half*>(b + w.k);
+  p.k = reinterpret_cast<__nv_bfloat16*>(b + w.k);
   p.v = reinterpret_cast<__half*>(b + w.v);
-  p.r = reinterpret_cast<__half*>(b + w.r);
+  p.r = reinterpret_cast<__nv_bfloat16*>(b + w.r);
   p.splits = w.splits;
   p.part = reinterpret_cast<float*>(b + w.part);
   p.ml = reinterpret_cast<float2*>(b + w.ml);

@@ -65,7 +65,7 @@ typedef struct CUstream_st* moe_stream_t; /* same type as cudaStream_t; NULL = l
 #define MOE_DEV_ERR_BAD_SEQ 16u   /* a sequence id, token position or query range outside the cache; skipped */
 #define MOE_DEV_ERR_BAD_PAGE 32u  /* a block-table entry names no page, or an append meets a page others share */
 #define MOE_DEV_ERR_CAPACITY 64u  /* too few free pages, blocks or workspace rows; the call changed nothing */
-#define MOE_DEV_ERR_RANGE 128u    /* an expanded key or value beyond 65504 was clamped to it */
+#define MOE_DEV_ERR_RANGE 128u    /* an expanded value beyond 65504 was clamped to it */
 
 /* fill policy of moe_cache_bind_slots: which q misses form the fill set F */
 #define MOE_FILL_LOWEST_ID 0  /* the q misses with the lowest expert ids */
@@ -671,13 +671,13 @@ int moe_latent_decode(const moe_kv_cache* cache, int layer, const void* q, const
  * Query rows q_offsets[b] .. q_offsets[b+1]-1 are the newest tokens of
  * sequence seqs[b], which is in the cache already: with n of them and length
  * len, row j sees t < len - n + j + 1.  q bf16 [T, heads, dn + rope], w_kv bf16
- * [heads, dn + dv, rank], out bf16 [T, heads, dv]; q_offsets int32 [B + 1],
- * ascending from 0 to T.  The expanded keys' and values' sums are fp32; they
- * and the probabilities are rounded to f16 for the products, which accumulate
- * in fp32, as do the softmax statistics.  An expanded entry beyond 65504 in
- * magnitude is clamped and sets MOE_DEV_ERR_RANGE; entries below 6e-5 keep an
- * absolute precision of 3e-8.  A cached value that is NaN or infinite may reach
- * every query of its sequence.
+ * [heads, dn + dv, rank], out bf16 [T, heads, dv] (32-byte aligned); q_offsets int32 [B + 1],
+ * ascending from 0 to T.  The expanded keys' and values' sums are fp32; keys
+ * are rounded to bf16, values and probabilities to f16 for the products, which
+ * accumulate in fp32, as do the softmax statistics.  An expanded value beyond
+ * 65504 in magnitude is clamped and sets MOE_DEV_ERR_RANGE; values below 6e-5
+ * keep an absolute precision of 3e-8.  A cached value that is NaN or infinite may
+ * reach every query of its sequence.
  * kv_tokens: host bound on the sum of the B lengths (sizes the workspace); a
  * sum the workspace has no rows for sets MOE_DEV_ERR_CAPACITY and nothing is
  * written.  A bad id or
@@ -687,7 +687,7 @@ int moe_latent_decode(const moe_kv_cache* cache, int layer, const void* q, const
  * heads < 1, kv_tokens < 0 (< 1 with queries), a scale that is not finite, NULL q, seqs, q_offsets, w_kv or
  * out (B and T > 0); MOE_ERR_UNSUPPORTED for rank not in {128, 256, 384, 512}, rope not a
  * multiple of 16 up to 64, max_blocks * page_tokens above 2^27, dn or dv not 64 or 128, heads > 1024, B > 4096, T * heads or
- * (kv_tokens + 128 B) * heads above INT_MAX, q, w_kv or out not 16-byte aligned; MOE_ERR_WORKSPACE /
+ * (kv_tokens + 128 B) * heads above INT_MAX, q or w_kv not 16-byte or out not 32-byte aligned; MOE_ERR_WORKSPACE /
  * MOE_ERR_UNSUPPORTED for ws.  B = 0 or T = 0 is a no-op. */
 size_t moe_latent_prefill_workspace_size(const moe_kv_cache* cache, int B, int T, int heads, int dn, int dv,
                                          int kv_tokens);
