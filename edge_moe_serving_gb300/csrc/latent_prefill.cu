@@ -42,6 +42,10 @@ struct QBlock {
   int base;         // first expanded row of its sequence
 };
 
+struct TokTile {
+  int seq, t0, len, pad;   // a tile of 128 expanded rows: its sequence in the cache, first token, the sequence's length
+};
+
 struct PrefillParams {
   KvView kv;
   int layer, B, T, heads, dn, dv, rope, kv_rows, max_blocks_q;
@@ -52,9 +56,9 @@ struct PrefillParams {
   const int32_t* q_off;
   const __nv_bfloat16* w;
   __nv_bfloat16* out;
-  int32_t* base;            // [B + 1] first expanded row of each sequence; base[B]: their end, < 0: over capacity
-  int32_t* counts;          // [0] query blocks, [1] next work item
+  int32_t* counts;          // [0] query blocks, [1] next work item, [2] tiles of expanded rows
   QBlock* blocks;
+  TokTile* tiles;           // [kv_rows / 128]
   __nv_bfloat16* k;         // [heads, kv_rows, dn]
   __half* v;                // [heads, kv_rows, dv]
   __nv_bfloat16* r;         // [kv_rows, rope]
@@ -95,6 +99,7 @@ __device__ inline uint32_t bf16x2_of(float x, float y) {
 // blocks: 256 rows each, a sequence's last block first (it sees most tokens, and
 // long work items started first leave the shortest tail).
 constexpr int kPlanThreads = 512;
+constexpr int kMaxB = 4096;
 
 __device__ inline void scan2(int (&v)[2], int (&total)[2], int (*sh)[kPlanThreads / 32]) {
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
@@ -125,6 +130,7 @@ __device__ inline void scan2(int (&v)[2], int (&total)[2], int (*sh)[kPlanThread
 
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PrefillParams p) {
   __shared__ int sh[2][kPlanThreads / 32];
+  __shared__ int s_base[kMaxB], s_len[kMaxB];   // first expanded row and length of each sequence
   pdl_wait();
   pdl_trigger();
   long long rows = 0;
@@ -148,7 +154,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PrefillParams 
     if (b < p.B) {
       const long long at = rows + (long long)v[0] * kRowAlign;
       const int base = at < p.kv_rows ? (int)at : p.kv_rows;
-      p.base[b] = base;
+      s_base[b] = base;
+      s_len[b] = len;
       for (int i = 0; i < mine; ++i) {
         const int x = blocks + v[1] + mine - 1 - i, j0 = i * kBlock;
         if (x < p.max_blocks_q) p.blocks[x] = QBlock{q0 + j0, min(kBlock, n - j0), len - n + j0 + 1, base};
@@ -157,12 +164,24 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PrefillParams 
     rows += (long long)total[0] * kRowAlign;
     blocks += total[1];
   }
+  const bool fits = rows <= p.kv_rows;
   if (threadIdx.x == 0) {
-    const bool fits = rows <= p.kv_rows;
     if (!fits) set_status(p.status, MOE_DEV_ERR_CAPACITY);
-    p.base[p.B] = fits ? (int)rows : -1;
     p.counts[0] = fits ? min(blocks, p.max_blocks_q) : 0;
     p.counts[1] = 0;
+    p.counts[2] = fits ? (int)(rows / kRowAlign) : 0;
+  }
+  if (!fits) return;
+  __syncthreads();
+  for (int t = threadIdx.x; t < (int)(rows / kRowAlign); t += kPlanThreads) {
+    const int row = t * kRowAlign;
+    int lo = 0, hi = p.B;   // the last b with base <= row; sequences without tokens own no row
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (s_base[mid] <= row) lo = mid;
+      else hi = mid;
+    }
+    p.tiles[t] = TokTile{p.seqs[lo], row - s_base[lo], s_len[lo], 0};
   }
 }
 
@@ -175,8 +194,10 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PrefillParams 
 // are written as zeros (the attention multiplies them by probability 0).
 // Bound by the weights' way from L2 to the SMs: 512 cycles of products per
 // 32 KB stage.
-// Warp 0 = TMA, warp 1 = MMA (and TMEM owner), warps 2..5 = epilogue.
-constexpr int kExThreads = 192;
+// Warp 0 = TMA, warp 1 = MMA (and TMEM owner), warps 2..9 = epilogue (4 lane
+// quarters x 2 halves of the features: with 4 warps the epilogue took 7200
+// cycles a unit against 4100 of products), warps 10, 11 = rotary keys.
+constexpr int kExThreads = 384;
 constexpr int kExStages = 3;
 constexpr int kExStage = 256 * kBK * 2;    // 32 KB of weights
 constexpr int kMaxChunks = 512 / kBK;
@@ -192,17 +213,6 @@ __device__ inline void st_sector(void* dst, const uint32_t* v) {
   asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(dst), "r"(v[0]), "r"(v[1]), "r"(v[2]),
                "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
                : "memory");
-}
-
-// The sequence that owns expanded row `row`.
-__device__ inline int seq_of_row(const PrefillParams& p, int row) {
-  int lo = 0, hi = p.B;   // the last b with base[b] <= row; sequences without tokens own no row
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (p.base[mid] <= row) lo = mid;
-    else hi = mid;
-  }
-  return lo;
 }
 
 __global__ void __launch_bounds__(kExThreads, 1)
@@ -222,7 +232,7 @@ expand_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.d_full[i], 1);
-      mbar_init(&sh.d_empty[i], 4);
+      mbar_init(&sh.d_empty[i], 8);
     }
     mbar_init(&sh.drain, 1);
     sh.abort = 0;
@@ -244,7 +254,7 @@ expand_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
   pdl_trigger();
   const uint32_t tmem = sh.tmem;
   volatile int* abort_flag = &sh.abort;
-  const int tiles = max(p.base[p.B], 0) / kTile;
+  const int tiles = p.counts[2];
   const int total = tiles * p.heads;                       // units: token tile major, head minor
   const int per = (total + gridDim.x - 1) / gridDim.x;
   const int u0 = min(total, (int)blockIdx.x * per), u1 = min(total, u0 + per);
@@ -260,11 +270,11 @@ expand_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
     for (int u = u0; ok && u < u1; ++u) {
       const int tile = u / p.heads, head = u - tile * p.heads;
       if (u == u0 || head == 0) {                          // another token tile
-        const int b = seq_of_row(p, tile * kTile), t0 = tile * kTile - p.base[b], len = seq_len(p, b);
-        const int nb = (int)uni((min(kTile, len - t0) + box - 1) / box);
+        const int4 d = __ldg(reinterpret_cast<const int4*>(p.tiles + tile));   // sequence, first token, length
+        const int nb = (int)uni((min(kTile, d.z - d.y) + box - 1) / box);
         int row = 0;
         if (lane < nb) {
-          int pg = p.kv.table[(size_t)p.seqs[b] * p.kv.max_blocks + ((t0 + lane * box) >> p.kv.page_shift)];
+          int pg = p.kv.table[(size_t)d.x * p.kv.max_blocks + ((d.y + lane * box) >> p.kv.page_shift)];
           if (pg < 0 || pg >= p.kv.n_pages) {
             set_status(p.status, MOE_DEV_ERR_BAD_PAGE);
             pg = 0;
@@ -341,52 +351,74 @@ expand_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
       mbar_wait(&sh.drain, 0, &no_abort);
     }
     __syncwarp();
+  } else if (warp >= 10) {
+    // ------------------------------------------------ rotary keys, once per token: 16 bytes a thread, neighbours in a row
+    const int vecs = p.rope / 8;
+    for (int u = u0; u < u1; ++u) {
+      const int tile = u / p.heads;
+      if (u != tile * p.heads) continue;                   // the CTA that has the tile's first head
+      const int4 d = __ldg(reinterpret_cast<const int4*>(p.tiles + tile));
+#pragma unroll 4
+      for (int x = tid - 320; x < kTile * vecs; x += 64) {
+        const int r = x / vecs, y = x - r * vecs, t = d.y + r;
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (t < d.z) {
+          int pg = p.kv.table[(size_t)d.x * p.kv.max_blocks + (t >> p.kv.page_shift)];
+          if (pg < 0 || pg >= p.kv.n_pages) pg = 0;
+          v = __ldg(reinterpret_cast<const uint4*>(p.kv.pages + p.kv.row_offset(p.layer, pg, t & (p.kv.page_tokens - 1)) +
+                                                   p.kv.rank) + y);
+        }
+        reinterpret_cast<uint4*>(p.r + ((size_t)tile * kTile + r) * p.rope)[y] = v;
+      }
+    }
   } else {
-    // ------------------------------------------------ epilogue: a thread owns a token row
-    const int quarter = warp & 3, r = quarter * 32 + lane;
+    // ------------------------------------------------ epilogue: a thread owns a token row and half the features
+    const int quarter = warp & 3, half = (warp - 2) >> 2, r = quarter * 32 + lane;
     const uint32_t lane_base = tmem + ((uint32_t)(quarter * 32) << 16);
-    int n = 0, b = 0, t = 0, len = 0;
+    const int c0 = half ? N / 64 * 32 : 0, c1 = half ? N : N / 64 * 32;      // its features, in blocks of 32
+    int n = 0;
+    uint32_t mask = 0;
     bool clamped = false;
     for (int u = u0; u < u1; ++u, ++n) {
       const int tile = u / p.heads, head = u - tile * p.heads, buf = n & 1;
-      const int row = tile * kTile + r;
       if (u == u0 || head == 0) {
-        b = seq_of_row(p, tile * kTile);
-        t = row - p.base[b];
-        len = seq_len(p, b);
-      }
-      const bool there = t < len;
-      if (head == 0 && p.rope) {                           // the rotary keys, once per token
-        const uint4* src = nullptr;
-        if (there) {
-          int pg = p.kv.table[(size_t)p.seqs[b] * p.kv.max_blocks + (t >> p.kv.page_shift)];
-          if (pg < 0 || pg >= p.kv.n_pages) pg = 0;
-          src = reinterpret_cast<const uint4*>(p.kv.pages + p.kv.row_offset(p.layer, pg, t & (p.kv.page_tokens - 1)) +
-                                               p.kv.rank);
-        }
-        for (int x = 0; x < p.rope / 8; ++x) {
-          *reinterpret_cast<uint4*>(p.r + (size_t)row * p.rope + 8 * x) = there ? src[x] : make_uint4(0, 0, 0, 0);
-        }
+        const int4 d = __ldg(reinterpret_cast<const int4*>(p.tiles + tile));
+        mask = d.y + r < d.z ? 0xFFFFFFFFu : 0u;                             // rows past the end: zeros
       }
       if (!warp_wait(&sh.d_full[buf], (n >> 1) & 1, abort_flag)) break;
       tc_fence_after();
-      const size_t at = (size_t)head * p.kv_rows + row;
+      const size_t at = (size_t)head * p.kv_rows + tile * kTile + r;
       uint32_t v[2][32];
       const uint32_t col = lane_base + buf * 256;
-      tmem_ld32(col, v[0]);
+      tmem_ld32(col + c0, v[0]);
 #pragma unroll
-      for (int c = 0; c < 8; ++c) {
-        if (32 * c >= N) break;
+      for (int i = 0; i < 4; ++i) {
+        const int c = c0 + 32 * i;
+        if (c >= c1) break;
         tmem_ld_wait();
-        if (32 * (c + 1) < N) tmem_ld32(col + 32 * (c + 1), v[(c + 1) & 1]);
+        if (c + 32 < c1) tmem_ld32(col + c + 32, v[(i + 1) & 1]);
+        const uint32_t(&x)[32] = v[i & 1];
         uint32_t o[16];
-        const bool key = 32 * c < p.dn;
+        void* dst;
+        if (c < p.dn) {
 #pragma unroll
-        for (int y = 0; y < 16; ++y) {
-          const float e0 = __uint_as_float(v[c & 1][2 * y]), e1 = __uint_as_float(v[c & 1][2 * y + 1]);
-          o[y] = !there ? 0u : key ? bf16x2_of(e0, e1) : half2_of(e0, e1, clamped);
+          for (int y = 0; y < 16; ++y) o[y] = bf16x2_of(__uint_as_float(x[2 * y]), __uint_as_float(x[2 * y + 1])) & mask;
+          dst = p.k + at * p.dn + c;
+        } else {
+          float big = 0.0f;
+#pragma unroll
+          for (int y = 0; y < 16; ++y) {
+            const float e0 = __uint_as_float(x[2 * y]), e1 = __uint_as_float(x[2 * y + 1]);
+            big = fmaxf(big, fmaxf(fabsf(e0), fabsf(e1)));
+            const __half2 h = __floats2half2_rn(e0, e1);
+            o[y] = *reinterpret_cast<const uint32_t*>(&h) & mask;
+          }
+          if ((big > 65504.0f) & (mask != 0u)) {
+#pragma unroll
+            for (int y = 0; y < 16; ++y) o[y] = half2_of(__uint_as_float(x[2 * y]), __uint_as_float(x[2 * y + 1]), clamped);
+          }
+          dst = p.v + at * p.dv + c - p.dn;
         }
-        void* dst = key ? (void*)(p.k + at * p.dn + 32 * c) : (void*)(p.v + at * p.dv + 32 * c - p.dn);
         st_sector(dst, o);
         st_sector((char*)dst + 32, o + 8);
       }
@@ -940,12 +972,12 @@ __global__ void __launch_bounds__(256) combine_splits_kernel(const PrefillParams
 
 // ---------------------------------------------------------------- host side
 struct PrefillWs {
-  size_t base, counts, blocks, k, v, r, part, ml, bytes;
+  size_t counts, blocks, tiles, k, v, r, part, ml, bytes;
   int rows, n_blocks, splits;
 };
 
 bool prefill_shape_ok(int B, int T, int heads, int dn, int dv, int kv_tokens) {
-  if ((dn != 64 && dn != 128) || (dv != 64 && dv != 128) || heads > 1024 || B > 4096) return false;
+  if ((dn != 64 && dn != 128) || (dv != 64 && dv != 128) || heads > 1024 || B > kMaxB) return false;
   return (long long)T * heads <= INT_MAX && ((long long)kv_tokens + 128LL * B) * heads <= INT_MAX;
 }
 
@@ -971,12 +1003,12 @@ PrefillWs prefill_ws(int B, int T, int heads, int dn, int dv, int rope, int kv_t
   w.rows = (kv_tokens + kRowAlign - 1) / kRowAlign * kRowAlign + kRowAlign * (B - 1);
   w.n_blocks = T / kBlock + B;
   size_t at = 0;
-  w.base = at;
-  at += align_up((size_t)(B + 1) * sizeof(int32_t), 256);
   w.counts = at;
   at += 256;
   w.blocks = at;
   at += align_up((size_t)w.n_blocks * sizeof(QBlock), 256);
+  w.tiles = at;
+  at += align_up((size_t)(w.rows / kRowAlign) * sizeof(TokTile), 256);
   w.k = at;
   at += align_up((size_t)heads * w.rows * dn * 2, 256);
   w.v = at;
@@ -1086,9 +1118,9 @@ int moe_latent_prefill(const moe_kv_cache* cache, int layer, const void* q, cons
   p.q_off = q_offsets;
   p.w = reinterpret_cast<const __nv_bfloat16*>(w_kv);
   p.out = reinterpret_cast<__nv_bfloat16*>(out);
-  p.base = reinterpret_cast<int32_t*>(b + w.base);
   p.counts = reinterpret_cast<int32_t*>(b + w.counts);
   p.blocks = reinterpret_cast<QBlock*>(b + w.blocks);
+  p.tiles = reinterpret_cast<TokTile*>(b + w.tiles);
   p.k = reinterpret_cast<__nv_bfloat16*>(b + w.k);
   p.v = reinterpret_cast<__half*>(b + w.v);
   p.r = reinterpret_cast<__nv_bfloat16*>(b + w.r);
