@@ -48,6 +48,7 @@ constexpr int kMaxSlots = 4;             // tiles in flight
 constexpr int kBatch = 512;              // sequences of one launch (lengths and tile sums in shared memory)
 constexpr int kThreads = 224;
 constexpr int kSoftThreads = 128;
+constexpr int kAhead = 3;                // tiles between a request to L2 and the copy to shared memory
 constexpr int kHead = 2;                 // tiles' worth of time that a piece costs beside its tiles
 constexpr int kTmemCols = 512;
 constexpr int kSCol = 256;               // S tiles at columns 256 and 320; O slices at 0, 64, 128, 192
@@ -350,6 +351,11 @@ decode_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_constant_
       // lane i: the pool row where box i of a tile begins; read one tile ahead
       auto block = [&](int t) { return seq_ok && lane < kTok / box && t < tok1 ? blocks[t >> p.kv.page_shift] : -1; };
       int ahead = block(tok0 + lane * box);
+      auto far_block = [&](int t) {
+        const int pg = block(t);
+        return pg < p.kv.n_pages ? pg : -1;
+      };
+      int far_t = tok0 + kAhead * kTok + lane * box, far_row = far_block(far_t);
       const int N = (int)uni(sg.N), row0 = (int)uni(sg.row0);
       // the queries follow the first tile: the tile's memory is free before the last piece's S lets go of its queries
       auto load_q = [&]() {
@@ -380,6 +386,12 @@ decode_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_constant_
           row = 0;
         }
         ahead = block(t + kTok);
+        // The two tiles that shared memory holds do not cover HBM's latency: tiles further on are asked into L2.  A box
+        // is one run of bytes in its page.
+        if (far_row >= 0 && far_t < tok1)
+          prefetch_l2(p.kv.pages + p.kv.row_offset(p.layer, far_row, far_t & (page - 1)), (uint32_t)(box * p.kv.row * 2));
+        far_t += kTok;
+        far_row = far_block(far_t);
         int rows[kTok / 16];
 #pragma unroll
         for (int i = 0; i < kTok / 16; ++i) rows[i] = (int)uni(lane == i ? row : 0);

@@ -33,6 +33,7 @@ constexpr int kTile = 128;               // tokens of a tile (and query rows of 
 constexpr int kChunkBytes = kTile * kBK * 2;   // 16 KB: 128 rows x 64 entries
 constexpr int kThreads = 384;            // warps 0..3: producer, MMA issuer, two idle; 4..7 and 8..11: softmax
 constexpr int kMaxSplits = 8;
+constexpr int kAhead = 4;                // tiles between a request to L2 and the copy to shared memory
 constexpr int kTmemCols = 512;
 constexpr float kGrow = 8.0f;            // log2 of the growth of a row's maximum that forces a rescaling
 
@@ -447,9 +448,9 @@ __device__ inline void tc_mma_ta_warp(uint32_t d_tmem, uint32_t a_tmem, uint64_t
 // fp32 accumulation, f16 operands, A and B K-major
 __host__ __device__ constexpr uint32_t idesc_f16(int M, int N) { return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24); }
 struct Shared {
-  uint64_t full[4], empty[4], r_full[2], r_empty[2];   // key and value tiles, rotary key tiles
+  uint64_t full[4], empty[4];                    // key (with their rotary part) and value tiles
   uint64_t q_full[2], q_empty[2];
-  uint64_t s_full[2], p_half[2], p_ready[2], o_full[2];   // p_half: the probabilities of the first 64 tokens
+  uint64_t s_full[2], p_ready[2], o_full[2];
   uint64_t w_full[2], w_empty[2];                // work items
   uint64_t drain;
   int item[2];
@@ -516,12 +517,9 @@ attend_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
       mbar_init(&sh.empty[i], 1);
     }
     for (int g = 0; g < 2; ++g) {
-      mbar_init(&sh.r_full[g], 1);
-      mbar_init(&sh.r_empty[g], 1);
       mbar_init(&sh.q_full[g], 1);
       mbar_init(&sh.q_empty[g], 1);
       mbar_init(&sh.s_full[g], 1);
-      mbar_init(&sh.p_half[g], 4);
       mbar_init(&sh.p_ready[g], 4);
       mbar_init(&sh.o_full[g], 1);
       mbar_init(&sh.w_full[g], 1);
@@ -560,37 +558,31 @@ attend_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
     if (warp == 0) {
       // ---------------------------------------------- work items and TMA
       const uint32_t smem0 = uni(smem_u32(smem));
-      const uint32_t full0 = uni(smem_u32(&sh.full[0])), rf = uni(smem_u32(&sh.r_full[0]));
+      const uint32_t full0 = uni(smem_u32(&sh.full[0]));
       const uint32_t qf = uni(smem_u32(&sh.q_full[0]));
       int n = 0, units = 0, slot = 0, ropes = 0, q_loads0 = 0, q_loads1 = 0;
       uint32_t par = 1;
       bool ok = true;
-      // `chunks` of 64 columns of 128 rows into the next place of the ring
-      auto load_unit = [&](const CUtensorMap* map, int chunks, int row) {
+      // `chunks` of 64 columns of 128 rows into the next place of the ring.  A key tile's rotary part goes into the
+      // buffer its last-but-one predecessor had, which is over before the ring's place is free.
+      auto load_unit = [&](const CUtensorMap* map, int chunks, int row, bool rope, int rope_row) {
         if (!ok) return;
         ok = warp_wait(&sh.empty[slot], par, abort_flag);
         if (!ok) return;
         ++units;
-        mbar_expect_tx_warp(full0 + 8 * slot, (uint32_t)(chunks * kChunkBytes));
+        mbar_expect_tx_warp(full0 + 8 * slot, (uint32_t)((chunks + (rope ? 1 : 0)) * kChunkBytes));
 #pragma unroll
         for (int c = 0; c < 2; ++c)
           if (c < chunks)
             tma_load_2d_warp(smem0 + A::kRing + slot * A::kUnit + c * kChunkBytes, map, full0 + 8 * slot, c * kBK, row);
+        if (rope)
+          tma_load_2d_warp(smem0 + A::kRope + (ropes++ & 1) * kChunkBytes, &map_r, full0 + 8 * slot, 0, rope_row);
         if (++slot == A::kUnits) {
           slot = 0;
           par ^= 1u;
         }
       };
-      auto load_k = [&](int head, int row) {
-        load_unit(&map_k, key_chunks, head * p.kv_rows + row);
-        if (!rope_chunk || !ok) return;
-        const int st = ropes & 1;
-        ok = warp_wait(&sh.r_empty[st], ((ropes >> 1) & 1) ^ 1u, abort_flag);
-        if (!ok) return;
-        ++ropes;
-        mbar_expect_tx_warp(rf + 8 * st, kChunkBytes);
-        tma_load_2d_warp(smem0 + A::kRope + st * kChunkBytes, &map_r, rf + 8 * st, 0, row);
-      };
+      auto load_k = [&](int head, int row) { load_unit(&map_k, key_chunks, head * p.kv_rows + row, rope_chunk != 0, row); };
       auto load_q = [&](int g, int& loads, int head, int row0) {
         ok = warp_wait(&sh.q_empty[g], (loads & 1) ^ 1u, abort_flag);
         if (!ok) return;
@@ -626,7 +618,15 @@ attend_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
         if (ok && tiles) load_k(head, base);
         if (ok && tb) load_q(1, q_loads1, head, row0);
         for (int i = 0; i < tiles && ok; ++i) {
-          load_unit(&map_v, VC, head * p.kv_rows + base + i * kTile);
+          // Query blocks of a head pass its tokens side by side, so each tile would come from HBM for all of them at once:
+          // one block in eight, another for each tile, asks for a tile ahead of time.
+          const int far = i + kAhead;
+          if (far < tiles && (far + it.block) % min(8, n_blocks) == 0) {
+            const size_t row = (size_t)head * p.kv_rows + base + far * kTile;
+            prefetch_l2_warp(p.k + row * p.dn, (uint32_t)(kTile * p.dn * 2));
+            prefetch_l2_warp(p.v + row * p.dv, (uint32_t)(kTile * p.dv * 2));
+          }
+          load_unit(&map_v, VC, head * p.kv_rows + base + i * kTile, false, 0);
           if (ok && i + 1 < tiles) load_k(head, base + (i + 1) * kTile);
         }
         if (!ok) break;
@@ -638,10 +638,6 @@ attend_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
       for (int i = 0; i < A::kUnits; ++i) {
         const int loads = units / A::kUnits + (units % A::kUnits > i ? 1 : 0);
         if (loads > 0) mbar_wait(&sh.full[i], (loads - 1) & 1, &no_abort);
-      }
-      for (int i = 0; i < 2; ++i) {
-        const int loads = (ropes + 1 - i) / 2;
-        if (loads > 0) mbar_wait(&sh.r_full[i], (loads - 1) & 1, &no_abort);
       }
       __syncwarp();
     } else if (warp == 1) {
@@ -655,24 +651,14 @@ attend_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
       constexpr int KN = KC < 2 ? KC : 2;      // key chunks at most
       const int rope_steps = (int)uni(p.rope / kUK);
       int n = 0, ropes = 0, q_uses0 = 0, q_uses1 = 0, p_uses0 = 0, p_uses1 = 0;
-      int slot = 0, slot2 = 1;                 // the ring's next tile and the one behind it
-      uint32_t par = 0, par2 = 0;
+      int slot = 0;                            // the ring's next tile
+      uint32_t par = 0;
       bool issued = false, ok = true;
-      auto advance = [&]() {                   // the next tile is done with: its place is free once the products are over
-        tc_commit_warp(&sh.empty[slot]);
-        slot = slot2;
-        par = par2;
-        if (++slot2 == A::kUnits) {
-          slot2 = 0;
-          par2 ^= 1u;
+      auto step = [&](int& at, uint32_t& parity) {
+        if (++at == A::kUnits) {
+          at = 0;
+          parity ^= 1u;
         }
-      };
-      auto wait_k = [&](int at, uint32_t parity) {
-        ok = warp_wait(&sh.full[at], parity, abort_flag);
-        if (ok && rope_chunk) ok = warp_wait(&sh.r_full[ropes & 1], (ropes >> 1) & 1, abort_flag);
-      };
-      auto free_rope = [&]() {
-        if (rope_chunk) tc_commit_warp(&sh.r_empty[ropes++ & 1]);
       };
       auto issue_s = [&](int g, int at) {
         const uint64_t dq = dq0 + (uint64_t)((g * A::kQ) >> 4), dk = dk0 + (uint64_t)((at * A::kUnit) >> 4);
@@ -692,14 +678,11 @@ attend_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
         tc_commit_warp(&sh.s_full[g]);
         issued = true;
       };
-      // half of a value product: 64 tokens
-      auto issue_pv = [&](int g, int half, uint32_t acc) {
-        const uint64_t dv = dv0 + (uint64_t)((slot * A::kUnit) >> 4);
+      auto issue_pv = [&](int g, int at, uint32_t acc) {
+        const uint64_t dv = dv0 + (uint64_t)((at * A::kUnit) >> 4);
 #pragma unroll
-        for (int y = 0; y < 4; ++y) {
-          const int x = 4 * half + y;
+        for (int x = 0; x < kTile / kUK; ++x)
           tc_mma_ta_warp(tm + 256 + g * kTile, tm + g * kTile + x * 8, dv + ((x * kUK * 128) >> 4), idesc_v, x ? 1u : acc);
-        }
       };
       for (;;) {
         ok = warp_wait(&sh.w_full[n & 1], (n >> 1) & 1, abort_flag);
@@ -711,7 +694,7 @@ attend_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
         if (!__any_sync(0xffffffffu, get_item(p, k, n_blocks, group, it))) break;
         const int ta = (int)uni(it.tiles[0]), tb = (int)uni(it.tiles[1]), tiles = max(ta, tb);
         if (!tiles) continue;
-        wait_k(slot, par);
+        ok = warp_wait(&sh.full[slot], par, abort_flag);
         if (!ok) break;
         if (ta) {
           ok = warp_wait(&sh.q_full[0], q_uses0 & 1, abort_flag);
@@ -729,44 +712,60 @@ attend_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
           issue_s(1, slot);
           if (tb == 1) tc_commit_warp(&sh.q_empty[1]);
         }
-        advance();
-        free_rope();
+        tc_commit_warp(&sh.empty[slot]);
+        step(slot, par);
+        ++ropes;
+        ok = warp_wait(&sh.full[slot], par, abort_flag);       // V(0)
+        if (!ok) break;
+        // The products' queue is short (a few instructions): between two groups of them the fewest waits and commits
+        // are left, the others stand behind a group that is still being worked off.  Tile b sees at least what a sees.
         for (int i = 0; i < tiles; ++i) {
           const uint32_t acc = i ? 1u : 0u;
-          bool have_v = false, have_k = false;
-          // both tiles of the step; a tile that sees fewer tokens ends earlier
-          auto tile_step = [&](int g, int t, int& p_uses) {
-            if (i >= t || !ok) return;
-            ok = warp_wait(&sh.p_half[g], p_uses & 1, abort_flag);
-            if (ok && !have_v) ok = warp_wait(&sh.full[slot], par, abort_flag);
-            if (!ok) return;
-            have_v = true;
+          const bool more = i + 1 < tiles;
+          int sk = slot;                                       // K(i+1)
+          uint32_t pk = par;
+          step(sk, pk);
+          if (i < ta) {
+            ok = warp_wait(&sh.p_ready[0], p_uses0++ & 1, abort_flag);
+            if (!ok) break;
             tc_fence_after();
-            issue_pv(g, 0, acc);
-            ok = warp_wait(&sh.p_ready[g], p_uses & 1, abort_flag);
-            if (!ok) return;
-            ++p_uses;
-            tc_fence_after();
-            issue_pv(g, 1, 1u);
-            if (i + 1 == t) {
-              tc_commit_warp(&sh.o_full[g]);
-              return;
-            }
-            if (!have_k) wait_k(slot2, par2);
-            if (!ok) return;
-            have_k = true;
-            tc_fence_after();
-            issue_s(g, slot2);
-            if (i + 2 == t) tc_commit_warp(&sh.q_empty[g]);
-          };
-          tile_step(0, ta, p_uses0);
-          tile_step(1, tb, p_uses1);
-          if (!ok) break;
-          advance();
-          if (i + 1 < tiles) {
-            advance();
-            free_rope();
+            issue_pv(0, slot, acc);
+            if (i + 1 == ta) tc_commit_warp(&sh.o_full[0]);
+            if (!tb) tc_commit_warp(&sh.empty[slot]);
           }
+          if (more) {
+            ok = warp_wait(&sh.full[sk], pk, abort_flag);
+            if (!ok) break;
+            tc_fence_after();
+          }
+          if (i + 1 < ta) {
+            issue_s(0, sk);
+            if (i + 2 == ta) tc_commit_warp(&sh.q_empty[0]);
+          }
+          if (i < tb) {
+            ok = warp_wait(&sh.p_ready[1], p_uses1++ & 1, abort_flag);
+            if (!ok) break;
+            tc_fence_after();
+            issue_pv(1, slot, acc);
+            if (i + 1 == tb) tc_commit_warp(&sh.o_full[1]);
+            tc_commit_warp(&sh.empty[slot]);
+          }
+          slot = sk;
+          par = pk;
+          step(slot, par);                                     // V(i+1)
+          if (!more) {
+            slot = sk;                                         // there is no K(i+1): the next item's keys
+            par = pk;
+            break;
+          }
+          ok = warp_wait(&sh.full[slot], par, abort_flag);
+          if (!ok) break;
+          if (i + 1 < tb) {
+            issue_s(1, sk);
+            if (i + 2 == tb) tc_commit_warp(&sh.q_empty[1]);
+          }
+          tc_commit_warp(&sh.empty[sk]);
+          ++ropes;
         }
         if (!ok) break;
       }
@@ -875,13 +874,11 @@ attend_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
             pk[j] = *reinterpret_cast<const uint32_t*>(&h);
           }
           tmem_st16(s_col + 16 * c, pk);
-          if (c & 1) {   // the value product of 64 tokens starts while the other 64 are still in the making
-            tmem_st_wait();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(c == 1 ? &sh.p_half[g] : &sh.p_ready[g]);
-          }
         }
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.p_ready[g]);
         l += (sum0.x + sum0.y) + (sum1.x + sum1.y);
       }
       if (!ok) break;
