@@ -48,7 +48,6 @@ constexpr int kMaxSlots = 4;             // tiles in flight
 constexpr int kBatch = 512;              // sequences of one launch (lengths and tile sums in shared memory)
 constexpr int kThreads = 224;
 constexpr int kSoftThreads = 128;
-constexpr int kAhead = 3;                // tiles between a request to L2 and the copy to shared memory
 constexpr int kHead = 2;                 // tiles' worth of time that a piece costs beside its tiles
 constexpr int kTmemCols = 512;
 constexpr int kSCol = 256;               // S tiles at columns 256 and 320; O slices at 0, 64, 128, 192
@@ -248,8 +247,9 @@ struct Shared {
 
 __global__ void __launch_bounds__(kThreads, 1)
 decode_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_constant__ CUtensorMap map_pair,
-              const __grid_constant__ CUtensorMap map_q16,
-              const __grid_constant__ CUtensorMap map_q64, const DecodeParams p) {
+              const __grid_constant__ CUtensorMap map_qs, const __grid_constant__ CUtensorMap map_qsr,
+              const __grid_constant__ CUtensorMap map_qp, const __grid_constant__ CUtensorMap map_qpr,
+              const DecodeParams p) {
   extern __shared__ uint8_t smem_raw[];
   __shared__ Shared sh;
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -257,6 +257,9 @@ decode_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_constant_
   const int chunks = 2 * p.pairs + 1;               // the last one holds the rotary part, then P
   uint8_t* skv = smem + chunks * kChunk;
   const int slot_bytes = chunks * kChunk;
+  // A tile comes and goes in these parts: the value product lets go of one pair after the other, and the next tile's
+  // copies follow at once (two parts a tile instead of five measured 13% to 20% slower on long sequences).
+  const int parts = p.pairs + (p.rope ? 1 : 0);
 
   if (tid == 0) {
     for (int s = 0; s < p.slots; ++s)
@@ -279,8 +282,8 @@ decode_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_constant_
   if (tid == 32 * 2) {
     prefetch_map(&map_kv);
     prefetch_map(&map_pair);
-    prefetch_map(&map_q16);
-    prefetch_map(&map_q64);
+    prefetch_map(&map_qs);
+    prefetch_map(&map_qsr);
   }
   if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&sh.tmem)),
@@ -351,23 +354,18 @@ decode_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_constant_
       // lane i: the pool row where box i of a tile begins; read one tile ahead
       auto block = [&](int t) { return seq_ok && lane < kTok / box && t < tok1 ? blocks[t >> p.kv.page_shift] : -1; };
       int ahead = block(tok0 + lane * box);
-      auto far_block = [&](int t) {
-        const int pg = block(t);
-        return pg < p.kv.n_pages ? pg : -1;
-      };
-      int far_t = tok0 + kAhead * kTok + lane * box, far_row = far_block(far_t);
-      const int N = (int)uni(sg.N), row0 = (int)uni(sg.row0);
+      const int row0 = (int)uni(sg.row0);
       // the queries follow the first tile: the tile's memory is free before the last piece's S lets go of its queries
       auto load_q = [&]() {
         if (!warp_wait(&sh.q_empty, (nseg & 1) ^ 1u, abort_flag)) return false;
-        mbar_expect_tx_warp(qbar, (uint32_t)(cq * N * 128));
+        // the tile's rows, chunk behind chunk of box rows (rows past the tile's are read and not used)
+        const CUtensorMap* mq = sg.prefix ? &map_qp : &map_qs;
+        const CUtensorMap* mr = sg.prefix ? &map_qpr : &map_qsr;
+        const int q_rows = sg.prefix ? p.NRp : p.NR;
+        mbar_expect_tx_warp(qbar, (uint32_t)(cq * q_rows * 128));
         ++nseg;
-        for (int c = 0; c < cq; ++c) {
-          if (N == kRows) tma_load_2d_warp(smem0 + c * kChunk, &map_q64, qbar, c * kBK, row0);
-          else
-            for (int r = 0; r < N; r += 16)
-              tma_load_2d_warp(smem0 + c * kChunk + r * 128, &map_q16, qbar, c * kBK, row0 + r);
-        }
+        tma_load_3d_hint_warp(smem0, mq, qbar, 0, row0, 0, shared);
+        if (p.rope) tma_load_2d_warp(smem0 + 2 * p.pairs * q_rows * 128, mr, qbar, p.kv.rank, row0);
         return true;
       };
       const bool q_first = nseg == 0;
@@ -386,41 +384,25 @@ decode_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_constant_
           row = 0;
         }
         ahead = block(t + kTok);
-        // The two tiles that shared memory holds do not cover HBM's latency: tiles further on are asked into L2.  A box
-        // is one run of bytes in its page.
-        if (far_row >= 0 && far_t < tok1)
-          prefetch_l2(p.kv.pages + p.kv.row_offset(p.layer, far_row, far_t & (page - 1)), (uint32_t)(box * p.kv.row * 2));
-        far_t += kTok;
-        far_row = far_block(far_t);
         int rows[kTok / 16];
 #pragma unroll
         for (int i = 0; i < kTok / 16; ++i) rows[i] = (int)uni(lane == i ? row : 0);
         const uint32_t dst = kv0 + slot * slot_bytes, bar = full0 + slot * (uint32_t)sizeof(sh.full[0]);
-        for (int j = 0; j < p.pairs; ++j) {
+        for (int j = 0; j < parts; ++j) {
           ok = warp_wait(&sh.empty[slot][j], par, abort_flag);
           if (!ok) break;
-          mbar_expect_tx_warp(bar + 8 * j, (uint32_t)(nb * box * 256));
-          if (box == kTok) {   // both chunks of the pair in one copy
-            tma_load_3d_hint_warp(dst + 2 * j * kChunk, &map_pair, bar + 8 * j, 0, rows[0], 2 * j, pol);
+          const bool pair = j < p.pairs;
+          const uint32_t to = dst + 2 * j * kChunk, fb = bar + 8 * j;
+          mbar_expect_tx_warp(fb, (uint32_t)(nb * box * (pair ? 256 : 128)));
+          if (box == kTok && pair) {   // both chunks of the pair in one copy
+            tma_load_3d_hint_warp(to, &map_pair, fb, 0, rows[0], 2 * j, pol);
           } else {
 #pragma unroll
             for (int i = 0; i < kTok / 16; ++i)
               if (i < nb) {
-                tma_load_2d_hint_warp(dst + 2 * j * kChunk + i * box * 128, &map_kv, bar + 8 * j, 2 * j * kBK, rows[i], pol);
-                tma_load_2d_hint_warp(dst + (2 * j + 1) * kChunk + i * box * 128, &map_kv, bar + 8 * j,
-                                      2 * j * kBK + kBK, rows[i], pol);
+                tma_load_2d_hint_warp(to + i * box * 128, &map_kv, fb, 2 * j * kBK, rows[i], pol);
+                if (pair) tma_load_2d_hint_warp(to + kChunk + i * box * 128, &map_kv, fb, 2 * j * kBK + kBK, rows[i], pol);
               }
-          }
-        }
-        if (ok && p.rope) {
-          const int j = p.pairs;
-          ok = warp_wait(&sh.empty[slot][j], par, abort_flag);
-          if (ok) {
-            mbar_expect_tx_warp(bar + 8 * j, (uint32_t)(nb * box * 128));
-#pragma unroll
-            for (int i = 0; i < kTok / 16; ++i)
-              if (i < nb)
-                tma_load_2d_hint_warp(dst + 2 * j * kChunk + i * box * 128, &map_kv, bar + 8 * j, 2 * j * kBK, rows[i], pol);
           }
         }
         if (ok && t0 == tok0 && !q_first) ok = load_q();
@@ -438,10 +420,8 @@ decode_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_constant_
     if (nseg) mbar_wait(&sh.q_full, (nseg - 1) & 1, &no_abort);
     for (int s = 0; s < p.slots; ++s) {
       const int loads = tile / p.slots + (tile % p.slots > s ? 1 : 0);
-      for (int j = 0; j <= p.pairs; ++j) {
-        if (j == p.pairs && p.rope == 0) break;
+      for (int j = 0; j < parts; ++j)
         if (loads > 0) mbar_wait(&sh.full[s][j], (loads - 1) & 1, &no_abort);
-      }
     }
     __syncwarp();
   } else if (warp == 1) {
@@ -456,6 +436,7 @@ decode_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_constant_
     while (__any_sync(0xffffffffu, ok && it.next(sg))) {
       ok = warp_wait(&sh.q_full, nseg & 1, abort_flag);
       const int n_tiles = (int)uni((sg.tok1 - sg.tok0 + kTok - 1) / kTok);
+      const uint64_t q_step = (uint64_t)((uni(sg.prefix ? p.NRp : p.NR) * 128) >> 4);   // from one chunk of the queries to the next
       for (int i = 0; ok && i < n_tiles; ++i, ++tile) {
         const int buf = tile & 1;
         ok = warp_wait(&sh.s_empty[buf], ((tile >> 1) & 1) ^ 1u, abort_flag);
@@ -467,12 +448,11 @@ decode_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_constant_
           if (!ok) break;
           tc_fence_after();
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const uint64_t off = ((k >> 2) * kChunk + (k & 3) * kUK * 2) >> 4;
-            tc_mma_warp(d, dq + off, dk + off, idesc_s, k ? 1u : (j ? 1u : 0u));
-          }
+          for (int k = 0; k < 8; ++k)
+            tc_mma_warp(d, dq + ((k & 3) * kUK * 2 >> 4) + (k >> 2) * q_step,
+                        dk + (((k >> 2) * kChunk + (k & 3) * kUK * 2) >> 4), idesc_s, k ? 1u : (j ? 1u : 0u));
           issued = true;
-          dq += (2 * kChunk) >> 4;
+          dq += 2 * q_step;
           dk += (2 * kChunk) >> 4;
         }
         if (ok && p.rope) {
@@ -901,17 +881,23 @@ int launch_decode(const moe_kv_cache& c, DecodeParams p, const void* q, cudaStre
   p.slots = (int)((227 * 1024 - sizeof(Shared) - 1024 - slot) / slot);   // what the query tile leaves
   if (p.slots > kMaxSlots) p.slots = kMaxSlots;
   const int smem = (1 + p.slots) * slot + 1024;
-  CUtensorMap kv, pair, q16, q64;
+  CUtensorMap kv, pair, qs, qsr, qp, qpr;   // cache rows by chunk and by pair; query tiles of sequences and of the prefix
   const uint64_t rows = (uint64_t)c.n_layers * c.n_pages * c.page_tokens, qrows = (uint64_t)p.B * p.Q * p.heads;
   if (!make_map(&kv, c.pages, row, rows, c.page_tokens < kTok ? c.page_tokens : kTok) ||
-      !make_map_chunks(&pair, c.pages, row, rows, kTok, 2) || !make_map(&q16, q, row, qrows, 16) || !make_map(&q64, q, row, qrows, 64))
+      !make_map_chunks(&pair, c.pages, row, rows, kTok, 2) || !make_map_chunks(&qs, q, row, qrows, p.NR, 2 * p.pairs) ||
+      !make_map(&qsr, q, row, qrows, p.NR))
+    return MOE_ERR_CUDA;
+  qp = qs;
+  qpr = qsr;
+  if (p.np && p.NRp != p.NR &&
+      (!make_map_chunks(&qp, q, row, qrows, p.NRp, 2 * p.pairs) || !make_map(&qpr, q, row, qrows, p.NRp)))
     return MOE_ERR_CUDA;
   static std::atomic<unsigned char> attr[kMaxDevices];
   cudaError_t e = once_per_device(attr, [] {
     return cudaFuncSetAttribute(decode_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 227 * 1024 - (int)sizeof(Shared));
   });
-  if (e == cudaSuccess) e = launch_k(decode_kernel, p.ctas, kThreads, smem, s, kv, pair, q16, q64, p);
+  if (e == cudaSuccess) e = launch_k(decode_kernel, p.ctas, kThreads, smem, s, kv, pair, qs, qsr, qp, qpr, p);
   // 4 sets of warps a row while the rows alone do not fill the SMs (then a row has many pieces)
   if (e == cudaSuccess)
     e = qrows <= 4ull * p.ctas ? launch_k(combine_parts_kernel<4>, (unsigned)qrows, 512, 0, s, p)

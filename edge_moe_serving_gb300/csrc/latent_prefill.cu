@@ -33,7 +33,6 @@ constexpr int kTile = 128;               // tokens of a tile (and query rows of 
 constexpr int kChunkBytes = kTile * kBK * 2;   // 16 KB: 128 rows x 64 entries
 constexpr int kThreads = 384;            // warps 0..3: producer, MMA issuer, two idle; 4..7 and 8..11: softmax
 constexpr int kMaxSplits = 8;
-constexpr int kAhead = 4;                // tiles between a request to L2 and the copy to shared memory
 constexpr int kTmemCols = 512;
 constexpr float kGrow = 8.0f;            // log2 of the growth of a row's maximum that forces a rescaling
 
@@ -618,14 +617,6 @@ attend_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
         if (ok && tiles) load_k(head, base);
         if (ok && tb) load_q(1, q_loads1, head, row0);
         for (int i = 0; i < tiles && ok; ++i) {
-          // Query blocks of a head pass its tokens side by side, so each tile would come from HBM for all of them at once:
-          // one block in eight, another for each tile, asks for a tile ahead of time.
-          const int far = i + kAhead;
-          if (far < tiles && (far + it.block) % min(8, n_blocks) == 0) {
-            const size_t row = (size_t)head * p.kv_rows + base + far * kTile;
-            prefetch_l2_warp(p.k + row * p.dn, (uint32_t)(kTile * p.dn * 2));
-            prefetch_l2_warp(p.v + row * p.dv, (uint32_t)(kTile * p.dv * 2));
-          }
           load_unit(&map_v, VC, head * p.kv_rows + base + i * kTile, false, 0);
           if (ok && i + 1 < tiles) load_k(head, base + (i + 1) * kTile);
         }
