@@ -711,42 +711,42 @@ decode_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_constant_
 
 // ---------------------------------------------------------------- combine
 // Per query row: its pieces' (m, l, O) in a fixed order (the prefix's pieces,
-// then the sequence's).  rank / 128 warps cover a row, 128 entries each, and
-// find the pieces and their weights on their own (lane k looks after piece k);
-// with GROUPS > 1 as many sets of warps share the pieces out (few query rows,
-// so many pieces each) and meet in shared memory.  Three dependent reads deep
-// (tile sums, statistics, rows); bound by those at small sizes and by L2 at
-// large ones.
-template <int GROUPS>
-__global__ void __launch_bounds__(128 * GROUPS)
-combine_parts_kernel(const DecodeParams p) {
-  __shared__ float4 s_acc[GROUPS > 1 ? 128 * GROUPS : 1];
-  pdl_wait();
-  pdl_trigger();
-  const int row = blockIdx.x, rank = p.kv.rank, lane = threadIdx.x & 31;
-  const int per_seq = p.Q * p.heads, b = row / per_seq, in_seq = row - b * per_seq, g = in_seq / p.NR;
-  const int total = p.plan[p.B], x0 = p.plan[b], x1 = p.plan[b + 1];
-  const int per = per_cta(total, p.teams);
-  const int t0 = x1 > x0 ? (x0 + kHead) / per : 0, t1 = x1 > x0 ? (x1 - 1) / per : -1;   // from its first tile on
-  const int n_s = t1 - t0 + 1;
-  int n_p = 0, c0 = 0, pr = 0;
-  long long pa = 0, pp = 1;
-  if (p.np) {
-    pp = p.per_p;
-    pr = row / p.NRp;
-    pa = (long long)pr * p.np;
-    c0 = (int)(pa / pp);
-    const long long c1 = (pa + p.np - 1) / pp;
-    n_p = (int)c1 - c0 + 1;
-  } else if (n_s == 1) {
-    return;   // written by decode_kernel
+// then the sequence's).  Three dependent reads deep (tile sums, statistics,
+// rows); bound by those at small sizes and by L2 at large ones.
+//
+// Where a row's pieces lie: lane k of a warp looks after piece k.
+struct Pieces {
+  const DecodeParams& p;
+  int row, b, in_seq, g, x0, x1, per, t0, n_p, n, c0, pr;
+  long long pa;
+
+  __device__ Pieces(const DecodeParams& p_, int row_) : p(p_), row(row_) {
+    const int per_seq = p.Q * p.heads;
+    b = row / per_seq;
+    in_seq = row - b * per_seq;
+    g = in_seq / p.NR;
+    const int total = p.plan[p.B];
+    x0 = p.plan[b];
+    x1 = p.plan[b + 1];
+    per = per_cta(total, p.teams);
+    t0 = x1 > x0 ? (x0 + kHead) / per : 0;                    // from its first tile on
+    const int n_s = (x1 > x0 ? (x1 - 1) / per : -1) - t0 + 1;
+    n_p = c0 = pr = 0;
+    pa = 0;
+    if (p.np) {
+      pr = row / p.NRp;
+      pa = (long long)pr * p.np;
+      c0 = (int)(pa / p.per_p);
+      n_p = (int)((pa + p.np - 1) / p.per_p) - c0 + 1;
+    }
+    n = n_p + n_s;
   }
-  const int n = n_p + n_s;
-  // where piece k of this row lies: its index among all rows of its line's pieces
-  auto place = [&](int k) {
+  __device__ bool direct() const { return n_p == 0 && n == 1; }   // written by decode_kernel
+  // piece k's index among all rows of its line's pieces
+  __device__ size_t place(int k) const {
     if (k < n_p) {
-      const long long from = (long long)(c0 + k) * pp;
-      const int slot = (pa >= from && pa + p.np <= from + pp) ? 2 * p.ctas + pr : 2 * (c0 + k) + (pa > from ? 1 : 0);
+      const long long from = (long long)(c0 + k) * p.per_p;
+      const int slot = (pa >= from && pa + p.np <= from + p.per_p) ? 2 * p.ctas + pr : 2 * (c0 + k) + (pa > from ? 1 : 0);
       return (size_t)slot * p.NRp + (row - pr * p.NRp);
     }
     const int t = t0 + k - n_p;
@@ -754,71 +754,128 @@ combine_parts_kernel(const DecodeParams p) {
     const int slot = (x0 + kHead >= from && x1 <= from + per) ? 2 * p.teams * p.G + b * p.G + g
                                                               : 2 * (t * p.G + g) + (x0 > from ? 1 : 0);
     return (size_t)slot * p.NR + (in_seq - g * p.NR);
-  };
-  float top = -INFINITY, l = 0.0f, lr = 0.0f;
-  for (int k = lane; k < n; k += 32) {
-    const float4 ml = (k < n_p ? p.ml_p : p.ml_s)[place(k)];
-    const float now = fmaxf(top, ml.x), ref = now == -INFINITY ? 0.0f : now;
-    const float f = ex2(top - ref), w = ex2(ml.x - ref);
+  }
+  __device__ float4 stats(int k, size_t at) const { return (k < n_p ? p.ml_p : p.ml_s)[at]; }
+  __device__ const float* values(int k, size_t at) const { return (k < n_p ? p.part_p : p.part_s) + at * p.kv.rank; }
+};
+
+// The row's reference maximum and its two sums over all pieces, in every lane.
+__device__ inline void join_stats(const Pieces& q, int lane, float& ref, float& l, float& lr) {
+  float top = -INFINITY;
+  l = lr = 0.0f;
+  for (int k = lane; k < q.n; k += 32) {
+    const float4 ml = q.stats(k, q.place(k));
+    const float now = fmaxf(top, ml.x), to = now == -INFINITY ? 0.0f : now;
+    const float f = ex2(top - to), w = ex2(ml.x - to);
     l = fmaf(l, f, ml.y * w);
     lr = fmaf(lr, f, ml.z * w);
     top = now;
   }
-  const float all = warp_max(top), ref = all == -INFINITY ? 0.0f : all;
+  const float all = warp_max(top);
+  ref = all == -INFINITY ? 0.0f : all;
   const float f = ex2(top - ref);
   l = warp_sum(l * f);
   lr = warp_sum(lr * f);
-  const int v = threadIdx.x % 128, grp = threadIdx.x / 128;   // float4 of the row; set of warps
+}
+
+__device__ inline void add_scaled(float4& acc, float w, const float4& x) {
+  acc.x = fmaf(w, x.x, acc.x);
+  acc.y = fmaf(w, x.y, acc.y);
+  acc.z = fmaf(w, x.z, acc.z);
+  acc.w = fmaf(w, x.w, acc.w);
+}
+
+__device__ inline void store_row(const DecodeParams& p, int row, int v, const float4& acc, float lr) {
+  const float inv = lr == 0.0f ? 0.0f : 1.0f / lr;
+  const __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x * inv, acc.y * inv);
+  const __nv_bfloat162 hi = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
+  uint2 packed;
+  packed.x = *reinterpret_cast<const uint32_t*>(&lo);
+  packed.y = *reinterpret_cast<const uint32_t*>(&hi);
+  reinterpret_cast<uint2*>(p.out + (size_t)row * p.kv.rank)[v] = packed;
+}
+
+__device__ inline void store_lse(const DecodeParams& p, int row, float ref, float l) {
+  if (p.lse) p.lse[row] = l == 0.0f ? -INFINITY : (ref + log2f(l)) * 0.6931471805599453f;
+}
+
+// Many rows: a warp a row, up to 4 float4 a lane, four pieces in flight.
+__global__ void __launch_bounds__(128) combine_rows_kernel(const DecodeParams p, int rows) {
+  pdl_wait();
+  pdl_trigger();
+  const int row = blockIdx.x * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31, vecs = p.kv.rank / 128;
+  if (row >= rows) return;
+  const Pieces q(p, row);
+  if (q.direct()) return;
+  float ref, l, lr;
+  join_stats(q, lane, ref, l, lr);
+  float4 acc[4];
+#pragma unroll
+  for (int y = 0; y < 4; ++y) acc[y] = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int k0 = 0; k0 < q.n; k0 += 4) {
+    float4 x[4][4];
+    float w[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int k = min(k0 + j, q.n - 1);
+      const size_t at = q.place(k);
+      w[j] = k0 + j < q.n ? ex2(q.stats(k, at).x - ref) : 0.0f;
+      const float4* from = reinterpret_cast<const float4*>(q.values(k, at)) + lane;
+#pragma unroll
+      for (int y = 0; y < 4; ++y)
+        if (y < vecs && k0 + j < q.n) x[j][y] = __ldcs(from + 32 * y);
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int y = 0; y < 4; ++y)
+        if (y < vecs && k0 + j < q.n) add_scaled(acc[y], w[j], x[j][y]);
+  }
+#pragma unroll
+  for (int y = 0; y < 4; ++y)
+    if (y < vecs) store_row(p, row, lane + 32 * y, acc[y], lr);
+  if (lane == 0) store_lse(p, row, ref, l);
+}
+
+// Few rows, many pieces each: a CTA a row, rank / 128 warps across it and four sets of them over the pieces, which
+// meet in shared memory.
+constexpr int kSets = 4;
+__global__ void __launch_bounds__(128 * kSets) combine_parts_kernel(const DecodeParams p) {
+  __shared__ float4 s_acc[128 * kSets];
+  pdl_wait();
+  pdl_trigger();
+  const int row = blockIdx.x, lane = threadIdx.x & 31;
+  const Pieces q(p, row);
+  if (q.direct()) return;
+  float ref, l, lr;
+  join_stats(q, lane, ref, l, lr);
+  const int v = threadIdx.x % 128, set = threadIdx.x / 128;   // float4 of the row; set of warps
+  const bool mine = 4 * v < p.kv.rank;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int k0 = 0; k0 < n; k0 += 32) {
-    const int mine = k0 + lane;
-    const size_t at = mine < n ? place(mine) : 0;
-    const float w_mine = mine < n ? ex2((mine < n_p ? p.ml_p : p.ml_s)[at].x - ref) : 0.0f;
-    const int m = min(32, n - k0);
-    for (int kb = grp; kb < m; kb += 8 * GROUPS) {   // eight reads in flight
-      float4 x[8];
-      float w[8];
+  for (int k0 = set; k0 < q.n; k0 += 8 * kSets) {   // eight reads in flight
+    float4 x[8];
+    float w[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int k = kb + j * GROUPS;
-        const size_t a = __shfl_sync(0xffffffffu, at, k & 31);
-        w[j] = __shfl_sync(0xffffffffu, w_mine, k & 31);
-        x[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (k < m && 4 * v < rank)
-          x[j] = __ldcs(reinterpret_cast<const float4*>((k0 + k < n_p ? p.part_p : p.part_s) + a * rank) + v);
-      }
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        if (kb + j * GROUPS >= m) break;
-        acc.x = fmaf(w[j], x[j].x, acc.x);
-        acc.y = fmaf(w[j], x[j].y, acc.y);
-        acc.z = fmaf(w[j], x[j].z, acc.z);
-        acc.w = fmaf(w[j], x[j].w, acc.w);
+    for (int j = 0; j < 8; ++j) {
+      const int k = k0 + j * kSets;
+      x[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+      w[j] = 0.0f;
+      if (k < q.n && mine) {
+        const size_t at = q.place(k);
+        x[j] = __ldcs(reinterpret_cast<const float4*>(q.values(k, at)) + v);
+        w[j] = ex2(q.stats(k, at).x - ref);
       }
     }
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (k0 + j * kSets < q.n) add_scaled(acc, w[j], x[j]);
   }
-  if (GROUPS > 1) {
-    s_acc[threadIdx.x] = acc;
-    __syncthreads();
-    if (grp > 0) return;
-    for (int q = 1; q < GROUPS; ++q) {
-      const float4 x = s_acc[q * 128 + v];
-      acc.x += x.x;
-      acc.y += x.y;
-      acc.z += x.z;
-      acc.w += x.w;
-    }
-  }
-  if (4 * v < rank) {
-    const float inv = lr == 0.0f ? 0.0f : 1.0f / lr;
-    const __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x * inv, acc.y * inv);
-    const __nv_bfloat162 hi = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
-    uint2 packed;
-    packed.x = *reinterpret_cast<const uint32_t*>(&lo);
-    packed.y = *reinterpret_cast<const uint32_t*>(&hi);
-    reinterpret_cast<uint2*>(p.out + (size_t)row * rank)[v] = packed;
-  }
-  if (p.lse && threadIdx.x == 0) p.lse[row] = l == 0.0f ? -INFINITY : (ref + log2f(l)) * 0.6931471805599453f;
+  s_acc[threadIdx.x] = acc;
+  __syncthreads();
+  if (set > 0 || !mine) return;
+  for (int i = 1; i < kSets; ++i) add_scaled(acc, 1.0f, s_acc[i * 128 + v]);
+  store_row(p, row, v, acc, lr);
+  if (threadIdx.x == 0) store_lse(p, row, ref, l);
 }
 
 // ---------------------------------------------------------------- host side
@@ -898,10 +955,10 @@ int launch_decode(const moe_kv_cache& c, DecodeParams p, const void* q, cudaStre
                                 227 * 1024 - (int)sizeof(Shared));
   });
   if (e == cudaSuccess) e = launch_k(decode_kernel, p.ctas, kThreads, smem, s, kv, pair, qs, qsr, qp, qpr, p);
-  // 4 sets of warps a row while the rows alone do not fill the SMs (then a row has many pieces)
+  // a CTA a row while the rows alone do not fill the SMs (then a row has many pieces), else a warp a row
   if (e == cudaSuccess)
-    e = qrows <= 4ull * p.ctas ? launch_k(combine_parts_kernel<4>, (unsigned)qrows, 512, 0, s, p)
-                               : launch_k(combine_parts_kernel<1>, (unsigned)qrows, 128, 0, s, p);
+    e = qrows <= 4ull * p.ctas ? launch_k(combine_parts_kernel, (unsigned)qrows, 128 * kSets, 0, s, p)
+                               : launch_k(combine_rows_kernel, (unsigned)((qrows + 3) / 4), 128, 0, s, p, (int)qrows);
   return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
