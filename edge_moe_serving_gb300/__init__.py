@@ -187,7 +187,7 @@ def _s(stream):
     if stream is None:
         # the current stream's handle alone: building a Stream object takes 3 us of every call
         import torch
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream

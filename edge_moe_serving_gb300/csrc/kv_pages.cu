@@ -15,6 +15,13 @@ namespace {
 
 constexpr int kPlanThreads = 1024;
 constexpr int kApplyThreads = 256;
+constexpr int kCluster = 8;              // CTAs of the one-launch forms
+
+// All threads of the cluster's CTAs; what they wrote before is seen after.
+__device__ inline void cluster_meet() {
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
 
 struct PlanScan {
   int warp[32];
@@ -145,28 +152,45 @@ reserve_kernel(const KvView kv, const int32_t* seqs, const int32_t* n_new, int n
 }
 
 // ---------------------------------------------------------------- append
-// One thread per 16 bytes of a row.
+// A warp takes `per` <= 32 rows at a time: one run of bytes to read, `per` places to write (61 MB of rows: 18 us, 6.7
+// TB/s read and written; with a thread per 16 bytes that finds its own place 24 us).
 __global__ void __launch_bounds__(kApplyThreads)
 append_kernel(const KvView kv, int layer, const uint4* rows, const int32_t* tok_seq, const int32_t* tok_pos, int N,
-              uint32_t* status) {
+              int per, uint32_t* status) {
   pdl_wait();
   pdl_trigger();
-  const int vecs = kv.row >> 3;
-  const long long total = (long long)N * vecs;
-  for (long long x = (long long)blockIdx.x * blockDim.x + threadIdx.x; x < total;
-       x += (long long)gridDim.x * blockDim.x) {
-    const int i = (int)(x / vecs), v = (int)(x - (long long)i * vecs);
-    const int s = tok_seq[i], pos = tok_pos[i];
-    if (s < 0 || s >= kv.max_seqs || pos < 0 || pos >= kv.len_of(s)) {
-      if (v == 0) set_status(status, MOE_DEV_ERR_BAD_SEQ);
-      continue;
+  const int vecs = kv.row >> 3, lane = threadIdx.x & 31;
+  const int warps = gridDim.x * (kApplyThreads / 32);
+  for (int i0 = per * (blockIdx.x * (kApplyThreads / 32) + (threadIdx.x >> 5)); i0 < N; i0 += per * warps) {
+    // lane j finds where row i0 + j goes (its dependent reads are the warp's only ones)
+    const int i = i0 + lane;
+    long long to = -1;
+    if (lane < per && i < N) {
+      const int s = tok_seq[i], pos = tok_pos[i];
+      if (s < 0 || s >= kv.max_seqs || pos < 0 || pos >= kv.len_of(s)) {
+        set_status(status, MOE_DEV_ERR_BAD_SEQ);
+      } else {
+        const int p = kv.table[(size_t)s * kv.max_blocks + (pos >> kv.page_shift)];
+        if (p < 0 || p >= kv.n_pages || kv.refs[p] != 1) set_status(status, MOE_DEV_ERR_BAD_PAGE);
+        else to = (long long)kv.row_offset(layer, p, pos & (kv.page_tokens - 1));
+      }
     }
-    const int p = kv.table[(size_t)s * kv.max_blocks + (pos >> kv.page_shift)];
-    if (p < 0 || p >= kv.n_pages || kv.refs[p] != 1) {
-      if (v == 0) set_status(status, MOE_DEV_ERR_BAD_PAGE);
-      continue;
+    const uint4* from = rows + (size_t)i0 * vecs;
+    const int total = min(per, N - i0) * vecs;
+    for (int x0 = 0; x0 < total; x0 += 32 * 8) {          // eight reads in flight
+      uint4 v[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int x = x0 + 32 * j + lane;
+        if (x < total) v[j] = __ldcs(from + x);
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int x = x0 + 32 * j + lane, r = min(x / vecs, 31);
+        const long long at = __shfl_sync(0xffffffffu, to, r);
+        if (x < total && at >= 0) reinterpret_cast<uint4*>(kv.pages + at)[x - r * vecs] = v[j];
+      }
     }
-    reinterpret_cast<uint4*>(kv.pages + kv.row_offset(layer, p, pos & (kv.page_tokens - 1)))[v] = rows[x];
   }
 }
 
@@ -178,25 +202,9 @@ struct ForkPlan {
   int old_len;  // what the destination held
 };
 
-// CTA 0 plans; the others keep the sources' block tables as they were (a
-// source may be another pair's destination).
-__global__ void __launch_bounds__(kPlanThreads)
-fork_plan_kernel(const KvView kv, const int32_t* src, const int32_t* dst, int n, ForkPlan* plan, int32_t* list,
-                 int32_t* snap, uint32_t* status) {
-  extern __shared__ int first[];
-  __shared__ PlanScan sh;
-  pdl_wait();
-  pdl_trigger();
-  if (blockIdx.x > 0) {
-    for (int i = blockIdx.x - 1; i < n; i += gridDim.x - 1) {
-      const int s = src[i];
-      if (s < 0 || s >= kv.max_seqs || s == dst[i]) continue;
-      const int blocks = kv.blocks_of(kv.len_of(s));
-      for (int b = threadIdx.x; b < blocks; b += blockDim.x)
-        snap[(size_t)i * kv.max_blocks + b] = kv.table[(size_t)s * kv.max_blocks + b];
-    }
-    return;
-  }
+// One CTA: which pairs are valid, which need a page, and which page.  first: one int per sequence in shared memory.
+__device__ void fork_plan(const KvView& kv, const int32_t* src, const int32_t* dst, int n, ForkPlan* plan,
+                          int32_t* list, int* first, PlanScan& sh, uint32_t* status) {
   mark_first(dst, n, kv.max_seqs, first);
   int total = 0;
   for (int i0 = 0; i0 < n; i0 += kPlanThreads) {
@@ -231,7 +239,62 @@ fork_plan_kernel(const KvView kv, const int32_t* src, const int32_t* dst, int n,
   }
 }
 
-// Block row 0: the pair's table and reference counts; rows 1..: a share of the copied page's rows.
+// The sources' block tables as they were (a source may be another pair's destination): pairs from, from + step, ...
+__device__ void fork_snapshot(const KvView& kv, const int32_t* src, const int32_t* dst, int n, int32_t* snap, int from,
+                              int step) {
+  for (int i = from; i < n; i += step) {
+    const int s = src[i];
+    if (s < 0 || s >= kv.max_seqs || s == dst[i]) continue;
+    const int blocks = kv.blocks_of(kv.len_of(s));
+    for (int b = threadIdx.x; b < blocks; b += blockDim.x)
+      snap[(size_t)i * kv.max_blocks + b] = kv.table[(size_t)s * kv.max_blocks + b];
+  }
+}
+
+// One pair's block table and reference counts (the CTA's threads).
+__device__ void fork_table(const KvView& kv, int d, const ForkPlan& f, const int32_t* snap) {
+  const int blocks = kv.blocks_of(f.len), old_blocks = kv.blocks_of(f.old_len);
+  int32_t* row = kv.table + (size_t)d * kv.max_blocks;
+  for (int b = threadIdx.x; b < max(blocks, old_blocks); b += blockDim.x) {
+    const int was = row[b];
+    const int now = b >= blocks ? -1 : (f.page >= 0 && b == blocks - 1) ? f.page : snap[b];
+    if (was == now) continue;
+    if (was >= 0 && was < kv.n_pages) atomicSub(&kv.refs[was], 1);
+    if (now >= 0 && now < kv.n_pages) atomicAdd(&kv.refs[now], 1);
+    row[b] = now;
+  }
+  if (threadIdx.x == 0) kv.lens[d] = f.len;
+}
+
+// The valid rows of one pair's partly filled page, every layer: thread `x` of `threads`.
+__device__ void fork_copy(const KvView& kv, const ForkPlan& f, int x, int threads, uint32_t* status) {
+  if (f.page < 0) return;
+  if (f.from < 0 || f.from >= kv.n_pages) {
+    if (x == 0) set_status(status, MOE_DEV_ERR_BAD_PAGE);
+    return;
+  }
+  const int vecs = (f.len & (kv.page_tokens - 1)) * (kv.row >> 3);   // the valid rows are one run of bytes
+  for (int layer = 0; layer < kv.n_layers; ++layer) {
+    const uint4* from = reinterpret_cast<const uint4*>(kv.pages + kv.row_offset(layer, f.from, 0));
+    uint4* to = reinterpret_cast<uint4*>(kv.pages + kv.row_offset(layer, f.page, 0));
+#pragma unroll 4
+    for (int v = x; v < vecs; v += threads) to[v] = from[v];
+  }
+}
+
+// Two launches, for copies that need the whole GPU: CTA 0 plans while the others take the snapshot, then a row of
+// CTAs a pair applies it (block row 0: the table; the others: a share of the page's rows).
+__global__ void __launch_bounds__(kPlanThreads)
+fork_plan_kernel(const KvView kv, const int32_t* src, const int32_t* dst, int n, ForkPlan* plan, int32_t* list,
+                 int32_t* snap, uint32_t* status) {
+  extern __shared__ int first[];
+  __shared__ PlanScan sh;
+  pdl_wait();
+  pdl_trigger();
+  if (blockIdx.x == 0) fork_plan(kv, src, dst, n, plan, list, first, sh, status);
+  else fork_snapshot(kv, src, dst, n, snap, blockIdx.x - 1, gridDim.x - 1);
+}
+
 __global__ void __launch_bounds__(kApplyThreads)
 fork_apply_kernel(const KvView kv, const int32_t* dst, const ForkPlan* plan, const int32_t* snap, uint32_t* status) {
   pdl_wait();
@@ -239,34 +302,28 @@ fork_apply_kernel(const KvView kv, const int32_t* dst, const ForkPlan* plan, con
   const int i = blockIdx.x;
   const ForkPlan f = plan[i];
   if (f.len < 0) return;
-  if (blockIdx.y > 0) {
-    if (f.page < 0) return;
-    if (f.from < 0 || f.from >= kv.n_pages) {
-      if (threadIdx.x == 0) set_status(status, MOE_DEV_ERR_BAD_PAGE);
-      return;
-    }
-    const int vecs = (f.len & (kv.page_tokens - 1)) * (kv.row >> 3);   // the valid rows are one run of bytes
-    const long long total = (long long)kv.n_layers * vecs;
-    for (long long x = (long long)(blockIdx.y - 1) * blockDim.x + threadIdx.x; x < total;
-         x += (long long)(gridDim.y - 1) * blockDim.x) {
-      const int layer = (int)(x / vecs), v = (int)(x - (long long)layer * vecs);
-      const uint4* from = reinterpret_cast<const uint4*>(kv.pages + kv.row_offset(layer, f.from, 0));
-      reinterpret_cast<uint4*>(kv.pages + kv.row_offset(layer, f.page, 0))[v] = from[v];
-    }
-    return;
+  if (blockIdx.y == 0) fork_table(kv, dst[i], f, snap + (size_t)i * kv.max_blocks);
+  else fork_copy(kv, f, (blockIdx.y - 1) * blockDim.x + threadIdx.x, (gridDim.y - 1) * blockDim.x, status);
+}
+
+// One launch of one cluster, for small copies: its CTAs meet between the plan and its application.
+__global__ void __launch_bounds__(kPlanThreads) __cluster_dims__(kCluster, 1, 1)
+fork_small_kernel(const KvView kv, const int32_t* src, const int32_t* dst, int n, ForkPlan* plan, int32_t* list,
+                  int32_t* snap, uint32_t* status) {
+  extern __shared__ int first[];
+  __shared__ PlanScan sh;
+  pdl_wait();
+  pdl_trigger();
+  const int c = blockIdx.x;
+  if (c == 0) fork_plan(kv, src, dst, n, plan, list, first, sh, status);
+  else fork_snapshot(kv, src, dst, n, snap, c - 1, kCluster - 1);
+  cluster_meet();
+  for (int i = c; i < n; i += kCluster) {
+    const ForkPlan f = plan[i];
+    if (f.len < 0) continue;
+    fork_table(kv, dst[i], f, snap + (size_t)i * kv.max_blocks);
+    fork_copy(kv, f, threadIdx.x, kPlanThreads, status);
   }
-  const int d = dst[i];
-  const int blocks = kv.blocks_of(f.len), old_blocks = kv.blocks_of(f.old_len);
-  int32_t* row = kv.table + (size_t)d * kv.max_blocks;
-  for (int b = threadIdx.x; b < max(blocks, old_blocks); b += blockDim.x) {
-    const int was = row[b];
-    const int now = b >= blocks ? -1 : (f.page >= 0 && b == blocks - 1) ? f.page : snap[(size_t)i * kv.max_blocks + b];
-    if (was == now) continue;
-    if (was >= 0 && was < kv.n_pages) atomicSub(&kv.refs[was], 1);
-    if (now >= 0 && now < kv.n_pages) atomicAdd(&kv.refs[now], 1);
-    row[b] = now;
-  }
-  if (threadIdx.x == 0) kv.lens[d] = f.len;
 }
 
 // ---------------------------------------------------------------- free
@@ -296,11 +353,9 @@ free_kernel(const KvView kv, const int32_t* seqs, uint32_t* status) {
 
 // ---------------------------------------------------------------- compact
 // counts[0] = pages that move, counts[1] = n_live; move[j] = (from, to); to[p] = new place of a page that moves
-__global__ void __launch_bounds__(kPlanThreads)
-compact_plan_kernel(const KvView kv, int32_t* counts, int32_t* from, int32_t* dest, int32_t* to, int32_t* n_live_opt) {
-  __shared__ PlanScan sh;
-  pdl_wait();
-  pdl_trigger();
+// One CTA.
+__device__ void compact_plan(const KvView& kv, int32_t* counts, int32_t* from, int32_t* dest, int32_t* to,
+                             int32_t* n_live_opt, PlanScan& sh) {
   int live = 0;
   for (int p = threadIdx.x; p < kv.n_pages; p += kPlanThreads) live += kv.refs[p] != 0;
   int n_live;
@@ -343,27 +398,79 @@ compact_plan_kernel(const KvView kv, int32_t* counts, int32_t* from, int32_t* de
   }
 }
 
-__global__ void __launch_bounds__(kApplyThreads)
-compact_apply_kernel(const KvView kv, const int32_t* counts, const int32_t* from, const int32_t* dest,
-                     const int32_t* to) {
-  pdl_wait();
-  pdl_trigger();
+// CTA c of `ctas`: its share of the block tables, and of the pages that move (a page of one layer at a time).
+__device__ void compact_apply(const KvView& kv, const int32_t* counts, const int32_t* from, const int32_t* dest,
+                              const int32_t* to, int c, int ctas) {
   const int moves = counts[0], n_live = counts[1];
   if (moves == 0) return;
-  const int stride = gridDim.x * blockDim.x, tid = blockIdx.x * blockDim.x + threadIdx.x;
-  for (long long e = tid; e < (long long)kv.max_seqs * kv.max_blocks; e += stride) {
+  for (long long e = (long long)c * blockDim.x + threadIdx.x; e < (long long)kv.max_seqs * kv.max_blocks;
+       e += (long long)ctas * blockDim.x) {
     const int p = kv.table[e];
     if (p >= n_live && p < kv.n_pages) kv.table[e] = to[p];
   }
   const int vecs = kv.page_tokens * (kv.row >> 3);
   const long long units = (long long)moves * kv.n_layers;
-  for (long long u = blockIdx.x; u < units; u += gridDim.x) {
+  for (long long u = c; u < units; u += ctas) {
     const int j = (int)(u / kv.n_layers), layer = (int)(u - (long long)j * kv.n_layers);
     const uint4* a = reinterpret_cast<const uint4*>(kv.pages + kv.row_offset(layer, from[j], 0));
     uint4* b = reinterpret_cast<uint4*>(kv.pages + kv.row_offset(layer, dest[j], 0));
+#pragma unroll 4
     for (int v = threadIdx.x; v < vecs; v += blockDim.x) b[v] = a[v];
   }
 }
+
+__global__ void __launch_bounds__(kPlanThreads)
+compact_plan_kernel(const KvView kv, int32_t* counts, int32_t* from, int32_t* dest, int32_t* to, int32_t* n_live_opt) {
+  __shared__ PlanScan sh;
+  pdl_wait();
+  pdl_trigger();
+  compact_plan(kv, counts, from, dest, to, n_live_opt, sh);
+}
+
+__global__ void __launch_bounds__(kApplyThreads)
+compact_apply_kernel(const KvView kv, const int32_t* counts, const int32_t* from, const int32_t* dest,
+                     const int32_t* to) {
+  pdl_wait();
+  pdl_trigger();
+  compact_apply(kv, counts, from, dest, to, blockIdx.x, gridDim.x);
+}
+
+__global__ void __launch_bounds__(kPlanThreads) __cluster_dims__(kCluster, 1, 1)
+compact_small_kernel(const KvView kv, int32_t* counts, int32_t* from, int32_t* dest, int32_t* to, int32_t* n_live_opt) {
+  __shared__ PlanScan sh;
+  pdl_wait();
+  pdl_trigger();
+  if (blockIdx.x == 0) compact_plan(kv, counts, from, dest, to, n_live_opt, sh);
+  cluster_meet();
+  // as compact_apply, with the pages' bytes as one run of work: four reads in flight a thread
+  const int moves = counts[0], n_live = counts[1], tid = blockIdx.x * kPlanThreads + threadIdx.x;
+  constexpr int kAll = kCluster * kPlanThreads;
+  if (moves == 0) return;
+  const int vecs = kv.page_tokens * (kv.row >> 3), total = moves * kv.n_layers * vecs;   // the pool is at most 16 MB
+  for (int x0 = tid; x0 < total; x0 += 4 * kAll) {
+    uint4 v[4];
+    uint4* at[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int x = x0 + q * kAll;
+      if (x < total) {
+        const int u = x / vecs, y = x - u * vecs, j = u / kv.n_layers, layer = u - j * kv.n_layers;
+        v[q] = reinterpret_cast<const uint4*>(kv.pages + kv.row_offset(layer, from[j], 0))[y];
+        at[q] = reinterpret_cast<uint4*>(kv.pages + kv.row_offset(layer, dest[j], 0)) + y;
+      }
+    }
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      if (x0 + q * kAll < total) *at[q] = v[q];
+  }
+  for (long long e = tid; e < (long long)kv.max_seqs * kv.max_blocks; e += kAll) {
+    const int p = kv.table[e];
+    if (p >= n_live && p < kv.n_pages) kv.table[e] = to[p];
+  }
+}
+
+// Up to these bytes a call runs as one cluster (copies of a fork; the pool that a compaction may move a part of).
+constexpr long long kSmallCopy = 4ll << 20, kSmallPool = 16ll << 20;
 
 size_t ints(size_t n) { return align_up(n * sizeof(int32_t), 256); }
 
@@ -415,11 +522,12 @@ int moe_kv_append(const moe_kv_cache* cache, int layer, const void* rows, const 
   if (N == 0) return MOE_OK;
   if (!rows || !tok_seq || !tok_pos) return MOE_ERR_INVALID_ARG;
   if (!kv_aligned(rows, 16)) return MOE_ERR_UNSUPPORTED;
-  const long long blocks = ((long long)N * ((cache->rank + cache->rope) / 8) + kApplyThreads - 1) / kApplyThreads;
-  const long long cap = 8LL * num_sms();
+  const int cap = 8 * num_sms(), warps = kApplyThreads / 32;
+  const int spread = (N + cap * warps - 1) / (cap * warps), per = spread < 32 ? spread : 32;   // few rows: spread over the SMs
+  const int blocks = (N + per * warps - 1) / (per * warps);
   return status_of(launch_k(append_kernel, (unsigned)(blocks < cap ? blocks : cap), kApplyThreads, 0,
                             reinterpret_cast<cudaStream_t>(stream), kv_view(*cache), layer,
-                            reinterpret_cast<const uint4*>(rows), tok_seq, tok_pos, N, dev_status));
+                            reinterpret_cast<const uint4*>(rows), tok_seq, tok_pos, N, per, dev_status));
 }
 
 int moe_kv_fork(const moe_kv_cache* cache, const int32_t* src, const int32_t* dst, int n, void* ws,
@@ -435,12 +543,17 @@ int moe_kv_fork(const moe_kv_cache* cache, const int32_t* src, const int32_t* ds
   int32_t* snap = reinterpret_cast<int32_t*>(b + ints(n));
   const KvView kv = kv_view(*cache);
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  cudaError_t e = launch_k(fork_plan_kernel, 1 + (n < 256 ? n : 256), kPlanThreads,
-                           (size_t)cache->max_seqs * sizeof(int), s, kv, src, dst, n, plan, list, snap, dev_status);
+  const size_t first = (size_t)cache->max_seqs * sizeof(int);
+  const long long page_vecs = (long long)cache->n_layers * cache->page_tokens * ((cache->rank + cache->rope) / 8);
+  // One launch on 8 SMs while the copies are small, two on all of them from there on.
+  if (n * page_vecs * 16 <= kSmallCopy)
+    return status_of(launch_k(fork_small_kernel, kCluster, kPlanThreads, first, s, kv, src, dst, n, plan, list, snap,
+                              dev_status));
+  cudaError_t e = launch_k(fork_plan_kernel, 1 + (n < 256 ? n : 256), kPlanThreads, first, s, kv, src, dst, n, plan, list,
+                           snap, dev_status);
   if (e != cudaSuccess) return MOE_ERR_CUDA;
   // copy CTAs of a pair: about 8 16-byte vectors a thread for a full page in every layer
-  const long long vecs = (long long)cache->n_layers * cache->page_tokens * ((cache->rank + cache->rope) / 8);
-  const long long want = (vecs + 8 * kApplyThreads - 1) / (8 * kApplyThreads);
+  const long long want = (page_vecs + 8 * kApplyThreads - 1) / (8 * kApplyThreads);
   return status_of(launch_k(fork_apply_kernel, dim3(n, 1 + (unsigned)(want < 64 ? want : 64)), kApplyThreads, 0, s, kv,
                             dst, plan, snap, dev_status));
 }
@@ -467,6 +580,9 @@ int moe_kv_compact(const moe_kv_cache* cache, int32_t* n_live_opt, void* ws, siz
   int32_t* to = reinterpret_cast<int32_t*>(b + ints(2) + 2 * list);
   const KvView kv = kv_view(*cache);
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const long long pool = (long long)cache->n_layers * cache->n_pages * cache->page_tokens * (cache->rank + cache->rope) * 2;
+  if (pool <= kSmallPool)
+    return status_of(launch_k(compact_small_kernel, kCluster, kPlanThreads, 0, s, kv, counts, from, dest, to, n_live_opt));
   cudaError_t e = launch_k(compact_plan_kernel, 1, kPlanThreads, 0, s, kv, counts, from, dest, to, n_live_opt);
   if (e != cudaSuccess) return MOE_ERR_CUDA;
   return status_of(launch_k(compact_apply_kernel, 8 * num_sms(), kApplyThreads, 0, s, kv, counts, from, dest, to));
