@@ -31,6 +31,7 @@
 // MOE_DEV_ERR_TIMEOUT, drains and returns.
 #include <cfloat>
 #include <cmath>
+#include <type_traits>
 
 #include "kv_common.cuh"
 #include "tc_common.cuh"
@@ -530,6 +531,7 @@ decode_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_constant_
     bool fail = false;
     const float scale = p.scale_log2;
     const float unseen = scale >= 0.0f ? -INFINITY : INFINITY;   // what a token out of sight scores
+    const int p_row = r0 * 128 + (lane & 3) * 4, p_swz = (r0 & 7) << 4;   // this thread's place in P; rows r and r + 8 swizzle alike
     if (st < kRows) sh.factor[st] = 1.0f;
     soft_any(false);
     while (!fail && it.next(sg)) {
@@ -549,6 +551,9 @@ decode_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_constant_
         m[e] = -INFINITY;
         l[e] = make_float2(0.0f, 0.0f);
       }
+      // tokens up to here are seen by all of the warp's rows
+      int sees_all = min(sg.tok1, min(active[0] ? limit[0] : INT_MAX, active[1] ? limit[1] : INT_MAX));
+      sees_all = __reduce_min_sync(0xffffffffu, sees_all);
       for (int t0 = sg.tok0; t0 < sg.tok1; t0 += kTok, ++tile) {
         const int buf = tile & 1, slot = tile % p.slots;
         const int n_tok = min(kTok, sg.tok1 - t0);
@@ -566,69 +571,86 @@ decode_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_constant_
         }
         bool grow = !ok;
         float ref[2];
+        if (t0 + kTok > sees_all) {
+          // some row does not see all 64 tokens
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int see = min(n_tok, limit[e] - t0);
-          if (!__all_sync(0xffffffffu, see >= kTok || !active[e])) {
+          for (int e = 0; e < 2; ++e) {
+            const int see = min(n_tok, limit[e] - t0);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
               if (8 * i + c2 >= see) s[4 * i + 2 * e] = unseen;
               if (8 * i + c2 + 1 >= see) s[4 * i + 2 * e + 1] = unseen;
             }
           }
-          float top = s[2 * e];
-          if (p.scale_log2 >= 0.0f) {
+        }
+        float top[2];
+        if (scale >= 0.0f) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) top = fmaxf(top, fmaxf(s[4 * i + 2 * e], s[4 * i + 2 * e + 1]));
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-          } else {
+          for (int e = 0; e < 2; ++e) {
+            float a = fmaxf(s[2 * e], s[2 * e + 1]), b = fmaxf(s[4 + 2 * e], s[5 + 2 * e]);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) top = fminf(top, fminf(s[4 * i + 2 * e], s[4 * i + 2 * e + 1]));
-            top = fminf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-            top = fminf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            for (int i = 2; i < 8; i += 2) {
+              a = fmaxf(fmaxf(a, s[4 * i + 2 * e]), s[4 * i + 2 * e + 1]);
+              b = fmaxf(fmaxf(b, s[4 * i + 4 + 2 * e]), s[4 * i + 5 + 2 * e]);
+            }
+            top[e] = fmaxf(a, b);
           }
-          top = see > 0 ? top * scale : -INFINITY;
-          if (active[e] && top > m[e]) {
-            if (m[e] == -INFINITY) {
-              m[e] = top;             // nothing summed for this row yet
-            } else if (top > m[e] + kGrow) {
-              const float f = ex2(m[e] - top);
+#pragma unroll
+          for (int o = 1; o <= 2; o <<= 1)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) top[e] = fmaxf(top[e], __shfl_xor_sync(0xffffffffu, top[e], o));
+        } else {
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            top[e] = s[2 * e];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) top[e] = fminf(top[e], fminf(s[4 * i + 2 * e], s[4 * i + 2 * e + 1]));
+#pragma unroll
+            for (int o = 1; o <= 2; o <<= 1) top[e] = fminf(top[e], __shfl_xor_sync(0xffffffffu, top[e], o));
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float now = limit[e] > t0 ? top[e] * scale : -INFINITY;
+          if (active[e] && now > m[e] + (m[e] == -INFINITY ? 0.0f : kGrow)) {
+            if (m[e] != -INFINITY) {        // else nothing is summed for this row yet
+              const float f = ex2(m[e] - now);
               l[e].x *= f;
               l[e].y *= f;
-              m[e] = top;
               grow = true;
               if ((lane & 3) == 0) sh.factor[r0 + 8 * e] = f;
             }
+            m[e] = now;
           }
           ref[e] = m[e] == -INFINITY ? 0.0f : m[e];
         }
-        // Probabilities, rounded to bf16 (the cache's type, the only one the product takes beside it).  Two sums:
-        // of the rounded ones, which the output is divided by (its weights then add up to one, and where few tokens
-        // carry the row most of their rounding cancels), and of the unrounded ones for the log-sum-exp.
-        uint8_t* sp = skv + slot * slot_bytes + 2 * p.pairs * kChunk + (lane & 3) * 4;
+        // Probabilities, rounded to bf16 (the cache's type, the only one the product takes beside it).  Their sum is of
+        // the rounded ones: the output is divided by it, so its weights add up to one, and where few tokens carry the
+        // row most of their rounding cancels.  The log-sum-exp wants the sum of the unrounded ones too.
+        uint8_t* sp = skv + slot * slot_bytes + 2 * p.pairs * kChunk + p_row;
+        auto probabilities = [&](auto with_lse) {
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int r = r0 + 8 * e;
-          if (r < sg.N) {
-            uint8_t* prow = sp + r * 128;
+          for (int e = 0; e < 2; ++e) {
+            if (r0 + 8 * e >= sg.N) continue;
+            const float2 mul = make_float2(scale, scale), sub = make_float2(-ref[e], -ref[e]);
             float2 sum = make_float2(0.0f, 0.0f), rsum = sum;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-              float2 x = fma2(make_float2(s[4 * i + 2 * e], s[4 * i + 2 * e + 1]), make_float2(scale, scale),
-                              make_float2(-ref[e], -ref[e]));
+              float2 x = fma2(make_float2(s[4 * i + 2 * e], s[4 * i + 2 * e + 1]), mul, sub);
               x.x = ex2(x.x);
               x.y = ex2(x.y);
               const __nv_bfloat162 h = __floats2bfloat162_rn(x.x, x.y);
               const uint32_t w = *reinterpret_cast<const uint32_t*>(&h);
-              sum = add2(sum, x);
+              if (decltype(with_lse)::value) sum = add2(sum, x);
               rsum = add2(rsum, make_float2(bf16_lo(w), bf16_hi(w)));
-              *reinterpret_cast<uint32_t*>(prow + ((i ^ (r & 7)) << 4)) = w;
+              *reinterpret_cast<uint32_t*>(sp + e * 1024 + (p_swz ^ (i << 4))) = w;
             }
             l[e].x += sum.x + sum.y;
             l[e].y += rsum.x + rsum.y;
           }
-        }
+        };
+        if (p.lse) probabilities(std::true_type{});
+        else probabilities(std::false_type{});
         if (n_tok < kTok) {
           // places past the last token: any bits may stand there, and 0 * NaN is NaN
           uint8_t* base = skv + slot * slot_bytes;
