@@ -234,6 +234,14 @@ __device__ inline bool soft_any(bool v) {
   return r != 0;
 }
 
+// Four 8 x 8 matrices of 16-bit entries in one store; lane l gives the address of row l % 8 of matrix l / 8.  (One
+// store for four: shared memory is busy with the products' operands, and a store waits its turn each time.)
+__device__ inline void store_matrices(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c),
+               "r"(d)
+               : "memory");
+}
+
 struct Shared {
   uint64_t full[kMaxSlots][kMaxPairs + 1], empty[kMaxSlots][kMaxPairs + 1];   // per 128-entry pair, then the rotary chunk
   uint64_t q_full, q_empty, s_full[2], s_empty[2], p_full, pv_done[2], drain[2];
@@ -531,7 +539,9 @@ decode_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_constant_
     bool fail = false;
     const float scale = p.scale_log2;
     const float unseen = scale >= 0.0f ? -INFINITY : INFINITY;   // what a token out of sight scores
-    const int p_row = r0 * 128 + (lane & 3) * 4, p_swz = (r0 & 7) << 4;   // this thread's place in P; rows r and r + 8 swizzle alike
+    // Where this lane's matrix row goes in P: row lane % 8 of the warp's 16 (+ 8: 1024 bytes on), 16-byte column group
+    // lane / 8 (+ 4: bit 6 flips), swizzled with the row.
+    const uint32_t p_row = (quarter * 16 + (lane & 7)) * 128, p_at0 = ((lane >> 3) ^ (lane & 7)) << 4;
     if (st < kRows) sh.factor[st] = 1.0f;
     soft_any(false);
     while (!fail && it.next(sg)) {
@@ -627,24 +637,26 @@ decode_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_constant_
         // Probabilities, rounded to bf16 (the cache's type, the only one the product takes beside it).  Their sum is of
         // the rounded ones: the output is divided by it, so its weights add up to one, and where few tokens carry the
         // row most of their rounding cancels.  The log-sum-exp wants the sum of the unrounded ones too.
-        uint8_t* sp = skv + slot * slot_bytes + 2 * p.pairs * kChunk + p_row;
+        const uint32_t sp = smem_u32(skv + slot * slot_bytes + 2 * p.pairs * kChunk) + p_row;
         auto probabilities = [&](auto with_lse) {
+          if (quarter * 16 >= sg.N) return;
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            if (r0 + 8 * e >= sg.N) continue;
             const float2 mul = make_float2(scale, scale), sub = make_float2(-ref[e], -ref[e]);
             float2 sum = make_float2(0.0f, 0.0f), rsum = sum;
+            uint32_t w[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
               float2 x = fma2(make_float2(s[4 * i + 2 * e], s[4 * i + 2 * e + 1]), mul, sub);
               x.x = ex2(x.x);
               x.y = ex2(x.y);
               const __nv_bfloat162 h = __floats2bfloat162_rn(x.x, x.y);
-              const uint32_t w = *reinterpret_cast<const uint32_t*>(&h);
+              w[i] = *reinterpret_cast<const uint32_t*>(&h);
               if (decltype(with_lse)::value) sum = add2(sum, x);
-              rsum = add2(rsum, make_float2(bf16_lo(w), bf16_hi(w)));
-              *reinterpret_cast<uint32_t*>(sp + e * 1024 + (p_swz ^ (i << 4))) = w;
+              rsum = add2(rsum, make_float2(bf16_lo(w[i]), bf16_hi(w[i])));
             }
+            store_matrices(sp + e * 1024 + p_at0, w[0], w[1], w[2], w[3]);
+            store_matrices(sp + e * 1024 + (p_at0 ^ 64), w[4], w[5], w[6], w[7]);
             l[e].x += sum.x + sum.y;
             l[e].y += rsum.x + rsum.y;
           }
