@@ -350,3 +350,92 @@ def test_both_forms_agree():
     assert c.bits() == 0
     # the absorbed query is rounded to bf16, as k is in the other form: each within the expanded form's 4e-3
     assert float((out - other).norm() / out.norm()) <= 8e-3
+
+
+def test_more_than_one_launch_of_sequences():
+    """More sequences than one launch takes (512), with and without a shared prefix."""
+    lens = [64 + (i * 7) % 40 for i in range(530)]
+    c = Paged(2 + sum(-(-n // 32) for n in lens), 32, 128, 16, 530, 4)
+    rows = c.fill(lens, seed=60, shared_blocks=2)
+    q = make_q(530, 5, c.row, 61)
+    for shared in (0, 64):
+        out, lse = run_decode(c, q, list(range(530)), 1, 5, 0.1, shared=shared)
+        assert c.bits() == 0
+        for b in (0, 1, 511, 512, 513, 529):
+            check_decode(c, rows, q[b:b + 1], [b], 1, 5, 0.1, out[b:b + 1], lse[b:b + 1])
+
+
+def test_attention_in_a_graph():
+    """Both calls captured once and replayed after the cache has grown: lengths and tables are read on the device."""
+    c = Paged(40, 16, 512, 64, 2, 12)
+    lens = [40, 90]
+    rows = c.fill([60, 110], seed=70)
+    q = make_q(2, 16, c.row, 71)
+    qp, w = make_q(2, 2, 192, 72), make_w(2, 256, 512, 73)
+    i32 = lambda v: torch.tensor(v, dtype=torch.int32, device=DEV)  # noqa: E731
+    seqs, offsets = i32([0, 1]), i32([0, 1, 2])
+    n1 = moe.moe_latent_decode_workspace_size(c.handle, 2, 1, 16, 0)
+    n2 = moe.moe_latent_prefill_workspace_size(c.handle, 2, 2, 2, 128, 128, 200)
+    ws1, ws2 = (torch.zeros(n, dtype=torch.uint8, device=DEV) for n in (n1, n2))
+    out = torch.zeros(2, 16, 512, dtype=torch.bfloat16, device=DEV)
+    outp = torch.zeros(2, 2, 128, dtype=torch.bfloat16, device=DEV)
+    c.lens.copy_(i32(lens))
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+
+    def both():
+        moe.moe_latent_decode(c.handle, 0, q, seqs, 2, 1, 16, 0.07, 0, out, None, ws1, n1, c.status)
+        moe.moe_latent_prefill(c.handle, 0, qp, seqs, offsets, 2, 2, 2, 128, 128, w, 0.07, 200, outp, ws2, n2, c.status)
+
+    with torch.cuda.stream(s):
+        both()
+    s.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=s):
+        both()
+    for now in (lens, [60, 110]):
+        c.lens.copy_(i32(now))
+        g.replay()
+        torch.cuda.synchronize()
+        cut = [x[:n] for x, n in zip(rows, now)]
+        check_decode(c, cut, q, [0, 1], 1, 16, 0.07, out, None)
+        check_prefill(c, cut, qp, [0, 1], [0, 1, 2], 2, 128, w, 0.07, outp)
+    assert c.bits() == 0
+
+
+def test_prefill_values_beyond_the_f16_range():
+    """A value past 65504 is clamped and reported; keys of that size are not touched (they stay bf16)."""
+    c = Paged(4, 64, 128, 16, 1, 3)
+    c.fill([80], seed=80)
+    w = make_w(1, 256, 128, 81)
+    q = torch.zeros(1, 1, 144, dtype=torch.bfloat16, device=DEV)
+    w[:, :128] *= 1e6
+    run_prefill(c, q, [0], [0, 1], 1, 128, 128, w, 0.1, 80)
+    assert c.bits() == 0
+    w[:, 128:] *= 1e6
+    out = run_prefill(c, q, [0], [0, 1], 1, 128, 128, w, 0.1, 80)
+    assert c.bits() == moe.MOE_DEV_ERR_RANGE
+    assert bool(torch.isfinite(out).all()) and float(out.abs().max()) <= 65536.0
+
+
+@pytest.mark.parametrize("heads,new,cached", [(3, 70, 5000), (2, 300, 1500)])
+def test_prefill_token_shares(heads, new, cached):
+    """Few query blocks over many tokens: their tokens are shared out and the shares joined."""
+    n = cached + new
+    c = Paged(-(-n // 64) + 1, 64, 512, 64, 1, -(-n // 64))
+    rows = c.fill([n], seed=90)
+    q, w = make_q(new, heads, 192, 91), make_w(heads, 256, 512, 92)
+    out = run_prefill(c, q, [0], [0, new], heads, 128, 128, w, 192 ** -0.5, n)
+    assert c.bits() == 0
+    check_prefill(c, rows, q, [0], [0, new], heads, 128, w, 192 ** -0.5, out)
+    assert torch.equal(out, run_prefill(c, q, [0], [0, new], heads, 128, 128, w, 192 ** -0.5, n))
+
+
+@pytest.mark.parametrize("scale", [-0.1, 0.0])
+def test_prefill_scales(scale):
+    c = Paged(8, 32, 256, 32, 2, 8)
+    rows = c.fill([150, 40], seed=95)
+    q, w = make_q(60, 2, 96, 96), make_w(2, 128, 256, 97)
+    out = run_prefill(c, q, [0, 1], [0, 40, 60], 2, 64, 64, w, scale, 190)
+    assert c.bits() == 0
+    check_prefill(c, rows, q, [0, 1], [0, 40, 60], 2, 64, w, scale, out)

@@ -97,6 +97,12 @@ def test_decode_refuses():
     for change in (dict(rank=64), dict(rank=640), dict(rope=8), dict(rope=80)):
         assert call(c=ctypes.byref(cache(**change))) == moe.MOE_ERR_UNSUPPORTED
     assert call(B=0, q=None, seqs=None, out=None, ws=None, nb=0) == moe.MOE_OK
+    need = moe.moe_latent_decode_workspace_size(c, 4, 1, 16, 64)
+    assert need > 0 and moe.moe_latent_decode_workspace_size(c, 4, 9, 128, 0) == 0
+    assert call(shared=64, nb=need - 1) == moe.MOE_ERR_WORKSPACE
+    assert call(shared=64, ws=None, nb=need) == moe.MOE_ERR_WORKSPACE
+    assert call(shared=64, ws=A + 16, nb=need) == moe.MOE_ERR_UNSUPPORTED
+    assert call(c=ctypes.byref(cache(max_blocks=1 << 22, max_seqs=1))) == moe.MOE_ERR_UNSUPPORTED
 
 
 def test_prefill_refuses():
