@@ -215,6 +215,12 @@ __device__ inline void store_columns(uint32_t taddr, int rows, int stride, T* ds
   }
 }
 
+// Two bf16 values, those that are NaN or infinite as 0.
+__device__ inline uint32_t finite_bf16x2(uint32_t v) {
+  if ((v & 0x7F80u) == 0x7F80u) v &= 0xFFFF0000u;
+  if ((v & 0x7F800000u) == 0x7F800000u) v &= 0x0000FFFFu;
+  return v;
+}
 
 __device__ inline float warp_max(float v) {
 #pragma unroll
@@ -249,6 +255,7 @@ struct Shared {
   int abort;
   float factor[kRows];   // rescaling of each row; in the epilogue 1 / l
   int warp_sum[kThreads / 32];
+  int sees[kSoftThreads / 32];
   int pref[kBatch + 1];
   int len[kBatch];
   int ids[kBatch];
@@ -543,7 +550,6 @@ decode_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_constant_
     // lane / 8 (+ 4: bit 6 flips), swizzled with the row.
     const uint32_t p_row = (quarter * 16 + (lane & 7)) * 128, p_at0 = ((lane >> 3) ^ (lane & 7)) << 4;
     if (st < kRows) sh.factor[st] = 1.0f;
-    soft_any(false);
     while (!fail && it.next(sg)) {
       int limit[2];
       bool active[2];
@@ -561,9 +567,12 @@ decode_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_constant_
         m[e] = -INFINITY;
         l[e] = make_float2(0.0f, 0.0f);
       }
-      // tokens up to here are seen by all of the warp's rows
-      int sees_all = min(sg.tok1, min(active[0] ? limit[0] : INT_MAX, active[1] ? limit[1] : INT_MAX));
-      sees_all = __reduce_min_sync(0xffffffffu, sees_all);
+      // tokens up to here are seen by all of the warp's rows, and by all of the tile's
+      int sees_all = __reduce_min_sync(0xffffffffu, min(active[0] ? limit[0] : INT_MAX, active[1] ? limit[1] : INT_MAX));
+      if (lane == 0) sh.sees[quarter] = sees_all;
+      soft_any(false);                      // and the factors are set
+      const int sees_tile = min(min(sh.sees[0], sh.sees[1]), min(sh.sees[2], sh.sees[3]));
+      sees_all = min(sees_all, sg.tok1);
       for (int t0 = sg.tok0; t0 < sg.tok1; t0 += kTok, ++tile) {
         const int buf = tile & 1, slot = tile % p.slots;
         const int n_tok = min(kTok, sg.tok1 - t0);
@@ -672,6 +681,18 @@ decode_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_constant_
             *reinterpret_cast<uint4*>(base + c * kChunk + n_tok * 128 + y * 16) = make_uint4(0, 0, 0, 0);
           }
         }
+        if (t0 + n_tok > sees_tile && ok) {
+          // Some row does not see some token (the last tile of several query tokens): its probability 0 times a NaN or
+          // infinite value would be NaN.  Such values become 0 here; the rows that do see the token get their NaN
+          // from its score, which was made of the value before.
+          for (int j = 0; j < p.pairs; ++j) mbar_wait(&sh.full[slot][j], (tile / p.slots) & 1, abort_flag);   // long over
+          uint4* base = reinterpret_cast<uint4*>(skv + slot * slot_bytes);
+          for (int x = st; x < p.pairs * (2 * kChunk / 16); x += kSoftThreads) {
+            const uint4 v = base[x];
+            const uint4 f = make_uint4(finite_bf16x2(v.x), finite_bf16x2(v.y), finite_bf16x2(v.z), finite_bf16x2(v.w));
+            if (((v.x ^ f.x) | (v.y ^ f.y) | (v.z ^ f.z) | (v.w ^ f.w)) != 0) base[x] = f;
+          }
+        }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         if (soft_any(grow)) {      // rare: some row's maximum rose by more than 2^8 (or a wait ran out)
           // O was last added to by the previous tile's product, and this tile's waits for us
@@ -734,7 +755,6 @@ decode_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_constant_
       tc_fence_before();
       soft_any(false);
       if (st < kRows) sh.factor[st] = 1.0f;
-      soft_any(false);
     }
   }
   __syncthreads();

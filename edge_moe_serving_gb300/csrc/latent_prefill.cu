@@ -3,7 +3,7 @@
 //
 // plan_kernel    where each sequence's expanded rows begin, and the query blocks
 // expand_kernel  [128 tokens] x [one head's keys and values]: latents W^T, fp32
-//                sums in tensor memory, f16 results into the workspace
+//                sums in tensor memory, bf16 keys and f16 values into the workspace
 // attend_kernel  256 query rows of one head against that head's keys and
 //                values, 128 tokens at a time
 //
@@ -72,21 +72,12 @@ __device__ inline int seq_len(const PrefillParams& p, int b) {
   return s >= 0 && s < p.kv.max_seqs ? p.kv.len_of(s) : 0;
 }
 
-// f16 of two values, clamped to its range; NaN and infinities stay what they are.
-__device__ inline uint32_t half2_of(float x, float y, bool& clamped) {
-  const float ax = fabsf(x), ay = fabsf(y);
-  if (fmaxf(ax, ay) > 65504.0f) {
-    if (ax > 65504.0f && ax < INFINITY) {
-      clamped = true;
-      x = copysignf(65504.0f, x);
-    }
-    if (ay > 65504.0f && ay < INFINITY) {
-      clamped = true;
-      y = copysignf(65504.0f, y);
-    }
-  }
-  const __half2 h = __floats2half2_rn(x, y);
-  return *reinterpret_cast<const uint32_t*>(&h);
+// f16 of two values within its range; a NaN becomes a number as well (its token's keys are NaN and carry it to the rows
+// that see the token, while a row that does not see it multiplies the value by probability 0).
+__device__ inline uint32_t half2_of(float x, float y) {
+  const __half2 top = __half2half2(__ushort_as_half(0x7BFFu)), h = __floats2half2_rn(x, y);   // 65504
+  const __half2 c = __hmax2(__hmin2(h, top), __hneg2(top));
+  return *reinterpret_cast<const uint32_t*>(&c);
 }
 
 __device__ inline uint32_t bf16x2_of(float x, float y) {
@@ -410,13 +401,9 @@ expand_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
           for (int y = 0; y < 16; ++y) {
             const float e0 = __uint_as_float(x[2 * y]), e1 = __uint_as_float(x[2 * y + 1]);
             big = fmaxf(big, fmaxf(fabsf(e0), fabsf(e1)));
-            const __half2 h = __floats2half2_rn(e0, e1);
-            o[y] = *reinterpret_cast<const uint32_t*>(&h) & mask;
+            o[y] = half2_of(e0, e1) & mask;
           }
-          if ((big > 65504.0f) & (mask != 0u)) {
-#pragma unroll
-            for (int y = 0; y < 16; ++y) o[y] = half2_of(__uint_as_float(x[2 * y]), __uint_as_float(x[2 * y + 1]), clamped);
-          }
+          clamped |= (big > 65504.0f) & (mask != 0u);
           dst = p.v + at * p.dv + c - p.dn;
         }
         st_sector(dst, o);

@@ -560,7 +560,7 @@ int moe_prefill_double_buffered(const moe_layer* layers, int n_layers, const moe
  * the latent vector all heads share (`rank` values) followed by the rotary key
  * (`rope` values).  Rows live in pages of page_tokens tokens; token t of
  * sequence s is row t % page_tokens of page table[s, t / page_tokens], in
- * every layer alike.  [P] section 4.1 pages its cache and shares prefixes the
+ * every layer alike.  [P] section 3.1 pages its cache and shares prefixes the
  * same way; compaction leaves the pool's tail free, memory the elastic expert
  * cache of [P] section 3.3 can take.
  *   pages [n_layers, n_pages, page_tokens, rank + rope] bf16
@@ -643,8 +643,8 @@ int moe_kv_compact(const moe_kv_cache* cache, int32_t* n_live_opt, void* ws, siz
  * [B*Q, heads] or NULL.  The Q tokens are in the cache already.  Products are
  * accumulated in fp32; the probabilities are rounded to bf16 for the second
  * product and divided by the sum of the rounded ones; lse comes from the
- * unrounded ones.  A cached value that is NaN or infinite reaches
- * every query of its sequence.  A query that sees no token (a sequence shorter
+ * unrounded ones.  A cached value that is NaN or infinite reaches the queries
+ * that see its token and no other.  A query that sees no token (a sequence shorter
  * than Q, or a bad id) gets zeros and lse = -inf.
  * shared_tokens > 0 (a multiple of page_tokens): the first shared_tokens
  * tokens of all B sequences are the ones in the pages of seqs[0] (as
@@ -676,8 +676,8 @@ int moe_latent_decode(const moe_kv_cache* cache, int layer, const void* q, const
  * are rounded to bf16, values and probabilities to f16 for the products, which
  * accumulate in fp32, as do the softmax statistics.  An expanded value beyond
  * 65504 in magnitude is clamped and sets MOE_DEV_ERR_RANGE; values below 6e-5
- * keep an absolute precision of 3e-8.  A cached value that is NaN or infinite may
- * reach every query of its sequence.
+ * keep an absolute precision of 3e-8.  A cached value that is NaN or infinite
+ * reaches queries that see its token (through its keys) and no other.
  * kv_tokens: host bound on the sum of the B lengths (sizes the workspace); a
  * sum the workspace has no rows for sets MOE_DEV_ERR_CAPACITY and nothing is
  * written.  A bad id or

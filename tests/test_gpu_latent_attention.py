@@ -439,3 +439,33 @@ def test_prefill_scales(scale):
     out = run_prefill(c, q, [0, 1], [0, 40, 60], 2, 64, 64, w, scale, 190)
     assert c.bits() == 0
     check_prefill(c, rows, q, [0, 1], [0, 40, 60], 2, 64, w, scale, out)
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
+def test_bad_values_reach_only_the_rows_that_see_them(bad):
+    """A token's NaN or infinite latent: queries before it are what they would be without it."""
+    Q, heads = 3, 5
+    c = Paged(12, 32, 256, 32, 2, 6)
+    rows = c.fill([100, 129], seed=100)
+    q, qp, w = make_q(2 * Q, heads, c.row, 101), make_q(60, 2, 96, 102), make_w(2, 128, 256, 103)
+    clean = [x.clone() for x in rows]
+    for s, n in ((0, 100), (1, 129)):          # the last token of each sequence
+        page = int(c.table[s, (n - 1) // 32])
+        c.pages[0, page, (n - 1) % 32, 7] = bad
+        clean[s][n - 1, 7] = 0.0
+    out, _ = run_decode(c, q, [0, 1], Q, heads, 0.1)
+    seen = torch.arange(2 * Q, device=DEV) % Q == Q - 1
+    assert c.bits() == 0 and bool(torch.isfinite(out[~seen]).all())
+    for b, n in ((0, 100), (1, 129)):
+        for i in range(Q - 1):
+            at = b * Q + i
+            check_decode(c, {b: clean[b][:n - Q + i + 1]}, q[at:at + 1], [b], 1, heads, 0.1, out[at:at + 1], None)
+    outp = run_prefill(c, qp, [0, 1], [0, 30, 60], 2, 64, 64, w, 0.1, 229)
+    c.bits()                                   # an infinite value is beyond the f16 range: reported
+    keep = [i for i in range(60) if i % 30 != 29]
+    assert bool(torch.isfinite(outp[keep]).all())
+    for b, n in ((0, 100), (1, 129)):
+        check_prefill(c, {b: clean[b][:n - 1]}, qp[30 * b:30 * b + 29], [b], [0, 29], 2, 64, w, 0.1,
+                      outp[30 * b:30 * b + 29])
+    if bad != bad:
+        assert bool(torch.isnan(out[seen]).any()) and bool(torch.isnan(outp[[29, 59]]).any())
