@@ -765,23 +765,65 @@ decode_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_constant_
 
 // ---------------------------------------------------------------- combine
 // Per query row: its pieces' (m, l, O) in a fixed order (the prefix's pieces,
-// then the sequence's).  Three dependent reads deep (tile sums, statistics,
-// rows); bound by those at small sizes and by L2 at large ones.
+// then the sequence's).  Bound by its dependent reads at small sizes and by L2
+// at large ones.
 //
+// The units of the sequences' line: all, and those before and through sequence b.
+struct LineSums {
+  int total, x0, x1;
+};
+
+// For up to 32 sequences every warp makes them from the lengths while it waits
+// for decode_kernel (whose start says that what came before it is complete, so
+// the lengths are final; read from L2 all the same): one read less in the chain
+// behind it.  Larger batches read the sums that decode_kernel wrote.
+constexpr int kEarly = 32;
+__device__ inline LineSums early_sums(const DecodeParams& p, int b, int lane) {
+  int n = 0;
+  if (lane < p.B) {
+    const int s = __ldcg(p.seqs + lane);
+    int len = s >= 0 && s < p.kv.max_seqs ? __ldcg(p.kv.lens + s) : 0;
+    len = (int)min((long long)max(len, 0), (long long)p.kv.max_blocks << p.kv.page_shift);
+    n = len > p.shared ? (len - p.shared + kTok - 1) / kTok + kHead : 0;
+  }
+  int inc = n;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int u = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += u;
+  }
+  LineSums l;
+  l.total = __shfl_sync(0xffffffffu, inc, 31);
+  l.x1 = __shfl_sync(0xffffffffu, inc, b);
+  l.x0 = l.x1 - __shfl_sync(0xffffffffu, n, b);
+  return l;
+}
+
+// Waits for decode_kernel; the whole warp.
+__device__ inline LineSums wait_for_pieces(const DecodeParams& p, int row, int lane) {
+  const int b = row / (p.Q * p.heads);
+  LineSums l;
+  if (p.B <= kEarly) l = early_sums(p, b, lane);
+  pdl_wait();
+  pdl_trigger();
+  if (p.B > kEarly) l = LineSums{p.plan[p.B], p.plan[b], p.plan[b + 1]};
+  return l;
+}
+
 // Where a row's pieces lie: lane k of a warp looks after piece k.
 struct Pieces {
   const DecodeParams& p;
   int row, b, in_seq, g, x0, x1, per, t0, n_p, n, c0, pr;
   long long pa;
 
-  __device__ Pieces(const DecodeParams& p_, int row_) : p(p_), row(row_) {
+  __device__ Pieces(const DecodeParams& p_, int row_, const LineSums& line) : p(p_), row(row_) {
     const int per_seq = p.Q * p.heads;
     b = row / per_seq;
     in_seq = row - b * per_seq;
     g = in_seq / p.NR;
-    const int total = p.plan[p.B];
-    x0 = p.plan[b];
-    x1 = p.plan[b + 1];
+    const int total = line.total;
+    x0 = line.x0;
+    x1 = line.x1;
     per = per_cta(total, p.teams);
     t0 = x1 > x0 ? (x0 + kHead) / per : 0;                    // from its first tile on
     const int n_s = (x1 > x0 ? (x1 - 1) / per : -1) - t0 + 1;
@@ -855,35 +897,40 @@ __device__ inline void store_lse(const DecodeParams& p, int row, float ref, floa
 
 // Many rows: a warp a row, up to 4 float4 a lane, four pieces in flight.
 __global__ void __launch_bounds__(128) combine_rows_kernel(const DecodeParams p, int rows) {
-  pdl_wait();
-  pdl_trigger();
-  const int row = blockIdx.x * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31, vecs = p.kv.rank / 128;
-  if (row >= rows) return;
-  const Pieces q(p, row);
-  if (q.direct()) return;
+  const int row = min((int)(blockIdx.x * 4 + (threadIdx.x >> 5)), rows - 1), lane = threadIdx.x & 31;
+  const int vecs = p.kv.rank / 128;
+  const LineSums line = wait_for_pieces(p, row, lane);
+  const Pieces q(p, row, line);
+  if (q.direct() || blockIdx.x * 4 + (threadIdx.x >> 5) >= rows) return;
+  float4 x[4][4];
+  float top[4];
+  auto load = [&](int k0) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int k = min(k0 + j, q.n - 1);
+      const size_t at = q.place(k);
+      const float4* from = reinterpret_cast<const float4*>(q.values(k, at)) + lane;
+#pragma unroll
+      for (int y = 0; y < 4; ++y)
+        if (y < vecs && k0 + j < q.n) x[j][y] = __ldcs(from + 32 * y);
+      top[j] = q.stats(k, at).x;
+    }
+  };
+  load(0);                       // the first values come with the statistics
   float ref, l, lr;
   join_stats(q, lane, ref, l, lr);
   float4 acc[4];
 #pragma unroll
   for (int y = 0; y < 4; ++y) acc[y] = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int k0 = 0; k0 < q.n; k0 += 4) {
-    float4 x[4][4];
-    float w[4];
+    if (k0) load(k0);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const int k = min(k0 + j, q.n - 1);
-      const size_t at = q.place(k);
-      w[j] = k0 + j < q.n ? ex2(q.stats(k, at).x - ref) : 0.0f;
-      const float4* from = reinterpret_cast<const float4*>(q.values(k, at)) + lane;
+      const float w = ex2(top[j] - ref);
 #pragma unroll
       for (int y = 0; y < 4; ++y)
-        if (y < vecs && k0 + j < q.n) x[j][y] = __ldcs(from + 32 * y);
+        if (y < vecs && k0 + j < q.n) add_scaled(acc[y], w, x[j][y]);
     }
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-#pragma unroll
-      for (int y = 0; y < 4; ++y)
-        if (y < vecs && k0 + j < q.n) add_scaled(acc[y], w[j], x[j][y]);
   }
 #pragma unroll
   for (int y = 0; y < 4; ++y)
@@ -896,33 +943,36 @@ __global__ void __launch_bounds__(128) combine_rows_kernel(const DecodeParams p,
 constexpr int kSets = 4;
 __global__ void __launch_bounds__(128 * kSets) combine_parts_kernel(const DecodeParams p) {
   __shared__ float4 s_acc[128 * kSets];
-  pdl_wait();
-  pdl_trigger();
   const int row = blockIdx.x, lane = threadIdx.x & 31;
-  const Pieces q(p, row);
+  const LineSums line = wait_for_pieces(p, row, lane);
+  const Pieces q(p, row, line);
   if (q.direct()) return;
-  float ref, l, lr;
-  join_stats(q, lane, ref, l, lr);
   const int v = threadIdx.x % 128, set = threadIdx.x / 128;   // float4 of the row; set of warps
   const bool mine = 4 * v < p.kv.rank;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int k0 = set; k0 < q.n; k0 += 8 * kSets) {   // eight reads in flight
-    float4 x[8];
-    float w[8];
+  float4 x[8];
+  float top[8];
+  auto load = [&](int k0) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const int k = k0 + j * kSets;
       x[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-      w[j] = 0.0f;
+      top[j] = -INFINITY;
       if (k < q.n && mine) {
         const size_t at = q.place(k);
         x[j] = __ldcs(reinterpret_cast<const float4*>(q.values(k, at)) + v);
-        w[j] = ex2(q.stats(k, at).x - ref);
+        top[j] = q.stats(k, at).x;
       }
     }
+  };
+  load(set);                     // the first eight values come with the statistics
+  float ref, l, lr;
+  join_stats(q, lane, ref, l, lr);
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int k0 = set; k0 < q.n; k0 += 8 * kSets) {
+    if (k0 != set) load(k0);
 #pragma unroll
     for (int j = 0; j < 8; ++j)
-      if (k0 + j * kSets < q.n) add_scaled(acc, w[j], x[j]);
+      if (k0 + j * kSets < q.n) add_scaled(acc, ex2(top[j] - ref), x[j]);
   }
   s_acc[threadIdx.x] = acc;
   __syncthreads();
