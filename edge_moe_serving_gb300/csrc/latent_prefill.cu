@@ -48,22 +48,22 @@ struct TokTile {
 
 struct PrefillParams {
   KvView kv;
-  int layer, B, T, heads, dn, dv, rope, kv_rows, max_blocks_q;
-  int splits;               // shares of a query block's tokens
+  int layer, B, T, heads, dn, dv, rope, kv_rows, max_blocks_q, sms;
+  int max_splits;           // shares of a query block's tokens that there is room for
   float scale_log2;
   const __nv_bfloat16* q;
   const int32_t* seqs;
   const int32_t* q_off;
   const __nv_bfloat16* w;
   __nv_bfloat16* out;
-  int32_t* counts;          // [0] query blocks, [1] next work item, [2] tiles of expanded rows
+  int32_t* counts;          // [0] query blocks, [1] next work item, [2] tiles of expanded rows, [3] shares of a block's tokens
   QBlock* blocks;
   TokTile* tiles;           // [kv_rows / 128]
   __nv_bfloat16* k;         // [heads, kv_rows, dn]
   __half* v;                // [heads, kv_rows, dv]
   __nv_bfloat16* r;         // [kv_rows, rope]
-  float* part;              // with splits: [splits, heads, T, dv] unnormalised outputs
-  float2* ml;               // [splits, heads, T] their (m, l)
+  float* part;              // with shares: [shares, heads, T, dv] unnormalised outputs
+  float2* ml;               // [shares, heads, T] their (m, l)
   uint32_t* status;
 };
 
@@ -119,11 +119,38 @@ __device__ inline void scan2(int (&v)[2], int (&total)[2], int (*sh)[kPlanThread
   __syncthreads();
 }
 
+// Shares of the blocks' tokens, where blocks and heads alone leave SMs idle or the longest block would run on alone.
+// The estimate: a step of 128 tokens takes about 2 us, an item half a step more; items of about one length go in whole
+// rounds over the SMs, others fill each other's gaps and the longest is the bound; shares cost a launch and their
+// partial results, written and read at about 4 TB/s.
+__device__ inline int token_shares(const PrefillParams& p, float items, float total, int longest, int shortest) {
+  int best = 1;
+  float least = FLT_MAX;
+  for (int s = 1; s <= p.max_splits && (s == 1 || longest >= 4 * s); ++s) {
+    const float rounds = ceilf(items * s / p.sms), longest_share = (float)longest / s;
+    const float steps = 4 * shortest > 3 * longest ? rounds * longest_share : fmaxf(longest_share, total / p.sms);
+    const float cost = 2.0f * (steps + 0.5f * rounds) + (s > 1 ? 4.0f + s * 2e-6f * p.T * p.heads * p.dv : 0.0f);
+    if (cost < least) {
+      least = cost;
+      best = s;
+    }
+  }
+  return best;
+}
+
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PrefillParams p) {
   __shared__ int sh[2][kPlanThreads / 32];
   __shared__ int s_base[kMaxB], s_len[kMaxB];   // first expanded row and length of each sequence
+  __shared__ int s_longest, s_shortest;         // tiles of tokens that a block of queries sees
+  __shared__ unsigned long long s_total;
   pdl_wait();
   pdl_trigger();
+  if (threadIdx.x == 0) {
+    s_longest = 0;
+    s_shortest = INT_MAX;
+    s_total = 0;
+  }
+  __syncthreads();
   long long rows = 0;
   int blocks = 0;
   for (int b0 = 0; b0 < p.B; b0 += kPlanThreads) {
@@ -147,6 +174,12 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PrefillParams 
       const int base = at < p.kv_rows ? (int)at : p.kv_rows;
       s_base[b] = base;
       s_len[b] = len;
+      if (p.max_splits > 1 && mine > 0) {
+        const int t0 = (len - n + min(kBlock, n) + kTile - 1) / kTile, t1 = (len + kTile - 1) / kTile;
+        atomicMin(&s_shortest, t0);
+        atomicMax(&s_longest, t1);
+        atomicAdd(&s_total, (unsigned long long)(t0 + t1) * mine);    // twice the sum, as if in even steps
+      }
       for (int i = 0; i < mine; ++i) {
         const int x = blocks + v[1] + mine - 1 - i, j0 = i * kBlock;
         if (x < p.max_blocks_q) p.blocks[x] = QBlock{q0 + j0, min(kBlock, n - j0), len - n + j0 + 1, base};
@@ -156,8 +189,10 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PrefillParams 
     blocks += total[1];
   }
   const bool fits = rows <= p.kv_rows;
+  __syncthreads();
   if (threadIdx.x == 0) {
     if (!fits) set_status(p.status, MOE_DEV_ERR_CAPACITY);
+    p.counts[3] = token_shares(p, (float)blocks * p.heads, 0.5f * (float)s_total * p.heads, s_longest, s_shortest);
     p.counts[0] = fits ? min(blocks, p.max_blocks_q) : 0;
     p.counts[1] = 0;
     p.counts[2] = fits ? (int)(rows / kRowAlign) : 0;
@@ -455,27 +490,27 @@ struct Attend {
   static constexpr int kSmem = kRing + kUnits * kUnit + 1024;
 };
 
-// A work item: 256 query rows of one head against one of p.splits shares of their tokens.
+// A work item: 256 query rows of one head against one of `splits` shares of their tokens.
 struct Item {
   int head, row0, rows, limit0, base, block, split;
   int first, tiles[2];   // its first tile of tokens, and how many each query tile takes
 };
 
-__device__ inline bool get_item(const PrefillParams& p, int k, int n_blocks, int group, Item& it) {
-  if (k >= n_blocks * p.heads * p.splits) return false;
+__device__ inline bool get_item(const PrefillParams& p, int k, int n_blocks, int splits, int group, Item& it) {
+  if (k >= n_blocks * p.heads * splits) return false;
   // heads in groups that fill the grid once, so that a group's keys and values are read while they are in L2
-  const int units = n_blocks * p.splits, per = units * group, gi = k / per, in = k - gi * per;
+  const int units = n_blocks * splits, per = units * group, gi = k / per, in = k - gi * per;
   const int gh = min(group, p.heads - gi * group), x = in / gh;
   it.head = gi * group + (in - x * gh);
-  it.block = x / p.splits;
-  it.split = x - it.block * p.splits;
+  it.block = x / splits;
+  it.split = x - it.block * splits;
   const int4 qb = __ldg(reinterpret_cast<const int4*>(p.blocks + it.block));
   it.row0 = qb.x;
   it.rows = qb.y;
   it.limit0 = qb.z;
   it.base = qb.w;
   const int all = (it.limit0 + it.rows - 1 + kTile - 1) / kTile;   // the last row sees the most
-  const int from = (int)((long long)all * it.split / p.splits), to = (int)((long long)all * (it.split + 1) / p.splits);
+  const int from = (int)((long long)all * it.split / splits), to = (int)((long long)all * (it.split + 1) / splits);
   it.first = from;
 #pragma unroll
   for (int g = 0; g < 2; ++g) {
@@ -533,8 +568,8 @@ attend_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
   pdl_trigger();
   const uint32_t tmem = sh.tmem;
   volatile int* abort_flag = &sh.abort;
-  const int n_blocks = p.counts[0];
-  const int group = n_blocks ? max(1, min(p.heads, (int)gridDim.x / (n_blocks * p.splits))) : 1;
+  const int n_blocks = p.counts[0], splits = p.counts[3];
+  const int group = n_blocks ? max(1, min(p.heads, (int)gridDim.x / (n_blocks * splits))) : 1;
   const int rope_chunk = p.rope ? 1 : 0, key_chunks = KC - rope_chunk;
   Item it;
   // A softmax thread holds a row of 128 scores: the first four warps give registers to the other eight
@@ -579,7 +614,9 @@ attend_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
           tma_load_2d_warp(smem0 + g * A::kQ + c * kChunkBytes, &map_q, qf + 8 * g, head * (p.dn + p.rope) + c * kBK,
                            row0 + g * kTile);
       };
-      // the next work item's number, for everyone; fetched one item ahead of its use
+      // The next work item's number, for everyone.  Fetched before the current item's last tile is asked for: early enough
+      // to hide the atomic, late enough that the items go to whoever is free (a whole item earlier, 8192 tokens of 8
+      // heads took 237 us instead of 155).
       auto fetch = [&]() {
         int k = 0;
         ok = warp_wait(&sh.w_empty[n & 1], ((n >> 1) & 1) ^ 1u, abort_flag);
@@ -594,17 +631,16 @@ attend_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
       };
       int ahead = fetch();
       while (ok) {
-        const int k = ahead;
-        if (!__any_sync(0xffffffffu, get_item(p, k, n_blocks, group, it))) break;
-        ahead = fetch();
-        if (!ok) break;
+        if (!__any_sync(0xffffffffu, get_item(p, ahead, n_blocks, splits, group, it))) break;
         const int row0 = (int)uni(it.row0), head = (int)uni(it.head), base = (int)uni(it.base + it.first * kTile);
         const int ta = (int)uni(it.tiles[0]), tb = (int)uni(it.tiles[1]), tiles = max(ta, tb);
         if (ta) load_q(0, q_loads0, head, row0);
         if (ok && tiles) load_k(head, base);
         if (ok && tb) load_q(1, q_loads1, head, row0);
+        if (!tiles) ahead = fetch();
         for (int i = 0; i < tiles && ok; ++i) {
-          load_unit(&map_v, VC, head * p.kv_rows + base + i * kTile, false, 0);
+          if (i + 1 == tiles) ahead = fetch();
+          if (ok) load_unit(&map_v, VC, head * p.kv_rows + base + i * kTile, false, 0);
           if (ok && i + 1 < tiles) load_k(head, base + (i + 1) * kTile);
         }
         if (!ok) break;
@@ -669,7 +705,7 @@ attend_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.w_empty[n & 1]);
         ++n;
-        if (!__any_sync(0xffffffffu, get_item(p, k, n_blocks, group, it))) break;
+        if (!__any_sync(0xffffffffu, get_item(p, k, n_blocks, splits, group, it))) break;
         const int ta = (int)uni(it.tiles[0]), tb = (int)uni(it.tiles[1]), tiles = max(ta, tb);
         if (!tiles) continue;
         ok = warp_wait(&sh.full[slot], par, abort_flag);
@@ -774,7 +810,7 @@ attend_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.w_empty[n & 1]);
         ++n;
-        if (!__any_sync(0xffffffffu, get_item(p, k, n_blocks, group, it))) return false;
+        if (!__any_sync(0xffffffffu, get_item(p, k, n_blocks, splits, group, it))) return false;
         if (g ? it.tiles[1] : it.tiles[0]) return true;
       }
     };
@@ -867,7 +903,7 @@ attend_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
       if (!have && !ok) break;
       if (!warp_wait(&sh.o_full[g], uses++ & 1, abort_flag)) break;
       tc_fence_after();
-      const bool parts = p.splits > 1;
+      const bool parts = splits > 1;
       const size_t at = parts ? ((size_t)split * p.heads + head) * p.T + row : row * p.heads + head;
       if (parts && mine) p.ml[at] = make_float2(m, l);
       const float inv_l = 1.0f / l;
@@ -904,44 +940,52 @@ attend_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
 }
 
 // ---------------------------------------------------------------- combine of the token shares
-// One warp per (query row, head): the shares' outputs weighted by their (m, l), in share order.  A share in which the
-// row's tile had no tokens wrote nothing: which ones did follows from the block, as in get_item.
+// The shares' outputs weighted by their (m, l), in share order: a thread has four entries of a (query row, head), and
+// its shares' values are asked for together with their statistics.  A share in which the row's tile had no tokens wrote
+// nothing: which ones did follows from the block, as in get_item.
 __global__ void __launch_bounds__(256) combine_splits_kernel(const PrefillParams p) {
   pdl_wait();
   pdl_trigger();
-  const int lane = threadIdx.x & 31, block = blockIdx.x;
-  if (block >= p.counts[0]) return;
+  const int block = blockIdx.x, splits = p.counts[3];
+  if (block >= p.counts[0] || splits == 1) return;
   const int4 qb = __ldg(reinterpret_cast<const int4*>(p.blocks + block));
-  const int all = (qb.z + qb.y - 1 + kTile - 1) / kTile;
-  for (int x = blockIdx.y * 8 + (threadIdx.x >> 5); x < qb.y * p.heads; x += gridDim.y * 8) {
-    const int j = x / p.heads, head = x - j * p.heads;
+  const int all = (qb.z + qb.y - 1 + kTile - 1) / kTile, vecs = p.dv / 4;
+  for (int x = blockIdx.y * blockDim.x + threadIdx.x; x < qb.y * p.heads * vecs; x += gridDim.y * blockDim.x) {
+    const int v = x % vecs, y = x / vecs, j = y / p.heads, head = y - j * p.heads;
     const int last = min(qb.y, (j / kTile + 1) * kTile) - 1, mine = (qb.z + last + kTile - 1) / kTile;
     const size_t row = (size_t)qb.x + j;
-    float top = -INFINITY;
     float2 ml[kMaxSplits];
+    float4 o[kMaxSplits];
+    float ref = -INFINITY;
 #pragma unroll
     for (int s = 0; s < kMaxSplits; ++s) {
       ml[s] = make_float2(-INFINITY, 0.0f);
-      if (s < p.splits && (int)((long long)all * s / p.splits) < min(mine, (int)((long long)all * (s + 1) / p.splits)))
-        ml[s] = p.ml[((size_t)s * p.heads + head) * p.T + row];
-      top = fmaxf(top, ml[s].x);
+      o[s] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      if (s < splits && (int)((long long)all * s / splits) < min(mine, (int)((long long)all * (s + 1) / splits))) {
+        const size_t at = ((size_t)s * p.heads + head) * p.T + row;
+        ml[s] = p.ml[at];
+        o[s] = __ldcs(reinterpret_cast<const float4*>(p.part + at * p.dv) + v);
+      }
     }
-    const float ref = top == -INFINITY ? 0.0f : top;
+#pragma unroll
+    for (int s = 0; s < kMaxSplits; ++s) ref = fmaxf(ref, ml[s].x);
+    ref = ref == -INFINITY ? 0.0f : ref;
     float l = 0.0f;
-    float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
     for (int s = 0; s < kMaxSplits; ++s) {
-      if (s >= p.splits || (ml[s].x == -INFINITY && ml[s].y == 0.0f)) continue;
+      if (ml[s].x == -INFINITY && ml[s].y == 0.0f) continue;   // the row saw none of the share's tokens
       const float w = ex2(ml[s].x - ref);
       l = fmaf(w, ml[s].y, l);
-      const float* o = p.part + (((size_t)s * p.heads + head) * p.T + row) * p.dv;
-#pragma unroll
-      for (int y = 0; y < 4; ++y)
-        if (lane + 32 * y < p.dv) acc[y] = fmaf(w, o[lane + 32 * y], acc[y]);
+      acc.x = fmaf(w, o[s].x, acc.x);
+      acc.y = fmaf(w, o[s].y, acc.y);
+      acc.z = fmaf(w, o[s].z, acc.z);
+      acc.w = fmaf(w, o[s].w, acc.w);
     }
-#pragma unroll
-    for (int y = 0; y < 4; ++y)
-      if (lane + 32 * y < p.dv) p.out[(row * p.heads + head) * p.dv + lane + 32 * y] = __float2bfloat16_rn(acc[y] / l);
+    uint2 packed;
+    packed.x = bf16x2_of(acc.x / l, acc.y / l);
+    packed.y = bf16x2_of(acc.z / l, acc.w / l);
+    reinterpret_cast<uint2*>(p.out + (row * p.heads + head) * p.dv)[v] = packed;
   }
 }
 
@@ -956,21 +1000,11 @@ bool prefill_shape_ok(int B, int T, int heads, int dn, int dv, int kv_tokens) {
   return (long long)T * heads <= INT_MAX && ((long long)kv_tokens + 128LL * B) * heads <= INT_MAX;
 }
 
-// Shares of the tokens where the query blocks and heads alone leave SMs idle: the count whose whole rounds over the
-// SMs come nearest to even work, with 2% charged per share for its partial results (1000 queries of 16 heads over
-// 16000 tokens: 64 items, 2 shares).
-int token_shares(long long items) {
-  const int sms = num_sms();
-  int best = 1;
-  float least = 1e30f;
-  for (int s = 1; s <= kMaxSplits && items < sms; ++s) {
-    const float cost = (float)((items * s + sms - 1) / sms) / s + 0.02f * s;
-    if (cost < least) {
-      least = cost;
-      best = s;
-    }
-  }
-  return best;
+// Shares of a block's tokens that a call has room for: up to about two items per SM (the plan takes what pays).  From
+// the queries' number alone, so that a loose kv_tokens changes no result.
+int most_shares(long long items) {
+  const long long s = 2LL * num_sms() / items;
+  return s < 1 ? 1 : s > kMaxSplits ? kMaxSplits : (int)s;
 }
 
 PrefillWs prefill_ws(int B, int T, int heads, int dn, int dv, int rope, int kv_tokens) {
@@ -990,7 +1024,7 @@ PrefillWs prefill_ws(int B, int T, int heads, int dn, int dv, int rope, int kv_t
   at += align_up((size_t)heads * w.rows * dv * 2, 256);
   w.r = at;
   at += align_up((size_t)w.rows * (rope ? rope : 8) * 2, 256);
-  w.splits = token_shares((long long)w.n_blocks * heads);
+  w.splits = most_shares((long long)w.n_blocks * heads);
   w.part = at;
   if (w.splits > 1) at += align_up((size_t)w.splits * heads * T * dv * sizeof(float), 256);
   w.ml = at;
@@ -1039,8 +1073,8 @@ int launch_prefill(const PrefillParams& p, cudaStream_t s) {
                    : kc == 2 ? launch_attend<2, 1>(mq, mk, mr, mv, p, s)
                              : launch_attend<1, 1>(mq, mk, mr, mv, p, s));
   }
-  if (e == cudaSuccess && p.splits > 1)
-    e = launch_k(combine_splits_kernel, dim3(p.max_blocks_q, 4 * num_sms() / p.max_blocks_q + 1), 256, 0, s, p);
+  if (e == cudaSuccess && p.max_splits > 1)
+    e = launch_k(combine_splits_kernel, dim3(p.max_blocks_q, 8 * num_sms() / p.max_blocks_q + 1), 256, 0, s, p);
   return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
@@ -1099,7 +1133,8 @@ int moe_latent_prefill(const moe_kv_cache* cache, int layer, const void* q, cons
   p.k = reinterpret_cast<__nv_bfloat16*>(b + w.k);
   p.v = reinterpret_cast<__half*>(b + w.v);
   p.r = reinterpret_cast<__nv_bfloat16*>(b + w.r);
-  p.splits = w.splits;
+  p.max_splits = w.splits;
+  p.sms = num_sms();
   p.part = reinterpret_cast<float*>(b + w.part);
   p.ml = reinterpret_cast<float2*>(b + w.ml);
   p.status = dev_status;
