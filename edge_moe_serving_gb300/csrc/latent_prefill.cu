@@ -466,6 +466,21 @@ __device__ inline void tc_mma_ta_warp(uint32_t d_tmem, uint32_t a_tmem, uint64_t
       : "memory");
 }
 
+// Which of three barriers are past their phases (bits 0, 1, 2); does not wait.
+__device__ inline uint32_t test_three(uint64_t* a, uint32_t pa, uint64_t* b, uint32_t pb, uint64_t* c, uint32_t pc) {
+  uint32_t x, y, z;
+  asm volatile(
+      "{\n .reg .pred p, q, r;\n"
+      " mbarrier.test_wait.parity.shared::cta.b64 p, [%3], %4;\n"
+      " mbarrier.test_wait.parity.shared::cta.b64 q, [%5], %6;\n"
+      " mbarrier.test_wait.parity.shared::cta.b64 r, [%7], %8;\n"
+      " selp.u32 %0, 1, 0, p;\n selp.u32 %1, 2, 0, q;\n selp.u32 %2, 4, 0, r;\n}\n"
+      : "=r"(x), "=r"(y), "=r"(z)
+      : "r"(smem_u32(a)), "r"(pa), "r"(smem_u32(b)), "r"(pb), "r"(smem_u32(c)), "r"(pc)
+      : "memory");
+  return x | y | z;
+}
+
 // fp32 accumulation, f16 operands, A and B K-major
 __host__ __device__ constexpr uint32_t idesc_f16(int M, int N) { return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24); }
 struct Shared {
@@ -726,28 +741,31 @@ attend_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
           issue_s(1, slot);
           if (tb == 1) tc_commit_warp(&sh.q_empty[1]);
         }
-        tc_commit_warp(&sh.empty[slot]);
         step(slot, par);
         ++ropes;
-        ok = warp_wait(&sh.full[slot], par, abort_flag);       // V(0)
-        if (!ok) break;
-        // The products' queue is short (a few instructions): between two groups of them the fewest waits and commits
-        // are left, the others stand behind a group that is still being worked off.  Tile b sees at least what a sees.
+        // The products' queue is short (a few instructions), so whatever stands between two groups of them shows: one
+        // look at the barriers of tile a's two products, and few commits (the softmax warps let go of the keys' places;
+        // the values' go back here, at once).  Tile b sees at least what a sees.
         for (int i = 0; i < tiles; ++i) {
           const uint32_t acc = i ? 1u : 0u;
-          const bool more = i + 1 < tiles;
-          int sk = slot;                                       // K(i+1)
+          const bool more = i + 1 < tiles, in_a = i < ta;
+          int sk = slot;                                       // K(i+1); slot is V(i)'s
           uint32_t pk = par;
           step(sk, pk);
-          if (i < ta) {
-            ok = warp_wait(&sh.p_ready[0], p_uses0++ & 1, abort_flag);
-            if (!ok) break;
-            tc_fence_after();
+          uint64_t* const p_bar = in_a ? &sh.p_ready[0] : &sh.full[slot];
+          const uint32_t p_par = in_a ? p_uses0 & 1 : par;
+          const uint32_t seen = __reduce_and_sync(
+              0xffffffffu, test_three(&sh.full[slot], par, p_bar, p_par, &sh.full[more ? sk : slot], more ? pk : par));
+          ok = ((seen & 1) || warp_wait(&sh.full[slot], par, abort_flag)) && ((seen & 2) || warp_wait(p_bar, p_par, abort_flag));
+          if (!ok) break;
+          tc_fence_after();
+          if (in_a) {
+            ++p_uses0;
             issue_pv(0, slot, acc);
             if (i + 1 == ta) tc_commit_warp(&sh.o_full[0]);
             if (!tb) tc_commit_warp(&sh.empty[slot]);
           }
-          if (more) {
+          if (more && !(seen & 4)) {
             ok = warp_wait(&sh.full[sk], pk, abort_flag);
             if (!ok) break;
             tc_fence_after();
@@ -764,22 +782,16 @@ attend_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
             if (i + 1 == tb) tc_commit_warp(&sh.o_full[1]);
             tc_commit_warp(&sh.empty[slot]);
           }
-          slot = sk;
-          par = pk;
-          step(slot, par);                                     // V(i+1)
-          if (!more) {
-            slot = sk;                                         // there is no K(i+1): the next item's keys
-            par = pk;
-            break;
-          }
-          ok = warp_wait(&sh.full[slot], par, abort_flag);
-          if (!ok) break;
           if (i + 1 < tb) {
             issue_s(1, sk);
             if (i + 2 == tb) tc_commit_warp(&sh.q_empty[1]);
           }
-          tc_commit_warp(&sh.empty[sk]);
-          ++ropes;
+          slot = sk;
+          par = pk;
+          if (more) {
+            step(slot, par);                                   // V(i+1); else the next item's K(0)
+            ++ropes;
+          }
         }
         if (!ok) break;
       }
@@ -801,6 +813,9 @@ attend_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
     const float scale = p.scale_log2;
     const bool neg = scale < 0.0f;
     const float unseen = neg ? INFINITY : -INFINITY;   // what a token out of sight scores
+    // A key tile's last reader is tile b's S (a's, without a b): when it is known to be over, one lane of that tile's warps
+    // lets go of the place.
+    int at_k = 0;   // the place of the step's keys
     // the next work item with tokens for this tile
     auto next_item = [&]() {
       for (;;) {
@@ -812,18 +827,21 @@ attend_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
         ++n;
         if (!__any_sync(0xffffffffu, get_item(p, k, n_blocks, splits, group, it))) return false;
         if (g ? it.tiles[1] : it.tiles[0]) return true;
+        at_k = (at_k + 2 * max(it.tiles[0], it.tiles[1])) % A::kUnits;
       }
     };
     bool have = next_item();
     while (have) {
       const int tiles = g ? it.tiles[1] : it.tiles[0], first = it.first, in_block = g * kTile + r;
       const int limit = it.limit0 + in_block - first * kTile;
-      const bool mine = in_block < it.rows;
+      const bool mine = in_block < it.rows, releases = g == 1 || it.tiles[1] == 0;
       float m = -INFINITY, l = 0.0f;
       for (int i = 0; i < tiles; ++i, ++steps) {
         ok = warp_wait(&sh.s_full[g], steps & 1, abort_flag);
         if (!ok) break;
         tc_fence_after();
+        if (releases && quarter == 0 && lane == 0) mbar_arrive(&sh.empty[at_k]);
+        at_k = at_k + 2 >= A::kUnits ? at_k + 2 - A::kUnits : at_k + 2;
         float s[kTile];
         uint32_t(&u)[kTile] = reinterpret_cast<uint32_t(&)[kTile]>(s);
 #pragma unroll
@@ -896,6 +914,7 @@ attend_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
         l += (sum0.x + sum0.y) + (sum1.x + sum1.y);
       }
       if (!ok) break;
+      if (!g) at_k = (at_k + 2 * (max(it.tiles[0], it.tiles[1]) - tiles)) % A::kUnits;   // a's item goes on without it
       // where this item's results go; the next item's numbers come before the wait for the last product
       const size_t row = (size_t)it.row0 + in_block;
       const int head = it.head, split = it.split;
