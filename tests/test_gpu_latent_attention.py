@@ -469,3 +469,23 @@ def test_bad_values_reach_only_the_rows_that_see_them(bad):
                       outp[30 * b:30 * b + 29])
     if bad != bad:
         assert bool(torch.isnan(out[seen]).any()) and bool(torch.isnan(outp[[29, 59]]).any())
+
+
+@pytest.mark.parametrize("B", [32, 33, 70])
+def test_prefill_of_many_sequences(B):
+    """Around and past the 32 sequences whose plan needs no launch of its own; some without queries, some empty."""
+    lens = [0 if i % 9 == 4 else 1 + (37 * i) % 200 for i in range(B)]
+    new = [0 if i % 5 == 3 else min(n, 1 + (11 * i) % 60) for i, n in enumerate(lens)]
+    c = Paged(sum(-(-n // 16) for n in lens) + 3, 16, 128, 16, B, 14)
+    rows = c.fill(lens, seed=B)
+    offsets = [0]
+    for n in new:
+        offsets.append(offsets[-1] + n)
+    q, w = make_q(offsets[-1], 3, 80, 104), make_w(3, 128, 128, 105)
+    out = run_prefill(c, q, list(range(B)), offsets, 3, 64, 64, w, 0.12, sum(lens))
+    assert c.bits() == 0
+    some = [b for b in range(B) if new[b]]
+    check_prefill(c, rows, q, some, [offsets[b] for b in some] + [offsets[-1]], 3, 64, w, 0.12, out)
+    # no room for the lengths: reported, nothing written
+    run_prefill(c, q, list(range(B)), offsets, 3, 64, 64, w, 0.12, 1)
+    assert c.bits() == (moe.MOE_DEV_ERR_CAPACITY if sum(-(-n // 128) for n in lens) > B else 0)
