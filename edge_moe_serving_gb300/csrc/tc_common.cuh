@@ -120,16 +120,7 @@ __device__ inline void tma_load_3d_hint_warp(uint32_t dst, const CUtensorMap* ma
 __device__ inline void prefetch_map(const CUtensorMap* map) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
 }
-// Asks for `bytes` (a multiple of 16) from a 16-byte aligned address into L2; one elected lane of a converged warp.
-__device__ inline void prefetch_l2_warp(const void* p, uint32_t bytes) {
-  asm volatile(
-      "{\n .reg .pred q;\n elect.sync _|q, 0xffffffff;\n @q cp.async.bulk.prefetch.L2.global [%0], %1;\n}\n" ::"l"(p),
-      "r"(bytes)
-      : "memory");
-}
-__device__ inline void prefetch_l2(const void* p, uint32_t bytes) {
-  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
-}
+// The default L2 policy, where a copy takes one.
 __device__ inline uint64_t l2_normal() {
   uint64_t pol;
   asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(pol));
