@@ -19,9 +19,19 @@
 // Work: the sequences' tiles form one line that is cut evenly over the CTAs
 // (teams of G CTAs where a sequence has G > 1 row tiles, so that its rows are
 // read from HBM once and from L2 by the others).  A cut sequence leaves fp32
-// partial (O, m, l) per piece; combine_kernel joins the pieces in order.  A
+// partial (O, m, l) per piece; a combine kernel joins the pieces in order.  A
 // shared prefix is a second line: row tiles over the whole batch's query rows
 // against the prefix's tiles.
+//
+// Bound: a tile with its 64 rows moves 322 KB through shared memory (Q and K for
+// S, V and P for O, the copies in), 2515 cycles at 128 bytes a cycle, and takes
+// 3050 to 3750; its products alone take 2230.  With fewer heads the rows of the
+// cache bound it, and for short sequences the chain launch, lengths, table, copy,
+// S, softmax, O, combine.  Measured, rank 512 and rope 64:
+//   1 x 333 tokens, 32 heads              12.9 us
+//   32 x 250..6001, 64 heads              36 us   3.2 TB/s of cached rows
+//   4 x 40001..65537, 128 heads, 2 tokens 168 us  0.67 PFLOP/s
+//   64 x 16384 shared + 17..1500, 32 heads 125 us 0.61 PFLOP/s
 //
 // Roles (224 threads): warp 0 = TMA producer, warp 1 = issuer of S (and TMEM
 // owner), warps 2..5 = softmax, rescaling and epilogue, warp 6 = issuer of the
