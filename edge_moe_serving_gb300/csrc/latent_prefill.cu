@@ -18,7 +18,7 @@
 //
 // Measured, rank 512, rope 64, keys and values of 128:
 //   5 prompts of 1..300 tokens, 32 heads     33 us
-//   1000 tokens over 15001, 16 heads         201 us  1.12 PFLOP/s
+//   1000 tokens over 15001, 16 heads         198 us  1.14 PFLOP/s
 //   8192 tokens, 32 heads                    530 us  1.43 PFLOP/s
 // of which expand_kernel takes about 58 us in the last two.
 #include <cfloat>
@@ -370,8 +370,20 @@ expand_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
     int loaded = 0, stage = 0, fills = 0;
     uint32_t par = 1;
     bool ok = true;
+    auto load_w = [&](int head, int c) {
+      ok = ok && warp_wait(&sh.b_empty[stage], par, abort_flag);
+      if (!ok) return;
+      mbar_expect_tx_warp(bf + 8 * stage, (uint32_t)(N * 128));
+      tma_load_2d_warp(b0 + stage * kExStage, &map_w, bf + 8 * stage, c * kBK, head * N);
+      ++fills;
+      if (++stage == kExStages) {
+        stage = 0;
+        par ^= 1u;
+      }
+    };
     for (int u = u0; ok && u < u1; ++u) {
       const int tile = u / p.heads, head = u - tile * p.heads;
+      int c0 = 0;
       if (u == u0 || head == 0) {                          // another token tile
         const int4 d = tile_of(p, sh, tile);   // sequence, first token, length
         const int nb = (int)uni((min(kTile, d.z - d.y) + box - 1) / box);
@@ -395,19 +407,12 @@ expand_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
 #pragma unroll
           for (int i = 0; i < kTile / 16; ++i)
             if (i < nb) tma_load_2d_warp(smem0 + c * kChunkBytes + i * box * 128, &map_x, af + 8 * c, c * kBK, rows[i]);
+          if (c < kExStages) load_w(head, c);              // between them: the first product needs both
         }
-      }
-      for (int c = 0; c < chunks; ++c) {
-        ok = warp_wait(&sh.b_empty[stage], par, abort_flag);
         if (!ok) break;
-        mbar_expect_tx_warp(bf + 8 * stage, (uint32_t)(N * 128));
-        tma_load_2d_warp(b0 + stage * kExStage, &map_w, bf + 8 * stage, c * kBK, head * N);
-        ++fills;
-        if (++stage == kExStages) {
-          stage = 0;
-          par ^= 1u;
-        }
+        c0 = min(chunks, kExStages);
       }
+      for (int c = c0; ok && c < chunks; ++c) load_w(head, c);
     }
     volatile int no_abort = 0;
     if (loaded)
