@@ -44,6 +44,7 @@
 #include <type_traits>
 
 #include "kv_common.cuh"
+#include "latent_line.h"
 #include "tc_common.cuh"
 
 namespace moe {
@@ -51,26 +52,20 @@ namespace {
 
 using namespace tc;
 
-constexpr int kTok = 64;                 // tokens of a tile
-constexpr int kRows = 64;                // query rows of a tile at most
 constexpr int kChunk = kTok * kBK * 2;   // 8 KB: 64 tokens x 64 entries (also 64 query rows x 64 entries)
 constexpr int kMaxPairs = 4;             // 128-entry slices of the latent
 constexpr int kMaxSlots = 4;             // tiles in flight
 constexpr int kBatch = 512;              // sequences of one launch (lengths and tile sums in shared memory)
 constexpr int kThreads = 224;
 constexpr int kSoftThreads = 128;
-constexpr int kHead = 2;                 // tiles' worth of time that a piece costs beside its tiles
 constexpr int kTmemCols = 512;
 constexpr int kSCol = 256;               // S tiles at columns 256 and 320; O slices at 0, 64, 128, 192
 constexpr float kGrow = 8.0f;            // log2 of the growth of a row's maximum that forces a rescaling
 
-struct DecodeParams {
+struct DecodeParams : LineShape {
   KvView kv;
-  int layer, B, Q, heads, rope, shared;
+  int layer, rope;
   int pairs, slots;          // rank / 128; tiles in flight
-  int G, NR, teams;          // row tiles of a sequence, their rows, and CTA teams
-  int Gp, NRp, np, ctas;     // row tiles of the prefix, their rows, prefix tiles; CTAs of the grid
-  int per_p;                 // tiles of the prefix line that a CTA takes
   float scale_log2;          // scale * log2(e): the exponentials are powers of two
   const int32_t* seqs;
   const int32_t* prefix_seq;
@@ -92,9 +87,6 @@ struct Seg {
   float4* ml;
   bool prefix;
 };
-
-__device__ __host__ inline int up16(int v) { return (v + 15) & ~15; }
-__device__ __host__ inline int per_cta(unsigned tiles, unsigned parts) { return (int)((tiles + parts - 1) / parts); }
 
 // A CTA's pieces: first of the prefix line, then of the sequences' line, which
 // the CTAs take from the other end (calls too small for both lines to fill the
@@ -778,11 +770,6 @@ decode_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_constant_
 // then the sequence's).  Bound by its dependent reads at small sizes and by L2
 // at large ones.
 //
-// The units of the sequences' line: all, and those before and through sequence b.
-struct LineSums {
-  int total, x0, x1;
-};
-
 // For up to 32 sequences every warp makes them from the lengths while it waits
 // for decode_kernel (whose start says that what came before it is complete, so
 // the lengths are final; read from L2 all the same): one read less in the chain
@@ -820,57 +807,21 @@ __device__ inline LineSums wait_for_pieces(const DecodeParams& p, int row, int l
   return l;
 }
 
-// Where a row's pieces lie: lane k of a warp looks after piece k.
-struct Pieces {
-  const DecodeParams& p;
-  int row, b, in_seq, g, x0, x1, per, t0, n_p, n, c0, pr;
-  long long pa;
-
-  __device__ Pieces(const DecodeParams& p_, int row_, const LineSums& line) : p(p_), row(row_) {
-    const int per_seq = p.Q * p.heads;
-    b = row / per_seq;
-    in_seq = row - b * per_seq;
-    g = in_seq / p.NR;
-    const int total = line.total;
-    x0 = line.x0;
-    x1 = line.x1;
-    per = per_cta(total, p.teams);
-    t0 = x1 > x0 ? (x0 + kHead) / per : 0;                    // from its first tile on
-    const int n_s = (x1 > x0 ? (x1 - 1) / per : -1) - t0 + 1;
-    n_p = c0 = pr = 0;
-    pa = 0;
-    if (p.np) {
-      pr = row / p.NRp;
-      pa = (long long)pr * p.np;
-      c0 = (int)(pa / p.per_p);
-      n_p = (int)((pa + p.np - 1) / p.per_p) - c0 + 1;
-    }
-    n = n_p + n_s;
-  }
-  __device__ bool direct() const { return n_p == 0 && n == 1; }   // written by decode_kernel
-  // piece k's index among all rows of its line's pieces
-  __device__ size_t place(int k) const {
-    if (k < n_p) {
-      const long long from = (long long)(c0 + k) * p.per_p;
-      const int slot = (pa >= from && pa + p.np <= from + p.per_p) ? 2 * p.ctas + pr : 2 * (c0 + k) + (pa > from ? 1 : 0);
-      return (size_t)slot * p.NRp + (row - pr * p.NRp);
-    }
-    const int t = t0 + k - n_p;
-    const long long from = (long long)t * per;
-    const int slot = (x0 + kHead >= from && x1 <= from + per) ? 2 * p.teams * p.G + b * p.G + g
-                                                              : 2 * (t * p.G + g) + (x0 > from ? 1 : 0);
-    return (size_t)slot * p.NR + (in_seq - g * p.NR);
-  }
-  __device__ float4 stats(int k, size_t at) const { return (k < n_p ? p.ml_p : p.ml_s)[at]; }
-  __device__ const float* values(int k, size_t at) const { return (k < n_p ? p.part_p : p.part_s) + at * p.kv.rank; }
-};
+// Piece k of a row, whose place is `at`: its (m, l, l of the rounded probabilities), and its values.
+__device__ inline float4 piece_stats(const DecodeParams& p, const Pieces& q, int k, size_t at) {
+  return (k < q.n_p ? p.ml_p : p.ml_s)[at];
+}
+__device__ inline const float4* piece_values(const DecodeParams& p, const Pieces& q, int k, size_t at) {
+  return reinterpret_cast<const float4*>((k < q.n_p ? p.part_p : p.part_s) + at * p.kv.rank);
+}
 
 // The row's reference maximum and its two sums over all pieces, in every lane.
-__device__ inline void join_stats(const Pieces& q, int lane, float& ref, float& l, float& lr) {
+__device__ inline void join_stats(const DecodeParams& p, const Pieces& q, int lane, float& ref, float& l, float& lr) {
   float top = -INFINITY;
   l = lr = 0.0f;
-  for (int k = lane; k < q.n; k += 32) {
-    const float4 ml = q.stats(k, q.place(k));
+  size_t at;
+  for (int k = lane; q.find(k, at); k += 32) {
+    const float4 ml = piece_stats(p, q, k, at);
     const float now = fmaxf(top, ml.x), to = now == -INFINITY ? 0.0f : now;
     const float f = ex2(top - to), w = ex2(ml.x - to);
     l = fmaf(l, f, ml.y * w);
@@ -917,18 +868,20 @@ __global__ void __launch_bounds__(128) combine_rows_kernel(const DecodeParams p,
   auto load = [&](int k0) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const int k = min(k0 + j, q.n - 1);
-      const size_t at = q.place(k);
-      const float4* from = reinterpret_cast<const float4*>(q.values(k, at)) + lane;
+      top[j] = -INFINITY;
+      size_t at;
+      if (q.find(k0 + j, at)) {
+        const float4* from = piece_values(p, q, k0 + j, at) + lane;
 #pragma unroll
-      for (int y = 0; y < 4; ++y)
-        if (y < vecs && k0 + j < q.n) x[j][y] = __ldcs(from + 32 * y);
-      top[j] = q.stats(k, at).x;
+        for (int y = 0; y < 4; ++y)
+          if (y < vecs) x[j][y] = __ldcs(from + 32 * y);
+        top[j] = piece_stats(p, q, k0 + j, at).x;
+      }
     }
   };
   load(0);                       // the first values come with the statistics
   float ref, l, lr;
-  join_stats(q, lane, ref, l, lr);
+  join_stats(p, q, lane, ref, l, lr);
   float4 acc[4];
 #pragma unroll
   for (int y = 0; y < 4; ++y) acc[y] = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -967,16 +920,16 @@ __global__ void __launch_bounds__(128 * kSets) combine_parts_kernel(const Decode
       const int k = k0 + j * kSets;
       x[j] = make_float4(0.f, 0.f, 0.f, 0.f);
       top[j] = -INFINITY;
-      if (k < q.n && mine) {
-        const size_t at = q.place(k);
-        x[j] = __ldcs(reinterpret_cast<const float4*>(q.values(k, at)) + v);
-        top[j] = q.stats(k, at).x;
+      size_t at;
+      if (mine && q.find(k, at)) {
+        x[j] = __ldcs(piece_values(p, q, k, at) + v);
+        top[j] = piece_stats(p, q, k, at).x;
       }
     }
   };
   load(set);                     // the first eight values come with the statistics
   float ref, l, lr;
-  join_stats(q, lane, ref, l, lr);
+  join_stats(p, q, lane, ref, l, lr);
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int k0 = set; k0 < q.n; k0 += 8 * kSets) {
     if (k0 != set) load(k0);
@@ -993,53 +946,29 @@ __global__ void __launch_bounds__(128 * kSets) combine_parts_kernel(const Decode
 }
 
 // ---------------------------------------------------------------- host side
-struct Tiles {
-  int n, rows;   // row tiles and their rows
-};
-// rows split into tiles of at most 64, evenly, in multiples of 16
-Tiles row_tiles(long long rows) {
-  Tiles t;
-  t.n = (int)((rows + kRows - 1) / kRows);
-  t.rows = up16((int)((rows + t.n - 1) / t.n));
-  t.n = (int)((rows + t.rows - 1) / t.rows);
-  return t;
-}
-
 struct DecodeWs {
   size_t plan, part_s, ml_s, part_p, ml_p, bytes;
 };
 
 void fill_shape(DecodeParams& p, const moe_kv_cache& c, int B, int Q, int heads, int shared) {
-  p.B = B;
-  p.Q = Q;
-  p.heads = heads;
-  p.shared = shared;
+  set_line(p, B, Q, heads, shared, num_sms());
   p.rope = c.rope;
   p.pairs = c.rank / 128;
-  p.ctas = num_sms();
-  const Tiles s = row_tiles((long long)Q * heads), f = row_tiles((long long)B * Q * heads);
-  p.G = s.n;
-  p.NR = s.rows;
-  p.teams = p.ctas / s.n;
-  p.np = (shared + kTok - 1) / kTok;
-  p.Gp = p.np ? f.n : 0;
-  p.NRp = f.rows;
-  p.per_p = (int)(((long long)p.Gp * p.np + p.ctas - 1) / p.ctas);
 }
 
 DecodeWs decode_ws(const DecodeParams& p, int rank) {
   DecodeWs w;
-  const size_t ns = (size_t)2 * p.teams * p.G + (p.np ? (size_t)p.B * p.G : 0), np = p.np ? (size_t)2 * p.ctas + p.Gp : 0;
+  const size_t ns = suffix_rows(p), np = prefix_rows(p);
   w.plan = 0;
   size_t at = align_up((size_t)(p.B + 1) * sizeof(int32_t), 256);
   w.part_s = at;
-  at += align_up(ns * p.NR * rank * sizeof(float), 256);
+  at += align_up(ns * rank * sizeof(float), 256);
   w.ml_s = at;
-  at += align_up(ns * p.NR * sizeof(float4), 256);
+  at += align_up(ns * sizeof(float4), 256);
   w.part_p = at;
-  at += align_up(np * p.NRp * rank * sizeof(float), 256);
+  at += align_up(np * rank * sizeof(float), 256);
   w.ml_p = at;
-  at += align_up(np * p.NRp * sizeof(float4), 256);
+  at += align_up(np * sizeof(float4), 256);
   w.bytes = at;
   return w;
 }

@@ -224,6 +224,22 @@ def test_decode_long_ragged_batch():
         check_decode(c, rows, q, seqs, 1, heads, 0.07, out, lse)
 
 
+def test_decode_padded_batch():
+    """A batch of fixed size whose unused slots are -1, with more query rows than SMs, in a workspace of exactly the
+    size asked for: zeros and -infinity for the padding and for empty sequences, also in front of the others."""
+    c = Paged(40, 32, 512, 64, 6, 12)
+    rows = c.fill([0, 300, 64, 0, 17], seed=10)
+    for seqs in ([-1, -1, 0, 1, 2, 3, 4, -1], [-1] * 8, [0, 3, 0], [1, -1, 2, 99, -1, -1, -1, -1]):
+        q = make_q(len(seqs), 64, c.row, 11)
+        out, lse = run_decode(c, q, seqs, 1, 64, 0.07)
+        assert c.bits() == (0 if seqs == [0, 3, 0] else moe.MOE_DEV_ERR_BAD_SEQ)
+        for b, s in enumerate(seqs):
+            if not 0 <= s < 6 or not len(rows[s]):
+                assert bool((out[b] == 0).all()) and bool((lse[b] == -math.inf).all())
+            else:
+                check_decode(c, rows, q[b:b + 1], [s], 1, 64, 0.07, out[b:b + 1], lse[b:b + 1])
+
+
 # ------------------------------------------------------------------ expanded form
 def run_prefill(c, q, seqs, offsets, heads, dn, dv, w, scale, kv_tokens, layer=0):
     B, T = len(seqs), q.shape[0]
