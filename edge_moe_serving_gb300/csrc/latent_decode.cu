@@ -250,9 +250,9 @@ __device__ inline void store_matrices(uint32_t addr, uint32_t a, uint32_t b, uin
                : "memory");
 }
 
-struct Shared {
+struct alignas(16) Shared {   // its size is what the dynamic shared memory leaves free
   uint64_t full[kMaxSlots][kMaxPairs + 1], empty[kMaxSlots][kMaxPairs + 1];   // per 128-entry pair, then the rotary chunk
-  uint64_t q_full, q_empty, s_full[2], s_empty[2], p_full, pv_done[2], drain[2];
+  uint64_t q_full, q_empty, s_full[2], s_empty[2], p_full[kPBars], pv_done[2], drain[2];
   uint32_t tmem;
   int abort;
   float factor[kRows];   // rescaling of each row; in the epilogue 1 / l
@@ -293,7 +293,7 @@ decode_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_constant_
       mbar_init(&sh.pv_done[i], 1);
       mbar_init(&sh.drain[i], 1);
     }
-    mbar_init(&sh.p_full, 1);
+    for (int i = 0; i < kPBars; ++i) mbar_init(&sh.p_full[i], 1);
     sh.abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -509,7 +509,7 @@ decode_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_constant_
       const int n_tiles = (int)uni((sg.tok1 - sg.tok0 + kTok - 1) / kTok);
       const uint32_t idesc = make_idesc(128, (int)uni(sg.N)) | kTransA;
       for (int i = 0; i < n_tiles; ++i, ++tile) {
-        ok = warp_wait(&sh.p_full, tile & 1, abort_flag);   // P is written, so S has read the whole tile
+        ok = warp_wait(&sh.p_full[p_bar(tile)], p_phase(tile), abort_flag);   // P is written, so S has read the whole tile
         if (!ok) break;
         tc_fence_after();
         const uint64_t step = (uint64_t)(slot * slot_bytes) >> 4;
@@ -719,7 +719,7 @@ decode_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_constant_
         }
         if (st == 0) {
           tc_fence_before();
-          mbar_arrive(&sh.p_full);
+          mbar_arrive(&sh.p_full[p_bar(tile)]);
         }
       }
       if (fail) break;

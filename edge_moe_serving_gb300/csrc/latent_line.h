@@ -65,6 +65,13 @@ MOE_HD inline size_t suffix_rows(const LineShape& p) {
 // The same of the prefix line: two pieces a CTA, and the whole row tiles.
 MOE_HD inline size_t prefix_rows(const LineShape& p) { return p.np ? ((size_t)2 * p.ctas + p.Gp) * p.NRp : 0; }
 
+// The barrier that says tile t's probabilities are written, and the phase of it.  The softmax warps wait for the value
+// product of two tiles ago only, so they may have arrived for two tiles that the product's warp has not looked at yet:
+// on one barrier the second arrival would hide the first.
+constexpr int kPBars = 2;
+MOE_HD inline int p_bar(int tile) { return tile % kPBars; }
+MOE_HD inline uint32_t p_phase(int tile) { return (uint32_t)(tile / kPBars) & 1u; }
+
 // The units of the sequences' line: all, and those before and through sequence b.
 struct LineSums {
   int total, x0, x1;

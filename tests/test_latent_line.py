@@ -1,6 +1,7 @@
 """The absorbed attention's division of work, on the CPU: the arithmetic that
 its kernels index partial results with, compiled as host code and asked about
-random batches with empty sequences (an id out of range counts as one)."""
+random batches with empty sequences (an id out of range counts as one); and
+the order of its probabilities' barriers, over every interleaving."""
 import os
 import subprocess
 
@@ -58,14 +59,53 @@ int main(int argc, char** argv) {
 }
 """
 
+# All states (tiles the softmax warps arrived for, tiles the product's warp saw, value products that ended) that can be
+# reached: a wait on a phase's parity passes once that phase is over and until the next one is.
+BARRIERS = r"""
+#include <cstdio>
+#include <set>
+#include <tuple>
+#include <vector>
+#include "latent_line.h"
+using namespace moe;
+int main() {
+  const int N = 9;
+  typedef std::tuple<int, int, int> State;
+  std::set<State> seen;
+  std::vector<State> todo(1, State(0, 0, 0));
+  while (!todo.empty()) {
+    const State st = todo.back();
+    todo.pop_back();
+    if (!seen.insert(st).second) continue;
+    const int soft = std::get<0>(st), product = std::get<1>(st), ended = std::get<2>(st);
+    const size_t before = todo.size();
+    if (soft < N && (soft < 2 || ended >= soft - 1)) todo.push_back(State(soft + 1, product, ended));
+    if (product < N) {
+      unsigned over = 0;                                     // phases of this tile's barrier that are over
+      for (int t = 0; t < soft; ++t) over += p_bar(t) == p_bar(product);
+      if ((over & 1u) != p_phase(product)) {
+        if (soft <= product) return std::printf("tile %d's product starts before its probabilities\n", product), 1;
+        todo.push_back(State(soft, product + 1, ended));
+      }
+    }
+    if (ended < product) todo.push_back(State(soft, product, ended + 1));
+    if (todo.size() == before && st != State(N, N, N)) return std::printf("stuck at %d %d %d\n", soft, product, ended), 1;
+  }
+  return seen.count(State(N, N, N)) ? 0 : 1;
+}
+"""
 
-@pytest.fixture(scope="module")
-def harness(tmp_path_factory):
-    d = tmp_path_factory.mktemp("line")
-    (d / "h.cpp").write_text(HARNESS)
+
+def compiled(d, source):
+    (d / "h.cpp").write_text(source)
     subprocess.run(["g++", "-std=c++17", "-O1", "-Wall", "-I", os.path.join(ROOT, "edge_moe_serving_gb300", "csrc"),
                     str(d / "h.cpp"), "-o", str(d / "h")], check=True)
     return str(d / "h")
+
+
+@pytest.fixture(scope="module")
+def harness(tmp_path_factory):
+    return compiled(tmp_path_factory.mktemp("line"), HARNESS)
 
 
 @pytest.mark.parametrize("seed", range(4))
@@ -74,3 +114,8 @@ def test_pieces_lie_inside_the_workspace(harness, seed):
     assert r.returncode == 0, r.stdout
     empty, cut = (int(x) for x in r.stdout.split())
     assert empty > 1000 and cut > 1000            # rows without pieces, and cut ones, were among them
+
+
+def test_probability_barriers_never_stick(tmp_path):
+    r = subprocess.run([compiled(tmp_path, BARRIERS)], capture_output=True, text=True)
+    assert r.returncode == 0, r.stdout
