@@ -11,6 +11,7 @@
 // small calls the plan's dependent reads and the launches.  16 beams that change
 // parents: 6.5 us.  64 branches off 8 contexts, 4 layers, 14.9 MB: 8.2 us.  A
 // quarter of 64 sequences replaced, 4 layers, 968 MB: 163 us, 5.9 TB/s.
+#include "kv_append_shape.h"
 #include "kv_common.cuh"
 
 namespace moe {
@@ -158,17 +159,17 @@ reserve_kernel(const KvView kv, const int32_t* seqs, const int32_t* n_new, int n
 // A warp takes `per` <= 32 rows at a time: one run of bytes to read, `per` places to write (61 MB of rows: 18 us, 6.7
 // TB/s read and written; with a thread per 16 bytes that finds its own place 24 us).
 __global__ void __launch_bounds__(kApplyThreads)
-append_kernel(const KvView kv, int layer, const uint4* rows, const int32_t* tok_seq, const int32_t* tok_pos, int N,
-              int per, uint32_t* status) {
+append_kernel(const KvView kv, int layer, const uint4* rows, const int32_t* tok_seq, const int32_t* tok_pos, unsigned N,
+              const AppendShape shape, uint32_t* status) {
   pdl_wait();
   pdl_trigger();
   const int vecs = kv.row >> 3, lane = threadIdx.x & 31;
-  const int warps = gridDim.x * (kApplyThreads / 32);
-  for (int i0 = per * (blockIdx.x * (kApplyThreads / 32) + (threadIdx.x >> 5)); i0 < N; i0 += per * warps) {
+  const unsigned per = shape.per, step = append_step(shape);
+  for (unsigned i0 = append_first(shape, blockIdx.x, threadIdx.x >> 5); i0 < N; i0 += step) {
     // lane j finds where row i0 + j goes (its dependent reads are the warp's only ones)
-    const int i = i0 + lane;
+    const unsigned i = i0 + lane;
     long long to = -1;
-    if (lane < per && i < N) {
+    if (lane < (int)per && i < N) {
       const int s = tok_seq[i], pos = tok_pos[i];
       if (s < 0 || s >= kv.max_seqs || pos < 0 || pos >= kv.len_of(s)) {
         set_status(status, MOE_DEV_ERR_BAD_SEQ);
@@ -179,7 +180,7 @@ append_kernel(const KvView kv, int layer, const uint4* rows, const int32_t* tok_
       }
     }
     const uint4* from = rows + (size_t)i0 * vecs;
-    const int total = min(per, N - i0) * vecs;
+    const int total = (int)min(per, N - i0) * vecs;
     for (int x0 = 0; x0 < total; x0 += 32 * 8) {          // eight reads in flight
       uint4 v[8];
 #pragma unroll
@@ -529,12 +530,11 @@ int moe_kv_append(const moe_kv_cache* cache, int layer, const void* rows, const 
   if (N == 0) return MOE_OK;
   if (!rows || !tok_seq || !tok_pos) return MOE_ERR_INVALID_ARG;
   if (!kv_aligned(rows, 16)) return MOE_ERR_UNSUPPORTED;
-  const int cap = 8 * num_sms(), warps = kApplyThreads / 32;
-  const int spread = (N + cap * warps - 1) / (cap * warps), per = spread < 32 ? spread : 32;   // few rows: spread over the SMs
-  const int blocks = (N + per * warps - 1) / (per * warps);
-  return status_of(launch_k(append_kernel, (unsigned)(blocks < cap ? blocks : cap), kApplyThreads, 0,
-                            reinterpret_cast<cudaStream_t>(stream), kv_view(*cache), layer,
-                            reinterpret_cast<const uint4*>(rows), tok_seq, tok_pos, N, per, dev_status));
+  static_assert(kAppendWarps == kApplyThreads / 32, "warps of a CTA");
+  const AppendShape shape = append_shape((unsigned)N, (unsigned)num_sms());
+  return status_of(launch_k(append_kernel, shape.ctas, kApplyThreads, 0, reinterpret_cast<cudaStream_t>(stream),
+                            kv_view(*cache), layer, reinterpret_cast<const uint4*>(rows), tok_seq, tok_pos, (unsigned)N,
+                            shape, dev_status));
 }
 
 int moe_kv_fork(const moe_kv_cache* cache, const int32_t* src, const int32_t* dst, int n, void* ws,

@@ -208,3 +208,30 @@ def test_calls_in_a_graph_on_another_stream():
     torch.cuda.synchronize()
     p.check(contents=False)
     assert p.c.bits() == 0
+
+
+@pytest.mark.parametrize("n", [9728, 9729, 20001, 330007])
+def test_append_of_many_rows(n):
+    """Up to 9728 rows a warp of the grid takes one row at a time, beyond that up to 32, and beyond 311296 of them it
+    comes back for more (152 SMs).  Tokens in any order, some entries that are refused among them."""
+    seqs, page = 41, 128
+    lens = [n // seqs + (i < n % seqs) for i in range(seqs)]
+    blocks = [-(-k // page) for k in lens]
+    c = Paged(sum(blocks), page, 16, 8, seqs, max(blocks), layers=2)
+    moe.moe_kv_reserve(c.handle, i32(range(seqs)), i32(lens), seqs, c.ws, c.ws.numel(), c.status)
+    order = np.random.RandomState(n).permutation(n)
+    tok_seq = np.repeat(np.arange(seqs), lens)[order]
+    tok_pos = np.concatenate([np.arange(k) for k in lens])[order]
+    words = torch.from_numpy(np.random.RandomState(1).randint(0, 1 << 30, (n, c.row // 2)).astype(np.int32)).to(DEV)
+    s, t = i32(tok_seq), i32(tok_pos)
+    refused = torch.arange(7, n, 1009, device=DEV)
+    s_in, t_in = s.clone(), t.clone()
+    s_in[refused[::2]] = seqs
+    t_in[refused[1::2]] = 1 << 20
+    moe.moe_kv_append(c.handle, 1, words.view(torch.bfloat16), s_in, t_in, n, c.status)
+    assert c.bits() == moe.MOE_DEV_ERR_BAD_SEQ
+    got = c.pages.view(torch.int32)[1, c.table[s.long(), t.long() // page].long(), t.long() % page]
+    want = words.clone()
+    want[refused] = torch.full((c.row,), float("nan"), dtype=torch.bfloat16, device=DEV).view(torch.int32)
+    assert torch.equal(got, want)
+    assert bool(torch.isnan(c.pages[0]).all())
