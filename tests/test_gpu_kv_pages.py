@@ -235,3 +235,45 @@ def test_append_of_many_rows(n):
     want[refused] = torch.full((c.row,), float("nan"), dtype=torch.bfloat16, device=DEV).view(torch.int32)
     assert torch.equal(got, want)
     assert bool(torch.isnan(c.pages[0]).all())
+
+
+@pytest.mark.parametrize("seed", [5, 6])
+def test_large_pools_and_copies(seed):
+    """Forks and compactions whose bytes take the whole GPU (a plan and a second launch) instead of one cluster: a pool
+    of 9.2 MB (above 8 MB), forks of 27 to 36 pairs of 15,360 bytes (above 384 KB), in place and onto empty sequences."""
+    rng = random.Random(seed)
+    p = Pair(n_pages=600, page=64, max_seqs=40, max_blocks=20, layers=5)
+    assert 5 * 600 * 64 * p.c.row * 2 > 8 << 20 and 27 * 5 * 64 * p.c.row * 2 > 384 << 10
+    for turn in range(4):
+        empty = [s for s in range(40) if p.m.lens[s] == 0]
+        new = rng.sample(empty, min(14, len(empty)))
+        n_new = [rng.choice([1, 63, 64, 65, rng.randint(1, 900)]) for _ in new]
+        assert p.reserve(new, n_new)
+        toks = [(s, t) for s, n in zip(new, n_new) for t in range(n)]
+        p.append([s for s, _ in toks], [t for _, t in toks])
+        dst = rng.sample(range(40), rng.randint(27, 36))
+        assert p.fork([rng.randrange(40) for _ in dst], dst)
+        p.check(contents=turn == 1)
+        p.free(rng.sample(range(40), 22))
+        p.check(contents=False)
+        p.compact()
+        p.check(contents=turn == 3)
+    assert p.c.bits() == 0
+
+
+def test_a_large_fork_that_is_refused():
+    """The two-launch form with too few free pages, bad ids and a source whose last page is missing."""
+    p = Pair(n_pages=64, page=64, max_seqs=32, max_blocks=4, layers=5)
+    p.reserve(list(range(30)), [65] * 30)
+    assert not p.fork([0] * 27, list(range(1, 28)))                     # 27 partial pages, 4 free
+    assert p.c.bits() == moe.MOE_DEV_ERR_CAPACITY
+    p.check()
+    p.free(list(range(3, 30)))
+    src, dst = [0] * 27, list(range(3, 30))
+    src[4], dst[9], dst[11] = 32, -1, 3                                 # a bad source, a bad destination, a repeat
+    assert p.fork(src, dst)
+    assert p.c.bits() == moe.MOE_DEV_ERR_BAD_SEQ
+    p.check()
+    p.c.table[0, 1] = -1
+    moe.moe_kv_fork(p.c.handle, i32([0] * 28), i32([31] + [1] * 27), 28, p.c.ws, p.c.ws.numel(), p.c.status)
+    assert p.c.bits() == moe.MOE_DEV_ERR_BAD_PAGE | moe.MOE_DEV_ERR_BAD_SEQ

@@ -505,3 +505,29 @@ def test_prefill_of_many_sequences(B):
     # no room for the lengths: reported, nothing written
     run_prefill(c, q, list(range(B)), offsets, 3, 64, 64, w, 0.12, 1)
     assert c.bits() == (moe.MOE_DEV_ERR_CAPACITY if sum(-(-n // 128) for n in lens) > B else 0)
+
+
+WIDTHS = [
+    # rank, rope, page, heads, dn, dv, lens, new: the widths of keys and values that PREFILL leaves out
+    (512, 0, 64, 3, 64, 64, [300, 1, 129], [300, 1, 129]),
+    (256, 0, 32, 2, 64, 128, [257, 600], [257, 31]),
+    (512, 64, 16, 3, 128, 64, [130, 520, 77], [130, 400, 76]),
+    (128, 0, 128, 2, 128, 128, [513], [513]),
+    (512, 64, 64, 2, 64, 64, [1000], [260]),
+]
+
+
+@pytest.mark.parametrize("rank,rope,page,heads,dn,dv,lens,new", WIDTHS)
+def test_prefill_widths(rank, rope, page, heads, dn, dv, lens, new):
+    """Every pair of widths, with and without a rotary part, whole prompts and chunks that are shared out."""
+    test_prefill(rank, rope, page, heads, dn, dv, lens, new)
+
+
+@pytest.mark.parametrize("rope,dn,dv", [(0, 64, 64), (0, 64, 128), (32, 128, 64), (0, 128, 128)])
+def test_prefill_widths_in_token_shares(rope, dn, dv):
+    c = Paged(40, 128, 256, rope, 1, 40)
+    rows = c.fill([4900], seed=110)
+    q, w = make_q(40, 2, dn + rope, 111), make_w(2, dn + dv, 256, 112)
+    out = run_prefill(c, q, [0], [0, 40], 2, dn, dv, w, 0.09, 4900)
+    assert c.bits() == 0
+    check_prefill(c, rows, q, [0], [0, 40], 2, dn, w, 0.09, out)
