@@ -58,12 +58,20 @@ MOE_HD inline void set_line(LineShape& p, int B, int Q, int heads, int shared, i
   p.per_p = (int)(((long long)p.Gp * p.np + p.ctas - 1) / p.ctas);
 }
 
-// Rows of partial results of the sequences' line: two pieces a CTA, and with a prefix the whole sequences too.
+// Room for partial results, in query rows: at least what a launch uses, and never less for more sequences, queries or
+// heads (an even split's tiles can be smaller for more rows), so that a workspace serves every smaller call.
+MOE_HD inline size_t tiles_at_most(long long rows) { return (size_t)((rows + kRows - 1) / kRows); }
+MOE_HD inline size_t tile_rows_at_most(long long rows) { return rows < kRows ? (size_t)up16((int)rows) : (size_t)kRows; }
+// The sequences' line: two pieces a CTA, and with a prefix the whole sequences too.
 MOE_HD inline size_t suffix_rows(const LineShape& p) {
-  return ((size_t)2 * p.teams * p.G + (p.np ? (size_t)p.B * p.G : 0)) * p.NR;
+  const long long rows = (long long)p.Q * p.heads;
+  return ((size_t)2 * p.ctas + (p.np ? p.B * tiles_at_most(rows) : 0)) * tile_rows_at_most(rows);
 }
-// The same of the prefix line: two pieces a CTA, and the whole row tiles.
-MOE_HD inline size_t prefix_rows(const LineShape& p) { return p.np ? ((size_t)2 * p.ctas + p.Gp) * p.NRp : 0; }
+// The prefix line: two pieces a CTA, and the whole row tiles.
+MOE_HD inline size_t prefix_rows(const LineShape& p) {
+  const long long rows = (long long)p.B * p.Q * p.heads;
+  return p.np ? ((size_t)2 * p.ctas + tiles_at_most(rows)) * tile_rows_at_most(rows) : 0;
+}
 
 // The barrier that says tile t's probabilities are written, and the phase of it.  The softmax warps wait for the value
 // product of two tiles ago only, so they may have arrived for two tiles that the product's warp has not looked at yet:

@@ -1117,6 +1117,20 @@ int most_shares(long long items) {
   return s < 1 ? 1 : s > kMaxSplits ? kMaxSplits : (int)s;
 }
 
+// Rows of partial results that there is room for: the most that a call of up to T queries and any number of sequences
+// writes.  Fewer queries can mean more shares, so the room for T alone would not do for the short last chunk of a prompt.
+size_t share_rows(int T, int heads) {
+  size_t most = 0;
+  for (int s = 2; s <= kMaxSplits; ++s) {
+    const long long blocks = 2LL * num_sms() / ((long long)heads * s);   // T / kBlock + 1 at most, for s shares or more
+    if (blocks < 1) continue;
+    const long long t = kBlock * blocks - 1;
+    const size_t rows = (size_t)s * (size_t)(t < T ? t : T);
+    if (rows > most) most = rows;
+  }
+  return most;
+}
+
 PrefillWs prefill_ws(int B, int T, int heads, int dn, int dv, int rope, int kv_tokens) {
   PrefillWs w;
   w.rows = (kv_tokens + kRowAlign - 1) / kRowAlign * kRowAlign + kRowAlign * (B - 1);
@@ -1136,9 +1150,10 @@ PrefillWs prefill_ws(int B, int T, int heads, int dn, int dv, int rope, int kv_t
   at += align_up((size_t)w.rows * (rope ? rope : 8) * 2, 256);
   w.splits = most_shares((long long)w.n_blocks * heads);
   w.part = at;
-  if (w.splits > 1) at += align_up((size_t)w.splits * heads * T * dv * sizeof(float), 256);
+  const size_t shares = share_rows(T, heads) * heads;
+  at += align_up(shares * dv * sizeof(float), 256);
   w.ml = at;
-  if (w.splits > 1) at += align_up((size_t)w.splits * heads * T * sizeof(float2), 256);
+  at += align_up(shares * sizeof(float2), 256);
   w.bytes = at;
   return w;
 }

@@ -590,7 +590,7 @@ typedef struct moe_kv_cache {
 } moe_kv_cache;
 
 /* Bytes of ws that the page calls below need for lists of up to n sequences
- * (0 for a bad struct or n < 0). */
+ * (0 for a bad struct or n < 0).  A workspace of that size serves shorter lists too. */
 size_t moe_kv_workspace_size(const moe_kv_cache* cache, int n);
 
 /* Grows n sequences: seqs[i] gets room for n_new[i] >= 0 more tokens (its
@@ -657,7 +657,9 @@ int moe_kv_compact(const moe_kv_cache* cache, int32_t* n_live_opt, void* ws, siz
  * max_blocks, a scale that is not finite, NULL q, seqs or out (B > 0);
  * MOE_ERR_UNSUPPORTED for rank not in {128, 256, 384, 512}, rope not a
  * multiple of 16 up to 64, max_blocks * page_tokens above 2^27, B > 4096, Q * heads > 1024, q or out not 16-byte aligned;
- * MOE_ERR_WORKSPACE / MOE_ERR_UNSUPPORTED for ws.  B = 0 is a no-op. */
+ * MOE_ERR_WORKSPACE / MOE_ERR_UNSUPPORTED for ws.  B = 0 is a no-op.
+ * The workspace size never falls when B, Q, heads or shared_tokens rises: one workspace for the largest call serves
+ * every smaller one. */
 size_t moe_latent_decode_workspace_size(const moe_kv_cache* cache, int B, int Q, int heads, int shared_tokens);
 int moe_latent_decode(const moe_kv_cache* cache, int layer, const void* q, const int32_t* seqs, int B, int Q,
                       int heads, float scale, int shared_tokens, void* out, float* lse_opt, void* ws,
@@ -688,7 +690,9 @@ int moe_latent_decode(const moe_kv_cache* cache, int layer, const void* q, const
  * out (B and T > 0); MOE_ERR_UNSUPPORTED for rank not in {128, 256, 384, 512}, rope not a
  * multiple of 16 up to 64, max_blocks * page_tokens above 2^27, dn or dv not 64 or 128, heads > 1024, B > 4096, T * heads or
  * (kv_tokens + 128 B) * heads above INT_MAX, q or w_kv not 16-byte or out not 32-byte aligned; MOE_ERR_WORKSPACE /
- * MOE_ERR_UNSUPPORTED for ws.  B = 0 or T = 0 is a no-op. */
+ * MOE_ERR_UNSUPPORTED for ws.  B = 0 or T = 0 is a no-op.
+ * The workspace size never falls when B, T or kv_tokens rises: one workspace for the largest chunk of prompts serves
+ * every smaller one, the short last chunk among them. */
 size_t moe_latent_prefill_workspace_size(const moe_kv_cache* cache, int B, int T, int heads, int dn, int dv,
                                          int kv_tokens);
 int moe_latent_prefill(const moe_kv_cache* cache, int layer, const void* q, const int32_t* seqs,

@@ -531,3 +531,32 @@ def test_prefill_widths_in_token_shares(rope, dn, dv):
     out = run_prefill(c, q, [0], [0, 40], 2, dn, dv, w, 0.09, 4900)
     assert c.bits() == 0
     check_prefill(c, rows, q, [0], [0, 40], 2, dn, w, 0.09, out)
+
+
+def test_one_workspace_for_all_chunks():
+    """The workspace of a full chunk takes the short last chunk, that of a large fan-out a smaller one: same results as
+    with a workspace of their own."""
+    c = Paged(60, 64, 512, 64, 5, 40)
+    rows = c.fill([2303, 320, 330, 340, 350], seed=120, shared_blocks=4)
+    heads, scale = 2, 192 ** -0.5
+    q, w = make_q(1280, heads, 192, 121), make_w(heads, 256, 512, 122)
+    i32 = lambda v: torch.tensor(v, dtype=torch.int32, device=DEV)  # noqa: E731
+    n = moe.moe_latent_prefill_workspace_size(c.handle, 1, 1280, heads, 128, 128, 2303)
+    ws = torch.full((n,), 255, dtype=torch.uint8, device=DEV)
+    for T in (1280, 255, 1):
+        own = run_prefill(c, q[:T], [0], [0, T], heads, 128, 128, w, scale, 2303)
+        out = torch.full((T, heads, 128), float("nan"), dtype=torch.bfloat16, device=DEV)
+        moe.moe_latent_prefill(c.handle, 0, q, i32([0]), i32([0, T]), 1, T, heads, 128, 128, w, scale, 2303, out, ws, n,
+                               c.status)
+        assert c.bits() == 0 and torch.equal(out, own)
+        check_prefill(c, rows, q[:T], [0], [0, T], heads, 128, w, scale, out)
+    q = make_q(5, 16, c.row, 123)
+    n = moe.moe_latent_decode_workspace_size(c.handle, 5, 1, 16, 256)
+    ws = torch.full((n,), 255, dtype=torch.uint8, device=DEV)
+    for B in (5, 4, 1):
+        seqs = list(range(B))
+        own, _ = run_decode(c, q[:B], seqs, 1, 16, scale, shared=256)
+        out = torch.full((B, 16, 512), float("nan"), dtype=torch.bfloat16, device=DEV)
+        moe.moe_latent_decode(c.handle, 0, q, i32(seqs), B, 1, 16, scale, 256, out, None, ws, n, c.status)
+        assert c.bits() == 0 and torch.equal(out, own)
+        check_decode(c, rows, q[:B], seqs, 1, 16, scale, out, None)
