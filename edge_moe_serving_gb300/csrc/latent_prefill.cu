@@ -42,6 +42,10 @@ constexpr int kThreads = 384;            // warps 0..3: producer, MMA issuer, tw
 constexpr int kMaxSplits = 8;
 constexpr int kTmemCols = 512;
 constexpr float kGrow = 8.0f;            // log2 of the growth of a row's maximum that forces a rescaling
+// Probabilities are kept as 2^7 times their ratio to the row's reference: with the growth above they reach 2^15, inside
+// f16, and each is off by at most 2^-32 of the row's largest where f16's subnormals begin (unlifted 2^-25: behind one
+// dominating token, a tail of many thousand small ones was lost).  Their sum carries the same factor.
+constexpr float kLift = 7.0f;
 
 struct QBlock {
   int row0, rows;   // first of its query rows in q, and how many
@@ -980,7 +984,7 @@ attend_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__
             tmem_st16(o_col + c, v);
           }
         }
-        const float ref = m == -INFINITY ? 0.0f : m;
+        const float ref = m == -INFINITY ? 0.0f : m - kLift;
         float2 sum0 = make_float2(0.0f, 0.0f), sum1 = sum0;
 #pragma unroll
         for (int c = 0; c < 4; ++c) {

@@ -678,7 +678,7 @@ int moe_latent_decode(const moe_kv_cache* cache, int layer, const void* q, const
  * are rounded to bf16, values and probabilities to f16 for the products, which
  * accumulate in fp32, as do the softmax statistics.  An expanded value beyond
  * 65504 in magnitude is clamped and sets MOE_DEV_ERR_RANGE; values below 6e-5
- * keep an absolute precision of 3e-8.  A cached value that is NaN or infinite
+ * keep an absolute precision of 3e-8, probabilities one of 2^-32 of their row's largest.  A cached value that is NaN or infinite
  * reaches queries that see its token (through its keys) and no other.
  * kv_tokens: host bound on the sum of the B lengths (sizes the workspace); a
  * sum the workspace has no rows for sets MOE_DEV_ERR_CAPACITY and nothing is

@@ -560,3 +560,33 @@ def test_one_workspace_for_all_chunks():
         moe.moe_latent_decode(c.handle, 0, q, i32(seqs), B, 1, 16, scale, 256, out, None, ws, n, c.status)
         assert c.bits() == 0 and torch.equal(out, own)
         check_decode(c, rows, q[:B], seqs, 1, 16, scale, out, None)
+
+
+@pytest.mark.parametrize("heads,n,bits", [(1, 5000, 26.5), (160, 900, 26.5), (160, 900, 20.5), (1, 5000, 31.0)])
+def test_prefill_long_tail_behind_one_token(heads, n, bits):
+    """The first token takes nearly all the probability and has value 0; the output is the tail's, n - 1 tokens of
+    probability 2^-bits each.  Scores come from the rotary part alone, which is not rounded, and all values are 0 or 1, so
+    the errors are the probabilities' f16 roundings (2^-12 of themselves, or 2^-32 of the largest), the output's bf16 one,
+    and fp32's: a score of 22 is off by 2^-19, the sum by 2^-13, 2^-12 together.  With token shares (one head) and without."""
+    c = Paged(-(-n // 64), 64, 128, 16, 1, -(-n // 64))
+    x = torch.zeros(n, c.row)
+    x[0, 128] = 4.0
+    x[1:, 0] = 1.0
+    rows = [x.double()]
+    for b in range(-(-n // 64)):
+        part = x[b * 64:(b + 1) * 64].to(torch.bfloat16)
+        c.pages[0, b, :len(part)] = part.to(DEV)
+    c.table[0] = torch.arange(c.table.shape[1], dtype=torch.int32)
+    c.lens[0] = n
+    q = torch.zeros(1, heads, 80, dtype=torch.bfloat16, device=DEV)
+    q[:, :, 64] = 4.0
+    w = torch.zeros(heads, 128, 128, dtype=torch.bfloat16, device=DEV)
+    w[:, 64:, 0] = 1.0
+    scale = bits * math.log(2.0) / 16.0
+    out = run_prefill(c, q, [0], [0, 1], heads, 64, 64, w, scale, n)
+    assert c.bits() == 0
+    ref, _, _ = attend64(q[0, :1].cpu().double(), torch.cat([torch.zeros(n, 64).double(), rows[0][:, 128:]], 1),
+                         rows[0][:, :1].expand(n, 64), scale, [n])
+    err = (out[0].cpu().double() - ref).abs()
+    bound = (U + 2.0 ** -12 + 2.0 ** -12) * ref + n * 2.0 ** -32
+    assert bool((err <= bound).all()), (float(err.max()), float(ref.max()), float(bound.max()))
