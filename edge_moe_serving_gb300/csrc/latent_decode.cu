@@ -258,6 +258,7 @@ struct alignas(16) Shared {   // its size is what the dynamic shared memory leav
   float factor[kRows];   // rescaling of each row; in the epilogue 1 / l
   int warp_sum[kThreads / 32];
   int sees[kSoftThreads / 32];
+  unsigned long long bad[2];   // tokens of a tile (by its parity) with a NaN or infinite latent entry, bit by bit
   int pref[kBatch + 1];
   int len[kBatch];
   int ids[kBatch];
@@ -295,6 +296,7 @@ decode_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_constant_
     }
     for (int i = 0; i < kPBars; ++i) mbar_init(&sh.p_full[i], 1);
     sh.abort = 0;
+    sh.bad[0] = sh.bad[1] = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (tid == 32 * 2) {
@@ -604,6 +606,37 @@ decode_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_constant_
             }
           }
         }
+        if (t0 + n_tok > sees_tile) {
+          // Some row does not see some token (the last tile of several query tokens): its probability 0 times a NaN or
+          // infinite value would be NaN.  Such values become 0 here, and a row that does see the token gets NaN through
+          // its score: the value may have made that -infinity, whose product with the value is NaN as well.
+          unsigned long long bad = 0;
+          if (ok) {
+            for (int j = 0; j < p.pairs; ++j) mbar_wait(&sh.full[slot][j], (tile / p.slots) & 1, abort_flag);   // long over
+            uint4* base = reinterpret_cast<uint4*>(skv + slot * slot_bytes);
+            for (int x = st; x < p.pairs * (2 * kChunk / 16); x += kSoftThreads) {
+              const uint4 v = base[x];
+              const uint4 f = make_uint4(finite_bf16x2(v.x), finite_bf16x2(v.y), finite_bf16x2(v.z), finite_bf16x2(v.w));
+              if (((v.x ^ f.x) | (v.y ^ f.y) | (v.z ^ f.z) | (v.w ^ f.w)) != 0) {
+                base[x] = f;
+                bad |= 1ull << ((x & (kChunk / 16 - 1)) >> 3);   // a token's row is 128 bytes of a chunk
+              }
+            }
+            if (bad) atomicOr(&sh.bad[buf], bad);
+          }
+          if (soft_any(bad != 0)) {
+            bad = sh.bad[buf];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int see = min(n_tok, limit[e] - t0);
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+#pragma unroll
+                for (int y = 0; y < 2; ++y)
+                  if (8 * i + c2 + y < see && (bad >> (8 * i + c2 + y) & 1)) s[4 * i + 2 * e + y] = NAN;
+            }
+          }
+        }
         float top[2];
         if (scale >= 0.0f) {
 #pragma unroll
@@ -683,18 +716,6 @@ decode_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_constant_
             *reinterpret_cast<uint4*>(base + c * kChunk + n_tok * 128 + y * 16) = make_uint4(0, 0, 0, 0);
           }
         }
-        if (t0 + n_tok > sees_tile && ok) {
-          // Some row does not see some token (the last tile of several query tokens): its probability 0 times a NaN or
-          // infinite value would be NaN.  Such values become 0 here; the rows that do see the token get their NaN
-          // from its score, which was made of the value before.
-          for (int j = 0; j < p.pairs; ++j) mbar_wait(&sh.full[slot][j], (tile / p.slots) & 1, abort_flag);   // long over
-          uint4* base = reinterpret_cast<uint4*>(skv + slot * slot_bytes);
-          for (int x = st; x < p.pairs * (2 * kChunk / 16); x += kSoftThreads) {
-            const uint4 v = base[x];
-            const uint4 f = make_uint4(finite_bf16x2(v.x), finite_bf16x2(v.y), finite_bf16x2(v.z), finite_bf16x2(v.w));
-            if (((v.x ^ f.x) | (v.y ^ f.y) | (v.z ^ f.z) | (v.w ^ f.w)) != 0) base[x] = f;
-          }
-        }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         if (soft_any(grow)) {      // rare: some row's maximum rose by more than 2^8 (or a wait ran out)
           // O was last added to by the previous tile's product, and this tile's waits for us
@@ -718,6 +739,7 @@ decode_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_constant_
           soft_any(false);
         }
         if (st == 0) {
+          sh.bad[buf] = 0;         // read by everyone before the vote above; the next tile writes the other one
           tc_fence_before();
           mbar_arrive(&sh.p_full[p_bar(tile)]);
         }

@@ -515,7 +515,13 @@ expand_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
         void* dst;
         if (c < p.dn) {
 #pragma unroll
-          for (int y = 0; y < 16; ++y) o[y] = bf16x2_of(__uint_as_float(x[2 * y]), __uint_as_float(x[2 * y + 1])) & mask;
+          for (int y = 0; y < 16; ++y) {
+            // k + 0 k: an infinite key becomes NaN.  Its token's values are infinite too, clamped below, and the score it
+            // would give may be -infinity: probability 0 times a finite value would hide it.
+            const float2 k = make_float2(__uint_as_float(x[2 * y]), __uint_as_float(x[2 * y + 1]));
+            const float2 z = fma2(k, make_float2(0.0f, 0.0f), k);
+            o[y] = bf16x2_of(z.x, z.y) & mask;
+          }
           dst = p.k + at * p.dn + c;
         } else {
           float big = 0.0f;

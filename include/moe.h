@@ -643,10 +643,10 @@ int moe_kv_compact(const moe_kv_cache* cache, int32_t* n_live_opt, void* ws, siz
  * [B*Q, heads] or NULL.  The Q tokens are in the cache already.  Products are
  * accumulated in fp32; the probabilities are rounded to bf16 for the second
  * product and divided by the sum of the rounded ones; lse comes from the
- * unrounded ones.  A cached value that is NaN or infinite reaches the queries
- * that see its token and no other.  A query that sees no token (a sequence shorter
- * than Q, or a bad id) gets zeros and lse = -inf.
- * shared_tokens > 0 (a multiple of page_tokens): the first shared_tokens
+ * unrounded ones.  A NaN in a token's row makes every query that sees the token
+ * NaN; an infinite latent entry makes that entry of theirs NaN, and may make the
+ * others; an infinite rotary entry that makes the score -infinity leaves the
+ * token out, else it makes them NaN.  No other query is touched.  A query * shared_tokens > 0 (a multiple of page_tokens): the first shared_tokens
  * tokens of all B sequences are the ones in the pages of seqs[0] (as
  * moe_kv_fork leaves them); they are then read and multiplied once for the
  * whole batch, and the partial results are merged.
@@ -678,8 +678,8 @@ int moe_latent_decode(const moe_kv_cache* cache, int layer, const void* q, const
  * are rounded to bf16, values and probabilities to f16 for the products, which
  * accumulate in fp32, as do the softmax statistics.  An expanded value beyond
  * 65504 in magnitude is clamped and sets MOE_DEV_ERR_RANGE; values below 6e-5
- * keep an absolute precision of 3e-8, probabilities one of 2^-32 of their row's largest.  A cached value that is NaN or infinite
- * reaches queries that see its token (through its keys) and no other.
+ * keep an absolute precision of 3e-8, probabilities one of 2^-32 of their row's largest.  A NaN in a token's row or
+ * an infinite latent entry makes every query that sees the token NaN (an infinite rotary entry as above), and no other.
  * kv_tokens: host bound on the sum of the B lengths (sizes the workspace); a
  * sum the workspace has no rows for sets MOE_DEV_ERR_CAPACITY and nothing is
  * written.  A bad id or

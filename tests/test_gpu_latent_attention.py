@@ -590,3 +590,62 @@ def test_prefill_long_tail_behind_one_token(heads, n, bits):
     err = (out[0].cpu().double() - ref).abs()
     bound = (U + 2.0 ** -12 + 2.0 ** -12) * ref + n * 2.0 ** -32
     assert bool((err <= bound).all()), (float(err.max()), float(ref.max()), float(bound.max()))
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
+@pytest.mark.parametrize("Q", [1, 3])
+def test_a_query_that_sees_a_bad_latent_entry_is_nan_there(Q, bad):
+    """Whatever the score becomes (with one infinite factor it is +infinity in some heads and -infinity in others), and
+    whether or not every row of the tile sees the token: the entry is NaN, for a NaN all entries are."""
+    heads = 6
+    c = Paged(12, 32, 256, 32, 2, 6)
+    c.fill([100, 129], seed=130)
+    for s, t in ((0, 99), (1, 128)):
+        c.pages[0, int(c.table[s, t // 32]), t % 32, 7] = bad
+    q = make_q(2 * Q, heads, c.row, 131)
+    q[:, ::2, 7] = q[:, ::2, 7].abs() + 0.1
+    q[:, 1::2, 7] = -q[:, 1::2, 7].abs() - 0.1
+    for scale in (0.1, -0.1):
+        out, _ = run_decode(c, q, [0, 1], Q, heads, scale)
+        assert c.bits() == 0
+        seen = torch.arange(2 * Q, device=DEV) % Q == Q - 1
+        assert bool(torch.isnan(out[seen][:, :, 7]).all()) and bool(torch.isfinite(out[~seen]).all())
+        if bad != bad:
+            assert bool(torch.isnan(out[seen]).all())
+
+
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+def test_prefill_a_query_that_sees_a_bad_latent_entry_is_nan(sign):
+    """An infinite latent makes all keys of its token infinite, and with keys of one sign and queries of one sign the score
+    is +infinity or -infinity, not NaN by itself."""
+    c = Paged(12, 32, 256, 32, 2, 6)
+    q, w = make_q(60, 2, 96, 132), make_w(2, 128, 256, 133)
+    q[:, :, :64] = sign * (q[:, :, :64].abs() + 0.1)
+    w[:, :64, 7] = w[:, :64, 7].abs() + 0.1
+    for bad in (float("inf"), float("-inf"), float("nan")):
+        c.fill([100, 129], seed=134)
+        for s, t in ((0, 99), (1, 120)):
+            c.pages[0, int(c.table[s, t // 32]), t % 32, 7] = bad
+        out = run_prefill(c, q, [0, 1], [0, 30, 60], 2, 64, 64, w, 0.1, 229)
+        c.bits()                                   # an infinite value is beyond the f16 range: reported
+        seen = torch.tensor([i == 29 or i >= 51 for i in range(60)], device=DEV)
+        assert bool(torch.isnan(out[seen]).all()) and bool(torch.isfinite(out[~seen]).all())
+
+
+def test_an_infinite_rotary_entry_leaves_its_token_out_or_is_nan():
+    c = Paged(12, 32, 256, 32, 1, 6)
+    rows = c.fill([90], seed=140)
+    c.pages[0, int(c.table[0, 0]), 5, 256] = float("inf")
+    q, qp, w = make_q(2, 4, c.row, 141), make_q(2, 2, 96, 142), make_w(2, 128, 256, 143)
+    clean = {0: torch.cat([rows[0][:5], rows[0][6:]])}
+    for sign in (1.0, -1.0):
+        q[:, :, 256] = sign
+        qp[:, :, 64] = sign
+        out, _ = run_decode(c, q, [0], 2, 4, 0.1)
+        outp = run_prefill(c, qp, [0], [0, 2], 2, 64, 64, w, 0.1, 90)
+        assert c.bits() == 0
+        if sign > 0:
+            assert bool(torch.isnan(out).all()) and bool(torch.isnan(outp).all())
+        else:
+            check_decode(c, clean, q, [0], 2, 4, 0.1, out, None)
+            check_prefill(c, clean, qp, [0], [0, 2], 2, 64, w, 0.1, outp)
