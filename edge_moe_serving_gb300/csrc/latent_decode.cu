@@ -818,6 +818,12 @@ __device__ inline LineSums early_sums(const DecodeParams& p, int b, int lane) {
   return l;
 }
 
+// Whether the shared tokens, if any, are a sequence's of the cache.  Where not, no row has a piece: the other rows'
+// pieces are made of whatever page stood in for the missing ones.  Asked before the wait, as the lengths.
+__device__ inline bool prefix_ok(const DecodeParams& p) {
+  return (unsigned)(p.np ? __ldcg(p.prefix_seq) : 0) < (unsigned)p.kv.max_seqs;
+}
+
 // Waits for decode_kernel; the whole warp.
 __device__ inline LineSums wait_for_pieces(const DecodeParams& p, int row, int lane) {
   const int b = row / (p.Q * p.heads);
@@ -882,8 +888,10 @@ __device__ inline void store_lse(const DecodeParams& p, int row, float ref, floa
 __global__ void __launch_bounds__(128) combine_rows_kernel(const DecodeParams p, int rows) {
   const int row = min((int)(blockIdx.x * 4 + (threadIdx.x >> 5)), rows - 1), lane = threadIdx.x & 31;
   const int vecs = p.kv.rank / 128;
+  const bool any = prefix_ok(p);
   const LineSums line = wait_for_pieces(p, row, lane);
-  const Pieces q(p, row, line);
+  Pieces q(p, row, line);
+  if (!any) q.n = 0;
   if (q.direct() || blockIdx.x * 4 + (threadIdx.x >> 5) >= rows) return;
   float4 x[4][4];
   float top[4];
@@ -929,8 +937,10 @@ constexpr int kSets = 4;
 __global__ void __launch_bounds__(128 * kSets) combine_parts_kernel(const DecodeParams p) {
   __shared__ float4 s_acc[128 * kSets];
   const int row = blockIdx.x, lane = threadIdx.x & 31;
+  const bool any = prefix_ok(p);
   const LineSums line = wait_for_pieces(p, row, lane);
-  const Pieces q(p, row, line);
+  Pieces q(p, row, line);
+  if (!any) q.n = 0;
   if (q.direct()) return;
   const int v = threadIdx.x % 128, set = threadIdx.x / 128;   // float4 of the row; set of warps
   const bool mine = 4 * v < p.kv.rank;

@@ -649,9 +649,10 @@ int moe_kv_compact(const moe_kv_cache* cache, int32_t* n_live_opt, void* ws, siz
  * token out, else it makes them NaN.  No other query is touched.  A query * shared_tokens > 0 (a multiple of page_tokens): the first shared_tokens
  * tokens of all B sequences are the ones in the pages of seqs[0] (as
  * moe_kv_fork leaves them); they are then read and multiplied once for the
- * whole batch, and the partial results are merged.
+ * whole batch, and the partial results are merged.  Where seqs[0] is a bad id, every row of such a call gets zeros and
+ * lse = -inf.
  * A block-table entry that names no page sets MOE_DEV_ERR_BAD_PAGE; the rows
- * of that sequence are then unspecified.
+ * of that sequence (of all, where it holds a shared token) are then unspecified.
  * Errors: the struct's; MOE_ERR_INVALID_ARG for layer outside [0, n_layers),
  * B < 0, Q or heads < 1, shared_tokens negative, not a multiple of page_tokens or beyond
  * max_blocks, a scale that is not finite, NULL q, seqs or out (B > 0);

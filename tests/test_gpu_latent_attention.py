@@ -368,6 +368,27 @@ def test_both_forms_agree():
     assert float((out - other).norm() / out.norm()) <= 8e-3
 
 
+@pytest.mark.parametrize("B,heads", [(3, 16), (40, 8), (530, 5)])
+def test_shared_prefix_of_a_bad_id(B, heads):
+    """The shared tokens are the first sequence's: where its id is outside the cache no row gets another's tokens."""
+    c = Paged(300, 16, 128, 16, 4, 12)
+    c.pages[0, 0] = 1.0                                    # what a stand-in for the missing table would name
+    rows = c.fill([100, 160, 70, 33], seed=62, shared_blocks=2)
+    q = make_q(B, heads, c.row, 63)
+    for first in (-1, 4):
+        out, lse = run_decode(c, q, [first] + [i % 4 for i in range(1, B)], 1, heads, 0.1, shared=32)
+        assert c.bits() == moe.MOE_DEV_ERR_BAD_SEQ
+        assert bool((out == 0).all()) and bool((lse == -math.inf).all())
+    seqs = [0] + [-1 if i % 5 == 2 else i % 4 for i in range(1, B)]      # elsewhere a bad id is that row's alone
+    out, lse = run_decode(c, q, seqs, 1, heads, 0.1, shared=32)
+    assert c.bits() == moe.MOE_DEV_ERR_BAD_SEQ
+    for b in (0, 1, 2, B - 1):
+        if seqs[b] < 0:
+            assert bool((out[b] == 0).all()) and bool((lse[b] == -math.inf).all())
+        else:
+            check_decode(c, rows, q[b:b + 1], [seqs[b]], 1, heads, 0.1, out[b:b + 1], lse[b:b + 1])
+
+
 def test_more_than_one_launch_of_sequences():
     """More sequences than one launch takes (512), with and without a shared prefix."""
     lens = [64 + (i * 7) % 40 for i in range(530)]
