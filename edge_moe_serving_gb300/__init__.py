@@ -185,9 +185,12 @@ def _p(t):
 
 def _s(stream):
     if stream is None:
-        # the current stream's handle alone: building a Stream object takes 3 us of every call
         import torch
-        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+        try:
+            # the current stream's handle alone: building a Stream object takes 3 us of every call
+            return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+        except AttributeError:      # not public names: a torch without them has the object
+            return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
