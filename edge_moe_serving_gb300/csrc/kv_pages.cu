@@ -8,9 +8,14 @@
 // is applied, by the whole grid or, for small calls, by a cluster in the same
 // launch: tables and reference counts by integer adds, which commute, and page
 // rows by 16-byte copies.  Bound: the rows that move, read and written once; for
-// small calls the plan's dependent reads and the launches.  16 beams that change
-// parents: 6.5 us.  64 branches off 8 contexts, 4 layers, 14.9 MB: 8.2 us.  A
-// quarter of 64 sequences replaced, 4 layers, 968 MB: 163 us, 5.9 TB/s.
+// small calls on pools of a few rounds the plan's dependent reads and the launches.
+// 16 beams that change parents: 6.5 us.  64 branches off 8 contexts, 4 layers, 14.9
+// MB: 8.2 us.  A quarter of 64 sequences replaced, 4 layers, 968 MB: 163 us, 5.9 TB/s.
+// One token more for 64 sequences, 4 layers (a reserve and four appends): 12.0 us.
+// On large pools the scan is what counts, about 0.9 us a round: with the free pages
+// behind all others a reserve of 64 pages takes 5 us of 1,000 and 4,000 pages, 7 of
+// 16,000, 19 of 64,000 and 33 of 128,000; a compaction that moves nothing 4, 4, 9, 26
+// and 49 (two rounds each).
 #include "kv_append_shape.h"
 #include "kv_common.cuh"
 

@@ -24,14 +24,15 @@
 // against the prefix's tiles.
 //
 // Bound: a tile with its 64 rows moves 322 KB through shared memory (Q and K for
-// S, V and P for O, the copies in), 2515 cycles at 128 bytes a cycle, and takes
-// 3050 to 3750; its products alone take 2230.  With fewer heads the rows of the
+// S, V and P for O, the copies in), 2515 cycles at 128 bytes a cycle; its products
+// alone take 2230.  Long documents take 4100 a tile, starts, pieces and the join
+// included (84 tiles an SM at 2070 MHz).  With fewer heads the rows of the
 // cache bound it, and for short sequences the chain launch, lengths, table, copy,
 // S, softmax, O, combine.  Measured, rank 512 and rope 64:
 //   1 x 333 tokens, 32 heads              12.9 us
-//   32 x 250..6001, 64 heads              36 us   3.2 TB/s of cached rows
-//   4 x 40001..65537, 128 heads, 2 tokens 168 us  0.67 PFLOP/s
-//   64 x 16384 shared + 17..1500, 32 heads 125 us 0.61 PFLOP/s
+//   32 x 250..6001, 64 heads              36.7 us 3.1 TB/s of cached rows
+//   4 x 40001..65537, 128 heads, 2 tokens 169 us  0.69 PFLOP/s
+//   64 x 16384 shared + 17..1500, 32 heads 127 us 0.60 PFLOP/s
 //
 // Roles (224 threads): warp 0 = TMA producer, warp 1 = issuer of S (and TMEM
 // owner), warps 2..5 = softmax, rescaling and epilogue, warp 6 = issuer of the

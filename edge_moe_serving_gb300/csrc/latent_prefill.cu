@@ -17,10 +17,14 @@
 // terms' size, which the softmax averages.
 //
 // Measured, rank 512, rope 64, keys and values of 128:
-//   5 prompts of 1..300 tokens, 32 heads     33 us
-//   1000 tokens over 15001, 16 heads         198 us  1.14 PFLOP/s
-//   8192 tokens, 32 heads                    530 us  1.43 PFLOP/s
-// of which expand_kernel takes about 58 us in the last two.
+//   5 prompts of 1..300 tokens, 32 heads     36.6 us
+//   1000 tokens over 15001, 16 heads         202 us  1.12 PFLOP/s
+//   8192 tokens, 32 heads                    539 us  1.40 PFLOP/s
+// of which expand_kernel takes about 60 us in the last two.  4096 tokens of 16
+// heads by widths (keys + rotary, values): 128 + 64, 128: 95 us (1.08 PFLOP/s); 128 +
+// 0, 128: 86; 128 + 64, 64: 85; 64 + 64, 128: 84; 64, 128: 79; 64 + 64, 64: 79; 64, 64: 73
+// (0.59 PFLOP/s; the forms with narrow values spill 40 to 52 bytes a thread).  70
+// prompts of 64..128 tokens, 16 heads: 90 us.
 #include <cfloat>
 #include <cmath>
 
@@ -279,7 +283,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PrefillParams 
 // weights.  Two accumulators in tensor memory (columns 0 and 256): the epilogue
 // of one unit runs under the products of the next.  Rows past a sequence's end
 // are written as zeros (the attention multiplies them by probability 0).
-// 16000 tokens of 16 heads: 58 us for 67 GFLOP and 134 MB of keys and values, about 4200 cycles of products in the 6000
+// 16000 tokens of 16 heads: 60 us for 67 GFLOP and 134 MB of keys and values, about 4200 cycles of products in the 6000
 // that a unit takes; without the stores it would take 4900, so it is the way of the 134 MB through L2 that bounds it.
 // Weights split over a pair of CTAs (half the reads of them), stores by TMA from shared memory and both L2 policies
 // made no difference.

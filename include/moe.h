@@ -614,14 +614,14 @@ int moe_kv_append(const moe_kv_cache* cache, int layer, const void* rows, const 
  * fine): full pages are shared, a partly filled last page is copied (its
  * valid rows, every layer) to the lowest page that was free before the call,
  * in list order, and the pages dst[i] held are released.  src[i] == dst[i] does
- * nothing.  Too few free pages: MOE_DEV_ERR_CAPACITY, nothing changes.  Ids
+ * nothing.  n <= max_seqs, else MOE_ERR_INVALID_ARG.  Too few free pages: MOE_DEV_ERR_CAPACITY, nothing changes.  Ids
  * outside [0, max_seqs) and repeats of a dst: MOE_DEV_ERR_BAD_SEQ, skipped. */
 int moe_kv_fork(const moe_kv_cache* cache, const int32_t* src, const int32_t* dst, int n, void* ws,
                 size_t ws_bytes, uint32_t* dev_status, moe_stream_t stream);
 
 /* Empties n sequences: their pages' refs drop by one and their blocks become
  * -1.  Repeats and empty sequences do nothing; ids out of range set
- * MOE_DEV_ERR_BAD_SEQ. */
+ * MOE_DEV_ERR_BAD_SEQ.  n <= max_seqs, else MOE_ERR_INVALID_ARG. */
 int moe_kv_free(const moe_kv_cache* cache, const int32_t* seqs, int n, uint32_t* dev_status, moe_stream_t stream);
 
 /* Moves the pages in use to the front of the pool: with n_live pages in use,
