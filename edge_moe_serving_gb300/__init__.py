@@ -62,6 +62,7 @@ class moe_pool_nvfp4(ctypes.Structure):
 
 
 MOE_FP4_MXFP4, MOE_FP4_NVFP4 = 0, 1
+MOE_KV_BF16, MOE_KV_FP4 = 0, 1
 
 
 class moe_cache_fp4(ctypes.Structure):
@@ -73,7 +74,7 @@ class moe_cache_fp4(ctypes.Structure):
 class moe_kv_cache(ctypes.Structure):
     _fields_ = [("pages", c_void_p), ("table", c_void_p), ("lens", c_void_p), ("refs", c_void_p),
                 ("n_layers", c_int32), ("n_pages", c_int32), ("page_tokens", c_int32), ("rank", c_int32),
-                ("rope", c_int32), ("max_seqs", c_int32), ("max_blocks", c_int32), ("reserved", c_int32)]
+                ("rope", c_int32), ("max_seqs", c_int32), ("max_blocks", c_int32), ("format", c_int32)]
 
 
 class moe_bw_profile(ctypes.Structure):
@@ -135,12 +136,19 @@ def _load():
         "moe_layer_forward": (c_int, [POINTER(moe_layer), POINTER(moe_cache), P, c_int, P, c_uint32, c_int,
                                       c_int, c_uint64, c_int, POINTER(moe_layer_buffers), P, c_size_t, P, P,
                                       P]),
+        "moe_kv_row_bytes": (c_size_t, [c_int, c_int, c_int]),
         "moe_kv_workspace_size": (c_size_t, [POINTER(moe_kv_cache), c_int]),
         "moe_kv_reserve": (c_int, [POINTER(moe_kv_cache), P, P, c_int, P, c_size_t, P, P]),
         "moe_kv_append": (c_int, [POINTER(moe_kv_cache), c_int, P, P, P, c_int, P, P]),
+        "moe_kv_read": (c_int, [POINTER(moe_kv_cache), c_int, P, P, c_int, P, P, P]),
         "moe_kv_fork": (c_int, [POINTER(moe_kv_cache), P, P, c_int, P, c_size_t, P, P]),
         "moe_kv_free": (c_int, [POINTER(moe_kv_cache), P, c_int, P, P]),
         "moe_kv_compact": (c_int, [POINTER(moe_kv_cache), P, P, c_size_t, P, P]),
+        "moe_kv_evict_workspace_size": (c_size_t, [POINTER(moe_kv_cache), c_int]),
+        "moe_kv_evict": (c_int, [POINTER(moe_kv_cache), P, c_int, P, c_int, c_int, c_int, P, P, c_size_t, P, P]),
+        "moe_latent_weights_workspace_size": (c_size_t, [POINTER(moe_kv_cache), c_int, c_int, c_int]),
+        "moe_latent_weights": (c_int, [POINTER(moe_kv_cache), c_int, P, P, c_int, c_int, c_int, c_float, P, c_float, P,
+                                       P, c_size_t, P, P]),
         "moe_latent_decode_workspace_size": (c_size_t, [POINTER(moe_kv_cache), c_int, c_int, c_int, c_int]),
         "moe_latent_decode": (c_int, [POINTER(moe_kv_cache), c_int, P, P, c_int, c_int, c_int, c_float, c_int, P, P,
                                       P, c_size_t, P, P]),
@@ -166,6 +174,8 @@ EXPORTED = ["moe_version", "moe_status_string", "moe_check_bounded_wait", "moe_k
             "moe_expert_ffn_nvfp4_workspace_size", "moe_expert_ffn_nvfp4", "moe_layer_fp4_workspace_size",
             "moe_layer_forward_fp4", "moe_combine",
             "moe_layer_workspace_size", "moe_layer_forward", "moe_prefill_double_buffered",
+            "moe_kv_row_bytes", "moe_kv_read", "moe_kv_evict_workspace_size", "moe_kv_evict",
+            "moe_latent_weights_workspace_size", "moe_latent_weights",
             "moe_kv_workspace_size", "moe_kv_reserve", "moe_kv_append", "moe_kv_fork", "moe_kv_free",
             "moe_kv_compact", "moe_latent_decode_workspace_size", "moe_latent_decode",
             "moe_latent_prefill_workspace_size", "moe_latent_prefill"]
@@ -363,6 +373,10 @@ def moe_prefill_double_buffered(layers, source, layer_buf, state, x, T, out, ffn
         _p(dev_status), _s(stream), _s(copy_stream)))
 
 
+def moe_kv_row_bytes(rank, rope, format):
+    return _lib.moe_kv_row_bytes(rank, rope, format)
+
+
 def moe_kv_workspace_size(cache, n):
     return _lib.moe_kv_workspace_size(ctypes.byref(cache), n)
 
@@ -375,6 +389,11 @@ def moe_kv_reserve(cache, seqs, n_new, n, ws, ws_bytes, dev_status, stream=None)
 def moe_kv_append(cache, layer, rows, tok_seq, tok_pos, N, dev_status, stream=None):
     return _check("moe_kv_append", _lib.moe_kv_append(
         ctypes.byref(cache), layer, _p(rows), _p(tok_seq), _p(tok_pos), N, _p(dev_status), _s(stream)))
+
+
+def moe_kv_read(cache, layer, tok_seq, tok_pos, N, rows, dev_status, stream=None):
+    return _check("moe_kv_read", _lib.moe_kv_read(
+        ctypes.byref(cache), layer, _p(tok_seq), _p(tok_pos), N, _p(rows), _p(dev_status), _s(stream)))
 
 
 def moe_kv_fork(cache, src, dst, n, ws, ws_bytes, dev_status, stream=None):
@@ -391,6 +410,16 @@ def moe_kv_compact(cache, n_live_opt, ws, ws_bytes, dev_status, stream=None):
         ctypes.byref(cache), _p(n_live_opt), _p(ws), ws_bytes, _p(dev_status), _s(stream)))
 
 
+def moe_kv_evict_workspace_size(cache, n):
+    return _lib.moe_kv_evict_workspace_size(ctypes.byref(cache), n)
+
+
+def moe_kv_evict(cache, seqs, n, weights, budget, first, recent, kept_opt, ws, ws_bytes, dev_status, stream=None):
+    return _check("moe_kv_evict", _lib.moe_kv_evict(
+        ctypes.byref(cache), _p(seqs), n, _p(weights), budget, first, recent, _p(kept_opt), _p(ws), ws_bytes,
+        _p(dev_status), _s(stream)))
+
+
 def moe_latent_decode_workspace_size(cache, B, Q, heads, shared_tokens):
     return _lib.moe_latent_decode_workspace_size(ctypes.byref(cache), B, Q, heads, shared_tokens)
 
@@ -400,6 +429,17 @@ def moe_latent_decode(cache, layer, q, seqs, B, Q, heads, scale, shared_tokens, 
     return _check("moe_latent_decode", _lib.moe_latent_decode(
         ctypes.byref(cache), layer, _p(q), _p(seqs), B, Q, heads, scale, shared_tokens, _p(out), _p(lse_opt),
         _p(ws), ws_bytes, _p(dev_status), _s(stream)))
+
+
+def moe_latent_weights_workspace_size(cache, B, Q, heads):
+    return _lib.moe_latent_weights_workspace_size(ctypes.byref(cache), B, Q, heads)
+
+
+def moe_latent_weights(cache, layer, q, seqs, B, Q, heads, scale, lse, decay, weights, ws, ws_bytes, dev_status,
+                       stream=None):
+    return _check("moe_latent_weights", _lib.moe_latent_weights(
+        ctypes.byref(cache), layer, _p(q), _p(seqs), B, Q, heads, scale, _p(lse), decay, _p(weights), _p(ws), ws_bytes,
+        _p(dev_status), _s(stream)))
 
 
 def moe_latent_prefill_workspace_size(cache, B, T, heads, dn, dv, kv_tokens):

@@ -17,7 +17,7 @@
 // 16,000, 19 of 64,000 and 33 of 128,000; a compaction that moves nothing 4, 4, 9, 26
 // and 49 (two rounds each).
 #include "kv_append_shape.h"
-#include "kv_common.cuh"
+#include "kv_fp4.cuh"
 
 namespace moe {
 namespace {
@@ -160,7 +160,21 @@ reserve_kernel(const KvView kv, const int32_t* seqs, const int32_t* n_new, int n
   }
 }
 
-// ---------------------------------------------------------------- append
+// ---------------------------------------------------------------- append and read
+// Where the row of a token lies, or -1 (and the reason in status).  To be written, its page has to be its sequence's alone.
+__device__ inline long long row_place(const KvView& kv, int layer, int s, int pos, bool write, uint32_t* status) {
+  if (s < 0 || s >= kv.max_seqs || pos < 0 || pos >= kv.len_of(s)) {
+    set_status(status, MOE_DEV_ERR_BAD_SEQ);
+    return -1;
+  }
+  const int p = kv.table[(size_t)s * kv.max_blocks + (pos >> kv.page_shift)];
+  if (p < 0 || p >= kv.n_pages || (write && kv.refs[p] != 1)) {
+    set_status(status, MOE_DEV_ERR_BAD_PAGE);
+    return -1;
+  }
+  return (long long)kv.row_offset(layer, p, pos & (kv.page_tokens - 1));
+}
+
 // A warp takes `per` <= 32 rows at a time: one run of bytes to read, `per` places to write (61 MB of rows: 18 us, 6.7
 // TB/s read and written; with a thread per 16 bytes that finds its own place 24 us).
 __global__ void __launch_bounds__(kApplyThreads)
@@ -173,17 +187,7 @@ append_kernel(const KvView kv, int layer, const uint4* rows, const int32_t* tok_
   for (unsigned i0 = append_first(shape, blockIdx.x, threadIdx.x >> 5); i0 < N; i0 += step) {
     // lane j finds where row i0 + j goes (its dependent reads are the warp's only ones)
     const unsigned i = i0 + lane;
-    long long to = -1;
-    if (lane < (int)per && i < N) {
-      const int s = tok_seq[i], pos = tok_pos[i];
-      if (s < 0 || s >= kv.max_seqs || pos < 0 || pos >= kv.len_of(s)) {
-        set_status(status, MOE_DEV_ERR_BAD_SEQ);
-      } else {
-        const int p = kv.table[(size_t)s * kv.max_blocks + (pos >> kv.page_shift)];
-        if (p < 0 || p >= kv.n_pages || kv.refs[p] != 1) set_status(status, MOE_DEV_ERR_BAD_PAGE);
-        else to = (long long)kv.row_offset(layer, p, pos & (kv.page_tokens - 1));
-      }
-    }
+    const long long to = lane < (int)per && i < N ? row_place(kv, layer, tok_seq[i], tok_pos[i], true, status) : -1;
     const uint4* from = rows + (size_t)i0 * vecs;
     const int total = (int)min(per, N - i0) * vecs;
     for (int x0 = 0; x0 < total; x0 += 32 * 8) {          // eight reads in flight
@@ -199,6 +203,136 @@ append_kernel(const KvView kv, int layer, const uint4* rows, const int32_t* tok_
         const long long at = __shfl_sync(0xffffffffu, to, r);
         if (x < total && at >= 0) reinterpret_cast<uint4*>(kv.pages + at)[x - r * vecs] = v[j];
       }
+    }
+  }
+}
+
+// The reverse: rows of the cache, bf16, to a list.
+__global__ void __launch_bounds__(kApplyThreads)
+read_kernel(const KvView kv, int layer, const int32_t* tok_seq, const int32_t* tok_pos, unsigned N, uint4* rows,
+            const AppendShape shape, uint32_t* status) {
+  pdl_wait();
+  pdl_trigger();
+  const int vecs = kv.row >> 3, lane = threadIdx.x & 31;
+  const unsigned per = shape.per, step = append_step(shape);
+  for (unsigned i0 = append_first(shape, blockIdx.x, threadIdx.x >> 5); i0 < N; i0 += step) {
+    const unsigned i = i0 + lane;
+    const long long from = lane < (int)per && i < N ? row_place(kv, layer, tok_seq[i], tok_pos[i], false, status) : -1;
+    uint4* to = rows + (size_t)i0 * vecs;
+    const int total = (int)min(per, N - i0) * vecs;
+    for (int x0 = 0; x0 < total; x0 += 32 * 8) {
+      uint4 v[8];
+      bool there[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int x = x0 + 32 * j + lane, r = min(x / vecs, 31);
+        const long long at = __shfl_sync(0xffffffffu, from, r);
+        there[j] = x < total && at >= 0;
+        if (there[j]) v[j] = reinterpret_cast<const uint4*>(kv.pages + at)[x - r * vecs];
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (there[j]) to[x0 + 32 * j + lane] = v[j];
+    }
+  }
+}
+
+// Rows in 4 bits: a warp takes `per` rows, four at a time, a lane 16 entries of each (32 bytes of bf16, 8 of codes).
+constexpr int kFpRows = 4;
+
+__global__ void __launch_bounds__(kApplyThreads)
+append_fp4_kernel(const KvView kv, int layer, const uint4* rows, const int32_t* tok_seq, const int32_t* tok_pos,
+                  unsigned N, const AppendShape shape, uint32_t* status) {
+  pdl_wait();
+  pdl_trigger();
+  const int lane = threadIdx.x & 31, blocks = kv.rank / kFpBlock, rope_vecs = kv.rope >> 3;
+  const int in_vecs = 2 * blocks + rope_vecs, scales_at = kv.rank / 2 + 2 * kv.rope, scale_bytes = 2 * kv.row - scales_at;
+  const unsigned per = shape.per, step = append_step(shape);
+  bool clamped = false;
+  for (unsigned i0 = append_first(shape, blockIdx.x, threadIdx.x >> 5); i0 < N; i0 += step) {
+    const unsigned i = i0 + lane;
+    const long long to = lane < (int)per && i < N ? row_place(kv, layer, tok_seq[i], tok_pos[i], true, status) : -1;
+    const int n = (int)min(per, N - i0);
+    for (int r0 = 0; r0 < n; r0 += kFpRows) {
+      uint8_t* dst[kFpRows];
+#pragma unroll
+      for (int j = 0; j < kFpRows; ++j) {
+        const long long at = __shfl_sync(0xffffffffu, to, min(r0 + j, 31));
+        dst[j] = r0 + j < n && at >= 0 ? reinterpret_cast<uint8_t*>(kv.pages + at) : nullptr;
+      }
+      const uint4* from = rows + (size_t)(i0 + r0) * in_vecs;
+      for (int b = lane; b < scale_bytes; b += 32) {
+        uint4 v[kFpRows][2];
+#pragma unroll
+        for (int j = 0; j < kFpRows; ++j)
+          if (dst[j] && b < blocks) {
+            v[j][0] = __ldcs(from + j * in_vecs + 2 * b);
+            v[j][1] = __ldcs(from + j * in_vecs + 2 * b + 1);
+          }
+#pragma unroll
+        for (int j = 0; j < kFpRows; ++j)
+          if (dst[j]) {
+            Fp4Block q = {};
+            if (b < blocks) {
+              q = fp4_quantise(v[j][0], v[j][1]);
+              *reinterpret_cast<uint2*>(dst[j] + 8 * b) = q.codes;
+              clamped |= q.clamped;
+            }
+            dst[j][scales_at + b] = (uint8_t)q.scale;       // zeros behind the scales
+          }
+      }
+#pragma unroll
+      for (int j = 0; j < kFpRows; ++j)
+        if (dst[j])
+          for (int y = lane; y < rope_vecs; y += 32)
+            reinterpret_cast<uint4*>(dst[j] + kv.rank / 2)[y] = __ldcs(from + j * in_vecs + 2 * blocks + y);
+    }
+  }
+  if (clamped) set_status(status, MOE_DEV_ERR_RANGE);
+}
+
+__global__ void __launch_bounds__(kApplyThreads)
+read_fp4_kernel(const KvView kv, int layer, const int32_t* tok_seq, const int32_t* tok_pos, unsigned N, uint4* rows,
+                const AppendShape shape, uint32_t* status) {
+  pdl_wait();
+  pdl_trigger();
+  const int lane = threadIdx.x & 31, blocks = kv.rank / kFpBlock, rope_vecs = kv.rope >> 3;
+  const int out_vecs = 2 * blocks + rope_vecs, scales_at = kv.rank / 2 + 2 * kv.rope;
+  const unsigned per = shape.per, step = append_step(shape);
+  for (unsigned i0 = append_first(shape, blockIdx.x, threadIdx.x >> 5); i0 < N; i0 += step) {
+    const unsigned i = i0 + lane;
+    const long long at0 = lane < (int)per && i < N ? row_place(kv, layer, tok_seq[i], tok_pos[i], false, status) : -1;
+    const int n = (int)min(per, N - i0);
+    for (int r0 = 0; r0 < n; r0 += kFpRows) {
+      const uint8_t* src[kFpRows];
+#pragma unroll
+      for (int j = 0; j < kFpRows; ++j) {
+        const long long at = __shfl_sync(0xffffffffu, at0, min(r0 + j, 31));
+        src[j] = r0 + j < n && at >= 0 ? reinterpret_cast<const uint8_t*>(kv.pages + at) : nullptr;
+      }
+      uint4* to = rows + (size_t)(i0 + r0) * out_vecs;
+      for (int b = lane; b < blocks; b += 32) {
+        uint2 c[kFpRows];
+        uint32_t s[kFpRows];
+#pragma unroll
+        for (int j = 0; j < kFpRows; ++j)
+          if (src[j]) {
+            c[j] = *reinterpret_cast<const uint2*>(src[j] + 8 * b);
+            s[j] = src[j][scales_at + b];
+          }
+#pragma unroll
+        for (int j = 0; j < kFpRows; ++j)
+          if (src[j]) {
+            const uint32_t f = fp4_factor(s[j]);
+            to[j * out_vecs + 2 * b] = fp4_expand8(c[j].x, f);
+            to[j * out_vecs + 2 * b + 1] = fp4_expand8(c[j].y, f);
+          }
+      }
+#pragma unroll
+      for (int j = 0; j < kFpRows; ++j)
+        if (src[j])
+          for (int y = lane; y < rope_vecs; y += 32)
+            to[j * out_vecs + 2 * blocks + y] = reinterpret_cast<const uint4*>(src[j] + kv.rank / 2)[y];
     }
   }
 }
@@ -510,6 +644,12 @@ using namespace moe;
 
 extern "C" {
 
+size_t moe_kv_row_bytes(int rank, int rope, int format) {
+  if (rank < 1 || rope < 0 || rank % 8 || rope % 8 || (long long)rank + rope > (1 << 20)) return 0;
+  if (format == MOE_KV_BF16) return 2 * ((size_t)rank + rope);
+  return format == MOE_KV_FP4 && rank % 32 == 0 ? fp4_row_bytes(rank, rope) : 0;
+}
+
 size_t moe_kv_workspace_size(const moe_kv_cache* cache, int n) {
   return check_kv(cache) != MOE_OK || n < 0 ? 0 : kv_ws_bytes(*cache, n);
 }
@@ -537,9 +677,23 @@ int moe_kv_append(const moe_kv_cache* cache, int layer, const void* rows, const 
   if (!kv_aligned(rows, 16)) return MOE_ERR_UNSUPPORTED;
   static_assert(kAppendWarps == kApplyThreads / 32, "warps of a CTA");
   const AppendShape shape = append_shape((unsigned)N, (unsigned)num_sms());
-  return status_of(launch_k(append_kernel, shape.ctas, kApplyThreads, 0, reinterpret_cast<cudaStream_t>(stream),
-                            kv_view(*cache), layer, reinterpret_cast<const uint4*>(rows), tok_seq, tok_pos, (unsigned)N,
-                            shape, dev_status));
+  return status_of(launch_k(cache->format == MOE_KV_FP4 ? append_fp4_kernel : append_kernel, shape.ctas, kApplyThreads, 0,
+                            reinterpret_cast<cudaStream_t>(stream), kv_view(*cache), layer,
+                            reinterpret_cast<const uint4*>(rows), tok_seq, tok_pos, (unsigned)N, shape, dev_status));
+}
+
+int moe_kv_read(const moe_kv_cache* cache, int layer, const int32_t* tok_seq, const int32_t* tok_pos, int N, void* rows,
+                uint32_t* dev_status, moe_stream_t stream) {
+  const int st = check_kv(cache);
+  if (st != MOE_OK) return st;
+  if (layer < 0 || layer >= cache->n_layers || N < 0) return MOE_ERR_INVALID_ARG;
+  if (N == 0) return MOE_OK;
+  if (!rows || !tok_seq || !tok_pos) return MOE_ERR_INVALID_ARG;
+  if (!kv_aligned(rows, 16)) return MOE_ERR_UNSUPPORTED;
+  const AppendShape shape = append_shape((unsigned)N, (unsigned)num_sms());
+  return status_of(launch_k(cache->format == MOE_KV_FP4 ? read_fp4_kernel : read_kernel, shape.ctas, kApplyThreads, 0,
+                            reinterpret_cast<cudaStream_t>(stream), kv_view(*cache), layer, tok_seq, tok_pos, (unsigned)N,
+                            reinterpret_cast<uint4*>(rows), shape, dev_status));
 }
 
 int moe_kv_fork(const moe_kv_cache* cache, const int32_t* src, const int32_t* dst, int n, void* ws,
@@ -556,7 +710,7 @@ int moe_kv_fork(const moe_kv_cache* cache, const int32_t* src, const int32_t* ds
   const KvView kv = kv_view(*cache);
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const size_t first = (size_t)cache->max_seqs * sizeof(int);
-  const long long page_vecs = (long long)cache->n_layers * cache->page_tokens * ((cache->rank + cache->rope) / 8);
+  const long long page_vecs = (long long)cache->n_layers * cache->page_tokens * (kv.row / 8);
   if (n * page_vecs * 16 <= kSmallCopy)
     return status_of(launch_k(fork_small_kernel, kCluster, kPlanThreads, first, s, kv, src, dst, n, plan, list, snap,
                               dev_status));
@@ -591,7 +745,7 @@ int moe_kv_compact(const moe_kv_cache* cache, int32_t* n_live_opt, void* ws, siz
   int32_t* to = reinterpret_cast<int32_t*>(b + ints(2) + 2 * list);
   const KvView kv = kv_view(*cache);
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const long long pool = (long long)cache->n_layers * cache->n_pages * cache->page_tokens * (cache->rank + cache->rope) * 2;
+  const long long pool = (long long)cache->n_layers * cache->n_pages * cache->page_tokens * kv.row * 2;
   if (pool <= kSmallPool)
     return status_of(launch_k(compact_small_kernel, kCluster, kPlanThreads, 0, s, kv, counts, from, dest, to, n_live_opt));
   cudaError_t e = launch_k(compact_plan_kernel, 1, kPlanThreads, 0, s, kv, counts, from, dest, to, n_live_opt);

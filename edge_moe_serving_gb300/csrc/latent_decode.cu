@@ -44,7 +44,7 @@
 #include <cmath>
 #include <type_traits>
 
-#include "kv_common.cuh"
+#include "kv_fp4.cuh"
 #include "latent_line.h"
 #include "tc_common.cuh"
 
@@ -57,7 +57,8 @@ constexpr int kChunk = kTok * kBK * 2;   // 8 KB: 64 tokens x 64 entries (also 6
 constexpr int kMaxPairs = 4;             // 128-entry slices of the latent
 constexpr int kMaxSlots = 4;             // tiles in flight
 constexpr int kBatch = 512;              // sequences of one launch (lengths and tile sums in shared memory)
-constexpr int kThreads = 224;
+constexpr int kThreads = 224;            // a bf16 cache's; one in 4 bits has kExpandWarps more
+constexpr int kExpandWarps = 8;
 constexpr int kSoftThreads = 128;
 constexpr int kTmemCols = 512;
 constexpr int kSCol = 256;               // S tiles at columns 256 and 320; O slices at 0, 64, 128, 192
@@ -257,7 +258,7 @@ struct alignas(16) Shared {   // its size is what the dynamic shared memory leav
   uint32_t tmem;
   int abort;
   float factor[kRows];   // rescaling of each row; in the epilogue 1 / l
-  int warp_sum[kThreads / 32];
+  int warp_sum[kThreads / 32 + kExpandWarps];
   int sees[kSoftThreads / 32];
   unsigned long long bad[2];   // tokens of a tile (by its parity) with a NaN or infinite latent entry, bit by bit
   int pref[kBatch + 1];
@@ -265,7 +266,8 @@ struct alignas(16) Shared {   // its size is what the dynamic shared memory leav
   int ids[kBatch];
 };
 
-__global__ void __launch_bounds__(kThreads, 1)
+template <bool FP4>
+__global__ void __launch_bounds__(kThreads + (FP4 ? 32 * kExpandWarps : 0), 1)
 decode_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_constant__ CUtensorMap map_pair,
               const __grid_constant__ CUtensorMap map_qs, const __grid_constant__ CUtensorMap map_qsr,
               const __grid_constant__ CUtensorMap map_qp, const __grid_constant__ CUtensorMap map_qpr,
@@ -273,6 +275,7 @@ decode_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_constant_
   extern __shared__ uint8_t smem_raw[];
   __shared__ Shared sh;
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  constexpr int kAll = kThreads + (FP4 ? 32 * kExpandWarps : 0);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int chunks = 2 * p.pairs + 1;               // the last one holds the rotary part, then P
   uint8_t* skv = smem + chunks * kChunk;
@@ -284,7 +287,7 @@ decode_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_constant_
   if (tid == 0) {
     for (int s = 0; s < p.slots; ++s)
       for (int j = 0; j <= p.pairs; ++j) {
-        mbar_init(&sh.full[s][j], 1);
+        mbar_init(&sh.full[s][j], FP4 && j < p.pairs ? kExpandWarps : 1);
         mbar_init(&sh.empty[s][j], 1);
       }
     mbar_init(&sh.q_full, 1);
@@ -302,7 +305,7 @@ decode_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_constant_
   }
   if (tid == 32 * 2) {
     prefetch_map(&map_kv);
-    prefetch_map(&map_pair);
+    if (!FP4) prefetch_map(&map_pair);
     prefetch_map(&map_qs);
     prefetch_map(&map_qsr);
   }
@@ -316,7 +319,7 @@ decode_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_constant_
   // lengths and tile sums of the batch (every CTA for itself)
   {
     int carry = 0;
-    for (int b0 = 0; b0 < p.B; b0 += kThreads) {
+    for (int b0 = 0; b0 < p.B; b0 += kAll) {
       const int b = b0 + tid;
       int n = 0;
       if (b < p.B) {
@@ -338,7 +341,7 @@ decode_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_constant_
       __syncthreads();
       int base = carry;
       for (int w = 0; w < warp; ++w) base += sh.warp_sum[w];
-      for (int w = 0; w < kThreads / 32; ++w) carry += sh.warp_sum[w];
+      for (int w = 0; w < kAll / 32; ++w) carry += sh.warp_sum[w];
       if (b < p.B) sh.pref[b + 1] = base + inc;
       __syncthreads();
     }
@@ -348,7 +351,7 @@ decode_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_constant_
   __syncthreads();
   tc_fence_after();
   if (blockIdx.x == 0)
-    for (int b = tid; b <= p.B; b += kThreads) p.plan[b] = sh.pref[b];
+    for (int b = tid; b <= p.B; b += kAll) p.plan[b] = sh.pref[b];
   const uint32_t tmem = sh.tmem;
   volatile int* abort_flag = &sh.abort;
   SegIter it(p, sh.pref, sh.len, sh.ids);
@@ -409,10 +412,10 @@ decode_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_constant_
 #pragma unroll
         for (int i = 0; i < kTok / 16; ++i) rows[i] = (int)uni(lane == i ? row : 0);
         const uint32_t dst = kv0 + slot * slot_bytes, bar = full0 + slot * (uint32_t)sizeof(sh.full[0]);
-        for (int j = 0; j < parts; ++j) {
+        for (int j = FP4 ? p.pairs : 0; j < parts; ++j) {    // in 4 bits: the rotary key alone
           ok = warp_wait(&sh.empty[slot][j], par, abort_flag);
           if (!ok) break;
-          const bool pair = j < p.pairs;
+          const bool pair = !FP4 && j < p.pairs;
           const uint32_t to = dst + 2 * j * kChunk, fb = bar + 8 * j;
           mbar_expect_tx_warp(fb, (uint32_t)(nb * box * (pair ? 256 : 128)));
           if (box == kTok && pair) {   // both chunks of the pair in one copy
@@ -421,7 +424,7 @@ decode_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_constant_
 #pragma unroll
             for (int i = 0; i < kTok / 16; ++i)
               if (i < nb) {
-                tma_load_2d_hint_warp(to + i * box * 128, &map_kv, fb, 2 * j * kBK, rows[i], pol);
+                tma_load_2d_hint_warp(to + i * box * 128, &map_kv, fb, FP4 ? p.kv.rope_at : 2 * j * kBK, rows[i], pol);
                 if (pair) tma_load_2d_hint_warp(to + kChunk + i * box * 128, &map_kv, fb, 2 * j * kBK + kBK, rows[i], pol);
               }
           }
@@ -441,7 +444,7 @@ decode_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_constant_
     if (nseg) mbar_wait(&sh.q_full, (nseg - 1) & 1, &no_abort);
     for (int s = 0; s < p.slots; ++s) {
       const int loads = tile / p.slots + (tile % p.slots > s ? 1 : 0);
-      for (int j = 0; j < parts; ++j)
+      for (int j = FP4 ? p.pairs : 0; j < parts; ++j)
         if (loads > 0) mbar_wait(&sh.full[s][j], (loads - 1) & 1, &no_abort);
     }
     __syncwarp();
@@ -536,6 +539,54 @@ decode_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_constant_
       volatile int no_abort = 0;
       tc_commit_warp(&sh.drain[1]);
       mbar_wait(&sh.drain[1], 0, &no_abort);
+    }
+    __syncwarp();
+  } else if (FP4 && warp >= kThreads / 32) {
+    // ------------------------------------------------ latents in 4 bits, expanded into the tile that a copy would fill
+    // Four threads a token; of each 128-entry pair a thread has 16 bytes of codes, a quarter.
+    const int et = tid - kThreads, r = et >> 2, v = et & 3;
+    const int scales_at = p.kv.rank / 2 + 2 * p.rope;
+    int slot = 0;
+    uint32_t par = 1;
+    bool ok = true;
+    const bool pseq_ok = p.np == 0 || (*p.prefix_seq >= 0 && *p.prefix_seq < p.kv.max_seqs);
+    while (__any_sync(0xffffffffu, ok && it.next(sg))) {
+      const bool seq_ok = !sg.prefix || pseq_ok;
+      const int32_t* blocks = p.kv.table + (seq_ok ? (size_t)sg.seq * p.kv.max_blocks : 0);
+      for (int t0 = sg.tok0; ok && t0 < sg.tok1; t0 += kTok) {
+        const int t = t0 + r;
+        const uint8_t* row = nullptr;
+        if (t < sg.tok1) {
+          int pg = seq_ok ? blocks[t >> p.kv.page_shift] : -1;
+          if (pg < 0 || pg >= p.kv.n_pages) {
+            set_status(p.status, seq_ok ? MOE_DEV_ERR_BAD_PAGE : MOE_DEV_ERR_BAD_SEQ);
+            pg = 0;
+          }
+          row = reinterpret_cast<const uint8_t*>(p.kv.pages + p.kv.row_offset(p.layer, pg, t & (p.kv.page_tokens - 1)));
+        }
+        uint4 c[kMaxPairs];
+        uint32_t s[kMaxPairs];
+#pragma unroll
+        for (int j = 0; j < kMaxPairs; ++j)
+          if (row && j < p.pairs) {
+            c[j] = ldg_stream(row + 64 * j + 16 * v);
+            s[j] = *reinterpret_cast<const unsigned short*>(row + scales_at + 8 * j + 2 * v);
+          }
+#pragma unroll
+        for (int j = 0; j < kMaxPairs; ++j) {
+          if (j >= p.pairs) break;
+          ok = ok && warp_wait(&sh.empty[slot][j], par, abort_flag);
+          if (!ok) break;
+          if (row) fp4_store32(skv + slot * slot_bytes + 2 * j * kChunk, kChunk, r, v, c[j], s[j]);
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh.full[slot][j]);
+        }
+        if (++slot == p.slots) {
+          slot = 0;
+          par ^= 1u;
+        }
+      }
     }
     __syncwarp();
   } else {
@@ -1008,6 +1059,19 @@ DecodeWs decode_ws(const DecodeParams& p, int rank) {
 
 bool decode_shape_ok(int B, int Q, int heads) { return B <= 4096 && (long long)Q * heads <= 1024; }
 
+template <bool FP4>
+cudaError_t launch_decode_kernel(const DecodeParams& p, int smem, cudaStream_t s, const CUtensorMap& kv, const CUtensorMap& pair,
+                                 const CUtensorMap& qs, const CUtensorMap& qsr, const CUtensorMap& qp,
+                                 const CUtensorMap& qpr) {
+  static std::atomic<unsigned char> attr[kMaxDevices];
+  const cudaError_t e = once_per_device(attr, [] {
+    return cudaFuncSetAttribute(decode_kernel<FP4>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                227 * 1024 - (int)sizeof(Shared));
+  });
+  constexpr int threads = kThreads + (FP4 ? 32 * kExpandWarps : 0);
+  return e == cudaSuccess ? launch_k(decode_kernel<FP4>, p.ctas, threads, smem, s, kv, pair, qs, qsr, qp, qpr, p) : e;
+}
+
 int launch_decode(const moe_kv_cache& c, DecodeParams p, const void* q, cudaStream_t s) {
   static_assert(sizeof(Shared) + 1024 + (2 * kMaxPairs + 1) * kChunk * 3 <= 227 * 1024, "shared memory");
   const int row = c.rank + c.rope, slot = (2 * p.pairs + 1) * kChunk;
@@ -1016,21 +1080,19 @@ int launch_decode(const moe_kv_cache& c, DecodeParams p, const void* q, cudaStre
   const int smem = (1 + p.slots) * slot + 1024;
   CUtensorMap kv, pair, qs, qsr, qp, qpr;   // cache rows by chunk and by pair; query tiles of sequences and of the prefix
   const uint64_t rows = (uint64_t)c.n_layers * c.n_pages * c.page_tokens, qrows = (uint64_t)p.B * p.Q * p.heads;
-  if (!make_map(&kv, c.pages, row, rows, c.page_tokens < kTok ? c.page_tokens : kTok) ||
-      !make_map_chunks(&pair, c.pages, row, rows, kTok, 2) || !make_map_chunks(&qs, q, row, qrows, p.NR, 2 * p.pairs) ||
+  const bool fp4 = c.format == MOE_KV_FP4;
+  if (!make_map(&kv, c.pages, p.kv.row, rows, c.page_tokens < kTok ? c.page_tokens : kTok) ||
+      (!fp4 && !make_map_chunks(&pair, c.pages, row, rows, kTok, 2)) || !make_map_chunks(&qs, q, row, qrows, p.NR, 2 * p.pairs) ||
       !make_map(&qsr, q, row, qrows, p.NR))
     return MOE_ERR_CUDA;
+  if (fp4) pair = kv;
   qp = qs;
   qpr = qsr;
   if (p.np && p.NRp != p.NR &&
       (!make_map_chunks(&qp, q, row, qrows, p.NRp, 2 * p.pairs) || !make_map(&qpr, q, row, qrows, p.NRp)))
     return MOE_ERR_CUDA;
-  static std::atomic<unsigned char> attr[kMaxDevices];
-  cudaError_t e = once_per_device(attr, [] {
-    return cudaFuncSetAttribute(decode_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                227 * 1024 - (int)sizeof(Shared));
-  });
-  if (e == cudaSuccess) e = launch_k(decode_kernel, p.ctas, kThreads, smem, s, kv, pair, qs, qsr, qp, qpr, p);
+  cudaError_t e = fp4 ? launch_decode_kernel<true>(p, smem, s, kv, pair, qs, qsr, qp, qpr)
+                      : launch_decode_kernel<false>(p, smem, s, kv, pair, qs, qsr, qp, qpr);
   // a CTA a row while the rows alone do not fill the SMs (then a row has many pieces), else a warp a row: whole calls over
   // 1200 tokens a sequence, us, CTA / warp: 128 rows 13.5 / 16.5, 160 rows 16.2 / 16.5, 288 rows 17.6 / 16.5, 1216 rows
   // 37.6 / 24.7

@@ -30,7 +30,7 @@
 
 #include <cuda_fp16.h>
 
-#include "kv_common.cuh"
+#include "kv_fp4.cuh"
 #include "tc_common.cuh"
 
 namespace moe {
@@ -65,6 +65,7 @@ struct PrefillParams {
   KvView kv;
   int layer, B, T, heads, dn, dv, rope, kv_rows, max_blocks_q, sms;
   int max_splits;           // shares of a query block's tokens that there is room for
+  bool fp4;                 // the cache's format
   float scale_log2;
   const __nv_bfloat16* q;
   const int32_t* seqs;
@@ -318,7 +319,8 @@ __device__ inline void st_sector(void* dst, const uint32_t* v) {
                : "memory");
 }
 
-__global__ void __launch_bounds__(kExThreads, 1)
+template <bool FP4>
+__global__ void __launch_bounds__(kExThreads + (FP4 ? 128 : 0), 1)
 expand_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_w,
               const PrefillParams p) {
   extern __shared__ uint8_t smem_raw[];
@@ -327,7 +329,7 @@ expand_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int chunks = p.kv.rank / kBK, N = p.dn + p.dv;
   if (tid == 0) {
-    for (int c = 0; c < chunks; ++c) mbar_init(&sh.a_full[c], 1);
+    for (int c = 0; c < chunks; ++c) mbar_init(&sh.a_full[c], FP4 ? 4 : 1);
     mbar_init(&sh.a_empty, 1);
     for (int i = 0; i < kExStages; ++i) {
       mbar_init(&sh.b_full[i], 1);
@@ -342,7 +344,7 @@ expand_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (tid == 64) {
-    prefetch_map(&map_x);
+    if (!FP4) prefetch_map(&map_x);
     prefetch_map(&map_w);
   }
   if (warp == 1) {
@@ -392,7 +394,7 @@ expand_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
     for (int u = u0; ok && u < u1; ++u) {
       const int tile = u / p.heads, head = u - tile * p.heads;
       int c0 = 0;
-      if (u == u0 || head == 0) {                          // another token tile
+      if (!FP4 && (u == u0 || head == 0)) {                // another token tile
         const int4 d = tile_of(p, sh, tile);   // sequence, first token, length
         const int nb = (int)uni((min(kTile, d.z - d.y) + box - 1) / box);
         int row = 0;
@@ -423,7 +425,7 @@ expand_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
       for (int c = c0; ok && c < chunks; ++c) load_w(head, c);
     }
     volatile int no_abort = 0;
-    if (loaded)
+    if (loaded)                                            // by copies, that is
       for (int c = 0; c < chunks; ++c) mbar_wait(&sh.a_full[c], (loaded - 1) & 1, &no_abort);
     for (int i = 0; i < kExStages; ++i) {
       const int n = fills / kExStages + (fills % kExStages > i ? 1 : 0);
@@ -467,6 +469,42 @@ expand_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
       mbar_wait(&sh.drain, 0, &no_abort);
     }
     __syncwarp();
+  } else if (FP4 && warp >= kExThreads / 32) {
+    // ------------------------------------------------ latents in 4 bits, expanded: a thread a token
+    const int r = tid - kExThreads, scales_at = p.kv.rank / 2 + 2 * p.rope;
+    int loaded = 0;
+    for (int u = u0; u < u1; ++u) {
+      const int tile = u / p.heads;
+      if (u != u0 && u != tile * p.heads) continue;
+      const int4 d = tile_of(p, sh, tile);
+      const int t = d.y + r;
+      const uint8_t* row = nullptr;
+      if (t < d.z) {
+        int pg = p.kv.table[(size_t)d.x * p.kv.max_blocks + (t >> p.kv.page_shift)];
+        if (pg < 0 || pg >= p.kv.n_pages) {
+          set_status(p.status, MOE_DEV_ERR_BAD_PAGE);
+          pg = 0;
+        }
+        row = reinterpret_cast<const uint8_t*>(p.kv.pages + p.kv.row_offset(p.layer, pg, t & (p.kv.page_tokens - 1)));
+      }
+      if (!warp_wait(&sh.a_empty, (loaded & 1) ^ 1u, abort_flag)) break;
+      ++loaded;
+      for (int c = 0; c < chunks; c += 2) {
+        if (row) {
+#pragma unroll
+          for (int v = 0; v < 4; ++v)
+            fp4_store32(smem + c * kChunkBytes, kChunkBytes, r, v, ldg_stream(row + 32 * c + 16 * v),
+                        *reinterpret_cast<const unsigned short*>(row + scales_at + 4 * c + 2 * v));
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&sh.a_full[c]);
+          mbar_arrive(&sh.a_full[c + 1]);
+        }
+      }
+    }
+    __syncwarp();
   } else if (warp >= 10) {
     // ------------------------------------------------ rotary keys, once per token: 16 bytes a thread, neighbours in a row
     const int vecs = p.rope / 8;
@@ -483,7 +521,7 @@ expand_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
           int pg = p.kv.table[(size_t)d.x * p.kv.max_blocks + (t >> p.kv.page_shift)];
           if (pg < 0 || pg >= p.kv.n_pages) pg = 0;
           v = __ldg(reinterpret_cast<const uint4*>(p.kv.pages + p.kv.row_offset(p.layer, pg, t & (p.kv.page_tokens - 1)) +
-                                                   p.kv.rank) + y);
+                                                   p.kv.rope_at) + y);
         }
         reinterpret_cast<uint4*>(p.r + ((size_t)tile * kTile + r) * p.rope)[y] = v;
       }
@@ -1184,6 +1222,18 @@ cudaError_t launch_attend(const CUtensorMap& mq, const CUtensorMap& mk, const CU
   return e == cudaSuccess ? launch_k(attend_kernel<KC, VC>, num_sms(), kThreads, A::kSmem, s, mq, mk, mr, mv, p) : e;
 }
 
+template <bool FP4>
+cudaError_t launch_expand(const CUtensorMap& mx, const CUtensorMap& mw, const PrefillParams& p, cudaStream_t s) {
+  const int smem = p.kv.rank / kBK * kChunkBytes + kExStages * kExStage + 1024;
+  constexpr int kExSmem = kMaxChunks * kChunkBytes + kExStages * kExStage + 1024;
+  static_assert(kExSmem + sizeof(ExShared) <= 227 * 1024, "shared memory");
+  static std::atomic<unsigned char> attr[kMaxDevices];
+  const cudaError_t e = once_per_device(attr, [] {
+    return cudaFuncSetAttribute(expand_kernel<FP4>, cudaFuncAttributeMaxDynamicSharedMemorySize, kExSmem);
+  });
+  return e == cudaSuccess ? launch_k(expand_kernel<FP4>, num_sms(), kExThreads + (FP4 ? 128 : 0), smem, s, mx, mw, p) : e;
+}
+
 // f16 bits move like bf16 bits: the maps' element type only has to be 16 bits wide
 int launch_prefill(const PrefillParams& p, cudaStream_t s) {
   CUtensorMap mq, mk, mr, mv, mx, mw;
@@ -1194,15 +1244,9 @@ int launch_prefill(const PrefillParams& p, cudaStream_t s) {
       !make_map(&mv, p.v, p.dv, rows, kTile) || !make_map(&mx, p.kv.pages, p.kv.row, cache_rows, p.kv.page_tokens) ||
       !make_map(&mw, p.w, p.kv.rank, (uint64_t)p.heads * (p.dn + p.dv), p.dn + p.dv))
     return MOE_ERR_CUDA;
-  const int ex_smem = p.kv.rank / kBK * kChunkBytes + kExStages * kExStage + 1024;
-  constexpr int kExSmem = kMaxChunks * kChunkBytes + kExStages * kExStage + 1024;
-  static_assert(kExSmem + sizeof(ExShared) <= 227 * 1024, "shared memory");
-  static std::atomic<unsigned char> attr[kMaxDevices];
-  cudaError_t e = once_per_device(attr, [] {
-    return cudaFuncSetAttribute(expand_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kExSmem);
-  });
+  cudaError_t e = cudaSuccess;
   if (e == cudaSuccess && p.B > kSmallB) e = launch_k(plan_kernel, 1, kPlanThreads, 0, s, p);
-  if (e == cudaSuccess) e = launch_k(expand_kernel, num_sms(), kExThreads, ex_smem, s, mx, mw, p);
+  if (e == cudaSuccess) e = p.fp4 ? launch_expand<true>(mx, mw, p, s) : launch_expand<false>(mx, mw, p, s);
   if (e == cudaSuccess) {
     const int kc = p.dn / kBK + (p.rope ? 1 : 0), vc = p.dv / kBK;
     e = vc == 2 ? (kc == 3   ? launch_attend<3, 2>(mq, mk, mr, mv, p, s)
@@ -1257,6 +1301,7 @@ int moe_latent_prefill(const moe_kv_cache* cache, int layer, const void* q, cons
   p.dn = dn;
   p.dv = dv;
   p.rope = cache->rope;
+  p.fp4 = cache->format == MOE_KV_FP4;
   p.kv_rows = w.rows;
   p.max_blocks_q = w.n_blocks;
   // zero as the smallest normal number: a token out of sight scores -infinity, and 0 * -infinity is NaN

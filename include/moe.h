@@ -65,7 +65,7 @@ typedef struct CUstream_st* moe_stream_t; /* same type as cudaStream_t; NULL = l
 #define MOE_DEV_ERR_BAD_SEQ 16u   /* a sequence id, token position or query range outside the cache; skipped */
 #define MOE_DEV_ERR_BAD_PAGE 32u  /* a block-table entry names no page, or an append meets a page others share */
 #define MOE_DEV_ERR_CAPACITY 64u  /* too few free pages, blocks or workspace rows; the call changed nothing */
-#define MOE_DEV_ERR_RANGE 128u    /* an expanded value beyond 65504 was clamped to it */
+#define MOE_DEV_ERR_RANGE 128u    /* a value beyond its form's range was clamped: an expanded value to 65504, a latent to 368640 */
 
 /* fill policy of moe_cache_bind_slots: which q misses form the fill set F */
 #define MOE_FILL_LOWEST_ID 0  /* the q misses with the lowest expert ids */
@@ -569,11 +569,25 @@ int moe_prefill_double_buffered(const moe_layer* layers, int n_layers, const moe
  *   refs  [n_pages] int32               block-table entries that name the page; 0 = free
  * An empty cache has table = -1, lens = 0, refs = 0.  Pages hold any bits
  * where no token was stored, NaN among them: nothing reads those.
+ *
+ * format MOE_KV_FP4 keeps the latents in 4 bits: pages [n_layers, n_pages,
+ * page_tokens, row bytes], a row of moe_kv_row_bytes bytes (rank 512, rope 64: 416
+ * where bf16 takes 1152) that holds, one behind the other,
+ *   rank / 2 bytes    codes, FP4 E2M1, entry 2c in the low nibble of byte c
+ *   2 rope bytes      the rotary key, bf16
+ *   rank / 16 bytes   scales, one per 16 entries: exponent (5 bits, bias 15) and
+ *                     significand (3 bits) as f16 has them, no sign; exponent 31 is NaN
+ *   zeros             up to a multiple of 16 bytes
+ * An entry is its code times its scale, a bf16 number exactly, so every call over
+ * such a cache answers as over a bf16 cache of the rows that moe_kv_read gives.
  * Every call below checks the struct: MOE_ERR_INVALID_ARG for a NULL struct or
- * array, a size below 1 (rope: below 0); MOE_ERR_UNSUPPORTED for page_tokens
- * not in {16, 32, 64, 128}, rank or rope not a multiple of 8, max_seqs above
+ * array, a size below 1 (rope: below 0), an unknown format; MOE_ERR_UNSUPPORTED for page_tokens
+ * not in {16, 32, 64, 128}, rank or rope not a multiple of 8 (MOE_KV_FP4: rank of 32), max_seqs above
  * 8192, n_layers * n_pages * page_tokens or max_seqs * max_blocks above
  * INT_MAX, pages not 16-byte aligned, an int32 array not 4-byte aligned. */
+#define MOE_KV_BF16 0
+#define MOE_KV_FP4 1
+
 typedef struct moe_kv_cache {
   void* pages;
   int32_t* table;
@@ -586,8 +600,11 @@ typedef struct moe_kv_cache {
   int32_t rope;
   int32_t max_seqs;
   int32_t max_blocks;
-  int32_t reserved;   /* 0 */
+  int32_t format;     /* MOE_KV_BF16 or MOE_KV_FP4 */
 } moe_kv_cache;
+
+/* Bytes of a cached row (0 for a rank, rope or format that the struct's checks refuse). */
+size_t moe_kv_row_bytes(int rank, int rope, int format);
 
 /* Bytes of ws that the page calls below need for lists of up to n sequences
  * (0 for a bad struct or n < 0).  A workspace of that size serves shorter lists too. */
@@ -605,9 +622,20 @@ int moe_kv_reserve(const moe_kv_cache* cache, const int32_t* seqs, const int32_t
 /* Stores N rows (bf16 [N, rank + rope], 16-byte aligned) in one layer: row i is
  * token tok_pos[i] of sequence tok_seq[i], inside the length that
  * moe_kv_reserve gave it.  Entries out of range set MOE_DEV_ERR_BAD_SEQ, entries
- * whose page is missing or shared (refs > 1) MOE_DEV_ERR_BAD_PAGE; both are skipped. */
+ * whose page is missing or shared (refs > 1) MOE_DEV_ERR_BAD_PAGE; both are skipped.
+ * MOE_KV_FP4: a scale is the largest magnitude of its 16 entries / 6, a code the
+ * entry / scale, each rounded to nearest, ties to even.  Where the scale would pass
+ * 61440 it is 61440, entries beyond 6 scales become 368640, and MOE_DEV_ERR_RANGE is
+ * set; a NaN or an infinity makes its 16 entries NaN. */
 int moe_kv_append(const moe_kv_cache* cache, int layer, const void* rows, const int32_t* tok_seq,
                   const int32_t* tok_pos, int N, uint32_t* dev_status, moe_stream_t stream);
+
+/* Reads N rows of one layer back as bf16 [N, rank + rope] (16-byte aligned): row i is
+ * token tok_pos[i] of sequence tok_seq[i], the value that its stored form stands for.
+ * Shared pages can be read.  Entries out of range set MOE_DEV_ERR_BAD_SEQ, a missing
+ * page MOE_DEV_ERR_BAD_PAGE; their rows are not written. */
+int moe_kv_read(const moe_kv_cache* cache, int layer, const int32_t* tok_seq, const int32_t* tok_pos, int N,
+                void* rows, uint32_t* dev_status, moe_stream_t stream);
 
 /* Makes dst[i] a copy of src[i] for n pairs at once, every source as it was
  * before the call (a permutation or a fan-out among the same sequences is
@@ -631,6 +659,32 @@ int moe_kv_free(const moe_kv_cache* cache, const int32_t* seqs, int n, uint32_t*
  * afterwards. */
 int moe_kv_compact(const moe_kv_cache* cache, int32_t* n_live_opt, void* ws, size_t ws_bytes,
                    uint32_t* dev_status, moe_stream_t stream);
+
+/* Shortens sequences to their heaviest tokens.  weights fp32 [n_layers, max_seqs,
+ * max_blocks * page_tokens]: what each token's attention adds up to, as
+ * moe_latent_weights leaves it.  Of each listed sequence of len > budget tokens these stay, in every layer:
+ *   the head    the first `first` tokens, and every token up to the end of the last
+ *               page that another block-table entry names too (dropping those would free nothing)
+ *   the tail    the last `recent` tokens
+ *   the rest    of the tokens between them the heaviest, as many as make
+ *               max(budget, head + tail) in all; of equal weights the earlier token, a NaN
+ *               before every number
+ * in the order they were in: token j of the shortened sequence is the j-th that stays, its
+ * row and its weight move there, weights from the new length to len become 0, and pages
+ * behind the new length are released.  Each layer chooses by its own weights; lengths
+ * and block tables are one for all layers.  A sequence within the budget stays as it is.
+ * kept_opt: int32 [n_layers, n, max_blocks * page_tokens] or NULL; entry j < new length of
+ * list entry i gets the position that its token j had, entries behind it are not written.
+ * An id outside [0, max_seqs) and every repeat of an id set MOE_DEV_ERR_BAD_SEQ, a
+ * sequence with a missing page MOE_DEV_ERR_BAD_PAGE: those entries are skipped.
+ * Errors: the struct's; MOE_ERR_INVALID_ARG for n < 0 or above max_seqs, budget < 1,
+ * first or recent < 0, first + recent > budget, NULL seqs or weights (n > 0);
+ * MOE_ERR_UNSUPPORTED for max_blocks * page_tokens above 2^20, weights or kept_opt not 4-byte aligned;
+ * MOE_ERR_WORKSPACE / MOE_ERR_UNSUPPORTED for ws.  A workspace for n sequences serves shorter lists. */
+size_t moe_kv_evict_workspace_size(const moe_kv_cache* cache, int n);
+int moe_kv_evict(const moe_kv_cache* cache, const int32_t* seqs, int n, float* weights, int budget, int first,
+                 int recent, int32_t* kept_opt, void* ws, size_t ws_bytes, uint32_t* dev_status,
+                 moe_stream_t stream);
 
 /* ---------------------------------------------------------------- latent attention, absorbed form
  * Attention of the newest Q tokens of each of B sequences over the cache,
@@ -665,6 +719,22 @@ size_t moe_latent_decode_workspace_size(const moe_kv_cache* cache, int B, int Q,
 int moe_latent_decode(const moe_kv_cache* cache, int layer, const void* q, const int32_t* seqs, int B, int Q,
                       int heads, float scale, int shared_tokens, void* out, float* lse_opt, void* ws,
                       size_t ws_bytes, uint32_t* dev_status, moe_stream_t stream);
+
+/* What moe_latent_decode's queries looked at, per cached token: with its s[t] and lse,
+ *   weights[seqs[b], t] = decay * weights[seqs[b], t] + sum_{i, h} exp(s_{b*Q+i, h}[t] - lse[b*Q + i, h])
+ * for every t < len, a query adding only to tokens it sees.  q, scale and lse as in and from
+ * that call; weights fp32 [max_seqs, max_blocks * page_tokens], one layer's.  decay 1 adds
+ * up, between 0 and 1 old weight fades, 0 does not read what stood there.  Sums are
+ * fp32 in a fixed order: the same bits on every run of a shape.  Q * heads up to 1024 lets the last tokens of a
+ * prompt vote at once.  A NaN in a token's row makes its own weight NaN, and those that a NaN lse reaches.
+ * A sequence listed twice counts once, its later entries set MOE_DEV_ERR_BAD_SEQ, as ids
+ * out of range do; a missing page sets MOE_DEV_ERR_BAD_PAGE, weights of that sequence are then unspecified.
+ * Errors: as moe_latent_decode, with lse and weights (4-byte aligned) in place of out, and
+ * MOE_ERR_INVALID_ARG for a decay outside [0, 1]. */
+size_t moe_latent_weights_workspace_size(const moe_kv_cache* cache, int B, int Q, int heads);
+int moe_latent_weights(const moe_kv_cache* cache, int layer, const void* q, const int32_t* seqs, int B, int Q,
+                       int heads, float scale, const float* lse, float decay, float* weights, void* ws,
+                       size_t ws_bytes, uint32_t* dev_status, moe_stream_t stream);
 
 /* ---------------------------------------------------------------- latent attention, expanded form
  * Causal attention of prompt tokens, keys and values expanded per head from
