@@ -1,4 +1,27 @@
-// What the queries of an absorbed latent attention looked at, per cached token.
+// What the queries of an absorbed latent attention looked at: per cached token
+// the sum of its probabilities over all query rows, from the log-sum-exp that the
+// attention left.
+//
+// A tile is 128 tokens against up to 128 query rows (a row = one query token of one head):
+//   S = K Q^T     M = tokens (128), N = query rows, K = rank + rope
+//   w[t] += sum_r exp(S[t, r] - lse[r])
+// Tokens are M, so that a token's sum is one thread's: no exchange between
+// threads, no atomics, the rows always in the same order.
+//
+// Work: the sequences' tiles form one line that is cut evenly over the CTAs.  Up
+// to 64 query rows stay in shared memory while their sequence's tiles pass by;
+// more come in passes of up to 128, in 64-entry chunks that stream through a
+// ring once per tile.  Where there are fewer tiles than CTAs, a tile's passes are
+// shared out, and finish_kernel adds the shares in order.
+//
+// Bound: the rows of the cache, read once; with many query rows shared memory (a
+// pass of 128 reads 295 KB of operands, 2300 cycles; its products alone take 2304).
+//
+// Roles: warp 0 = copies of the cache, warp 1 = products (and TMEM owner), warp 2 =
+// copies of the queries, warps 4..7 = sums, and for a cache in 4 bits warps 8..15, which
+// expand its rows.  Every mbarrier wait is bounded; on expiry the CTA reports
+// MOE_DEV_ERR_TIMEOUT, drains and returns.
+#include <cfloat>
 #include <cmath>
 
 #include "kv_fp4.cuh"
@@ -7,70 +30,484 @@
 namespace moe {
 namespace {
 
-constexpr int kWThreads = 256;
+using namespace tc;
+
+constexpr int kTile = 128;                       // tokens
+constexpr int kChunkBytes = kTile * kBK * 2;     // 16 KB: 128 rows x 64 entries
+constexpr int kMaxChunks = 9;
+constexpr int kResident = 64;                    // query rows that stay in shared memory
+constexpr int kPassRows = 128;                   // query rows of a pass where they do not
+constexpr int kRing = 4;                         // chunks of such a pass in flight
+constexpr int kThreads = 256;                    // a bf16 cache's; one in 4 bits has kExpandWarps more
+constexpr int kExpandWarps = 8;
+constexpr int kSumThreads = 128;
+constexpr int kTmemCols = 256;                   // two passes of 128 columns
+constexpr int kBatch = 512;                      // sequences of one launch (lengths and tile sums in shared memory)
+constexpr float kLog2e = 1.4426950408889634f;
 
 struct WeightParams {
   KvView kv;
-  int layer, B, Q, heads, fp4;
+  int layer, B, Q, heads, first;      // first: the launch's first entry of the list
+  int chunks, latent_chunks;          // 64-entry chunks of a row, and those of its latent
+  int passes, rows_pass, ring;        // passes over the query rows, rows of each, chunks of queries in shared memory
+  int ctas;
   float scale_log2, decay;
-  const __nv_bfloat16* q;
-  const int32_t* seqs;
+  const int32_t* seqs;                // the whole list
   const float* lse;
   float* weights;
+  int32_t* plan;                      // [B + 1] tile sums, then the ids that count
+  float* part;                        // [ctas][128] sums of a tile's shares
   uint32_t* status;
 };
 
-// A warp a token: its row in shared memory, then one query row after the other.
-__global__ void __launch_bounds__(kWThreads) weights_kernel(const WeightParams p) {
-  extern __shared__ __nv_bfloat16 rows[];
+// A tile of one sequence, and which of the passes over its query rows.
+struct Tile {
+  int b, seq, t0, len, unit, p0, p1;
+  bool first, last;    // of its sequence in this CTA
+};
+
+// Shares of a tile's passes.
+__host__ __device__ inline int pass_shares(int tiles, int passes, int ctas) {
+  const int s = tiles > 0 ? ctas / tiles : 1;
+  return s < 1 ? 1 : s < passes ? s : passes;
+}
+
+struct Tiles {
+  const int *pref, *len, *ids;
+  int u, u1, b, shares, passes;
+
+  __device__ Tiles(const WeightParams& p, const int* pref_, const int* len_, const int* ids_) : pref(pref_), len(len_), ids(ids_) {
+    passes = p.passes;
+    shares = pass_shares(pref[p.B], passes, p.ctas);
+    const int units = pref[p.B] * shares, per = (units + p.ctas - 1) / p.ctas;
+    u = (int)min((long long)units, (long long)blockIdx.x * per);
+    u1 = min(units, u + per);
+    int lo = 0, hi = p.B;   // the last b with pref[b] <= the first tile
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (pref[mid] <= u / shares) lo = mid;
+      else hi = mid;
+    }
+    b = lo;
+    first = true;
+  }
+  __device__ bool next(Tile& t) {
+    if (u >= u1) return false;
+    const int tile = u / shares, share = u - tile * shares;
+    while (pref[b + 1] <= tile) {
+      ++b;
+      first = true;
+    }
+    t.b = b;
+    t.seq = ids[b];
+    t.t0 = (tile - pref[b]) * kTile;
+    t.len = len[b];
+    t.unit = u;
+    t.p0 = passes * share / shares;
+    t.p1 = passes * (share + 1) / shares;
+    t.first = first;
+    t.last = u + 1 >= u1 || pref[b + 1] <= (u + 1) / shares;
+    first = false;
+    ++u;
+    return true;
+  }
+
+ private:
+  bool first;
+};
+
+struct alignas(16) Shared {
+  uint64_t k_full[kMaxChunks], k_empty[kMaxChunks], q_full[kMaxChunks], q_empty[kMaxChunks], d_full[2], d_empty[2], drain;
+  uint32_t tmem;
+  int abort;
+  int warp_sum[kThreads / 32 + kExpandWarps];
+  int repeat;
+  union {
+    uint32_t listed[kMaxSeqs / 32];               // bit by bit: ids met so far
+    struct {
+      alignas(16) float lse[2][kPassRows];        // read four at a time: of a pass's rows, times log2(e)
+      int limit[2][kPassRows];                    // the tokens below it are seen by the row
+    };
+  };
+  int pref[kBatch + 1];
+  int len[kBatch];
+  int ids[kBatch];
+};
+
+// All threads of the sums' warps (named barrier 1).
+__device__ inline void sums_meet() {
+  __syncwarp();
+  asm volatile("bar.sync 1, %0;" ::"n"(kSumThreads) : "memory");
+}
+
+// 32 columns' probabilities of one token.  `edge`: rows that do not see it, or columns past the pass's rows.
+__device__ inline float sum32(const uint32_t (&s)[32], const float* lse, const int* limit, int t, int rows, float scale, bool edge) {
+  float2 a = make_float2(0.0f, 0.0f);
+#pragma unroll
+  for (int x = 0; x < 32; x += 4) {
+    const float4 l = *reinterpret_cast<const float4*>(lse + x);
+    float e[4] = {ex2(fmaf(__uint_as_float(s[x]), scale, -l.x)), ex2(fmaf(__uint_as_float(s[x + 1]), scale, -l.y)),
+                  ex2(fmaf(__uint_as_float(s[x + 2]), scale, -l.z)), ex2(fmaf(__uint_as_float(s[x + 3]), scale, -l.w))};
+    if (edge) {
+#pragma unroll
+      for (int y = 0; y < 4; ++y)
+        if (x + y >= rows || t >= limit[x + y]) e[y] = 0.0f;
+    }
+    a = add2(a, add2(make_float2(e[0], e[1]), make_float2(e[2], e[3])));
+  }
+  return a.x + a.y;
+}
+
+template <bool FP4>
+__global__ void __launch_bounds__(kThreads + (FP4 ? 32 * kExpandWarps : 0), 1)
+weights_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_q, const WeightParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ Shared sh;
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  constexpr int kAll = kThreads + (FP4 ? 32 * kExpandWarps : 0);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid == 0) {
+    for (int c = 0; c < kMaxChunks; ++c) {
+      mbar_init(&sh.k_full[c], FP4 && c < p.latent_chunks ? kExpandWarps : 1);
+      mbar_init(&sh.k_empty[c], 1);
+      mbar_init(&sh.q_full[c], 1);
+      mbar_init(&sh.q_empty[c], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sh.d_full[i], 1);
+      mbar_init(&sh.d_empty[i], kSumThreads / 32);
+    }
+    mbar_init(&sh.drain, 1);
+    sh.abort = 0;
+    sh.repeat = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (tid == 96) {
+    prefetch_map(&map_k);
+    prefetch_map(&map_q);
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&sh.tmem)),
+                 "r"(kTmemCols));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  for (int i = tid; i < kMaxSeqs / 32; i += kAll) sh.listed[i] = 0;
+  __syncthreads();
   pdl_wait();
   pdl_trigger();
-  const int b = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, seq = p.seqs[b];
-  bool good = seq >= 0 && seq < p.kv.max_seqs;
-  for (int j = 0; good && j < b; ++j) good = p.seqs[j] != seq;
-  if (!good) {
-    if (threadIdx.x == 0 && blockIdx.x == 0) set_status(p.status, MOE_DEV_ERR_BAD_SEQ);
-    return;
+  // Ids, and whether any of them was listed before (in this launch's part of the list or an earlier one's).
+  for (int i = tid; i < p.first + p.B; i += kAll) {
+    const int s = p.seqs[i];
+    if (i >= p.first) sh.ids[i - p.first] = s;
+    if (s >= 0 && s < p.kv.max_seqs && (atomicOr(&sh.listed[s >> 5], 1u << (s & 31)) >> (s & 31) & 1u)) sh.repeat = 1;
   }
-  const int len = p.kv.len_of(seq), dim = p.kv.rank + p.kv.rope;
-  __nv_bfloat16* row = rows + warp * dim;
-  const size_t cap = (size_t)p.kv.max_blocks << p.kv.page_shift;
-  for (int t = blockIdx.x * (kWThreads / 32) + warp; t < len; t += gridDim.x * (kWThreads / 32)) {
-    int pg = p.kv.table[(size_t)seq * p.kv.max_blocks + (t >> p.kv.page_shift)];
-    if (pg < 0 || pg >= p.kv.n_pages) {
-      set_status(p.status, MOE_DEV_ERR_BAD_PAGE);
-      pg = 0;
+  __syncthreads();
+  const bool repeat = sh.repeat != 0;
+  {
+    int carry = 0;
+    for (int b0 = 0; b0 < p.B; b0 += kAll) {
+      const int b = b0 + tid;
+      int n = 0;
+      if (b < p.B) {
+        const int s = sh.ids[b];
+        bool good = s >= 0 && s < p.kv.max_seqs;
+        if (good && repeat)      // rare: look for the entry's first place
+          for (int j = 0; good && j < p.first + b; ++j) good = p.seqs[j] != s;
+        if (!good && blockIdx.x == 0) set_status(p.status, MOE_DEV_ERR_BAD_SEQ);
+        const int len = good ? p.kv.len_of(s) : 0;
+        sh.len[b] = len;
+        n = (len + kTile - 1) / kTile;
+      }
+      int inc = n;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += u;
+      }
+      if (lane == 31) sh.warp_sum[warp] = inc;
+      __syncthreads();
+      int base = carry;
+      for (int w = 0; w < warp; ++w) base += sh.warp_sum[w];
+      for (int w = 0; w < kAll / 32; ++w) carry += sh.warp_sum[w];
+      if (b < p.B) sh.pref[b + 1] = base + inc;
+      __syncthreads();
     }
-    const __nv_bfloat16* src = p.kv.pages + p.kv.row_offset(p.layer, pg, t & (p.kv.page_tokens - 1));
+    if (tid == 0) sh.pref[0] = 0;
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (blockIdx.x == 0)
+    for (int b = tid; b <= p.B; b += kAll) p.plan[b] = sh.pref[b];
+  const uint32_t tmem = sh.tmem;
+  volatile int* abort_flag = &sh.abort;
+  const int rows_all = p.Q * p.heads, q_chunk = p.rows_pass * 128;
+  uint8_t* sq = smem + p.chunks * kChunkBytes;
+  Tiles it(p, sh.pref, sh.len, sh.ids);
+  Tile tl;
+
+  if (warp == 0) {
+    // ------------------------------------------------ copies of the cache (in 4 bits: of the rotary keys)
+    const int page = p.kv.page_tokens, layer_page = p.layer * p.kv.n_pages;
+    const uint32_t smem0 = uni(smem_u32(smem)), bar0 = uni(smem_u32(&sh.k_full[0]));
+    const uint64_t once = l2_evict_first();
+    const int c_first = FP4 ? p.latent_chunks : 0;
+    int tile = 0;
+    bool ok = true;
+    while (__any_sync(0xffffffffu, ok && it.next(tl))) {
+      const int nb = (int)uni((min(kTile, tl.len - tl.t0) + page - 1) / page);
+      int row = 0;
+      if (lane < nb) {
+        int pg = p.kv.table[(size_t)tl.seq * p.kv.max_blocks + ((tl.t0 + lane * page) >> p.kv.page_shift)];
+        if (pg < 0 || pg >= p.kv.n_pages) {
+          set_status(p.status, MOE_DEV_ERR_BAD_PAGE);
+          pg = 0;
+        }
+        row = (layer_page + pg) * page;
+      }
+      int rows[kTile / 16];
+#pragma unroll
+      for (int i = 0; i < kTile / 16; ++i) rows[i] = (int)uni(lane == i ? row : 0);
+      for (int c = c_first; c < p.chunks; ++c) {
+        ok = warp_wait(&sh.k_empty[c], (tile & 1) ^ 1u, abort_flag);
+        if (!ok) break;
+        mbar_expect_tx_warp(bar0 + 8 * c, (uint32_t)(nb * page * 128));
+        const int at = c < p.latent_chunks ? c * kBK : p.kv.rope_at;
+#pragma unroll
+        for (int i = 0; i < kTile / 16; ++i)
+          if (i < nb) tma_load_2d_hint_warp(smem0 + c * kChunkBytes + i * page * 128, &map_k, bar0 + 8 * c, at, rows[i], once);
+      }
+      ++tile;
+    }
+    // drain: whatever was asked for lands before the CTA can exit
+    volatile int no_abort = 0;
+    if (tile)
+      for (int c = c_first; c < p.chunks; ++c) mbar_wait(&sh.k_full[c], (tile - 1) & 1, &no_abort);
     __syncwarp();
-    for (int d = lane; d < dim; d += 32) {
-      if (d >= p.kv.rank) row[d] = src[p.kv.rope_at + d - p.kv.rank];
-      else if (!p.fp4) row[d] = src[d];
-      else {
-        const uint8_t* bytes = reinterpret_cast<const uint8_t*>(src);
-        const uint32_t c = bytes[d / 2] >> (d & 1 ? 4 : 0) & 15;
-        const uint4 v = fp4_expand8(c, fp4_factor(bytes[p.kv.rank / 2 + 2 * p.kv.rope + d / kFpBlock]));
-        row[d] = __ushort_as_bfloat16((unsigned short)(v.x & 0xFFFFu));
+  } else if (warp == 2) {
+    // ------------------------------------------------ copies of the queries
+    const uint32_t q0 = uni(smem_u32(sq)), bar0 = uni(smem_u32(&sh.q_full[0]));
+    const uint64_t keep = l2_normal();
+    int slot = 0, loads = 0;
+    uint32_t par = 1;
+    bool ok = true;
+    while (__any_sync(0xffffffffu, ok && it.next(tl))) {
+      if (p.passes == 1 && !tl.first) continue;            // they are there
+      for (int g = (int)uni(tl.p0); ok && g < tl.p1; ++g) {
+        const int row0 = (int)uni(tl.b * rows_all + g * p.rows_pass);
+        for (int c = 0; c < p.chunks; ++c) {
+          ok = warp_wait(&sh.q_empty[slot], par, abort_flag);
+          if (!ok) break;
+          mbar_expect_tx_warp(bar0 + 8 * slot, (uint32_t)q_chunk);
+          tma_load_2d_hint_warp(q0 + slot * q_chunk, &map_q, bar0 + 8 * slot, c < p.latent_chunks ? c * kBK : p.kv.rank, row0, keep);
+          ++loads;
+          if (++slot == p.ring) {
+            slot = 0;
+            par ^= 1u;
+          }
+        }
+      }
+    }
+    volatile int no_abort = 0;
+    for (int s = 0; s < p.ring; ++s) {
+      const int n = loads / p.ring + (loads % p.ring > s ? 1 : 0);
+      if (n > 0) mbar_wait(&sh.q_full[s], (n - 1) & 1, &no_abort);
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ------------------------------------------------ products
+    const uint32_t tm = uni(tmem), smem0 = uni(smem_u32(smem));
+    const uint64_t dk0 = smem_desc(smem0), dq0 = smem_desc(smem0 + p.chunks * kChunkBytes);
+    int tile = 0, pass = 0, slot = 0;
+    uint32_t par = 0;
+    bool ok = true, issued = false;
+    while (__any_sync(0xffffffffu, ok && it.next(tl))) {
+      const int p0 = (int)uni(tl.p0), p1 = (int)uni(tl.p1);
+      const bool keep = p.passes == 1 && !uni(tl.last);     // the next tile takes the same queries
+      for (int g = p0; ok && g < p1; ++g, ++pass) {
+        const int buf = pass & 1;
+        ok = warp_wait(&sh.d_empty[buf], ((pass >> 1) & 1) ^ 1u, abort_flag);
+        if (!ok) break;
+        const uint32_t idesc = make_idesc(kTile, (min(p.rows_pass, rows_all - g * p.rows_pass) + 15) & ~15);
+        for (int c = 0; c < p.chunks; ++c) {
+          ok = warp_wait(&sh.q_full[slot], par, abort_flag) && warp_wait(&sh.k_full[c], tile & 1, abort_flag);
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t dk = dk0 + ((uint64_t)(c * kChunkBytes) >> 4), dq = dq0 + ((uint64_t)(slot * q_chunk) >> 4);
+          const int depth = c < p.latent_chunks ? kBK : p.kv.rope;
+#pragma unroll
+          for (int k = 0; k < kBK / kUK; ++k)
+            if (k * kUK < depth)
+              tc_mma_warp(tm + buf * kPassRows, dk + ((k * kUK * 2) >> 4), dq + ((k * kUK * 2) >> 4), idesc, k ? 1u : (c ? 1u : 0u));
+          issued = true;
+          if (g == p1 - 1) tc_commit_warp(&sh.k_empty[c]);
+          if (!keep) tc_commit_warp(&sh.q_empty[slot]);
+          if (++slot == p.ring) {
+            slot = 0;
+            if (!keep) par ^= 1u;
+          }
+        }
+        if (ok) tc_commit_warp(&sh.d_full[buf]);
+      }
+      ++tile;
+    }
+    if (issued) {   // every issued product completes before tensor memory is released
+      volatile int no_abort = 0;
+      tc_commit_warp(&sh.drain);
+      mbar_wait(&sh.drain, 0, &no_abort);
+    }
+    __syncwarp();
+  } else if (FP4 && warp >= kThreads / 32) {
+    // ------------------------------------------------ latents in 4 bits, expanded into the tile that a copy would fill
+    // Four threads a token, two tokens a thread; of each 128-entry pair a thread has 16 bytes of codes, a quarter.  What
+    // the next tile needs is asked for as soon as its registers are free.
+    const int et = tid - kThreads, r = et >> 2, v = et & 3, scales_at = p.kv.rank / 2 + 2 * p.kv.rope;
+    const int pairs = p.latent_chunks / 2;
+    const uint8_t* row[2] = {nullptr, nullptr};
+    uint4 code[2][4];
+    uint32_t scale[2][4];
+    auto find = [&](bool any) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int t = tl.t0 + r + 64 * e;
+        row[e] = nullptr;
+        if (any && t < tl.len) {
+          int pg = p.kv.table[(size_t)tl.seq * p.kv.max_blocks + (t >> p.kv.page_shift)];
+          if (pg < 0 || pg >= p.kv.n_pages) {
+            set_status(p.status, MOE_DEV_ERR_BAD_PAGE);
+            pg = 0;
+          }
+          row[e] = reinterpret_cast<const uint8_t*>(p.kv.pages + p.kv.row_offset(p.layer, pg, t & (p.kv.page_tokens - 1)));
+        }
+      }
+    };
+    auto load = [&](int j) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        if (row[e]) {
+          code[e][j] = ldg_stream(row[e] + 64 * j + 16 * v);
+          scale[e][j] = *reinterpret_cast<const unsigned short*>(row[e] + scales_at + 8 * j + 2 * v);
+        }
+    };
+    bool more = it.next(tl), ok = true;
+    find(more);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (j < pairs) load(j);
+    for (int tile = 0; ok && more; ++tile) {
+      const bool here[2] = {row[0] != nullptr, row[1] != nullptr};
+      more = it.next(tl);
+      find(more);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (j >= pairs) break;
+        ok = ok && warp_wait(&sh.k_empty[2 * j], (tile & 1) ^ 1u, abort_flag) &&
+             warp_wait(&sh.k_empty[2 * j + 1], (tile & 1) ^ 1u, abort_flag);
+        if (!ok) break;
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          if (here[e]) fp4_store32(smem + 2 * j * kChunkBytes, kChunkBytes, r + 64 * e, v, code[e][j], scale[e][j]);
+        load(j);
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&sh.k_full[2 * j]);
+          mbar_arrive(&sh.k_full[2 * j + 1]);
+        }
       }
     }
     __syncwarp();
+  } else if (warp >= 4) {
+    // ------------------------------------------------ sums: a thread a token
+    const int quarter = warp & 3, st = tid - kSumThreads;
+    const uint32_t lane_base = tmem + ((uint32_t)(quarter * 32) << 16);
+    const size_t cap = (size_t)p.kv.max_blocks << p.kv.page_shift;
+    const float scale = p.scale_log2;
+    int pass = 0, stage = 0;
+    bool ok = true;
+    while (ok && it.next(tl)) {
+      const int t = tl.t0 + st;
+      float* w = p.weights + (size_t)tl.seq * cap + t;
+      const bool mine = t < tl.len;
+      const float old = mine && it.shares == 1 && p.decay != 0.0f ? *w : 0.0f;
+      float sum = 0.0f;
+      for (int g = tl.p0; g < tl.p1; ++g, ++pass) {
+        const int rows = min(p.rows_pass, rows_all - g * p.rows_pass);
+        if (p.passes > 1 || tl.first) {
+          stage ^= 1;
+          if (st < rows) {
+            const int r = g * p.rows_pass + st;
+            sh.lse[stage][st] = p.lse[(size_t)(p.first + tl.b) * rows_all + r] * kLog2e;
+            sh.limit[stage][st] = tl.len - p.Q + r / p.heads + 1;
+          }
+          sums_meet();      // whoever writes this stage's place next has met everyone who read it
+        }
+        const int buf = pass & 1;
+        ok = warp_wait(&sh.d_full[buf], (pass >> 1) & 1, abort_flag);
+        if (!ok) break;
+        tc_fence_after();
+        const int limit0 = tl.len - p.Q + g * p.rows_pass / p.heads + 1;       // the pass's first row sees the least
+        const bool seen = tl.t0 + kTile <= limit0;
+        for (int c = 0; c < rows; c += 32) {
+          uint32_t s[32];
+          tmem_ld32(lane_base + buf * kPassRows + c, s);
+          tmem_ld_wait();
+          const float* l = sh.lse[stage] + c;
+          const int* limit = sh.limit[stage] + c;
+          sum += seen && c + 32 <= rows ? sum32(s, l, limit, t, rows - c, scale, false) : sum32(s, l, limit, t, rows - c, scale, true);
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.d_empty[buf]);
+      }
+      if (!ok) break;
+      if (it.shares > 1) p.part[(size_t)tl.unit * kTile + st] = sum;
+      else if (mine) *w = p.decay == 0.0f ? sum : fmaf(p.decay, old, sum);
+    }
+  }
+  __syncthreads();
+  if (*abort_flag && tid == 0) set_status(p.status, MOE_DEV_ERR_TIMEOUT);
+  tc_fence_after();
+  if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols));
+}
+
+// Shares of tiles, added in order (calls of more than one pass; returns at once where none were shared out).
+__global__ void __launch_bounds__(kTile) finish_weights_kernel(const WeightParams p) {
+  pdl_wait();
+  pdl_trigger();
+  const int tiles = p.plan[p.B], shares = pass_shares(tiles, p.passes, p.ctas);
+  if (shares == 1) return;
+  for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+    int lo = 0, hi = p.B;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (p.plan[mid] <= tile) lo = mid;
+      else hi = mid;
+    }
+    const int seq = p.seqs[p.first + lo], t = (tile - p.plan[lo]) * kTile + threadIdx.x;
+    if (t >= p.kv.len_of(seq)) continue;
     float sum = 0.0f;
-    for (int r = 0; r < p.Q * p.heads; ++r) {
-      if (t >= len - p.Q + r / p.heads + 1) continue;
-      const size_t at = (size_t)b * p.Q * p.heads + r;
-      float s = 0.0f;
-      for (int d = lane; d < dim; d += 32) s = fmaf(__bfloat162float(p.q[at * dim + d]), __bfloat162float(row[d]), s);
-      s = warp_sum(s);
-      sum += tc::ex2(fmaf(s, p.scale_log2, -p.lse[at] * 1.4426950408889634f));
-    }
-    if (lane == 0) {
-      float* w = p.weights + (size_t)seq * cap + t;
-      *w = p.decay == 0.0f ? sum : fmaf(p.decay, *w, sum);
-    }
+    for (int s = 0; s < shares; ++s) sum += p.part[((size_t)tile * shares + s) * kTile + threadIdx.x];
+    float* w = p.weights + (size_t)seq * ((size_t)p.kv.max_blocks << p.kv.page_shift) + t;
+    *w = p.decay == 0.0f ? sum : fmaf(p.decay, *w, sum);
   }
 }
 
+// ---------------------------------------------------------------- host side
 bool weights_shape_ok(int B, int Q, int heads) { return B <= 4096 && (long long)Q * heads <= 1024; }
+
+size_t plan_bytes(int B) { return align_up((size_t)((B < kBatch ? B : kBatch) + 1) * sizeof(int32_t), 256); }
+
+template <bool FP4>
+cudaError_t launch_weights(const CUtensorMap& mk, const CUtensorMap& mq, const WeightParams& p, int smem, cudaStream_t s) {
+  static std::atomic<unsigned char> attr[kMaxDevices];
+  const cudaError_t e = once_per_device(attr, [] {
+    return cudaFuncSetAttribute(weights_kernel<FP4>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                227 * 1024 - (int)sizeof(Shared));
+  });
+  constexpr int threads = kThreads + (FP4 ? 32 * kExpandWarps : 0);
+  return e == cudaSuccess ? launch_k(weights_kernel<FP4>, p.ctas, threads, smem, s, mk, mq, p) : e;
+}
 
 }  // namespace
 }  // namespace moe
@@ -81,12 +518,14 @@ extern "C" {
 
 size_t moe_latent_weights_workspace_size(const moe_kv_cache* cache, int B, int Q, int heads) {
   if (check_latent(cache, 0) != MOE_OK || B < 1 || Q < 1 || heads < 1 || !weights_shape_ok(B, Q, heads)) return 0;
-  return 256;
+  return plan_bytes(B) + (Q * heads > kResident ? align_up((size_t)num_sms() * kTile * sizeof(float), 256) : 0);
 }
 
 int moe_latent_weights(const moe_kv_cache* cache, int layer, const void* q, const int32_t* seqs, int B, int Q, int heads,
                        float scale, const float* lse, float decay, float* weights, void* ws, size_t ws_bytes,
                        uint32_t* dev_status, moe_stream_t stream) {
+  static_assert(sizeof(Shared) + 1024 + kMaxChunks * (kChunkBytes + kResident * kBK * 2) <= 227 * 1024 &&
+                    kRing * kPassRows * kBK * 2 <= kMaxChunks * kResident * kBK * 2, "shared memory");
   int st = check_latent(cache, layer);
   if (st == MOE_ERR_INVALID_ARG || check_kv(cache) != MOE_OK) return st;
   if (B < 0 || Q < 1 || heads < 1 || !std::isfinite(scale) || !(decay >= 0.0f && decay <= 1.0f)) return MOE_ERR_INVALID_ARG;
@@ -97,24 +536,46 @@ int moe_latent_weights(const moe_kv_cache* cache, int layer, const void* q, cons
   if (!kv_aligned(q, 16) || !kv_aligned(lse, 4) || !kv_aligned(weights, 4)) return MOE_ERR_UNSUPPORTED;
   st = check_ws(ws, ws_bytes, moe_latent_weights_workspace_size(cache, B, Q, heads));
   if (st != MOE_OK) return st;
+  const bool fp4 = cache->format == MOE_KV_FP4;
+  const int rows = Q * heads, row = cache->rank + cache->rope;
   WeightParams p;
   p.kv = kv_view(*cache);
   p.layer = layer;
-  p.B = B;
   p.Q = Q;
   p.heads = heads;
-  p.fp4 = cache->format == MOE_KV_FP4;
-  p.scale_log2 = scale * 1.4426950408889634f;
+  p.latent_chunks = cache->rank / kBK;
+  p.chunks = p.latent_chunks + (cache->rope ? 1 : 0);
+  const int most = rows <= kResident ? kResident : kPassRows;
+  p.passes = (rows + most - 1) / most;
+  p.rows_pass = ((rows + p.passes - 1) / p.passes + 15) & ~15;       // evenly, in multiples of 16
+  p.passes = (rows + p.rows_pass - 1) / p.rows_pass;
+  p.ring = rows <= kResident ? p.chunks : kRing;
+  p.ctas = num_sms();
+  // zero as the smallest normal number, as in the attention whose log-sum-exp this is
+  p.scale_log2 = scale == 0.0f ? FLT_MIN : scale * kLog2e;
   p.decay = decay;
-  p.q = reinterpret_cast<const __nv_bfloat16*>(q);
   p.seqs = seqs;
   p.lse = lse;
   p.weights = weights;
+  p.plan = reinterpret_cast<int32_t*>(ws);
+  p.part = reinterpret_cast<float*>(reinterpret_cast<char*>(ws) + plan_bytes(B));
   p.status = dev_status;
-  const size_t smem = (size_t)(kWThreads / 32) * (cache->rank + cache->rope) * 2;
-  const int per = 8 * num_sms() / B + 1;
-  return launch_k(weights_kernel, dim3(per, B), kWThreads, smem, reinterpret_cast<cudaStream_t>(stream), p) == cudaSuccess
-             ? MOE_OK : MOE_ERR_CUDA;
+  const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const int smem = p.chunks * kChunkBytes + p.ring * p.rows_pass * kBK * 2 + 1024;
+  CUtensorMap mk;
+  if (!make_map(&mk, cache->pages, p.kv.row, (uint64_t)cache->n_layers * cache->n_pages * cache->page_tokens, cache->page_tokens))
+    return MOE_ERR_CUDA;
+  for (int b0 = 0; b0 < B; b0 += kBatch) {   // lists of more than 512 sequences: several launches
+    p.first = b0;
+    p.B = B - b0 < kBatch ? B - b0 : kBatch;
+    CUtensorMap mq;
+    if (!make_map(&mq, reinterpret_cast<const __nv_bfloat16*>(q) + (size_t)b0 * rows * row, row, (uint64_t)p.B * rows, p.rows_pass))
+      return MOE_ERR_CUDA;
+    cudaError_t e = fp4 ? launch_weights<true>(mk, mq, p, smem, s) : launch_weights<false>(mk, mq, p, smem, s);
+    if (e == cudaSuccess && p.passes > 1) e = launch_k(finish_weights_kernel, p.ctas, kTile, 0, s, p);
+    if (e != cudaSuccess) return MOE_ERR_CUDA;
+  }
+  return MOE_OK;
 }
 
 }  // extern "C"
