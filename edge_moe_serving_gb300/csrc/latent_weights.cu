@@ -8,11 +8,13 @@
 // Tokens are M, so that a token's sum is one thread's: no exchange between
 // threads, no atomics, the rows always in the same order.
 //
-// Work: the sequences' tiles form one line that is cut evenly over the CTAs.  Up
-// to 64 query rows stay in shared memory while their sequence's tiles pass by;
-// more come in passes of up to 128, in 64-entry chunks that stream through a
-// ring once per tile.  Where there are fewer tiles than CTAs, a tile's passes are
-// shared out, and finish_kernel adds the shares in order.
+// Work: the sequences' tokens form one line, in units of 32, that is cut evenly
+// over the CTAs; a tile is up to four units of one sequence.  Up to 64 query rows
+// stay in shared memory while their sequence's tiles pass by; more come in passes of
+// up to 128, in 64-entry chunks that stream through a ring once per tile, each CTA
+// beginning with another pass (all at once on the same rows, they wait for the few
+// L2 slices that hold them).  Where there are fewer units than CTAs, a unit's passes
+// are shared out, and finish_weights_kernel adds the shares in order.
 //
 // Bound: the rows of the cache, read once; with many query rows shared memory (a
 // pass of 128 reads 295 KB of operands, 2300 cycles; its products alone take 2304).
@@ -33,6 +35,7 @@ namespace {
 using namespace tc;
 
 constexpr int kTile = 128;                       // tokens
+constexpr int kUnit = 32;                        // tokens that the line is cut by
 constexpr int kChunkBytes = kTile * kBK * 2;     // 16 KB: 128 rows x 64 entries
 constexpr int kMaxChunks = 9;
 constexpr int kResident = 64;                    // query rows that stay in shared memory
@@ -55,37 +58,39 @@ struct WeightParams {
   const int32_t* seqs;                // the whole list
   const float* lse;
   float* weights;
-  int32_t* plan;                      // [B + 1] tile sums, then the ids that count
-  float* part;                        // [ctas][128] sums of a tile's shares
+  int32_t* plan;                      // [B + 1] units before each sequence
+  float* part;                        // [ctas][32] sums of a unit's shares
   uint32_t* status;
 };
 
 // A tile of one sequence, and which of the passes over its query rows.
 struct Tile {
-  int b, seq, t0, len, unit, p0, p1;
+  int b, seq, t0, t1, len, work, p0, p1;
   bool first, last;    // of its sequence in this CTA
 };
 
-// Shares of a tile's passes.
-__host__ __device__ inline int pass_shares(int tiles, int passes, int ctas) {
-  const int s = tiles > 0 ? ctas / tiles : 1;
+// Shares of a unit's passes.
+__host__ __device__ inline int pass_shares(int units, int passes, int ctas) {
+  const int s = units > 0 ? ctas / units : 1;
   return s < 1 ? 1 : s < passes ? s : passes;
 }
 
 struct Tiles {
   const int *pref, *len, *ids;
-  int u, u1, b, shares, passes;
+  int u, u1, b, shares, share, passes;
 
   __device__ Tiles(const WeightParams& p, const int* pref_, const int* len_, const int* ids_) : pref(pref_), len(len_), ids(ids_) {
+    const int units = pref[p.B];
     passes = p.passes;
-    shares = pass_shares(pref[p.B], passes, p.ctas);
-    const int units = pref[p.B] * shares, per = (units + p.ctas - 1) / p.ctas;
-    u = (int)min((long long)units, (long long)blockIdx.x * per);
+    shares = pass_shares(units, passes, p.ctas);
+    const int per = (units + p.ctas - 1) / p.ctas;      // 1 where units are shared out
+    u = (int)min((long long)units, (long long)(blockIdx.x / shares) * per);
     u1 = min(units, u + per);
-    int lo = 0, hi = p.B;   // the last b with pref[b] <= the first tile
+    share = blockIdx.x % shares;
+    int lo = 0, hi = p.B;   // the last b with pref[b] <= the first unit
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
-      if (pref[mid] <= u / shares) lo = mid;
+      if (pref[mid] <= u) lo = mid;
       else hi = mid;
     }
     b = lo;
@@ -93,24 +98,27 @@ struct Tiles {
   }
   __device__ bool next(Tile& t) {
     if (u >= u1) return false;
-    const int tile = u / shares, share = u - tile * shares;
-    while (pref[b + 1] <= tile) {
+    while (pref[b + 1] <= u) {
       ++b;
       first = true;
     }
+    const int end = min(pref[b + 1], u1), n = min(kTile / kUnit, end - u);
     t.b = b;
     t.seq = ids[b];
-    t.t0 = (tile - pref[b]) * kTile;
     t.len = len[b];
-    t.unit = u;
+    t.t0 = (u - pref[b]) * kUnit;
+    t.t1 = min(t.len, t.t0 + n * kUnit);
+    t.work = u * shares + share;
     t.p0 = passes * share / shares;
     t.p1 = passes * (share + 1) / shares;
     t.first = first;
-    t.last = u + 1 >= u1 || pref[b + 1] <= (u + 1) / shares;
+    t.last = u + n >= end;
     first = false;
-    ++u;
+    u += n;
     return true;
   }
+  // the k-th pass of a tile
+  __device__ static int pass(const Tile& t, int k) { return t.p0 + (k + (int)blockIdx.x) % (t.p1 - t.p0); }
 
  private:
   bool first;
@@ -126,7 +134,7 @@ struct alignas(16) Shared {
     uint32_t listed[kMaxSeqs / 32];               // bit by bit: ids met so far
     struct {
       alignas(16) float lse[2][kPassRows];        // read four at a time: of a pass's rows, times log2(e)
-      int limit[2][kPassRows];                    // the tokens below it are seen by the row
+      alignas(16) int limit[2][kPassRows];        // the tokens below it are seen by the row
     };
   };
   int pref[kBatch + 1];
@@ -149,9 +157,11 @@ __device__ inline float sum32(const uint32_t (&s)[32], const float* lse, const i
     float e[4] = {ex2(fmaf(__uint_as_float(s[x]), scale, -l.x)), ex2(fmaf(__uint_as_float(s[x + 1]), scale, -l.y)),
                   ex2(fmaf(__uint_as_float(s[x + 2]), scale, -l.z)), ex2(fmaf(__uint_as_float(s[x + 3]), scale, -l.w))};
     if (edge) {
-#pragma unroll
-      for (int y = 0; y < 4; ++y)
-        if (x + y >= rows || t >= limit[x + y]) e[y] = 0.0f;
+      const int4 m = *reinterpret_cast<const int4*>(limit + x);
+      e[0] = (t < m.x) & (x < rows) ? e[0] : 0.0f;
+      e[1] = (t < m.y) & (x + 1 < rows) ? e[1] : 0.0f;
+      e[2] = (t < m.z) & (x + 2 < rows) ? e[2] : 0.0f;
+      e[3] = (t < m.w) & (x + 3 < rows) ? e[3] : 0.0f;
     }
     a = add2(a, add2(make_float2(e[0], e[1]), make_float2(e[2], e[3])));
   }
@@ -216,7 +226,7 @@ weights_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
         if (!good && blockIdx.x == 0) set_status(p.status, MOE_DEV_ERR_BAD_SEQ);
         const int len = good ? p.kv.len_of(s) : 0;
         sh.len[b] = len;
-        n = (len + kTile - 1) / kTile;
+        n = (len + kUnit - 1) / kUnit;
       }
       int inc = n;
 #pragma unroll
@@ -248,22 +258,23 @@ weights_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
 
   if (warp == 0) {
     // ------------------------------------------------ copies of the cache (in 4 bits: of the rotary keys)
-    const int page = p.kv.page_tokens, layer_page = p.layer * p.kv.n_pages;
+    const int page = p.kv.page_tokens, box = min(page, kUnit), layer_page = p.layer * p.kv.n_pages;
     const uint32_t smem0 = uni(smem_u32(smem)), bar0 = uni(smem_u32(&sh.k_full[0]));
     const uint64_t once = l2_evict_first();
     const int c_first = FP4 ? p.latent_chunks : 0;
     int tile = 0;
     bool ok = true;
     while (__any_sync(0xffffffffu, ok && it.next(tl))) {
-      const int nb = (int)uni((min(kTile, tl.len - tl.t0) + page - 1) / page);
+      const int nb = (int)uni((tl.t1 - tl.t0 + box - 1) / box);
       int row = 0;
       if (lane < nb) {
-        int pg = p.kv.table[(size_t)tl.seq * p.kv.max_blocks + ((tl.t0 + lane * page) >> p.kv.page_shift)];
+        const int t = tl.t0 + lane * box;
+        int pg = p.kv.table[(size_t)tl.seq * p.kv.max_blocks + (t >> p.kv.page_shift)];
         if (pg < 0 || pg >= p.kv.n_pages) {
           set_status(p.status, MOE_DEV_ERR_BAD_PAGE);
           pg = 0;
         }
-        row = (layer_page + pg) * page;
+        row = (layer_page + pg) * page + (t & (page - 1));
       }
       int rows[kTile / 16];
 #pragma unroll
@@ -271,11 +282,11 @@ weights_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
       for (int c = c_first; c < p.chunks; ++c) {
         ok = warp_wait(&sh.k_empty[c], (tile & 1) ^ 1u, abort_flag);
         if (!ok) break;
-        mbar_expect_tx_warp(bar0 + 8 * c, (uint32_t)(nb * page * 128));
+        mbar_expect_tx_warp(bar0 + 8 * c, (uint32_t)(nb * box * 128));
         const int at = c < p.latent_chunks ? c * kBK : p.kv.rope_at;
 #pragma unroll
         for (int i = 0; i < kTile / 16; ++i)
-          if (i < nb) tma_load_2d_hint_warp(smem0 + c * kChunkBytes + i * page * 128, &map_k, bar0 + 8 * c, at, rows[i], once);
+          if (i < nb) tma_load_2d_hint_warp(smem0 + c * kChunkBytes + i * box * 128, &map_k, bar0 + 8 * c, at, rows[i], once);
       }
       ++tile;
     }
@@ -293,8 +304,9 @@ weights_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
     bool ok = true;
     while (__any_sync(0xffffffffu, ok && it.next(tl))) {
       if (p.passes == 1 && !tl.first) continue;            // they are there
-      for (int g = (int)uni(tl.p0); ok && g < tl.p1; ++g) {
-        const int row0 = (int)uni(tl.b * rows_all + g * p.rows_pass);
+      const int n = (int)uni(tl.p1 - tl.p0);
+      for (int k = 0; ok && k < n; ++k) {
+        const int row0 = (int)uni(tl.b * rows_all + Tiles::pass(tl, k) * p.rows_pass);
         for (int c = 0; c < p.chunks; ++c) {
           ok = warp_wait(&sh.q_empty[slot], par, abort_flag);
           if (!ok) break;
@@ -322,10 +334,10 @@ weights_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
     uint32_t par = 0;
     bool ok = true, issued = false;
     while (__any_sync(0xffffffffu, ok && it.next(tl))) {
-      const int p0 = (int)uni(tl.p0), p1 = (int)uni(tl.p1);
+      const int n = (int)uni(tl.p1 - tl.p0);
       const bool keep = p.passes == 1 && !uni(tl.last);     // the next tile takes the same queries
-      for (int g = p0; ok && g < p1; ++g, ++pass) {
-        const int buf = pass & 1;
+      for (int k = 0; ok && k < n; ++k, ++pass) {
+        const int buf = pass & 1, g = (int)uni(Tiles::pass(tl, k));
         ok = warp_wait(&sh.d_empty[buf], ((pass >> 1) & 1) ^ 1u, abort_flag);
         if (!ok) break;
         const uint32_t idesc = make_idesc(kTile, (min(p.rows_pass, rows_all - g * p.rows_pass) + 15) & ~15);
@@ -336,11 +348,11 @@ weights_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
           const uint64_t dk = dk0 + ((uint64_t)(c * kChunkBytes) >> 4), dq = dq0 + ((uint64_t)(slot * q_chunk) >> 4);
           const int depth = c < p.latent_chunks ? kBK : p.kv.rope;
 #pragma unroll
-          for (int k = 0; k < kBK / kUK; ++k)
-            if (k * kUK < depth)
-              tc_mma_warp(tm + buf * kPassRows, dk + ((k * kUK * 2) >> 4), dq + ((k * kUK * 2) >> 4), idesc, k ? 1u : (c ? 1u : 0u));
+          for (int x = 0; x < kBK / kUK; ++x)
+            if (x * kUK < depth)
+              tc_mma_warp(tm + buf * kPassRows, dk + ((x * kUK * 2) >> 4), dq + ((x * kUK * 2) >> 4), idesc, x ? 1u : (c ? 1u : 0u));
           issued = true;
-          if (g == p1 - 1) tc_commit_warp(&sh.k_empty[c]);
+          if (k == n - 1) tc_commit_warp(&sh.k_empty[c]);
           if (!keep) tc_commit_warp(&sh.q_empty[slot]);
           if (++slot == p.ring) {
             slot = 0;
@@ -371,7 +383,7 @@ weights_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
       for (int e = 0; e < 2; ++e) {
         const int t = tl.t0 + r + 64 * e;
         row[e] = nullptr;
-        if (any && t < tl.len) {
+        if (any && t < tl.t1) {
           int pg = p.kv.table[(size_t)tl.seq * p.kv.max_blocks + (t >> p.kv.page_shift)];
           if (pg < 0 || pg >= p.kv.n_pages) {
             set_status(p.status, MOE_DEV_ERR_BAD_PAGE);
@@ -428,10 +440,11 @@ weights_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
     while (ok && it.next(tl)) {
       const int t = tl.t0 + st;
       float* w = p.weights + (size_t)tl.seq * cap + t;
-      const bool mine = t < tl.len;
+      const bool mine = t < tl.t1;
       const float old = mine && it.shares == 1 && p.decay != 0.0f ? *w : 0.0f;
       float sum = 0.0f;
-      for (int g = tl.p0; g < tl.p1; ++g, ++pass) {
+      for (int k = 0; k < tl.p1 - tl.p0; ++k, ++pass) {
+        const int g = Tiles::pass(tl, k);
         const int rows = min(p.rows_pass, rows_all - g * p.rows_pass);
         if (p.passes > 1 || tl.first) {
           stage ^= 1;
@@ -447,7 +460,7 @@ weights_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
         if (!ok) break;
         tc_fence_after();
         const int limit0 = tl.len - p.Q + g * p.rows_pass / p.heads + 1;       // the pass's first row sees the least
-        const bool seen = tl.t0 + kTile <= limit0;
+        const bool seen = tl.t1 <= limit0;
         for (int c = 0; c < rows; c += 32) {
           uint32_t s[32];
           tmem_ld32(lane_base + buf * kPassRows + c, s);
@@ -461,8 +474,11 @@ weights_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
         if (lane == 0) mbar_arrive(&sh.d_empty[buf]);
       }
       if (!ok) break;
-      if (it.shares > 1) p.part[(size_t)tl.unit * kTile + st] = sum;
-      else if (mine) *w = p.decay == 0.0f ? sum : fmaf(p.decay, old, sum);
+      if (it.shares > 1) {
+        if (st < kUnit) p.part[(size_t)tl.work * kUnit + st] = sum;
+      } else if (mine) {
+        *w = p.decay == 0.0f ? sum : fmaf(p.decay, old, sum);
+      }
     }
   }
   __syncthreads();
@@ -471,26 +487,24 @@ weights_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
   if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols));
 }
 
-// Shares of tiles, added in order (calls of more than one pass; returns at once where none were shared out).
-__global__ void __launch_bounds__(kTile) finish_weights_kernel(const WeightParams p) {
+// Shares of units, added in order (calls of more than one pass; returns at once where none were shared out).
+__global__ void __launch_bounds__(kUnit) finish_weights_kernel(const WeightParams p) {
   pdl_wait();
   pdl_trigger();
-  const int tiles = p.plan[p.B], shares = pass_shares(tiles, p.passes, p.ctas);
-  if (shares == 1) return;
-  for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
-    int lo = 0, hi = p.B;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (p.plan[mid] <= tile) lo = mid;
-      else hi = mid;
-    }
-    const int seq = p.seqs[p.first + lo], t = (tile - p.plan[lo]) * kTile + threadIdx.x;
-    if (t >= p.kv.len_of(seq)) continue;
-    float sum = 0.0f;
-    for (int s = 0; s < shares; ++s) sum += p.part[((size_t)tile * shares + s) * kTile + threadIdx.x];
-    float* w = p.weights + (size_t)seq * ((size_t)p.kv.max_blocks << p.kv.page_shift) + t;
-    *w = p.decay == 0.0f ? sum : fmaf(p.decay, *w, sum);
+  const int units = p.plan[p.B], shares = pass_shares(units, p.passes, p.ctas), unit = blockIdx.x;
+  if (shares == 1 || unit >= units) return;
+  int lo = 0, hi = p.B;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (p.plan[mid] <= unit) lo = mid;
+    else hi = mid;
   }
+  const int seq = p.seqs[p.first + lo], t = (unit - p.plan[lo]) * kUnit + threadIdx.x;
+  if (t >= p.kv.len_of(seq)) return;
+  float sum = 0.0f;
+  for (int s = 0; s < shares; ++s) sum += p.part[((size_t)unit * shares + s) * kUnit + threadIdx.x];
+  float* w = p.weights + (size_t)seq * ((size_t)p.kv.max_blocks << p.kv.page_shift) + t;
+  *w = p.decay == 0.0f ? sum : fmaf(p.decay, *w, sum);
 }
 
 // ---------------------------------------------------------------- host side
@@ -518,7 +532,7 @@ extern "C" {
 
 size_t moe_latent_weights_workspace_size(const moe_kv_cache* cache, int B, int Q, int heads) {
   if (check_latent(cache, 0) != MOE_OK || B < 1 || Q < 1 || heads < 1 || !weights_shape_ok(B, Q, heads)) return 0;
-  return plan_bytes(B) + (Q * heads > kResident ? align_up((size_t)num_sms() * kTile * sizeof(float), 256) : 0);
+  return plan_bytes(B) + (Q * heads > kResident ? align_up((size_t)num_sms() * kUnit * sizeof(float), 256) : 0);
 }
 
 int moe_latent_weights(const moe_kv_cache* cache, int layer, const void* q, const int32_t* seqs, int B, int Q, int heads,
@@ -563,7 +577,8 @@ int moe_latent_weights(const moe_kv_cache* cache, int layer, const void* q, cons
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const int smem = p.chunks * kChunkBytes + p.ring * p.rows_pass * kBK * 2 + 1024;
   CUtensorMap mk;
-  if (!make_map(&mk, cache->pages, p.kv.row, (uint64_t)cache->n_layers * cache->n_pages * cache->page_tokens, cache->page_tokens))
+  if (!make_map(&mk, cache->pages, p.kv.row, (uint64_t)cache->n_layers * cache->n_pages * cache->page_tokens,
+                cache->page_tokens < kUnit ? cache->page_tokens : kUnit))
     return MOE_ERR_CUDA;
   for (int b0 = 0; b0 < B; b0 += kBatch) {   // lists of more than 512 sequences: several launches
     p.first = b0;
@@ -572,7 +587,7 @@ int moe_latent_weights(const moe_kv_cache* cache, int layer, const void* q, cons
     if (!make_map(&mq, reinterpret_cast<const __nv_bfloat16*>(q) + (size_t)b0 * rows * row, row, (uint64_t)p.B * rows, p.rows_pass))
       return MOE_ERR_CUDA;
     cudaError_t e = fp4 ? launch_weights<true>(mk, mq, p, smem, s) : launch_weights<false>(mk, mq, p, smem, s);
-    if (e == cudaSuccess && p.passes > 1) e = launch_k(finish_weights_kernel, p.ctas, kTile, 0, s, p);
+    if (e == cudaSuccess && p.passes > 1) e = launch_k(finish_weights_kernel, p.ctas / 2, kUnit, 0, s, p);   // no more units are shared out
     if (e != cudaSuccess) return MOE_ERR_CUDA;
   }
   return MOE_OK;
