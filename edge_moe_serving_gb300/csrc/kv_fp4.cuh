@@ -60,6 +60,15 @@ __device__ inline void fp4_store32(uint8_t* tile, int chunk_bytes, int r, int v,
   for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4*>(row + ((x ^ i) << 4)) = fp4_expand8(w[i], i < 2 ? fa : fb);
 }
 
+__device__ inline uint32_t ldg_stream_u16(const void* p) {
+  uint16_t v;
+  asm volatile("ld.global.nc.L1::no_allocate.u16 %0, [%1];" : "=h"(v) : "l"(p));
+  return v;
+}
+
+// Between ordinary writes to shared memory and the tensor cores' reads of them.
+__device__ inline void proxy_fence() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
 // ---------------------------------------------------------------- bf16 to codes
 struct Fp4Block {
   uint2 codes;

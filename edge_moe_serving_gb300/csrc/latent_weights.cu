@@ -37,10 +37,11 @@ using namespace tc;
 constexpr int kTile = 128;                       // tokens
 constexpr int kUnit = 32;                        // tokens that the line is cut by
 constexpr int kChunkBytes = kTile * kBK * 2;     // 16 KB: 128 rows x 64 entries
-constexpr int kMaxChunks = 9;
+constexpr int kMaxPairs = 4;                     // 128-entry slices of the latent
+constexpr int kMaxParts = kMaxPairs + 1;         // and the rotary key
 constexpr int kResident = 64;                    // query rows that stay in shared memory
 constexpr int kPassRows = 128;                   // query rows of a pass where they do not
-constexpr int kRing = 4;                         // chunks of such a pass in flight
+constexpr int kRing = 2;                         // parts of such a pass in flight
 constexpr int kThreads = 256;                    // a bf16 cache's; one in 4 bits has kExpandWarps more
 constexpr int kExpandWarps = 8;
 constexpr int kSumThreads = 128;
@@ -51,8 +52,8 @@ constexpr float kLog2e = 1.4426950408889634f;
 struct WeightParams {
   KvView kv;
   int layer, B, Q, heads, first;      // first: the launch's first entry of the list
-  int chunks, latent_chunks;          // 64-entry chunks of a row, and those of its latent
-  int passes, rows_pass, ring;        // passes over the query rows, rows of each, chunks of queries in shared memory
+  int pairs, parts;                   // a row comes in parts: 128-entry pairs of chunks, then the rotary key
+  int passes, rows_pass, ring;        // passes over the query rows, rows of each, parts of queries in shared memory
   int ctas;
   float scale_log2, decay;
   const int32_t* seqs;                // the whole list
@@ -125,7 +126,7 @@ struct Tiles {
 };
 
 struct alignas(16) Shared {
-  uint64_t k_full[kMaxChunks], k_empty[kMaxChunks], q_full[kMaxChunks], q_empty[kMaxChunks], d_full[2], d_empty[2], drain;
+  uint64_t k_full[kMaxParts], k_empty[kMaxParts], q_full[kMaxParts], q_empty[kMaxParts], d_full[2], d_empty[2], drain;
   uint32_t tmem;
   int abort;
   int warp_sum[kThreads / 32 + kExpandWarps];
@@ -177,11 +178,11 @@ weights_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
   constexpr int kAll = kThreads + (FP4 ? 32 * kExpandWarps : 0);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
-    for (int c = 0; c < kMaxChunks; ++c) {
-      mbar_init(&sh.k_full[c], FP4 && c < p.latent_chunks ? kExpandWarps : 1);
-      mbar_init(&sh.k_empty[c], 1);
-      mbar_init(&sh.q_full[c], 1);
-      mbar_init(&sh.q_empty[c], 1);
+    for (int j = 0; j < kMaxParts; ++j) {
+      mbar_init(&sh.k_full[j], FP4 && j < p.pairs ? kExpandWarps : 1);
+      mbar_init(&sh.k_empty[j], 1);
+      mbar_init(&sh.q_full[j], 1);
+      mbar_init(&sh.q_empty[j], 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.d_full[i], 1);
@@ -252,7 +253,7 @@ weights_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
   const uint32_t tmem = sh.tmem;
   volatile int* abort_flag = &sh.abort;
   const int rows_all = p.Q * p.heads, q_chunk = p.rows_pass * 128;
-  uint8_t* sq = smem + p.chunks * kChunkBytes;
+  uint8_t* sq = smem + (2 * p.pairs + (p.parts > p.pairs)) * kChunkBytes;
   Tiles it(p, sh.pref, sh.len, sh.ids);
   Tile tl;
 
@@ -261,7 +262,7 @@ weights_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
     const int page = p.kv.page_tokens, box = min(page, kUnit), layer_page = p.layer * p.kv.n_pages;
     const uint32_t smem0 = uni(smem_u32(smem)), bar0 = uni(smem_u32(&sh.k_full[0]));
     const uint64_t once = l2_evict_first();
-    const int c_first = FP4 ? p.latent_chunks : 0;
+    const int j_first = FP4 ? p.pairs : 0;
     int tile = 0;
     bool ok = true;
     while (__any_sync(0xffffffffu, ok && it.next(tl))) {
@@ -279,21 +280,26 @@ weights_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
       int rows[kTile / 16];
 #pragma unroll
       for (int i = 0; i < kTile / 16; ++i) rows[i] = (int)uni(lane == i ? row : 0);
-      for (int c = c_first; c < p.chunks; ++c) {
-        ok = warp_wait(&sh.k_empty[c], (tile & 1) ^ 1u, abort_flag);
+      for (int j = j_first; j < p.parts; ++j) {
+        ok = warp_wait(&sh.k_empty[j], (tile & 1) ^ 1u, abort_flag);
         if (!ok) break;
-        mbar_expect_tx_warp(bar0 + 8 * c, (uint32_t)(nb * box * 128));
-        const int at = c < p.latent_chunks ? c * kBK : p.kv.rope_at;
+        const bool pair = j < p.pairs;
+        const uint32_t to = smem0 + 2 * j * kChunkBytes, bar = bar0 + 8 * j;
+        const int at = pair ? 2 * j * kBK : p.kv.rope_at;
+        mbar_expect_tx_warp(bar, (uint32_t)(nb * box * (pair ? 256 : 128)));
 #pragma unroll
         for (int i = 0; i < kTile / 16; ++i)
-          if (i < nb) tma_load_2d_hint_warp(smem0 + c * kChunkBytes + i * box * 128, &map_k, bar0 + 8 * c, at, rows[i], once);
+          if (i < nb) {
+            tma_load_2d_hint_warp(to + i * box * 128, &map_k, bar, at, rows[i], once);
+            if (pair) tma_load_2d_hint_warp(to + kChunkBytes + i * box * 128, &map_k, bar, at + kBK, rows[i], once);
+          }
       }
       ++tile;
     }
     // drain: whatever was asked for lands before the CTA can exit
     volatile int no_abort = 0;
     if (tile)
-      for (int c = c_first; c < p.chunks; ++c) mbar_wait(&sh.k_full[c], (tile - 1) & 1, &no_abort);
+      for (int j = j_first; j < p.parts; ++j) mbar_wait(&sh.k_full[j], (tile - 1) & 1, &no_abort);
     __syncwarp();
   } else if (warp == 2) {
     // ------------------------------------------------ copies of the queries
@@ -307,11 +313,14 @@ weights_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
       const int n = (int)uni(tl.p1 - tl.p0);
       for (int k = 0; ok && k < n; ++k) {
         const int row0 = (int)uni(tl.b * rows_all + Tiles::pass(tl, k) * p.rows_pass);
-        for (int c = 0; c < p.chunks; ++c) {
+        for (int j = 0; j < p.parts; ++j) {
           ok = warp_wait(&sh.q_empty[slot], par, abort_flag);
           if (!ok) break;
-          mbar_expect_tx_warp(bar0 + 8 * slot, (uint32_t)q_chunk);
-          tma_load_2d_hint_warp(q0 + slot * q_chunk, &map_q, bar0 + 8 * slot, c < p.latent_chunks ? c * kBK : p.kv.rank, row0, keep);
+          const bool pair = j < p.pairs;
+          const uint32_t to = q0 + 2 * slot * q_chunk, bar = bar0 + 8 * slot;
+          mbar_expect_tx_warp(bar, (uint32_t)(pair ? 2 * q_chunk : q_chunk));
+          tma_load_2d_hint_warp(to, &map_q, bar, 2 * j * kBK, row0, keep);      // the rotary key stands behind the latent
+          if (pair) tma_load_2d_hint_warp(to + q_chunk, &map_q, bar, 2 * j * kBK + kBK, row0, keep);
           ++loads;
           if (++slot == p.ring) {
             slot = 0;
@@ -329,7 +338,8 @@ weights_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
   } else if (warp == 1) {
     // ------------------------------------------------ products
     const uint32_t tm = uni(tmem), smem0 = uni(smem_u32(smem));
-    const uint64_t dk0 = smem_desc(smem0), dq0 = smem_desc(smem0 + p.chunks * kChunkBytes);
+    const uint32_t sq0 = uni(smem_u32(sq));
+    const uint64_t dk0 = smem_desc(smem0), dq0 = smem_desc(sq0), q_step = (uint64_t)(q_chunk >> 4);
     int tile = 0, pass = 0, slot = 0;
     uint32_t par = 0;
     bool ok = true, issued = false;
@@ -341,18 +351,25 @@ weights_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
         ok = warp_wait(&sh.d_empty[buf], ((pass >> 1) & 1) ^ 1u, abort_flag);
         if (!ok) break;
         const uint32_t idesc = make_idesc(kTile, (min(p.rows_pass, rows_all - g * p.rows_pass) + 15) & ~15);
-        for (int c = 0; c < p.chunks; ++c) {
-          ok = warp_wait(&sh.q_full[slot], par, abort_flag) && warp_wait(&sh.k_full[c], tile & 1, abort_flag);
+        const uint32_t d = tm + buf * kPassRows;
+        for (int j = 0; j < p.parts; ++j) {
+          ok = warp_wait(&sh.q_full[slot], par, abort_flag) && warp_wait(&sh.k_full[j], tile & 1, abort_flag);
           if (!ok) break;
+          if (FP4) proxy_fence();               // the expanded rows, for the products
           tc_fence_after();
-          const uint64_t dk = dk0 + ((uint64_t)(c * kChunkBytes) >> 4), dq = dq0 + ((uint64_t)(slot * q_chunk) >> 4);
-          const int depth = c < p.latent_chunks ? kBK : p.kv.rope;
+          const uint64_t dk = dk0 + ((uint64_t)(2 * j * kChunkBytes) >> 4), dq = dq0 + 2 * slot * q_step;
+          if (j < p.pairs) {
 #pragma unroll
-          for (int x = 0; x < kBK / kUK; ++x)
-            if (x * kUK < depth)
-              tc_mma_warp(tm + buf * kPassRows, dk + ((x * kUK * 2) >> 4), dq + ((x * kUK * 2) >> 4), idesc, x ? 1u : (c ? 1u : 0u));
+            for (int x = 0; x < 8; ++x)
+              tc_mma_warp(d, dk + (((x >> 2) * kChunkBytes + (x & 3) * kUK * 2) >> 4),
+                          dq + ((x & 3) * kUK * 2 >> 4) + (x >> 2) * q_step, idesc, x ? 1u : (j ? 1u : 0u));
+          } else {
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+              if (x * kUK < p.kv.rope) tc_mma_warp(d, dk + ((x * kUK * 2) >> 4), dq + ((x * kUK * 2) >> 4), idesc, 1u);
+          }
           issued = true;
-          if (k == n - 1) tc_commit_warp(&sh.k_empty[c]);
+          if (k == n - 1) tc_commit_warp(&sh.k_empty[j]);
           if (!keep) tc_commit_warp(&sh.q_empty[slot]);
           if (++slot == p.ring) {
             slot = 0;
@@ -371,26 +388,34 @@ weights_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
     __syncwarp();
   } else if (FP4 && warp >= kThreads / 32) {
     // ------------------------------------------------ latents in 4 bits, expanded into the tile that a copy would fill
-    // Four threads a token, two tokens a thread; of each 128-entry pair a thread has 16 bytes of codes, a quarter.  What
-    // the next tile needs is asked for as soon as its registers are free.
+    // Four threads a token, two tokens a thread; of each 128-entry pair a thread has 16 bytes of codes, a quarter.  Codes
+    // are asked for a tile ahead, as soon as their registers are free, and pages two tiles ahead.  No fence here: it
+    // would wait for those loads.  The issuer of the products has it, behind its wait for these warps.
     const int et = tid - kThreads, r = et >> 2, v = et & 3, scales_at = p.kv.rank / 2 + 2 * p.kv.rope;
-    const int pairs = p.latent_chunks / 2;
-    const uint8_t* row[2] = {nullptr, nullptr};
+    const int pairs = p.pairs;
+    const uint8_t* row[2];
+    bool here[2];
+    int page[2], slot[2];         // of the tile after the next: page (-1: no token) and place in it
     uint4 code[2][4];
     uint32_t scale[2][4];
-    auto find = [&](bool any) {
+    auto look_up = [&](bool any) {
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int t = tl.t0 + r + 64 * e;
+        slot[e] = any && t < tl.t1 ? t & (p.kv.page_tokens - 1) : -1;
+        if (slot[e] >= 0) page[e] = __ldg(p.kv.table + (size_t)tl.seq * p.kv.max_blocks + (t >> p.kv.page_shift));
+      }
+    };
+    auto locate = [&]() {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
         row[e] = nullptr;
-        if (any && t < tl.t1) {
-          int pg = p.kv.table[(size_t)tl.seq * p.kv.max_blocks + (t >> p.kv.page_shift)];
-          if (pg < 0 || pg >= p.kv.n_pages) {
-            set_status(p.status, MOE_DEV_ERR_BAD_PAGE);
-            pg = 0;
-          }
-          row[e] = reinterpret_cast<const uint8_t*>(p.kv.pages + p.kv.row_offset(p.layer, pg, t & (p.kv.page_tokens - 1)));
+        if (slot[e] < 0) continue;
+        if (page[e] < 0 || page[e] >= p.kv.n_pages) {
+          set_status(p.status, MOE_DEV_ERR_BAD_PAGE);
+          page[e] = 0;
         }
+        row[e] = reinterpret_cast<const uint8_t*>(p.kv.pages + p.kv.row_offset(p.layer, page[e], slot[e]));
       }
     };
     auto load = [&](int j) {
@@ -398,35 +423,40 @@ weights_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
       for (int e = 0; e < 2; ++e)
         if (row[e]) {
           code[e][j] = ldg_stream(row[e] + 64 * j + 16 * v);
-          scale[e][j] = *reinterpret_cast<const unsigned short*>(row[e] + scales_at + 8 * j + 2 * v);
+          scale[e][j] = ldg_stream_u16(row[e] + scales_at + 8 * j + 2 * v);
         }
     };
-    bool more = it.next(tl), ok = true;
-    find(more);
+    bool now = it.next(tl), ok = true;
+    look_up(now);
+    locate();
 #pragma unroll
     for (int j = 0; j < 4; ++j)
       if (j < pairs) load(j);
-    for (int tile = 0; ok && more; ++tile) {
-      const bool here[2] = {row[0] != nullptr, row[1] != nullptr};
-      more = it.next(tl);
-      find(more);
+    here[0] = row[0] != nullptr;
+    here[1] = row[1] != nullptr;
+    bool next = it.next(tl);
+    look_up(next);
+    locate();
+    for (int tile = 0; ok && now; ++tile) {
+      const bool after = it.next(tl);
+      look_up(after);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         if (j >= pairs) break;
-        ok = ok && warp_wait(&sh.k_empty[2 * j], (tile & 1) ^ 1u, abort_flag) &&
-             warp_wait(&sh.k_empty[2 * j + 1], (tile & 1) ^ 1u, abort_flag);
+        ok = ok && warp_wait(&sh.k_empty[j], (tile & 1) ^ 1u, abort_flag);
         if (!ok) break;
 #pragma unroll
         for (int e = 0; e < 2; ++e)
           if (here[e]) fp4_store32(smem + 2 * j * kChunkBytes, kChunkBytes, r + 64 * e, v, code[e][j], scale[e][j]);
         load(j);
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&sh.k_full[2 * j]);
-          mbar_arrive(&sh.k_full[2 * j + 1]);
-        }
+        if (lane == 0) mbar_arrive(&sh.k_full[j]);
       }
+      here[0] = row[0] != nullptr;
+      here[1] = row[1] != nullptr;
+      now = next;
+      next = after;
+      locate();
     }
     __syncwarp();
   } else if (warp >= 4) {
@@ -538,8 +568,9 @@ size_t moe_latent_weights_workspace_size(const moe_kv_cache* cache, int B, int Q
 int moe_latent_weights(const moe_kv_cache* cache, int layer, const void* q, const int32_t* seqs, int B, int Q, int heads,
                        float scale, const float* lse, float decay, float* weights, void* ws, size_t ws_bytes,
                        uint32_t* dev_status, moe_stream_t stream) {
+  constexpr int kMaxChunks = 2 * kMaxPairs + 1;
   static_assert(sizeof(Shared) + 1024 + kMaxChunks * (kChunkBytes + kResident * kBK * 2) <= 227 * 1024 &&
-                    kRing * kPassRows * kBK * 2 <= kMaxChunks * kResident * kBK * 2, "shared memory");
+                    2 * kRing * kPassRows <= kMaxChunks * kResident, "shared memory");
   int st = check_latent(cache, layer);
   if (st == MOE_ERR_INVALID_ARG || check_kv(cache) != MOE_OK) return st;
   if (B < 0 || Q < 1 || heads < 1 || !std::isfinite(scale) || !(decay >= 0.0f && decay <= 1.0f)) return MOE_ERR_INVALID_ARG;
@@ -557,13 +588,13 @@ int moe_latent_weights(const moe_kv_cache* cache, int layer, const void* q, cons
   p.layer = layer;
   p.Q = Q;
   p.heads = heads;
-  p.latent_chunks = cache->rank / kBK;
-  p.chunks = p.latent_chunks + (cache->rope ? 1 : 0);
+  p.pairs = cache->rank / 128;
+  p.parts = p.pairs + (cache->rope ? 1 : 0);
   const int most = rows <= kResident ? kResident : kPassRows;
   p.passes = (rows + most - 1) / most;
   p.rows_pass = ((rows + p.passes - 1) / p.passes + 15) & ~15;       // evenly, in multiples of 16
   p.passes = (rows + p.rows_pass - 1) / p.rows_pass;
-  p.ring = rows <= kResident ? p.chunks : kRing;
+  p.ring = rows <= kResident ? p.parts : kRing;
   p.ctas = num_sms();
   // zero as the smallest normal number, as in the attention whose log-sum-exp this is
   p.scale_log2 = scale == 0.0f ? FLT_MIN : scale * kLog2e;
@@ -575,7 +606,8 @@ int moe_latent_weights(const moe_kv_cache* cache, int layer, const void* q, cons
   p.part = reinterpret_cast<float*>(reinterpret_cast<char*>(ws) + plan_bytes(B));
   p.status = dev_status;
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const int smem = p.chunks * kChunkBytes + p.ring * p.rows_pass * kBK * 2 + 1024;
+  const int chunks = 2 * p.pairs + (cache->rope ? 1 : 0), q_chunks = rows <= kResident ? chunks : 2 * kRing;
+  const int smem = chunks * kChunkBytes + q_chunks * p.rows_pass * kBK * 2 + 1024;
   CUtensorMap mk;
   if (!make_map(&mk, cache->pages, p.kv.row, (uint64_t)cache->n_layers * cache->n_pages * cache->page_tokens,
                 cache->page_tokens < kUnit ? cache->page_tokens : kUnit))
