@@ -46,18 +46,62 @@ __device__ inline uint4 fp4_expand8(uint32_t w, uint32_t factor) {
   return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
-// A quarter of 128 entries of row r (16 bytes of codes, their two scales) into the two 64-entry chunks of a K-major tile with
-// the 128-byte swizzle that TMA writes: quarter v is half of chunk v / 2.  The eight lanes of a store phase (two rows,
-// four quarters) meet eight different 16-byte columns only if the quarters of chunk 1 go the other way round.
-__device__ inline void fp4_store32(uint8_t* tile, int chunk_bytes, int r, int v, const uint4& c, uint32_t scales) {
-  const uint32_t f0 = fp4_factor(scales & 0xFFu), f1 = fp4_factor(scales >> 8 & 0xFFu);
-  uint8_t* row = tile + (v >> 1) * chunk_bytes + r * 128;
-  const bool turn = v >= 2;
-  const uint32_t w[4] = {turn ? c.z : c.x, turn ? c.w : c.y, turn ? c.x : c.z, turn ? c.y : c.w};
-  const uint32_t fa = turn ? f1 : f0, fb = turn ? f0 : f1;
-  const int x = ((v & 1) * 4 + (turn ? 2 : 0)) ^ (r & 7);
+// The same with one product a pair, for scales below 4: factor = 2^126 times the scale.
+__device__ inline uint4 fp4_expand8_small(uint32_t w, uint32_t factor) {
+  const uint32_t a = w & 0x0F0F0F0Fu, b = (w >> 4) & 0x0F0F0F0Fu;
+  uint32_t o[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4*>(row + ((x ^ i) << 4)) = fp4_expand8(w[i], i < 2 ? fa : fb);
+  for (int j = 0; j < 4; ++j) {
+    uint32_t t;
+    asm("prmt.b32 %0, %1, %2, %3;" : "=r"(t) : "r"(a), "r"(b), "r"(0x8080u | (uint32_t)j | (4u + j) << 8));
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(o[j]) : "r"((t * 0x1040u) & 0x81C081C0u), "r"(factor));
+  }
+  return make_uint4(o[0], o[1], o[2], o[3]);
+}
+__device__ inline uint32_t fp4_factor_small(uint32_t scales, int which) {      // of the two scales in a 16-bit word
+  uint32_t b, f;
+  asm("prmt.b32 %0, %1, 0, %2;" : "=r"(b) : "r"(scales), "r"(which ? 0x4141u : 0x4040u));   // the byte in both halves
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(f) : "r"(b << 4), "r"(0x7B007B00u));                // 2^119, twice: from 2^-112
+  asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(f) : "r"(0x7B007B00u));
+  return f;
+}
+
+// Where a thread's quarter of 128 entries of a tile's row lies (16 bytes of codes, 32 entries): four 16-byte columns of a
+// K-major tile with the 128-byte swizzle that TMA writes.  Quarter v is half of 64-entry chunk v / 2.  Lanes l, l + 8,
+// l + 16, l + 24 have one row, so that the eight lanes of a store phase meet eight rows, whose columns all differ.
+struct Fp4Place {
+  uint32_t at[4];
+  __device__ Fp4Place(uint32_t tile, int chunk_bytes, int row, int v) {
+    const uint32_t base = tile + (v >> 1) * chunk_bytes + row * 128, x = (uint32_t)(((v & 1) * 4) ^ (row & 7));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) at[i] = base + ((x ^ i) << 4);
+  }
+};
+
+template <int OFFSET>
+__device__ inline void st_shared_v4(uint32_t at, const uint4& v) {
+  asm volatile("st.shared.v4.b32 [%0 + %5], {%1, %2, %3, %4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w), "n"(OFFSET)
+               : "memory");
+}
+
+// The quarter's entries to `to` + OFFSET (a whole warp at once): with one product where all of the warp's scales are below
+// 4 (a block whose largest entry is 24, far above a normalised latent), else with two, which also know a scale that is NaN.
+template <int OFFSET>
+__device__ inline void fp4_store32(const Fp4Place& to, uint32_t slot, const uint4& c, uint32_t scales) {
+  const bool large = (scales & 0xFFu) >= 0x88u || scales >= 0x8800u;
+  if (!__any_sync(0xffffffffu, large)) {
+    const uint32_t f0 = fp4_factor_small(scales, 0), f1 = fp4_factor_small(scales, 1);
+    st_shared_v4<OFFSET>(to.at[0] + slot, fp4_expand8_small(c.x, f0));
+    st_shared_v4<OFFSET>(to.at[1] + slot, fp4_expand8_small(c.y, f0));
+    st_shared_v4<OFFSET>(to.at[2] + slot, fp4_expand8_small(c.z, f1));
+    st_shared_v4<OFFSET>(to.at[3] + slot, fp4_expand8_small(c.w, f1));
+  } else {
+    const uint32_t f0 = fp4_factor(scales & 0xFFu), f1 = fp4_factor(scales >> 8);
+    st_shared_v4<OFFSET>(to.at[0] + slot, fp4_expand8(c.x, f0));
+    st_shared_v4<OFFSET>(to.at[1] + slot, fp4_expand8(c.y, f0));
+    st_shared_v4<OFFSET>(to.at[2] + slot, fp4_expand8(c.z, f1));
+    st_shared_v4<OFFSET>(to.at[3] + slot, fp4_expand8(c.w, f1));
+  }
 }
 
 __device__ inline uint32_t ldg_stream_u16(const void* p) {

@@ -470,6 +470,7 @@ decode_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_constant_
         for (int j = 0; j < p.pairs; ++j) {
           ok = warp_wait(&sh.full[slot][j], par, abort_flag);
           if (!ok) break;
+          if (FP4) proxy_fence();          // the expanded entries, for the products
           tc_fence_after();
 #pragma unroll
           for (int k = 0; k < 8; ++k)
@@ -543,49 +544,82 @@ decode_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_constant_
     __syncwarp();
   } else if (FP4 && warp >= kThreads / 32) {
     // ------------------------------------------------ latents in 4 bits, expanded into the tile that a copy would fill
-    // Four threads a token; of each 128-entry pair a thread has 16 bytes of codes, a quarter.
-    const int et = tid - kThreads, r = et >> 2, v = et & 3;
+    // Four threads a token; of each 128-entry pair a thread has 16 bytes of codes, a quarter.  Codes are asked for a tile
+    // ahead, as soon as their registers are free, and pages two tiles ahead.  Places past a piece's last token get some
+    // row's entries, which the softmax warps hide and clear.  The fence between these writes and the products is the
+    // products' issuers': here it would wait for the loads in flight.
+    const int r = (warp - kThreads / 32) * 8 + (lane & 7), v = lane >> 3;
     const int scales_at = p.kv.rank / 2 + 2 * p.rope;
+    const Fp4Place to(smem_u32(skv), kChunk, r, v);
+    const bool pseq_ok = p.np == 0 || (*p.prefix_seq >= 0 && *p.prefix_seq < p.kv.max_seqs);
+    int t0 = 0, t1 = 0;            // where the look-up stands in its piece
+    auto next_tile = [&]() {
+      t0 += kTok;
+      if (t0 < t1) return true;
+      if (!it.next(sg)) return false;
+      t0 = sg.tok0;
+      t1 = sg.tok1;
+      return true;
+    };
+    const uint8_t* row;
+    int page, at;                  // of the tile after the next
+    auto look_up = [&](bool any) {
+      const int t = t0 + r;
+      page = at = 0;
+      if (any && t < t1) {
+        const bool seq_ok = !sg.prefix || pseq_ok;
+        page = seq_ok ? __ldg(p.kv.table + (size_t)sg.seq * p.kv.max_blocks + (t >> p.kv.page_shift)) : INT_MIN;
+        at = t & (p.kv.page_tokens - 1);
+      }
+    };
+    auto locate = [&]() {
+      if (page < 0 || page >= p.kv.n_pages) {
+        set_status(p.status, page == INT_MIN ? MOE_DEV_ERR_BAD_SEQ : MOE_DEV_ERR_BAD_PAGE);
+        page = 0;
+      }
+      row = reinterpret_cast<const uint8_t*>(p.kv.pages + p.kv.row_offset(p.layer, page, at)) + 16 * v;
+    };
+    uint4 code[kMaxPairs];
+    uint32_t scale[kMaxPairs];
+    auto load = [&](int j) {
+      code[j] = ldg_stream(row + 64 * j);
+      scale[j] = ldg_stream_u16(row + scales_at + 8 * j - 14 * v);
+    };
+    bool now = next_tile(), ok = true;
+    look_up(now);
+    locate();
+#pragma unroll
+    for (int j = 0; j < kMaxPairs; ++j)
+      if (j < p.pairs) load(j);
+    bool next = now && next_tile();
+    look_up(next);
+    locate();
     int slot = 0;
     uint32_t par = 1;
-    bool ok = true;
-    const bool pseq_ok = p.np == 0 || (*p.prefix_seq >= 0 && *p.prefix_seq < p.kv.max_seqs);
-    while (__any_sync(0xffffffffu, ok && it.next(sg))) {
-      const bool seq_ok = !sg.prefix || pseq_ok;
-      const int32_t* blocks = p.kv.table + (seq_ok ? (size_t)sg.seq * p.kv.max_blocks : 0);
-      for (int t0 = sg.tok0; ok && t0 < sg.tok1; t0 += kTok) {
-        const int t = t0 + r;
-        const uint8_t* row = nullptr;
-        if (t < sg.tok1) {
-          int pg = seq_ok ? blocks[t >> p.kv.page_shift] : -1;
-          if (pg < 0 || pg >= p.kv.n_pages) {
-            set_status(p.status, seq_ok ? MOE_DEV_ERR_BAD_PAGE : MOE_DEV_ERR_BAD_SEQ);
-            pg = 0;
-          }
-          row = reinterpret_cast<const uint8_t*>(p.kv.pages + p.kv.row_offset(p.layer, pg, t & (p.kv.page_tokens - 1)));
-        }
-        uint4 c[kMaxPairs];
-        uint32_t s[kMaxPairs];
-#pragma unroll
-        for (int j = 0; j < kMaxPairs; ++j)
-          if (row && j < p.pairs) {
-            c[j] = ldg_stream(row + 64 * j + 16 * v);
-            s[j] = *reinterpret_cast<const unsigned short*>(row + scales_at + 8 * j + 2 * v);
-          }
-#pragma unroll
-        for (int j = 0; j < kMaxPairs; ++j) {
-          if (j >= p.pairs) break;
-          ok = ok && warp_wait(&sh.empty[slot][j], par, abort_flag);
-          if (!ok) break;
-          if (row) fp4_store32(skv + slot * slot_bytes + 2 * j * kChunk, kChunk, r, v, c[j], s[j]);
-          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&sh.full[slot][j]);
-        }
-        if (++slot == p.slots) {
-          slot = 0;
-          par ^= 1u;
-        }
+    while (ok && now) {
+      const bool after = next && next_tile();
+      look_up(after);
+      const uint32_t here = slot * slot_bytes;
+      auto expand = [&](auto J) {
+        constexpr int j = decltype(J)::value;
+        if (j >= p.pairs) return;
+        ok = ok && warp_wait(&sh.empty[slot][j], par, abort_flag);
+        if (!ok) return;
+        fp4_store32<2 * j * kChunk>(to, here, code[j], scale[j]);
+        load(j);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.full[slot][j]);
+      };
+      expand(std::integral_constant<int, 0>{});
+      expand(std::integral_constant<int, 1>{});
+      expand(std::integral_constant<int, 2>{});
+      expand(std::integral_constant<int, 3>{});
+      now = next;
+      next = after;
+      locate();
+      if (++slot == p.slots) {
+        slot = 0;
+        par ^= 1u;
       }
     }
     __syncwarp();

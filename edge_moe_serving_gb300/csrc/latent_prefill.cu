@@ -470,33 +470,42 @@ expand_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
     }
     __syncwarp();
   } else if (FP4 && warp >= kExThreads / 32) {
-    // ------------------------------------------------ latents in 4 bits, expanded: a thread a token
-    const int r = tid - kExThreads, scales_at = p.kv.rank / 2 + 2 * p.rope;
+    // ------------------------------------------------ latents in 4 bits, expanded: four threads a token, four tokens a thread
+    const int r0 = (warp - kExThreads / 32) * 8 + (lane & 7), v = lane >> 3, scales_at = p.kv.rank / 2 + 2 * p.rope;
     int loaded = 0;
     for (int u = u0; u < u1; ++u) {
       const int tile = u / p.heads;
       if (u != u0 && u != tile * p.heads) continue;
       const int4 d = tile_of(p, sh, tile);
-      const int t = d.y + r;
-      const uint8_t* row = nullptr;
-      if (t < d.z) {
-        int pg = p.kv.table[(size_t)d.x * p.kv.max_blocks + (t >> p.kv.page_shift)];
-        if (pg < 0 || pg >= p.kv.n_pages) {
-          set_status(p.status, MOE_DEV_ERR_BAD_PAGE);
-          pg = 0;
+      const uint8_t* row[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int t = d.y + r0 + 32 * e;
+        int pg = 0;
+        if (t < d.z) {
+          pg = p.kv.table[(size_t)d.x * p.kv.max_blocks + (t >> p.kv.page_shift)];
+          if (pg < 0 || pg >= p.kv.n_pages) {
+            set_status(p.status, MOE_DEV_ERR_BAD_PAGE);
+            pg = 0;
+          }
         }
-        row = reinterpret_cast<const uint8_t*>(p.kv.pages + p.kv.row_offset(p.layer, pg, t & (p.kv.page_tokens - 1)));
+        // past the last token some row: the epilogue writes zeros there
+        row[e] = reinterpret_cast<const uint8_t*>(p.kv.pages + p.kv.row_offset(p.layer, pg, t & (p.kv.page_tokens - 1))) + 16 * v;
       }
       if (!warp_wait(&sh.a_empty, (loaded & 1) ^ 1u, abort_flag)) break;
       ++loaded;
       for (int c = 0; c < chunks; c += 2) {
-        if (row) {
+        uint4 code[4];
+        uint32_t scale[4];
 #pragma unroll
-          for (int v = 0; v < 4; ++v)
-            fp4_store32(smem + c * kChunkBytes, kChunkBytes, r, v, ldg_stream(row + 32 * c + 16 * v),
-                        *reinterpret_cast<const unsigned short*>(row + scales_at + 4 * c + 2 * v));
+        for (int e = 0; e < 4; ++e) {
+          code[e] = ldg_stream(row[e] + 32 * c);
+          scale[e] = ldg_stream_u16(row[e] + scales_at + 4 * c - 14 * v);
         }
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          fp4_store32<0>(Fp4Place(smem_u32(smem) + c * kChunkBytes, kChunkBytes, r0 + 32 * e, v), 0, code[e], scale[e]);
+        proxy_fence();
         __syncwarp();
         if (lane == 0) {
           mbar_arrive(&sh.a_full[c]);

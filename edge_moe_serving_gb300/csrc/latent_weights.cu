@@ -25,6 +25,7 @@
 // MOE_DEV_ERR_TIMEOUT, drains and returns.
 #include <cfloat>
 #include <cmath>
+#include <type_traits>
 
 #include "kv_fp4.cuh"
 #include "tc_common.cuh"
@@ -78,16 +79,17 @@ __host__ __device__ inline int pass_shares(int units, int passes, int ctas) {
 
 struct Tiles {
   const int *pref, *len, *ids;
-  int u, u1, b, shares, share, passes;
+  int u, u1, b, shares, share, p0, p1;
 
   __device__ Tiles(const WeightParams& p, const int* pref_, const int* len_, const int* ids_) : pref(pref_), len(len_), ids(ids_) {
     const int units = pref[p.B];
-    passes = p.passes;
-    shares = pass_shares(units, passes, p.ctas);
+    shares = pass_shares(units, p.passes, p.ctas);
     const int per = (units + p.ctas - 1) / p.ctas;      // 1 where units are shared out
     u = (int)min((long long)units, (long long)(blockIdx.x / shares) * per);
     u1 = min(units, u + per);
     share = blockIdx.x % shares;
+    p0 = p.passes * share / shares;
+    p1 = p.passes * (share + 1) / shares;
     int lo = 0, hi = p.B;   // the last b with pref[b] <= the first unit
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
@@ -110,8 +112,8 @@ struct Tiles {
     t.t0 = (u - pref[b]) * kUnit;
     t.t1 = min(t.len, t.t0 + n * kUnit);
     t.work = u * shares + share;
-    t.p0 = passes * share / shares;
-    t.p1 = passes * (share + 1) / shares;
+    t.p0 = p0;
+    t.p1 = p1;
     t.first = first;
     t.last = u + n >= end;
     first = false;
@@ -389,71 +391,70 @@ weights_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
   } else if (FP4 && warp >= kThreads / 32) {
     // ------------------------------------------------ latents in 4 bits, expanded into the tile that a copy would fill
     // Four threads a token, two tokens a thread; of each 128-entry pair a thread has 16 bytes of codes, a quarter.  Codes
-    // are asked for a tile ahead, as soon as their registers are free, and pages two tiles ahead.  No fence here: it
-    // would wait for those loads.  The issuer of the products has it, behind its wait for these warps.
-    const int et = tid - kThreads, r = et >> 2, v = et & 3, scales_at = p.kv.rank / 2 + 2 * p.kv.rope;
-    const int pairs = p.pairs;
+    // are asked for a tile ahead, as soon as their registers are free, and pages two tiles ahead.  Places past a tile's
+    // last token get some row's entries: the sums there are not written.
+    const int r = (warp - kThreads / 32) * 8 + (lane & 7), v = lane >> 3;
+    const int scales_at = p.kv.rank / 2 + 2 * p.kv.rope, pairs = p.pairs;
+    const Fp4Place to[2] = {Fp4Place(smem_u32(smem), kChunkBytes, r, v), Fp4Place(smem_u32(smem), kChunkBytes, r + 64, v)};
     const uint8_t* row[2];
-    bool here[2];
-    int page[2], slot[2];         // of the tile after the next: page (-1: no token) and place in it
-    uint4 code[2][4];
-    uint32_t scale[2][4];
+    int page[2], at[2];           // of the tile after the next: page and place in it
+    uint4 code[2][kMaxPairs];
+    uint32_t scale[2][kMaxPairs];
     auto look_up = [&](bool any) {
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int t = tl.t0 + r + 64 * e;
-        slot[e] = any && t < tl.t1 ? t & (p.kv.page_tokens - 1) : -1;
-        if (slot[e] >= 0) page[e] = __ldg(p.kv.table + (size_t)tl.seq * p.kv.max_blocks + (t >> p.kv.page_shift));
+        page[e] = at[e] = 0;
+        if (any && t < tl.t1) {
+          page[e] = __ldg(p.kv.table + (size_t)tl.seq * p.kv.max_blocks + (t >> p.kv.page_shift));
+          at[e] = t & (p.kv.page_tokens - 1);
+        }
       }
     };
     auto locate = [&]() {
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        row[e] = nullptr;
-        if (slot[e] < 0) continue;
         if (page[e] < 0 || page[e] >= p.kv.n_pages) {
           set_status(p.status, MOE_DEV_ERR_BAD_PAGE);
           page[e] = 0;
         }
-        row[e] = reinterpret_cast<const uint8_t*>(p.kv.pages + p.kv.row_offset(p.layer, page[e], slot[e]));
+        row[e] = reinterpret_cast<const uint8_t*>(p.kv.pages + p.kv.row_offset(p.layer, page[e], at[e])) + 16 * v;
       }
     };
     auto load = [&](int j) {
 #pragma unroll
-      for (int e = 0; e < 2; ++e)
-        if (row[e]) {
-          code[e][j] = ldg_stream(row[e] + 64 * j + 16 * v);
-          scale[e][j] = ldg_stream_u16(row[e] + scales_at + 8 * j + 2 * v);
-        }
+      for (int e = 0; e < 2; ++e) {
+        code[e][j] = ldg_stream(row[e] + 64 * j);
+        scale[e][j] = ldg_stream_u16(row[e] + scales_at + 8 * j - 14 * v);
+      }
     };
     bool now = it.next(tl), ok = true;
     look_up(now);
     locate();
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
+    for (int j = 0; j < kMaxPairs; ++j)
       if (j < pairs) load(j);
-    here[0] = row[0] != nullptr;
-    here[1] = row[1] != nullptr;
     bool next = it.next(tl);
     look_up(next);
     locate();
     for (int tile = 0; ok && now; ++tile) {
       const bool after = it.next(tl);
       look_up(after);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        if (j >= pairs) break;
+      auto expand = [&](auto J) {
+        constexpr int j = decltype(J)::value;
+        if (j >= pairs) return;
         ok = ok && warp_wait(&sh.k_empty[j], (tile & 1) ^ 1u, abort_flag);
-        if (!ok) break;
-#pragma unroll
-        for (int e = 0; e < 2; ++e)
-          if (here[e]) fp4_store32(smem + 2 * j * kChunkBytes, kChunkBytes, r + 64 * e, v, code[e][j], scale[e][j]);
+        if (!ok) return;
+        fp4_store32<2 * j * kChunkBytes>(to[0], 0, code[0][j], scale[0][j]);
+        fp4_store32<2 * j * kChunkBytes>(to[1], 0, code[1][j], scale[1][j]);
         load(j);
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.k_full[j]);
-      }
-      here[0] = row[0] != nullptr;
-      here[1] = row[1] != nullptr;
+      };
+      expand(std::integral_constant<int, 0>{});
+      expand(std::integral_constant<int, 1>{});
+      expand(std::integral_constant<int, 2>{});
+      expand(std::integral_constant<int, 3>{});
       now = next;
       next = after;
       locate();
