@@ -8,7 +8,7 @@ namespace {
 
 constexpr int kSelThreads = 1024;
 constexpr int kMoveThreads = 256;
-constexpr int kMoveSteps = 8;            // 16-byte loads a thread has in flight
+constexpr int kMoveSteps = 4;            // 16-byte loads of a chunk that a thread has in flight
 constexpr int kSliceVecs = 8;            // 16-byte vectors of a row that a CTA moves
 
 struct EvictPlan {
@@ -43,6 +43,8 @@ struct SelShared {
   uint32_t digit;
   int left;
 };
+
+constexpr int kHeld = 8;                 // words of 32 weights that a warp keeps in registers: sequences up to 8192 tokens
 
 __global__ void __launch_bounds__(kSelThreads) select_kernel(const EvictParams p) {
   __shared__ SelShared sh;
@@ -100,76 +102,119 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const EvictParams p
   if (tid == 0 && layer == 0) p.plan[i] = EvictPlan{seq, len, now, head};
   const float* w = p.weights + ((size_t)layer * p.kv.max_seqs + seq) * p.cap;
 
+  // A warp takes a run of words of 32 tokens, a lane a token of each; the first words' keys stay in registers.  Key 0:
+  // a place that is not chosen among (it lies in the head or the tail, or past the end).
+  const int words = (len + 31) / 32, per = (words + 31) / 32, w0 = min(words, warp * per), w1 = min(words, w0 + per);
+  auto key_of = [&](int word) {
+    const int t = word * 32 + lane;
+    return t >= head && t < tail ? order_key(w[t]) : 0u;     // a weight's own key is above 0 (-infinity: 0x007FFFFF)
+  };
+  uint32_t held[kHeld];
+  if (want > 0) {
+#pragma unroll
+    for (int x = 0; x < kHeld; ++x) held[x] = w0 + x < w1 ? key_of(w0 + x) : 0u;
+  }
+
   // the want-th largest key, digit by digit; `left` of the keys equal to it stay
   uint32_t prefix = 0;
   int left = want;
   if (want > 0) {
+#pragma unroll 1
     for (int shift = 24; shift >= 0; shift -= 8) {
       for (int d = tid; d < 256; d += kSelThreads) sh.hist[d] = 0;
       __syncthreads();
-      for (int t = head + tid; t < tail; t += kSelThreads) {
-        const uint32_t k = order_key(w[t]);
-        if (shift == 24 || (k >> (shift + 8)) == (prefix >> (shift + 8))) atomicAdd(&sh.hist[k >> shift & 255], 1);
-      }
+      // weights of a context crowd into few digits: lanes with one digit add together
+      auto count = [&](uint32_t k) {
+        const bool in = k != 0 && (shift == 24 || (k >> (shift + 8)) == (prefix >> (shift + 8)));
+        if (!__any_sync(0xffffffffu, in)) return;
+        const uint32_t d = in ? k >> shift & 255 : 256u;
+        const uint32_t same = __match_any_sync(0xffffffffu, d);
+        if (in && lane == __ffs(same) - 1) atomicAdd(&sh.hist[d], __popc(same));
+      };
+#pragma unroll
+      for (int x = 0; x < kHeld; ++x)
+        if (w0 + x < w1) count(held[x]);
+      for (int x = w0 + kHeld; x < w1; ++x) count(key_of(x));
       __syncthreads();
-      if (tid == 0) {
-        int d = 255, l = left;
-        while (sh.hist[d] < l) l -= sh.hist[d--];
-        sh.digit = (uint32_t)d;
-        sh.left = l;
+      if (warp == 0) {             // the digit whose keys, with those above it, first reach `left`
+        int mine[8], sum = 0;
+#pragma unroll
+        for (int y = 0; y < 8; ++y) {
+          mine[y] = sh.hist[255 - (8 * lane + y)];
+          sum += mine[y];
+        }
+        int before = sum;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int u = __shfl_up_sync(0xffffffffu, before, o);
+          if (lane >= o) before += u;
+        }
+        before -= sum;
+        if (before < left && before + sum >= left) {
+          int l = left - before, y = 0;
+#pragma unroll
+          for (int z = 0; z < 7; ++z)
+            if (y == z && mine[z] < l) {
+              l -= mine[z];
+              y = z + 1;
+            }
+          sh.digit = (uint32_t)(255 - (8 * lane + y));
+          sh.left = l;
+        }
       }
       __syncthreads();
       prefix |= sh.digit << shift;
       left = sh.left;
-      __syncthreads();
     }
   }
-  // masks: a warp takes a run of words; keys above the threshold stay, and the first `left` of those equal to it
-  const int words = (len + 31) / 32, per = (words + 31) / 32, w0 = min(words, warp * per), w1 = min(words, w0 + per);
-  auto classify = [&](int word, uint32_t& sure, uint32_t& equal) {
+  // masks: keys above the threshold stay, and the first `left` of those equal to it
+  auto classify = [&](int word, uint32_t k, uint32_t& sure, uint32_t& equal) {
     const int t = word * 32 + lane;
-    bool s = t < head || (t >= tail && t < len), e = false;
-    if (want > 0 && t >= head && t < tail) {
-      const uint32_t k = order_key(w[t]);
-      s = k > prefix;
-      e = k == prefix;
-    }
-    sure = __ballot_sync(0xffffffffu, s);
-    equal = __ballot_sync(0xffffffffu, e);
+    sure = __ballot_sync(0xffffffffu, t < head || (t >= tail && t < len) || (want > 0 && k > prefix));
+    equal = __ballot_sync(0xffffffffu, want > 0 && k == prefix);
   };
   int gt = 0, eq = 0;
-  for (int x = w0; x < w1; ++x) {
+  auto tally = [&](int word, uint32_t k) {
     uint32_t s, e;
-    classify(x, s, e);
+    classify(word, k, s, e);
     gt += __popc(s);
     eq += __popc(e);
-  }
+  };
+#pragma unroll
+  for (int x = 0; x < kHeld; ++x)
+    if (w0 + x < w1) tally(w0 + x, held[x]);
+  for (int x = w0 + kHeld; x < w1; ++x) tally(x, key_of(x));
   if (lane == 0) {
     sh.warp_gt[warp] = gt;
     sh.warp_eq[warp] = eq;
   }
   __syncthreads();
   int at = 0, equals = 0;                 // what stays before this warp's words; keys equal to the threshold before them
-  for (int y = 0; y < warp; ++y) {
-    at += sh.warp_gt[y];
-    equals += sh.warp_eq[y];
+  {
+    const int g = lane < warp ? sh.warp_gt[lane] : 0, e = lane < warp ? sh.warp_eq[lane] : 0;
+    at = __reduce_add_sync(0xffffffffu, g);
+    equals = __reduce_add_sync(0xffffffffu, e);
   }
   at += min(equals, left);
   uint32_t* mask = p.mask + ((size_t)layer * p.n + i) * p.words;
   int32_t* before = p.before + ((size_t)layer * p.n + i) * p.words;
-  for (int x = w0; x < w1; ++x) {
+  auto mark = [&](int word, uint32_t k) {
     uint32_t s, e;
-    classify(x, s, e);
+    classify(word, k, s, e);
     const bool mine = (e >> lane & 1) && equals + __popc(e & ((1u << lane) - 1)) < left;
     const uint32_t m = s | __ballot_sync(0xffffffffu, mine);
     if (lane == 0) {
-      mask[x] = m;
-      before[x] = at;
+      mask[word] = m;
+      before[word] = at;
     }
-    if (kept && (m >> lane & 1)) kept[at + __popc(m & ((1u << lane) - 1))] = x * 32 + lane;
+    if (kept && (m >> lane & 1)) kept[at + __popc(m & ((1u << lane) - 1))] = word * 32 + lane;
     at += __popc(m);
     equals += __popc(e);
-  }
+  };
+#pragma unroll
+  for (int x = 0; x < kHeld; ++x)
+    if (w0 + x < w1) mark(w0 + x, held[x]);
+  for (int x = w0 + kHeld; x < w1; ++x) mark(x, key_of(x));
 }
 
 // In place: a token never moves to a later place, and a chunk of tokens is read before any of it is written, so
@@ -212,9 +257,9 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(const EvictParams p,
   auto place = [&](int t) {
     return reinterpret_cast<uint4*>(p.kv.pages + p.kv.row_offset(layer, table[t >> p.kv.page_shift], t & (p.kv.page_tokens - 1))) + v;
   };
-  for (int t0 = e.head; t0 < e.len; t0 += kChunk) {
-    uint4 x[kMoveSteps];
-    int to[kMoveSteps];
+  uint4 x[2][kMoveSteps];
+  int to[2][kMoveSteps];
+  auto read = [&](int t0, uint4 (&x)[kMoveSteps], int (&to)[kMoveSteps]) {
 #pragma unroll
     for (int u = 0; u < kMoveSteps; ++u) {
       const int t = t0 + u * kRowsStep + tid / kSliceVecs;
@@ -230,10 +275,22 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(const EvictParams p,
         }
       }
     }
-    __syncthreads();
+  };
+  auto write = [&](const uint4 (&x)[kMoveSteps], const int (&to)[kMoveSteps]) {
 #pragma unroll
     for (int u = 0; u < kMoveSteps; ++u)
       if (to[u] >= 0) *place(to[u]) = x[u];
+  };
+  // two chunks in turn: a chunk's reads are on their way while the one before is written
+  read(e.head, x[0], to[0]);
+  for (int t0 = e.head; t0 < e.len; t0 += 2 * kChunk) {
+    if (t0 + kChunk < e.len) read(t0 + kChunk, x[1], to[1]);
+    __syncthreads();               // everyone has read the first chunk
+    write(x[0], to[0]);
+    if (t0 + kChunk >= e.len) break;
+    if (t0 + 2 * kChunk < e.len) read(t0 + 2 * kChunk, x[0], to[0]);
+    __syncthreads();
+    write(x[1], to[1]);
   }
 }
 

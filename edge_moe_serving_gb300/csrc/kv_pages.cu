@@ -237,103 +237,105 @@ read_kernel(const KvView kv, int layer, const int32_t* tok_seq, const int32_t* t
   }
 }
 
-// Rows in 4 bits: a warp takes `per` rows, four at a time, a lane 16 entries of each (32 bytes of bf16, 8 of codes).
+// Rows in 4 bits: a warp takes up to four rows, a lane 16 entries of each (32 bytes of bf16, 8 of codes).  Few rows: one
+// each, spread over the SMs.
 constexpr int kFpRows = 4;
 
-__global__ void __launch_bounds__(kApplyThreads)
+__host__ __device__ inline unsigned fp4_rows_per_warp(unsigned N, unsigned sms) {
+  const unsigned per = N / (sms * 32);                      // 32 warps an SM before any takes a second row
+  return per < 1 ? 1 : per < kFpRows ? per : kFpRows;
+}
+
+__global__ void __launch_bounds__(kApplyThreads, 2)
 append_fp4_kernel(const KvView kv, int layer, const uint4* rows, const int32_t* tok_seq, const int32_t* tok_pos,
-                  unsigned N, const AppendShape shape, uint32_t* status) {
+                  unsigned N, unsigned per, uint32_t* status) {
   pdl_wait();
   pdl_trigger();
   const int lane = threadIdx.x & 31, blocks = kv.rank / kFpBlock, rope_vecs = kv.rope >> 3;
   const int in_vecs = 2 * blocks + rope_vecs, scales_at = kv.rank / 2 + 2 * kv.rope, scale_bytes = 2 * kv.row - scales_at;
-  const unsigned per = shape.per, step = append_step(shape);
+  const unsigned i0 = (blockIdx.x * kAppendWarps + (threadIdx.x >> 5)) * per;
+  if (i0 >= N) return;
+  const int n = (int)min(per, N - i0);
+  const uint4* from = rows + (size_t)i0 * in_vecs;
+  uint4 v[kFpRows][2];
+  auto load = [&](int b) {
+#pragma unroll
+    for (int j = 0; j < kFpRows; ++j)
+      if (j < n && b < blocks) {
+        v[j][0] = __ldcs(from + j * in_vecs + 2 * b);
+        v[j][1] = __ldcs(from + j * in_vecs + 2 * b + 1);
+      }
+  };
+  load(lane);                     // the rows are on their way while their places are found
+  const long long to = lane < n ? row_place(kv, layer, tok_seq[i0 + lane], tok_pos[i0 + lane], true, status) : -1;
+  uint8_t* dst[kFpRows];
+#pragma unroll
+  for (int j = 0; j < kFpRows; ++j) {
+    const long long at = __shfl_sync(0xffffffffu, to, j);
+    dst[j] = j < n && at >= 0 ? reinterpret_cast<uint8_t*>(kv.pages + at) : nullptr;
+  }
+  for (int x = lane; x < kFpRows * rope_vecs; x += 32) {
+    const int j = x / rope_vecs, y = x - j * rope_vecs;
+    uint8_t* d = j == 0 ? dst[0] : j == 1 ? dst[1] : j == 2 ? dst[2] : dst[3];
+    if (d) reinterpret_cast<uint4*>(d + kv.rank / 2)[y] = __ldcs(from + j * in_vecs + 2 * blocks + y);
+  }
   bool clamped = false;
-  for (unsigned i0 = append_first(shape, blockIdx.x, threadIdx.x >> 5); i0 < N; i0 += step) {
-    const unsigned i = i0 + lane;
-    const long long to = lane < (int)per && i < N ? row_place(kv, layer, tok_seq[i], tok_pos[i], true, status) : -1;
-    const int n = (int)min(per, N - i0);
-    for (int r0 = 0; r0 < n; r0 += kFpRows) {
-      uint8_t* dst[kFpRows];
+  for (int b = lane; b < scale_bytes; b += 32) {
+    if (b != lane) load(b);
 #pragma unroll
-      for (int j = 0; j < kFpRows; ++j) {
-        const long long at = __shfl_sync(0xffffffffu, to, min(r0 + j, 31));
-        dst[j] = r0 + j < n && at >= 0 ? reinterpret_cast<uint8_t*>(kv.pages + at) : nullptr;
+    for (int j = 0; j < kFpRows; ++j)
+      if (dst[j]) {
+        Fp4Block q = {};
+        if (b < blocks) {
+          q = fp4_quantise(v[j][0], v[j][1]);
+          *reinterpret_cast<uint2*>(dst[j] + 8 * b) = q.codes;
+          clamped |= q.clamped;
+        }
+        dst[j][scales_at + b] = (uint8_t)q.scale;       // zeros behind the scales
       }
-      const uint4* from = rows + (size_t)(i0 + r0) * in_vecs;
-      for (int b = lane; b < scale_bytes; b += 32) {
-        uint4 v[kFpRows][2];
-#pragma unroll
-        for (int j = 0; j < kFpRows; ++j)
-          if (dst[j] && b < blocks) {
-            v[j][0] = __ldcs(from + j * in_vecs + 2 * b);
-            v[j][1] = __ldcs(from + j * in_vecs + 2 * b + 1);
-          }
-#pragma unroll
-        for (int j = 0; j < kFpRows; ++j)
-          if (dst[j]) {
-            Fp4Block q = {};
-            if (b < blocks) {
-              q = fp4_quantise(v[j][0], v[j][1]);
-              *reinterpret_cast<uint2*>(dst[j] + 8 * b) = q.codes;
-              clamped |= q.clamped;
-            }
-            dst[j][scales_at + b] = (uint8_t)q.scale;       // zeros behind the scales
-          }
-      }
-#pragma unroll
-      for (int j = 0; j < kFpRows; ++j)
-        if (dst[j])
-          for (int y = lane; y < rope_vecs; y += 32)
-            reinterpret_cast<uint4*>(dst[j] + kv.rank / 2)[y] = __ldcs(from + j * in_vecs + 2 * blocks + y);
-    }
   }
   if (clamped) set_status(status, MOE_DEV_ERR_RANGE);
 }
 
 __global__ void __launch_bounds__(kApplyThreads)
 read_fp4_kernel(const KvView kv, int layer, const int32_t* tok_seq, const int32_t* tok_pos, unsigned N, uint4* rows,
-                const AppendShape shape, uint32_t* status) {
+                unsigned per, uint32_t* status) {
   pdl_wait();
   pdl_trigger();
   const int lane = threadIdx.x & 31, blocks = kv.rank / kFpBlock, rope_vecs = kv.rope >> 3;
   const int out_vecs = 2 * blocks + rope_vecs, scales_at = kv.rank / 2 + 2 * kv.rope;
-  const unsigned per = shape.per, step = append_step(shape);
-  for (unsigned i0 = append_first(shape, blockIdx.x, threadIdx.x >> 5); i0 < N; i0 += step) {
-    const unsigned i = i0 + lane;
-    const long long at0 = lane < (int)per && i < N ? row_place(kv, layer, tok_seq[i], tok_pos[i], false, status) : -1;
-    const int n = (int)min(per, N - i0);
-    for (int r0 = 0; r0 < n; r0 += kFpRows) {
-      const uint8_t* src[kFpRows];
+  const unsigned i0 = (blockIdx.x * kAppendWarps + (threadIdx.x >> 5)) * per;
+  if (i0 >= N) return;
+  const int n = (int)min(per, N - i0);
+  const long long at0 = lane < n ? row_place(kv, layer, tok_seq[i0 + lane], tok_pos[i0 + lane], false, status) : -1;
+  const uint8_t* src[kFpRows];
 #pragma unroll
-      for (int j = 0; j < kFpRows; ++j) {
-        const long long at = __shfl_sync(0xffffffffu, at0, min(r0 + j, 31));
-        src[j] = r0 + j < n && at >= 0 ? reinterpret_cast<const uint8_t*>(kv.pages + at) : nullptr;
-      }
-      uint4* to = rows + (size_t)(i0 + r0) * out_vecs;
-      for (int b = lane; b < blocks; b += 32) {
-        uint2 c[kFpRows];
-        uint32_t s[kFpRows];
+  for (int j = 0; j < kFpRows; ++j) {
+    const long long at = __shfl_sync(0xffffffffu, at0, j);
+    src[j] = j < n && at >= 0 ? reinterpret_cast<const uint8_t*>(kv.pages + at) : nullptr;
+  }
+  uint4* to = rows + (size_t)i0 * out_vecs;
+  for (int b = lane; b < blocks; b += 32) {
+    uint2 c[kFpRows];
+    uint32_t s[kFpRows];
 #pragma unroll
-        for (int j = 0; j < kFpRows; ++j)
-          if (src[j]) {
-            c[j] = *reinterpret_cast<const uint2*>(src[j] + 8 * b);
-            s[j] = src[j][scales_at + b];
-          }
-#pragma unroll
-        for (int j = 0; j < kFpRows; ++j)
-          if (src[j]) {
-            const uint32_t f = fp4_factor(s[j]);
-            to[j * out_vecs + 2 * b] = fp4_expand8(c[j].x, f);
-            to[j * out_vecs + 2 * b + 1] = fp4_expand8(c[j].y, f);
-          }
+    for (int j = 0; j < kFpRows; ++j)
+      if (src[j]) {
+        c[j] = *reinterpret_cast<const uint2*>(src[j] + 8 * b);
+        s[j] = src[j][scales_at + b];
       }
 #pragma unroll
-      for (int j = 0; j < kFpRows; ++j)
-        if (src[j])
-          for (int y = lane; y < rope_vecs; y += 32)
-            to[j * out_vecs + 2 * blocks + y] = reinterpret_cast<const uint4*>(src[j] + kv.rank / 2)[y];
-    }
+    for (int j = 0; j < kFpRows; ++j)
+      if (src[j]) {
+        const uint32_t f = fp4_factor(s[j]);
+        to[j * out_vecs + 2 * b] = fp4_expand8(c[j].x, f);
+        to[j * out_vecs + 2 * b + 1] = fp4_expand8(c[j].y, f);
+      }
+  }
+  for (int x = lane; x < kFpRows * rope_vecs; x += 32) {
+    const int j = x / rope_vecs, y = x - j * rope_vecs;
+    const uint8_t* f = j == 0 ? src[0] : j == 1 ? src[1] : j == 2 ? src[2] : src[3];
+    if (f) to[j * out_vecs + 2 * blocks + y] = reinterpret_cast<const uint4*>(f + kv.rank / 2)[y];
   }
 }
 
@@ -676,9 +678,14 @@ int moe_kv_append(const moe_kv_cache* cache, int layer, const void* rows, const 
   if (!rows || !tok_seq || !tok_pos) return MOE_ERR_INVALID_ARG;
   if (!kv_aligned(rows, 16)) return MOE_ERR_UNSUPPORTED;
   static_assert(kAppendWarps == kApplyThreads / 32, "warps of a CTA");
+  const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (cache->format == MOE_KV_FP4) {
+    const unsigned per = fp4_rows_per_warp((unsigned)N, (unsigned)num_sms()), rows_cta = per * kAppendWarps;
+    return status_of(launch_k(append_fp4_kernel, ((unsigned)N + rows_cta - 1) / rows_cta, kApplyThreads, 0, s, kv_view(*cache),
+                              layer, reinterpret_cast<const uint4*>(rows), tok_seq, tok_pos, (unsigned)N, per, dev_status));
+  }
   const AppendShape shape = append_shape((unsigned)N, (unsigned)num_sms());
-  return status_of(launch_k(cache->format == MOE_KV_FP4 ? append_fp4_kernel : append_kernel, shape.ctas, kApplyThreads, 0,
-                            reinterpret_cast<cudaStream_t>(stream), kv_view(*cache), layer,
+  return status_of(launch_k(append_kernel, shape.ctas, kApplyThreads, 0, s, kv_view(*cache), layer,
                             reinterpret_cast<const uint4*>(rows), tok_seq, tok_pos, (unsigned)N, shape, dev_status));
 }
 
@@ -690,10 +697,15 @@ int moe_kv_read(const moe_kv_cache* cache, int layer, const int32_t* tok_seq, co
   if (N == 0) return MOE_OK;
   if (!rows || !tok_seq || !tok_pos) return MOE_ERR_INVALID_ARG;
   if (!kv_aligned(rows, 16)) return MOE_ERR_UNSUPPORTED;
+  const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (cache->format == MOE_KV_FP4) {
+    const unsigned per = fp4_rows_per_warp((unsigned)N, (unsigned)num_sms()), rows_cta = per * kAppendWarps;
+    return status_of(launch_k(read_fp4_kernel, ((unsigned)N + rows_cta - 1) / rows_cta, kApplyThreads, 0, s, kv_view(*cache),
+                              layer, tok_seq, tok_pos, (unsigned)N, reinterpret_cast<uint4*>(rows), per, dev_status));
+  }
   const AppendShape shape = append_shape((unsigned)N, (unsigned)num_sms());
-  return status_of(launch_k(cache->format == MOE_KV_FP4 ? read_fp4_kernel : read_kernel, shape.ctas, kApplyThreads, 0,
-                            reinterpret_cast<cudaStream_t>(stream), kv_view(*cache), layer, tok_seq, tok_pos, (unsigned)N,
-                            reinterpret_cast<uint4*>(rows), shape, dev_status));
+  return status_of(launch_k(read_kernel, shape.ctas, kApplyThreads, 0, s, kv_view(*cache), layer, tok_seq, tok_pos,
+                            (unsigned)N, reinterpret_cast<uint4*>(rows), shape, dev_status));
 }
 
 int moe_kv_fork(const moe_kv_cache* cache, const int32_t* src, const int32_t* dst, int n, void* ws,
