@@ -70,38 +70,55 @@ __device__ inline uint32_t fp4_factor_small(uint32_t scales, int which) {      /
 // K-major tile with the 128-byte swizzle that TMA writes.  Quarter v is half of 64-entry chunk v / 2.  Lanes l, l + 8,
 // l + 16, l + 24 have one row, so that the eight lanes of a store phase meet eight rows, whose columns all differ.
 struct Fp4Place {
-  uint32_t at[4];
-  __device__ Fp4Place(uint32_t tile, int chunk_bytes, int row, int v) {
-    const uint32_t base = tile + (v >> 1) * chunk_bytes + row * 128, x = (uint32_t)(((v & 1) * 4) ^ (row & 7));
-#pragma unroll
-    for (int i = 0; i < 4; ++i) at[i] = base + ((x ^ i) << 4);
-  }
+  uint32_t at;       // column 0's address; column i's has bits 4 and 5 flipped by i
+  __device__ Fp4Place(uint32_t tile, int chunk_bytes, int row, int v)
+      : at(tile + (v >> 1) * chunk_bytes + row * 128 + ((((v & 1) * 4) ^ (row & 7)) << 4)) {}
 };
 
-template <int OFFSET>
 __device__ inline void st_shared_v4(uint32_t at, const uint4& v) {
-  asm volatile("st.shared.v4.b32 [%0 + %5], {%1, %2, %3, %4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w), "n"(OFFSET)
-               : "memory");
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
 
-// The quarter's entries to `to` + OFFSET (a whole warp at once): with one product where all of the warp's scales are below
-// 4 (a block whose largest entry is 24, far above a normalised latent), else with two, which also know a scale that is NaN.
-template <int OFFSET>
-__device__ inline void fp4_store32(const Fp4Place& to, uint32_t slot, const uint4& c, uint32_t scales) {
+// The quarter's entries to `to`, `offset` bytes on (a whole warp at once): with one product where all of the warp's scales
+// are below 4 (a block whose largest entry is 24, far above a normalised latent), else with two, which also know a scale
+// that is NaN.  A word at a time, rolled: the warps that expand share their instruction caches with the softmax and the
+// issuers, and four quarters unrolled took 750 cycles each, one 226 to 380, all with instruction fetches.
+__device__ inline void fp4_store32(const Fp4Place& to, uint32_t offset, uint4 c, uint32_t scales) {
   const bool large = (scales & 0xFFu) >= 0x88u || scales >= 0x8800u;
+  uint32_t at = to.at + offset;
   if (!__any_sync(0xffffffffu, large)) {
-    const uint32_t f0 = fp4_factor_small(scales, 0), f1 = fp4_factor_small(scales, 1);
-    st_shared_v4<OFFSET>(to.at[0] + slot, fp4_expand8_small(c.x, f0));
-    st_shared_v4<OFFSET>(to.at[1] + slot, fp4_expand8_small(c.y, f0));
-    st_shared_v4<OFFSET>(to.at[2] + slot, fp4_expand8_small(c.z, f1));
-    st_shared_v4<OFFSET>(to.at[3] + slot, fp4_expand8_small(c.w, f1));
+    uint32_t f = fp4_factor_small(scales, 0);
+#pragma unroll 1
+    for (int i = 0; i < 4; ++i) {
+      if (i == 2) f = fp4_factor_small(scales, 1);
+      st_shared_v4(at ^ (i << 4), fp4_expand8_small(c.x, f));
+      c.x = c.y;
+      c.y = c.z;
+      c.z = c.w;
+    }
   } else {
-    const uint32_t f0 = fp4_factor(scales & 0xFFu), f1 = fp4_factor(scales >> 8);
-    st_shared_v4<OFFSET>(to.at[0] + slot, fp4_expand8(c.x, f0));
-    st_shared_v4<OFFSET>(to.at[1] + slot, fp4_expand8(c.y, f0));
-    st_shared_v4<OFFSET>(to.at[2] + slot, fp4_expand8(c.z, f1));
-    st_shared_v4<OFFSET>(to.at[3] + slot, fp4_expand8(c.w, f1));
+#pragma unroll 1
+    for (int i = 0; i < 4; ++i) {
+      st_shared_v4(at ^ (i << 4), fp4_expand8(c.x, fp4_factor(i < 2 ? scales & 0xFFu : scales >> 8)));
+      c.x = c.y;
+      c.y = c.z;
+      c.z = c.w;
+    }
   }
+}
+
+// A tile's codes and scales as they come from the pages, `rows` rows: 128-byte pieces of the codes, one region behind the
+// other, each with the 128-byte swizzle (eight rows' quarters then lie in different banks), and 32 bytes of scales a row.
+__host__ __device__ inline int fp4_regions(int rank) { return (rank / 2 + 127) / 128; }
+__host__ __device__ inline int fp4_stage_bytes(int rank, int rows) { return rows * (128 * fp4_regions(rank) + 32); }
+
+// Quarter v of pair j of row r of a stage that begins at `stage`.
+__device__ inline void fp4_fetch(uint32_t stage, int rows, int regions, int r, int v, int j, uint4& c, uint32_t& scales) {
+  const uint32_t at = stage + (uint32_t)((j >> 1) * rows * 128 + r * 128 + ((((j & 1) * 4 + v) ^ (r & 7)) << 4));
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(c.x), "=r"(c.y), "=r"(c.z), "=r"(c.w) : "r"(at) : "memory");
+  uint16_t x;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(x) : "r"(stage + (uint32_t)(regions * rows * 128 + r * 32 + 8 * j + 2 * v)) : "memory");
+  scales = x;
 }
 
 __device__ inline uint32_t ldg_stream_u16(const void* p) {

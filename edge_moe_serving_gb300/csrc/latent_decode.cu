@@ -57,8 +57,11 @@ constexpr int kChunk = kTok * kBK * 2;   // 8 KB: 64 tokens x 64 entries (also 6
 constexpr int kMaxPairs = 4;             // 128-entry slices of the latent
 constexpr int kMaxSlots = 4;             // tiles in flight
 constexpr int kBatch = 512;              // sequences of one launch (lengths and tile sums in shared memory)
+constexpr int kBatch4 = 256;             // of one over a cache in 4 bits, whose codes need the room
 constexpr int kThreads = 224;            // a bf16 cache's; one in 4 bits has kExpandWarps more
-constexpr int kExpandWarps = 8;
+constexpr int kExpandWarps = 8;          // and one that copies their codes
+constexpr int kBufs = 8;                 // pairs of a cache in 4 bits that are expanded at once, at most
+constexpr int kStages = 2;               // tiles of codes in flight, and of rotary keys
 constexpr int kSoftThreads = 128;
 constexpr int kTmemCols = 512;
 constexpr int kSCol = 256;               // S tiles at columns 256 and 320; O slices at 0, 64, 128, 192
@@ -67,7 +70,7 @@ constexpr float kGrow = 8.0f;            // log2 of the growth of a row's maximu
 struct DecodeParams : LineShape {
   KvView kv;
   int layer, rope;
-  int pairs, slots;          // rank / 128; tiles in flight
+  int pairs, slots, bufs;    // rank / 128; tiles in flight; in 4 bits, pairs that are expanded at once
   float scale_log2;          // scale * log2(e): the exponentials are powers of two
   const int32_t* seqs;
   const int32_t* prefix_seq;
@@ -252,44 +255,63 @@ __device__ inline void store_matrices(uint32_t addr, uint32_t a, uint32_t b, uin
                : "memory");
 }
 
+template <int BATCH>
 struct alignas(16) Shared {   // its size is what the dynamic shared memory leaves free
-  uint64_t full[kMaxSlots][kMaxPairs + 1], empty[kMaxSlots][kMaxPairs + 1];   // per 128-entry pair, then the rotary chunk
+  // bf16: per 128-entry pair of a slot, then the rotary chunk.  In 4 bits, one behind the other: a ring of expanded pairs
+  // (kBufs), the rotary chunks and the stages of codes (kStages each).
+  uint64_t full[kMaxSlots][kMaxPairs + 1], empty[kMaxSlots][kMaxPairs + 1];
   uint64_t q_full, q_empty, s_full[2], s_empty[2], p_full[kPBars], pv_done[2], drain[2];
   uint32_t tmem;
   int abort;
   float factor[kRows];   // rescaling of each row; in the epilogue 1 / l
-  int warp_sum[kThreads / 32 + kExpandWarps];
+  int warp_sum[kThreads / 32 + kExpandWarps + 1];
   int sees[kSoftThreads / 32];
   unsigned long long bad[2];   // tokens of a tile (by its parity) with a NaN or infinite latent entry, bit by bit
-  int pref[kBatch + 1];
-  int len[kBatch];
-  int ids[kBatch];
+  int pref[BATCH + 1];
+  int len[BATCH];
+  int ids[BATCH];
 };
 
 template <bool FP4>
-__global__ void __launch_bounds__(kThreads + (FP4 ? 32 * kExpandWarps : 0), 1)
+constexpr int kAllThreads = kThreads + (FP4 ? 32 * (kExpandWarps + 1) : 0);
+
+template <bool FP4>
+__global__ void __launch_bounds__(kAllThreads<FP4>, 1)
 decode_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_constant__ CUtensorMap map_pair,
               const __grid_constant__ CUtensorMap map_qs, const __grid_constant__ CUtensorMap map_qsr,
               const __grid_constant__ CUtensorMap map_qp, const __grid_constant__ CUtensorMap map_qpr,
-              const DecodeParams p) {
+              const __grid_constant__ CUtensorMap map_scales, const DecodeParams p) {
   extern __shared__ uint8_t smem_raw[];
-  __shared__ Shared sh;
+  __shared__ Shared<FP4 ? kBatch4 : kBatch> sh;
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  constexpr int kAll = kThreads + (FP4 ? 32 * kExpandWarps : 0);
+  constexpr int kAll = kAllThreads<FP4>;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int chunks = 2 * p.pairs + 1;               // the last one holds the rotary part, then P
   uint8_t* skv = smem + chunks * kChunk;
   const int slot_bytes = chunks * kChunk;
+  // in 4 bits: expanded pairs, rotary chunks, stages of codes, and their barriers
+  uint8_t* srope = skv + (FP4 ? p.bufs * 2 * kChunk : 0);
+  uint8_t* sstage = srope + kStages * kChunk;
+  uint64_t *const full4 = &sh.full[0][0], *const empty4 = &sh.empty[0][0];
+  constexpr int kRopeBar = kBufs, kStageBar = kBufs + kStages;
+  static_assert(kStageBar + kStages <= kMaxSlots * (kMaxPairs + 1), "barriers");
   // A tile comes and goes in these parts: the value product lets go of one pair after the other, and the next tile's
   // copies follow at once (two parts a tile instead of five measured 13% to 20% slower on long sequences).
   const int parts = p.pairs + (p.rope ? 1 : 0);
 
   if (tid == 0) {
-    for (int s = 0; s < p.slots; ++s)
-      for (int j = 0; j <= p.pairs; ++j) {
-        mbar_init(&sh.full[s][j], FP4 && j < p.pairs ? kExpandWarps : 1);
-        mbar_init(&sh.empty[s][j], 1);
+    if (FP4) {
+      for (int i = 0; i < kStageBar + kStages; ++i) {
+        mbar_init(full4 + i, i < kRopeBar ? kExpandWarps : 1);
+        mbar_init(empty4 + i, i < kStageBar ? 1 : kExpandWarps);
       }
+    } else {
+      for (int s = 0; s < p.slots; ++s)
+        for (int j = 0; j <= p.pairs; ++j) {
+          mbar_init(&sh.full[s][j], 1);
+          mbar_init(&sh.empty[s][j], 1);
+        }
+    }
     mbar_init(&sh.q_full, 1);
     mbar_init(&sh.q_empty, 1);
     for (int i = 0; i < 2; ++i) {
@@ -305,7 +327,8 @@ decode_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_constant_
   }
   if (tid == 32 * 2) {
     prefetch_map(&map_kv);
-    if (!FP4) prefetch_map(&map_pair);
+    prefetch_map(&map_pair);
+    if (FP4) prefetch_map(&map_scales);
     prefetch_map(&map_qs);
     prefetch_map(&map_qsr);
   }
@@ -411,22 +434,35 @@ decode_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_constant_
         int rows[kTok / 16];
 #pragma unroll
         for (int i = 0; i < kTok / 16; ++i) rows[i] = (int)uni(lane == i ? row : 0);
-        const uint32_t dst = kv0 + slot * slot_bytes, bar = full0 + slot * (uint32_t)sizeof(sh.full[0]);
-        for (int j = FP4 ? p.pairs : 0; j < parts; ++j) {    // in 4 bits: the rotary key alone
-          ok = warp_wait(&sh.empty[slot][j], par, abort_flag);
-          if (!ok) break;
-          const bool pair = !FP4 && j < p.pairs;
-          const uint32_t to = dst + 2 * j * kChunk, fb = bar + 8 * j;
-          mbar_expect_tx_warp(fb, (uint32_t)(nb * box * (pair ? 256 : 128)));
-          if (box == kTok && pair) {   // both chunks of the pair in one copy
-            tma_load_3d_hint_warp(to, &map_pair, fb, 0, rows[0], 2 * j, pol);
-          } else {
+        if (FP4) {                   // the rotary keys alone
+          if (p.rope) {
+            ok = warp_wait(empty4 + kRopeBar + slot, par, abort_flag);
+            if (ok) {
+              const uint32_t to = uni(smem_u32(srope)) + slot * kChunk, fb = full0 + 8 * (kRopeBar + slot);
+              mbar_expect_tx_warp(fb, (uint32_t)(nb * box * 128));
 #pragma unroll
-            for (int i = 0; i < kTok / 16; ++i)
-              if (i < nb) {
-                tma_load_2d_hint_warp(to + i * box * 128, &map_kv, fb, FP4 ? p.kv.rope_at : 2 * j * kBK, rows[i], pol);
-                if (pair) tma_load_2d_hint_warp(to + kChunk + i * box * 128, &map_kv, fb, 2 * j * kBK + kBK, rows[i], pol);
-              }
+              for (int i = 0; i < kTok / 16; ++i)
+                if (i < nb) tma_load_2d_hint_warp(to + i * box * 128, &map_kv, fb, p.kv.rope_at, rows[i], pol);
+            }
+          }
+        } else {
+          const uint32_t dst = kv0 + slot * slot_bytes, bar = full0 + slot * (uint32_t)sizeof(sh.full[0]);
+          for (int j = 0; j < parts; ++j) {
+            ok = warp_wait(&sh.empty[slot][j], par, abort_flag);
+            if (!ok) break;
+            const bool pair = j < p.pairs;
+            const uint32_t to = dst + 2 * j * kChunk, fb = bar + 8 * j;
+            mbar_expect_tx_warp(fb, (uint32_t)(nb * box * (pair ? 256 : 128)));
+            if (box == kTok && pair) {   // both chunks of the pair in one copy
+              tma_load_3d_hint_warp(to, &map_pair, fb, 0, rows[0], 2 * j, pol);
+            } else {
+#pragma unroll
+              for (int i = 0; i < kTok / 16; ++i)
+                if (i < nb) {
+                  tma_load_2d_hint_warp(to + i * box * 128, &map_kv, fb, 2 * j * kBK, rows[i], pol);
+                  if (pair) tma_load_2d_hint_warp(to + kChunk + i * box * 128, &map_kv, fb, 2 * j * kBK + kBK, rows[i], pol);
+                }
+            }
           }
         }
         if (ok && t0 == tok0 && !q_first) ok = load_q();
@@ -444,8 +480,12 @@ decode_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_constant_
     if (nseg) mbar_wait(&sh.q_full, (nseg - 1) & 1, &no_abort);
     for (int s = 0; s < p.slots; ++s) {
       const int loads = tile / p.slots + (tile % p.slots > s ? 1 : 0);
-      for (int j = FP4 ? p.pairs : 0; j < parts; ++j)
-        if (loads > 0) mbar_wait(&sh.full[s][j], (loads - 1) & 1, &no_abort);
+      if (FP4) {
+        if (loads > 0 && p.rope) mbar_wait(full4 + kRopeBar + s, (loads - 1) & 1, &no_abort);
+      } else {
+        for (int j = 0; j < parts; ++j)
+          if (loads > 0) mbar_wait(&sh.full[s][j], (loads - 1) & 1, &no_abort);
+      }
     }
     __syncwarp();
   } else if (warp == 1) {
@@ -456,7 +496,9 @@ decode_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_constant_
     bool issued = false, ok = true;
     constexpr uint32_t idesc_s = make_idesc(64, kTok);
     const uint32_t tm = uni(tmem), smem0 = uni(smem_u32(smem));
-    const uint64_t dq0 = smem_desc(smem0), dk0 = smem_desc(smem0 + chunks * kChunk);
+    const uint64_t dq0 = smem_desc(smem0), dk0 = smem_desc(smem0 + chunks * kChunk), dr0 = smem_desc(uni(smem_u32(srope)));
+    int buf4 = 0;
+    uint32_t par4 = 0;
     while (__any_sync(0xffffffffu, ok && it.next(sg))) {
       ok = warp_wait(&sh.q_full, nseg & 1, abort_flag);
       const int n_tiles = (int)uni((sg.tok1 - sg.tok0 + kTok - 1) / kTok);
@@ -468,9 +510,16 @@ decode_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_constant_
         uint64_t dq = dq0, dk = dk0 + ((uint64_t)(slot * slot_bytes) >> 4);
         const uint32_t d = tm + kSCol + buf * kTok;
         for (int j = 0; j < p.pairs; ++j) {
-          ok = warp_wait(&sh.full[slot][j], par, abort_flag);
+          ok = warp_wait(FP4 ? full4 + buf4 : &sh.full[slot][j], FP4 ? par4 : par, abort_flag);
           if (!ok) break;
-          if (FP4) proxy_fence();          // the expanded entries, for the products
+          if (FP4) {
+            proxy_fence();                 // the expanded entries, for the products
+            dk = dk0 + ((uint64_t)(buf4 * 2 * kChunk) >> 4);
+            if (++buf4 == p.bufs) {
+              buf4 = 0;
+              par4 ^= 1u;
+            }
+          }
           tc_fence_after();
 #pragma unroll
           for (int k = 0; k < 8; ++k)
@@ -481,8 +530,9 @@ decode_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_constant_
           dk += (2 * kChunk) >> 4;
         }
         if (ok && p.rope) {
-          ok = warp_wait(&sh.full[slot][p.pairs], par, abort_flag);
+          ok = warp_wait(FP4 ? full4 + kRopeBar + slot : &sh.full[slot][p.pairs], par, abort_flag);
           if (ok) {
+            if (FP4) dk = dr0 + ((uint64_t)(slot * kChunk) >> 4);
             tc_fence_after();
 #pragma unroll
             for (int k = 0; k < 4; ++k)
@@ -511,7 +561,8 @@ decode_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_constant_
     bool issued = false, ok = true;
     const uint32_t tm = uni(tmem), smem0 = uni(smem_u32(smem));
     const uint64_t dv0 = smem_desc_mn(smem0 + chunks * kChunk, kChunk);
-    const uint64_t dp0 = smem_desc(smem0 + chunks * kChunk) + (uint64_t)((2 * p.pairs * kChunk) >> 4);
+    const uint64_t dp0 = FP4 ? smem_desc(uni(smem_u32(srope))) : smem_desc(smem0 + chunks * kChunk) + (uint64_t)((2 * p.pairs * kChunk) >> 4);
+    int buf4 = 0;
     while (__any_sync(0xffffffffu, ok && it.next(sg))) {
       const int n_tiles = (int)uni((sg.tok1 - sg.tok0 + kTok - 1) / kTok);
       const uint32_t idesc = make_idesc(128, (int)uni(sg.N)) | kTransA;
@@ -519,18 +570,20 @@ decode_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_constant_
         ok = warp_wait(&sh.p_full[p_bar(tile)], p_phase(tile), abort_flag);   // P is written, so S has read the whole tile
         if (!ok) break;
         tc_fence_after();
-        const uint64_t step = (uint64_t)(slot * slot_bytes) >> 4;
+        const uint64_t step = (uint64_t)(slot * (FP4 ? kChunk : slot_bytes)) >> 4;
         uint64_t dv = dv0 + step;
         const uint64_t dp = dp0 + step;
         for (int j = 0; j < p.pairs; ++j) {
+          if (FP4) dv = dv0 + ((uint64_t)(buf4 * 2 * kChunk) >> 4);
 #pragma unroll
           for (int k = 0; k < kTok / kUK; ++k)
             tc_mma_warp(tm + j * kRows, dv + ((k * kUK * 128) >> 4), dp + ((k * kUK * 2) >> 4), idesc,
                         k ? 1u : (i ? 1u : 0u));
-          tc_commit_warp(&sh.empty[slot][j]);
+          tc_commit_warp(FP4 ? empty4 + buf4 : &sh.empty[slot][j]);
           dv += (2 * kChunk) >> 4;
+          if (FP4 && ++buf4 == p.bufs) buf4 = 0;
         }
-        if (p.rope) tc_commit_warp(&sh.empty[slot][p.pairs]);
+        if (p.rope) tc_commit_warp(FP4 ? empty4 + kRopeBar + slot : &sh.empty[slot][p.pairs]);
         tc_commit_warp(&sh.pv_done[tile & 1]);
         issued = true;
         if (++slot == p.slots) slot = 0;
@@ -542,84 +595,99 @@ decode_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_constant_
       mbar_wait(&sh.drain[1], 0, &no_abort);
     }
     __syncwarp();
-  } else if (FP4 && warp >= kThreads / 32) {
-    // ------------------------------------------------ latents in 4 bits, expanded into the tile that a copy would fill
-    // Four threads a token; of each 128-entry pair a thread has 16 bytes of codes, a quarter.  Codes are asked for a tile
-    // ahead, as soon as their registers are free, and pages two tiles ahead.  Places past a piece's last token get some
-    // row's entries, which the softmax warps hide and clear.  The fence between these writes and the products is the
-    // products' issuers': here it would wait for the loads in flight.
-    const int r = (warp - kThreads / 32) * 8 + (lane & 7), v = lane >> 3;
-    const int scales_at = p.kv.rank / 2 + 2 * p.rope;
-    const Fp4Place to(smem_u32(skv), kChunk, r, v);
-    const bool pseq_ok = p.np == 0 || (*p.prefix_seq >= 0 && *p.prefix_seq < p.kv.max_seqs);
-    int t0 = 0, t1 = 0;            // where the look-up stands in its piece
-    auto next_tile = [&]() {
-      t0 += kTok;
-      if (t0 < t1) return true;
-      if (!it.next(sg)) return false;
-      t0 = sg.tok0;
-      t1 = sg.tok1;
-      return true;
-    };
-    const uint8_t* row;
-    int page, at;                  // of the tile after the next
-    auto look_up = [&](bool any) {
-      const int t = t0 + r;
-      page = at = 0;
-      if (any && t < t1) {
-        const bool seq_ok = !sg.prefix || pseq_ok;
-        page = seq_ok ? __ldg(p.kv.table + (size_t)sg.seq * p.kv.max_blocks + (t >> p.kv.page_shift)) : INT_MIN;
-        at = t & (p.kv.page_tokens - 1);
-      }
-    };
-    auto locate = [&]() {
-      if (page < 0 || page >= p.kv.n_pages) {
-        set_status(p.status, page == INT_MIN ? MOE_DEV_ERR_BAD_SEQ : MOE_DEV_ERR_BAD_PAGE);
-        page = 0;
-      }
-      row = reinterpret_cast<const uint8_t*>(p.kv.pages + p.kv.row_offset(p.layer, page, at)) + 16 * v;
-    };
-    uint4 code[kMaxPairs];
-    uint32_t scale[kMaxPairs];
-    auto load = [&](int j) {
-      code[j] = ldg_stream(row + 64 * j);
-      scale[j] = ldg_stream_u16(row + scales_at + 8 * j - 14 * v);
-    };
-    bool now = next_tile(), ok = true;
-    look_up(now);
-    locate();
-#pragma unroll
-    for (int j = 0; j < kMaxPairs; ++j)
-      if (j < p.pairs) load(j);
-    bool next = now && next_tile();
-    look_up(next);
-    locate();
-    int slot = 0;
+  } else if (FP4 && warp == kThreads / 32 + kExpandWarps) {
+    // ------------------------------------------------ copies of codes and scales, as they are
+    int tile = 0, stage = 0;
     uint32_t par = 1;
-    while (ok && now) {
-      const bool after = next && next_tile();
-      look_up(after);
-      const uint32_t here = slot * slot_bytes;
-      auto expand = [&](auto J) {
-        constexpr int j = decltype(J)::value;
-        if (j >= p.pairs) return;
-        ok = ok && warp_wait(&sh.empty[slot][j], par, abort_flag);
-        if (!ok) return;
-        fp4_store32<2 * j * kChunk>(to, here, code[j], scale[j]);
-        load(j);
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.full[slot][j]);
-      };
-      expand(std::integral_constant<int, 0>{});
-      expand(std::integral_constant<int, 1>{});
-      expand(std::integral_constant<int, 2>{});
-      expand(std::integral_constant<int, 3>{});
-      now = next;
-      next = after;
-      locate();
-      if (++slot == p.slots) {
-        slot = 0;
-        par ^= 1u;
+    bool ok = true;
+    const int page = p.kv.page_tokens, box = min(page, kTok), layer_page = p.layer * p.kv.n_pages;
+    const int regions = fp4_regions(p.kv.rank), bytes = fp4_stage_bytes(p.kv.rank, kTok);
+    const uint32_t stage0 = uni(smem_u32(sstage)), bar0 = uni(smem_u32(full4 + kStageBar));
+    const bool pseq_ok = p.np == 0 || (*p.prefix_seq >= 0 && *p.prefix_seq < p.kv.max_seqs);
+    const uint64_t once = l2_evict_first(), shared = l2_normal();
+    while (__any_sync(0xffffffffu, ok && it.next(sg))) {
+      const bool seq_ok = !sg.prefix || pseq_ok;
+      const uint64_t pol = sg.prefix || p.G > 1 ? shared : once;
+      const int32_t* blocks = p.kv.table + (seq_ok ? (size_t)sg.seq * p.kv.max_blocks : 0);
+      const int tok0 = (int)uni(sg.tok0), tok1 = (int)uni(sg.tok1);
+      auto block = [&](int t) { return seq_ok && lane < kTok / box && t < tok1 ? blocks[t >> p.kv.page_shift] : -1; };
+      int ahead = block(tok0 + lane * box);
+      for (int t0 = tok0; ok && t0 < tok1; t0 += kTok) {
+        const int nb = (min(kTok, tok1 - t0) + box - 1) / box;       // boxes that hold tokens
+        const int t = t0 + lane * box;
+        int row = ahead;
+        if (lane < nb) {
+          if (row < 0 || row >= p.kv.n_pages) {
+            set_status(p.status, seq_ok ? MOE_DEV_ERR_BAD_PAGE : MOE_DEV_ERR_BAD_SEQ);
+            row = 0;
+          }
+          row = (layer_page + row) * page + (t & (page - 1));
+        } else {
+          row = 0;
+        }
+        ahead = block(t + kTok);
+        ok = warp_wait(empty4 + kStageBar + stage, par, abort_flag);
+        if (!ok) break;
+        const uint32_t to = stage0 + stage * bytes, bar = bar0 + 8 * stage;
+        mbar_expect_tx_warp(bar, (uint32_t)(nb * box * (128 * regions + 32)));
+#pragma unroll 1
+        for (int i = 0; i < nb; ++i) {
+          const int r = (int)uni(__shfl_sync(0xffffffffu, row, i));
+#pragma unroll 1
+          for (int g = 0; g < regions; ++g)
+            tma_load_2d_hint_warp(to + g * kTok * 128 + i * box * 128, &map_pair, bar, 128 * g, r, pol);
+          tma_load_2d_hint_warp(to + regions * kTok * 128 + i * box * 32, &map_scales, bar, p.kv.rank / 2 + 2 * p.rope, r, pol);
+        }
+        ++tile;
+        if (++stage == kStages) {
+          stage = 0;
+          par ^= 1u;
+        }
+      }
+    }
+    volatile int no_abort = 0;
+    for (int s = 0; s < kStages; ++s) {
+      const int loads = tile / kStages + (tile % kStages > s ? 1 : 0);
+      if (loads > 0) mbar_wait(full4 + kStageBar + s, (loads - 1) & 1, &no_abort);
+    }
+    __syncwarp();
+  } else if (FP4 && warp >= kThreads / 32) {
+    // ------------------------------------------------ latents in 4 bits, expanded into the pairs that a copy would fill
+    // Four threads a token; of each 128-entry pair a thread has 16 bytes of codes, a quarter.  Places past a piece's last
+    // token get whatever the stage holds, which the softmax warps hide and clear.
+    const int r = (warp - kThreads / 32) * 8 + (lane & 7), v = lane >> 3;
+    const int regions = fp4_regions(p.kv.rank), bytes = fp4_stage_bytes(p.kv.rank, kTok);
+    const Fp4Place to(smem_u32(skv), kChunk, r, v);
+    const uint32_t stage0 = smem_u32(sstage);
+    int stage = 0, buf = 0;
+    uint32_t par_s = 0, par = 1;
+    bool ok = true;
+    while (__any_sync(0xffffffffu, ok && it.next(sg))) {
+      const int n_tiles = (sg.tok1 - sg.tok0 + kTok - 1) / kTok;
+      for (int i = 0; ok && i < n_tiles; ++i) {
+        ok = warp_wait(full4 + kStageBar + stage, par_s, abort_flag);
+#pragma unroll 1
+        for (int j = 0; ok && j < p.pairs; ++j) {
+          uint4 c;
+          uint32_t scales;
+          fp4_fetch(stage0 + stage * bytes, kTok, regions, r, v, j, c, scales);
+          ok = warp_wait(empty4 + buf, par, abort_flag);
+          if (!ok) break;
+          fp4_store32(to, buf * 2 * kChunk, c, scales);
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(full4 + buf);
+            if (j == p.pairs - 1) mbar_arrive(empty4 + kStageBar + stage);
+          }
+          if (++buf == p.bufs) {
+            buf = 0;
+            par ^= 1u;
+          }
+        }
+        if (++stage == kStages) {
+          stage = 0;
+          par_s ^= 1u;
+        }
       }
     }
     __syncwarp();
@@ -665,6 +733,8 @@ decode_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_constant_
       sees_all = min(sees_all, sg.tok1);
       for (int t0 = sg.tok0; t0 < sg.tok1; t0 += kTok, ++tile) {
         const int buf = tile & 1, slot = tile % p.slots;
+        // where the tile's pair j lies
+        auto pair_at = [&](int j) { return skv + (FP4 ? (tile * p.pairs + j) % p.bufs * 2 * kChunk : slot * slot_bytes + 2 * j * kChunk); };
         const int n_tok = min(kTok, sg.tok1 - t0);
         // The product of two tiles ago is long over; waiting for each in turn keeps its barrier's phase unambiguous.
         const bool ok = (tile < 2 || warp_wait(&sh.pv_done[buf], ((tile - 2) >> 1) & 1, abort_flag)) &&
@@ -698,14 +768,17 @@ decode_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_constant_
           // its score: the value may have made that -infinity, whose product with the value is NaN as well.
           unsigned long long bad = 0;
           if (ok) {
-            for (int j = 0; j < p.pairs; ++j) mbar_wait(&sh.full[slot][j], (tile / p.slots) & 1, abort_flag);   // long over
-            uint4* base = reinterpret_cast<uint4*>(skv + slot * slot_bytes);
-            for (int x = st; x < p.pairs * (2 * kChunk / 16); x += kSoftThreads) {
-              const uint4 v = base[x];
-              const uint4 f = make_uint4(finite_bf16x2(v.x), finite_bf16x2(v.y), finite_bf16x2(v.z), finite_bf16x2(v.w));
-              if (((v.x ^ f.x) | (v.y ^ f.y) | (v.z ^ f.z) | (v.w ^ f.w)) != 0) {
-                base[x] = f;
-                bad |= 1ull << ((x & (kChunk / 16 - 1)) >> 3);   // a token's row is 128 bytes of a chunk
+            for (int j = 0; j < p.pairs; ++j) {
+              if (FP4) mbar_wait(full4 + (tile * p.pairs + j) % p.bufs, (tile * p.pairs + j) / p.bufs & 1, abort_flag);
+              else mbar_wait(&sh.full[slot][j], (tile / p.slots) & 1, abort_flag);   // long over
+              uint4* base = reinterpret_cast<uint4*>(pair_at(j));
+              for (int x = st; x < 2 * kChunk / 16; x += kSoftThreads) {
+                const uint4 v = base[x];
+                const uint4 f = make_uint4(finite_bf16x2(v.x), finite_bf16x2(v.y), finite_bf16x2(v.z), finite_bf16x2(v.w));
+                if (((v.x ^ f.x) | (v.y ^ f.y) | (v.z ^ f.z) | (v.w ^ f.w)) != 0) {
+                  base[x] = f;
+                  bad |= 1ull << ((x & (kChunk / 16 - 1)) >> 3);   // a token's row is 128 bytes of a chunk
+                }
               }
             }
             if (bad) atomicOr(&sh.bad[buf], bad);
@@ -767,7 +840,7 @@ decode_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_constant_
         // Probabilities, rounded to bf16 (the cache's type, the only one the product takes beside it).  Their sum is of
         // the rounded ones: the output is divided by it, so its weights add up to one, and where few tokens carry the
         // row most of their rounding cancels.  The log-sum-exp wants the sum of the unrounded ones too.
-        const uint32_t sp = smem_u32(skv + slot * slot_bytes + 2 * p.pairs * kChunk) + p_row;
+        const uint32_t sp = smem_u32(FP4 ? srope + slot * kChunk : skv + slot * slot_bytes + 2 * p.pairs * kChunk) + p_row;
         auto probabilities = [&](auto with_lse) {
           if (quarter * 16 >= sg.N) return;
 #pragma unroll
@@ -795,12 +868,12 @@ decode_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_constant_
         else probabilities(std::false_type{});
         if (n_tok < kTok) {
           // places past the last token: any bits may stand there, and 0 * NaN is NaN
-          uint8_t* base = skv + slot * slot_bytes;
           const int rows = kTok - n_tok;
-          for (int x = st; x < rows * 8 * 2 * p.pairs; x += kSoftThreads) {
-            const int c = x / (rows * 8), y = x - c * rows * 8;
-            *reinterpret_cast<uint4*>(base + c * kChunk + n_tok * 128 + y * 16) = make_uint4(0, 0, 0, 0);
-          }
+          for (int j = 0; j < p.pairs; ++j)
+            for (int x = st; x < rows * 16; x += kSoftThreads) {
+              const int c = x >= rows * 8, y = x - c * rows * 8;
+              *reinterpret_cast<uint4*>(pair_at(j) + c * kChunk + n_tok * 128 + y * 16) = make_uint4(0, 0, 0, 0);
+            }
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         if (soft_any(grow)) {      // rare: some row's maximum rose by more than 2^8 (or a wait ran out)
@@ -1096,37 +1169,54 @@ bool decode_shape_ok(int B, int Q, int heads) { return B <= 4096 && (long long)Q
 template <bool FP4>
 cudaError_t launch_decode_kernel(const DecodeParams& p, int smem, cudaStream_t s, const CUtensorMap& kv, const CUtensorMap& pair,
                                  const CUtensorMap& qs, const CUtensorMap& qsr, const CUtensorMap& qp,
-                                 const CUtensorMap& qpr) {
+                                 const CUtensorMap& qpr, const CUtensorMap& scales) {
   static std::atomic<unsigned char> attr[kMaxDevices];
   const cudaError_t e = once_per_device(attr, [] {
     return cudaFuncSetAttribute(decode_kernel<FP4>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                227 * 1024 - (int)sizeof(Shared));
+                                227 * 1024 - (int)sizeof(Shared<FP4 ? kBatch4 : kBatch>));
   });
-  constexpr int threads = kThreads + (FP4 ? 32 * kExpandWarps : 0);
-  return e == cudaSuccess ? launch_k(decode_kernel<FP4>, p.ctas, threads, smem, s, kv, pair, qs, qsr, qp, qpr, p) : e;
+  return e == cudaSuccess
+             ? launch_k(decode_kernel<FP4>, p.ctas, kAllThreads<FP4>, smem, s, kv, pair, qs, qsr, qp, qpr, scales, p)
+             : e;
 }
 
 int launch_decode(const moe_kv_cache& c, DecodeParams p, const void* q, cudaStream_t s) {
-  static_assert(sizeof(Shared) + 1024 + (2 * kMaxPairs + 1) * kChunk * 3 <= 227 * 1024, "shared memory");
-  const int row = c.rank + c.rope, slot = (2 * p.pairs + 1) * kChunk;
-  p.slots = (int)((227 * 1024 - sizeof(Shared) - 1024 - slot) / slot);   // what the query tile leaves
-  if (p.slots > kMaxSlots) p.slots = kMaxSlots;
-  const int smem = (1 + p.slots) * slot + 1024;
-  CUtensorMap kv, pair, qs, qsr, qp, qpr;   // cache rows by chunk and by pair; query tiles of sequences and of the prefix
-  const uint64_t rows = (uint64_t)c.n_layers * c.n_pages * c.page_tokens, qrows = (uint64_t)p.B * p.Q * p.heads;
+  static_assert(sizeof(Shared<kBatch>) + 1024 + (2 * kMaxPairs + 1) * kChunk * 3 <= 227 * 1024, "shared memory");
+  static_assert(sizeof(Shared<kBatch4>) + 1024 + (2 * kMaxPairs + 1) * kChunk + kStages * (kChunk + kTok * (256 + 32)) +
+                        (kMaxPairs + 1) * 2 * kChunk <= 227 * 1024, "more pairs than a tile has");
   const bool fp4 = c.format == MOE_KV_FP4;
-  if (!make_map(&kv, c.pages, p.kv.row, rows, c.page_tokens < kTok ? c.page_tokens : kTok) ||
-      (!fp4 && !make_map_chunks(&pair, c.pages, row, rows, kTok, 2)) || !make_map_chunks(&qs, q, row, qrows, p.NR, 2 * p.pairs) ||
+  const int row = c.rank + c.rope, slot = (2 * p.pairs + 1) * kChunk;
+  int smem;
+  if (fp4) {
+    const int rest = slot + kStages * (kChunk + fp4_stage_bytes(c.rank, kTok)) + 1024;
+    p.slots = kStages;
+    p.bufs = (int)((227 * 1024 - sizeof(Shared<kBatch4>) - rest) / (2 * kChunk));
+    if (p.bufs > 2 * p.pairs) p.bufs = 2 * p.pairs;
+    smem = rest + p.bufs * 2 * kChunk;
+  } else {
+    p.slots = (int)((227 * 1024 - sizeof(Shared<kBatch>) - 1024 - slot) / slot);   // what the query tile leaves
+    if (p.slots > kMaxSlots) p.slots = kMaxSlots;
+    smem = (1 + p.slots) * slot + 1024;
+  }
+  // cache rows by chunk and by pair (in 4 bits: rotary keys, codes and scales); query tiles of sequences and of the prefix
+  CUtensorMap kv, pair, qs, qsr, qp, qpr, scales;
+  const uint64_t rows = (uint64_t)c.n_layers * c.n_pages * c.page_tokens, qrows = (uint64_t)p.B * p.Q * p.heads;
+  const uint32_t box = c.page_tokens < kTok ? c.page_tokens : kTok;
+  if (!make_map(&kv, c.pages, p.kv.row, rows, box) || !make_map_chunks(&qs, q, row, qrows, p.NR, 2 * p.pairs) ||
       !make_map(&qsr, q, row, qrows, p.NR))
     return MOE_ERR_CUDA;
-  if (fp4) pair = kv;
+  if (fp4 ? !make_map_bytes(&pair, c.pages, 2 * p.kv.row, rows, 128, box, true) ||
+                !make_map_bytes(&scales, c.pages, 2 * p.kv.row, rows, 32, box, false)
+          : !make_map_chunks(&pair, c.pages, row, rows, kTok, 2))
+    return MOE_ERR_CUDA;
+  if (!fp4) scales = kv;
   qp = qs;
   qpr = qsr;
   if (p.np && p.NRp != p.NR &&
       (!make_map_chunks(&qp, q, row, qrows, p.NRp, 2 * p.pairs) || !make_map(&qpr, q, row, qrows, p.NRp)))
     return MOE_ERR_CUDA;
-  cudaError_t e = fp4 ? launch_decode_kernel<true>(p, smem, s, kv, pair, qs, qsr, qp, qpr)
-                      : launch_decode_kernel<false>(p, smem, s, kv, pair, qs, qsr, qp, qpr);
+  cudaError_t e = fp4 ? launch_decode_kernel<true>(p, smem, s, kv, pair, qs, qsr, qp, qpr, scales)
+                      : launch_decode_kernel<false>(p, smem, s, kv, pair, qs, qsr, qp, qpr, scales);
   // a CTA a row while the rows alone do not fill the SMs (then a row has many pieces), else a warp a row: whole calls over
   // 1200 tokens a sequence, us, CTA / warp: 128 rows 13.5 / 16.5, 160 rows 16.2 / 16.5, 288 rows 17.6 / 16.5, 1216 rows
   // 37.6 / 24.7
@@ -1166,9 +1256,10 @@ int moe_latent_decode(const moe_kv_cache* cache, int layer, const void* q, const
   if (!kv_aligned(q, 16) || !kv_aligned(out, 16)) return MOE_ERR_UNSUPPORTED;
   st = check_ws(ws, ws_bytes, moe_latent_decode_workspace_size(cache, B, Q, heads, shared_tokens));
   if (st != MOE_OK) return st;
-  for (int b0 = 0; b0 < B && st == MOE_OK; b0 += kBatch) {   // batches of more than 512 sequences: several launches
+  const int batch = cache->format == MOE_KV_FP4 ? kBatch4 : kBatch;
+  for (int b0 = 0; b0 < B && st == MOE_OK; b0 += batch) {   // larger batches: several launches
     DecodeParams p = {};
-    fill_shape(p, *cache, B - b0 < kBatch ? B - b0 : kBatch, Q, heads, shared_tokens);
+    fill_shape(p, *cache, B - b0 < batch ? B - b0 : batch, Q, heads, shared_tokens);
     const DecodeWs w = decode_ws(p, cache->rank);
     char* base = reinterpret_cast<char*>(ws);
     const size_t row0 = (size_t)b0 * Q * heads;

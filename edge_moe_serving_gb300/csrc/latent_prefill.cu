@@ -504,7 +504,7 @@ expand_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
         }
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          fp4_store32<0>(Fp4Place(smem_u32(smem) + c * kChunkBytes, kChunkBytes, r0 + 32 * e, v), 0, code[e], scale[e]);
+          fp4_store32(Fp4Place(smem_u32(smem) + c * kChunkBytes, kChunkBytes, r0 + 32 * e, v), 0, code[e], scale[e]);
         proxy_fence();
         __syncwarp();
         if (lane == 0) {

@@ -445,8 +445,8 @@ weights_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
         if (j >= pairs) return;
         ok = ok && warp_wait(&sh.k_empty[j], (tile & 1) ^ 1u, abort_flag);
         if (!ok) return;
-        fp4_store32<2 * j * kChunkBytes>(to[0], 0, code[0][j], scale[0][j]);
-        fp4_store32<2 * j * kChunkBytes>(to[1], 0, code[1][j], scale[1][j]);
+        fp4_store32(to[0], 2 * j * kChunkBytes, code[0][j], scale[0][j]);
+        fp4_store32(to[1], 2 * j * kChunkBytes, code[1][j], scale[1][j]);
         load(j);
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.k_full[j]);
