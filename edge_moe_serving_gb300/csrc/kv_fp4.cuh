@@ -58,9 +58,9 @@ __device__ inline uint4 fp4_expand8_small(uint32_t w, uint32_t factor) {
   }
   return make_uint4(o[0], o[1], o[2], o[3]);
 }
-__device__ inline uint32_t fp4_factor_small(uint32_t scales, int which) {      // of the two scales in a 16-bit word
+__device__ inline uint32_t fp4_factor_small(uint32_t scales) {      // of the low byte
   uint32_t b, f;
-  asm("prmt.b32 %0, %1, 0, %2;" : "=r"(b) : "r"(scales), "r"(which ? 0x4141u : 0x4040u));   // the byte in both halves
+  asm("prmt.b32 %0, %1, 0, %2;" : "=r"(b) : "r"(scales), "r"(0x4040u));                      // the byte in both halves
   asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(f) : "r"(b << 4), "r"(0x7B007B00u));                // 2^119, twice: from 2^-112
   asm("mul.rn.bf16x2 %0, %0, %1;" : "+r"(f) : "r"(0x7B007B00u));
   return f;
@@ -81,20 +81,21 @@ __device__ inline void st_shared_v4(uint32_t at, const uint4& v) {
 
 // The quarter's entries to `to`, `offset` bytes on (a whole warp at once): with one product where all of the warp's scales
 // are below 4 (a block whose largest entry is 24, far above a normalised latent), else with two, which also know a scale
-// that is NaN.  A word at a time, rolled: the warps that expand share their instruction caches with the softmax and the
+// that is NaN.  Two words at a time, rolled: the warps that expand share their instruction caches with the softmax and the
 // issuers, and four quarters unrolled took 750 cycles each, one 226 to 380, all with instruction fetches.
 __device__ inline void fp4_store32(const Fp4Place& to, uint32_t offset, uint4 c, uint32_t scales) {
   const bool large = (scales & 0xFFu) >= 0x88u || scales >= 0x8800u;
   uint32_t at = to.at + offset;
   if (!__any_sync(0xffffffffu, large)) {
-    uint32_t f = fp4_factor_small(scales, 0);
 #pragma unroll 1
-    for (int i = 0; i < 4; ++i) {
-      if (i == 2) f = fp4_factor_small(scales, 1);
-      st_shared_v4(at ^ (i << 4), fp4_expand8_small(c.x, f));
-      c.x = c.y;
-      c.y = c.z;
-      c.z = c.w;
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t f = fp4_factor_small(scales);
+      st_shared_v4(at, fp4_expand8_small(c.x, f));
+      st_shared_v4(at ^ 16, fp4_expand8_small(c.y, f));
+      c.x = c.z;
+      c.y = c.w;
+      scales >>= 8;
+      at ^= 32;
     }
   } else {
 #pragma unroll 1

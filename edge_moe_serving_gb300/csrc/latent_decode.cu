@@ -57,11 +57,10 @@ constexpr int kChunk = kTok * kBK * 2;   // 8 KB: 64 tokens x 64 entries (also 6
 constexpr int kMaxPairs = 4;             // 128-entry slices of the latent
 constexpr int kMaxSlots = 4;             // tiles in flight
 constexpr int kBatch = 512;              // sequences of one launch (lengths and tile sums in shared memory)
-constexpr int kBatch4 = 256;             // of one over a cache in 4 bits, whose codes need the room
 constexpr int kThreads = 224;            // a bf16 cache's; one in 4 bits has kExpandWarps more
 constexpr int kExpandWarps = 8;          // and one that copies their codes
 constexpr int kBufs = 8;                 // pairs of a cache in 4 bits that are expanded at once, at most
-constexpr int kStages = 2;               // tiles of codes in flight, and of rotary keys
+constexpr int kStages = 2;               // tiles of rotary keys in flight there (of codes one: its readers hold the one before)
 constexpr int kSoftThreads = 128;
 constexpr int kTmemCols = 512;
 constexpr int kSCol = 256;               // S tiles at columns 256 and 320; O slices at 0, 64, 128, 192
@@ -71,6 +70,7 @@ struct DecodeParams : LineShape {
   KvView kv;
   int layer, rope;
   int pairs, slots, bufs;    // rank / 128; tiles in flight; in 4 bits, pairs that are expanded at once
+  int q_bytes;               // in 4 bits: room of a tile's queries
   float scale_log2;          // scale * log2(e): the exponentials are powers of two
   const int32_t* seqs;
   const int32_t* prefix_seq;
@@ -255,10 +255,9 @@ __device__ inline void store_matrices(uint32_t addr, uint32_t a, uint32_t b, uin
                : "memory");
 }
 
-template <int BATCH>
 struct alignas(16) Shared {   // its size is what the dynamic shared memory leaves free
   // bf16: per 128-entry pair of a slot, then the rotary chunk.  In 4 bits, one behind the other: a ring of expanded pairs
-  // (kBufs), the rotary chunks and the stages of codes (kStages each).
+  // (kBufs), the rotary chunks (kStages), the stage of codes.
   uint64_t full[kMaxSlots][kMaxPairs + 1], empty[kMaxSlots][kMaxPairs + 1];
   uint64_t q_full, q_empty, s_full[2], s_empty[2], p_full[kPBars], pv_done[2], drain[2];
   uint32_t tmem;
@@ -267,9 +266,9 @@ struct alignas(16) Shared {   // its size is what the dynamic shared memory leav
   int warp_sum[kThreads / 32 + kExpandWarps + 1];
   int sees[kSoftThreads / 32];
   unsigned long long bad[2];   // tokens of a tile (by its parity) with a NaN or infinite latent entry, bit by bit
-  int pref[BATCH + 1];
-  int len[BATCH];
-  int ids[BATCH];
+  int pref[kBatch + 1];
+  int len[kBatch];
+  int ids[kBatch];
 };
 
 template <bool FP4>
@@ -282,26 +281,27 @@ decode_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_constant_
               const __grid_constant__ CUtensorMap map_qp, const __grid_constant__ CUtensorMap map_qpr,
               const __grid_constant__ CUtensorMap map_scales, const DecodeParams p) {
   extern __shared__ uint8_t smem_raw[];
-  __shared__ Shared<FP4 ? kBatch4 : kBatch> sh;
+  __shared__ Shared sh;
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   constexpr int kAll = kAllThreads<FP4>;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int chunks = 2 * p.pairs + 1;               // the last one holds the rotary part, then P
-  uint8_t* skv = smem + chunks * kChunk;
-  const int slot_bytes = chunks * kChunk;
-  // in 4 bits: expanded pairs, rotary chunks, stages of codes, and their barriers
+  uint8_t* skv = smem + (FP4 ? p.q_bytes : chunks * kChunk);
+  const int slot_bytes = chunks * kChunk, kv_at = FP4 ? p.q_bytes : slot_bytes;
+  // in 4 bits: queries, expanded pairs, rotary chunks, the stage of codes, and their barriers.  The queries' last chunk is
+  // read 64 rows deep; the places past its rows are the first pair's.
   uint8_t* srope = skv + (FP4 ? p.bufs * 2 * kChunk : 0);
   uint8_t* sstage = srope + kStages * kChunk;
   uint64_t *const full4 = &sh.full[0][0], *const empty4 = &sh.empty[0][0];
   constexpr int kRopeBar = kBufs, kStageBar = kBufs + kStages;
-  static_assert(kStageBar + kStages <= kMaxSlots * (kMaxPairs + 1), "barriers");
+  static_assert(kStageBar < kMaxSlots * (kMaxPairs + 1), "barriers");
   // A tile comes and goes in these parts: the value product lets go of one pair after the other, and the next tile's
   // copies follow at once (two parts a tile instead of five measured 13% to 20% slower on long sequences).
   const int parts = p.pairs + (p.rope ? 1 : 0);
 
   if (tid == 0) {
     if (FP4) {
-      for (int i = 0; i < kStageBar + kStages; ++i) {
+      for (int i = 0; i <= kStageBar; ++i) {
         mbar_init(full4 + i, i < kRopeBar ? kExpandWarps : 1);
         mbar_init(empty4 + i, i < kStageBar ? 1 : kExpandWarps);
       }
@@ -496,7 +496,7 @@ decode_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_constant_
     bool issued = false, ok = true;
     constexpr uint32_t idesc_s = make_idesc(64, kTok);
     const uint32_t tm = uni(tmem), smem0 = uni(smem_u32(smem));
-    const uint64_t dq0 = smem_desc(smem0), dk0 = smem_desc(smem0 + chunks * kChunk), dr0 = smem_desc(uni(smem_u32(srope)));
+    const uint64_t dq0 = smem_desc(smem0), dk0 = smem_desc(smem0 + kv_at), dr0 = smem_desc(uni(smem_u32(srope)));
     int buf4 = 0;
     uint32_t par4 = 0;
     while (__any_sync(0xffffffffu, ok && it.next(sg))) {
@@ -560,8 +560,8 @@ decode_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_constant_
     int tile = 0, slot = 0;
     bool issued = false, ok = true;
     const uint32_t tm = uni(tmem), smem0 = uni(smem_u32(smem));
-    const uint64_t dv0 = smem_desc_mn(smem0 + chunks * kChunk, kChunk);
-    const uint64_t dp0 = FP4 ? smem_desc(uni(smem_u32(srope))) : smem_desc(smem0 + chunks * kChunk) + (uint64_t)((2 * p.pairs * kChunk) >> 4);
+    const uint64_t dv0 = smem_desc_mn(smem0 + kv_at, kChunk);
+    const uint64_t dp0 = FP4 ? smem_desc(uni(smem_u32(srope))) : smem_desc(smem0 + kv_at) + (uint64_t)((2 * p.pairs * kChunk) >> 4);
     int buf4 = 0;
     while (__any_sync(0xffffffffu, ok && it.next(sg))) {
       const int n_tiles = (int)uni((sg.tok1 - sg.tok0 + kTok - 1) / kTok);
@@ -597,12 +597,11 @@ decode_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_constant_
     __syncwarp();
   } else if (FP4 && warp == kThreads / 32 + kExpandWarps) {
     // ------------------------------------------------ copies of codes and scales, as they are
-    int tile = 0, stage = 0;
-    uint32_t par = 1;
+    int tile = 0;
     bool ok = true;
     const int page = p.kv.page_tokens, box = min(page, kTok), layer_page = p.layer * p.kv.n_pages;
-    const int regions = fp4_regions(p.kv.rank), bytes = fp4_stage_bytes(p.kv.rank, kTok);
-    const uint32_t stage0 = uni(smem_u32(sstage)), bar0 = uni(smem_u32(full4 + kStageBar));
+    const int regions = fp4_regions(p.kv.rank);
+    const uint32_t to = uni(smem_u32(sstage)), bar = uni(smem_u32(full4 + kStageBar));
     const bool pseq_ok = p.np == 0 || (*p.prefix_seq >= 0 && *p.prefix_seq < p.kv.max_seqs);
     const uint64_t once = l2_evict_first(), shared = l2_normal();
     while (__any_sync(0xffffffffu, ok && it.next(sg))) {
@@ -626,9 +625,8 @@ decode_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_constant_
           row = 0;
         }
         ahead = block(t + kTok);
-        ok = warp_wait(empty4 + kStageBar + stage, par, abort_flag);
+        ok = warp_wait(empty4 + kStageBar, (tile & 1) ^ 1u, abort_flag);
         if (!ok) break;
-        const uint32_t to = stage0 + stage * bytes, bar = bar0 + 8 * stage;
         mbar_expect_tx_warp(bar, (uint32_t)(nb * box * (128 * regions + 32)));
 #pragma unroll 1
         for (int i = 0; i < nb; ++i) {
@@ -639,54 +637,51 @@ decode_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_constant_
           tma_load_2d_hint_warp(to + regions * kTok * 128 + i * box * 32, &map_scales, bar, p.kv.rank / 2 + 2 * p.rope, r, pol);
         }
         ++tile;
-        if (++stage == kStages) {
-          stage = 0;
-          par ^= 1u;
-        }
       }
     }
     volatile int no_abort = 0;
-    for (int s = 0; s < kStages; ++s) {
-      const int loads = tile / kStages + (tile % kStages > s ? 1 : 0);
-      if (loads > 0) mbar_wait(full4 + kStageBar + s, (loads - 1) & 1, &no_abort);
-    }
+    if (tile) mbar_wait(full4 + kStageBar, (tile - 1) & 1, &no_abort);
     __syncwarp();
   } else if (FP4 && warp >= kThreads / 32) {
     // ------------------------------------------------ latents in 4 bits, expanded into the pairs that a copy would fill
-    // Four threads a token; of each 128-entry pair a thread has 16 bytes of codes, a quarter.  Places past a piece's last
+    // Four threads a token; of each 128-entry pair a thread has 16 bytes of codes, a quarter.  A tile's codes go to
+    // registers at once, so that the next tile's are on their way while these are expanded.  Places past a piece's last
     // token get whatever the stage holds, which the softmax warps hide and clear.
     const int r = (warp - kThreads / 32) * 8 + (lane & 7), v = lane >> 3;
-    const int regions = fp4_regions(p.kv.rank), bytes = fp4_stage_bytes(p.kv.rank, kTok);
+    const int regions = fp4_regions(p.kv.rank);
     const Fp4Place to(smem_u32(skv), kChunk, r, v);
-    const uint32_t stage0 = smem_u32(sstage);
-    int stage = 0, buf = 0;
-    uint32_t par_s = 0, par = 1;
+    const uint32_t stage = smem_u32(sstage);
+    int buf = 0, tile = 0;
+    uint32_t par = 1;
     bool ok = true;
     while (__any_sync(0xffffffffu, ok && it.next(sg))) {
       const int n_tiles = (sg.tok1 - sg.tok0 + kTok - 1) / kTok;
-      for (int i = 0; ok && i < n_tiles; ++i) {
-        ok = warp_wait(full4 + kStageBar + stage, par_s, abort_flag);
+      for (int i = 0; ok && i < n_tiles; ++i, ++tile) {
+        ok = warp_wait(full4 + kStageBar, tile & 1, abort_flag);
+        if (!ok) break;
+        uint4 c[kMaxPairs];
+        uint32_t scales[kMaxPairs];
+#pragma unroll
+        for (int j = 0; j < kMaxPairs; ++j)
+          if (j < p.pairs) fp4_fetch(stage, kTok, regions, r, v, j, c[j], scales[j]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(empty4 + kStageBar);
 #pragma unroll 1
-        for (int j = 0; ok && j < p.pairs; ++j) {
-          uint4 c;
-          uint32_t scales;
-          fp4_fetch(stage0 + stage * bytes, kTok, regions, r, v, j, c, scales);
+        for (int j = 0; j < p.pairs; ++j) {
           ok = warp_wait(empty4 + buf, par, abort_flag);
           if (!ok) break;
-          fp4_store32(to, buf * 2 * kChunk, c, scales);
+          fp4_store32(to, buf * 2 * kChunk, c[0], scales[0]);
           __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(full4 + buf);
-            if (j == p.pairs - 1) mbar_arrive(empty4 + kStageBar + stage);
-          }
+          if (lane == 0) mbar_arrive(full4 + buf);
           if (++buf == p.bufs) {
             buf = 0;
             par ^= 1u;
           }
-        }
-        if (++stage == kStages) {
-          stage = 0;
-          par_s ^= 1u;
+#pragma unroll
+          for (int x = 0; x + 1 < kMaxPairs; ++x) {       // rolled: one copy of the expansion
+            c[x] = c[x + 1];
+            scales[x] = scales[x + 1];
+          }
         }
       }
     }
@@ -1173,7 +1168,7 @@ cudaError_t launch_decode_kernel(const DecodeParams& p, int smem, cudaStream_t s
   static std::atomic<unsigned char> attr[kMaxDevices];
   const cudaError_t e = once_per_device(attr, [] {
     return cudaFuncSetAttribute(decode_kernel<FP4>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                227 * 1024 - (int)sizeof(Shared<FP4 ? kBatch4 : kBatch>));
+                                227 * 1024 - (int)sizeof(Shared));
   });
   return e == cudaSuccess
              ? launch_k(decode_kernel<FP4>, p.ctas, kAllThreads<FP4>, smem, s, kv, pair, qs, qsr, qp, qpr, scales, p)
@@ -1181,20 +1176,23 @@ cudaError_t launch_decode_kernel(const DecodeParams& p, int smem, cudaStream_t s
 }
 
 int launch_decode(const moe_kv_cache& c, DecodeParams p, const void* q, cudaStream_t s) {
-  static_assert(sizeof(Shared<kBatch>) + 1024 + (2 * kMaxPairs + 1) * kChunk * 3 <= 227 * 1024, "shared memory");
-  static_assert(sizeof(Shared<kBatch4>) + 1024 + (2 * kMaxPairs + 1) * kChunk + kStages * (kChunk + kTok * (256 + 32)) +
+  static_assert(sizeof(Shared) + 1024 + (2 * kMaxPairs + 1) * kChunk * 3 <= 227 * 1024, "shared memory");
+  static_assert(sizeof(Shared) + 1024 + (2 * kMaxPairs + 1) * kChunk + kStages * kChunk + kTok * (256 + 32) +
                         (kMaxPairs + 1) * 2 * kChunk <= 227 * 1024, "more pairs than a tile has");
   const bool fp4 = c.format == MOE_KV_FP4;
   const int row = c.rank + c.rope, slot = (2 * p.pairs + 1) * kChunk;
   int smem;
   if (fp4) {
-    const int rest = slot + kStages * (kChunk + fp4_stage_bytes(c.rank, kTok)) + 1024;
+    // Queries of up to 48 rows leave room for two tiles' pairs; with 64 rows of rank 512 there are 7 of the 8.
+    const int q_rows = p.np && p.NRp > p.NR ? p.NRp : p.NR;
+    p.q_bytes = ((2 * p.pairs + 1) * q_rows * 128 + 1023) & ~1023;
+    const int rest = p.q_bytes + kStages * kChunk + fp4_stage_bytes(c.rank, kTok) + 1024;
     p.slots = kStages;
-    p.bufs = (int)((227 * 1024 - sizeof(Shared<kBatch4>) - rest) / (2 * kChunk));
+    p.bufs = (int)((227 * 1024 - sizeof(Shared) - rest) / (2 * kChunk));
     if (p.bufs > 2 * p.pairs) p.bufs = 2 * p.pairs;
     smem = rest + p.bufs * 2 * kChunk;
   } else {
-    p.slots = (int)((227 * 1024 - sizeof(Shared<kBatch>) - 1024 - slot) / slot);   // what the query tile leaves
+    p.slots = (int)((227 * 1024 - sizeof(Shared) - 1024 - slot) / slot);   // what the query tile leaves
     if (p.slots > kMaxSlots) p.slots = kMaxSlots;
     smem = (1 + p.slots) * slot + 1024;
   }
@@ -1256,10 +1254,9 @@ int moe_latent_decode(const moe_kv_cache* cache, int layer, const void* q, const
   if (!kv_aligned(q, 16) || !kv_aligned(out, 16)) return MOE_ERR_UNSUPPORTED;
   st = check_ws(ws, ws_bytes, moe_latent_decode_workspace_size(cache, B, Q, heads, shared_tokens));
   if (st != MOE_OK) return st;
-  const int batch = cache->format == MOE_KV_FP4 ? kBatch4 : kBatch;
-  for (int b0 = 0; b0 < B && st == MOE_OK; b0 += batch) {   // larger batches: several launches
+  for (int b0 = 0; b0 < B && st == MOE_OK; b0 += kBatch) {   // batches of more than 512 sequences: several launches
     DecodeParams p = {};
-    fill_shape(p, *cache, B - b0 < batch ? B - b0 : batch, Q, heads, shared_tokens);
+    fill_shape(p, *cache, B - b0 < kBatch ? B - b0 : kBatch, Q, heads, shared_tokens);
     const DecodeWs w = decode_ws(p, cache->rank);
     char* base = reinterpret_cast<char*>(ws);
     const size_t row0 = (size_t)b0 * Q * heads;
