@@ -1,6 +1,6 @@
 // Eviction from the latent cache: sequences past a budget keep their heaviest
 // tokens.  select_kernel finds, per sequence and layer, which tokens stay; move_kernel
-// closes the gaps in place; finish_kernel shortens the block tables.
+// closes the gaps in place, and the last of a sequence's CTAs shortens its block table.
 #include "kv_common.cuh"
 
 namespace moe {
@@ -26,6 +26,7 @@ struct EvictParams {
   EvictPlan* plan;        // [n]
   uint32_t* mask;         // [n_layers][n][words] bit t % 32 of word t / 32: token t stays
   int32_t* before;        // [n_layers][n][words] tokens that stay before the word's
+  int32_t* done;          // [n] CTAs of move_kernel that have moved their share
   uint32_t* status;
 };
 
@@ -53,6 +54,7 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const EvictParams p
   const int i = blockIdx.x, layer = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int seq = p.seqs[i];
   if (tid == 0) {
+    if (layer == 0) p.done[i] = 0;
     sh.bad = 0;
     sh.blocks_shared = 0;
   }
@@ -67,6 +69,18 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const EvictParams p
   __syncthreads();
   const int len = in_range ? p.kv.len_of(seq) : 0;
   const bool over = sh.bad == 0 && len > p.budget;
+  // A warp takes a run of words of 32 tokens, a lane a token of each.  The first words' weights stay in registers; they
+  // are on their way while the block table is looked through.
+  const int words = (len + 31) / 32, per = (words + 31) / 32, w0 = min(words, warp * per), w1 = min(words, w0 + per);
+  const float* w = p.weights + ((size_t)layer * p.kv.max_seqs + (in_range ? seq : 0)) * p.cap;
+  float raw[kHeld];
+  if (over) {
+#pragma unroll
+    for (int x = 0; x < kHeld; ++x) {
+      const int t = (w0 + x) * 32 + lane;
+      raw[x] = w0 + x < w1 && t < len ? w[t] : 0.0f;
+    }
+  }
   if (over) {
     const int32_t* row = p.kv.table + (size_t)seq * p.kv.max_blocks;
     int last = 0;
@@ -100,20 +114,19 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const EvictParams p
   const int now = max(p.budget, head + len - tail);
   const int want = now - head - (len - tail);                  // of the tokens between them, fewer than there are
   if (tid == 0 && layer == 0) p.plan[i] = EvictPlan{seq, len, now, head};
-  const float* w = p.weights + ((size_t)layer * p.kv.max_seqs + seq) * p.cap;
 
-  // A warp takes a run of words of 32 tokens, a lane a token of each; the first words' keys stay in registers.  Key 0:
-  // a place that is not chosen among (it lies in the head or the tail, or past the end).
-  const int words = (len + 31) / 32, per = (words + 31) / 32, w0 = min(words, warp * per), w1 = min(words, w0 + per);
-  auto key_of = [&](int word) {
+  // Key 0: a place that is not chosen among (it lies in the head or the tail, or past the end).
+  auto key_of = [&](int word, float weight) {
     const int t = word * 32 + lane;
-    return t >= head && t < tail ? order_key(w[t]) : 0u;     // a weight's own key is above 0 (-infinity: 0x007FFFFF)
+    return t >= head && t < tail ? order_key(weight) : 0u;   // a weight's own key is above 0 (-infinity: 0x007FFFFF)
+  };
+  auto key_at = [&](int word) {
+    const int t = word * 32 + lane;
+    return key_of(word, t < len ? w[t] : 0.0f);
   };
   uint32_t held[kHeld];
-  if (want > 0) {
 #pragma unroll
-    for (int x = 0; x < kHeld; ++x) held[x] = w0 + x < w1 ? key_of(w0 + x) : 0u;
-  }
+  for (int x = 0; x < kHeld; ++x) held[x] = w0 + x < w1 ? key_of(w0 + x, raw[x]) : 0u;
 
   // the want-th largest key, digit by digit; `left` of the keys equal to it stay
   uint32_t prefix = 0;
@@ -134,7 +147,7 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const EvictParams p
 #pragma unroll
       for (int x = 0; x < kHeld; ++x)
         if (w0 + x < w1) count(held[x]);
-      for (int x = w0 + kHeld; x < w1; ++x) count(key_of(x));
+      for (int x = w0 + kHeld; x < w1; ++x) count(key_at(x));
       __syncthreads();
       if (warp == 0) {             // the digit whose keys, with those above it, first reach `left`
         int mine[8], sum = 0;
@@ -183,7 +196,7 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const EvictParams p
 #pragma unroll
   for (int x = 0; x < kHeld; ++x)
     if (w0 + x < w1) tally(w0 + x, held[x]);
-  for (int x = w0 + kHeld; x < w1; ++x) tally(x, key_of(x));
+  for (int x = w0 + kHeld; x < w1; ++x) tally(x, key_at(x));
   if (lane == 0) {
     sh.warp_gt[warp] = gt;
     sh.warp_eq[warp] = eq;
@@ -214,12 +227,30 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const EvictParams p
 #pragma unroll
   for (int x = 0; x < kHeld; ++x)
     if (w0 + x < w1) mark(w0 + x, held[x]);
-  for (int x = w0 + kHeld; x < w1; ++x) mark(x, key_of(x));
+  for (int x = w0 + kHeld; x < w1; ++x) mark(x, key_at(x));
+}
+
+// The last of a sequence's CTAs (all layers) takes the pages behind the new length out of its block table.
+__device__ inline void finish(const EvictParams& p, int i, const EvictPlan& e, int slices) {
+  __shared__ int s_last;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    __threadfence();
+    s_last = atomicAdd(&p.done[i], 1) == (slices + 1) * p.kv.n_layers - 1;
+  }
+  __syncthreads();
+  if (!s_last) return;
+  int32_t* row = p.kv.table + (size_t)e.seq * p.kv.max_blocks;
+  for (int b = p.kv.blocks_of(e.now) + threadIdx.x; b < p.kv.blocks_of(e.len); b += kMoveThreads) {
+    atomicSub(&p.kv.refs[row[b]], 1);
+    row[b] = -1;
+  }
+  if (threadIdx.x == 0) p.kv.lens[e.seq] = e.now;
 }
 
 // In place: a token never moves to a later place, and a chunk of tokens is read before any of it is written, so
 // what a chunk writes lies before everything that a later one reads.  A CTA moves 128 bytes of every row, the last CTA the weights.
-__global__ void __launch_bounds__(kMoveThreads) move_kernel(const EvictParams p, int slices) {
+__global__ void __launch_bounds__(kMoveThreads, 3) move_kernel(const EvictParams p, int slices) {
   pdl_wait();
   pdl_trigger();
   const int i = blockIdx.y, layer = blockIdx.z, tid = threadIdx.x;
@@ -249,6 +280,7 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(const EvictParams p,
     }
     __syncthreads();
     for (int t = e.now + tid; t < e.len; t += kMoveThreads) w[t] = 0.0f;
+    finish(p, i, e, slices);
     return;
   }
   const int vecs = p.kv.row >> 3, v = blockIdx.x * kSliceVecs + (tid % kSliceVecs);
@@ -292,23 +324,11 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(const EvictParams p,
     __syncthreads();
     write(x[1], to[1]);
   }
-}
-
-__global__ void __launch_bounds__(kMoveThreads) finish_kernel(const EvictParams p) {
-  pdl_wait();
-  pdl_trigger();
-  const EvictPlan e = p.plan[blockIdx.x];
-  if (e.seq < 0 || e.now == e.len) return;
-  int32_t* row = p.kv.table + (size_t)e.seq * p.kv.max_blocks;
-  for (int b = p.kv.blocks_of(e.now) + threadIdx.x; b < p.kv.blocks_of(e.len); b += kMoveThreads) {
-    atomicSub(&p.kv.refs[row[b]], 1);
-    row[b] = -1;
-  }
-  if (threadIdx.x == 0) p.kv.lens[e.seq] = e.now;
+  finish(p, i, e, slices);
 }
 
 struct EvictWs {
-  size_t plan, mask, before, bytes;
+  size_t plan, mask, before, done, bytes;
 };
 
 EvictWs evict_ws(const moe_kv_cache& c, int n) {
@@ -317,7 +337,8 @@ EvictWs evict_ws(const moe_kv_cache& c, int n) {
   w.plan = 0;
   w.mask = align_up((size_t)n * sizeof(EvictPlan), 256);
   w.before = w.mask + align_up(words * 4, 256);
-  w.bytes = w.before + align_up(words * 4, 256);
+  w.done = w.before + align_up(words * 4, 256);
+  w.bytes = w.done + align_up((size_t)n * 4, 256);
   return w;
 }
 
@@ -365,12 +386,12 @@ int moe_kv_evict(const moe_kv_cache* cache, const int32_t* seqs, int n, float* w
   p.plan = reinterpret_cast<EvictPlan*>(b + w.plan);
   p.mask = reinterpret_cast<uint32_t*>(b + w.mask);
   p.before = reinterpret_cast<int32_t*>(b + w.before);
+  p.done = reinterpret_cast<int32_t*>(b + w.done);
   p.status = dev_status;
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const int slices = ((p.kv.row >> 3) + kSliceVecs - 1) / kSliceVecs;
   cudaError_t e = launch_k(select_kernel, dim3(n, cache->n_layers), kSelThreads, 0, s, p);
   if (e == cudaSuccess) e = launch_k(move_kernel, dim3(slices + 1, n, cache->n_layers), kMoveThreads, 0, s, p, slices);
-  if (e == cudaSuccess) e = launch_k(finish_kernel, n, kMoveThreads, 0, s, p);
   return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 

@@ -492,25 +492,37 @@ expand_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
         // past the last token some row: the epilogue writes zeros there
         row[e] = reinterpret_cast<const uint8_t*>(p.kv.pages + p.kv.row_offset(p.layer, pg, t & (p.kv.page_tokens - 1))) + 16 * v;
       }
-      if (!warp_wait(&sh.a_empty, (loaded & 1) ^ 1u, abort_flag)) break;
-      ++loaded;
-      for (int c = 0; c < chunks; c += 2) {
-        uint4 code[4];
-        uint32_t scale[4];
+      // two pairs' codes are on their way while one is expanded
+      uint4 code[2][4];
+      uint32_t scale[2][4];
+      auto load = [&](int c, uint4 (&code)[4], uint32_t (&scale)[4]) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           code[e] = ldg_stream(row[e] + 32 * c);
           scale[e] = ldg_stream_u16(row[e] + scales_at + 4 * c - 14 * v);
         }
+      };
+      auto expand = [&](int c, const uint4 (&code)[4], const uint32_t (&scale)[4]) {
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          fp4_store32(Fp4Place(smem_u32(smem) + c * kChunkBytes, kChunkBytes, r0 + 32 * e, v), 0, code[e], scale[e]);
+          fp4_store32(Fp4Place(smem_u32(smem), kChunkBytes, r0 + 32 * e, v), c * kChunkBytes, code[e], scale[e]);
         proxy_fence();
         __syncwarp();
         if (lane == 0) {
           mbar_arrive(&sh.a_full[c]);
           mbar_arrive(&sh.a_full[c + 1]);
         }
+      };
+      load(0, code[0], scale[0]);
+      if (!warp_wait(&sh.a_empty, (loaded & 1) ^ 1u, abort_flag)) break;
+      ++loaded;
+#pragma unroll 1
+      for (int c = 0; c < chunks; c += 4) {
+        if (c + 2 < chunks) load(c + 2, code[1], scale[1]);
+        expand(c, code[0], scale[0]);
+        if (c + 2 >= chunks) break;
+        if (c + 4 < chunks) load(c + 4, code[0], scale[0]);
+        expand(c + 2, code[1], scale[1]);
       }
     }
     __syncwarp();
