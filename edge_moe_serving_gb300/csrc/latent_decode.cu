@@ -71,6 +71,8 @@ struct DecodeParams : LineShape {
   int layer, rope;
   int pairs, slots, bufs;    // rank / 128; tiles in flight; in 4 bits, pairs that are expanded at once
   int q_bytes;               // in 4 bits: room of a tile's queries
+  int lines;                 // which lines this launch takes: 1 the prefix, 2 the sequences', 3 both
+  const int32_t* prefix_blocks;   // the prefix's block table where it is not its sequence's, else nullptr
   float scale_log2;          // scale * log2(e): the exponentials are powers of two
   const int32_t* seqs;
   const int32_t* prefix_seq;
@@ -112,7 +114,7 @@ struct SegIter {
     phase = 0;
     const long long total = (long long)p.Gp * p.np;
     pos = min(total, (long long)blockIdx.x * p.per_p);
-    end = min(total, pos + p.per_p);
+    end = p.lines & 1 ? min(total, pos + p.per_p) : pos;
     first = true;
   }
   __device__ void start_suffix() {
@@ -154,6 +156,7 @@ struct SegIter {
         first = false;
         return true;
       }
+      if (!(p.lines & 2)) return false;
       start_suffix();
     }
     if (pos >= end) return false;
@@ -396,7 +399,8 @@ decode_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_constant_
     while (__any_sync(0xffffffffu, ok && it.next(sg))) {
       const bool seq_ok = !sg.prefix || pseq_ok;      // a bad id in the batch has no tokens
       const uint64_t pol = sg.prefix || p.G > 1 ? shared : once;
-      const int32_t* blocks = p.kv.table + (seq_ok ? (size_t)sg.seq * p.kv.max_blocks : 0);
+      const int32_t* blocks = sg.prefix && p.prefix_blocks ? p.prefix_blocks
+                                                             : p.kv.table + (seq_ok ? (size_t)sg.seq * p.kv.max_blocks : 0);
       const int tok0 = (int)uni(sg.tok0), tok1 = (int)uni(sg.tok1);
       // lane i: the pool row where box i of a tile begins; read one tile ahead
       auto block = [&](int t) { return seq_ok && lane < kTok / box && t < tok1 ? blocks[t >> p.kv.page_shift] : -1; };
@@ -607,7 +611,8 @@ decode_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_constant_
     while (__any_sync(0xffffffffu, ok && it.next(sg))) {
       const bool seq_ok = !sg.prefix || pseq_ok;
       const uint64_t pol = sg.prefix || p.G > 1 ? shared : once;
-      const int32_t* blocks = p.kv.table + (seq_ok ? (size_t)sg.seq * p.kv.max_blocks : 0);
+      const int32_t* blocks = sg.prefix && p.prefix_blocks ? p.prefix_blocks
+                                                             : p.kv.table + (seq_ok ? (size_t)sg.seq * p.kv.max_blocks : 0);
       const int tok0 = (int)uni(sg.tok0), tok1 = (int)uni(sg.tok1);
       auto block = [&](int t) { return seq_ok && lane < kTok / box && t < tok1 ? blocks[t >> p.kv.page_shift] : -1; };
       int ahead = block(tok0 + lane * box);
@@ -1131,9 +1136,36 @@ __global__ void __launch_bounds__(128 * kSets) combine_parts_kernel(const Decode
   if (threadIdx.x == 0) store_lse(p, row, ref, l);
 }
 
+// ---------------------------------------------------------------- a prefix in 4 bits, once for all row tiles
+// The shared tokens' rows as bf16 pages of the workspace, and those pages' block table.
+__global__ void __launch_bounds__(128) unpack_prefix_kernel(const DecodeParams p, __nv_bfloat16* pages, int32_t* table) {
+  pdl_wait();
+  pdl_trigger();
+  const int t = blockIdx.x * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31, seq = *p.prefix_seq;
+  if (t >= p.shared) return;
+  if (lane == 0 && (t & (p.kv.page_tokens - 1)) == 0) table[t >> p.kv.page_shift] = t >> p.kv.page_shift;
+  if (seq < 0 || seq >= p.kv.max_seqs) return;                    // reported, and answered with zeros, by those that follow
+  int pg = p.kv.table[(size_t)seq * p.kv.max_blocks + (t >> p.kv.page_shift)];
+  if (pg < 0 || pg >= p.kv.n_pages) {
+    if (lane == 0) set_status(p.status, MOE_DEV_ERR_BAD_PAGE);
+    pg = 0;
+  }
+  const int rank = p.kv.rank, vecs = (rank + p.rope) >> 3;
+  const uint8_t* from = reinterpret_cast<const uint8_t*>(p.kv.pages + p.kv.row_offset(p.layer, pg, t & (p.kv.page_tokens - 1)));
+  uint4* to = reinterpret_cast<uint4*>(pages) + (size_t)t * vecs;
+  const int b = lane, rope_vecs = p.rope >> 3;
+  if (b < rank / kFpBlock) {                                      // rank is 512 at most
+    const uint2 c = *reinterpret_cast<const uint2*>(from + 8 * b);
+    const uint32_t f = fp4_factor(from[rank / 2 + 2 * p.rope + b]);
+    to[2 * b] = fp4_expand8(c.x, f);
+    to[2 * b + 1] = fp4_expand8(c.y, f);
+  }
+  if (lane < rope_vecs) to[rank / 8 + lane] = reinterpret_cast<const uint4*>(from + rank / 2)[lane];
+}
+
 // ---------------------------------------------------------------- host side
 struct DecodeWs {
-  size_t plan, part_s, ml_s, part_p, ml_p, bytes;
+  size_t plan, part_s, ml_s, part_p, ml_p, pages, table, bytes;
 };
 
 void fill_shape(DecodeParams& p, const moe_kv_cache& c, int B, int Q, int heads, int shared) {
@@ -1142,7 +1174,8 @@ void fill_shape(DecodeParams& p, const moe_kv_cache& c, int B, int Q, int heads,
   p.pairs = c.rank / 128;
 }
 
-DecodeWs decode_ws(const DecodeParams& p, int rank) {
+DecodeWs decode_ws(const DecodeParams& p, const moe_kv_cache& c) {
+  const int rank = c.rank;
   DecodeWs w;
   const size_t ns = suffix_rows(p), np = prefix_rows(p);
   w.plan = 0;
@@ -1155,6 +1188,10 @@ DecodeWs decode_ws(const DecodeParams& p, int rank) {
   at += align_up(np * rank * sizeof(float), 256);
   w.ml_p = at;
   at += align_up(np * sizeof(float4), 256);
+  w.pages = at;              // the prefix as bf16
+  if (c.format == MOE_KV_FP4) at += align_up((size_t)p.shared * (rank + c.rope) * 2, 256);
+  w.table = at;
+  if (c.format == MOE_KV_FP4) at += align_up((size_t)p.shared / 16 * sizeof(int32_t), 256);
   w.bytes = at;
   return w;
 }
@@ -1175,18 +1212,18 @@ cudaError_t launch_decode_kernel(const DecodeParams& p, int smem, cudaStream_t s
              : e;
 }
 
-int launch_decode(const moe_kv_cache& c, DecodeParams p, const void* q, cudaStream_t s) {
+// One launch of the main kernel over p.kv, whose rows are in 4 bits or not.
+cudaError_t launch_lines(DecodeParams p, bool fp4, const void* q, cudaStream_t s) {
   static_assert(sizeof(Shared) + 1024 + (2 * kMaxPairs + 1) * kChunk * 3 <= 227 * 1024, "shared memory");
   static_assert(sizeof(Shared) + 1024 + (2 * kMaxPairs + 1) * kChunk + kStages * kChunk + kTok * (256 + 32) +
                         (kMaxPairs + 1) * 2 * kChunk <= 227 * 1024, "more pairs than a tile has");
-  const bool fp4 = c.format == MOE_KV_FP4;
-  const int row = c.rank + c.rope, slot = (2 * p.pairs + 1) * kChunk;
+  const int rank = p.kv.rank, row = rank + p.rope, slot = (2 * p.pairs + 1) * kChunk;
   int smem;
   if (fp4) {
     // Queries of up to 48 rows leave room for two tiles' pairs; with 64 rows of rank 512 there are 7 of the 8.
     const int q_rows = p.np && p.NRp > p.NR ? p.NRp : p.NR;
     p.q_bytes = ((2 * p.pairs + 1) * q_rows * 128 + 1023) & ~1023;
-    const int rest = p.q_bytes + kStages * kChunk + fp4_stage_bytes(c.rank, kTok) + 1024;
+    const int rest = p.q_bytes + kStages * kChunk + fp4_stage_bytes(rank, kTok) + 1024;
     p.slots = kStages;
     p.bufs = (int)((227 * 1024 - sizeof(Shared) - rest) / (2 * kChunk));
     if (p.bufs > 2 * p.pairs) p.bufs = 2 * p.pairs;
@@ -1198,23 +1235,54 @@ int launch_decode(const moe_kv_cache& c, DecodeParams p, const void* q, cudaStre
   }
   // cache rows by chunk and by pair (in 4 bits: rotary keys, codes and scales); query tiles of sequences and of the prefix
   CUtensorMap kv, pair, qs, qsr, qp, qpr, scales;
-  const uint64_t rows = (uint64_t)c.n_layers * c.n_pages * c.page_tokens, qrows = (uint64_t)p.B * p.Q * p.heads;
-  const uint32_t box = c.page_tokens < kTok ? c.page_tokens : kTok;
-  if (!make_map(&kv, c.pages, p.kv.row, rows, box) || !make_map_chunks(&qs, q, row, qrows, p.NR, 2 * p.pairs) ||
+  const uint64_t rows = (uint64_t)p.kv.n_layers * p.kv.n_pages * p.kv.page_tokens, qrows = (uint64_t)p.B * p.Q * p.heads;
+  const uint32_t box = p.kv.page_tokens < kTok ? p.kv.page_tokens : kTok;
+  if (!make_map(&kv, p.kv.pages, p.kv.row, rows, box) || !make_map_chunks(&qs, q, row, qrows, p.NR, 2 * p.pairs) ||
       !make_map(&qsr, q, row, qrows, p.NR))
-    return MOE_ERR_CUDA;
-  if (fp4 ? !make_map_bytes(&pair, c.pages, 2 * p.kv.row, rows, 128, box, true) ||
-                !make_map_bytes(&scales, c.pages, 2 * p.kv.row, rows, 32, box, false)
-          : !make_map_chunks(&pair, c.pages, row, rows, kTok, 2))
-    return MOE_ERR_CUDA;
+    return cudaErrorInvalidValue;
+  if (fp4 ? !make_map_bytes(&pair, p.kv.pages, 2 * p.kv.row, rows, 128, box, true) ||
+                !make_map_bytes(&scales, p.kv.pages, 2 * p.kv.row, rows, 32, box, false)
+          : !make_map_chunks(&pair, p.kv.pages, row, rows, kTok, 2))
+    return cudaErrorInvalidValue;
   if (!fp4) scales = kv;
   qp = qs;
   qpr = qsr;
   if (p.np && p.NRp != p.NR &&
       (!make_map_chunks(&qp, q, row, qrows, p.NRp, 2 * p.pairs) || !make_map(&qpr, q, row, qrows, p.NRp)))
-    return MOE_ERR_CUDA;
-  cudaError_t e = fp4 ? launch_decode_kernel<true>(p, smem, s, kv, pair, qs, qsr, qp, qpr, scales)
-                      : launch_decode_kernel<false>(p, smem, s, kv, pair, qs, qsr, qp, qpr, scales);
+    return cudaErrorInvalidValue;
+  return fp4 ? launch_decode_kernel<true>(p, smem, s, kv, pair, qs, qsr, qp, qpr, scales)
+             : launch_decode_kernel<false>(p, smem, s, kv, pair, qs, qsr, qp, qpr, scales);
+}
+
+// A prefix in 4 bits that many row tiles read is expanded once, to bf16 pages that they read in its place.  With 32 heads,
+// expanded by each / once: 64 sequences over 16384 shared tokens (54 tiles of a row tile a CTA) 184 / 154 us, 16 over 65536
+// (54) 177 / 165, 64 over 2048 (7) 67 / 73, 16 over 16384 (13) 76 / 78.
+bool unpack_pays(const DecodeParams& p) { return p.np > 0 && p.Gp >= 8 && p.Gp * p.np >= 24 * p.ctas; }
+
+// unpacked: bf16 pages and their block table in the workspace; `there`: an earlier launch of the call has filled them
+int launch_decode(const moe_kv_cache& c, DecodeParams p, const void* q, __nv_bfloat16* unpacked, int32_t* blocks, bool& there,
+                  cudaStream_t s) {
+  const bool fp4 = c.format == MOE_KV_FP4;
+  cudaError_t e = cudaSuccess;
+  p.lines = 3;
+  p.prefix_blocks = nullptr;
+  if (fp4 && unpack_pays(p)) {
+    if (!there) e = launch_k(unpack_prefix_kernel, (unsigned)(p.shared + 3) / 4, 128, 0, s, p, unpacked, blocks);
+    there = true;
+    DecodeParams first = p;
+    first.kv.pages = unpacked;
+    first.kv.n_layers = 1;
+    first.kv.n_pages = p.shared >> p.kv.page_shift;
+    first.kv.row = p.kv.rank + p.rope;
+    first.kv.rope_at = p.kv.rank;
+    first.layer = 0;
+    first.prefix_blocks = blocks;
+    first.lines = 1;
+    if (e == cudaSuccess) e = launch_lines(first, false, q, s);
+    p.lines = 2;
+  }
+  if (e == cudaSuccess) e = launch_lines(p, fp4, q, s);
+  const uint64_t qrows = (uint64_t)p.B * p.Q * p.heads;
   // a CTA a row while the rows alone do not fill the SMs (then a row has many pieces), else a warp a row: whole calls over
   // 1200 tokens a sequence, us, CTA / warp: 128 rows 13.5 / 16.5, 160 rows 16.2 / 16.5, 288 rows 17.6 / 16.5, 1216 rows
   // 37.6 / 24.7
@@ -1236,7 +1304,7 @@ size_t moe_latent_decode_workspace_size(const moe_kv_cache* cache, int B, int Q,
   if (!decode_shape_ok(B, Q, heads)) return 0;
   DecodeParams p = {};
   fill_shape(p, *cache, B < kBatch ? B : kBatch, Q, heads, shared_tokens);
-  return decode_ws(p, cache->rank).bytes;
+  return decode_ws(p, *cache).bytes;
 }
 
 int moe_latent_decode(const moe_kv_cache* cache, int layer, const void* q, const int32_t* seqs, int B, int Q,
@@ -1254,12 +1322,19 @@ int moe_latent_decode(const moe_kv_cache* cache, int layer, const void* q, const
   if (!kv_aligned(q, 16) || !kv_aligned(out, 16)) return MOE_ERR_UNSUPPORTED;
   st = check_ws(ws, ws_bytes, moe_latent_decode_workspace_size(cache, B, Q, heads, shared_tokens));
   if (st != MOE_OK) return st;
+  __nv_bfloat16* pages = nullptr;      // a prefix in 4 bits as bf16: where the first launch's workspace has room for it
+  int32_t* blocks = nullptr;
+  bool unpacked = false;
   for (int b0 = 0; b0 < B && st == MOE_OK; b0 += kBatch) {   // batches of more than 512 sequences: several launches
     DecodeParams p = {};
     fill_shape(p, *cache, B - b0 < kBatch ? B - b0 : kBatch, Q, heads, shared_tokens);
-    const DecodeWs w = decode_ws(p, cache->rank);
+    const DecodeWs w = decode_ws(p, *cache);
     char* base = reinterpret_cast<char*>(ws);
     const size_t row0 = (size_t)b0 * Q * heads;
+    if (b0 == 0) {
+      pages = reinterpret_cast<__nv_bfloat16*>(base + w.pages);
+      blocks = reinterpret_cast<int32_t*>(base + w.table);
+    }
     p.kv = kv_view(*cache);
     p.layer = layer;
     // zero as the smallest normal number: a token out of sight scores -infinity, and 0 * -infinity is NaN
@@ -1275,7 +1350,7 @@ int moe_latent_decode(const moe_kv_cache* cache, int layer, const void* q, const
     p.ml_p = reinterpret_cast<float4*>(base + w.ml_p);
     p.status = dev_status;
     st = launch_decode(*cache, p, reinterpret_cast<const __nv_bfloat16*>(q) + row0 * (cache->rank + cache->rope),
-                       reinterpret_cast<cudaStream_t>(stream));
+                       pages, blocks, unpacked, reinterpret_cast<cudaStream_t>(stream));
   }
   return st;
 }

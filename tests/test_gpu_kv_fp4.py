@@ -302,6 +302,33 @@ def test_shared_prefix(rank, rope, page, heads, Q, shared_blocks, own):
     assert torch.equal(out, twin) and torch.equal(lse, twin_lse)
 
 
+@pytest.mark.parametrize("B,heads,first", [(40, 64, 0), (600, 8, 0), (40, 64, -1)])
+def test_a_prefix_of_many_row_tiles(B, heads, first):
+    """Enough row tiles over the shared tokens that these are expanded once for all of them (at 600 sequences in the first
+    of two launches alone); sequences that end inside the shared tokens and behind them; a bad first id."""
+    shared, page = 6400, 64
+    c = Paged4(110, page, 128, 16, B, 104, layers=2)
+    rows = c.fill([shared + 100], seed=B, layer=1)[0]
+    c.table[1:] = c.table[:1]
+    lens = [shared + 100 - (i * 7) % 150 for i in range(B)]
+    c.lens.copy_(i32(lens))
+    q = make_q(B, heads, c.row, 4)
+    seqs = list(range(B))
+    seqs[0] = first
+    out, lse = run_decode(c, q, seqs, 1, heads, 0.1, shared=shared, layer=1)
+    if first < 0:
+        assert c.bits() == moe.MOE_DEV_ERR_BAD_SEQ and bool((out == 0).all()) and bool((lse == -math.inf).all())
+        return
+    assert c.bits() == 0
+    twin, twin_lse = run_decode(c.twin(), q, seqs, 1, heads, 0.1, shared=shared, layer=1)
+    assert torch.equal(out, twin) and torch.equal(lse, twin_lse)
+    for b in (0, 1, 17, B - 1):
+        check_decode(c, {b: rows[:lens[b]]}, q[b:b + 1], [b], 1, heads, 0.1, out[b:b + 1], lse[b:b + 1])
+    c.table[:, 3] = 10 ** 6
+    run_decode(c, q, seqs, 1, heads, 0.1, shared=shared, layer=1)
+    assert c.bits() == moe.MOE_DEV_ERR_BAD_PAGE
+
+
 def test_decode_of_many_sequences_and_layers():
     """More sequences than one launch takes, empty ones among them, in the second of three layers."""
     lens = [(i * 37) % 150 for i in range(600)]
