@@ -56,6 +56,7 @@ struct WeightParams {
   int pairs, parts;                   // a row comes in parts: 128-entry pairs of chunks, then the rotary key
   int passes, rows_pass, ring;        // passes over the query rows, rows of each, parts of queries in shared memory
   int ctas;
+  bool resident;                      // the queries stay in shared memory while their sequence's tiles pass by
   float scale_log2, decay;
   const int32_t* seqs;                // the whole list
   const float* lse;
@@ -311,7 +312,7 @@ weights_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
     uint32_t par = 1;
     bool ok = true;
     while (__any_sync(0xffffffffu, ok && it.next(tl))) {
-      if (p.passes == 1 && !tl.first) continue;            // they are there
+      if (p.resident && !tl.first) continue;               // they are there
       const int n = (int)uni(tl.p1 - tl.p0);
       for (int k = 0; ok && k < n; ++k) {
         const int row0 = (int)uni(tl.b * rows_all + Tiles::pass(tl, k) * p.rows_pass);
@@ -347,7 +348,7 @@ weights_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
     bool ok = true, issued = false;
     while (__any_sync(0xffffffffu, ok && it.next(tl))) {
       const int n = (int)uni(tl.p1 - tl.p0);
-      const bool keep = p.passes == 1 && !uni(tl.last);     // the next tile takes the same queries
+      const bool keep = p.resident && !uni(tl.last);        // the next tile takes the same queries
       for (int k = 0; ok && k < n; ++k, ++pass) {
         const int buf = pass & 1, g = (int)uni(Tiles::pass(tl, k));
         ok = warp_wait(&sh.d_empty[buf], ((pass >> 1) & 1) ^ 1u, abort_flag);
@@ -474,16 +475,24 @@ weights_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
       const bool mine = t < tl.t1;
       const float old = mine && it.shares == 1 && p.decay != 0.0f ? *w : 0.0f;
       float sum = 0.0f;
-      for (int k = 0; k < tl.p1 - tl.p0; ++k, ++pass) {
+      // a thread brings one row's log-sum-exp, a pass ahead
+      const float* lse = p.lse + (size_t)(p.first + tl.b) * rows_all;
+      auto lse_of = [&](int k) {
+        const int r = Tiles::pass(tl, k) * p.rows_pass + st;
+        return st < p.rows_pass && r < rows_all ? lse[r] * kLog2e : 0.0f;
+      };
+      float ahead = p.passes > 1 || tl.first ? lse_of(0) : 0.0f;
+      const int n = tl.p1 - tl.p0;
+      for (int k = 0; k < n; ++k, ++pass) {
         const int g = Tiles::pass(tl, k);
         const int rows = min(p.rows_pass, rows_all - g * p.rows_pass);
         if (p.passes > 1 || tl.first) {
           stage ^= 1;
           if (st < rows) {
-            const int r = g * p.rows_pass + st;
-            sh.lse[stage][st] = p.lse[(size_t)(p.first + tl.b) * rows_all + r] * kLog2e;
-            sh.limit[stage][st] = tl.len - p.Q + r / p.heads + 1;
+            sh.lse[stage][st] = ahead;
+            sh.limit[stage][st] = tl.len - p.Q + (g * p.rows_pass + st) / p.heads + 1;
           }
+          if (k + 1 < n) ahead = lse_of(k + 1);
           sums_meet();      // whoever writes this stage's place next has met everyone who read it
         }
         const int buf = pass & 1;
@@ -595,7 +604,8 @@ int moe_latent_weights(const moe_kv_cache* cache, int layer, const void* q, cons
   p.passes = (rows + most - 1) / most;
   p.rows_pass = ((rows + p.passes - 1) / p.passes + 15) & ~15;       // evenly, in multiples of 16
   p.passes = (rows + p.rows_pass - 1) / p.rows_pass;
-  p.ring = rows <= kResident ? p.parts : kRing;
+  p.resident = rows <= kResident;
+  p.ring = p.resident ? p.parts : kRing;
   p.ctas = num_sms();
   // zero as the smallest normal number, as in the attention whose log-sum-exp this is
   p.scale_log2 = scale == 0.0f ? FLT_MIN : scale * kLog2e;
@@ -607,7 +617,7 @@ int moe_latent_weights(const moe_kv_cache* cache, int layer, const void* q, cons
   p.part = reinterpret_cast<float*>(reinterpret_cast<char*>(ws) + plan_bytes(B));
   p.status = dev_status;
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const int chunks = 2 * p.pairs + (cache->rope ? 1 : 0), q_chunks = rows <= kResident ? chunks : 2 * kRing;
+  const int chunks = 2 * p.pairs + (cache->rope ? 1 : 0), q_chunks = p.resident ? chunks : 2 * kRing;
   const int smem = chunks * kChunkBytes + q_chunks * p.rows_pass * kBK * 2 + 1024;
   CUtensorMap mk;
   if (!make_map(&mk, cache->pages, p.kv.row, (uint64_t)cache->n_layers * cache->n_pages * cache->page_tokens,

@@ -99,6 +99,21 @@ def test_weights(rank, rope, page, heads, Q, lens, decay, four):
         assert torch.equal(got, run_weights(c, q, seqs, Q, heads, scale, lse, decay, old.clone()))   # the same bits
 
 
+@pytest.mark.parametrize("heads,Q", [(16, 1), (65, 1), (128, 1), (100, 2)])
+@pytest.mark.parametrize("four", [False, True])
+def test_several_tiles_of_a_sequence_in_turn(heads, Q, four):
+    """More than 152 x 128 tokens: every CTA takes tile after tile, with queries that stay, that do not in one pass, in several."""
+    n = 45000
+    c = (Paged4 if four else Paged)(-(-n // 128) + 1, 128, 128, 16, 2, -(-n // 128))
+    rows = c.fill([n, 70], seed=heads)
+    q = make_q(2 * Q, heads, c.row, 3)
+    lse = lse64(rows, q, [1, 0], Q, heads, 0.1)
+    old = torch.rand(2, c.table.shape[1] * 128, device=DEV)
+    got = run_weights(c, q, [1, 0], Q, heads, 0.1, lse, 0.5, old.clone())
+    assert c.bits() == 0
+    check(rows, q, [1, 0], Q, heads, 0.1, lse, 0.5, old, got)
+
+
 @pytest.mark.parametrize("four", [False, True])
 def test_with_the_decode_calls_lse(four):
     """One step as it is used: the weights of a step sum to queries x heads."""
