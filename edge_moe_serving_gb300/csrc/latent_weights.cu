@@ -392,13 +392,13 @@ weights_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
   } else if (FP4 && warp >= kThreads / 32) {
     // ------------------------------------------------ latents in 4 bits, expanded into the tile that a copy would fill
     // Four threads a token, two tokens a thread; of each 128-entry pair a thread has 16 bytes of codes, a quarter.  Codes
-    // are asked for a tile ahead, as soon as their registers are free, and pages two tiles ahead.  Places past a tile's
-    // last token get some row's entries: the sums there are not written.
+    // are asked for a tile ahead, as soon as their registers are free.  Places past a tile's last token get some row's
+    // entries: the sums there are not written.
     const int r = (warp - kThreads / 32) * 8 + (lane & 7), v = lane >> 3;
     const int scales_at = p.kv.rank / 2 + 2 * p.kv.rope, pairs = p.pairs;
     const Fp4Place to[2] = {Fp4Place(smem_u32(smem), kChunkBytes, r, v), Fp4Place(smem_u32(smem), kChunkBytes, r + 64, v)};
     const uint8_t* row[2];
-    int page[2], at[2];           // of the tile after the next: page and place in it
+    int page[2], at[2];           // of the next tile: page and place in it
     uint4 code[2][kMaxPairs];
     uint32_t scale[2][kMaxPairs];
     auto look_up = [&](bool any) {
@@ -435,12 +435,9 @@ weights_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
 #pragma unroll
     for (int j = 0; j < kMaxPairs; ++j)
       if (j < pairs) load(j);
-    bool next = it.next(tl);
-    look_up(next);
-    locate();
     for (int tile = 0; ok && now; ++tile) {
-      const bool after = it.next(tl);
-      look_up(after);
+      const bool next = it.next(tl);
+      look_up(next);
       auto expand = [&](auto J) {
         constexpr int j = decltype(J)::value;
         if (j >= pairs) return;
@@ -448,6 +445,7 @@ weights_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
         if (!ok) return;
         fp4_store32(to[0], 2 * j * kChunkBytes, code[0][j], scale[0][j]);
         fp4_store32(to[1], 2 * j * kChunkBytes, code[1][j], scale[1][j]);
+        if (j == 0) locate();      // the look-up has had the first expansion's time
         load(j);
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.k_full[j]);
@@ -457,8 +455,6 @@ weights_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
       expand(std::integral_constant<int, 2>{});
       expand(std::integral_constant<int, 3>{});
       now = next;
-      next = after;
-      locate();
     }
     __syncwarp();
   } else if (warp >= 4) {
