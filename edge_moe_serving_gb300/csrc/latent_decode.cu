@@ -1164,6 +1164,12 @@ __global__ void __launch_bounds__(128) unpack_prefix_kernel(const DecodeParams p
 }
 
 // ---------------------------------------------------------------- host side
+// A prefix in 4 bits that many row tiles read is expanded once, to bf16 pages that they read in its place.  With 32 heads,
+// expanded by each / once: 64 sequences over 16384 shared tokens (54 tiles of a row tile a CTA) 184 / 154 us, 16 over 65536
+// (54) 177 / 165, 64 over 2048 (7) 67 / 73, 16 over 16384 (13) 76 / 78.
+// (Rises with the rows and the shared tokens, as the workspace has to.)
+bool unpack_pays(const DecodeParams& p) { return p.np > 0 && p.Gp >= 8 && p.Gp * p.np >= 24 * p.ctas; }
+
 struct DecodeWs {
   size_t plan, part_s, ml_s, part_p, ml_p, pages, table, bytes;
 };
@@ -1189,9 +1195,11 @@ DecodeWs decode_ws(const DecodeParams& p, const moe_kv_cache& c) {
   w.ml_p = at;
   at += align_up(np * sizeof(float4), 256);
   w.pages = at;              // the prefix as bf16
-  if (c.format == MOE_KV_FP4) at += align_up((size_t)p.shared * (rank + c.rope) * 2, 256);
   w.table = at;
-  if (c.format == MOE_KV_FP4) at += align_up((size_t)p.shared / 16 * sizeof(int32_t), 256);
+  if (c.format == MOE_KV_FP4 && unpack_pays(p)) {
+    w.table += align_up((size_t)p.shared * (rank + c.rope) * 2, 256);
+    at = w.table + align_up((size_t)p.shared / 16 * sizeof(int32_t), 256);
+  }
   w.bytes = at;
   return w;
 }
@@ -1253,11 +1261,6 @@ cudaError_t launch_lines(DecodeParams p, bool fp4, const void* q, cudaStream_t s
   return fp4 ? launch_decode_kernel<true>(p, smem, s, kv, pair, qs, qsr, qp, qpr, scales)
              : launch_decode_kernel<false>(p, smem, s, kv, pair, qs, qsr, qp, qpr, scales);
 }
-
-// A prefix in 4 bits that many row tiles read is expanded once, to bf16 pages that they read in its place.  With 32 heads,
-// expanded by each / once: 64 sequences over 16384 shared tokens (54 tiles of a row tile a CTA) 184 / 154 us, 16 over 65536
-// (54) 177 / 165, 64 over 2048 (7) 67 / 73, 16 over 16384 (13) 76 / 78.
-bool unpack_pays(const DecodeParams& p) { return p.np > 0 && p.Gp >= 8 && p.Gp * p.np >= 24 * p.ctas; }
 
 // unpacked: bf16 pages and their block table in the workspace; `there`: an earlier launch of the call has filled them
 int launch_decode(const moe_kv_cache& c, DecodeParams p, const void* q, __nv_bfloat16* unpacked, int32_t* blocks, bool& there,

@@ -47,7 +47,8 @@ constexpr int kThreads = 256;                    // a bf16 cache's; one in 4 bit
 constexpr int kExpandWarps = 8;
 constexpr int kSumThreads = 128;
 constexpr int kTmemCols = 256;                   // two passes of 128 columns
-constexpr int kBatch = 512;                      // sequences of one launch (lengths and tile sums in shared memory)
+constexpr int kBatch = 256;                      // sequences of one launch: their lengths lie in shared memory, and 256 times 2^27
+                                                 // tokens are 2^30 units
 constexpr float kLog2e = 1.4426950408889634f;
 
 struct WeightParams {
@@ -465,7 +466,7 @@ weights_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
     const float scale = p.scale_log2;
     int pass = 0, stage = 0;
     bool ok = true;
-    while (ok && it.next(tl)) {
+    while (it.next(tl)) {
       const int t = tl.t0 + st;
       float* w = p.weights + (size_t)tl.seq * cap + t;
       const bool mine = t < tl.t1;
@@ -492,8 +493,11 @@ weights_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
           sums_meet();      // whoever writes this stage's place next has met everyone who read it
         }
         const int buf = pass & 1;
-        ok = warp_wait(&sh.d_full[buf], (pass >> 1) & 1, abort_flag);
-        if (!ok) break;
+        // a warp whose wait ran out goes on through the passes without their sums: the others wait for it at sums_meet
+        if (!warp_wait(&sh.d_full[buf], (pass >> 1) & 1, abort_flag)) {
+          ok = false;
+          continue;
+        }
         tc_fence_after();
         const int limit0 = tl.len - p.Q + g * p.rows_pass / p.heads + 1;       // the pass's first row sees the least
         const bool seen = tl.t1 <= limit0;
@@ -509,7 +513,7 @@ weights_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.d_empty[buf]);
       }
-      if (!ok) break;
+      if (!ok) continue;
       if (it.shares > 1) {
         if (st < kUnit) p.part[(size_t)tl.work * kUnit + st] = sum;
       } else if (mine) {
@@ -619,7 +623,7 @@ int moe_latent_weights(const moe_kv_cache* cache, int layer, const void* q, cons
   if (!make_map(&mk, cache->pages, p.kv.row, (uint64_t)cache->n_layers * cache->n_pages * cache->page_tokens,
                 cache->page_tokens < kUnit ? cache->page_tokens : kUnit))
     return MOE_ERR_CUDA;
-  for (int b0 = 0; b0 < B; b0 += kBatch) {   // lists of more than 512 sequences: several launches
+  for (int b0 = 0; b0 < B; b0 += kBatch) {   // longer lists: several launches
     p.first = b0;
     p.B = B - b0 < kBatch ? B - b0 : kBatch;
     CUtensorMap mq;

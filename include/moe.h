@@ -623,6 +623,7 @@ int moe_kv_reserve(const moe_kv_cache* cache, const int32_t* seqs, const int32_t
  * token tok_pos[i] of sequence tok_seq[i], inside the length that
  * moe_kv_reserve gave it.  Entries out of range set MOE_DEV_ERR_BAD_SEQ, entries
  * whose page is missing or shared (refs > 1) MOE_DEV_ERR_BAD_PAGE; both are skipped.
+ * A token that one call lists twice holds parts of both rows.
  * MOE_KV_FP4: a scale is the largest magnitude of its 16 entries / 6, a code the
  * entry / scale, each rounded to nearest, ties to even.  Where the scale would pass
  * 61440 it is 61440, entries beyond 6 scales become 368640, and MOE_DEV_ERR_RANGE is

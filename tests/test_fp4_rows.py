@@ -134,6 +134,17 @@ def test_evict_refuses():
     assert all(a <= b for a, b in zip(sizes, sizes[1:]))
 
 
+@pytest.mark.parametrize("heads", [1, 16, 20, 64])
+def test_decode_size_never_falls(heads):
+    c = fp4(max_blocks=1024, max_seqs=600)
+    for shared in (0, 1024, 16384, 65536):
+        for Q in (1, 2, 5):
+            sizes = [moe.moe_latent_decode_workspace_size(c, B, Q, heads, shared) for B in range(1, 560)]
+            assert sizes[0] > 0 and all(a <= b for a, b in zip(sizes, sizes[1:]))
+    sizes = [moe.moe_latent_decode_workspace_size(c, 64, 1, heads, 64 * n) for n in range(1025)]
+    assert all(a <= b for a, b in zip(sizes, sizes[1:]))
+
+
 def test_weights_size_never_falls():
     c = fp4()
     for a, b in (((1, 1, 8), (4, 1, 8)), ((4, 1, 8), (4, 8, 8)), ((4, 8, 8), (4, 8, 128)), ((4, 1, 64), (600, 1, 65))):
