@@ -1,6 +1,18 @@
 // Eviction from the latent cache: sequences past a budget keep their heaviest
 // tokens.  select_kernel finds, per sequence and layer, which tokens stay; move_kernel
 // closes the gaps in place, and the last of a sequence's CTAs shortens its block table.
+//
+// Selection: the weight that the last token to stay has, found a byte at a time from
+// the top (a histogram of those that share the bytes found so far), then a mask and a
+// prefix count per 32 tokens.  Of equal weights the first ones stay, by their order in
+// the sequence and not by arrival: the same tokens on every run.
+// Moves: the order is kept, so every token behind the first gap moves, once, to
+// a lower place.  A row is cut into slices that move without knowing of each other.
+//
+// Bound: rows that move, read and written once (HBM), and for few sequences the
+// chains of dependent reads: 8 sequences of 520..700 tokens to 512, one layer: 13 us
+// (with a reserve for the next chunk 16.8); 32 of 2500..8192 to 4096, 4 layers, 515 MB: 84
+// us, 6.1 TB/s (87 with the reserve).
 #include "kv_common.cuh"
 
 namespace moe {

@@ -34,10 +34,25 @@
 //   4 x 40001..65537, 128 heads, 2 tokens 169 us  0.69 PFLOP/s
 //   64 x 16384 shared + 17..1500, 32 heads 127 us 0.60 PFLOP/s
 //
+// A cache in 4 bits (kv_fp4.cuh) differs in how a tile comes: its codes are staged by
+// TMA as they are, and eight more warps expand them into the places that copies of bf16
+// rows would fill, a ring of 128-entry pairs.  Products, softmax and pieces are the same,
+// and so are the answers, bit for bit those of a bf16 cache of the same values.  It
+// holds 2.8 times the tokens; it is not faster: a tile of 64 tokens takes 5100 cycles
+// where bf16 takes 3700.  The softmax is the reason (3000 cycles of it where it takes 1100
+// alone): its code and the expansion's take turns in the instruction caches, and every copy of the
+// expansion that unrolling added made it worse (kv_fp4.cuh).  A prefix that many row tiles read is
+// expanded once, to bf16.  Measured, rank 512 and rope 64, with what bf16 takes:
+//   1 x 333 tokens, 32 heads              15.2 us  13.2
+//   32 x 250..6001, 16 heads              42 us    33.2
+//   4 x 40001..65537, 32 heads, 2 tokens  90 us    74
+//   64 x 16384 shared + 17..1500, 32 heads 154 us  126
+//
 // Roles (224 threads): warp 0 = TMA producer, warp 1 = issuer of S (and TMEM
 // owner), warps 2..5 = softmax, rescaling and epilogue, warp 6 = issuer of the
 // value products (an issuer of its own: a tile's value product frees the tile's
-// memory, and must not wait behind the next tile's S, which waits for its loads).
+// memory, and must not wait behind the next tile's S, which waits for its loads);
+// in 4 bits warps 7..14 expand, warp 15 copies codes.
 // Every mbarrier wait is bounded; on expiry the CTA reports
 // MOE_DEV_ERR_TIMEOUT, drains and returns.
 #include <cfloat>
