@@ -81,13 +81,16 @@ __device__ inline void st_shared_v4(uint32_t at, const uint4& v) {
 
 // The quarter's entries to `to`, `offset` bytes on (a whole warp at once): with one product where all of the warp's scales
 // are below 4 (a block whose largest entry is 24, far above a normalised latent), else with two, which also know a scale
-// that is NaN.  Two words at a time, rolled: the warps that expand share their instruction caches with the softmax and the
-// issuers, and four quarters unrolled took 750 cycles each, one 226 to 380, all with instruction fetches.
+// that is NaN.  HALVES: how many halves of the quarter are written out.  The warps that expand share their instruction
+// caches with the kernel's other roles: beside the decode kernel's softmax one half in a loop is best (832,000 tokens of 16
+// heads 223 us, with both written out 244, with all four quarters of a row 307), in the smaller weights kernel both are (168
+// us, one in a loop 177).
+template <int HALVES>
 __device__ inline void fp4_store32(const Fp4Place& to, uint32_t offset, uint4 c, uint32_t scales) {
   const bool large = (scales & 0xFFu) >= 0x88u || scales >= 0x8800u;
   uint32_t at = to.at + offset;
   if (!__any_sync(0xffffffffu, large)) {
-#pragma unroll 1
+#pragma unroll HALVES
     for (int i = 0; i < 2; ++i) {
       const uint32_t f = fp4_factor_small(scales);
       st_shared_v4(at, fp4_expand8_small(c.x, f));

@@ -690,7 +690,7 @@ decode_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_constant_
         for (int j = 0; j < p.pairs; ++j) {
           ok = warp_wait(empty4 + buf, par, abort_flag);
           if (!ok) break;
-          fp4_store32(to, buf * 2 * kChunk, c[0], scales[0]);
+          fp4_store32<1>(to, buf * 2 * kChunk, c[0], scales[0]);
           __syncwarp();
           if (lane == 0) mbar_arrive(full4 + buf);
           if (++buf == p.bufs) {

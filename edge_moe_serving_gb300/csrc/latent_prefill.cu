@@ -508,7 +508,7 @@ expand_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__
       auto expand = [&](int c, const uint4 (&code)[4], const uint32_t (&scale)[4]) {
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          fp4_store32(Fp4Place(smem_u32(smem), kChunkBytes, r0 + 32 * e, v), c * kChunkBytes, code[e], scale[e]);
+          fp4_store32<2>(Fp4Place(smem_u32(smem), kChunkBytes, r0 + 32 * e, v), c * kChunkBytes, code[e], scale[e]);
         proxy_fence();
         __syncwarp();
         if (lane == 0) {

@@ -17,12 +17,12 @@
 // are shared out, and finish_weights_kernel adds the shares in order.
 //
 // Bound: the rows of the cache, read once (bf16: 6.6 TB/s on long batches), in 4
-// bits their expansion (about 8000 cycles a tile), with many query rows the products
+// bits their expansion (about 7500 cycles a tile), with many query rows the products
 // (a pass of 128 takes 2304 cycles of them, and 5000 with what lies between its parts).
 // Measured, rank 512 and rope 64:
 //   32 x 250..6001, 64 heads             23.6 us   4.3 TB/s; 832,000 tokens 151 us
-//   32 x 250..6001, 64 heads, 4 bits     30 us
-//   1 x 16001, 32 queries of 32 heads    28.7 us   4 bits 31
+//   32 x 250..6001, 64 heads, 4 bits     28 us     832,000 tokens 168 us
+//   1 x 16001, 32 queries of 32 heads    28.7 us   4 bits 30.5
 //
 // Roles: warp 0 = copies of the cache, warp 1 = products (and TMEM owner), warp 2 =
 // copies of the queries, warps 4..7 = sums, and for a cache in 4 bits warps 8..15, which
@@ -30,7 +30,6 @@
 // MOE_DEV_ERR_TIMEOUT, drains and returns.
 #include <cfloat>
 #include <cmath>
-#include <type_traits>
 
 #include "kv_fp4.cuh"
 #include "tc_common.cuh"
@@ -398,15 +397,16 @@ weights_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
   } else if (FP4 && warp >= kThreads / 32) {
     // ------------------------------------------------ latents in 4 bits, expanded into the tile that a copy would fill
     // Four threads a token, two tokens a thread; of each 128-entry pair a thread has 16 bytes of codes, a quarter.  Codes
-    // are asked for a tile ahead, as soon as their registers are free.  Places past a tile's last token get some row's
-    // entries: the sums there are not written.
+    // are asked for a pair ahead, pages a tile ahead.  Places past a tile's last token get some row's entries: the sums
+    // there are not written.
     const int r = (warp - kThreads / 32) * 8 + (lane & 7), v = lane >> 3;
-    const int scales_at = p.kv.rank / 2 + 2 * p.kv.rope, pairs = p.pairs;
-    const Fp4Place to[2] = {Fp4Place(smem_u32(smem), kChunkBytes, r, v), Fp4Place(smem_u32(smem), kChunkBytes, r + 64, v)};
+    const int scales_at = p.kv.rank / 2 + 2 * p.kv.rope;
+    const Fp4Place to(smem_u32(smem), kChunkBytes, r, v);      // of the first token; the second's lies 64 rows on
     const uint8_t* row[2];
     int page[2], at[2];           // of the next tile: page and place in it
-    uint4 code[2][kMaxPairs];
-    uint32_t scale[2][kMaxPairs];
+    uint4 code[2];
+    uint32_t scale[2];
+    int j_load = 0;
     auto look_up = [&](bool any) {
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
@@ -428,38 +428,35 @@ weights_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
         row[e] = reinterpret_cast<const uint8_t*>(p.kv.pages + p.kv.row_offset(p.layer, page[e], at[e])) + 16 * v;
       }
     };
-    auto load = [&](int j) {
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        code[e][j] = ldg_stream(row[e] + 64 * j);
-        scale[e][j] = ldg_stream_u16(row[e] + scales_at + 8 * j - 14 * v);
-      }
+    auto load = [&](int e) {
+      code[e] = ldg_stream(row[e] + 64 * j_load);
+      scale[e] = ldg_stream_u16(row[e] + scales_at + 8 * j_load - 14 * v);
     };
     bool now = it.next(tl), ok = true;
     look_up(now);
     locate();
-#pragma unroll
-    for (int j = 0; j < kMaxPairs; ++j)
-      if (j < pairs) load(j);
+    load(0);
+    load(1);
+#pragma unroll 1
     for (int tile = 0; ok && now; ++tile) {
       const bool next = it.next(tl);
       look_up(next);
-      auto expand = [&](auto J) {
-        constexpr int j = decltype(J)::value;
-        if (j >= pairs) return;
-        ok = ok && warp_wait(&sh.k_empty[j], (tile & 1) ^ 1u, abort_flag);
-        if (!ok) return;
-        fp4_store32(to[0], 2 * j * kChunkBytes, code[0][j], scale[0][j]);
-        fp4_store32(to[1], 2 * j * kChunkBytes, code[1][j], scale[1][j]);
-        if (j == 0) locate();      // the look-up has had the first expansion's time
-        load(j);
+#pragma unroll 1
+      for (int j = 0; j < p.pairs; ++j) {
+        if (++j_load == p.pairs) {
+          j_load = 0;
+          locate();
+        }
+        ok = warp_wait(&sh.k_empty[j], (tile & 1) ^ 1u, abort_flag);
+        if (!ok) break;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          fp4_store32<2>(to, 2 * j * kChunkBytes + e * (64 * 128), code[e], scale[e]);
+          load(e);
+        }
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.k_full[j]);
-      };
-      expand(std::integral_constant<int, 0>{});
-      expand(std::integral_constant<int, 1>{});
-      expand(std::integral_constant<int, 2>{});
-      expand(std::integral_constant<int, 3>{});
+      }
       now = next;
     }
     __syncwarp();
