@@ -298,8 +298,10 @@ def _own_weights(s):
 def _own_evict(s):
     moe, h = _handle(s)
     c = s["case"]
-    moe.moe_kv_evict(h, s["seqs"], c["batch"], s["weights"], c["budget"], c["first"], c["recent"], s["kept"],
-                     s["ws"], s["ws"].numel(), s["status"])
+    # the system prompt stays whether or not another sequence holds its pages too
+    first = max(c["first"], c["shared"])
+    moe.moe_kv_evict(h, s["seqs"], c["batch"], s["weights"], max(c["budget"], first + c["recent"]), first, c["recent"],
+                     s["kept"], s["ws"], s["ws"].numel(), s["status"])
     moe.moe_kv_reserve(h, s["seqs"], s["n_new"], c["batch"], s["ws"], s["ws"].numel(), s["status"])
     return _evict_state(s)
 
