@@ -1183,7 +1183,7 @@ __global__ void __launch_bounds__(128) unpack_prefix_kernel(const DecodeParams p
 // expanded by each / once: 64 sequences over 16384 shared tokens (54 tiles of a row tile a CTA) 184 / 154 us, 16 over 65536
 // (54) 177 / 165, 64 over 2048 (7) 67 / 73, 16 over 16384 (13) 76 / 78.
 // (Rises with the rows and the shared tokens, as the workspace has to.)
-bool unpack_pays(const DecodeParams& p) { return p.np > 0 && p.Gp >= 8 && p.Gp * p.np >= 24 * p.ctas; }
+bool unpack_pays(const DecodeParams& p) { return p.np > 0 && p.Gp >= 8 && (long long)p.Gp * p.np >= 24LL * p.ctas; }
 
 struct DecodeWs {
   size_t plan, part_s, ml_s, part_p, ml_p, pages, table, bytes;
@@ -1277,14 +1277,15 @@ cudaError_t launch_lines(DecodeParams p, bool fp4, const void* q, cudaStream_t s
              : launch_decode_kernel<false>(p, smem, s, kv, pair, qs, qsr, qp, qpr, scales);
 }
 
-// unpacked: bf16 pages and their block table in the workspace; `there`: an earlier launch of the call has filled them
+// unpacked: bf16 pages and their block table in the workspace (nullptr: it has no room for them); `there`: an earlier
+// launch of the call has filled them
 int launch_decode(const moe_kv_cache& c, DecodeParams p, const void* q, __nv_bfloat16* unpacked, int32_t* blocks, bool& there,
                   cudaStream_t s) {
   const bool fp4 = c.format == MOE_KV_FP4;
   cudaError_t e = cudaSuccess;
   p.lines = 3;
   p.prefix_blocks = nullptr;
-  if (fp4 && unpack_pays(p)) {
+  if (unpacked && unpack_pays(p)) {
     if (!there) e = launch_k(unpack_prefix_kernel, (unsigned)(p.shared + 3) / 4, 128, 0, s, p, unpacked, blocks);
     there = true;
     DecodeParams first = p;
@@ -1349,7 +1350,7 @@ int moe_latent_decode(const moe_kv_cache* cache, int layer, const void* q, const
     const DecodeWs w = decode_ws(p, *cache);
     char* base = reinterpret_cast<char*>(ws);
     const size_t row0 = (size_t)b0 * Q * heads;
-    if (b0 == 0) {
+    if (b0 == 0 && w.pages < w.table) {      // the first launch's shape, which the workspace is sized by, decides
       pages = reinterpret_cast<__nv_bfloat16*>(base + w.pages);
       blocks = reinterpret_cast<int32_t*>(base + w.table);
     }
