@@ -52,7 +52,7 @@ MOE_HD inline void set_line(LineShape& p, int B, int Q, int heads, int shared, i
   p.G = s.n;
   p.NR = s.rows;
   p.teams = p.ctas / s.n;
-  p.np = (shared + kTok - 1) / kTok;
+  p.np = shared / kTok + (shared % kTok != 0);    // no sum that could pass an int
   p.Gp = p.np ? f.n : 0;
   p.NRp = f.rows;
   p.per_p = (int)(((long long)p.Gp * p.np + p.ctas - 1) / p.ctas);

@@ -28,3 +28,11 @@ def test_sizes_never_fall_up_to_the_longest_prefix():
         for B in (88, 512, 4096):
             sizes = [size(c, B, Q, heads, 1 << x) for x in range(6, 28)]
             assert sizes[0] > 0 and all(a <= b for a, b in zip(sizes, sizes[1:]))
+
+
+@pytest.mark.parametrize("four", [0, 1])
+def test_sizes_never_fall_at_the_end_of_int(four):
+    """Longer than any cache's prefix: the call refuses it, the size is still that of the longest."""
+    c = cache(reserved=four, page_tokens=16, n_pages=4096, max_blocks=1 << 21)
+    sizes = [size(c, 4, 1, 128, 2 ** 31 - x) for x in (128, 64, 32, 16, 1)]
+    assert sizes[0] > 0 and all(a <= b for a, b in zip(sizes, sizes[1:])), sizes
