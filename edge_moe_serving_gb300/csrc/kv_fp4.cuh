@@ -131,7 +131,8 @@ __device__ inline uint32_t ldg_stream_u16(const void* p) {
   return v;
 }
 
-// Between ordinary writes to shared memory and the tensor cores' reads of them.
+// Between a thread's ordinary writes to shared memory and the tensor cores' reads of them: by the thread that wrote, before
+// it signals.
 __device__ inline void proxy_fence() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
 // ---------------------------------------------------------------- bf16 to codes

@@ -532,7 +532,6 @@ decode_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_constant_
           ok = warp_wait(FP4 ? full4 + buf4 : &sh.full[slot][j], FP4 ? par4 : par, abort_flag);
           if (!ok) break;
           if (FP4) {
-            proxy_fence();                 // the expanded entries, for the products
             dk = dk0 + ((uint64_t)(buf4 * 2 * kChunk) >> 4);
             if (++buf4 == p.bufs) {
               buf4 = 0;
@@ -691,6 +690,7 @@ decode_kernel(const __grid_constant__ CUtensorMap map_kv, const __grid_constant_
           ok = warp_wait(empty4 + buf, par, abort_flag);
           if (!ok) break;
           fp4_store32<1>(to, buf * 2 * kChunk, c[0], scales[0]);
+          proxy_fence();
           __syncwarp();
           if (lane == 0) mbar_arrive(full4 + buf);
           if (++buf == p.bufs) {

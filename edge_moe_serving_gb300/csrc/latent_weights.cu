@@ -363,7 +363,6 @@ weights_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
         for (int j = 0; j < p.parts; ++j) {
           ok = warp_wait(&sh.q_full[slot], par, abort_flag) && warp_wait(&sh.k_full[j], tile & 1, abort_flag);
           if (!ok) break;
-          if (FP4) proxy_fence();               // the expanded rows, for the products
           tc_fence_after();
           const uint64_t dk = dk0 + ((uint64_t)(2 * j * kChunkBytes) >> 4), dq = dq0 + 2 * slot * q_step;
           if (j < p.pairs) {
@@ -454,6 +453,7 @@ weights_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
           fp4_store32<2>(to, 2 * j * kChunkBytes + e * (64 * 128), code[e], scale[e]);
           load(e);
         }
+        proxy_fence();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.k_full[j]);
       }
