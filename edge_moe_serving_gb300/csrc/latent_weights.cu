@@ -478,7 +478,8 @@ weights_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant_
       const float* lse = p.lse + (size_t)(p.first + tl.b) * rows_all;
       auto lse_of = [&](int k) {
         const int r = Tiles::pass(tl, k) * p.rows_pass + st;
-        return st < p.rows_pass && r < rows_all ? lse[r] * kLog2e : 0.0f;
+        const float x = st < p.rows_pass && r < rows_all ? lse[r] * kLog2e : 0.0f;
+        return x == -INFINITY ? INFINITY : x;       // a row that looked at nothing adds nothing: s - infinity, not s + infinity
       };
       float ahead = p.passes > 1 || tl.first ? lse_of(0) : 0.0f;
       const int n = tl.p1 - tl.p0;

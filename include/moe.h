@@ -723,8 +723,8 @@ int moe_latent_decode(const moe_kv_cache* cache, int layer, const void* q, const
 
 /* What moe_latent_decode's queries looked at, per cached token: with its s[t] and lse,
  *   weights[seqs[b], t] = decay * weights[seqs[b], t] + sum_{i, h} exp(s_{b*Q+i, h}[t] - lse[b*Q + i, h])
- * for every t < len, a query adding only to tokens it sees.  q, scale and lse as in and from
- * that call; weights fp32 [max_seqs, max_blocks * page_tokens], one layer's.  decay 1 adds
+ * for every t < len, a query adding only to tokens it sees, and a row whose lse is -inf (it
+ * looked at nothing) to none.  q, scale and lse as in and from that call; weights fp32 [max_seqs, max_blocks * page_tokens], one layer's.  decay 1 adds
  * up, between 0 and 1 old weight fades, 0 does not read what stood there.  Sums are
  * fp32 in a fixed order: the same bits on every run of a shape.  Q * heads up to 1024 lets the last tokens of a
  * prompt vote at once.  A NaN in a token's row makes its own weight NaN, and those that a NaN lse reaches.
