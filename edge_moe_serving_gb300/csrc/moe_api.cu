@@ -30,7 +30,7 @@ int num_sms() {
 
 namespace {
 
-constexpr int kVersion = 100;   // 1.0.0
+constexpr int kVersion = 110;   // 1.1.0
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 // workspaces are carved into 256-byte aligned regions read with vector loads

@@ -155,6 +155,8 @@ typedef struct moe_layer_buffers {
   float* y_rows;      /* [T*k, H], row t*k+j = output of token t's j-th expert */
 } moe_layer_buffers;
 
+/* 100 * major + 10 * minor + patch.  110 (1.1.0) and later read moe_kv_cache.format, which was `reserved` and
+ * ignored before, and have the calls over 4-bit pages, moe_latent_weights and moe_kv_evict. */
 int moe_version(void);
 const char* moe_status_string(int status);
 
