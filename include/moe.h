@@ -625,11 +625,13 @@ int moe_kv_reserve(const moe_kv_cache* cache, const int32_t* seqs, const int32_t
  * token tok_pos[i] of sequence tok_seq[i], inside the length that
  * moe_kv_reserve gave it.  Entries out of range set MOE_DEV_ERR_BAD_SEQ, entries
  * whose page is missing or shared (refs > 1) MOE_DEV_ERR_BAD_PAGE; both are skipped.
- * A token that one call lists twice holds parts of both rows.
+ * A token that one call lists twice holds parts of both rows (in MOE_KV_FP4 maybe one's
+ * codes under the other's scales).
  * MOE_KV_FP4: a scale is the largest magnitude of its 16 entries / 6, a code the
  * entry / scale, each rounded to nearest, ties to even.  Where the scale would pass
  * 61440 it is 61440, entries beyond 6 scales become 368640, and MOE_DEV_ERR_RANGE is
- * set; a NaN or an infinity makes its 16 entries NaN. */
+ * set; where it is 2^-18 or less before its rounding (no entry above 6 * 2^-18) all 16 are 0; a NaN or an infinity
+ * makes its 16 entries NaN. */
 int moe_kv_append(const moe_kv_cache* cache, int layer, const void* rows, const int32_t* tok_seq,
                   const int32_t* tok_pos, int N, uint32_t* dev_status, moe_stream_t stream);
 
@@ -676,13 +678,16 @@ int moe_kv_compact(const moe_kv_cache* cache, int32_t* n_live_opt, void* ws, siz
  * row and its weight move there, weights from the new length to len become 0, and pages
  * behind the new length are released.  Each layer chooses by its own weights; lengths
  * and block tables are one for all layers.  A sequence within the budget stays as it is.
+ * From then on a token's place in the cache (tok_pos, and what the page calls count) is no longer the
+ * position that its rotary key was turned by: the next token of a conversation still takes the
+ * conversation's next position there, which the caller counts.
  * kept_opt: int32 [n_layers, n, max_blocks * page_tokens] or NULL; entry j < new length of
  * list entry i gets the position that its token j had, entries behind it are not written.
  * An id outside [0, max_seqs) and every repeat of an id set MOE_DEV_ERR_BAD_SEQ, a
  * sequence with a missing page MOE_DEV_ERR_BAD_PAGE: those entries are skipped.
  * Errors: the struct's; MOE_ERR_INVALID_ARG for n < 0 or above max_seqs, budget < 1,
  * first or recent < 0, first + recent > budget, NULL seqs or weights (n > 0);
- * MOE_ERR_UNSUPPORTED for max_blocks * page_tokens above 2^20, weights or kept_opt not 4-byte aligned;
+ * MOE_ERR_UNSUPPORTED for max_blocks * page_tokens above 2^20, n_layers above 65535, weights or kept_opt not 4-byte aligned;
  * MOE_ERR_WORKSPACE / MOE_ERR_UNSUPPORTED for ws.  A workspace for n sequences serves shorter lists. */
 size_t moe_kv_evict_workspace_size(const moe_kv_cache* cache, int n);
 int moe_kv_evict(const moe_kv_cache* cache, const int32_t* seqs, int n, float* weights, int budget, int first,
@@ -703,7 +708,9 @@ int moe_kv_evict(const moe_kv_cache* cache, const int32_t* seqs, int n, float* w
  * unrounded ones.  A NaN in a token's row makes every query that sees the token
  * NaN; an infinite latent entry makes that entry of theirs NaN, and may make the
  * others; an infinite rotary entry that makes the score -infinity leaves the
- * token out, else it makes them NaN.  No other query is touched.  A query * shared_tokens > 0 (a multiple of page_tokens): the first shared_tokens
+ * token out, else it makes them NaN.  No other query is touched.  A query that sees no
+ * token (a sequence shorter than Q, or a bad id) gets zeros and lse = -inf.
+ * shared_tokens > 0 (a multiple of page_tokens): the first shared_tokens
  * tokens of all B sequences are the ones in the pages of seqs[0] (as
  * moe_kv_fork leaves them); they are then read and multiplied once for the
  * whole batch, and the partial results are merged.  Where seqs[0] is a bad id, every row of such a call gets zeros and
@@ -726,9 +733,14 @@ int moe_latent_decode(const moe_kv_cache* cache, int layer, const void* q, const
 /* What moe_latent_decode's queries looked at, per cached token: with its s[t] and lse,
  *   weights[seqs[b], t] = decay * weights[seqs[b], t] + sum_{i, h} exp(s_{b*Q+i, h}[t] - lse[b*Q + i, h])
  * for every t < len, a query adding only to tokens it sees, and a row whose lse is -inf (it
- * looked at nothing) to none.  q, scale and lse as in and from that call; weights fp32 [max_seqs, max_blocks * page_tokens], one layer's.  decay 1 adds
- * up, between 0 and 1 old weight fades, 0 does not read what stood there.  Sums are
- * fp32 in a fixed order: the same bits on every run of a shape.  Q * heads up to 1024 lets the last tokens of a
+ * looked at nothing) to none.  q, scale and lse as in and from that call;
+ * weights fp32 [max_seqs, max_blocks * page_tokens], one layer's.  decay 1 adds
+ * up, between 0 and 1 old weight fades, 0 does not read what stood there.  The array is the
+ * caller's, and moe_kv_evict alone moves it with the tokens: moe_kv_free, moe_kv_reserve and moe_kv_fork do
+ * not touch it.  So the caller sets the row of a freed or new sequence to 0, and copies a source's
+ * row to a fork's, before the next call that reads them.  Sums are
+ * fp32 in a fixed order: the same bits on every run of a list (their last bits may depend on
+ * the lengths of the list's other sequences).  Q * heads up to 1024 lets the last tokens of a
  * prompt vote at once.  A NaN in a token's row makes its own weight NaN, and those that a NaN lse reaches.
  * A sequence listed twice counts once, its later entries set MOE_DEV_ERR_BAD_SEQ, as ids
  * out of range do; a missing page sets MOE_DEV_ERR_BAD_PAGE, weights of that sequence are then unspecified.
