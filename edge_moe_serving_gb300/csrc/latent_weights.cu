@@ -20,8 +20,8 @@
 // bits their expansion (about 7500 cycles a tile), with many query rows the products
 // (a pass of 128 takes 2304 cycles of them, and 5000 with what lies between its parts).
 // Measured, rank 512 and rope 64:
-//   32 x 250..6001, 64 heads             23.6 us   4.3 TB/s; 832,000 tokens 151 us
-//   32 x 250..6001, 64 heads, 4 bits     28 us     832,000 tokens 168 us
+//   32 x 250..6001, 64 heads             23.6 us   4.3 TB/s; 832,000 tokens (967 MB with their weights) 147 us
+//   32 x 250..6001, 64 heads, 4 bits     28 us     832,000 tokens 167 us
 //   1 x 16001, 32 queries of 32 heads    28.7 us   4 bits 30.5
 //
 // Roles: warp 0 = copies of the cache, warp 1 = products (and TMEM owner), warp 2 =
