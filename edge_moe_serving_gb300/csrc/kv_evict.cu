@@ -12,7 +12,7 @@
 // Bound: rows that move, read and written once (HBM), and for few sequences the
 // chains of dependent reads: 8 sequences of 520..700 tokens to 512, one layer: 13 us
 // (with a reserve for the next chunk 16.8); 32 of 2500..8192 to 4096, 4 layers, 515 MB: 84
-// us, 6.1 TB/s (82 to 88 with the reserve, over 4-bit rows 55).  A sequence is walked by one CTA a slice and chosen from
+// us, 6.1 TB/s (82 to 91 with the reserve, over 4-bit rows 55).  A sequence is walked by one CTA a slice and chosen from
 // by one CTA a layer, however long: half of 16,001 tokens takes 60 us and of 65,537 220, one layer or four, bf16 or 4 bits.
 #include "kv_common.cuh"
 

@@ -17,7 +17,7 @@
 // terms' size, which the softmax averages.
 //
 // A cache in 4 bits: four more warps of expand_kernel expand a tile's codes (kv_fp4.cuh) into the places that copies of
-// bf16 rows would fill; 1000 tokens over 15001, 16 heads 204 us, 5 prompts of 1..300 over 100, 32 heads 47 us.
+// bf16 rows would fill; 1000 tokens over 15001, 16 heads 208 us, 5 prompts of 1..300 over 100, 32 heads 48 us.
 //
 // Measured, rank 512, rope 64, keys and values of 128:
 //   5 prompts of 1..300 tokens, 32 heads     36.6 us
